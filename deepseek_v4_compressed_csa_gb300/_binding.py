@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libcsa.so")
 CSA_F32, CSA_BF16 = 0, 1
 OP_COMPRESS, OP_INDEX_TOPK, OP_ATTEND_DECODE, OP_ATTEND_PREFILL, OP_COMPRESS_PAIR = 0, 1, 2, 3, 4
 OP_COMPRESS_VARLEN, OP_ATTEND_PREFILL_VARLEN = 5, 6
+OP_COMPRESS_TREE, OP_ATTEND_TREE = 7, 8
 FP8_ROW_BYTES = 144  # CSA_FP8_ROW_BYTES: 128 E4M3 codes, the fp32 scale, 12 zero bytes
 DEV_CAPACITY, DEV_STATE, DEV_RANGE, DEV_ROLLBACK = 1, 2, 4, 8
 CSA_OK, CSA_ERR_ARG, CSA_ERR_UNSUPPORTED, CSA_ERR_CUDA, CSA_ERR_WORKSPACE = 0, 1, 2, 3, 4
@@ -30,7 +31,8 @@ EXPORTS = ("csa_kernel_launches", "csa_frontier_slots", "csa_workspace_size", "c
            "csa_attend_decode", "csa_attend_prefill_chunk", "csa_status_string", "csa_static_scratch_bytes",
            "csa_index_topk_static", "csa_index_topk_overlapped", "csa_advance_positions",
            "csa_compress_append_pair", "csa_trim", "csa_index_topk_verify", "csa_attend_verify",
-           "csa_compress_append_varlen", "csa_attend_prefill_varlen", "csa_index_rows_fp8")
+           "csa_compress_append_varlen", "csa_attend_prefill_varlen", "csa_index_rows_fp8", "csa_norm_rope",
+           "csa_compress_tree", "csa_index_scores_tree", "csa_attend_tree", "csa_commit_tree")
 
 
 class CSAError(RuntimeError):
@@ -49,6 +51,12 @@ class _Layer(ctypes.Structure):
 class _Comp(ctypes.Structure):
     _fields_ = [("wkv", ctypes.c_void_p), ("wgate", ctypes.c_void_p), ("ape", ctypes.c_void_p),
                 ("norm_w", ctypes.c_void_p), ("d", ctypes.c_int)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("heads", ctypes.c_int), ("dim", ctypes.c_int), ("norm", ctypes.c_int),
+                ("x_stride", ctypes.c_longlong)]
 
 
 _lib = None
@@ -105,6 +113,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.csa_attend_prefill_varlen.restype = i32
     lib.csa_index_rows_fp8.argtypes = [vp, vp, ctypes.c_longlong, vp, vp]
     lib.csa_index_rows_fp8.restype = i32
+    lib.csa_norm_rope.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
+    lib.csa_norm_rope.restype = i32
+    lib.csa_compress_tree.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.csa_compress_tree.restype = i32
+    lib.csa_index_scores_tree.argtypes = [vp, vp, vp, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp]
+    lib.csa_index_scores_tree.restype = i32
+    lib.csa_attend_tree.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp,
+                                    vp]
+    lib.csa_attend_tree.restype = i32
+    lib.csa_commit_tree.argtypes = [vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp,
+                                    i32, vp, vp, vp, vp]
+    lib.csa_commit_tree.restype = i32
     _lib = lib
     return lib
 
@@ -591,4 +611,228 @@ def attend_verify(layer: Layer, q, kv_new, sink, window, pool, n_rows, sel, n_se
     _check("csa_attend_verify", load_library().csa_attend_verify(
         ctypes.byref(L), _ptr(q), _ptr(kv_new), _ptr(sink), B, T, _ptr(window), _ptr(pool), cap, _ptr(n_rows),
         _ptr(sel), _ptr(n_sel), _ptr(pos), _ptr(inv_freq), _ptr(out), _ptr(ws), nb, _ptr(err), _stream(stream)))
+    return err
+
+
+def _tree_ptr(name: str, t, dtype, shape, dev=None):
+    """Checks of one tensor of a tree call (type, shape, contiguity, device); its address."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} is required") if t is None else TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: CSA tensors must live on a CUDA device")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name}: on device {t.get_device()}, the call's tensors are on device {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: CSA tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _tree_err(err, dev):
+    if err is None:
+        return torch.zeros(1, dtype=torch.int32, device=f"cuda:{dev}")
+    _expect_err(err)
+    if not err.is_cuda or err.get_device() != dev:
+        raise ValueError(f"err: expected a tensor on device {dev}")
+    return err
+
+
+def _tree_ws(layer, op, B, T, cap, ws, dev):
+    need = workspace_size(layer, op, B, T, cap)
+    if ws is None:
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=f"cuda:{dev}")
+    elif not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor on device {dev}")
+    return ws, ws.numel() * ws.element_size()
+
+
+def _tree_call(fn: str, dev: int, stream, *args):
+    """The C call on the tensors' device, on `stream` or that device's current stream."""
+    f = getattr(load_library(), fn)
+    if dev == torch.cuda.current_device():
+        _check(fn, f(*args, _stream(stream)))
+        return
+    with torch.cuda.device(dev):
+        _check(fn, f(*args, _stream(stream)))
+
+
+def _tree_dims(name: str, t, tail: tuple):
+    """(B, T, device) of a tensor [B, T, *tail]."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2 + len(tail) or tuple(t.shape[2:]) != tail:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [B, T{''.join(', %d' % n for n in tail)}]")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: CSA tensors must live on a CUDA device")
+    return t.shape[0], t.shape[1], t.get_device()
+
+
+def norm_rope(layer: Layer, xs, pos=None, inv_freq=None, parent=None, weights=None, norm=None, outs=None, err=None,
+              stream=None):
+    """csa_norm_rope: every head row of the tensors xs (up to four, each [B, T, heads, dim] or [B, T, dim]) RMS-normed
+    (norm[k], default True; weights[k] fp32 [dim] or None) and rotated to its token's position: pos[b] + depth in the
+    tree `parent` [B, T], or pos[b] + i without one.  inv_freq None: no rotation (for the calls that rotate by
+    themselves).  An x may be a slice of a wider tensor: its heads contiguous, one stride from token to token.
+    Returns the outputs (`outs`, or new tensors; a new tensor's rows of unused tree slots are zeros)."""
+    n = len(xs)
+    if not 1 <= n <= 4:
+        raise ValueError(f"norm_rope takes 1 to 4 tensors, got {n}")
+    weights = [None] * n if weights is None else weights
+    norm = [True] * n if norm is None else norm
+    if len(weights) != n or len(norm) != n or (outs is not None and len(outs) != n):
+        raise ValueError("weights, norm and outs need one entry per tensor")
+    if not isinstance(xs[0], torch.Tensor) or xs[0].dim() not in (3, 4):
+        raise ValueError("xs: expected tensors [B, T, heads, dim] or [B, T, dim]")
+    B, T, dev = xs[0].shape[0], xs[0].shape[1], xs[0].get_device()
+    if outs is None:
+        new = torch.empty if parent is None else torch.zeros
+        outs = [new(x.shape, dtype=x.dtype, device=x.device) for x in xs]
+    rows = (_Rows * n)()
+    for k, x in enumerate(xs):
+        if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4) or tuple(x.shape[:2]) != (B, T):
+            raise ValueError(f"xs[{k}]: expected [{B}, {T}, heads, dim] or [{B}, {T}, dim]")
+        if x.dtype != layer.dtype:
+            raise TypeError(f"xs[{k}]: dtype {x.dtype}, expected {layer.dtype}")
+        if not x.is_cuda or x.get_device() != dev:
+            raise ValueError(f"xs[{k}]: expected a CUDA tensor on device {dev}")
+        heads, dim = (1 if x.dim() == 3 else x.shape[2]), x.shape[-1]
+        stride = 0
+        if not x.is_contiguous():
+            st = x.stride()
+            stride = st[1] if T > 1 else (st[0] if B > 1 else 0)
+            if st[-1] != 1 or (x.dim() == 4 and heads > 1 and st[2] != dim) or (T > 1 and B > 1 and st[0] != T * st[1]):
+                raise ValueError(f"xs[{k}]: strides {st}; heads must be contiguous, tokens one stride apart")
+        w = weights[k]
+        rows[k] = _Rows(x.data_ptr(), _tree_ptr(f"outs[{k}]", outs[k], layer.dtype, tuple(x.shape), dev),
+                        None if w is None else _tree_ptr(f"weights[{k}]", w, torch.float32, (dim,), dev), heads, dim,
+                        int(bool(norm[k])), stride)
+    p_par = None if parent is None else _tree_ptr("parent", parent, torch.int32, (B, T), dev)
+    p_pos = None if pos is None and inv_freq is None else _tree_ptr("pos", pos, torch.int32, (B,), dev)
+    p_frq = None if inv_freq is None else _tree_ptr("inv_freq", inv_freq, torch.float32, (layer.R // 2,), dev)
+    err = _tree_err(err, dev)
+    L = layer._c()
+    _tree_call("csa_norm_rope", dev, stream, ctypes.byref(L), rows, n, B, T, p_par, p_pos, p_frq, err.data_ptr())
+    return list(outs)
+
+
+def compress_tree(layer: Layer, comp_a: Compressor, x, parent, pos, frontier_a, proj_a, rows_a, inv_freq, comp_i=None,
+                  frontier_i=None, proj_i=None, rows_i=None, ws=None, err=None, stream=None):
+    """csa_compress_tree: x [B, T, X], parent [B, T]; writes proj_a [B, T, 2 L D], rows_a [B, T, D] and, with comp_i,
+    the index pool's proj_i, rows_i.  The frontiers are read only.  Returns the device error word tensor."""
+    B, T, dev = _tree_dims("x", x, (layer.X,))
+    F = _frontier_len(layer)
+    _expect_comp(layer, comp_a, "comp_a")
+    args = [_tree_ptr("x", x, layer.dtype, (B, T, layer.X)), B, T,
+            _tree_ptr("parent", parent, torch.int32, (B, T), dev), _tree_ptr("pos", pos, torch.int32, (B,), dev)]
+    for nm, d, fr, pj, rw in (("a", comp_a.d, frontier_a, proj_a, rows_a),
+                              ("i", comp_i.d if comp_i is not None else 0, frontier_i, proj_i, rows_i)):
+        if nm == "i" and comp_i is None:
+            if fr is not None or pj is not None or rw is not None:
+                raise ValueError("frontier_i, proj_i, rows_i come with comp_i")
+            args += [None, None, None]
+            continue
+        wide = 2 * layer.lanes * d
+        dt, row = layer.pool_spec(d) if nm == "i" else (layer.dtype, d)
+        args += [_tree_ptr(f"frontier_{nm}", fr, layer.dtype, (B, F, wide), dev),
+                 _tree_ptr(f"proj_{nm}", pj, layer.dtype, (B, T, wide), dev),
+                 _tree_ptr(f"rows_{nm}", rw, dt, (B, T, row), dev)]
+    if comp_i is not None:
+        _expect_comp(layer, comp_i, "comp_i")
+    args.append(_tree_ptr("inv_freq", inv_freq, torch.float32, (layer.R // 2,), dev))
+    ws, nb = _tree_ws(layer, OP_COMPRESS_TREE, B, T, 1, ws, dev)
+    err = _tree_err(err, dev)
+    L, Ca = layer._c(), comp_a._c()
+    Ci = ctypes.byref(comp_i._c()) if comp_i is not None else None
+    _tree_call("csa_compress_tree", dev, stream, ctypes.byref(L), ctypes.byref(Ca), Ci, *args, ws.data_ptr(), nb,
+               err.data_ptr())
+    return err
+
+
+def index_scores_tree(layer: Layer, iq, iw, ikeys, rows_i, parent, n_rows, pos, scores, err=None, stream=None):
+    """csa_index_scores_tree: rotated iq [B, T, Hi, Di], iw [B, T, Hi], ikeys [B, cap, Di], rows_i [B, T, Di];
+    writes scores [B, T, cap + T] (fp32).  Returns the device error word tensor."""
+    B, T, dev = _tree_dims("iq", iq, (layer.Hi, layer.Di))
+    if not isinstance(ikeys, torch.Tensor) or ikeys.dim() != 3:
+        raise ValueError(f"ikeys: expected [{B}, cap, {layer.Di}]")
+    cap = ikeys.shape[1]
+    dt, row = layer.pool_spec(layer.Di)
+    args = [_tree_ptr("iq", iq, layer.dtype, (B, T, layer.Hi, layer.Di)),
+            _tree_ptr("iw", iw, layer.dtype, (B, T, layer.Hi), dev), B, T,
+            _tree_ptr("parent", parent, torch.int32, (B, T), dev), _tree_ptr("ikeys", ikeys, dt, (B, cap, row), dev), cap,
+            _tree_ptr("rows_i", rows_i, dt, (B, T, row), dev), _tree_ptr("n_rows", n_rows, torch.int32, (B,), dev),
+            _tree_ptr("pos", pos, torch.int32, (B,), dev),
+            _tree_ptr("scores", scores, torch.float32, (B, T, cap + T), dev)]
+    err = _tree_err(err, dev)
+    L = layer._c()
+    _tree_call("csa_index_scores_tree", dev, stream, ctypes.byref(L), *args, err.data_ptr())
+    return err
+
+
+def attend_tree(layer: Layer, q, kv, sink, window, pool, rows_a, scores, parent, n_rows, pos, inv_freq, out,
+                sel_out=None, ws=None, err=None, stream=None):
+    """csa_attend_tree: rotated q [B, T, H, D] and kv [B, T, D]; scores [B, T, cap + T] of index_scores_tree, or None
+    (every visible row); out [B, T, H, D]; sel_out [B, T, topk] int32 or None.  The cache is read only.  Returns the
+    device error word tensor."""
+    B, T, dev = _tree_dims("q", q, (layer.H, layer.D))
+    if not isinstance(pool, torch.Tensor) or pool.dim() != 3:
+        raise ValueError(f"pool: expected [{B}, cap, {layer.D}]")
+    cap, dt = pool.shape[1], layer.dtype
+    args = [_tree_ptr("q", q, dt, (B, T, layer.H, layer.D)), _tree_ptr("kv", kv, dt, (B, T, layer.D), dev),
+            _tree_ptr("sink", sink, torch.float32, (layer.H,), dev), B, T,
+            _tree_ptr("parent", parent, torch.int32, (B, T), dev),
+            _tree_ptr("window", window, dt, (B, layer.ring_slots, layer.D), dev),
+            _tree_ptr("pool", pool, dt, (B, cap, layer.D), dev), cap,
+            _tree_ptr("rows_a", rows_a, dt, (B, T, layer.D), dev),
+            None if scores is None else _tree_ptr("scores", scores, torch.float32, (B, T, cap + T), dev),
+            _tree_ptr("n_rows", n_rows, torch.int32, (B,), dev), _tree_ptr("pos", pos, torch.int32, (B,), dev),
+            _tree_ptr("inv_freq", inv_freq, torch.float32, (layer.R // 2,), dev),
+            _tree_ptr("out", out, dt, (B, T, layer.H, layer.D), dev),
+            None if sel_out is None else _tree_ptr("sel_out", sel_out, torch.int32, (B, T, layer.topk), dev)]
+    ws, nb = _tree_ws(layer, OP_ATTEND_TREE, B, T, cap, ws, dev)
+    err = _tree_err(err, dev)
+    L = layer._c()
+    _tree_call("csa_attend_tree", dev, stream, ctypes.byref(L), *args, ws.data_ptr(), nb, err.data_ptr())
+    return err
+
+
+def commit_tree(layer: Layer, parent, leaf, pos, n_rows_a, kv, window, proj_a, frontier_a, rows_a, pool_a,
+                n_rows_i=None, proj_i=None, frontier_i=None, rows_i=None, pool_i=None, pos_out=None, n_rows_a_out=None,
+                n_rows_i_out=None, err=None, stream=None):
+    """csa_commit_tree: the path to leaf[b] (int32 [B]; -1: nothing accepted) enters the cache.  pos, n_rows_a and
+    n_rows_i advance in place unless pos_out, n_rows_a_out, n_rows_i_out are given.  The index pool's arguments come
+    together or not at all.  Returns the device error word tensor."""
+    B, T, dev = _tree_dims("parent", parent, ())
+    dt, D, F = layer.dtype, layer.D, _frontier_len(layer)
+    i32, vec = torch.int32, (B,)
+    wide = 2 * layer.lanes
+
+    def pool_args(nm, d, pj, fr, rw, pl, nr, nr_out, spec):
+        if not isinstance(pl, torch.Tensor) or pl.dim() != 3:
+            raise ValueError(f"pool_{nm}: expected [{B}, cap, {spec[1]}]")
+        cap = pl.shape[1]
+        return [_tree_ptr(f"proj_{nm}", pj, dt, (B, T, wide * d), dev),
+                _tree_ptr(f"frontier_{nm}", fr, dt, (B, F, wide * d), dev),
+                _tree_ptr(f"rows_{nm}", rw, spec[0], (B, T, spec[1]), dev),
+                _tree_ptr(f"pool_{nm}", pl, spec[0], (B, cap, spec[1]), dev), cap,
+                _tree_ptr(f"n_rows_{nm}", nr, i32, vec, dev),
+                _tree_ptr(f"n_rows_{nm}_out", nr if nr_out is None else nr_out, i32, vec, dev)]
+
+    args = [B, T, _tree_ptr("parent", parent, i32, (B, T)), _tree_ptr("leaf", leaf, i32, vec, dev),
+            _tree_ptr("pos", pos, i32, vec, dev),
+            _tree_ptr("pos_out", pos if pos_out is None else pos_out, i32, vec, dev),
+            _tree_ptr("kv", kv, dt, (B, T, D), dev), _tree_ptr("window", window, dt, (B, layer.ring_slots, D), dev)]
+    args += pool_args("a", D, proj_a, frontier_a, rows_a, pool_a, n_rows_a, n_rows_a_out, (dt, D))
+    if pool_i is not None:
+        args += pool_args("i", layer.Di, proj_i, frontier_i, rows_i, pool_i, n_rows_i, n_rows_i_out,
+                          layer.pool_spec(layer.Di))
+    elif any(t is not None for t in (n_rows_i, proj_i, frontier_i, rows_i, n_rows_i_out)):
+        raise ValueError("n_rows_i, proj_i, frontier_i, rows_i, n_rows_i_out come with pool_i")
+    else:
+        args += [None, None, None, None, 0, None, None]
+    err = _tree_err(err, dev)
+    L = layer._c()
+    _tree_call("csa_commit_tree", dev, stream, ctypes.byref(L), *args, err.data_ptr())
     return err

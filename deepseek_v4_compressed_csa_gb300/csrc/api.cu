@@ -99,6 +99,16 @@ size_t ws_prefill(const Dims& L, int T, int cap) {
   return c.off;
 }
 
+// A batch of trees: at most 64 nodes each (a path is a 64-bit mask), and grids of B x T queries.
+bool tree_sizes_ok(int B, int T) {
+  return B >= 1 && B <= 65535 && T >= 1 && T <= 64 && (long long)B * T <= (1 << 18);
+}
+size_t ws_attend_tree(const Dims& L, int B, int T, int cap) {
+  Carver c(nullptr);
+  carve_attend_tree(c, L, B, T, cap);
+  return c.off;
+}
+
 }  // namespace
 
 extern "C" {
@@ -153,6 +163,14 @@ csa_status csa_workspace_size(const csa_layer* layer, int op, int B, int T, int 
     case CSA_OP_ATTEND_PREFILL_VARLEN:  // T: the batch's total tokens N
       if (T < 1 || T > 16384) return CSA_ERR_ARG;
       *bytes = ws_prefill(L, T, cap);
+      return CSA_OK;
+    case CSA_OP_COMPRESS_TREE:
+      if (!tree_sizes_ok(B, T)) return CSA_ERR_ARG;
+      *bytes = L.has_indexer() ? ws_compress_pair(L, B, T) : ws_compress(L, L.D, B, T);
+      return CSA_OK;
+    case CSA_OP_ATTEND_TREE:
+      if (!tree_sizes_ok(B, T)) return CSA_ERR_ARG;
+      *bytes = ws_attend_tree(L, B, T, cap);
       return CSA_OK;
   }
   return CSA_ERR_ARG;
@@ -437,6 +455,122 @@ csa_status csa_index_rows_fp8(const csa_layer* layer, const void* src, long long
   if (n == 0) return CSA_OK;
   if (!dev_tensor(src) || !dev_tensor(dst)) return CSA_ERR_ARG;
   return cuda_status(launch_index_rows_fp8(src, n, dst, static_cast<cudaStream_t>(stream)));
+}
+
+csa_status csa_norm_rope(const csa_layer* layer, const csa_rows* rows, int n, int B, int T, const int32_t* parent,
+                         const int32_t* pos, const float* inv_freq, int32_t* err, void* stream) {
+  Dims L;
+  csa_status st = make_dims(layer, &L);
+  if (st != CSA_OK) return st;
+  if (!rows || n < 1 || n > 4 || B < 1 || T < 1 || (long long)B * T > (1 << 24) || !dev_i32(err)) return CSA_ERR_ARG;
+  if (parent && (!dev_i32(parent) || T > 64)) return CSA_ERR_ARG;
+  if (inv_freq && (!dev_tensor(inv_freq) || !dev_i32(pos))) return CSA_ERR_ARG;
+  for (int k = 0; k < n; ++k) {
+    const csa_rows& r = rows[k];
+    if (!dev_tensor(r.x) || !dev_tensor(r.out) || (r.weight && !dev_tensor(r.weight))) return CSA_ERR_ARG;
+    if (r.heads < 1 || r.heads > 4096 || r.dim < 8 || r.dim > 1024 || r.dim % 8 || r.dim < L.R || (r.dim - L.R) % 8 ||
+        (r.norm != 0 && r.norm != 1))
+      return CSA_ERR_ARG;
+    const long long dense = (long long)r.heads * r.dim;
+    if (r.x_stride != 0 && (r.x_stride < dense || r.x_stride % 8)) return CSA_ERR_ARG;
+    if (r.x == r.out && r.x_stride > dense) return CSA_ERR_ARG;
+  }
+  return cuda_status(launch_norm_rope(L, rows, n, B, T, parent, pos, inv_freq, err,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+csa_status csa_compress_tree(const csa_layer* layer, const csa_compressor* comp_a, const csa_compressor* comp_i,
+                             const void* x, int B, int T, const int32_t* parent, const int32_t* pos,
+                             const void* frontier_a, void* proj_a, void* rows_a, const void* frontier_i, void* proj_i,
+                             void* rows_i, const float* inv_freq, void* ws, size_t ws_bytes, int32_t* err,
+                             void* stream) {
+  Dims L;
+  csa_status st = make_dims(layer, &L);
+  if (st != CSA_OK) return st;
+  if (!tree_sizes_ok(B, T)) return CSA_ERR_ARG;
+  if (comp_i && !L.has_indexer()) return CSA_ERR_UNSUPPORTED;
+  if (!compress_args_ok(L, comp_a, B, T, 1, frontier_a, proj_a, pos) || comp_a->d != L.D || !dev_tensor(rows_a))
+    return CSA_ERR_ARG;
+  if (comp_i && (!compress_args_ok(L, comp_i, B, T, 1, frontier_i, proj_i, pos) || comp_i->d != L.Di ||
+                 !dev_tensor(rows_i)))
+    return CSA_ERR_ARG;
+  if (!dev_tensor(x) || !dev_i32(parent) || !dev_tensor(inv_freq) || !dev_i32(err)) return CSA_ERR_ARG;
+  const size_t need = comp_i ? ws_compress_pair(L, B, T) : ws_compress(L, L.D, B, T);
+  if (ws_bytes < need || !dev_tensor(ws)) return CSA_ERR_WORKSPACE;
+  Carver c(ws);
+  TreeCompress pools[2] = {};
+  pools[0] = TreeCompress{comp_a, frontier_a, proj_a, rows_a, carve_compress(c, L, L.D, B, T)};
+  if (comp_i) pools[1] = TreeCompress{comp_i, frontier_i, proj_i, rows_i, carve_compress(c, L, L.Di, B, T)};
+  return cuda_status(launch_compress_tree(L, pools, comp_i ? 2 : 1, x, B, T, parent, pos, inv_freq, err,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+csa_status csa_index_scores_tree(const csa_layer* layer, const void* iq, const void* iw, int B, int T,
+                                 const int32_t* parent, const void* ikeys, int cap, const void* rows_i,
+                                 const int32_t* n_rows, const int32_t* pos, float* scores, int32_t* err,
+                                 void* stream) {
+  Dims L;
+  csa_status st = make_dims(layer, &L);
+  if (st != CSA_OK) return st;
+  if (!L.has_indexer() || L.ikey_fp8) return CSA_ERR_UNSUPPORTED;
+  if (!tree_sizes_ok(B, T) || cap < 1) return CSA_ERR_ARG;
+  if (!dev_tensor(iq) || !dev_i32(iw) || !dev_tensor(ikeys) || !dev_tensor(rows_i) || !dev_i32(scores))
+    return CSA_ERR_ARG;
+  if (!dev_i32(parent) || !dev_i32(n_rows) || !dev_i32(pos) || !dev_i32(err)) return CSA_ERR_ARG;
+  return cuda_status(launch_index_scores_tree(L, iq, iw, B, T, parent, ikeys, cap, rows_i, n_rows, pos, scores, err,
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+csa_status csa_attend_tree(const csa_layer* layer, const void* q, const void* kv, const float* sink, int B, int T,
+                           const int32_t* parent, const void* window, const void* pool, int cap, const void* rows_a,
+                           const float* scores, const int32_t* n_rows, const int32_t* pos, const float* inv_freq,
+                           void* out, int32_t* sel_out, void* ws, size_t ws_bytes, int32_t* err, void* stream) {
+  Dims L;
+  csa_status st = make_dims(layer, &L);
+  if (st != CSA_OK) return st;
+  if (!tree_sizes_ok(B, T) || cap < 1) return CSA_ERR_ARG;
+  if (!dev_tensor(q) || !dev_tensor(kv) || !dev_i32(sink) || !dev_tensor(window) || !dev_tensor(pool) ||
+      !dev_tensor(rows_a) || !dev_tensor(inv_freq) || !dev_tensor(out))
+    return CSA_ERR_ARG;
+  if (!dev_i32(parent) || !dev_i32(n_rows) || !dev_i32(pos) || !dev_i32(err)) return CSA_ERR_ARG;
+  if (scores && (!L.has_indexer() || !dev_i32(scores))) return CSA_ERR_ARG;
+  if (sel_out && (!scores || !dev_i32(sel_out))) return CSA_ERR_ARG;
+  const size_t need = ws_attend_tree(L, B, T, cap);
+  if (ws_bytes < need || (need && !dev_tensor(ws))) return CSA_ERR_WORKSPACE;
+  Carver c(ws);
+  TreeAttend t{q, kv, window, pool, rows_a, scores, sink, inv_freq, parent, n_rows, pos, out, sel_out, B, T, cap,
+               carve_attend_tree(c, L, B, T, cap)};
+  return cuda_status(launch_attend_tree(L, t, err, static_cast<cudaStream_t>(stream)));
+}
+
+csa_status csa_commit_tree(const csa_layer* layer, int B, int T, const int32_t* parent, const int32_t* leaf,
+                           const int32_t* pos, int32_t* pos_out, const void* kv, void* window, const void* proj_a,
+                           void* frontier_a, const void* rows_a, void* pool_a, int cap_a, const int32_t* n_rows_a,
+                           int32_t* n_rows_a_out, const void* proj_i, void* frontier_i, const void* rows_i,
+                           void* pool_i, int cap_i, const int32_t* n_rows_i, int32_t* n_rows_i_out, int32_t* err,
+                           void* stream) {
+  Dims L;
+  csa_status st = make_dims(layer, &L);
+  if (st != CSA_OK) return st;
+  if (!tree_sizes_ok(B, T) || cap_a < 1) return CSA_ERR_ARG;
+  if (!dev_i32(parent) || !dev_i32(leaf) || !dev_i32(pos) || !dev_i32(pos_out) || !dev_i32(err)) return CSA_ERR_ARG;
+  if (!dev_tensor(kv) || !dev_tensor(window) || !dev_tensor(proj_a) || !dev_tensor(frontier_a) ||
+      !dev_tensor(rows_a) || !dev_tensor(pool_a) || !dev_i32(n_rows_a) || !dev_i32(n_rows_a_out))
+    return CSA_ERR_ARG;
+  if (pool_i) {
+    if (!L.has_indexer()) return CSA_ERR_UNSUPPORTED;
+    if (!dev_tensor(proj_i) || !dev_tensor(frontier_i) || !dev_tensor(rows_i) || !dev_tensor(pool_i) || cap_i < 1 ||
+        !dev_i32(n_rows_i) || !dev_i32(n_rows_i_out))
+      return CSA_ERR_ARG;
+  }
+  TreeCommit t{};
+  t.parent = parent; t.leaf = leaf; t.pos = pos; t.pos_out = pos_out; t.kv = kv; t.window = window;
+  t.proj[0] = proj_a; t.rows[0] = rows_a; t.frontier[0] = frontier_a; t.pool[0] = pool_a;
+  t.n_rows[0] = n_rows_a; t.n_rows_out[0] = n_rows_a_out; t.cap[0] = cap_a;
+  t.proj[1] = proj_i; t.rows[1] = rows_i; t.frontier[1] = frontier_i; t.pool[1] = pool_i;
+  t.n_rows[1] = n_rows_i; t.n_rows_out[1] = n_rows_i_out; t.cap[1] = cap_i;
+  t.npool = pool_i ? 2 : 1; t.B = B; t.T = T;
+  return cuda_status(launch_commit_tree(L, t, err, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

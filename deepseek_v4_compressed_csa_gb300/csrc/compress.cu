@@ -78,6 +78,23 @@ __global__ void __launch_bounds__(256) k_project_simt(const T* __restrict__ x, c
   }
 }
 
+cudaError_t launch_project_simt(const Dims& L, int d, const void* x, int ntok, const void* wkv, const void* wgate,
+                                void* proj, cudaStream_t s) {
+  const int Ld = L.lanes * d;
+  const dim3 g((2 * Ld + 7) / 8, (ntok + 7) / 8);
+  if (g.y > 65535) return cudaErrorInvalidValue;
+  if (L.dtype == CSA_BF16) {
+    using T = __nv_bfloat16;
+    CSA_LAUNCH(k_project_simt<T, 8>, g, dim3(256), 0, s, static_cast<const T*>(x), static_cast<const T*>(wkv),
+               static_cast<const T*>(wgate), ntok, L.X, Ld, static_cast<T*>(proj));
+  } else {
+    using T = float;
+    CSA_LAUNCH(k_project_simt<T, 8>, g, dim3(256), 0, s, static_cast<const T*>(x), static_cast<const T*>(wkv),
+               static_cast<const T*>(wgate), ntok, L.X, Ld, static_cast<T*>(proj));
+  }
+  return cudaGetLastError();
+}
+
 // An index row of 128 values in shared memory (model dtype) -> its fp8 row at dst, written by warp 0 once every
 // thread of the block has stored its values (all threads call this).
 __device__ __forceinline__ void store_fp8_row(uint8_t* dst, const float* row) {

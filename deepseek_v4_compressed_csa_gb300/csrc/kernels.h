@@ -111,6 +111,10 @@ cudaError_t launch_compress_varlen(const Dims& L, const csa_compressor& comp, co
                                    const CompressWs& ws, int32_t* err, cudaStream_t s);
 CompressWs carve_compress_varlen(Carver& c, const Dims& L, int d, int B, int N);
 
+// The projection of ntok tokens into proj [ntok, 2*L*d] on the SIMT path (any type and size).
+cudaError_t launch_project_simt(const Dims& L, int d, const void* x, int ntok, const void* wkv, const void* wgate,
+                                void* proj, cudaStream_t s);
+
 // ---- indexer.cu
 struct IndexWs {
   float* qr;      // [Q, Hi, Di] roped index queries (model-dtype values held as fp32)
@@ -253,5 +257,53 @@ cudaError_t launch_attend_verify(const Dims& L, const void* q, const void* kv_ne
                                  void* window, const void* pool, int cap, const int32_t* n_rows, const int32_t* sel,
                                  const int32_t* n_sel, const int32_t* pos, const float* inv_freq, void* out,
                                  const AttendWs& ws, int32_t* err, cudaStream_t s);
+
+// ---- tree.cu (a tree of drafted tokens; parent [B, T], T <= 64)
+cudaError_t launch_norm_rope(const Dims& L, const csa_rows* rows, int n, int B, int T, const int32_t* parent,
+                             const int32_t* pos, const float* inv_freq, int32_t* err, cudaStream_t s);
+// One pool of a compress call: the committed frontier, and the draft buffers proj [B, T, 2*L*d] and rows [B, T, d]
+// (ws carved by carve_compress for B x T tokens).
+struct TreeCompress {
+  const csa_compressor* comp;
+  const void* frontier;
+  void* proj;
+  void* rows;
+  CompressWs ws;
+};
+cudaError_t launch_compress_tree(const Dims& L, const TreeCompress* pools, int npool, const void* x, int B, int T,
+                                 const int32_t* parent, const int32_t* pos, const float* inv_freq, int32_t* err,
+                                 cudaStream_t s);
+cudaError_t launch_index_scores_tree(const Dims& L, const void* iq, const void* iw, int B, int T,
+                                     const int32_t* parent, const void* ikeys, int cap, const void* rows,
+                                     const int32_t* n_rows, const int32_t* pos, float* scores, int32_t* err,
+                                     cudaStream_t s);
+struct TreeAttendWs {
+  int32_t* sel;    // [B*T, topk] when the caller wants no selection (null without an indexer)
+  int32_t* n_sel;  // [B*T]
+};
+TreeAttendWs carve_attend_tree(Carver& c, const Dims& L, int B, int T, int cap);
+struct TreeAttend {
+  const void *q, *kv, *window, *pool, *rows;
+  const float *scores, *sink, *inv_freq;
+  const int32_t *parent, *n_rows, *pos;
+  void* out;
+  int32_t* sel_out;
+  int B, T, cap;
+  TreeAttendWs ws;
+};
+cudaError_t launch_attend_tree(const Dims& L, const TreeAttend& t, int32_t* err, cudaStream_t s);
+// Pool 0: the attention pool; pool 1 (npool == 2): the index pool.
+struct TreeCommit {
+  const int32_t *parent, *leaf, *pos;
+  int32_t* pos_out;
+  const void* kv;
+  void* window;
+  const void *proj[2], *rows[2];
+  void *frontier[2], *pool[2];
+  const int32_t* n_rows[2];
+  int32_t* n_rows_out[2];
+  int cap[2], npool, B, T;
+};
+cudaError_t launch_commit_tree(const Dims& L, const TreeCommit& c, int32_t* err, cudaStream_t s);
 
 }  // namespace csa

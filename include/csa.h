@@ -15,7 +15,9 @@
  *   csa_attend_prefill_chunk the same for a chunk of T queries of one
  *                            sequence, each with its own causal top-k.
  *   (*_varlen: a packed batch of chunks of different lengths; *_verify: verify
- *   blocks of T tokens per sequence; csa_trim: rewind for speculative decoding.)
+ *   blocks of T tokens per sequence; csa_trim: rewind for speculative decoding;
+ *   csa_norm_rope: per-head norm and rotation of what they take; *_tree: a tree
+ *   of drafted tokens per sequence.)
  *
  * Definitions follow the pages the method is described on:
  *   [MTPLX#216]  "DeepSeek-V4-Flash: native deepseek_v4 AR backend"
@@ -88,7 +90,9 @@ enum {
   CSA_OP_ATTEND_PREFILL = 3,
   CSA_OP_COMPRESS_PAIR = 4, /* csa_compress_append_pair (ratio-4 layers) */
   CSA_OP_COMPRESS_VARLEN = 5,       /* csa_compress_append_varlen: B sequences, T = N packed tokens */
-  CSA_OP_ATTEND_PREFILL_VARLEN = 6  /* csa_attend_prefill_varlen: B sequences, T = N packed tokens */
+  CSA_OP_ATTEND_PREFILL_VARLEN = 6, /* csa_attend_prefill_varlen: B sequences, T = N packed tokens */
+  CSA_OP_COMPRESS_TREE = 7,         /* csa_compress_tree: B trees of T nodes */
+  CSA_OP_ATTEND_TREE = 8            /* csa_attend_tree: B trees of T nodes */
 };
 
 /* One CSA layer.
@@ -416,6 +420,126 @@ csa_status csa_attend_verify(const csa_layer* layer, const void* q, const void* 
  * CSA_DEV_STATE) is OR-ed into err.  One small kernel on `stream`. */
 csa_status csa_trim(const csa_layer* layer, int B, const int32_t* n_back, int32_t* pos, int32_t* n_rows_a,
                     int32_t* n_rows_i, int32_t* hw, int32_t* err, void* stream);
+
+/* csa_norm_rope — the rows that attention and the indexer take, prepared in one
+ * pass: per token and head, an RMS norm and the rotation.
+ *
+ * Definition (heads normalised one by one, the latent with its weight, then RoPE
+ * in fp32: [MTPLX#216] "What V4 adds"; OmarB97's RoPE fixes in [mlx-lm#1189]):
+ *   y = x * (mean(x^2) + rms_eps)^-1/2 * weight   (norm != 0; weight NULL: ones)
+ *   out = RoPE(y, p), p = pos[b] + depth           (inv_freq NULL: no rotation)
+ * in fp32, rounded to the model dtype once.  depth is the node's depth in its
+ * sequence's tree when `parent` is given (see csa_compress_tree; T <= 64) and
+ * the token's index i otherwise, so one call serves a decode step (T = 1), a
+ * chunk, a verify block and a tree.  With inv_freq NULL the rows are only
+ * normalised: what csa_attend_decode, _prefill_chunk, _verify take, which rotate
+ * by themselves.  csa_index_scores_tree and csa_attend_tree take rotated rows.
+ * Arguments
+ *   rows      n <= 4 descriptors (host array), each one tensor of B x T tokens:
+ *     x       `heads` rows of `dim` values per token, token (b, i) at
+ *             x + (b T + i) x_stride (elements; 0: heads * dim, dense; else a
+ *             multiple of 8 and at least heads * dim)
+ *     out     [B, T, heads, dim] dense; may be x itself when x is dense, and must
+ *             not overlap any tensor of the call otherwise
+ *     weight  [dim] fp32 or NULL; norm: 0 or 1; dim a multiple of 8, R <= dim <=
+ *             1024, (dim - R) a multiple of 8
+ *   parent    [B, T] int32 or NULL; an unused slot's rows are left as they were
+ *   pos [B]   (may be NULL without a rotation), inv_freq [R/2] fp32
+ * Errors: CSA_ERR_ARG for sizes out of range (B, T, B*T <= 2^24, heads <= 4096,
+ * T <= 64 with a parent array); CSA_DEV_STATE for pos[b] < 0 or an inconsistent
+ * parent array (those tokens are skipped). */
+typedef struct {
+  const void* x;
+  void* out;
+  const float* weight;
+  int heads, dim, norm;
+  long long x_stride;
+} csa_rows;
+csa_status csa_norm_rope(const csa_layer* layer, const csa_rows* rows, int n, int B, int T, const int32_t* parent,
+                         const int32_t* pos, const float* inv_freq, int32_t* err, void* stream);
+
+/* csa_compress_tree, csa_index_scores_tree, csa_attend_tree, csa_commit_tree — a
+ * speculative step that verifies a TREE of drafted tokens per sequence.
+ *
+ * The tree of sequence b is parent[b][0 .. T): parent -1 follows the last
+ * committed token, 0 <= parent < i follows that node, and a value below -1 marks
+ * an unused slot (sequences of a batch may have trees of different sizes; T <= 64,
+ * B <= 65535, B*T <= 2^18).  Node i is a token at position p = pos[b] + depth(i), depth 0 for a child
+ * of the last committed token.
+ *
+ * Definition: every node's row, scores and output are what sequential decoding
+ * of its path (its ancestors from the root, then itself) would give
+ * ([MTPLX#216] "Verification": the same results whether tokens arrive one by one
+ * or in a block).  The cache is read only until csa_commit_tree; what the nodes
+ * add is kept in draft buffers of the caller:
+ *   kv     [B, T, D]       latent rows, normalised and rotated (csa_norm_rope)
+ *   proj_a [B, T, 2*L*D]   projected kv | gate rows (csa_compress_tree)
+ *   rows_a [B, T, D]       the compressed row that node i completes, (p + 1) mod
+ *                          ratio == 0; the other nodes' entries are not touched
+ *   proj_i, rows_i         the same for the index pool (rows of Di values, or of
+ *                          CSA_FP8_ROW_BYTES with index_fp8)
+ * An unused slot's entries and outputs are left as they were.  A parent that is
+ * not below its node, or a used node under an unused one, raises CSA_DEV_STATE
+ * and the nodes it concerns are skipped; so does a sequence with pos[b] < 0 or
+ * n_rows[b] != floor(pos[b] / ratio).  With two calls in flight on different
+ * streams, workspaces and draft buffers must differ.
+ *
+ * csa_compress_tree: x [B, T, X] model dtype; the entries of a window before
+ * pos[b] come from the frontier rings, the others from the path's nodes; every
+ * rounding is csa_compress_append's, so that a committed row is the row it would
+ * have written.  comp_i and its buffers are NULL for the attention pool alone.
+ * Workspace: CSA_OP_COMPRESS_TREE (cap ignored). */
+csa_status csa_compress_tree(const csa_layer* layer, const csa_compressor* comp_a, const csa_compressor* comp_i,
+                             const void* x, int B, int T, const int32_t* parent, const int32_t* pos,
+                             const void* frontier_a, void* proj_a, void* rows_a, const void* frontier_i, void* proj_i,
+                             void* rows_i, const float* inv_freq, void* ws, size_t ws_bytes, int32_t* err,
+                             void* stream);
+
+/* csa_index_scores_tree: the nodes' index scores, csa_index_topk's formula on
+ * rotated queries iq [B, T, Hi, Di] (csa_norm_rope without a norm), iw [B, T, Hi]:
+ *   scores [B, T, cap + T] fp32; columns c < n_rows[b]: committed row c;
+ *   columns n_rows[b] + a, a < T: the row of node a for the nodes a of i's path
+ *   that complete one, -infinity for the others; later columns are not touched.
+ * ikeys [B, cap, Di], rows_i [B, T, Di].  Requires ratio == 4; index_fp8 is not
+ * supported (CSA_ERR_UNSUPPORTED). */
+csa_status csa_index_scores_tree(const csa_layer* layer, const void* iq, const void* iw, int B, int T,
+                                 const int32_t* parent, const void* ikeys, int cap, const void* rows_i,
+                                 const int32_t* n_rows, const int32_t* pos, float* scores, int32_t* err,
+                                 void* stream);
+
+/* csa_attend_tree: selection and attention of every node.
+ *   visible columns: c < n_rows[b], and n_rows[b] + a for the completing nodes a
+ *   of the path; the topk largest scores among them (ties to the lower column),
+ *   all of them when there are no more or when scores is NULL (layers without an
+ *   indexer, or every row wanted);
+ *   keys = those rows (pool, or rows_a) ++ window tokens t in [p - W + 1, p]
+ *   (window ring before pos[b], kv of the path's nodes from there);
+ *   o = softmax with the sink as in csa_attend_decode, on rotated q;
+ *   out = RoPE^-1(o, p), in fp32, rounded to the model dtype once.
+ *   q [B, T, H, D], sink [H] fp32, scores [B, T, cap + T] or NULL,
+ *   out [B, T, H, D], sel_out [B, T, topk] int32 or NULL: the selected columns,
+ *   ascending, -1 padded (only with scores).
+ * Workspace: CSA_OP_ATTEND_TREE. */
+csa_status csa_attend_tree(const csa_layer* layer, const void* q, const void* kv, const float* sink, int B, int T,
+                           const int32_t* parent, const void* window, const void* pool, int cap, const void* rows_a,
+                           const float* scores, const int32_t* n_rows, const int32_t* pos, const float* inv_freq,
+                           void* out, int32_t* sel_out, void* ws, size_t ws_bytes, int32_t* err, void* stream);
+
+/* csa_commit_tree: leaf[b] (-1: nothing) is the last accepted node of sequence b;
+ * its path becomes committed tokens: their kv rows enter the window ring, their
+ * projections the frontier rings, the rows that they complete the pools, and
+ * pos_out[b] = pos[b] + (path length), n_rows_out[b] = floor(pos_out[b] / ratio).
+ * pos_out, n_rows_a_out, n_rows_i_out may be pos, n_rows_a, n_rows_i themselves.
+ * A sequence whose leaf is no node, whose state is inconsistent (CSA_DEV_STATE) or
+ * whose pool is too small (CSA_DEV_CAPACITY) is left unchanged (the outputs are
+ * the inputs).  The index pool's arguments are NULL for the attention pool alone.
+ * After it csa_trim rewinds as after decoding. */
+csa_status csa_commit_tree(const csa_layer* layer, int B, int T, const int32_t* parent, const int32_t* leaf,
+                           const int32_t* pos, int32_t* pos_out, const void* kv, void* window, const void* proj_a,
+                           void* frontier_a, const void* rows_a, void* pool_a, int cap_a, const int32_t* n_rows_a,
+                           int32_t* n_rows_a_out, const void* proj_i, void* frontier_i, const void* rows_i,
+                           void* pool_i, int cap_i, const int32_t* n_rows_i, int32_t* n_rows_i_out, int32_t* err,
+                           void* stream);
 
 /* csa_index_topk_static — csa_index_topk without a caller-supplied workspace.
  *
