@@ -277,6 +277,11 @@ cudaError_t launch_index_scores_tree(const Dims& L, const void* iq, const void* 
                                      const int32_t* parent, const void* ikeys, int cap, const void* rows,
                                      const int32_t* n_rows, const int32_t* pos, float* scores, int32_t* err,
                                      cudaStream_t s);
+// ---- tc_tree_scores.cu (the same on the tensor cores; bf16, Hi = 64, Di = 128)
+bool tc_tree_scores_supported(const Dims& L, int B, int cap);
+cudaError_t launch_tc_tree_scores(const Dims& L, const void* iq, const void* iw, int B, int T, const int32_t* parent,
+                                  const void* ikeys, int cap, const void* rows, const int32_t* n_rows,
+                                  const int32_t* pos, float* scores, int32_t* err, cudaStream_t s);
 struct TreeAttendWs {
   int32_t* sel;    // [B*T, topk] when the caller wants no selection (null without an indexer)
   int32_t* n_sel;  // [B*T]

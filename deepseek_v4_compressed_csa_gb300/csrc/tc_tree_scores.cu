@@ -1,0 +1,350 @@
+// Index scores of a tree's nodes on the 5th-generation tensor cores (bf16, Hi = 64 heads of Di = 128 dims).
+//
+// score[i][j] = sum_h w_ih ReLU(iq_ih . key_j), w = iw Di^-1/2 Hi^-1/2, for the committed keys of the node's sequence
+// and the index rows of its tree (definition: include/csa.h, csa_index_scores_tree).
+//
+// The product is computed transposed, S^T = K Q^T: M = 128 key rows per tile (TMEM lane = key row), N = 4 nodes x 64
+// heads, K = 128.  An epilogue thread then owns one key row and reduces the heads by itself.  Four nodes of a
+// sequence share every key tile: a tile (32 KB) costs eight 128 x 256 x 16 products (~1024 tensor clocks), which is
+// slower than fetching it from L2, so the kernel is bound by the tensor pipe for four nodes or more and by the key
+// stream for fewer.  The tree's own rows are one more tile per group (T <= 64 rows of the draft buffer), masked by
+// the path: they need no launch of their own.
+//
+// Work: the (sequence, group of 4 nodes, tile) triples that exist, in that order, cut into equal runs, one per CTA
+// (one CTA per SM).  Each CTA finds its run by a scan over the sequences' row counts, so ragged batches stay
+// balanced.  Ten warps: 0 TMA (a ring of three key tiles, two query blocks of 64 KB), 1 MMA (two accumulators of 256
+// columns), 2-9 epilogue: two warps per TMEM lane quarter, two nodes each.
+#include "kernels.h"
+#include "tc.cuh"
+#include "tree.cuh"
+
+namespace csa {
+
+namespace {
+
+constexpr int kRows = 128;               // key rows per tile
+constexpr int kG = 4;                    // nodes per group
+constexpr int kN = 64 * kG;
+constexpr int kTileBytes = kRows * 256;  // two 64-dim boxes of 128 rows
+constexpr int kQBytes = kN * 256;
+constexpr int kStages = 3, kQSlots = 2, kAcc = 2;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kOffK = kQSlots * kQBytes;
+constexpr int kOffW = kOffK + kStages * kTileBytes;  // [256] head weights of the group in the epilogue
+constexpr int kOffBars = kOffW + kN * 4;
+constexpr int kNumBars = 2 * kStages + 2 * kQSlots + 2 * kAcc + 1;
+constexpr int kOffRun = kOffBars + kNumBars * 8;     // the CTA's run: b, group, tile, count; TMEM address
+constexpr int kSmem = kOffRun + 32 + 1024;
+static_assert(kSmem <= 232448, "shared memory per block");
+
+struct TsArgs {
+  const __nv_bfloat16* iw;  // [B, T, 64]
+  const int32_t* parent;
+  const int32_t* pos;
+  const int32_t* n_rows;
+  float wscale;
+  int B, T, cap, ratio, groups;  // groups: of kG nodes, per sequence
+  float* scores;                 // [B, T, cap + T]
+  int32_t* err;
+};
+
+// Tiles of a group of sequence b: its committed rows and one of the tree's rows; 0 when the state is inconsistent.
+__device__ __forceinline__ int seq_tiles(const TsArgs& a, int b) {
+  const int p0 = __ldg(a.pos + b), n = __ldg(a.n_rows + b);
+  if (p0 < 0 || n != p0 / a.ratio || n > a.cap) return 0;
+  return (n + kRows - 1) / kRows + 1;
+}
+
+// Walks the CTA's run: (b, g, t) of its items in order.
+struct Walk {
+  int b, g, t, tiles, left;
+  __device__ __forceinline__ void start(const TsArgs& a, const int* run) {
+    b = run[0];
+    g = run[1];
+    t = run[2];
+    left = run[3];
+    tiles = left > 0 ? seq_tiles(a, b) : 0;
+  }
+  __device__ __forceinline__ bool last_of_group() const { return t == tiles - 1 || left == 1; }
+  __device__ __forceinline__ void next(const TsArgs& a) {
+    --left;
+    if (++t < tiles || left <= 0) return;
+    t = 0;
+    if (++g < a.groups) return;
+    g = 0;
+    do tiles = seq_tiles(a, ++b);
+    while (tiles == 0 && b < a.B - 1);
+  }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    k_tc_tree_scores(const __grid_constant__ CUtensorMap tm_keys, const __grid_constant__ CUtensorMap tm_rows,
+                     const __grid_constant__ CUtensorMap tm_q, TsArgs a) {
+  pdl_trigger();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qbuf = smem;
+  uint8_t* kbuf = smem + kOffK;
+  float* wbuf = reinterpret_cast<float*>(smem + kOffW);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBars);
+  uint64_t* empty = full + kStages;
+  uint64_t* q_full = empty + kStages;
+  uint64_t* q_empty = q_full + kQSlots;
+  uint64_t* acc_full = q_empty + kQSlots;
+  uint64_t* acc_empty = acc_full + kAcc;
+  uint64_t* drain = acc_empty + kAcc;
+  int* run = reinterpret_cast<int*>(smem + kOffRun);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(run + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kQSlots; ++s) {
+      tc::mbar_init(&q_full[s], 1);
+      tc::mbar_init(&q_empty[s], 1);
+    }
+    for (int s = 0; s < kAcc; ++s) {
+      tc::mbar_init(&acc_full[s], 1);
+      tc::mbar_init(&acc_empty[s], 32 * kEpiWarps);
+    }
+    tc::mbar_init(drain, 1);
+    tc::fence_mbar_init();
+    tc::tma_prefetch(&tm_keys);
+    tc::tma_prefetch(&tm_rows);
+    tc::tma_prefetch(&tm_q);
+  }
+  pdl_wait();
+  if (warp == 1) {
+    tc::tmem_alloc(tmem_slot, kAcc * kN);
+    tc::tmem_relinquish();
+  }
+  if (warp == 0) {
+    // The CTA's run.  Lane l sums the items of a contiguous share of the sequences; the lane whose share holds the
+    // run's first item walks its share for it.
+    const int per = (a.B + 31) / 32, b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      const int tiles = seq_tiles(a, b);
+      mine += (long long)tiles * a.groups;
+      if (tiles == 0 && blockIdx.x == 0) {  // reported once, and only where there is a node
+        bool used = false;
+        for (int i = 0; i < a.T; ++i) used |= __ldg(a.parent + (size_t)b * a.T + i) >= -1;
+        if (used) atomicOr(a.err, CSA_DEV_STATE);
+      }
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long n = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += n;
+    }
+    const long long total = __shfl_sync(0xffffffffu, incl, 31);
+    const long long x0 = total * blockIdx.x / gridDim.x, x1 = total * (blockIdx.x + 1) / gridDim.x;
+    if (lane == 0) run[3] = (int)(x1 - x0);
+    long long at = incl - mine;
+    if (x0 < x1 && x0 >= at && x0 < incl) {
+      for (int b = b0; b < b1; ++b) {
+        const int tiles = seq_tiles(a, b);
+        const long long here = (long long)tiles * a.groups;
+        if (x0 < at + here) {
+          run[0] = b;
+          run[1] = (int)((x0 - at) / tiles);
+          run[2] = (int)((x0 - at) % tiles);
+          break;
+        }
+        at += here;
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  bool failed = false;
+  Walk w;
+  w.start(a, run);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA
+    if (lane == 0) {
+      int stage = 0, nq = 0;
+      uint32_t phase = 0, used = 0, par = 0, q_used = 0, q_par = 0;
+      bool fresh = true;  // the next item starts a group
+      for (; w.left > 0; w.next(a)) {
+        if (fresh) {
+          const int slot = nq % kQSlots;
+          const uint32_t ph = (nq / kQSlots) & 1;
+          if (!tc::mbar_wait(&q_empty[slot], ph ^ 1)) { failed = true; break; }
+          const int row = (w.b * a.T + w.g * kG) * 64;
+          tc::mbar_arrive_expect_tx(&q_full[slot], kQBytes);
+          tc::tma_load_2d(qbuf + slot * kQBytes, &tm_q, &q_full[slot], 0, row);
+          tc::tma_load_2d(qbuf + slot * kQBytes + kQBytes / 2, &tm_q, &q_full[slot], 64, row);
+          q_used |= 1u << slot;
+          q_par = (q_par & ~(1u << slot)) | (ph << slot);
+          ++nq;
+        }
+        if (!tc::mbar_wait(&empty[stage], phase ^ 1)) { failed = true; break; }
+        const bool tree = w.t == w.tiles - 1;
+        const CUtensorMap* tm = tree ? &tm_rows : &tm_keys;
+        const int row = tree ? w.b * a.T : w.b * a.cap + w.t * kRows;
+        uint8_t* dst = kbuf + stage * kTileBytes;
+        tc::mbar_arrive_expect_tx(&full[stage], kTileBytes);
+        tc::tma_load_2d(dst, tm, &full[stage], 0, row);
+        tc::tma_load_2d(dst + kTileBytes / 2, tm, &full[stage], 64, row);
+        used |= 1u << stage;
+        par = (par & ~(1u << stage)) | (phase << stage);
+        if (++stage == kStages) { stage = 0; phase ^= 1; }
+        fresh = w.last_of_group();
+      }
+      // every load issued must land before the CTA may exit
+      for (int s = 0; s < kStages; ++s)
+        if (((used >> s) & 1) && !tc::mbar_wait(&full[s], (par >> s) & 1)) failed = true;
+      for (int s = 0; s < kQSlots; ++s)
+        if (((q_used >> s) & 1) && !tc::mbar_wait(&q_full[s], (q_par >> s) & 1)) failed = true;
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA
+    if (lane == 0) {
+      constexpr uint32_t idesc = tc::idesc_bf16(kRows, kN);
+      int stage = 0, acc = 0, nq = 0;
+      uint32_t phase = 0, acc_ph = 0;
+      bool fresh = true;
+      for (; w.left > 0; w.next(a)) {
+        if (fresh) {
+          if (!tc::mbar_wait(&q_full[nq % kQSlots], (nq / kQSlots) & 1)) { failed = true; break; }
+          ++nq;
+        }
+        const int slot = (nq - 1) % kQSlots;
+        if (!tc::mbar_wait(&full[stage], phase)) { failed = true; break; }
+        if (!tc::mbar_wait(&acc_empty[acc], acc_ph ^ 1)) { failed = true; break; }
+        tc::fence_after_sync();
+        const uint32_t a_base = tc::smem_u32(kbuf + stage * kTileBytes);
+        const uint32_t b_base = tc::smem_u32(qbuf + slot * kQBytes);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint64_t ad = tc::sdesc_kmajor_sw128(a_base + (kk >> 2) * (kTileBytes / 2) + (kk & 3) * 32);
+          const uint64_t bd = tc::sdesc_kmajor_sw128(b_base + (kk >> 2) * (kQBytes / 2) + (kk & 3) * 32);
+          tc::mma_bf16(tmem + acc * kN, ad, bd, idesc, kk > 0);
+        }
+        tc::mma_commit(&empty[stage]);
+        tc::mma_commit(&acc_full[acc]);
+        fresh = w.last_of_group();
+        if (fresh) tc::mma_commit(&q_empty[slot]);
+        if (++acc == kAcc) { acc = 0; acc_ph ^= 1; }
+        if (++stage == kStages) { stage = 0; phase ^= 1; }
+      }
+      tc::mma_commit(drain);  // every MMA retires before tensor memory is released
+      if (!tc::mbar_wait(drain, 0)) failed = true;
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3, row = quarter * 32 + lane, e = threadIdx.x - 64;
+    const int q0 = ((warp - 2) >> 2) * 2;  // this warp's two nodes of the group
+    int acc = 0;
+    uint32_t acc_ph = 0;
+    bool fresh = true;
+    uint64_t closers[2] = {0, 0};
+    bool live[2] = {false, false};
+    int n = 0;
+    for (; w.left > 0; w.next(a)) {
+      if (fresh) {
+        const int i0 = w.g * kG, cnt = min(kG, a.T - i0);
+        const size_t qb = (size_t)w.b * a.T + i0;
+        const float wt = (e >> 6) < cnt ? __bfloat162float(a.iw[qb * 64 + e]) * a.wscale : 0.f;
+        n = a.n_rows[w.b];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          bool bad = false;
+          const uint64_t m = tree_path_warp(a.parent + (size_t)w.b * a.T, a.T, min(i0 + q0 + u, a.T - 1), bad);
+          live[u] = q0 + u < cnt && m != 0;
+          closers[u] = tree_closers(m, a.pos[w.b], a.ratio);
+          if (bad && lane == 0) atomicOr(a.err, CSA_DEV_STATE);
+        }
+        tc::named_bar(1, 32 * kEpiWarps);  // the previous group's weights are no longer read
+        wbuf[e] = wt;
+        tc::named_bar(1, 32 * kEpiWarps);
+      }
+      // (after a wait that ran out, the rest of the group is walked without waiting)
+      if (!failed) failed = __any_sync(0xffffffffu, !tc::mbar_wait(&acc_full[acc], acc_ph));
+      tc::fence_after_sync();
+      uint32_t v[2][64];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + acc * kN + (q0 + u) * 64;
+        tc::tmem_ld32(ta, v[u]);
+        tc::tmem_ld32(ta + 32, v[u] + 32);
+      }
+      tc::tmem_wait_ld();
+      tc::fence_before_sync();
+      tc::mbar_arrive(&acc_empty[acc]);
+      const bool tree = w.t == w.tiles - 1;
+      const int col = tree ? n + row : w.t * kRows + row;
+      const bool in = tree ? row < a.T : col < n;
+      const float4* w4 = reinterpret_cast<const float4*>(wbuf);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        // four partial sums (heads 0, 1, 2, 3 mod 4), as two packed pairs
+        float2 s01 = make_float2(0.f, 0.f), s23 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int h4 = 0; h4 < 16; ++h4) {
+          const float4 wt = w4[(q0 + u) * 16 + h4];
+          s01 = __ffma2_rn(make_float2(wt.x, wt.y), make_float2(fmaxf(__uint_as_float(v[u][4 * h4]), 0.f),
+                                                                fmaxf(__uint_as_float(v[u][4 * h4 + 1]), 0.f)), s01);
+          s23 = __ffma2_rn(make_float2(wt.z, wt.w), make_float2(fmaxf(__uint_as_float(v[u][4 * h4 + 2]), 0.f),
+                                                                fmaxf(__uint_as_float(v[u][4 * h4 + 3]), 0.f)), s23);
+        }
+        float s = (s01.x + s01.y) + (s23.x + s23.y);
+        if (tree && !((closers[u] >> (row & 63)) & 1)) s = -INFINITY;
+        if (in && live[u])
+          a.scores[((size_t)w.b * a.T + w.g * kG + q0 + u) * (a.cap + a.T) + col] = s;
+      }
+      fresh = w.last_of_group();
+      if (++acc == kAcc) { acc = 0; acc_ph ^= 1; }
+      // one answer for the warps that share the weights' barrier
+      if (fresh && tc::named_bar_any(2, 32 * kEpiWarps, failed)) {
+        failed = true;
+        break;
+      }
+    }
+  }
+  if (failed) atomicOr(a.err, tc::kErrTimeout);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) tc::tmem_dealloc(tmem, kAcc * kN);
+}
+
+}  // namespace
+
+// (a tile's row in the key map is a 32-bit coordinate)
+bool tc_tree_scores_supported(const Dims& L, int B, int cap) {
+  return L.dtype == CSA_BF16 && L.Hi == 64 && L.Di == 128 && (long long)B * cap < INT32_MAX - kRows;
+}
+
+cudaError_t launch_tc_tree_scores(const Dims& L, const void* iq, const void* iw, int B, int T, const int32_t* parent,
+                                  const void* ikeys, int cap, const void* rows, const int32_t* n_rows,
+                                  const int32_t* pos, float* scores, int32_t* err, cudaStream_t s) {
+  int sms = 0, dev = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  CUtensorMap tk, tr, tq;
+  if (!make_tmap_2d_bf16(&tk, ikeys, (uint64_t)B * cap, 128, 256, kRows) ||
+      !make_tmap_2d_bf16(&tr, rows, (uint64_t)B * T, 128, 256, kRows) ||
+      !make_tmap_2d_bf16(&tq, iq, (uint64_t)B * T * 64, 128, 256, kN))
+    return cudaErrorInvalidValue;
+  TsArgs a{};
+  a.iw = static_cast<const __nv_bfloat16*>(iw);
+  a.parent = parent; a.pos = pos; a.n_rows = n_rows;
+  a.wscale = (float)(1.0 / sqrt((double)L.Di * (double)L.Hi));
+  a.B = B; a.T = T; a.cap = cap; a.ratio = L.ratio; a.groups = (T + kG - 1) / kG;
+  a.scores = scores; a.err = err;
+  const long long most = (long long)B * a.groups * ((cap + kRows - 1) / kRows + 1);
+  cudaFuncSetAttribute(k_tc_tree_scores, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  CSA_LAUNCH(k_tc_tree_scores, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), kSmem, s, tk, tr, tq, a);
+  return cudaGetLastError();
+}
+
+}  // namespace csa
