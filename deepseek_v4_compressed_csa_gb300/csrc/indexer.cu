@@ -12,6 +12,7 @@
 #include "common.cuh"
 #include "fp8_row.cuh"
 #include "kernels.h"
+#include "tree.cuh"
 
 namespace csa {
 
@@ -165,14 +166,60 @@ __device__ __forceinline__ int block_excl_count(int flag, int* warp_tot, int* to
   return warp_tot[wid] + inwarp;
 }
 
+// Selections of a tree's nodes (kTree instances of the top-k kernels): query q is node q % T of sequence q / T, its
+// columns are the n committed rows and the T rows of the tree (the last ones visible by the path alone), its row of
+// scores is cap + T long, and what the attention reads of the node is written to nodes[q].
+struct TopkTree {
+  const int32_t* parent;
+  int T;
+  TreeNode* nodes;
+  int32_t* err;
+};
+
+// The block's node: warp 0 looks at it and writes the record (nsel = its selected columns); every thread calls this
+// and finds the view in *sv after the barrier inside.  Returns the columns to search, 0 when there is nothing to
+// select from (an unused slot, or every visible column is selected and already written to out).
+__device__ __forceinline__ int topk_tree_node(const TopkTree& t, int q, const int32_t* pos, const int32_t* n_rows,
+                                              int cap, int ratio, int topk, int32_t* out, NodeView* sv, int* s_ok) {
+  if (threadIdx.x < 32) {
+    NodeView v;
+    const bool ok = node_view(v, t.parent, t.T, pos, n_rows, cap, ratio, q, t.err);
+    if (threadIdx.x == 0) {
+      *sv = v;
+      *s_ok = ok;
+      TreeNode r{};
+      r.nsel = -1;
+      if (ok) {
+        r.mask = v.mask; r.closers = v.closers; r.p = v.p; r.p0 = v.p0; r.n = v.n;
+        r.nsel = min(topk, v.n + __popcll(v.closers));
+      }
+      t.nodes[q] = r;
+    }
+  }
+  __syncthreads();
+  if (!*s_ok) return 0;
+  const int nvis = sv->n + __popcll(sv->closers);
+  if (nvis <= topk) {
+    for (int k = threadIdx.x; k < topk; k += blockDim.x)
+      out[k] = k < sv->n ? k : (k < nvis ? sv->n + tree_node_at(sv->closers, k - sv->n) : -1);
+    return 0;
+  }
+  return sv->n + t.T;
+}
+// The order key of column c: an invisible column's is 0, below every visible one's.
+__device__ __forceinline__ uint32_t tree_key(const NodeView& v, int c, float score) {
+  return c < v.n || ((v.closers >> (c - v.n)) & 1) ? max(ord_key(score), 1u) : 0u;
+}
+
 // Exact top-k of scores[q][0 .. nvis) by (score desc, row asc), written in
 // ascending row order.  Radix select of the k-th largest order key over four
 // 8-bit digits, then one ascending pass that keeps every row above the
 // threshold and the lowest-indexed rows equal to it.
+template <bool kTree>
 __global__ void __launch_bounds__(1024) k_topk(const float* __restrict__ scores, int cap,
                                                const int32_t* __restrict__ n_rows, const int32_t* __restrict__ pos,
                                                int pos0, const int32_t* __restrict__ cu, int ratio, int topk,
-                                               int32_t* __restrict__ sel, int32_t* __restrict__ n_sel) {
+                                               int32_t* __restrict__ sel, int32_t* __restrict__ n_sel, TopkTree tr) {
   pdl_trigger();
   pdl_wait();
   __shared__ int hist[256];
@@ -180,23 +227,33 @@ __global__ void __launch_bounds__(1024) k_topk(const float* __restrict__ scores,
   __shared__ int s_total;
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
-  const int q = blockIdx.x, bseq = query_seq(pos, pos0, cu, q);
-  const int p = query_pos(pos, pos0, cu, q);
-  const int nvis = min(min(n_rows[bseq], cap), (p + 1) / ratio);
+  __shared__ NodeView s_view;
+  __shared__ int s_ok;
+  const int q = blockIdx.x;
   int32_t* out = sel + (size_t)q * topk;
-  if (nvis <= topk) {
-    for (int i = threadIdx.x; i < topk; i += blockDim.x) out[i] = (i < nvis) ? i : -1;
-    if (threadIdx.x == 0) n_sel[q] = max(nvis, 0);
-    return;
+  int nvis;
+  if constexpr (kTree) {
+    nvis = topk_tree_node(tr, q, pos, n_rows, cap, ratio, topk, out, &s_view, &s_ok);
+    if (nvis == 0) return;
+  } else {
+    const int bseq = query_seq(pos, pos0, cu, q);
+    const int p = query_pos(pos, pos0, cu, q);
+    nvis = min(min(n_rows[bseq], cap), (p + 1) / ratio);
+    if (nvis <= topk) {
+      for (int i = threadIdx.x; i < topk; i += blockDim.x) out[i] = (i < nvis) ? i : -1;
+      if (threadIdx.x == 0) n_sel[q] = max(nvis, 0);
+      return;
+    }
   }
-  const float* sc = scores + (size_t)q * cap;
+  const float* sc = scores + (size_t)q * (kTree ? cap + tr.T : cap);
+  auto key = [&](int j) { return kTree ? tree_key(s_view, j, sc[j]) : ord_key(sc[j]); };
   uint32_t prefix = 0, mask = 0;
   int need = topk;  // rank (1-based, from the top) of the threshold among keys matching prefix
   for (int shift = 24; shift >= 0; shift -= 8) {
     for (int i = threadIdx.x; i < 256; i += blockDim.x) hist[i] = 0;
     __syncthreads();
     for (int j = threadIdx.x; j < nvis; j += blockDim.x) {
-      const uint32_t u = ord_key(sc[j]);
+      const uint32_t u = key(j);
       if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1);
     }
     __syncthreads();
@@ -219,7 +276,7 @@ __global__ void __launch_bounds__(1024) k_topk(const float* __restrict__ scores,
   int eq_base = 0, out_base = 0;
   for (int j0 = 0; j0 < nvis; j0 += blockDim.x) {
     const int j = j0 + threadIdx.x;
-    uint32_t u = (j < nvis) ? ord_key(sc[j]) : 0u;
+    uint32_t u = (j < nvis) ? key(j) : 0u;
     const int eq = (j < nvis) && (u == prefix);
     const int gt = (j < nvis) && (u > prefix);
     const int eq_rank = eq_base + block_excl_count(eq, warp_tot, &s_total);
@@ -232,7 +289,7 @@ __global__ void __launch_bounds__(1024) k_topk(const float* __restrict__ scores,
     out_base += take_tot;
   }
   for (int i = out_base + threadIdx.x; i < topk; i += blockDim.x) out[i] = -1;
-  if (threadIdx.x == 0) n_sel[q] = min(out_base, topk);
+  if (!kTree && threadIdx.x == 0) n_sel[q] = min(out_base, topk);
 }
 
 // Inclusive prefix sum over the 1024 threads of the block (one value each).
@@ -346,35 +403,46 @@ __device__ __forceinline__ void select_bin_every_warp(const int* h, int& need, u
 // histograms; the bucket holding the k-th key is found by a block-wide scan
 // over the bins in descending order), then one ascending pass that keeps the
 // keys above the threshold and the lowest-indexed keys equal to it.
+template <bool kTree>
 __global__ void __launch_bounds__(1024) k_topk_smem(const float* __restrict__ scores, int cap,
                                                     const int32_t* __restrict__ n_rows,
                                                     const int32_t* __restrict__ pos, int pos0,
                                                     const int32_t* __restrict__ cu, int ratio, int topk,
-                                                    int32_t* __restrict__ sel, int32_t* __restrict__ n_sel) {
+                                                    int32_t* __restrict__ sel, int32_t* __restrict__ n_sel, TopkTree tr) {
   pdl_trigger();
   pdl_wait();
-  extern __shared__ uint32_t sm_keys[];  // [cap] keys, then hist[2048]
-  int* hist = reinterpret_cast<int*>(sm_keys + cap);
+  extern __shared__ uint32_t sm_keys[];  // [cap (+ T)] keys, then hist[2048]
+  const int stride = kTree ? cap + tr.T : cap;
+  int* hist = reinterpret_cast<int*>(sm_keys + stride);
   __shared__ int warp_tot[32];
   __shared__ int s_total;
   __shared__ uint32_t s_prefix;
   __shared__ int s_need, s_count;
-  const int q = blockIdx.x, bseq = query_seq(pos, pos0, cu, q);
-  const int p = query_pos(pos, pos0, cu, q);
-  const int nvis = min(min(n_rows[bseq], cap), (p + 1) / ratio);
+  __shared__ NodeView s_view;
+  __shared__ int s_ok;
+  const int q = blockIdx.x;
   int32_t* out = sel + (size_t)q * topk;
-  if (nvis <= topk) {
-    for (int i = threadIdx.x; i < topk; i += blockDim.x) out[i] = (i < nvis) ? i : -1;
-    if (threadIdx.x == 0) n_sel[q] = max(nvis, 0);
-    return;
+  int nvis;
+  if constexpr (kTree) {
+    nvis = topk_tree_node(tr, q, pos, n_rows, cap, ratio, topk, out, &s_view, &s_ok);
+    if (nvis == 0) return;
+  } else {
+    const int bseq = query_seq(pos, pos0, cu, q);
+    const int p = query_pos(pos, pos0, cu, q);
+    nvis = min(min(n_rows[bseq], cap), (p + 1) / ratio);
+    if (nvis <= topk) {
+      for (int i = threadIdx.x; i < topk; i += blockDim.x) out[i] = (i < nvis) ? i : -1;
+      if (threadIdx.x == 0) n_sel[q] = max(nvis, 0);
+      return;
+    }
   }
-  const float* sc = scores + (size_t)q * cap;
+  const float* sc = scores + (size_t)q * stride;
   // the first digit's histogram is counted while the keys are stored
   for (int i = threadIdx.x; i < 2048; i += blockDim.x) hist[i] = 0;
   __syncthreads();
 #pragma unroll 4
   for (int j = threadIdx.x; j < nvis; j += blockDim.x) {
-    const uint32_t u = ord_key(__ldg(sc + j));
+    const uint32_t u = kTree ? tree_key(s_view, j, __ldg(sc + j)) : ord_key(__ldg(sc + j));
     sm_keys[j] = u;
     atomicAdd(&hist[u >> 21], 1);
   }
@@ -466,7 +534,7 @@ __global__ void __launch_bounds__(1024) k_topk_smem(const float* __restrict__ sc
   }
   const int total = s_total;
   for (int i2 = total + threadIdx.x; i2 < topk; i2 += blockDim.x) out[i2] = -1;
-  if (threadIdx.x == 0) n_sel[q] = min(total, topk);
+  if (!kTree && threadIdx.x == 0) n_sel[q] = min(total, topk);
 }
 
 // Exact top-k with every key in registers, for up to kTopkRegKeys x 1024 visible rows: thread t owns the
@@ -508,40 +576,51 @@ __device__ __forceinline__ void score_rows(const __nv_bfloat16* __restrict__ qr,
 // qr / w / keys non-null: the scan before this kernel covered rows < floor(p/ratio) only (it ran while the index
 // pool's compress call for this token could still write); the rows that call may have written (row
 // floor(p/ratio) and row n_rows-1) are scored here and replace what the score buffer holds for them.
+template <bool kTree>
 __global__ void __launch_bounds__(1024) k_topk_reg(const float* __restrict__ scores, int cap,
                                                    const int32_t* __restrict__ n_rows, const int32_t* __restrict__ pos,
                                                    int pos0, const int32_t* __restrict__ cu, int ratio, int topk,
                                                    int32_t* __restrict__ sel,
                                                    int32_t* __restrict__ n_sel, const __nv_bfloat16* __restrict__ qr,
-                                                   const float* __restrict__ w, const __nv_bfloat16* __restrict__ keys) {
+                                                   const float* __restrict__ w, const __nv_bfloat16* __restrict__ keys,
+                                                   TopkTree tr) {
   pdl_trigger();
   __shared__ int hist[3][2048];  // pass n counts into hist[n] and clears the next pass's bins
   __shared__ int warp_tot[32], warp_tot2[32];
   __shared__ float part[2][64];
   __shared__ float new_score[2];
-  const int q = blockIdx.x, bseq = query_seq(pos, pos0, cu, q);
+  __shared__ NodeView s_view;
+  __shared__ int s_ok;
+  const int q = blockIdx.x, bseq = kTree ? q / tr.T : query_seq(pos, pos0, cu, q);
   // The position is a step input (no kernel of the step writes it), so the most rows this query can see, and so
   // this thread's rows, are known before the wait: the score loads then go out in the same round as n_rows.
-  const int p = query_pos(pos, pos0, cu, q);
-  const int nv_max = max(0, min(cap, (p + 1) / ratio));
+  const int p = kTree ? pos[bseq] : query_pos(pos, pos0, cu, q);
+  const int nv_max = kTree ? max(0, min(cap, p / ratio)) + tr.T : max(0, min(cap, (p + 1) / ratio));
   const int K = max(1, (nv_max + 1023) >> 10);
   const int r0 = threadIdx.x * K;
-  const float* sc = scores + (size_t)q * cap + r0;
+  const float* sc = scores + (size_t)q * (kTree ? cap + tr.T : cap) + r0;
   pdl_wait();
   float fk[kTopkRegKeys];
 #pragma unroll
   for (int i = 0; i < kTopkRegKeys; ++i) fk[i] = (i < K && r0 + i < nv_max) ? __ldg(sc + i) : 0.f;
-  const int nvis = min(min(n_rows[bseq], cap), nv_max);
   int32_t* out = sel + (size_t)q * topk;
-  if (nvis <= topk) {
-    for (int i = threadIdx.x; i < topk; i += blockDim.x) out[i] = (i < nvis) ? i : -1;
-    if (threadIdx.x == 0) n_sel[q] = max(nvis, 0);
-    return;
+  int nvis;
+  if constexpr (kTree) {
+    nvis = topk_tree_node(tr, q, pos, n_rows, cap, ratio, topk, out, &s_view, &s_ok);
+    if (nvis == 0) return;
+  } else {
+    nvis = min(min(n_rows[bseq], cap), nv_max);
+    if (nvis <= topk) {
+      for (int i = threadIdx.x; i < topk; i += blockDim.x) out[i] = (i < nvis) ? i : -1;
+      if (threadIdx.x == 0) n_sel[q] = max(nvis, 0);
+      return;
+    }
   }
   uint32_t uk[kTopkRegKeys];
 #pragma unroll
-  for (int i = 0; i < kTopkRegKeys; ++i) uk[i] = (i < K && r0 + i < nvis) ? ord_key(fk[i]) : 0u;
-  if (qr) {
+  for (int i = 0; i < kTopkRegKeys; ++i)
+    uk[i] = (i < K && r0 + i < nvis) ? (kTree ? tree_key(s_view, r0 + i, fk[i]) : ord_key(fk[i])) : 0u;
+  if (!kTree && qr) {
     const int j0 = min(cap, p / ratio), jl = min(n_rows[bseq], cap) - 1;
     const int jr[2] = {j0 < nvis ? j0 : -1, (jl >= 0 && jl < nvis && jl != j0) ? jl : -1};
     score_rows(qr, w, keys + (size_t)bseq * cap * 128, q, jr, part, new_score);
@@ -627,7 +706,7 @@ __global__ void __launch_bounds__(1024) k_topk_reg(const float* __restrict__ sco
     }
   }
   for (int i = total + threadIdx.x; i < topk; i += blockDim.x) out[i] = -1;
-  if (threadIdx.x == 0) n_sel[q] = min(total, topk);
+  if (!kTree && threadIdx.x == 0) n_sel[q] = min(total, topk);
 }
 
 constexpr int kTopkSmemMaxCap = 52 * 1024;
@@ -635,18 +714,41 @@ constexpr int kTopkSmemMaxCap = 52 * 1024;
 static cudaError_t launch_topk(const Dims& L, const float* scores, int cap, const int32_t* n_rows, const int32_t* pos,
                         int pos0, const int32_t* cu, int Q, int32_t* sel, int32_t* n_sel, cudaStream_t s) {
   if (cap <= kTopkRegKeys * 1024) {
-    CSA_LAUNCH(k_topk_reg, dim3(Q), dim3(1024), 0, s, scores, cap, n_rows, pos, pos0, cu, L.ratio, L.topk, sel, n_sel,
-               static_cast<const __nv_bfloat16*>(nullptr), static_cast<const float*>(nullptr),
-               static_cast<const __nv_bfloat16*>(nullptr));
+    CSA_LAUNCH(k_topk_reg<false>, dim3(Q), dim3(1024), 0, s, scores, cap, n_rows, pos, pos0, cu, L.ratio, L.topk, sel,
+               n_sel, static_cast<const __nv_bfloat16*>(nullptr), static_cast<const float*>(nullptr),
+               static_cast<const __nv_bfloat16*>(nullptr), TopkTree{});
   } else if (cap <= kTopkSmemMaxCap) {
     const size_t smem = (size_t)cap * 4 + 2048 * 4;
-    cudaFuncSetAttribute(k_topk_smem, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    CSA_LAUNCH(k_topk_smem, dim3(Q), dim3(1024), smem, s, scores, cap, n_rows, pos, pos0, cu, L.ratio, L.topk, sel,
-               n_sel);
+    cudaFuncSetAttribute(k_topk_smem<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    CSA_LAUNCH(k_topk_smem<false>, dim3(Q), dim3(1024), smem, s, scores, cap, n_rows, pos, pos0, cu, L.ratio, L.topk,
+               sel, n_sel, TopkTree{});
   } else {
-    CSA_LAUNCH(k_topk, dim3(Q), dim3(1024), 0, s, scores, cap, n_rows, pos, pos0, cu, L.ratio, L.topk, sel, n_sel);
+    CSA_LAUNCH(k_topk<false>, dim3(Q), dim3(1024), 0, s, scores, cap, n_rows, pos, pos0, cu, L.ratio, L.topk, sel, n_sel,
+               TopkTree{});
   }
   return cudaSuccess;
+}
+
+cudaError_t launch_topk_tree(const Dims& L, const float* scores, int B, int T, const int32_t* parent, int cap,
+                             const int32_t* n_rows, const int32_t* pos, int32_t* sel, TreeNode* nodes, int32_t* err,
+                             cudaStream_t s) {
+  const TopkTree tr{parent, T, nodes, err};
+  const int32_t* none = nullptr;
+  int32_t* no_count = nullptr;
+  if (cap + T <= kTopkRegKeys * 1024) {
+    CSA_LAUNCH(k_topk_reg<true>, dim3(B * T), dim3(1024), 0, s, scores, cap, n_rows, pos, 0, none, L.ratio, L.topk, sel,
+               no_count, static_cast<const __nv_bfloat16*>(nullptr), static_cast<const float*>(nullptr),
+               static_cast<const __nv_bfloat16*>(nullptr), tr);
+  } else if (cap + T <= kTopkSmemMaxCap) {
+    const size_t smem = (size_t)(cap + T) * 4 + 2048 * 4;
+    cudaFuncSetAttribute(k_topk_smem<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    CSA_LAUNCH(k_topk_smem<true>, dim3(B * T), dim3(1024), smem, s, scores, cap, n_rows, pos, 0, none, L.ratio, L.topk,
+               sel, no_count, tr);
+  } else {
+    CSA_LAUNCH(k_topk<true>, dim3(B * T), dim3(1024), 0, s, scores, cap, n_rows, pos, 0, none, L.ratio, L.topk, sel,
+               no_count, tr);
+  }
+  return cudaGetLastError();
 }
 
 template <typename T>
@@ -693,9 +795,9 @@ cudaError_t launch_index_topk_overlapped(const Dims& L, const void* iq, const vo
   }
   const auto* qr = reinterpret_cast<const __nv_bfloat16*>(ws.qr);
   const auto* w = reinterpret_cast<const float*>(reinterpret_cast<const char*>(ws.qr) + (size_t)Q * 64 * 128 * 2);
-  CSA_LAUNCH(k_topk_reg, dim3(Q), dim3(1024), 0, s, ws.scores, cap, n_rows, pos, 0,
+  CSA_LAUNCH(k_topk_reg<false>, dim3(Q), dim3(1024), 0, s, ws.scores, cap, n_rows, pos, 0,
              static_cast<const int32_t*>(nullptr), L.ratio, L.topk, sel, n_sel, qr,
-             w, static_cast<const __nv_bfloat16*>(ikeys));
+             w, static_cast<const __nv_bfloat16*>(ikeys), TopkTree{});
   return cudaGetLastError();
 }
 

@@ -282,9 +282,20 @@ bool tc_tree_scores_supported(const Dims& L, int B, int cap);
 cudaError_t launch_tc_tree_scores(const Dims& L, const void* iq, const void* iw, int B, int T, const int32_t* parent,
                                   const void* ikeys, int cap, const void* rows, const int32_t* n_rows,
                                   const int32_t* pos, float* scores, int32_t* err, cudaStream_t s);
+// What the attention kernels read of a node: its path and the path's completing nodes as masks, its position, the
+// committed length and rows of its sequence, and its keys' count from the pool and the draft rows (nsel < 0: an
+// unused slot, or a node that an error skips).
+struct TreeNode {
+  unsigned long long mask, closers;
+  int32_t p, p0, n, nsel;
+};
+// ---- indexer.cu: the selection of every node (sel [B*T, topk], columns of scores [B*T, cap + T]; nodes [B*T])
+cudaError_t launch_topk_tree(const Dims& L, const float* scores, int B, int T, const int32_t* parent, int cap,
+                             const int32_t* n_rows, const int32_t* pos, int32_t* sel, TreeNode* nodes, int32_t* err,
+                             cudaStream_t s);
 struct TreeAttendWs {
   int32_t* sel;    // [B*T, topk] when the caller wants no selection (null without an indexer)
-  int32_t* n_sel;  // [B*T]
+  TreeNode* nodes; // [B*T]
 };
 TreeAttendWs carve_attend_tree(Carver& c, const Dims& L, int B, int T, int cap);
 struct TreeAttend {
@@ -297,6 +308,12 @@ struct TreeAttend {
   TreeAttendWs ws;
 };
 cudaError_t launch_attend_tree(const Dims& L, const TreeAttend& t, int32_t* err, cudaStream_t s);
+// The same on the tensor cores (tc_attend_supported shapes), the node records already in t.ws: a CTA per query
+// streaming its tiles (tc_attend_prefill.cu), or S <= 4 splits per query merged in a cluster (tc_attend_decode.cu).
+cudaError_t launch_tc_attend_tree(const Dims& L, const TreeAttend& t, const int32_t* sel, int32_t* err,
+                                  cudaStream_t s);
+cudaError_t launch_tc_attend_tree_split(const Dims& L, const TreeAttend& t, const int32_t* sel, int S, int32_t* err,
+                                        cudaStream_t s);
 // Pool 0: the attention pool; pool 1 (npool == 2): the index pool.
 struct TreeCommit {
   const int32_t *parent, *leaf, *pos;

@@ -34,6 +34,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
+#include "tree.cuh"
 
 namespace csa {
 
@@ -69,7 +70,10 @@ constexpr int kOffTmem = kOffBars + 8 * 8;
 constexpr int kSmem = kOffTmem + 16 + 1024;     // + alignment slack
 static_assert(kSmem <= 232448, "shared memory per block");
 
-// row codes: >= 0 pool row (b * cap + j); kRowNone: empty; kRowNew: the new token; <= kRowRing0: ring row
+// row codes: >= 0 pool row (b * cap + j); kRowNone: empty; kRowNew: the new token; <= kRowRing0: ring row.  A tree's
+// nodes (kTree): kRowRing0 - kTreeKv - (b * T + node) is a node's latent row, kRowRing0 - kTreeRow - (b * T + node) the
+// compressed row that it completes.
+constexpr int kTreeKv = 1 << 28, kTreeRow = 1 << 29;
 constexpr int kRowNone = -1;
 constexpr int kRowNew = -2;
 constexpr int kRowRing0 = -3;
@@ -90,6 +94,12 @@ struct DecArgs {
   int qps;                      // consecutive queries per sequence (a verify block; 1 for decode)
   int kv_in_ring;               // the new tokens are already in the ring (verify): none is roped here
   int cluster;                  // S in {2, 4}: the S splits of a query are one cluster and merge through DSMEM
+  // a tree's nodes (kTree; q already rotated): query q is node q % T of sequence q / T
+  const int32_t* parent;        // [B, T]
+  const TreeNode* nodes;        // [B * T], written by the kernel before
+  const __nv_bfloat16* tkv;     // [B, T, 512] the nodes' latent rows
+  const __nv_bfloat16* trows;   // [B, T, 512] the rows that they complete
+  int T_;
   float scale2;                 // softmax scale * log2(e)
   float* part_ml;
   float* part_acc;
@@ -123,14 +133,29 @@ __device__ __forceinline__ float2 reduce_scatter64(float (&v)[64]) {
 struct Item {
   int q, s, b, p, nwin, w_begin, nw;  // before the wait
   int nrows, nsel, s_begin, ns;       // after it
+  int p0;                             // kTree: the committed length, the path, its completing nodes
+  uint64_t mask, closers;
 };
 
+template <bool kTree>
 __device__ __forceinline__ Item make_item(const DecArgs& a) {
   Item it;
   it.q = blockIdx.x / a.S;
   it.s = blockIdx.x % a.S;
-  it.b = it.q / a.qps;
-  it.p = a.pos[it.b] + it.q % a.qps;
+  it.mask = it.closers = 0;
+  it.p0 = 0;
+  if constexpr (kTree) {
+    // the parents and positions are step inputs: the window share is known before the wait (a node that an error
+    // skips is found after it)
+    it.b = it.q / a.T_;
+    it.p0 = a.pos[it.b];
+    bool bad = false;
+    it.mask = tree_path_warp(a.parent + (size_t)it.b * a.T_, a.T_, it.q % a.T_, bad);
+    it.p = it.mask && it.p0 >= 0 ? it.p0 + __popcll(it.mask) - 1 : -1;
+  } else {
+    it.b = it.q / a.qps;
+    it.p = a.pos[it.b] + it.q % a.qps;
+  }
   it.nwin = it.p >= 0 ? min(a.W, it.p + 1) : 0;
   const int wper = (it.nwin + a.S - 1) / a.S;
   it.w_begin = min(it.nwin, it.s * wper);
@@ -140,31 +165,60 @@ __device__ __forceinline__ Item make_item(const DecArgs& a) {
 }
 
 // the selection share (reads the predecessors' outputs: call after the programmatic wait)
-__device__ __forceinline__ void item_selection(const DecArgs& a, Item& it) {
+template <bool kTree>
+__device__ __forceinline__ bool item_selection(const DecArgs& a, Item& it) {
+  if constexpr (kTree) {
+    const TreeNode r = a.nodes[it.q];
+    if (r.nsel < 0) {  // an unused slot, or skipped: no rows, no output
+      it.nw = it.ns = 0;
+      return false;
+    }
+    it.nrows = r.n;
+    it.nsel = r.nsel;
+    it.closers = r.closers;
+  } else {
   it.nrows = min(a.n_rows[it.b], a.cap);
   it.nsel = a.sel ? min(max(a.n_sel[it.q], 0), a.topk) : max(0, min(it.nrows, (it.p + 1) / a.ratio));
+  }
   const int sper = (it.nsel + a.S - 1) / a.S;
   it.s_begin = min(it.nsel, it.s * sper);
   it.ns = min(it.nsel, it.s_begin + sper) - it.s_begin;
   if (it.nw + it.ns > kCR) it.ns = max(0, kCR - it.nw);  // callers keep both shares within one tile
+  return true;
 }
 
 // Code of window token w (0 .. nwin-1, oldest first) and of selected row k (0 .. nsel-1; j = sel[q][k] when a
 // selection is given); an out-of-range selection is reported and left empty.
+template <bool kTree>
 __device__ __forceinline__ int window_code(const DecArgs& a, const Item& it, int w) {
   const int tok = it.p - it.nwin + 1 + w;
+  if constexpr (kTree) {
+    if (tok >= it.p0) return kRowRing0 - kTreeKv - (it.b * a.T_ + tree_node_at(it.mask, tok - it.p0));
+    return kRowRing0 - (it.b * a.Wr + tok % a.Wr);
+  }
   if (tok == it.p && !a.kv_in_ring) return kRowNew;
   return kRowRing0 - (it.b * a.Wr + tok % a.Wr);
 }
+template <bool kTree>
 __device__ __forceinline__ int selected_code(const DecArgs& a, const Item& it, int k, int j) {
+  if constexpr (kTree) {  // column j of the selection, or of all visible columns (see launch_topk_tree)
+    if (!a.sel) j = k < it.nrows ? k : it.nrows + tree_node_at(it.closers, k - it.nrows);
+    return j < it.nrows ? it.b * a.cap + j : kRowRing0 - kTreeRow - (it.b * a.T_ + (j - it.nrows));
+  }
   if (!a.sel) j = k;
   if (j >= 0 && j < it.nrows) return it.b * a.cap + j;
   atomicOr(a.err, CSA_DEV_RANGE);
   return kRowNone;
 }
 
+template <bool kTree>
 __device__ __forceinline__ const __nv_bfloat16* code_ptr(const DecArgs& a, int code) {
   if (code >= 0) return a.pool + (size_t)code * kAD;
+  if constexpr (kTree) {
+    const int x = kRowRing0 - code;
+    if (x >= kTreeRow) return a.trows + (size_t)(x - kTreeRow) * kAD;
+    if (x >= kTreeKv) return a.tkv + (size_t)(x - kTreeKv) * kAD;
+  }
   if (code <= kRowRing0) return a.ring + (size_t)(kRowRing0 - code) * kAD;
   return nullptr;
 }
@@ -220,13 +274,14 @@ __device__ __forceinline__ void write_p(uint8_t* pbuf, int row, const float (&sv
 
 // Copy tile rows [r0, r1) from their codes (cp.async, 2 x 512 contiguous bytes per warp instruction; rows spread
 // over the main warps); an empty row is zero-filled and the new token is skipped (roped separately).
+template <bool kTree>
 __device__ __forceinline__ void gather_rows(const DecArgs& a, const int* rowc, uint32_t r_base, int r0, int r1) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll 4
   for (int r = r0 + warp; r < r1; r += kMainWarps) {
     const int code = rowc[r];
     if (code == kRowNew) continue;
-    const __nv_bfloat16* src = code_ptr(a, code);
+    const __nv_bfloat16* src = code_ptr<kTree>(a, code);
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
       const int ch = lane + 32 * hh;
@@ -237,7 +292,9 @@ __device__ __forceinline__ void gather_rows(const DecArgs& a, const int* rowc, u
   }
 }
 
-// S > 1 writes (m, l, acc) partials for the merge kernel; S == 1 finalises directly.
+// S > 1 writes (m, l, acc) partials for the merge kernel; S == 1 finalises directly.  kTree: the nodes of trees
+// (csa_attend_tree); S is 1 or a cluster, and the output is rounded once, after its rotation.
+template <bool kTree>
 __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
@@ -268,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
     tc::mbar_init(drain, 1);
     tc::fence_mbar_init();
   }
-  Item it = make_item(a);
+  Item it = make_item<kTree>(a);
   const uint32_t r_base = tc::smem_u32(rows), q_base = tc::smem_u32(qbuf);
   if (warp < kMainWarps) {
     // ---- before the programmatic wait: the query block, the RoPE table, this split's window rows and the new
@@ -283,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
                        qsrc + (size_t)h * kAD + ch * 8, 16u);
       }
     }
-    if (row < it.nw) rowc[row] = window_code(a, it, it.w_begin + row);
+    if (row < it.nw) rowc[row] = window_code<kTree>(a, it, it.w_begin + row);
     if (tid < 32) {
       float cs, sn;
       rope_cs(it.p, a.inv_freq, tid, &cs, &sn);
@@ -291,10 +348,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
       rsin[tid] = sn;
     }
     tc::named_bar(1, kMain);
-    gather_rows(a, rowc, r_base, 0, it.nw);
+    gather_rows<kTree>(a, rowc, r_base, 0, it.nw);
     // the new token (the window's last): RoPE at p, into the tile and into its ring slot (the slot belongs to the
     // token leaving the window, which no CTA reads)
-    const int cur_row = (!a.kv_in_ring && it.nw > 0 && it.w_begin + it.nw == it.nwin) ? it.nw - 1 : -1;
+    const int cur_row = (!kTree && !a.kv_in_ring && it.nw > 0 && it.w_begin + it.nw == it.nwin) ? it.nw - 1 : -1;
     if (cur_row >= 0 && warp == cur_row % kMainWarps) {
       const __nv_bfloat16* cur = a.kv_new + (size_t)it.b * kAD;
 #pragma unroll
@@ -309,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
     tc::cp_async_wait_all();
     tc::named_bar(1, kMain);  // every thread's share of the query block has landed
 #pragma unroll
-    for (int e = tid; e < kAH * 8; e += kMain) {
+    for (int e = tid; !kTree && e < kAH * 8; e += kMain) {
       const int h = e >> 3, ch = 56 + (e & 7);
       uint4* slot = reinterpret_cast<uint4*>(qbuf + (ch >> 3) * kQBox + h * 128 + (((ch & 7) ^ (h & 7)) << 4));
       uint4 raw = *slot;
@@ -328,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
   const uint32_t tmem = *tmem_slot;
   const uint32_t tm_s = tmem;  // S^T: rows 0-127 in cols 0-63, rows 128-255 in cols 64-127
   const uint32_t tm_o = tmem;  // O^T tile m: cols 128m + (0-63: P_hi part, 64-127: P_lo part); overwrites S^T
-  item_selection(a, it);
+  const bool live = item_selection<kTree>(a, it);
   const int nr = it.nw + it.ns;
   bool failed = false;
 
@@ -377,10 +434,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
     if (row >= it.nw) {
       const int k = it.s_begin + (row - it.nw);
       const int j = (a.sel && row < nr) ? a.sel[(size_t)it.q * a.topk + k] : 0;
-      rowc[row] = row < nr ? selected_code(a, it, k, j) : kRowNone;
+      rowc[row] = row < nr ? selected_code<kTree>(a, it, k, j) : kRowNone;
     }
     tc::named_bar(1, kMain);
-    gather_rows(a, rowc, r_base, it.nw, kCR);
+    gather_rows<kTree>(a, rowc, r_base, it.nw, kCR);
     tc::cp_async_wait_all();
     tc::fence_proxy_async_smem();
     tc::fence_before_sync();
@@ -556,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
         }
         const float invZ = tab[h * (S + 1) + S];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = rnd<__nv_bfloat16>(v[e] * invZ);
+        for (int e = 0; e < 4; ++e) v[e] = kTree ? v[e] * invZ : rnd<__nv_bfloat16>(v[e] * invZ);
         if (d >= kAD - 64) {
 #pragma unroll
           for (int e = 0; e < 4; e += 2) {
@@ -570,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
         __nv_bfloat162* hv = reinterpret_cast<__nv_bfloat162*>(&pk);
         hv[0] = __floats2bfloat162_rn(v[0], v[1]);
         hv[1] = __floats2bfloat162_rn(v[2], v[3]);
-        *reinterpret_cast<uint2*>(a.out + ((size_t)it.q * kAH + h) * kAD + d) = pk;
+        if (!kTree || live) *reinterpret_cast<uint2*>(a.out + ((size_t)it.q * kAH + h) * kAD + d) = pk;
         }
       }
     }
@@ -591,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
           for (int h = 0; h < 64; ++h) dst[(size_t)h * kAD] = o[h];
         }
       }
-    } else {
+    } else if (!kTree || live) {
       for (int m = m0; m < m0 + 2; ++m) {
         const int d = 128 * m + dl;
         float o[64];
@@ -604,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
           const float M2 = fmaxf(z2, mr);
           const float f = mr == -INFINITY ? 0.f : exp2f(mr - M2);
           const float Z = exp2f(z2 - M2) + lsum[h] * f;
-          float v = rnd<__nv_bfloat16>(o[h] * (f / Z));
+          float v = kTree ? o[h] * (f / Z) : rnd<__nv_bfloat16>(o[h] * (f / Z));
           const float partner = __shfl_xor_sync(0xffffffffu, v, 1);
           if (d >= kAD - 64) {
             const int i = (d - (kAD - 64)) >> 1;
@@ -660,7 +717,7 @@ bool tc_attend_decode_cluster(int S) {
   static int known[5] = {-1, -1, -1, -1, -1};
   if (S != 2 && S != 4) return false;
   if (known[S] < 0) {
-    cudaFuncSetAttribute(k_tc_attend_decode, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cudaFuncSetAttribute(k_tc_attend_decode<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(S);
     cfg.blockDim = dim3(kThreads);
@@ -673,7 +730,7 @@ bool tc_attend_decode_cluster(int S) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, k_tc_attend_decode, &cfg);
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, k_tc_attend_decode<false>, &cfg);
     if (e != cudaSuccess) cudaGetLastError();  // leave no sticky error behind
     known[S] = (e == cudaSuccess && n > 0) ? 1 : 0;
   }
@@ -699,13 +756,41 @@ cudaError_t launch_tc_attend_decode(const Dims& L, const void* q, const void* po
   a.part_ml = part_ml; a.part_acc = part_acc;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.err = err;
-  cudaFuncSetAttribute(k_tc_attend_decode, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaFuncSetAttribute(k_tc_attend_decode<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (cluster) {
     if (S != 2 && S != 4) return cudaErrorInvalidValue;
-    const cudaError_t e = launch_pdl_cluster(k_tc_attend_decode, dim3(Q * S), dim3(kThreads), kSmem, s, S, a);
+    const cudaError_t e = launch_pdl_cluster(k_tc_attend_decode<false>, dim3(Q * S), dim3(kThreads), kSmem, s, S, a);
     if (e != cudaSuccess) return e;
   } else {
-    CSA_LAUNCH(k_tc_attend_decode, dim3(Q * S), dim3(kThreads), kSmem, s, a);
+    CSA_LAUNCH(k_tc_attend_decode<false>, dim3(Q * S), dim3(kThreads), kSmem, s, a);
+  }
+  return cudaGetLastError();
+}
+
+// A tree's nodes (csa_attend_tree): B * T queries of S splits each (S 1, or 2 or 4 as a cluster).
+cudaError_t launch_tc_attend_tree_split(const Dims& L, const TreeAttend& t, const int32_t* sel, int S, int32_t* err,
+                                        cudaStream_t s) {
+  const int Q = t.B * t.T;
+  DecArgs a{};
+  a.cluster = S > 1 ? 1 : 0;
+  a.qps = 1;
+  a.q = static_cast<const __nv_bfloat16*>(t.q);
+  a.pool = static_cast<const __nv_bfloat16*>(t.pool);
+  a.ring = static_cast<__nv_bfloat16*>(const_cast<void*>(t.window));  // (read only here: no token is appended)
+  a.sel = sel; a.n_rows = t.n_rows; a.pos = t.pos; a.sink = t.sink; a.inv_freq = t.inv_freq;
+  a.cap = t.cap; a.topk = L.topk; a.W = L.W; a.Wr = L.Wr; a.ratio = L.ratio; a.S = S;
+  a.parent = t.parent; a.nodes = t.ws.nodes; a.T_ = t.T;
+  a.tkv = static_cast<const __nv_bfloat16*>(t.kv);
+  a.trows = static_cast<const __nv_bfloat16*>(t.rows);
+  a.scale2 = L.scale * 1.4426950408889634f;
+  a.out = static_cast<__nv_bfloat16*>(t.out);
+  a.err = err;
+  cudaFuncSetAttribute(k_tc_attend_decode<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (S > 1) {
+    const cudaError_t e = launch_pdl_cluster(k_tc_attend_decode<true>, dim3(Q * S), dim3(kThreads), kSmem, s, S, a);
+    if (e != cudaSuccess) return e;
+  } else {
+    CSA_LAUNCH(k_tc_attend_decode<true>, dim3(Q), dim3(kThreads), kSmem, s, a);
   }
   return cudaGetLastError();
 }

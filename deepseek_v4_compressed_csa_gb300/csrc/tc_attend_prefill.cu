@@ -37,6 +37,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
+#include "tree.cuh"
 
 namespace csa {
 
@@ -96,6 +97,10 @@ struct PfArgs {
   int T, pos0, cap, topk, W, ratio;
   int Wr;                      // ring slots (W + rollback); a query attends its last W tokens
   int chunk_tiles;             // T >= 128: 128-row boxes of the chunk's rows are available
+  // a tree's nodes (kTree; q already rotated): query q is node q % tree_T of sequence q / tree_T; the chunk's map
+  // holds the nodes' latent rows [B, tree_T, 512], the chunk tiles' map the rows that they complete
+  const TreeNode* nodes;
+  int tree_T;
   float scale2;                // softmax scale * log2(e)
   __nv_bfloat16* out;          // [T, 64, 512]
   int32_t* err;
@@ -103,10 +108,28 @@ struct PfArgs {
 
 struct Query {
   int b, p, nsel, nwin, nrows, ntiles;
+  int p0;                  // kTree
+  uint64_t mask, closers;
 };
 
+template <bool kTree>
 __device__ __forceinline__ Query query_info(const PfArgs& a, int qi) {
   Query r;
+  r.p0 = 0;
+  r.mask = r.closers = 0;
+  if constexpr (kTree) {
+    const TreeNode n = a.nodes[qi];
+    r.b = qi / a.tree_T;
+    r.p = n.p;
+    r.p0 = n.p0;
+    r.mask = n.mask;
+    r.closers = n.closers;
+    r.nrows = n.n;
+    r.nsel = n.nsel;
+    r.nwin = min(a.W, n.p + 1);
+    r.ntiles = n.nsel < 0 ? 0 : (r.nsel + r.nwin + kPR - 1) / kPR;  // 0: an unused slot, every role passes it over
+    return r;
+  }
   if (a.cu) {
     r.b = varlen_seq(a.cu, a.nseq, qi);
     r.p = a.pos[r.b] + qi - __ldg(a.cu + r.b);
@@ -125,8 +148,22 @@ __device__ __forceinline__ Query query_info(const PfArgs& a, int qi) {
 // code is its row in the pool tensor map (b * cap + j); a window token's is kRowTok0 - token for a chunk, and
 // kRowTok0 - (b * Wr + token mod Wr), its ring row, for verify blocks; in a variable-length batch, kRowTok0 -
 // its ring row (tokens before the sequence's chunk) or kRowTok0 - (kChunkFlag + its packed chunk row).
+// Of a tree's node (kTree): kRowTok0 - its ring row, - (kTreeKv + its row of the nodes' latents) or - (kTreeRow + its
+// row of the completed rows).
 constexpr int kChunkFlag = 1 << 29;
+constexpr int kTreeKv = 1 << 28, kTreeRow = 1 << 29;
+template <bool kTree>
 __device__ __forceinline__ int row_code(const PfArgs& a, const Query& qu, int r_abs, int j) {
+  if constexpr (kTree) {
+    if (r_abs < qu.nsel) {
+      if (!a.sel) j = r_abs < qu.nrows ? r_abs : qu.nrows + tree_node_at(qu.closers, r_abs - qu.nrows);
+      return j < qu.nrows ? qu.b * a.cap + j : kRowTok0 - (kTreeRow + qu.b * a.tree_T + (j - qu.nrows));
+    }
+    if (r_abs >= qu.nsel + qu.nwin) return kRowNone;
+    const int tok = qu.p - qu.nwin + 1 + (r_abs - qu.nsel);
+    if (tok < qu.p0) return kRowTok0 - (qu.b * a.Wr + tok % a.Wr);
+    return kRowTok0 - (kTreeKv + qu.b * a.tree_T + tree_node_at(qu.mask, tok - qu.p0));
+  }
   if (r_abs < qu.nsel) {
     if (!a.sel) j = r_abs;
     if (j >= 0 && j < qu.nrows) return qu.b * a.cap + j;
@@ -147,12 +184,20 @@ __device__ __forceinline__ int row_code(const PfArgs& a, const Query& qu, int r_
 }
 
 // Tensor map of a row: the pool, the chunk's roped rows, the ring before the chunk; kSrcNone: empty row.
-constexpr int kSrcPool = 0, kSrcChunk = 1, kSrcRing = 2, kSrcNone = 3;
+constexpr int kSrcPool = 0, kSrcChunk = 1, kSrcRing = 2, kSrcNone = 3, kSrcTreeRow = 4;
 
+template <bool kTree>
 __device__ __forceinline__ int row_src(const PfArgs& a, int code, int& row) {
   if (code >= 0) {
     row = code;
     return kSrcPool;
+  }
+  if constexpr (kTree) {
+    const int x = kRowTok0 - code;
+    row = 0;
+    if (x < 0) return kSrcNone;
+    row = x >= kTreeRow ? x - kTreeRow : (x >= kTreeKv ? x - kTreeKv : x);
+    return x >= kTreeRow ? kSrcTreeRow : (x >= kTreeKv ? kSrcChunk : kSrcRing);
   }
   if (code <= kRowTok0) {
     const int tok = kRowTok0 - code;
@@ -176,7 +221,8 @@ __device__ __forceinline__ int row_src(const PfArgs& a, int code, int& row) {
 }
 
 __device__ __forceinline__ const CUtensorMap* src_map(int src, const CUtensorMap* pool, const CUtensorMap* chunk,
-                                                      const CUtensorMap* ring) {
+                                                      const CUtensorMap* ring, const CUtensorMap* tree_rows) {
+  if (src == kSrcTreeRow) return tree_rows;
   return src == kSrcPool ? pool : (src == kSrcChunk ? chunk : ring);
 }
 
@@ -225,6 +271,7 @@ __device__ __forceinline__ void rope4(uint4& raw, const float (&rc)[4], const fl
   }
 }
 
+template <bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
     k_tc_attend_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_pool,
                         const __grid_constant__ CUtensorMap tm_kvr, const __grid_constant__ CUtensorMap tm_ring,
@@ -287,7 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t r_base = tc::smem_u32(rows), q_base = tc::smem_u32(qbuf), p_base = tc::smem_u32(pbuf);
       uint32_t nq = 0, nt = 0;
       for (int qi = blockIdx.x; qi < a.T && !failed; qi += gridDim.x, ++nq) {
-        const int ntiles = query_info(a, qi).ntiles;
+        const int ntiles = query_info<kTree>(a, qi).ntiles;
+        if (kTree && ntiles == 0) { --nq; continue; }
         if (!tc::mbar_wait(q_full, nq & 1)) { failed = true; break; }
         tc::fence_after_sync();
         for (int t = 0; t < ntiles; ++t, ++nt) {
@@ -349,14 +397,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     uint32_t nq = 0, nt = 0;
     for (int qi = blockIdx.x; qi < a.T && !failed; qi += gridDim.x, ++nq) {
-      const Query qu = query_info(a, qi);
+      const Query qu = query_info<kTree>(a, qi);
+      if (kTree && qu.ntiles == 0) { --nq; continue; }
       // codes of this thread's rows (lt, lt + 64) of a tile
       auto codes = [&](int t, int& x0, int& x1) {
         const int ra = t * kPR + lt, rb = ra + 64;
         const int ja = (a.sel && ra < qu.nsel) ? a.sel[(size_t)qi * a.topk + ra] : 0;
         const int jb = (a.sel && rb < qu.nsel) ? a.sel[(size_t)qi * a.topk + rb] : 0;
-        x0 = row_code(a, qu, ra, ja);
-        x1 = row_code(a, qu, rb, jb);
+        x0 = row_code<kTree>(a, qu, ra, ja);
+        x1 = row_code<kTree>(a, qu, rb, jb);
       };
       int c0, c1;
       codes(0, c0, c1);
@@ -374,13 +423,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rch = 56 + (lt & 7);
       float rcs[4], rsn[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) rope_cs(qu.p, a.inv_freq, (rch - 56) * 4 + k, &rcs[k], &rsn[k]);
+      for (int k = 0; !kTree && k < 4; ++k) rope_cs(qu.p, a.inv_freq, (rch - 56) * 4 + k, &rcs[k], &rsn[k]);
       if (tc::named_bar_any(kBarLoad, kLoaders, !tc::mbar_wait(q_loaded, nq & 1))) {
         failed = true;
         break;
       }
 #pragma unroll
-      for (int h = lt >> 3; h < kAH; h += kLoaders / 8) {
+      for (int h = lt >> 3; !kTree && h < kAH; h += kLoaders / 8) {
         uint4* slot = reinterpret_cast<uint4*>(qbuf + 7 * kQBox + h * 128 + (((rch & 7) ^ (h & 7)) << 4));
         uint4 raw = *slot;
         rope4(raw, rcs, rsn);
@@ -404,14 +453,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool same = true;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          src[i] = row_src(a, rowc[g4 + i], row[i]);
+          src[i] = row_src<kTree>(a, rowc[g4 + i], row[i]);
           same &= src[i] == src[0];
         }
         same &= src[0] != kSrcNone;
         // a tile of 128 consecutive chunk rows (a window in the chunk): one 128-row box load per 64 dims
         int row_first, row_last;
-        const bool chunk_tile = a.chunk_tiles && row_src(a, rowc[0], row_first) == kSrcChunk &&
-                                row_src(a, rowc[kPR - 1], row_last) == kSrcChunk;
+        const bool chunk_tile = !kTree && a.chunk_tiles && row_src<kTree>(a, rowc[0], row_first) == kSrcChunk &&
+                                row_src<kTree>(a, rowc[kPR - 1], row_last) == kSrcChunk;
         for (int m = 0; m < 4; ++m) {
           if (m > 0 && nt > 0 && tc::named_bar_any(kBarLoad, kLoaders, !tc::mbar_wait(box_free + m, par))) {
             failed = true;
@@ -428,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           } else if (same) {
             tc::mbar_arrive_expect_tx(rows_full + m, 4 * 128);
-            tc::tma_gather4(dst, src_map(src[0], &tm_pool, &tm_kvr, &tm_ring), rows_full + m, 64 * box, row[0], row[1],
+            tc::tma_gather4(dst, src_map(src[0], &tm_pool, &tm_kvr, &tm_ring, &tm_kvr_tile), rows_full + m, 64 * box, row[0], row[1],
                             row[2], row[3]);
           } else {
             // rows from different sources, or empty rows: one-row loads, zeros written here
@@ -447,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if (src[i] != kSrcNone)
-                tc::tma_load_2d(dst + i * 128, src_map(src[i], &tm_pool, &tm_kvr, &tm_ring), rows_full + m, 64 * box,
+                tc::tma_load_2d(dst + i * 128, src_map(src[i], &tm_pool, &tm_kvr, &tm_ring, &tm_kvr_tile), rows_full + m, 64 * box,
                                 row[i]);
           }
         }
@@ -466,7 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float l[32];
     uint32_t nq = 0, nt = 0;
     for (int qi = blockIdx.x; qi < a.T && !failed; qi += gridDim.x, ++nq) {
-      const Query qu = query_info(a, qi);
+      const Query qu = query_info<kTree>(a, qi);
+      if (kTree && qu.ntiles == 0) { --nq; continue; }
       for (int t = 0; t < qu.ntiles; ++t, ++nt) {
         if (tc::named_bar_any(bar_half, kHalf, !tc::mbar_wait(s_full, nt & 1))) {
           failed = true;
@@ -603,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool rot = (m == 3) && quad >= 2;
 #pragma unroll
         for (int h = 0; h < 32; ++h) {
-          float v = rnd<__nv_bfloat16>(o[h] * f[h]);
+          float v = kTree ? o[h] * f[h] : rnd<__nv_bfloat16>(o[h] * f[h]);  // kTree: one rounding, at the end
           const float partner = __shfl_xor_sync(0xffffffffu, v, 1);
           if (rot) v = (d & 1) ? fmaf(-partner, rs, v * rc) : fmaf(v, rc, partner * rs);
           obase[(size_t)(hb + h) * kAD + d] = __float2bfloat16_rn(v);
@@ -667,8 +717,36 @@ cudaError_t launch_tc_attend_prefill(const Dims& L, const void* q, const void* p
       !make_tmap_2d_bf16(&tr, ring, (uint64_t)nseq * L.Wr, kAD, kAD * 2, 1) ||
       !make_tmap_2d_bf16(&tkt, kvr, (uint64_t)T, kAD, kAD * 2, a.chunk_tiles ? kPR : 1))
     return cudaErrorInvalidValue;
-  cudaFuncSetAttribute(k_tc_attend_prefill, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  CSA_LAUNCH(k_tc_attend_prefill, dim3(min(T, g_sms_pf)), dim3(kThreads), kSmem, s, tq, tp, tk, tr, tkt, a);
+  cudaFuncSetAttribute(k_tc_attend_prefill<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  CSA_LAUNCH(k_tc_attend_prefill<false>, dim3(min(T, g_sms_pf)), dim3(kThreads), kSmem, s, tq, tp, tk, tr, tkt, a);
+  return cudaGetLastError();
+}
+
+// A tree's nodes (csa_attend_tree): B * T queries, a persistent CTA per SM.
+cudaError_t launch_tc_attend_tree(const Dims& L, const TreeAttend& t, const int32_t* sel, int32_t* err,
+                                  cudaStream_t s) {
+  if (!g_sms_pf) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&g_sms_pf, cudaDevAttrMultiProcessorCount, dev);
+  }
+  const int Q = t.B * t.T;
+  PfArgs a{};
+  a.sel = sel; a.sink = t.sink; a.inv_freq = t.inv_freq;
+  a.T = Q; a.cap = t.cap; a.topk = L.topk; a.W = L.W; a.Wr = L.Wr; a.ratio = L.ratio; a.qps = 1;
+  a.nodes = t.ws.nodes; a.tree_T = t.T;
+  a.scale2 = L.scale * 1.4426950408889634f;
+  a.out = static_cast<__nv_bfloat16*>(t.out);
+  a.err = err;
+  CUtensorMap tq, tp, tk, tr, trow;
+  if (!make_tmap_2d_bf16(&tq, t.q, (uint64_t)Q * kAH, kAD, kAD * 2, 64) ||
+      !make_tmap_2d_bf16(&tp, t.pool, (uint64_t)t.B * t.cap, kAD, kAD * 2, 1) ||
+      !make_tmap_2d_bf16(&tk, t.kv, (uint64_t)Q, kAD, kAD * 2, 1) ||
+      !make_tmap_2d_bf16(&tr, t.window, (uint64_t)t.B * L.Wr, kAD, kAD * 2, 1) ||
+      !make_tmap_2d_bf16(&trow, t.rows, (uint64_t)Q, kAD, kAD * 2, 1))
+    return cudaErrorInvalidValue;
+  cudaFuncSetAttribute(k_tc_attend_prefill<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  CSA_LAUNCH(k_tc_attend_prefill<true>, dim3(min(Q, g_sms_pf)), dim3(kThreads), kSmem, s, tq, tp, tk, tr, trow, a);
   return cudaGetLastError();
 }
 

@@ -292,28 +292,6 @@ __global__ void __launch_bounds__(256) k_tree_pool(TreePool<T> pa, TreePool<T> p
   }
 }
 
-// ---------------------------------------------------------------- a node's view of its sequence
-struct NodeView {
-  uint64_t mask, closers;  // the path; its nodes that complete a window
-  int b, i, p0, p, n;      // sequence, node, committed length, the node's position, committed rows
-};
-// One warp, every lane; false: an unused slot, or a state error (reported by lane 0).
-__device__ __forceinline__ bool node_view(NodeView& v, const int32_t* parent, int T_, const int32_t* pos,
-                                          const int32_t* n_rows, int cap, int ratio, int q, int32_t* err) {
-  v.b = q / T_;
-  v.i = q - v.b * T_;
-  v.p0 = pos[v.b];
-  v.n = n_rows[v.b];
-  bool bad = false;
-  v.mask = tree_path_warp(parent + (size_t)v.b * T_, T_, v.i, bad);
-  const bool state = v.p0 < 0 || v.n != v.p0 / ratio || v.n > cap;
-  if ((bad || (state && v.mask)) && (threadIdx.x & 31) == 0) atomicOr(err, CSA_DEV_STATE);
-  if (state || v.mask == 0) return false;
-  v.p = v.p0 + __popcll(v.mask) - 1;
-  v.closers = tree_closers(v.mask, v.p0, ratio);
-  return true;
-}
-
 // ---------------------------------------------------------------- index scores
 // Block (node, column share): one warp per column in turn, a lane per head.
 template <typename T>
@@ -367,101 +345,6 @@ __global__ void __launch_bounds__(256) k_tree_scores(const T* __restrict__ iq, c
   }
 }
 
-// ---------------------------------------------------------------- selection
-// The topk largest scores of a node's visible columns (columns below n, and n + a for the path's completing nodes
-// a), ties to the lower column, in ascending order, padded with -1; every visible column where there are no more.
-// An invisible column's key is 0, below every score's.  Radix select over four 8-bit digits, then one ascending pass.
-__global__ void __launch_bounds__(1024) k_tree_topk(const float* __restrict__ scores, int cap, int T_,
-                                                    const int32_t* __restrict__ parent,
-                                                    const int32_t* __restrict__ pos,
-                                                    const int32_t* __restrict__ n_rows, int ratio, int topk,
-                                                    int32_t* __restrict__ sel, int32_t* __restrict__ n_sel,
-                                                    int32_t* err) {
-  pdl_trigger();
-  __shared__ NodeView sv;
-  __shared__ int s_ok, s_need, s_total;
-  __shared__ uint32_t s_prefix;
-  __shared__ int hist[256], warp_tot[32];
-  pdl_wait();
-  const int q = blockIdx.x, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  if (wid == 0) {
-    NodeView v;
-    const bool ok = node_view(v, parent, T_, pos, n_rows, cap, ratio, q, err);
-    if (lane == 0) {
-      sv = v;
-      s_ok = ok;
-    }
-  }
-  __syncthreads();
-  if (!s_ok) {
-    if (tid == 0) n_sel[q] = 0;
-    return;
-  }
-  const int n = sv.n, extra = __popcll(sv.closers), nvis = n + extra;
-  int32_t* out = sel + (size_t)q * topk;
-  if (nvis <= topk) {
-    for (int k = tid; k < topk; k += 1024)
-      out[k] = k < n ? k : (k < nvis ? n + tree_node_at(sv.closers, k - n) : -1);
-    if (tid == 0) n_sel[q] = nvis;
-    return;
-  }
-  const float* sc = scores + (size_t)q * (cap + T_);
-  const int ncol = n + T_;
-  auto key = [&](int c) { return c < n || ((sv.closers >> (c - n)) & 1) ? max(ord_key(sc[c]), 1u) : 0u; };
-  uint32_t prefix = 0, mask = 0;
-  int need = topk;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int c = tid; c < ncol; c += 1024) {
-      const uint32_t u = key(c);
-      if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1);
-    }
-    __syncthreads();
-    if (tid == 0) {
-      int c = 0, bkt;
-      for (bkt = 255; bkt > 0; --bkt) {
-        if (c + hist[bkt] >= need) break;
-        c += hist[bkt];
-      }
-      s_need = need - c;
-      s_prefix = prefix | ((uint32_t)bkt << shift);
-    }
-    __syncthreads();
-    need = s_need;
-    prefix = s_prefix;
-    mask |= 255u << shift;
-  }
-  int eq_base = 0, out_base = 0;
-  for (int c0 = 0; c0 < ncol; c0 += 1024) {
-    const int c = c0 + tid;
-    const uint32_t u = c < ncol ? key(c) : 0u;
-    // keys equal to the threshold keep the lowest columns; both counts in one scan (each below 2^16)
-    const int mine = (c < ncol && u > prefix ? 1 << 16 : 0) | (c < ncol && u == prefix ? 1 : 0);
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
-    __syncthreads();
-    if (lane == 31) warp_tot[wid] = incl;
-    __syncthreads();
-    int before = 0;
-    for (int w = 0; w < wid; ++w) before += warp_tot[w];
-    if (tid == 1023) s_total = before + incl;
-    __syncthreads();
-    const int excl = before + incl - mine;
-    const int eq_before = eq_base + (excl & 0xffff);
-    const int slot = out_base + (excl >> 16) + min(eq_before, need);
-    const bool take = (mine >> 16) || ((mine & 1) && eq_before < need);
-    if (take && slot < topk) out[slot] = c;
-    eq_base += s_total & 0xffff;
-    out_base += s_total >> 16;
-  }
-  if (tid == 0) n_sel[q] = topk;
-}
-
 // ---------------------------------------------------------------- attention
 template <typename T>
 struct TreeAttnArgs {
@@ -470,18 +353,36 @@ struct TreeAttnArgs {
   const T* window;  // [B, Wr, D]
   const T* pool;    // [B, cap, D]
   const T* rows;    // [B, T, D] rows that the tree's paths complete
-  const int32_t* sel;
-  const int32_t* n_sel;
-  const int32_t* n_rows;
-  const int32_t* parent;
-  const int32_t* pos;
+  const int32_t* sel;  // [Q, topk] columns, or null: every visible one
+  const TreeNode* nodes;
   const float* sink;
   const float* inv_freq;
-  int T_, H, D, R, W, Wr, cap, topk, ratio;
+  int T_, H, D, R, W, Wr, cap, topk;
   float scale;
   T* out;
-  int32_t* err;
 };
+
+// One warp per node: the records of a call without a selection.
+__global__ void __launch_bounds__(256) k_tree_nodes(const int32_t* __restrict__ parent, int T_, int Q,
+                                                    const int32_t* __restrict__ pos,
+                                                    const int32_t* __restrict__ n_rows, int cap, int ratio,
+                                                    TreeNode* __restrict__ nodes, int32_t* err) {
+  pdl_trigger();
+  pdl_wait();
+  const int q = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (q >= Q) return;
+  NodeView v;
+  const bool ok = node_view(v, parent, T_, pos, n_rows, cap, ratio, q, err);
+  if ((threadIdx.x & 31) == 0) {
+    TreeNode r{};
+    r.nsel = -1;
+    if (ok) {
+      r.mask = v.mask; r.closers = v.closers; r.p = v.p; r.p0 = v.p0; r.n = v.n;
+      r.nsel = v.n + __popcll(v.closers);
+    }
+    nodes[q] = r;
+  }
+}
 
 // Block (node, head): chunks of 64 keys (selected rows, then the window's tokens), logits one warp per key, then
 // each thread accumulates its dims; the running maximum and sum in fp32, the sink once at the end.
@@ -490,25 +391,13 @@ __global__ void __launch_bounds__(128) k_tree_attend(TreeAttnArgs<T> a) {
   pdl_trigger();
   constexpr int kKeys = 64, kMaxC = 8;
   extern __shared__ float sm_ta[];  // [D] query
-  __shared__ NodeView sv;
-  __shared__ int s_ok;
   __shared__ const T* kp[kKeys];
   __shared__ float lg[kKeys];
   pdl_wait();
   const int h = blockIdx.y, q = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (warp == 0) {
-    NodeView v;
-    const bool ok = node_view(v, a.parent, a.T_, a.pos, a.n_rows, a.cap, a.ratio, q, a.err);
-    if (lane == 0) {
-      sv = v;
-      s_ok = ok;
-    }
-  }
-  __syncthreads();
-  if (!s_ok) return;
-  const int nclose = __popcll(sv.closers);
-  const int nsel = a.sel ? a.n_sel[q] : sv.n + nclose;
-  const int nwin = min(a.W, sv.p + 1), nkeys = nsel + nwin;
+  const TreeNode sv = a.nodes[q];
+  if (sv.nsel < 0) return;
+  const int b = q / a.T_, nsel = sv.nsel, nwin = min(a.W, sv.p + 1), nkeys = nsel + nwin;
   float* qs = sm_ta;
   for (int e = tid; e < a.D; e += 128) qs[e] = to_f(a.q[((size_t)q * a.H + h) * a.D + e]);
   float acc[kMaxC];
@@ -523,11 +412,11 @@ __global__ void __launch_bounds__(128) k_tree_attend(TreeAttnArgs<T> a) {
       const T* r;
       if (k < nsel) {
         int c = a.sel ? a.sel[(size_t)q * a.topk + k] : (k < sv.n ? k : sv.n + tree_node_at(sv.closers, k - sv.n));
-        r = c < sv.n ? a.pool + ((size_t)sv.b * a.cap + c) * a.D : a.rows + ((size_t)sv.b * a.T_ + (c - sv.n)) * a.D;
+        r = c < sv.n ? a.pool + ((size_t)b * a.cap + c) * a.D : a.rows + ((size_t)b * a.T_ + (c - sv.n)) * a.D;
       } else {
         const int t = sv.p - nwin + 1 + (k - nsel);
-        r = t < sv.p0 ? a.window + ((size_t)sv.b * a.Wr + t % a.Wr) * a.D
-                      : a.kv + ((size_t)sv.b * a.T_ + tree_node_at(sv.mask, t - sv.p0)) * a.D;
+        r = t < sv.p0 ? a.window + ((size_t)b * a.Wr + t % a.Wr) * a.D
+                      : a.kv + ((size_t)b * a.T_ + tree_node_at(sv.mask, t - sv.p0)) * a.D;
       }
       kp[tid] = r;
     }
@@ -716,10 +605,8 @@ cudaError_t launch_index_scores_tree(const Dims& L, const void* iq, const void* 
 TreeAttendWs carve_attend_tree(Carver& c, const Dims& L, int B, int T, int cap) {
   TreeAttendWs w{};
   (void)cap;
-  if (L.has_indexer()) {
-    w.sel = c.take<int32_t>((size_t)B * T * L.topk);
-    w.n_sel = c.take<int32_t>((size_t)B * T);
-  }
+  w.nodes = c.take<TreeNode>((size_t)B * T);
+  if (L.has_indexer()) w.sel = c.take<int32_t>((size_t)B * T * L.topk);
   return w;
 }
 
@@ -729,16 +616,31 @@ static cudaError_t attend_tree_t(const Dims& L, const TreeAttend& t, int32_t* er
   TreeAttnArgs<T> a{};
   if (t.scores) {
     int32_t* sel = t.sel_out ? t.sel_out : t.ws.sel;
-    CSA_LAUNCH(k_tree_topk, dim3(Q), dim3(1024), 0, s, t.scores, t.cap, t.T, t.parent, t.pos, t.n_rows, L.ratio,
-               L.topk, sel, t.ws.n_sel, err);
+    cudaError_t e = launch_topk_tree(L, t.scores, t.B, t.T, t.parent, t.cap, t.n_rows, t.pos, sel, t.ws.nodes, err, s);
+    if (e != cudaSuccess) return e;
     a.sel = sel;
-    a.n_sel = t.ws.n_sel;
+  } else {
+    CSA_LAUNCH(k_tree_nodes, dim3((Q + 7) / 8), dim3(256), 0, s, t.parent, t.T, Q, t.pos, t.n_rows, t.cap, L.ratio,
+               t.ws.nodes, err);
+  }
+  // Tensor-core shapes.  Few nodes: S splits of one 160-row tile each, a cluster per query, while every split has an
+  // SM.  More: a CTA per query streaming its tiles.
+  const bool codes_fit = (long long)t.B * t.cap < INT32_MAX && (long long)t.B * L.Wr < (1 << 28);
+  if (tc_attend_supported(L) && codes_fit) {
+    int sms = 0, dev = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int n_max = t.scores ? L.topk : t.cap + t.T;
+    for (int S = 1; S <= 4; S *= 2)
+      if ((L.W + S - 1) / S + (n_max + S - 1) / S <= 160 && (long)Q * S <= sms && (S == 1 || tc_attend_decode_cluster(S)))
+        return launch_tc_attend_tree_split(L, t, a.sel, S, err, s);
+    return launch_tc_attend_tree(L, t, a.sel, err, s);
   }
   a.q = static_cast<const T*>(t.q); a.kv = static_cast<const T*>(t.kv); a.window = static_cast<const T*>(t.window);
   a.pool = static_cast<const T*>(t.pool); a.rows = static_cast<const T*>(t.rows);
-  a.n_rows = t.n_rows; a.parent = t.parent; a.pos = t.pos; a.sink = t.sink; a.inv_freq = t.inv_freq;
+  a.nodes = t.ws.nodes; a.sink = t.sink; a.inv_freq = t.inv_freq;
   a.T_ = t.T; a.H = L.H; a.D = L.D; a.R = L.R; a.W = L.W; a.Wr = L.Wr; a.cap = t.cap; a.topk = L.topk;
-  a.ratio = L.ratio; a.scale = L.scale; a.out = static_cast<T*>(t.out); a.err = err;
+  a.scale = L.scale; a.out = static_cast<T*>(t.out);
   CSA_LAUNCH(k_tree_attend<T>, dim3(Q, L.H), dim3(128), L.D * sizeof(float), s, a);
   return cudaGetLastError();
 }

@@ -96,4 +96,26 @@ __device__ __forceinline__ uint64_t tree_closers(uint64_t mask, int p0, int rati
   return c;
 }
 
+// ---------------------------------------------------------------- a node's view of its sequence
+struct NodeView {
+  uint64_t mask, closers;  // the path; its nodes that complete a window
+  int b, i, p0, p, n;      // sequence, node, committed length, the node's position, committed rows
+};
+// One warp, every lane; false: an unused slot, or a state error (reported by lane 0).
+__device__ __forceinline__ bool node_view(NodeView& v, const int32_t* parent, int T_, const int32_t* pos,
+                                          const int32_t* n_rows, int cap, int ratio, int q, int32_t* err) {
+  v.b = q / T_;
+  v.i = q - v.b * T_;
+  v.p0 = pos[v.b];
+  v.n = n_rows[v.b];
+  bool bad = false;
+  v.mask = tree_path_warp(parent + (size_t)v.b * T_, T_, v.i, bad);
+  const bool state = v.p0 < 0 || v.n != v.p0 / ratio || v.n > cap;
+  if ((bad || (state && v.mask)) && (threadIdx.x & 31) == 0) atomicOr(err, CSA_DEV_STATE);
+  if (state || v.mask == 0) return false;
+  v.p = v.p0 + __popcll(v.mask) - 1;
+  v.closers = tree_closers(v.mask, v.p0, ratio);
+  return true;
+}
+
 }  // namespace csa
