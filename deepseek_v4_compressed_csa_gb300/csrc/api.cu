@@ -103,6 +103,12 @@ size_t ws_prefill(const Dims& L, int T, int cap) {
 bool tree_sizes_ok(int B, int T) {
   return B >= 1 && B <= 65535 && T >= 1 && T <= 64 && (long long)B * T <= (1 << 18);
 }
+size_t ws_compress_tree(const Dims& L, bool both, int B, int T) {
+  Carver c(nullptr);
+  carve_compress_tree(c, L, L.D, B, T);
+  if (both) carve_compress_tree(c, L, L.Di, B, T);
+  return c.off;
+}
 size_t ws_attend_tree(const Dims& L, int B, int T, int cap) {
   Carver c(nullptr);
   carve_attend_tree(c, L, B, T, cap);
@@ -166,7 +172,7 @@ csa_status csa_workspace_size(const csa_layer* layer, int op, int B, int T, int 
       return CSA_OK;
     case CSA_OP_COMPRESS_TREE:
       if (!tree_sizes_ok(B, T)) return CSA_ERR_ARG;
-      *bytes = L.has_indexer() ? ws_compress_pair(L, B, T) : ws_compress(L, L.D, B, T);
+      *bytes = ws_compress_tree(L, L.has_indexer(), B, T);
       return CSA_OK;
     case CSA_OP_ATTEND_TREE:
       if (!tree_sizes_ok(B, T)) return CSA_ERR_ARG;
@@ -495,12 +501,12 @@ csa_status csa_compress_tree(const csa_layer* layer, const csa_compressor* comp_
                  !dev_tensor(rows_i)))
     return CSA_ERR_ARG;
   if (!dev_tensor(x) || !dev_i32(parent) || !dev_tensor(inv_freq) || !dev_i32(err)) return CSA_ERR_ARG;
-  const size_t need = comp_i ? ws_compress_pair(L, B, T) : ws_compress(L, L.D, B, T);
-  if (ws_bytes < need || !dev_tensor(ws)) return CSA_ERR_WORKSPACE;
+  const size_t need = ws_compress_tree(L, comp_i != nullptr, B, T);
+  if (ws_bytes < need || (need && !dev_tensor(ws))) return CSA_ERR_WORKSPACE;
   Carver c(ws);
   TreeCompress pools[2] = {};
-  pools[0] = TreeCompress{comp_a, frontier_a, proj_a, rows_a, carve_compress(c, L, L.D, B, T)};
-  if (comp_i) pools[1] = TreeCompress{comp_i, frontier_i, proj_i, rows_i, carve_compress(c, L, L.Di, B, T)};
+  pools[0] = TreeCompress{comp_a, frontier_a, proj_a, rows_a, carve_compress_tree(c, L, L.D, B, T)};
+  if (comp_i) pools[1] = TreeCompress{comp_i, frontier_i, proj_i, rows_i, carve_compress_tree(c, L, L.Di, B, T)};
   return cuda_status(launch_compress_tree(L, pools, comp_i ? 2 : 1, x, B, T, parent, pos, inv_freq, err,
                                           static_cast<cudaStream_t>(stream)));
 }

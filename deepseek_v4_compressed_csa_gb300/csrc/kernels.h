@@ -261,15 +261,21 @@ cudaError_t launch_attend_verify(const Dims& L, const void* q, const void* kv_ne
 // ---- tree.cu (a tree of drafted tokens; parent [B, T], T <= 64)
 cudaError_t launch_norm_rope(const Dims& L, const csa_rows* rows, int n, int B, int T, const int32_t* parent,
                              const int32_t* pos, const float* inv_freq, int32_t* err, cudaStream_t s);
-// One pool of a compress call: the committed frontier, and the draft buffers proj [B, T, 2*L*d] and rows [B, T, d]
-// (ws carved by carve_compress for B x T tokens).
+// One pool of a compress call: the committed frontier, and the draft buffers proj [B, T, 2*L*d] and rows [B, T, d].
+// ws: [B*T, 2*L*d] of the model dtype for the SIMT projection, which projects unused slots too (null where the
+// tensor-core projection applies).
 struct TreeCompress {
   const csa_compressor* comp;
   const void* frontier;
   void* proj;
   void* rows;
-  CompressWs ws;
+  void* ws;
 };
+void* carve_compress_tree(Carver& c, const Dims& L, int d, int B, int T);
+// ---- tc_tree_project.cu: the projections of all pools into the draft buffers (bf16; whole 128-feature tiles)
+bool tc_tree_project_supported(const Dims& L, int d);
+cudaError_t launch_tc_tree_project(const Dims& L, const TreeCompress* pools, int npool, const void* x, int B, int T,
+                                   const int32_t* parent, const int32_t* pos, int32_t* err, cudaStream_t s);
 cudaError_t launch_compress_tree(const Dims& L, const TreeCompress* pools, int npool, const void* x, int B, int T,
                                  const int32_t* parent, const int32_t* pos, const float* inv_freq, int32_t* err,
                                  cudaStream_t s);

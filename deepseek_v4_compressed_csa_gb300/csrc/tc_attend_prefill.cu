@@ -58,6 +58,9 @@ constexpr int kMmaWarp = kSoftWarps;     // warp 8: TMEM owner and MMA issuer
 constexpr int kLoadWarp0 = kMmaWarp + 1; // warps 9-10
 constexpr int kLoaders = 64;
 constexpr int kThreads = kSoft + 32 + kLoaders;
+// A tree's nodes: four loader warps, a row per thread (see the loaders)
+constexpr int kTreeLoadWarps = kPR / 32;
+constexpr int kTreeThreads = kSoft + 32 + 32 * kTreeLoadWarps;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColO3 = 384;         // O^T tile 3 (hi + lo in one accumulator)
 constexpr uint32_t kColS = 448;          // S^T
@@ -97,9 +100,10 @@ struct PfArgs {
   int T, pos0, cap, topk, W, ratio;
   int Wr;                      // ring slots (W + rollback); a query attends its last W tokens
   int chunk_tiles;             // T >= 128: 128-row boxes of the chunk's rows are available
-  // a tree's nodes (kTree; q already rotated): query q is node q % tree_T of sequence q / tree_T; the chunk's map
-  // holds the nodes' latent rows [B, tree_T, 512], the chunk tiles' map the rows that they complete
+  // a tree's nodes (kTree; q already rotated): query q is node q % tree_T of sequence q / tree_T; kvr holds the nodes'
+  // latent rows [B, tree_T, 512], trows the rows that they complete; rows are copied by address, without tensor maps
   const TreeNode* nodes;
+  const __nv_bfloat16* trows;
   int tree_T;
   float scale2;                // softmax scale * log2(e)
   __nv_bfloat16* out;          // [T, 64, 512]
@@ -221,8 +225,7 @@ __device__ __forceinline__ int row_src(const PfArgs& a, int code, int& row) {
 }
 
 __device__ __forceinline__ const CUtensorMap* src_map(int src, const CUtensorMap* pool, const CUtensorMap* chunk,
-                                                      const CUtensorMap* ring, const CUtensorMap* tree_rows) {
-  if (src == kSrcTreeRow) return tree_rows;
+                                                      const CUtensorMap* ring) {
   return src == kSrcPool ? pool : (src == kSrcChunk ? chunk : ring);
 }
 
@@ -272,7 +275,7 @@ __device__ __forceinline__ void rope4(uint4& raw, const float (&rc)[4], const fl
 }
 
 template <bool kTree>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kTree ? kTreeThreads : kThreads, 1)
     k_tc_attend_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_pool,
                         const __grid_constant__ CUtensorMap tm_kvr, const __grid_constant__ CUtensorMap tm_ring,
                         const __grid_constant__ CUtensorMap tm_kvr_tile, PfArgs a) {
@@ -300,10 +303,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    tc::mbar_init(q_full, kLoaders);
+    tc::mbar_init(q_full, kTree ? 1 : kLoaders);
     tc::mbar_init(q_empty, 1);
     for (int m = 0; m < 4; ++m) {
-      tc::mbar_init(rows_full + m, kLoaders);  // one arrival (with its bytes) per loader thread
+      // one arrival (with its bytes) per loader thread; a tree's loaders: one per warp
+      tc::mbar_init(rows_full + m, kTree ? kTreeLoadWarps : kLoaders);
       tc::mbar_init(box_free + m, 1);
     }
     tc::mbar_init(s_full, 1);
@@ -385,6 +389,95 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     failed = __shfl_sync(0xffffffffu, (int)failed, 0) != 0;
+  } else if (kTree && warp >= kLoadWarp0) {
+    // ------------------------------------------------------------ loaders of a tree's nodes (warps 9-12)
+    // Warp w copies rows 32w .. 32w + 31 of a tile, 256 bytes of each row per box pair: a lane knows the address of
+    // one row, an instruction copies two rows' 512 bytes, and a pair's 16 instructions a warp are one commit group, up
+    // to three of them in flight.  A tile takes 8 x 32 tile::gather4 requests otherwise, which the copy engine serves
+    // at ~7 B a clock per SM (the tile then lasts 11.7 us, four fifths of it waiting); four warps of 16-byte copies
+    // keep 96 KB in flight.  The address of the next tile's row, a selected column to be read first, is fetched while
+    // the last pairs land, the next query's record with it.
+    const int lw = warp - kLoadWarp0;
+    const uint32_t r_base = tc::smem_u32(rows) + (32 * lw + (lane >> 4)) * 128 + ((lane >> 3) & 1) * kBox;
+    auto row_ptr = [&](const Query& qu, int qi, int t) -> const __nv_bfloat16* {
+      const int r = t * kPR + 32 * lw + lane;
+      const int j = (a.sel && r < qu.nsel) ? __ldg(a.sel + (size_t)qi * a.topk + r) : 0;
+      int row;
+      switch (row_src<kTree>(a, row_code<kTree>(a, qu, r, j), row)) {
+        case kSrcPool: return a.pool + (size_t)row * kAD;
+        case kSrcTreeRow: return a.trows + (size_t)row * kAD;
+        case kSrcChunk: return a.kvr + (size_t)row * kAD;
+        case kSrcRing: return a.ring + (size_t)row * kAD;
+      }
+      return nullptr;
+    };
+    Query qu;
+    auto find = [&](int qi) {  // the first query from qi on that has rows
+      for (; qi < a.T; qi += gridDim.x) {
+        qu = query_info<kTree>(a, qi);
+        if (qu.ntiles > 0) break;
+      }
+      return qi;
+    };
+    if (lw == 0 && lane == 0) tc::tma_prefetch(&tm_q);
+    uint32_t nq = 0, nt = 0;
+    int qi = find(blockIdx.x);
+    const __nv_bfloat16* ptr = qi < a.T ? row_ptr(qu, qi, 0) : nullptr;
+    while (qi < a.T && !failed) {
+      if (lw == 0 && lane == 0) {
+        // the query block (8 boxes of 64 heads x 64 dims), once the previous query's last score product has retired
+        if (nq > 0 && !tc::mbar_wait(q_empty, (nq - 1) & 1)) failed = true;
+        if (!failed) {
+          tc::mbar_arrive_expect_tx(q_full, kQBytes);
+          for (int c = 0; c < 8; ++c) tc::tma_load_2d(qbuf + c * kQBox, &tm_q, q_full, 64 * c, qi * kAH);
+        }
+      }
+      ++nq;
+      const int ntiles = qu.ntiles;
+      int next = qi;
+      for (int t = 0; t < ntiles; ++t, ++nt) {
+        const uint32_t par = (nt - 1) & 1;  // phase of the previous tile's releases
+        const long long mine = reinterpret_cast<long long>(ptr);
+        for (int m = 0; m < 4; ++m) {
+          if (nt > 0 && !tc::mbar_wait(box_free + m, par)) failed = true;
+          if (__any_sync(0xffffffffu, failed)) { failed = true; break; }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int r = 2 * i + (lane >> 4), c = lane & 15;
+            const auto* src = reinterpret_cast<const __nv_bfloat16*>(__shfl_sync(0xffffffffu, mine, r));
+            tc::cp_async16(r_base + 2 * m * kBox + 2 * i * 128 + (((c & 7) ^ (r & 7)) << 4),
+                           src ? src + 128 * m + 8 * c : a.pool, src ? 16u : 0u);
+          }
+          tc::cp_async_commit();
+          if (m >= 2) {
+            tc::cp_async_wait_group<2>();
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(rows_full + m - 2);
+          }
+        }
+        if (failed) break;
+        if (t + 1 < ntiles) {
+          ptr = row_ptr(qu, qi, t + 1);
+        } else {
+          next = find(qi + gridDim.x);
+          ptr = next < a.T ? row_ptr(qu, next, 0) : nullptr;
+        }
+        tc::cp_async_wait_group<1>();
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(rows_full + 2);
+        tc::cp_async_wait_group<0>();
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(rows_full + 3);
+      }
+      qi = next;
+    }
+    tc::cp_async_wait_all();
+    // (a query block whose load was issued lands before the CTA exits: its score products wait for it; after a
+    // failed wait it is given the time here)
+    if (failed && nq > 0 && lw == 0 && lane == 0) tc::mbar_wait(q_full, (nq - 1) & 1);
   } else if (warp >= kLoadWarp0) {
     // ------------------------------------------------------------ loaders (warps 9-10, 64 threads)
     const int lt = tid - kLoadWarp0 * 32;
@@ -398,7 +491,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t nq = 0, nt = 0;
     for (int qi = blockIdx.x; qi < a.T && !failed; qi += gridDim.x, ++nq) {
       const Query qu = query_info<kTree>(a, qi);
-      if (kTree && qu.ntiles == 0) { --nq; continue; }
       // codes of this thread's rows (lt, lt + 64) of a tile
       auto codes = [&](int t, int& x0, int& x1) {
         const int ra = t * kPR + lt, rb = ra + 64;
@@ -423,13 +515,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rch = 56 + (lt & 7);
       float rcs[4], rsn[4];
 #pragma unroll
-      for (int k = 0; !kTree && k < 4; ++k) rope_cs(qu.p, a.inv_freq, (rch - 56) * 4 + k, &rcs[k], &rsn[k]);
+      for (int k = 0; k < 4; ++k) rope_cs(qu.p, a.inv_freq, (rch - 56) * 4 + k, &rcs[k], &rsn[k]);
       if (tc::named_bar_any(kBarLoad, kLoaders, !tc::mbar_wait(q_loaded, nq & 1))) {
         failed = true;
         break;
       }
 #pragma unroll
-      for (int h = lt >> 3; !kTree && h < kAH; h += kLoaders / 8) {
+      for (int h = lt >> 3; h < kAH; h += kLoaders / 8) {
         uint4* slot = reinterpret_cast<uint4*>(qbuf + 7 * kQBox + h * 128 + (((rch & 7) ^ (h & 7)) << 4));
         uint4 raw = *slot;
         rope4(raw, rcs, rsn);
@@ -459,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         same &= src[0] != kSrcNone;
         // a tile of 128 consecutive chunk rows (a window in the chunk): one 128-row box load per 64 dims
         int row_first, row_last;
-        const bool chunk_tile = !kTree && a.chunk_tiles && row_src<kTree>(a, rowc[0], row_first) == kSrcChunk &&
+        const bool chunk_tile = a.chunk_tiles && row_src<kTree>(a, rowc[0], row_first) == kSrcChunk &&
                                 row_src<kTree>(a, rowc[kPR - 1], row_last) == kSrcChunk;
         for (int m = 0; m < 4; ++m) {
           if (m > 0 && nt > 0 && tc::named_bar_any(kBarLoad, kLoaders, !tc::mbar_wait(box_free + m, par))) {
@@ -477,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           } else if (same) {
             tc::mbar_arrive_expect_tx(rows_full + m, 4 * 128);
-            tc::tma_gather4(dst, src_map(src[0], &tm_pool, &tm_kvr, &tm_ring, &tm_kvr_tile), rows_full + m, 64 * box, row[0], row[1],
+            tc::tma_gather4(dst, src_map(src[0], &tm_pool, &tm_kvr, &tm_ring), rows_full + m, 64 * box, row[0], row[1],
                             row[2], row[3]);
           } else {
             // rows from different sources, or empty rows: one-row loads, zeros written here
@@ -496,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if (src[i] != kSrcNone)
-                tc::tma_load_2d(dst + i * 128, src_map(src[i], &tm_pool, &tm_kvr, &tm_ring, &tm_kvr_tile), rows_full + m, 64 * box,
+                tc::tma_load_2d(dst + i * 128, src_map(src[i], &tm_pool, &tm_kvr, &tm_ring), rows_full + m, 64 * box,
                                 row[i]);
           }
         }
@@ -523,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc::fence_after_sync();
-        const bool valid = rowc[row] != kRowNone;
+        const bool valid = kTree ? t * kPR + row < qu.nsel + qu.nwin : rowc[row] != kRowNone;
         float s[32];
         load_scores(tmem + kColS + hb + lane_base, valid, a.scale2, s);
         bool ovf = false;
@@ -738,15 +830,14 @@ cudaError_t launch_tc_attend_tree(const Dims& L, const TreeAttend& t, const int3
   a.scale2 = L.scale * 1.4426950408889634f;
   a.out = static_cast<__nv_bfloat16*>(t.out);
   a.err = err;
-  CUtensorMap tq, tp, tk, tr, trow;
-  if (!make_tmap_2d_bf16(&tq, t.q, (uint64_t)Q * kAH, kAD, kAD * 2, 64) ||
-      !make_tmap_2d_bf16(&tp, t.pool, (uint64_t)t.B * t.cap, kAD, kAD * 2, 1) ||
-      !make_tmap_2d_bf16(&tk, t.kv, (uint64_t)Q, kAD, kAD * 2, 1) ||
-      !make_tmap_2d_bf16(&tr, t.window, (uint64_t)t.B * L.Wr, kAD, kAD * 2, 1) ||
-      !make_tmap_2d_bf16(&trow, t.rows, (uint64_t)Q, kAD, kAD * 2, 1))
-    return cudaErrorInvalidValue;
+  a.pool = static_cast<const __nv_bfloat16*>(t.pool);
+  a.ring = static_cast<const __nv_bfloat16*>(t.window);
+  a.kvr = static_cast<const __nv_bfloat16*>(t.kv);
+  a.trows = static_cast<const __nv_bfloat16*>(t.rows);
+  CUtensorMap tq;
+  if (!make_tmap_2d_bf16(&tq, t.q, (uint64_t)Q * kAH, kAD, kAD * 2, 64)) return cudaErrorInvalidValue;
   cudaFuncSetAttribute(k_tc_attend_prefill<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  CSA_LAUNCH(k_tc_attend_prefill<true>, dim3(min(Q, g_sms_pf)), dim3(kThreads), kSmem, s, tq, tp, tk, tr, trow, a);
+  CSA_LAUNCH(k_tc_attend_prefill<true>, dim3(min(Q, g_sms_pf)), dim3(kTreeThreads), kSmem, s, tq, tq, tq, tq, tq, a);
   return cudaGetLastError();
 }
 

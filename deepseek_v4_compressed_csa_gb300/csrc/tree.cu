@@ -6,6 +6,7 @@
 
 #include "fp8_row.cuh"
 #include "kernels.h"
+#include "tc.cuh"
 
 namespace csa {
 
@@ -13,10 +14,14 @@ namespace {
 
 // ---------------------------------------------------------------- norm and rotation
 // y = x rsqrt(mean(x^2) + eps) w, then the last R dims of the row turned by the token's position.  One pass: a row
-// is read once into registers (fp32), its square sum reduced inside the lanes that hold it, and written once,
-// rounded once.  Bound by memory: 2 x the tensors' bytes.
+// is read once into registers, its square sum reduced in fp32 inside the lanes that hold it, and written once, rounded
+// once.  Bound by memory (2 x the tensors' bytes) only while a row costs few instructions: a row of up to 256 values
+// sits in 2^k lanes (several rows a warp), a longer one in a warp, 8 values a lane and chunk, sums and products run as
+// packed pairs, and a block takes a whole token, so that its angles (sines of up to 10^5 rad, some hundred instructions
+// each) are found once; with few tokens a token's rows are split over blocks.  4096 tokens of 64 x 512, 512 and 64 x 128
+// values: 130 us, 5.2 TB/s (two or four tokens a block 134 and 153 us; four rows in flight a warp in place of two 131 us).
 constexpr int kNrParts = 4;
-constexpr int kNrThreads = 256;
+constexpr int kNrWarps = 8;
 
 template <typename T>
 struct NrPart {
@@ -24,14 +29,13 @@ struct NrPart {
   T* out;
   const float* w;
   int heads, dim, norm, lpr_log2;  // lpr: lanes that hold a row (a power of two, at most 32)
+  float inv_dim;
   long long x_stride;              // elements between tokens
 };
 template <typename T>
 struct NrArgs {
   NrPart<T> part[kNrParts];
-  int n_parts, rows, R, T_, B;     // rows: row groups (one warp pass each) of a token over all parts
-  int groups_per_block;
-  int first[kNrParts + 1];         // first row group of each part
+  int n_parts, R, T_;
   const int32_t* parent;
   const int32_t* pos;
   const float* inv_freq;
@@ -39,102 +43,143 @@ struct NrArgs {
   int32_t* err;
 };
 
+// 8 values as loaded
+template <typename T> struct Raw8;
+template <> struct Raw8<__nv_bfloat16> { uint4 v; };
+template <> struct Raw8<float> { float4 a, b; };
+__device__ __forceinline__ void raw_load(Raw8<__nv_bfloat16>& r, const __nv_bfloat16* p) {
+  r.v = *reinterpret_cast<const uint4*>(p);
+}
+__device__ __forceinline__ void raw_load(Raw8<float>& r, const float* p) {
+  r.a = reinterpret_cast<const float4*>(p)[0];
+  r.b = reinterpret_cast<const float4*>(p)[1];
+}
+__device__ __forceinline__ void raw_get(const Raw8<__nv_bfloat16>& r, float2 (&o)[4]) {
+  const uint32_t u[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void raw_get(const Raw8<float>& r, float2 (&o)[4]) {
+  o[0] = make_float2(r.a.x, r.a.y); o[1] = make_float2(r.a.z, r.a.w);
+  o[2] = make_float2(r.b.x, r.b.y); o[3] = make_float2(r.b.z, r.b.w);
+}
+
+// This warp's rows of one tensor for one token; kChunks: 8-value chunks a lane holds of a row (more than one: a row
+// takes the warp).
 template <typename T, int kChunks>
-__device__ __forceinline__ void norm_rope_rows(const NrPart<T>& pt, int tok, int row, int R, float eps, bool rotate,
-                                               const float* rc, const float* rs) {
-  const int lane = threadIdx.x & 31, lpr = 1 << pt.lpr_log2, sub = lane & (lpr - 1);
-  const int h = row + (lane >> pt.lpr_log2);
-  const bool live = h < pt.heads;
-  const int n8 = pt.dim >> 3;
-  const T* src = pt.x + (size_t)tok * pt.x_stride + (size_t)h * pt.dim;
-  float v[kChunks][8];
-  float ss = 0.f;
+__device__ __forceinline__ void norm_rope_part(const NrPart<T>& pt, int tok, int first, int step, int R, float eps,
+                                               bool rotate, const float2* cs) {
+  constexpr int kB = sizeof(T) == 2 && kChunks < 4 ? 2 : 1;  // row groups in flight
+  const int lane = threadIdx.x & 31, lg = kChunks > 1 ? 5 : pt.lpr_log2, sub = lane & ((1 << lg) - 1);
+  const int rpw = 32 >> lg, n8 = pt.dim >> 3, r0 = pt.dim - R, heads = pt.heads, dim = pt.dim, norm = pt.norm;
+  const float* w = pt.w;
+  const float inv_dim = pt.inv_dim;
+  const T* x = pt.x + (size_t)tok * pt.x_stride + sub * 8;
+  T* out = pt.out + (size_t)tok * heads * dim + sub * 8;
+  const int h0 = lane >> lg;
+  for (int g0 = first; g0 * rpw < heads; g0 += kB * step) {
+    Raw8<T> raw[kB][kChunks];
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    const int c = sub + i * lpr;
-    if (live && c < n8) {
-      load8(src + 8 * c, v[i]);
+    for (int u = 0; u < kB; ++u) {
+      const int h = (g0 + u * step) * rpw + h0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+      for (int i = 0; i < kChunks; ++i)
+        if (h < heads && sub + 32 * i < n8) raw_load(raw[u][i], x + (size_t)h * dim + 256 * i);
     }
-  }
-  float inv = 1.f;
-  if (pt.norm) {
-    for (int o = lpr >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    inv = 1.0f / sqrtf(ss / (float)pt.dim + eps);
-  }
-  T* dst = pt.out + ((size_t)tok * pt.heads + h) * pt.dim;
-  const int r0 = pt.dim - R;
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    const int c = sub + i * lpr;
-    if (!live || c >= n8) continue;
-    if (pt.norm) {
+    for (int u = 0; u < kB; ++u) {
+      if ((g0 + u * step) * rpw >= heads) break;  // the whole warp
+      const int h = (g0 + u * step) * rpw + h0;
+      float2 v[kChunks][4];
+      float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] *= inv;
-      if (pt.w) {
-        float w[8];
-        load8_nc(pt.w + 8 * c, w);
+      for (int i = 0; i < kChunks; ++i) {
+        if (h < heads && sub + 32 * i < n8) {
+          raw_get(raw[u][i], v[i]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] *= w[e];
+          for (int e = 0; e < 4; ++e) s2 = __ffma2_rn(v[i][e], v[i][e], s2);
+        }
+      }
+      if (norm) {
+        float ss = s2.x + s2.y;
+        if (kChunks > 1) {
+          ss = warp_sum(ss);
+        } else {
+          for (int o = 1 << lg >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        }
+        const float inv = rsqrtf(fmaf(ss, inv_dim, eps));
+        const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[i][e] = __fmul2_rn(v[i][e], inv2);
+      }
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int c = sub + 32 * i;
+        if (h >= heads || c >= n8) continue;
+        if (norm && w) {
+          const float4 wa = __ldg(reinterpret_cast<const float4*>(w + 8 * c));
+          const float4 wb = __ldg(reinterpret_cast<const float4*>(w + 8 * c) + 1);
+          v[i][0] = __fmul2_rn(v[i][0], make_float2(wa.x, wa.y));
+          v[i][1] = __fmul2_rn(v[i][1], make_float2(wa.z, wa.w));
+          v[i][2] = __fmul2_rn(v[i][2], make_float2(wb.x, wb.y));
+          v[i][3] = __fmul2_rn(v[i][3], make_float2(wb.z, wb.w));
+        }
+        if (rotate && 8 * c >= r0) {
+          const float4* t = reinterpret_cast<const float4*>(cs + ((8 * c - r0) >> 1));
+          const float4 t0 = t[0], t1 = t[1];
+          const float2 a[4] = {make_float2(t0.x, t0.y), make_float2(t0.z, t0.w), make_float2(t1.x, t1.y),
+                               make_float2(t1.z, t1.w)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[i][e] = make_float2(fmaf(v[i][e].x, a[e].x, -v[i][e].y * a[e].y),
+                                  fmaf(v[i][e].x, a[e].y, v[i][e].y * a[e].x));
+        }
+        store8(out + (size_t)h * dim + 256 * i, reinterpret_cast<const float*>(v[i]));
       }
     }
-    if (rotate && 8 * c >= r0) {
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const int k = (8 * c + e - r0) >> 1;
-        const float a = v[i][e], b = v[i][e + 1];
-        v[i][e] = fmaf(a, rc[k], -b * rs[k]);
-        v[i][e + 1] = fmaf(a, rs[k], b * rc[k]);
-      }
-    }
-    store8(dst + 8 * c, v[i]);
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kNrThreads) k_norm_rope(NrArgs<T> a) {
+// Block (token, share): the token's row groups blockIdx.y * kNrWarps + warp, and so on by kNrWarps * gridDim.y.  kLong:
+// some row is longer than 512 values (an instance of its own, for its registers).
+template <typename T, bool kLong>
+__global__ void __launch_bounds__(32 * kNrWarps, kLong ? 2 : 3) k_norm_rope(const __grid_constant__ NrArgs<T> a) {
   // no early trigger: kernels of later calls read queries and keys before their own wait
-  extern __shared__ float sm_nr[];
-  float* rc = sm_nr;
-  float* rs = sm_nr + a.R / 2;
+  extern __shared__ __align__(16) float2 cs[];  // [R / 2] cos, sin
   __shared__ int s_depth;
   pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tok = blockIdx.x, b = tok / a.T_, i = tok - b * a.T_;
-  int depth = i;
-  if (a.parent) {
-    if (threadIdx.x < 32) {
+  const bool rotate = a.inv_freq != nullptr;
+  if (warp == 0) {
+    int depth = i;
+    if (a.parent) {
       bool bad = false;
-      const uint64_t m = tree_path_warp(a.parent + (size_t)b * a.T_, a.T_, i, bad);
-      if (threadIdx.x == 0) {
-        s_depth = __popcll(m) - 1;
-        if (bad) atomicOr(a.err, CSA_DEV_STATE);
+      depth = __popcll(tree_path_warp(a.parent + (size_t)b * a.T_, a.T_, i, bad)) - 1;
+      if (bad && lane == 0) atomicOr(a.err, CSA_DEV_STATE);
+    }
+    if (depth >= 0 && rotate) {
+      const int p0 = a.pos[b];
+      if (p0 < 0) {
+        if (lane == 0) atomicOr(a.err, CSA_DEV_STATE);
+        depth = -1;
+      } else {
+        for (int k = lane; k < a.R / 2; k += 32) rope_cs(p0 + depth, a.inv_freq, k, &cs[k].x, &cs[k].y);
       }
     }
-    __syncthreads();
-    depth = s_depth;
-    if (depth < 0) return;
+    if (lane == 0) s_depth = depth;
   }
-  const bool rotate = a.inv_freq != nullptr;
-  if (rotate) {
-    const int p = a.pos[b] + depth;
-    if (a.pos[b] < 0) {
-      if (threadIdx.x == 0) atomicOr(a.err, CSA_DEV_STATE);
-      return;
-    }
-    for (int k = threadIdx.x; k < a.R / 2; k += blockDim.x) rope_cs(p, a.inv_freq, k, rc + k, rs + k);
-    __syncthreads();
-  }
-  const int g1 = min(a.rows, (int)(blockIdx.y + 1) * a.groups_per_block);
-  for (int g = blockIdx.y * a.groups_per_block + (threadIdx.x >> 5); g < g1; g += kNrThreads / 32) {
-    int k = 0;
-    while (k + 1 < a.n_parts && g >= a.first[k + 1]) ++k;
+  __syncthreads();
+  if (s_depth < 0) return;
+  const int first = blockIdx.y * kNrWarps + warp, step = kNrWarps * gridDim.y;
+#pragma unroll 1
+  for (int k = 0; k < a.n_parts; ++k) {
     const NrPart<T>& pt = a.part[k];
-    const int row = (g - a.first[k]) << (5 - pt.lpr_log2);
-    const int chunks = ((pt.dim >> 3) + (1 << pt.lpr_log2) - 1) >> pt.lpr_log2;
-    if (chunks == 1) norm_rope_rows<T, 1>(pt, tok, row, a.R, a.eps, rotate, rc, rs);
-    else if (chunks == 2) norm_rope_rows<T, 2>(pt, tok, row, a.R, a.eps, rotate, rc, rs);
-    else norm_rope_rows<T, 4>(pt, tok, row, a.R, a.eps, rotate, rc, rs);
+    if (pt.dim <= 256) norm_rope_part<T, 1>(pt, tok, first, step, a.R, a.eps, rotate, cs);
+    else if (pt.dim <= 512) norm_rope_part<T, 2>(pt, tok, first, step, a.R, a.eps, rotate, cs);
+    else if (kLong) norm_rope_part<T, 4>(pt, tok, first, step, a.R, a.eps, rotate, cs);
   }
 }
 
@@ -143,8 +188,8 @@ cudaError_t norm_rope_t(const Dims& L, const csa_rows* rows, int n, int B, int T
                         const int32_t* pos, const float* inv_freq, int32_t* err, cudaStream_t s) {
   NrArgs<T> a{};
   a.n_parts = n;
-  a.R = L.R; a.T_ = T_; a.B = B; a.parent = parent; a.pos = pos; a.inv_freq = inv_freq; a.eps = L.eps; a.err = err;
-  int groups = 0;
+  a.R = L.R; a.T_ = T_; a.parent = parent; a.pos = pos; a.inv_freq = inv_freq; a.eps = L.eps; a.err = err;
+  int most = 1, longest = 0;
   for (int k = 0; k < n; ++k) {
     NrPart<T>& p = a.part[k];
     p.x = static_cast<const T*>(rows[k].x);
@@ -153,17 +198,23 @@ cudaError_t norm_rope_t(const Dims& L, const csa_rows* rows, int n, int B, int T
     p.heads = rows[k].heads;
     p.dim = rows[k].dim;
     p.norm = rows[k].norm;
+    p.inv_dim = 1.0f / (float)p.dim;
     p.x_stride = rows[k].x_stride > 0 ? rows[k].x_stride : (long long)p.heads * p.dim;
     p.lpr_log2 = 0;
     while ((1 << p.lpr_log2) < 32 && (1 << p.lpr_log2) < p.dim / 8) ++p.lpr_log2;
-    a.first[k] = groups;
-    groups += (p.heads + (32 >> p.lpr_log2) - 1) / (32 >> p.lpr_log2);
+    const int rpw = 32 >> p.lpr_log2;
+    most = max(most, (p.heads + rpw - 1) / rpw);
+    longest = max(longest, p.dim);
   }
-  a.first[n] = groups;
-  a.rows = groups;
-  a.groups_per_block = kNrThreads / 32;
-  const int gy = (groups + a.groups_per_block - 1) / a.groups_per_block;
-  CSA_LAUNCH(k_norm_rope<T>, dim3(B * T_, gy), dim3(kNrThreads), L.R * sizeof(float), s, a);
+  // few tokens: the rows of a token over as many blocks as give every SM eight, up to one warp per row group
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int ntok = B * T_, split = min((most + kNrWarps - 1) / kNrWarps, (8 * sms + ntok - 1) / ntok);
+  const dim3 grid(ntok, max(1, split));
+  const size_t smem = L.R * sizeof(float);
+  if (longest > 512) CSA_LAUNCH((k_norm_rope<T, true>), grid, dim3(32 * kNrWarps), smem, s, a);
+  else CSA_LAUNCH((k_norm_rope<T, false>), grid, dim3(32 * kNrWarps), smem, s, a);
   return cudaGetLastError();
 }
 
@@ -171,7 +222,7 @@ cudaError_t norm_rope_t(const Dims& L, const csa_rows* rows, int n, int B, int T
 template <typename T>
 struct TreePool {
   const T* frontier;  // [B, F, 2 L d]
-  const T* src;       // [B, T, 2 L d] the projections of every slot
+  const T* src;       // [B, T, 2 L d] the projections of every slot, or (src == proj) the nodes' in place
   T* proj;            // [B, T, 2 L d] the draft buffer that keeps the nodes'
   T* rows;            // [B, T, d], or fp8 rows
   const float* ape;
@@ -179,115 +230,126 @@ struct TreePool {
   int d, fp8;
 };
 
+__device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+}
+__device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float x, float y) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y);
+}
+__device__ __forceinline__ void store2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
+
 // Block (i, b, pool): node i of sequence b.  If its token completes window j along its path, the row that the
 // compressor would emit: entries before pos from the frontier ring, from pos on the path's nodes.  Arithmetic and
-// roundings are those of the committed rows (compress.cu), so that an accepted row is the row decoding would have
-// written.
+// roundings are those of the committed rows (compress.cu: the pooled value, its norm and its rotation each in the
+// model dtype), so that an accepted row is the row decoding would have written.  A thread takes two neighbouring
+// channels, and eight entries' loads are in flight together.  Latency-bound: three of four nodes complete nothing.
 template <typename T>
-__global__ void __launch_bounds__(256) k_tree_pool(TreePool<T> pa, TreePool<T> pi, int T_, int ratio, int lanes, int R,
-                                                   int F, float eps, const int32_t* __restrict__ parent,
+__global__ void __launch_bounds__(256) k_tree_pool(const __grid_constant__ TreePool<T> pa,
+                                                   const __grid_constant__ TreePool<T> pi, int T_, int ratio, int lanes,
+                                                   int R, int F, float eps, const int32_t* __restrict__ parent,
                                                    const int32_t* __restrict__ pos,
                                                    const float* __restrict__ inv_freq, int32_t* err) {
   pdl_trigger();
-  extern __shared__ float sm_tp[];  // [d] pooled, [d] normed, 32 reduction slots
+  extern __shared__ __align__(16) float sm_tp[];  // [d] pooled, then normed; 32 reduction slots
   __shared__ uint64_t s_mask;
   __shared__ int s_path[kTreeMax];
-  const bool second = blockIdx.z != 0;
-  const T* __restrict__ frontier = second ? pi.frontier : pa.frontier;
-  const T* __restrict__ src = second ? pi.src : pa.src;
-  T* proj = second ? pi.proj : pa.proj;
-  T* rows = second ? pi.rows : pa.rows;
-  const float* __restrict__ ape = second ? pi.ape : pa.ape;
-  const float* __restrict__ norm_w = second ? pi.norm_w : pa.norm_w;
-  const int d = second ? pi.d : pa.d, fp8 = second ? pi.fp8 : pa.fp8;
+  const TreePool<T>& tp = blockIdx.z ? pi : pa;
+  const int d = tp.d, Ld = lanes * d, rowlen = 2 * Ld;
   float* u = sm_tp;
-  float* y = u + d;
-  float* red = y + d;
-  pdl_wait();
+  float* red = u + d;
   const int i = blockIdx.x, b = blockIdx.y, p0 = pos[b];
   if (threadIdx.x < 32) {
     bool bad = false;
     const uint64_t m = tree_path_warp(parent + (size_t)b * T_, T_, i, bad);
     if (threadIdx.x == 0) {
       s_mask = p0 < 0 ? 0 : m;
-      if (bad || p0 < 0) atomicOr(err, CSA_DEV_STATE);
+      if (bad || (p0 < 0 && m)) atomicOr(err, CSA_DEV_STATE);
       int k = 0;
       for (uint64_t r = m; r; r &= r - 1) s_path[k++] = __ffsll((long long)r) - 1;
     }
   }
   __syncthreads();
   if (s_mask == 0) return;
-  const int Ld = lanes * d, rowlen = 2 * Ld, p = p0 + __popcll(s_mask) - 1;
-  const T* pj = src + (size_t)b * T_ * rowlen;
-  for (int e = threadIdx.x * 8; e < rowlen; e += blockDim.x * 8)
-    copy8<T>(proj + ((size_t)b * T_ + i) * rowlen + e, pj + (size_t)i * rowlen + e);
-  if ((p + 1) % ratio != 0) return;
+  const int p = p0 + __popcll(s_mask) - 1;
+  const bool closes = (p + 1) % ratio == 0;
+  const T* src = tp.src + (size_t)b * T_ * rowlen;
+  if (!closes && tp.src == tp.proj) return;
+  pdl_wait();
+  if (tp.src != tp.proj)
+    for (int e = threadIdx.x * 8; e < rowlen; e += blockDim.x * 8)
+      copy8<T>(tp.proj + ((size_t)b * T_ + i) * rowlen + e, src + (size_t)i * rowlen + e);
+  if (!closes) return;
   const int j = (p + 1) / ratio - 1;
-  const T* fr = frontier + (size_t)b * F * rowlen;
+  const T* fr = tp.frontier + (size_t)b * F * rowlen;
   const int t_lo = lanes == 2 ? max(0, (j - 1) * ratio) : j * ratio;
   const int t_hi = (j + 1) * ratio;
   float ss = 0.f;
-  for (int c = threadIdx.x; c < d; c += blockDim.x) {
-    float m = -INFINITY, num = 0.f, den = 0.f;
+  for (int c = 2 * threadIdx.x; c < d; c += 2 * blockDim.x) {
+    float2 m = make_float2(-INFINITY, -INFINITY), num = make_float2(0.f, 0.f), den = make_float2(0.f, 0.f);
     for (int t0 = t_lo; t0 < t_hi; t0 += 8) {
-      float sv[8], kv[8];
+      float2 sv[8], kv[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int t = t0 + k;
-        sv[k] = -INFINITY;
-        kv[k] = 0.f;
+        sv[k] = make_float2(-INFINITY, -INFINITY);
+        kv[k] = make_float2(0.f, 0.f);
         if (t < t_hi) {
-          const int l = (lanes == 2 && t >= j * ratio) ? 1 : 0;
-          const T* row = t < p0 ? fr + (size_t)(t % F) * rowlen : pj + (size_t)s_path[t - p0] * rowlen;
-          kv[k] = to_f(row[l * d + c]);
-          sv[k] = to_f(row[Ld + l * d + c]) + __ldg(ape + (size_t)(t % ratio) * Ld + l * d + c);
+          const int at = ((lanes == 2 && t >= j * ratio) ? d : 0) + c;
+          const T* row = t < p0 ? fr + (size_t)(t % F) * rowlen : src + (size_t)s_path[t - p0] * rowlen;
+          kv[k] = load2(row + at);
+          const float2 g = load2(row + Ld + at), w = load2(tp.ape + (size_t)(t % ratio) * Ld + at);
+          sv[k] = make_float2(g.x + w.x, g.y + w.y);
         }
       }
-      float cm = m;
+      float2 cm = m;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) cm = fmaxf(cm, sv[k]);
-      const float al = (m == -INFINITY) ? 0.f : expf(m - cm);
-      num *= al;
-      den *= al;
+      for (int k = 0; k < 8; ++k) cm = make_float2(fmaxf(cm.x, sv[k].x), fmaxf(cm.y, sv[k].y));
+      const float ax = (m.x == -INFINITY) ? 0.f : expf(m.x - cm.x), ay = (m.y == -INFINITY) ? 0.f : expf(m.y - cm.y);
+      num = make_float2(num.x * ax, num.y * ay);
+      den = make_float2(den.x * ax, den.y * ay);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float e = (sv[k] == -INFINITY) ? 0.f : expf(sv[k] - cm);
-        den += e;
-        num = fmaf(e, kv[k], num);
+        const float ex = (sv[k].x == -INFINITY) ? 0.f : expf(sv[k].x - cm.x);
+        const float ey = (sv[k].y == -INFINITY) ? 0.f : expf(sv[k].y - cm.y);
+        den = make_float2(den.x + ex, den.y + ey);
+        num = make_float2(fmaf(ex, kv[k].x, num.x), fmaf(ey, kv[k].y, num.y));
       }
       m = cm;
     }
-    const float uc = rnd<T>(num / den);
-    u[c] = uc;
-    ss = fmaf(uc, uc, ss);
+    const float x = rnd<T>(num.x / den.x), y = rnd<T>(num.y / den.y);
+    u[c] = x;
+    u[c + 1] = y;
+    ss = fmaf(x, x, fmaf(y, y, ss));
   }
   ss = block_sum(ss, red);
   const float inv = 1.0f / sqrtf(ss / (float)d + eps);
-  for (int c = threadIdx.x; c < d; c += blockDim.x) y[c] = rnd<T>(u[c] * inv * __ldg(norm_w + c));
-  __syncthreads();
-  T* dst = rows + ((size_t)b * T_ + i) * d;
-  for (int c = threadIdx.x; c < d; c += blockDim.x) {
-    float v = y[c];
+  T* dst = tp.rows + ((size_t)b * T_ + i) * d;
+  for (int c = 2 * threadIdx.x; c < d; c += 2 * blockDim.x) {  // (the thread's own channels, a rotated pair whole)
+    const float2 w = load2(tp.norm_w + c);
+    float x = rnd<T>(u[c] * inv * w.x), y = rnd<T>(u[c + 1] * inv * w.y);
     if (c >= d - R) {
-      const int k = (c - (d - R)) >> 1;
       float cs, sn;
-      rope_cs(j * ratio, inv_freq, k, &cs, &sn);
-      const float x0 = y[d - R + 2 * k], x1 = y[d - R + 2 * k + 1];
-      v = ((c - (d - R)) & 1) ? fmaf(x0, sn, x1 * cs) : fmaf(x0, cs, -x1 * sn);
+      rope_cs(j * ratio, inv_freq, (c - (d - R)) >> 1, &cs, &sn);
+      const float x0 = x, y0 = y;
+      x = fmaf(x0, cs, -y0 * sn);
+      y = fmaf(x0, sn, y0 * cs);
     }
-    if (fp8)
-      u[c] = rnd<T>(v);
-    else
-      dst[c] = from_f<T>(v);
+    if (tp.fp8) {
+      u[c] = rnd<T>(x);
+      u[c + 1] = rnd<T>(y);
+    } else {
+      store2(dst + c, x, y);
+    }
   }
-  if (fp8) {
+  if (tp.fp8) {
     __syncthreads();
     if (threadIdx.x < 32) {
       const int lane = threadIdx.x;
       float q[4] = {u[4 * lane], u[4 * lane + 1], u[4 * lane + 2], u[4 * lane + 3]};
       float scale;
       const uint32_t packed = fp8_rotate_quantize(q, lane, &scale);
-      fp8_row_store(reinterpret_cast<uint8_t*>(rows) + ((size_t)b * T_ + i) * kFp8RowBytes, lane, packed, scale);
+      fp8_row_store(reinterpret_cast<uint8_t*>(tp.rows) + ((size_t)b * T_ + i) * kFp8RowBytes, lane, packed, scale);
     }
   }
 }
@@ -490,51 +552,74 @@ struct CommitArgs {
   int32_t* err;
 };
 
-// One block per sequence: the accepted path's rows from the draft buffers into the window ring, the frontier rings
-// and the pools, then the new position and row counts.  Nothing is written before the checks.
+// A cluster of kCommitCtas blocks per sequence: the accepted path's rows from the draft buffers into the window ring,
+// the frontier rings and the pools, a warp per (token, destination), then the new position and row counts.  The
+// position may be replaced in place, so every block has read it (a cluster barrier) before the first one writes.
+// Nothing is written before the checks.  Latency-bound: a few hundred KB at most, so the copies are spread over enough
+// warps that each makes one round trip or two.
 // No early trigger: kernels of the next step read positions and ring rows before their own wait.
+constexpr int kCommitCtas = 8, kCommitWarps = 8;
+
 template <typename T>
-__global__ void __launch_bounds__(512) k_tree_commit(CommitArgs<T> a) {
+__global__ void __launch_bounds__(32 * kCommitWarps) k_tree_commit(const __grid_constant__ CommitArgs<T> a) {
   __shared__ uint64_t masks[kTreeMax];
   __shared__ int par[kTreeMax], path[kTreeMax];
   pdl_wait();
-  const int b = blockIdx.x, tid = threadIdx.x;
-  const bool tree_ok = tree_masks_block(a.parent + (size_t)b * a.T_, a.T_, masks, par);
+  const int b = blockIdx.x / kCommitCtas, rank = blockIdx.x % kCommitCtas, tid = threadIdx.x;
   const int leaf = a.leaf[b], p0 = a.pos[b];
+  int rows[2] = {0, 0};
+  for (int k = 0; k < a.npool; ++k) rows[k] = a.pool[k].n_rows[b];
+  const bool tree_ok = tree_masks_block(a.parent + (size_t)b * a.T_, a.T_, masks, par);
   int bad = 0;
   if (p0 < 0 || !tree_ok || leaf < -1 || leaf >= a.T_ || (leaf >= 0 && masks[leaf] == 0)) bad = CSA_DEV_STATE;
   const uint64_t m = bad || leaf < 0 ? 0 : masks[leaf];
   const int n = __popcll(m), end = p0 + n;
   for (int k = 0; k < a.npool; ++k) {
-    if (!bad && a.pool[k].n_rows[b] != p0 / a.ratio) bad = CSA_DEV_STATE;
+    if (!bad && rows[k] != p0 / a.ratio) bad = CSA_DEV_STATE;
     if (!bad && end / a.ratio > a.pool[k].cap) bad = CSA_DEV_CAPACITY;
   }
-  if (bad && tid == 0) atomicOr(a.err, bad);
   if (tid < n && !bad) path[tid] = tree_node_at(m, tid);
-  __syncthreads();  // every thread has read the positions and counts before thread 0 may replace them
-  if (tid == 0) {
+  tc::cluster_sync();
+  if (rank == 0 && tid == 0) {
+    if (bad) atomicOr(a.err, bad);
     a.pos_out[b] = bad ? p0 : end;
-    for (int k = 0; k < a.npool; ++k) a.pool[k].n_rows_out[b] = bad ? a.pool[k].n_rows[b] : end / a.ratio;
+    for (int k = 0; k < a.npool; ++k) a.pool[k].n_rows_out[b] = bad ? rows[k] : end / a.ratio;
   }
   if (bad) return;
-  auto copy = [&](char* dst, const char* src, int bytes) {
-    for (int e = tid * 16; e < bytes; e += blockDim.x * 16)
-      *reinterpret_cast<uint4*>(dst + e) = *reinterpret_cast<const uint4*>(src + e);
-  };
-  for (int k = 0; k < n; ++k) {
-    const int t = p0 + k, node = path[k];
-    const size_t row = (size_t)b * a.T_ + node;
-    if (t >= end - a.Wr)  // a later token of the path takes the slot otherwise
-      copy(reinterpret_cast<char*>(a.window + ((size_t)b * a.Wr + t % a.Wr) * a.D),
-           reinterpret_cast<const char*>(a.kv + row * a.D), a.D * (int)sizeof(T));
-    for (int g = 0; g < a.npool; ++g) {
-      const CommitPool<T>& cp = a.pool[g];
-      if (t >= end - a.F)
-        copy(reinterpret_cast<char*>(cp.frontier + ((size_t)b * a.F + t % a.F) * cp.rowlen),
-             reinterpret_cast<const char*>(cp.proj + row * cp.rowlen), cp.rowlen * (int)sizeof(T));
-      if ((t + 1) % a.ratio == 0)
-        copy(cp.pool + ((size_t)b * cp.cap + (t + 1) / a.ratio - 1) * cp.row_bytes, cp.rows + row * cp.row_bytes,
-             cp.row_bytes);
+  const int lane = tid & 31, kinds = 1 + 2 * a.npool;  // window, then a frontier and a pool per pool
+  for (int e = rank * kCommitWarps + (tid >> 5); e < n * kinds; e += kCommitCtas * kCommitWarps) {
+    const int k = e / kinds, kind = e - k * kinds, t = p0 + k;
+    const size_t row = (size_t)b * a.T_ + path[k];
+    const char* src;
+    char* dst;
+    int bytes;
+    if (kind == 0) {
+      if (t < end - a.Wr) continue;  // a later token of the path takes the slot
+      bytes = a.D * (int)sizeof(T);
+      src = reinterpret_cast<const char*>(a.kv + row * a.D);
+      dst = reinterpret_cast<char*>(a.window + ((size_t)b * a.Wr + t % a.Wr) * a.D);
+    } else {
+      const CommitPool<T>& cp = a.pool[(kind - 1) >> 1];
+      if (kind & 1) {
+        if (t < end - a.F) continue;
+        bytes = cp.rowlen * (int)sizeof(T);
+        src = reinterpret_cast<const char*>(cp.proj + row * cp.rowlen);
+        dst = reinterpret_cast<char*>(cp.frontier + ((size_t)b * a.F + t % a.F) * cp.rowlen);
+      } else {
+        if ((t + 1) % a.ratio) continue;
+        bytes = cp.row_bytes;
+        src = cp.rows + row * cp.row_bytes;
+        dst = cp.pool + ((size_t)b * cp.cap + (t + 1) / a.ratio - 1) * cp.row_bytes;
+      }
+    }
+    for (int o = lane * 16; o < bytes; o += 4 * 512) {
+      uint4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (o + 512 * u < bytes) v[u] = *reinterpret_cast<const uint4*>(src + o + 512 * u);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (o + 512 * u < bytes) *reinterpret_cast<uint4*>(dst + o + 512 * u) = v[u];
     }
   }
 }
@@ -547,26 +632,40 @@ cudaError_t launch_norm_rope(const Dims& L, const csa_rows* rows, int n, int B, 
   return norm_rope_t<float>(L, rows, n, B, T, parent, pos, inv_freq, err, s);
 }
 
+void* carve_compress_tree(Carver& c, const Dims& L, int d, int B, int T) {
+  if (tc_tree_project_supported(L, d)) return nullptr;
+  return c.take<char>((size_t)B * T * 2 * L.lanes * d * esize(L.dtype));
+}
+
 template <typename T>
 static cudaError_t compress_tree_t(const Dims& L, const TreeCompress* pools, int npool, const void* x, int B, int T_,
                                    const int32_t* parent, const int32_t* pos, const float* inv_freq, int32_t* err,
                                    cudaStream_t s) {
   TreePool<T> tp[2];
+  // pools on the tensor cores share a grid; the others are projected one by one into the workspace
+  TreeCompress tc_pools[2];
+  int ntc = 0;
   for (int k = 0; k < npool; ++k) {
     const TreeCompress& c = pools[k];
     const int d = c.comp->d;
-    // every slot is projected into the workspace; the pooling kernel keeps the nodes' rows
-    cudaError_t e = tc_project_supported(L, d)
-                        ? launch_tc_project(L, d, x, B * T_, c.comp->wkv, c.comp->wgate, c.ws.proj, c.ws.part,
-                                            c.ws.tickets, true, err, s)
-                        : launch_project_simt(L, d, x, B * T_, c.comp->wkv, c.comp->wgate, c.ws.proj, s);
+    const bool on_tc = tc_tree_project_supported(L, d);
+    if (on_tc) {
+      tc_pools[ntc++] = c;
+    } else {
+      const cudaError_t e = launch_project_simt(L, d, x, B * T_, c.comp->wkv, c.comp->wgate, c.ws, s);
+      if (e != cudaSuccess) return e;
+    }
+    tp[k] = TreePool<T>{static_cast<const T*>(c.frontier), static_cast<const T*>(on_tc ? c.proj : c.ws),
+                        static_cast<T*>(c.proj), static_cast<T*>(c.rows), c.comp->ape, c.comp->norm_w, d,
+                        L.ikey_fp8 && d == L.Di && k == 1};
+  }
+  if (ntc > 0) {
+    const cudaError_t e = launch_tc_tree_project(L, tc_pools, ntc, x, B, T_, parent, pos, err, s);
     if (e != cudaSuccess) return e;
-    tp[k] = TreePool<T>{static_cast<const T*>(c.frontier), static_cast<const T*>(c.ws.proj), static_cast<T*>(c.proj), static_cast<T*>(c.rows),
-                        c.comp->ape, c.comp->norm_w, d, L.ikey_fp8 && d == L.Di && k == 1};
   }
   if (npool == 1) tp[1] = tp[0];
   const int dm = max(tp[0].d, tp[1].d);
-  CSA_LAUNCH(k_tree_pool<T>, dim3(T_, B, npool), dim3(256), (2 * (size_t)dm + 32) * sizeof(float), s, tp[0], tp[1], T_,
+  CSA_LAUNCH(k_tree_pool<T>, dim3(T_, B, npool), dim3(256), ((size_t)dm + 32) * sizeof(float), s, tp[0], tp[1], T_,
              L.ratio, L.lanes, L.R, L.F, L.eps, parent, pos, inv_freq, err);
   return cudaGetLastError();
 }
@@ -662,8 +761,9 @@ static cudaError_t commit_tree_t(const Dims& L, const TreeCommit& c, int32_t* er
                               c.n_rows_out[k], 2 * L.lanes * d,
                               k && L.ikey_fp8 ? kFp8RowBytes : d * (int)sizeof(T), c.cap[k]};
   }
-  CSA_LAUNCH(k_tree_commit<T>, dim3(c.B), dim3(512), 0, s, a);
-  return cudaGetLastError();
+  const cudaError_t e = launch_pdl_cluster(k_tree_commit<T>, dim3(c.B * kCommitCtas), dim3(32 * kCommitWarps), 0, s,
+                                           kCommitCtas, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_commit_tree(const Dims& L, const TreeCommit& c, int32_t* err, cudaStream_t s) {

@@ -65,7 +65,9 @@ def test_compress_tree_refusals(lib):
     assert _compress(lib, ca=None) == B.CSA_ERR_ARG
     assert _compress(lib, ca=_comp(128)) == B.CSA_ERR_ARG and _compress(lib, ci=_comp(512)) == B.CSA_ERR_ARG
     assert _compress(lib, layer=_layer(ratio=128)) == B.CSA_ERR_UNSUPPORTED
-    assert _compress(lib, ws_bytes=1024) == B.CSA_ERR_WORKSPACE and _compress(lib, ws=None) == B.CSA_ERR_WORKSPACE
+    f32 = dict(layer=_layer(dtype=B.CSA_F32))  # (the tensor-core projection of the bf16 layer needs no workspace)
+    assert _compress(lib, ws_bytes=1024, **f32) == B.CSA_ERR_WORKSPACE
+    assert _compress(lib, ws=None, **f32) == B.CSA_ERR_WORKSPACE
 
 
 def test_index_scores_tree_refusals(lib):
@@ -124,7 +126,8 @@ def test_workspace_sizes(lib):
     for op in (B.OP_COMPRESS_TREE, B.OP_ATTEND_TREE):
         for bad in ((0, 8), (2, 0), (2, 65), (65536, 1), (65535, 64)):
             assert lib.csa_workspace_size(ctypes.byref(_layer()), op, *bad, 100, ctypes.byref(n)) == B.CSA_ERR_ARG
-        assert lib.csa_workspace_size(ctypes.byref(_layer()), op, 2, 64, 100, ctypes.byref(n)) == 0 and n.value > 0
+        assert lib.csa_workspace_size(ctypes.byref(_layer(dtype=B.CSA_F32)), op, 2, 64, 100, ctypes.byref(n)) == 0
+        assert n.value > 0
 
 
 # ------------------------------------------------------------------------------------------------ the binding
