@@ -616,47 +616,49 @@ def attend_verify(layer: Layer, q, kv_new, sink, window, pool, n_rows, sel, n_se
 
 def _tree_ptr(name: str, t, dtype, shape, dev=None):
     """Checks of one tensor of a tree call (type, shape, contiguity, device); its address."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and (t.is_cuda if dev is None else t.get_device() == dev)):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} is required") if t is None else TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name}: CSA tensors must live on a CUDA device")
-    if dev is not None and t.get_device() != dev:
-        raise ValueError(f"{name}: on device {t.get_device()}, the call's tensors are on device {dev}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: CSA tensors must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name}: on device {t.get_device()}, the call's tensors are on device {dev}")
 
 
 def _tree_err(err, dev):
     if err is None:
         return torch.zeros(1, dtype=torch.int32, device=f"cuda:{dev}")
     _expect_err(err)
-    if not err.is_cuda or err.get_device() != dev:
+    if err.get_device() != dev:
         raise ValueError(f"err: expected a tensor on device {dev}")
     return err
 
 
 def _tree_ws(layer, op, B, T, cap, ws, dev):
-    need = workspace_size(layer, op, B, T, cap)
+    """The caller's workspace (the library checks its size), or a new one."""
     if ws is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=f"cuda:{dev}")
-    elif not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.get_device() != dev or not ws.is_contiguous():
+        ws = torch.empty(max(workspace_size(layer, op, B, T, cap), 256), dtype=torch.uint8, device=f"cuda:{dev}")
+    elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"ws: expected a contiguous tensor on device {dev}")
     return ws, ws.numel() * ws.element_size()
 
 
 def _tree_call(fn: str, dev: int, stream, *args):
     """The C call on the tensors' device, on `stream` or that device's current stream."""
-    f = getattr(load_library(), fn)
-    if dev == torch.cuda.current_device():
-        _check(fn, f(*args, _stream(stream)))
+    f = getattr(_lib or load_library(), fn)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        _check(fn, f(*args, raw))
         return
     with torch.cuda.device(dev):
-        _check(fn, f(*args, _stream(stream)))
+        _check(fn, f(*args, raw))
 
 
 def _tree_dims(name: str, t, tail: tuple):

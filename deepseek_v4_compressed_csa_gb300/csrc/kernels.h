@@ -315,7 +315,7 @@ struct TreeAttend {
 };
 cudaError_t launch_attend_tree(const Dims& L, const TreeAttend& t, int32_t* err, cudaStream_t s);
 // The same on the tensor cores (tc_attend_supported shapes), the node records already in t.ws: a CTA per query
-// streaming its tiles (tc_attend_prefill.cu), or S <= 4 splits per query merged in a cluster (tc_attend_decode.cu).
+// streaming its tiles (tc_tree_attend.cu), or S <= 4 splits per query merged in a cluster (tc_attend_decode.cu).
 cudaError_t launch_tc_attend_tree(const Dims& L, const TreeAttend& t, const int32_t* sel, int32_t* err,
                                   cudaStream_t s);
 cudaError_t launch_tc_attend_tree_split(const Dims& L, const TreeAttend& t, const int32_t* sel, int S, int32_t* err,

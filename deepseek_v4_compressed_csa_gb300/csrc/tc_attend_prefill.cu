@@ -37,7 +37,6 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
-#include "tree.cuh"
 
 namespace csa {
 
@@ -58,9 +57,6 @@ constexpr int kMmaWarp = kSoftWarps;     // warp 8: TMEM owner and MMA issuer
 constexpr int kLoadWarp0 = kMmaWarp + 1; // warps 9-10
 constexpr int kLoaders = 64;
 constexpr int kThreads = kSoft + 32 + kLoaders;
-// A tree's nodes: four loader warps, a row per thread (see the loaders)
-constexpr int kTreeLoadWarps = kPR / 32;
-constexpr int kTreeThreads = kSoft + 32 + 32 * kTreeLoadWarps;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColO3 = 384;         // O^T tile 3 (hi + lo in one accumulator)
 constexpr uint32_t kColS = 448;          // S^T
@@ -100,11 +96,6 @@ struct PfArgs {
   int T, pos0, cap, topk, W, ratio;
   int Wr;                      // ring slots (W + rollback); a query attends its last W tokens
   int chunk_tiles;             // T >= 128: 128-row boxes of the chunk's rows are available
-  // a tree's nodes (kTree; q already rotated): query q is node q % tree_T of sequence q / tree_T; kvr holds the nodes'
-  // latent rows [B, tree_T, 512], trows the rows that they complete; rows are copied by address, without tensor maps
-  const TreeNode* nodes;
-  const __nv_bfloat16* trows;
-  int tree_T;
   float scale2;                // softmax scale * log2(e)
   __nv_bfloat16* out;          // [T, 64, 512]
   int32_t* err;
@@ -112,28 +103,10 @@ struct PfArgs {
 
 struct Query {
   int b, p, nsel, nwin, nrows, ntiles;
-  int p0;                  // kTree
-  uint64_t mask, closers;
 };
 
-template <bool kTree>
 __device__ __forceinline__ Query query_info(const PfArgs& a, int qi) {
   Query r;
-  r.p0 = 0;
-  r.mask = r.closers = 0;
-  if constexpr (kTree) {
-    const TreeNode n = a.nodes[qi];
-    r.b = qi / a.tree_T;
-    r.p = n.p;
-    r.p0 = n.p0;
-    r.mask = n.mask;
-    r.closers = n.closers;
-    r.nrows = n.n;
-    r.nsel = n.nsel;
-    r.nwin = min(a.W, n.p + 1);
-    r.ntiles = n.nsel < 0 ? 0 : (r.nsel + r.nwin + kPR - 1) / kPR;  // 0: an unused slot, every role passes it over
-    return r;
-  }
   if (a.cu) {
     r.b = varlen_seq(a.cu, a.nseq, qi);
     r.p = a.pos[r.b] + qi - __ldg(a.cu + r.b);
@@ -152,22 +125,8 @@ __device__ __forceinline__ Query query_info(const PfArgs& a, int qi) {
 // code is its row in the pool tensor map (b * cap + j); a window token's is kRowTok0 - token for a chunk, and
 // kRowTok0 - (b * Wr + token mod Wr), its ring row, for verify blocks; in a variable-length batch, kRowTok0 -
 // its ring row (tokens before the sequence's chunk) or kRowTok0 - (kChunkFlag + its packed chunk row).
-// Of a tree's node (kTree): kRowTok0 - its ring row, - (kTreeKv + its row of the nodes' latents) or - (kTreeRow + its
-// row of the completed rows).
 constexpr int kChunkFlag = 1 << 29;
-constexpr int kTreeKv = 1 << 28, kTreeRow = 1 << 29;
-template <bool kTree>
 __device__ __forceinline__ int row_code(const PfArgs& a, const Query& qu, int r_abs, int j) {
-  if constexpr (kTree) {
-    if (r_abs < qu.nsel) {
-      if (!a.sel) j = r_abs < qu.nrows ? r_abs : qu.nrows + tree_node_at(qu.closers, r_abs - qu.nrows);
-      return j < qu.nrows ? qu.b * a.cap + j : kRowTok0 - (kTreeRow + qu.b * a.tree_T + (j - qu.nrows));
-    }
-    if (r_abs >= qu.nsel + qu.nwin) return kRowNone;
-    const int tok = qu.p - qu.nwin + 1 + (r_abs - qu.nsel);
-    if (tok < qu.p0) return kRowTok0 - (qu.b * a.Wr + tok % a.Wr);
-    return kRowTok0 - (kTreeKv + qu.b * a.tree_T + tree_node_at(qu.mask, tok - qu.p0));
-  }
   if (r_abs < qu.nsel) {
     if (!a.sel) j = r_abs;
     if (j >= 0 && j < qu.nrows) return qu.b * a.cap + j;
@@ -188,20 +147,12 @@ __device__ __forceinline__ int row_code(const PfArgs& a, const Query& qu, int r_
 }
 
 // Tensor map of a row: the pool, the chunk's roped rows, the ring before the chunk; kSrcNone: empty row.
-constexpr int kSrcPool = 0, kSrcChunk = 1, kSrcRing = 2, kSrcNone = 3, kSrcTreeRow = 4;
+constexpr int kSrcPool = 0, kSrcChunk = 1, kSrcRing = 2, kSrcNone = 3;
 
-template <bool kTree>
 __device__ __forceinline__ int row_src(const PfArgs& a, int code, int& row) {
   if (code >= 0) {
     row = code;
     return kSrcPool;
-  }
-  if constexpr (kTree) {
-    const int x = kRowTok0 - code;
-    row = 0;
-    if (x < 0) return kSrcNone;
-    row = x >= kTreeRow ? x - kTreeRow : (x >= kTreeKv ? x - kTreeKv : x);
-    return x >= kTreeRow ? kSrcTreeRow : (x >= kTreeKv ? kSrcChunk : kSrcRing);
   }
   if (code <= kRowTok0) {
     const int tok = kRowTok0 - code;
@@ -274,8 +225,7 @@ __device__ __forceinline__ void rope4(uint4& raw, const float (&rc)[4], const fl
   }
 }
 
-template <bool kTree>
-__global__ void __launch_bounds__(kTree ? kTreeThreads : kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     k_tc_attend_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_pool,
                         const __grid_constant__ CUtensorMap tm_kvr, const __grid_constant__ CUtensorMap tm_ring,
                         const __grid_constant__ CUtensorMap tm_kvr_tile, PfArgs a) {
@@ -303,11 +253,10 @@ __global__ void __launch_bounds__(kTree ? kTreeThreads : kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    tc::mbar_init(q_full, kTree ? 1 : kLoaders);
+    tc::mbar_init(q_full, kLoaders);
     tc::mbar_init(q_empty, 1);
     for (int m = 0; m < 4; ++m) {
-      // one arrival (with its bytes) per loader thread; a tree's loaders: one per warp
-      tc::mbar_init(rows_full + m, kTree ? kTreeLoadWarps : kLoaders);
+      tc::mbar_init(rows_full + m, kLoaders);  // one arrival (with its bytes) per loader thread
       tc::mbar_init(box_free + m, 1);
     }
     tc::mbar_init(s_full, 1);
@@ -338,8 +287,7 @@ __global__ void __launch_bounds__(kTree ? kTreeThreads : kThreads, 1)
       const uint32_t r_base = tc::smem_u32(rows), q_base = tc::smem_u32(qbuf), p_base = tc::smem_u32(pbuf);
       uint32_t nq = 0, nt = 0;
       for (int qi = blockIdx.x; qi < a.T && !failed; qi += gridDim.x, ++nq) {
-        const int ntiles = query_info<kTree>(a, qi).ntiles;
-        if (kTree && ntiles == 0) { --nq; continue; }
+        const int ntiles = query_info(a, qi).ntiles;
         if (!tc::mbar_wait(q_full, nq & 1)) { failed = true; break; }
         tc::fence_after_sync();
         for (int t = 0; t < ntiles; ++t, ++nt) {
@@ -389,95 +337,6 @@ __global__ void __launch_bounds__(kTree ? kTreeThreads : kThreads, 1)
     }
     __syncwarp();
     failed = __shfl_sync(0xffffffffu, (int)failed, 0) != 0;
-  } else if (kTree && warp >= kLoadWarp0) {
-    // ------------------------------------------------------------ loaders of a tree's nodes (warps 9-12)
-    // Warp w copies rows 32w .. 32w + 31 of a tile, 256 bytes of each row per box pair: a lane knows the address of
-    // one row, an instruction copies two rows' 512 bytes, and a pair's 16 instructions a warp are one commit group, up
-    // to three of them in flight.  A tile takes 8 x 32 tile::gather4 requests otherwise, which the copy engine serves
-    // at ~7 B a clock per SM (the tile then lasts 11.7 us, four fifths of it waiting); four warps of 16-byte copies
-    // keep 96 KB in flight.  The address of the next tile's row, a selected column to be read first, is fetched while
-    // the last pairs land, the next query's record with it.
-    const int lw = warp - kLoadWarp0;
-    const uint32_t r_base = tc::smem_u32(rows) + (32 * lw + (lane >> 4)) * 128 + ((lane >> 3) & 1) * kBox;
-    auto row_ptr = [&](const Query& qu, int qi, int t) -> const __nv_bfloat16* {
-      const int r = t * kPR + 32 * lw + lane;
-      const int j = (a.sel && r < qu.nsel) ? __ldg(a.sel + (size_t)qi * a.topk + r) : 0;
-      int row;
-      switch (row_src<kTree>(a, row_code<kTree>(a, qu, r, j), row)) {
-        case kSrcPool: return a.pool + (size_t)row * kAD;
-        case kSrcTreeRow: return a.trows + (size_t)row * kAD;
-        case kSrcChunk: return a.kvr + (size_t)row * kAD;
-        case kSrcRing: return a.ring + (size_t)row * kAD;
-      }
-      return nullptr;
-    };
-    Query qu;
-    auto find = [&](int qi) {  // the first query from qi on that has rows
-      for (; qi < a.T; qi += gridDim.x) {
-        qu = query_info<kTree>(a, qi);
-        if (qu.ntiles > 0) break;
-      }
-      return qi;
-    };
-    if (lw == 0 && lane == 0) tc::tma_prefetch(&tm_q);
-    uint32_t nq = 0, nt = 0;
-    int qi = find(blockIdx.x);
-    const __nv_bfloat16* ptr = qi < a.T ? row_ptr(qu, qi, 0) : nullptr;
-    while (qi < a.T && !failed) {
-      if (lw == 0 && lane == 0) {
-        // the query block (8 boxes of 64 heads x 64 dims), once the previous query's last score product has retired
-        if (nq > 0 && !tc::mbar_wait(q_empty, (nq - 1) & 1)) failed = true;
-        if (!failed) {
-          tc::mbar_arrive_expect_tx(q_full, kQBytes);
-          for (int c = 0; c < 8; ++c) tc::tma_load_2d(qbuf + c * kQBox, &tm_q, q_full, 64 * c, qi * kAH);
-        }
-      }
-      ++nq;
-      const int ntiles = qu.ntiles;
-      int next = qi;
-      for (int t = 0; t < ntiles; ++t, ++nt) {
-        const uint32_t par = (nt - 1) & 1;  // phase of the previous tile's releases
-        const long long mine = reinterpret_cast<long long>(ptr);
-        for (int m = 0; m < 4; ++m) {
-          if (nt > 0 && !tc::mbar_wait(box_free + m, par)) failed = true;
-          if (__any_sync(0xffffffffu, failed)) { failed = true; break; }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int r = 2 * i + (lane >> 4), c = lane & 15;
-            const auto* src = reinterpret_cast<const __nv_bfloat16*>(__shfl_sync(0xffffffffu, mine, r));
-            tc::cp_async16(r_base + 2 * m * kBox + 2 * i * 128 + (((c & 7) ^ (r & 7)) << 4),
-                           src ? src + 128 * m + 8 * c : a.pool, src ? 16u : 0u);
-          }
-          tc::cp_async_commit();
-          if (m >= 2) {
-            tc::cp_async_wait_group<2>();
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(rows_full + m - 2);
-          }
-        }
-        if (failed) break;
-        if (t + 1 < ntiles) {
-          ptr = row_ptr(qu, qi, t + 1);
-        } else {
-          next = find(qi + gridDim.x);
-          ptr = next < a.T ? row_ptr(qu, next, 0) : nullptr;
-        }
-        tc::cp_async_wait_group<1>();
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(rows_full + 2);
-        tc::cp_async_wait_group<0>();
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(rows_full + 3);
-      }
-      qi = next;
-    }
-    tc::cp_async_wait_all();
-    // (a query block whose load was issued lands before the CTA exits: its score products wait for it; after a
-    // failed wait it is given the time here)
-    if (failed && nq > 0 && lw == 0 && lane == 0) tc::mbar_wait(q_full, (nq - 1) & 1);
   } else if (warp >= kLoadWarp0) {
     // ------------------------------------------------------------ loaders (warps 9-10, 64 threads)
     const int lt = tid - kLoadWarp0 * 32;
@@ -490,14 +349,14 @@ __global__ void __launch_bounds__(kTree ? kTreeThreads : kThreads, 1)
     }
     uint32_t nq = 0, nt = 0;
     for (int qi = blockIdx.x; qi < a.T && !failed; qi += gridDim.x, ++nq) {
-      const Query qu = query_info<kTree>(a, qi);
+      const Query qu = query_info(a, qi);
       // codes of this thread's rows (lt, lt + 64) of a tile
       auto codes = [&](int t, int& x0, int& x1) {
         const int ra = t * kPR + lt, rb = ra + 64;
         const int ja = (a.sel && ra < qu.nsel) ? a.sel[(size_t)qi * a.topk + ra] : 0;
         const int jb = (a.sel && rb < qu.nsel) ? a.sel[(size_t)qi * a.topk + rb] : 0;
-        x0 = row_code<kTree>(a, qu, ra, ja);
-        x1 = row_code<kTree>(a, qu, rb, jb);
+        x0 = row_code(a, qu, ra, ja);
+        x1 = row_code(a, qu, rb, jb);
       };
       int c0, c1;
       codes(0, c0, c1);
@@ -545,14 +404,14 @@ __global__ void __launch_bounds__(kTree ? kTreeThreads : kThreads, 1)
         bool same = true;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          src[i] = row_src<kTree>(a, rowc[g4 + i], row[i]);
+          src[i] = row_src(a, rowc[g4 + i], row[i]);
           same &= src[i] == src[0];
         }
         same &= src[0] != kSrcNone;
         // a tile of 128 consecutive chunk rows (a window in the chunk): one 128-row box load per 64 dims
         int row_first, row_last;
-        const bool chunk_tile = a.chunk_tiles && row_src<kTree>(a, rowc[0], row_first) == kSrcChunk &&
-                                row_src<kTree>(a, rowc[kPR - 1], row_last) == kSrcChunk;
+        const bool chunk_tile = a.chunk_tiles && row_src(a, rowc[0], row_first) == kSrcChunk &&
+                                row_src(a, rowc[kPR - 1], row_last) == kSrcChunk;
         for (int m = 0; m < 4; ++m) {
           if (m > 0 && nt > 0 && tc::named_bar_any(kBarLoad, kLoaders, !tc::mbar_wait(box_free + m, par))) {
             failed = true;
@@ -607,15 +466,14 @@ __global__ void __launch_bounds__(kTree ? kTreeThreads : kThreads, 1)
     float l[32];
     uint32_t nq = 0, nt = 0;
     for (int qi = blockIdx.x; qi < a.T && !failed; qi += gridDim.x, ++nq) {
-      const Query qu = query_info<kTree>(a, qi);
-      if (kTree && qu.ntiles == 0) { --nq; continue; }
+      const Query qu = query_info(a, qi);
       for (int t = 0; t < qu.ntiles; ++t, ++nt) {
         if (tc::named_bar_any(bar_half, kHalf, !tc::mbar_wait(s_full, nt & 1))) {
           failed = true;
           break;
         }
         tc::fence_after_sync();
-        const bool valid = kTree ? t * kPR + row < qu.nsel + qu.nwin : rowc[row] != kRowNone;
+        const bool valid = rowc[row] != kRowNone;
         float s[32];
         load_scores(tmem + kColS + hb + lane_base, valid, a.scale2, s);
         bool ovf = false;
@@ -745,7 +603,7 @@ __global__ void __launch_bounds__(kTree ? kTreeThreads : kThreads, 1)
         const bool rot = (m == 3) && quad >= 2;
 #pragma unroll
         for (int h = 0; h < 32; ++h) {
-          float v = kTree ? o[h] * f[h] : rnd<__nv_bfloat16>(o[h] * f[h]);  // kTree: one rounding, at the end
+          float v = rnd<__nv_bfloat16>(o[h] * f[h]);
           const float partner = __shfl_xor_sync(0xffffffffu, v, 1);
           if (rot) v = (d & 1) ? fmaf(-partner, rs, v * rc) : fmaf(v, rc, partner * rs);
           obase[(size_t)(hb + h) * kAD + d] = __float2bfloat16_rn(v);
@@ -809,35 +667,8 @@ cudaError_t launch_tc_attend_prefill(const Dims& L, const void* q, const void* p
       !make_tmap_2d_bf16(&tr, ring, (uint64_t)nseq * L.Wr, kAD, kAD * 2, 1) ||
       !make_tmap_2d_bf16(&tkt, kvr, (uint64_t)T, kAD, kAD * 2, a.chunk_tiles ? kPR : 1))
     return cudaErrorInvalidValue;
-  cudaFuncSetAttribute(k_tc_attend_prefill<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  CSA_LAUNCH(k_tc_attend_prefill<false>, dim3(min(T, g_sms_pf)), dim3(kThreads), kSmem, s, tq, tp, tk, tr, tkt, a);
-  return cudaGetLastError();
-}
-
-// A tree's nodes (csa_attend_tree): B * T queries, a persistent CTA per SM.
-cudaError_t launch_tc_attend_tree(const Dims& L, const TreeAttend& t, const int32_t* sel, int32_t* err,
-                                  cudaStream_t s) {
-  if (!g_sms_pf) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&g_sms_pf, cudaDevAttrMultiProcessorCount, dev);
-  }
-  const int Q = t.B * t.T;
-  PfArgs a{};
-  a.sel = sel; a.sink = t.sink; a.inv_freq = t.inv_freq;
-  a.T = Q; a.cap = t.cap; a.topk = L.topk; a.W = L.W; a.Wr = L.Wr; a.ratio = L.ratio; a.qps = 1;
-  a.nodes = t.ws.nodes; a.tree_T = t.T;
-  a.scale2 = L.scale * 1.4426950408889634f;
-  a.out = static_cast<__nv_bfloat16*>(t.out);
-  a.err = err;
-  a.pool = static_cast<const __nv_bfloat16*>(t.pool);
-  a.ring = static_cast<const __nv_bfloat16*>(t.window);
-  a.kvr = static_cast<const __nv_bfloat16*>(t.kv);
-  a.trows = static_cast<const __nv_bfloat16*>(t.rows);
-  CUtensorMap tq;
-  if (!make_tmap_2d_bf16(&tq, t.q, (uint64_t)Q * kAH, kAD, kAD * 2, 64)) return cudaErrorInvalidValue;
-  cudaFuncSetAttribute(k_tc_attend_prefill<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  CSA_LAUNCH(k_tc_attend_prefill<true>, dim3(min(Q, g_sms_pf)), dim3(kTreeThreads), kSmem, s, tq, tq, tq, tq, tq, a);
+  cudaFuncSetAttribute(k_tc_attend_prefill, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  CSA_LAUNCH(k_tc_attend_prefill, dim3(min(T, g_sms_pf)), dim3(kThreads), kSmem, s, tq, tp, tk, tr, tkt, a);
   return cudaGetLastError();
 }
 
