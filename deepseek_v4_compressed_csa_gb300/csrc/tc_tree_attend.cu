@@ -374,19 +374,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tc::cp_async_commit();
-        if (m >= 2) {
-          tc::cp_async_wait_group<2>();
+        if (m >= 1) {
+          tc::cp_async_wait_group<1>();
           tc::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(rows_full + m - 2);
+          if (lane == 0) tc::mbar_arrive(rows_full + m - 1);
         }
       }
       if (failed) break;
       if (by_box) continue;
-      tc::cp_async_wait_group<1>();
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(rows_full + 2);
       tc::cp_async_wait_group<0>();
       tc::fence_proxy_async_smem();
       __syncwarp();
@@ -422,31 +418,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k0 = 0; k0 < keys; k0 += kPR, ++nt) {
         if (!tc::mbar_wait(s_full, nt & 1)) failed = true;
         tc::fence_after_sync();
-        uint32_t u[32];
-        tc::tmem_ld32(ts + kColS, u);
-        tc::tmem_wait_ld();
-        float2 x[16];
-        float mx = -INFINITY;
         const bool live = k0 + row < keys;
+        float2 x[16];  // scores over the reference (log2 units), then probabilities
+        float mx = -INFINITY;
+        auto scores = [&]() {
+          uint32_t u[32];
+          tc::tmem_ld32(ts + kColS, u);
+          tc::tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 r = nr4[i];
-          x[2 * i] = __ffma2_rn(make_float2(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1])), sc2,
-                                make_float2(r.x, r.y));
-          x[2 * i + 1] = __ffma2_rn(make_float2(__uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])), sc2,
-                                    make_float2(r.z, r.w));
-          mx = fmaxf(fmaxf(mx, fmaxf(x[2 * i].x, x[2 * i].y)), fmaxf(x[2 * i + 1].x, x[2 * i + 1].y));
-        }
-        // (a failed wait goes round with the flag, so that the half's threads leave together)
+          for (int i = 0; i < 8; ++i) {
+            const float4 r = nr4[i];
+            x[2 * i] = __ffma2_rn(make_float2(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1])), sc2,
+                                  make_float2(r.x, r.y));
+            x[2 * i + 1] = __ffma2_rn(make_float2(__uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])), sc2,
+                                      make_float2(r.z, r.w));
+          }
+        };
+        // fp32 for the sums (left in x), two bf16 parts of P^T (MN-major) for the PV products
+        auto probabilities = [&]() {
+          if (!live) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = make_float2(-INFINITY, -INFINITY);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 p = make_float2(ex2(x[4 * j + k].x), ex2(x[4 * j + k].y));
+              x[4 * j + k] = p;
+              const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
+              hi[k] = *reinterpret_cast<const uint32_t*>(&h);
+              const __nv_bfloat162 d = __floats2bfloat162_rn(p.x - __uint_as_float(hi[k] << 16),
+                                                             p.y - __uint_as_float(hi[k] & 0xffff0000u));
+              lo[k] = *reinterpret_cast<const uint32_t*>(&d);
+            }
+            const int off = ((4 * half + j) ^ (row & 7)) << 4;
+            *reinterpret_cast<uint4*>(pdst + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(pdst + kPPart + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+          tc::fence_proxy_async_smem();
+        };
+        scores();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, fmaxf(x[i].x, x[i].y));
+        probabilities();
+        // The tile's probabilities stand unless a logit was above the headroom: the question goes round once they are
+        // written, when the half's warps have to meet anyway (a failed wait goes round with it).
         if (tc::named_bar_any(bar, kHalf, failed || (live && mx > kRaiseAt))) {
           if (tc::named_bar_any(bar, kHalf, failed)) {
             failed = true;
             break;
           }
-          // a logit above the headroom: the reference of its head becomes the tile's column maximum
+          // the reference of such a head becomes the tile's column maximum; the sums and O^T are rescaled
           float v[32];
+          {
+            uint32_t u[32];
+            tc::tmem_ld32(ts + kColS, u);
+            tc::tmem_wait_ld();
 #pragma unroll
-          for (int h = 0; h < 32; ++h) v[h] = live ? __uint_as_float(u[h]) * a.scale2 : -INFINITY;
+            for (int h = 0; h < 32; ++h) v[h] = live ? __uint_as_float(u[h]) * a.scale2 : -INFINITY;
+          }
           red[quad * 64 + hb + lane] = reduce_scatter32<true>(v);
           tc::named_bar(bar, kHalf);
 #pragma unroll
@@ -477,38 +509,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::tmem_wait_st();
           }
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            x[i] = __ffma2_rn(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), sc2,
-                              reinterpret_cast<const float2*>(nref + hb)[i]);
+          scores();
+          probabilities();
         }
-        if (!live) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = make_float2(-INFINITY, -INFINITY);
-        }
-        // ---- probabilities: fp32 for the sums, two bf16 parts of P^T (MN-major) for the PV products
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 e = x[4 * j + k];
-            const float2 p = make_float2(ex2(e.x), ex2(e.y));
-            l[4 * j + k] = __fadd2_rn(l[4 * j + k], p);
-            const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
-            hi[k] = *reinterpret_cast<const uint32_t*>(&h);
-            const float2 back = make_float2(__uint_as_float(hi[k] << 16), __uint_as_float(hi[k] & 0xffff0000u));
-            const __nv_bfloat162 d = __floats2bfloat162_rn(p.x - back.x, p.y - back.y);
-            lo[k] = *reinterpret_cast<const uint32_t*>(&d);
-          }
-          const int off = ((4 * half + j) ^ (row & 7)) << 4;
-          *reinterpret_cast<uint4*>(pdst + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(pdst + kPPart + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-        tc::fence_proxy_async_smem();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(p_full);
+#pragma unroll
+        for (int h = 0; h < 16; ++h) l[h] = __fadd2_rn(l[h], x[h]);
       }
       // ---- the output: 1 / Z per head, then O^T dim by dim.  After a failed wait a half comes here at once: the barrier
       // of all softmax warps below is where both learn of it and leave together.
