@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -57,6 +58,10 @@ class _Rows(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("weight", ctypes.c_void_p),
                 ("heads", ctypes.c_int), ("dim", ctypes.c_int), ("norm", ctypes.c_int),
                 ("x_stride", ctypes.c_longlong)]
+
+
+# the same layouts for struct.pack, a few microseconds a call cheaper than building ctypes structures
+_COMP_FMT, _ROWS_FMT = "@4Pi0P", "@3P3iq"
 
 
 _lib = None
@@ -166,6 +171,14 @@ class Layer:
         code = CSA_BF16 if self.dtype == torch.bfloat16 else CSA_F32
         return _Layer(code, self.H, self.D, self.R, self.W, self.ratio, self.Hi, self.Di, self.topk, self.X,
                       float(self.scale), float(self.rms_eps), int(self.rollback), int(self.index_fp8))
+
+    def _packed(self) -> bytes:
+        """The bytes of the C struct (kept: the fields are frozen)."""
+        p = self.__dict__.get("_bytes")
+        if p is None:
+            p = bytes(self._c())
+            object.__setattr__(self, "_bytes", p)
+        return p
 
     def pool_spec(self, d: int):
         """(dtype, row length) of a pool with rows of d values: fp8 index rows are FP8_ROW_BYTES bytes."""
@@ -614,11 +627,8 @@ def attend_verify(layer: Layer, q, kv_new, sink, window, pool, n_rows, sel, n_se
     return err
 
 
-def _tree_ptr(name: str, t, dtype, shape, dev=None):
-    """Checks of one tensor of a tree call (type, shape, contiguity, device); its address."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and (t.is_cuda if dev is None else t.get_device() == dev)):
-        return t.data_ptr()
+def _refuse(name: str, t, dtype, shape, dev):
+    """Raise what is wrong with one tensor of a tree call."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} is required") if t is None else TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -632,10 +642,26 @@ def _tree_ptr(name: str, t, dtype, shape, dev=None):
     raise ValueError(f"{name}: on device {t.get_device()}, the call's tensors are on device {dev}")
 
 
+def _ptrs(dev: int, *specs) -> list:
+    """Addresses of a tree call's tensors, each spec (name, tensor, dtype, shape), after checks of type, shape, device
+    and contiguity."""
+    out = []
+    for name, t, dtype, shape in specs:
+        try:
+            if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+                out.append(t.data_ptr())
+                continue
+        except AttributeError:  # no tensor
+            pass
+        _refuse(name, t, dtype, shape, dev)
+    return out
+
+
 def _tree_err(err, dev):
     if err is None:
         return torch.zeros(1, dtype=torch.int32, device=f"cuda:{dev}")
-    _expect_err(err)
+    if not (isinstance(err, torch.Tensor) and err.dtype is torch.int32 and err.numel() >= 1):
+        _expect_err(err)
     if err.get_device() != dev:
         raise ValueError(f"err: expected a tensor on device {dev}")
     return err
@@ -655,21 +681,34 @@ def _tree_call(fn: str, dev: int, stream, *args):
     f = getattr(_lib or load_library(), fn)
     raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if dev == torch._C._cuda_getDevice():
-        _check(fn, f(*args, raw))
-        return
-    with torch.cuda.device(dev):
-        _check(fn, f(*args, raw))
+        code = f(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            code = f(*args, raw)
+    if code:
+        raise CSAError(fn, code)
 
 
 def _tree_dims(name: str, t, tail: tuple):
     """(B, T, device) of a tensor [B, T, *tail]."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 2 + len(tail) or tuple(t.shape[2:]) != tail:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [B, T{''.join(', %d' % n for n in tail)}]")
+    shape = t.shape
+    if len(shape) != 2 + len(tail) or shape[2:] != tail:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [B, T{''.join(', %d' % n for n in tail)}]")
     if not t.is_cuda:
         raise ValueError(f"{name}: CSA tensors must live on a CUDA device")
-    return t.shape[0], t.shape[1], t.get_device()
+    return shape[0], shape[1], t.get_device()
+
+
+def _tree_comp(layer: Layer, comp: Compressor, which: str, dev: int) -> bytes:
+    """The bytes of a compressor's C struct after the checks of its weights."""
+    n, d = layer.lanes * comp.d, comp.d
+    return struct.pack(_COMP_FMT, *_ptrs(
+        dev, (f"{which}.wkv", comp.wkv, layer.dtype, (n, layer.X)),
+        (f"{which}.wgate", comp.wgate, layer.dtype, (n, layer.X)),
+        (f"{which}.ape", comp.ape, torch.float32, (layer.ratio, n)),
+        (f"{which}.norm_w", comp.norm_w, torch.float32, (d,))), d)
 
 
 def norm_rope(layer: Layer, xs, pos=None, inv_freq=None, parent=None, weights=None, norm=None, outs=None, err=None,
@@ -682,41 +721,51 @@ def norm_rope(layer: Layer, xs, pos=None, inv_freq=None, parent=None, weights=No
     n = len(xs)
     if not 1 <= n <= 4:
         raise ValueError(f"norm_rope takes 1 to 4 tensors, got {n}")
-    weights = [None] * n if weights is None else weights
-    norm = [True] * n if norm is None else norm
-    if len(weights) != n or len(norm) != n or (outs is not None and len(outs) != n):
+    if (weights is not None and len(weights) != n) or (norm is not None and len(norm) != n) or (
+            outs is not None and len(outs) != n):
         raise ValueError("weights, norm and outs need one entry per tensor")
-    if not isinstance(xs[0], torch.Tensor) or xs[0].dim() not in (3, 4):
+    x = xs[0]
+    if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4):
         raise ValueError("xs: expected tensors [B, T, heads, dim] or [B, T, dim]")
-    B, T, dev = xs[0].shape[0], xs[0].shape[1], xs[0].get_device()
+    B, T = x.shape[:2]
+    dev = x.get_device()
     if outs is None:
         new = torch.empty if parent is None else torch.zeros
         outs = [new(x.shape, dtype=x.dtype, device=x.device) for x in xs]
-    rows = (_Rows * n)()
-    for k, x in enumerate(xs):
-        if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4) or tuple(x.shape[:2]) != (B, T):
+    rows = b""
+    dtype = layer.dtype
+    for k in range(n):
+        x, out = xs[k], outs[k]
+        if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4) or x.shape[:2] != (B, T):
             raise ValueError(f"xs[{k}]: expected [{B}, {T}, heads, dim] or [{B}, {T}, dim]")
-        if x.dtype != layer.dtype:
-            raise TypeError(f"xs[{k}]: dtype {x.dtype}, expected {layer.dtype}")
+        if x.dtype is not dtype:
+            raise TypeError(f"xs[{k}]: dtype {x.dtype}, expected {dtype}")
         if not x.is_cuda or x.get_device() != dev:
             raise ValueError(f"xs[{k}]: expected a CUDA tensor on device {dev}")
-        heads, dim = (1 if x.dim() == 3 else x.shape[2]), x.shape[-1]
+        shape = x.shape
+        heads, dim = (1 if len(shape) == 3 else shape[2]), shape[-1]
         stride = 0
         if not x.is_contiguous():
             st = x.stride()
             stride = st[1] if T > 1 else (st[0] if B > 1 else 0)
-            if st[-1] != 1 or (x.dim() == 4 and heads > 1 and st[2] != dim) or (T > 1 and B > 1 and st[0] != T * st[1]):
+            if st[-1] != 1 or (len(shape) == 4 and heads > 1 and st[2] != dim) or (
+                    T > 1 and B > 1 and st[0] != T * st[1]):
                 raise ValueError(f"xs[{k}]: strides {st}; heads must be contiguous, tokens one stride apart")
-        w = weights[k]
-        rows[k] = _Rows(x.data_ptr(), _tree_ptr(f"outs[{k}]", outs[k], layer.dtype, tuple(x.shape), dev),
-                        None if w is None else _tree_ptr(f"weights[{k}]", w, torch.float32, (dim,), dev), heads, dim,
-                        int(bool(norm[k])), stride)
-    p_par = None if parent is None else _tree_ptr("parent", parent, torch.int32, (B, T), dev)
-    p_pos = None if pos is None and inv_freq is None else _tree_ptr("pos", pos, torch.int32, (B,), dev)
-    p_frq = None if inv_freq is None else _tree_ptr("inv_freq", inv_freq, torch.float32, (layer.R // 2,), dev)
-    err = _tree_err(err, dev)
-    L = layer._c()
-    _tree_call("csa_norm_rope", dev, stream, ctypes.byref(L), rows, n, B, T, p_par, p_pos, p_frq, err.data_ptr())
+        if not (isinstance(out, torch.Tensor) and out.dtype is dtype and out.shape == shape
+                and out.get_device() == dev and out.is_contiguous()):
+            _refuse(f"outs[{k}]", out, dtype, shape, dev)
+        w = None if weights is None else weights[k]
+        p_w = 0 if w is None else _ptrs(dev, (f"weights[{k}]", w, torch.float32, (dim,)))[0]
+        rows += struct.pack(_ROWS_FMT, x.data_ptr(), out.data_ptr(), p_w, heads, dim,
+                            1 if norm is None or norm[k] else 0, stride)
+    p_par = p_pos = p_frq = None
+    if parent is not None:
+        p_par, = _ptrs(dev, ("parent", parent, torch.int32, (B, T)))
+    if inv_freq is not None:
+        p_pos, p_frq = _ptrs(dev, ("pos", pos, torch.int32, (B,)),
+                             ("inv_freq", inv_freq, torch.float32, (layer.R // 2,)))
+    _tree_call("csa_norm_rope", dev, stream, layer._packed(), rows, n, B, T, p_par, p_pos, p_frq,
+               _tree_err(err, dev).data_ptr())
     return list(outs)
 
 
@@ -724,52 +773,45 @@ def compress_tree(layer: Layer, comp_a: Compressor, x, parent, pos, frontier_a, 
                   frontier_i=None, proj_i=None, rows_i=None, ws=None, err=None, stream=None):
     """csa_compress_tree: x [B, T, X], parent [B, T]; writes proj_a [B, T, 2 L D], rows_a [B, T, D] and, with comp_i,
     the index pool's proj_i, rows_i.  The frontiers are read only.  Returns the device error word tensor."""
+    dt, i32 = layer.dtype, torch.int32
     B, T, dev = _tree_dims("x", x, (layer.X,))
-    F = _frontier_len(layer)
-    _expect_comp(layer, comp_a, "comp_a")
-    args = [_tree_ptr("x", x, layer.dtype, (B, T, layer.X)), B, T,
-            _tree_ptr("parent", parent, torch.int32, (B, T), dev), _tree_ptr("pos", pos, torch.int32, (B,), dev)]
-    for nm, d, fr, pj, rw in (("a", comp_a.d, frontier_a, proj_a, rows_a),
-                              ("i", comp_i.d if comp_i is not None else 0, frontier_i, proj_i, rows_i)):
-        if nm == "i" and comp_i is None:
-            if fr is not None or pj is not None or rw is not None:
-                raise ValueError("frontier_i, proj_i, rows_i come with comp_i")
-            args += [None, None, None]
-            continue
-        wide = 2 * layer.lanes * d
-        dt, row = layer.pool_spec(d) if nm == "i" else (layer.dtype, d)
-        args += [_tree_ptr(f"frontier_{nm}", fr, layer.dtype, (B, F, wide), dev),
-                 _tree_ptr(f"proj_{nm}", pj, layer.dtype, (B, T, wide), dev),
-                 _tree_ptr(f"rows_{nm}", rw, dt, (B, T, row), dev)]
+    F, wide = _frontier_len(layer), 2 * layer.lanes
+    Ca = _tree_comp(layer, comp_a, "comp_a", dev)
+    p_x, p_par, p_pos, p_fa, p_pa, p_ra, p_frq = _ptrs(
+        dev, ("x", x, dt, (B, T, layer.X)), ("parent", parent, i32, (B, T)), ("pos", pos, i32, (B,)),
+        ("frontier_a", frontier_a, dt, (B, F, wide * comp_a.d)), ("proj_a", proj_a, dt, (B, T, wide * comp_a.d)),
+        ("rows_a", rows_a, dt, (B, T, comp_a.d)), ("inv_freq", inv_freq, torch.float32, (layer.R // 2,)))
+    Ci = p_fi = p_pi = p_ri = None
     if comp_i is not None:
-        _expect_comp(layer, comp_i, "comp_i")
-    args.append(_tree_ptr("inv_freq", inv_freq, torch.float32, (layer.R // 2,), dev))
+        Ci = _tree_comp(layer, comp_i, "comp_i", dev)
+        row_dt, row = layer.pool_spec(comp_i.d)
+        p_fi, p_pi, p_ri = _ptrs(dev, ("frontier_i", frontier_i, dt, (B, F, wide * comp_i.d)),
+                                 ("proj_i", proj_i, dt, (B, T, wide * comp_i.d)), ("rows_i", rows_i, row_dt, (B, T, row)))
+    elif not (frontier_i is None and proj_i is None and rows_i is None):
+        raise ValueError("frontier_i, proj_i, rows_i come with comp_i")
     ws, nb = _tree_ws(layer, OP_COMPRESS_TREE, B, T, 1, ws, dev)
     err = _tree_err(err, dev)
-    L, Ca = layer._c(), comp_a._c()
-    Ci = ctypes.byref(comp_i._c()) if comp_i is not None else None
-    _tree_call("csa_compress_tree", dev, stream, ctypes.byref(L), ctypes.byref(Ca), Ci, *args, ws.data_ptr(), nb,
-               err.data_ptr())
+    _tree_call("csa_compress_tree", dev, stream, layer._packed(), Ca, Ci, p_x, B, T, p_par, p_pos, p_fa, p_pa, p_ra,
+               p_fi, p_pi, p_ri, p_frq, ws.data_ptr(), nb, err.data_ptr())
     return err
 
 
 def index_scores_tree(layer: Layer, iq, iw, ikeys, rows_i, parent, n_rows, pos, scores, err=None, stream=None):
     """csa_index_scores_tree: rotated iq [B, T, Hi, Di], iw [B, T, Hi], ikeys [B, cap, Di], rows_i [B, T, Di];
     writes scores [B, T, cap + T] (fp32).  Returns the device error word tensor."""
-    B, T, dev = _tree_dims("iq", iq, (layer.Hi, layer.Di))
+    dt, i32, Hi, Di = layer.dtype, torch.int32, layer.Hi, layer.Di
+    B, T, dev = _tree_dims("iq", iq, (Hi, Di))
     if not isinstance(ikeys, torch.Tensor) or ikeys.dim() != 3:
-        raise ValueError(f"ikeys: expected [{B}, cap, {layer.Di}]")
+        raise ValueError(f"ikeys: expected [{B}, cap, {Di}]")
     cap = ikeys.shape[1]
-    dt, row = layer.pool_spec(layer.Di)
-    args = [_tree_ptr("iq", iq, layer.dtype, (B, T, layer.Hi, layer.Di)),
-            _tree_ptr("iw", iw, layer.dtype, (B, T, layer.Hi), dev), B, T,
-            _tree_ptr("parent", parent, torch.int32, (B, T), dev), _tree_ptr("ikeys", ikeys, dt, (B, cap, row), dev), cap,
-            _tree_ptr("rows_i", rows_i, dt, (B, T, row), dev), _tree_ptr("n_rows", n_rows, torch.int32, (B,), dev),
-            _tree_ptr("pos", pos, torch.int32, (B,), dev),
-            _tree_ptr("scores", scores, torch.float32, (B, T, cap + T), dev)]
+    key_dt, row = layer.pool_spec(Di)
+    p = _ptrs(dev, ("iq", iq, dt, (B, T, Hi, Di)), ("iw", iw, dt, (B, T, Hi)), ("parent", parent, i32, (B, T)),
+              ("ikeys", ikeys, key_dt, (B, cap, row)), ("rows_i", rows_i, key_dt, (B, T, row)),
+              ("n_rows", n_rows, i32, (B,)), ("pos", pos, i32, (B,)),
+              ("scores", scores, torch.float32, (B, T, cap + T)))
     err = _tree_err(err, dev)
-    L = layer._c()
-    _tree_call("csa_index_scores_tree", dev, stream, ctypes.byref(L), *args, err.data_ptr())
+    _tree_call("csa_index_scores_tree", dev, stream, layer._packed(), p[0], p[1], B, T, p[2], p[3], cap, p[4], p[5],
+               p[6], p[7], err.data_ptr())
     return err
 
 
@@ -778,25 +820,25 @@ def attend_tree(layer: Layer, q, kv, sink, window, pool, rows_a, scores, parent,
     """csa_attend_tree: rotated q [B, T, H, D] and kv [B, T, D]; scores [B, T, cap + T] of index_scores_tree, or None
     (every visible row); out [B, T, H, D]; sel_out [B, T, topk] int32 or None.  The cache is read only.  Returns the
     device error word tensor."""
-    B, T, dev = _tree_dims("q", q, (layer.H, layer.D))
+    dt, i32, f32, H, D = layer.dtype, torch.int32, torch.float32, layer.H, layer.D
+    B, T, dev = _tree_dims("q", q, (H, D))
     if not isinstance(pool, torch.Tensor) or pool.dim() != 3:
-        raise ValueError(f"pool: expected [{B}, cap, {layer.D}]")
-    cap, dt = pool.shape[1], layer.dtype
-    args = [_tree_ptr("q", q, dt, (B, T, layer.H, layer.D)), _tree_ptr("kv", kv, dt, (B, T, layer.D), dev),
-            _tree_ptr("sink", sink, torch.float32, (layer.H,), dev), B, T,
-            _tree_ptr("parent", parent, torch.int32, (B, T), dev),
-            _tree_ptr("window", window, dt, (B, layer.ring_slots, layer.D), dev),
-            _tree_ptr("pool", pool, dt, (B, cap, layer.D), dev), cap,
-            _tree_ptr("rows_a", rows_a, dt, (B, T, layer.D), dev),
-            None if scores is None else _tree_ptr("scores", scores, torch.float32, (B, T, cap + T), dev),
-            _tree_ptr("n_rows", n_rows, torch.int32, (B,), dev), _tree_ptr("pos", pos, torch.int32, (B,), dev),
-            _tree_ptr("inv_freq", inv_freq, torch.float32, (layer.R // 2,), dev),
-            _tree_ptr("out", out, dt, (B, T, layer.H, layer.D), dev),
-            None if sel_out is None else _tree_ptr("sel_out", sel_out, torch.int32, (B, T, layer.topk), dev)]
+        raise ValueError(f"pool: expected [{B}, cap, {D}]")
+    cap = pool.shape[1]
+    p_q, p_kv, p_sink, p_par, p_win, p_pool, p_rows, p_n, p_pos, p_frq, p_out = _ptrs(
+        dev, ("q", q, dt, (B, T, H, D)), ("kv", kv, dt, (B, T, D)), ("sink", sink, f32, (H,)),
+        ("parent", parent, i32, (B, T)), ("window", window, dt, (B, layer.ring_slots, D)),
+        ("pool", pool, dt, (B, cap, D)), ("rows_a", rows_a, dt, (B, T, D)), ("n_rows", n_rows, i32, (B,)),
+        ("pos", pos, i32, (B,)), ("inv_freq", inv_freq, f32, (layer.R // 2,)), ("out", out, dt, (B, T, H, D)))
+    p_sc = p_sel = None
+    if scores is not None:
+        p_sc, = _ptrs(dev, ("scores", scores, f32, (B, T, cap + T)))
+    if sel_out is not None:
+        p_sel, = _ptrs(dev, ("sel_out", sel_out, i32, (B, T, layer.topk)))
     ws, nb = _tree_ws(layer, OP_ATTEND_TREE, B, T, cap, ws, dev)
     err = _tree_err(err, dev)
-    L = layer._c()
-    _tree_call("csa_attend_tree", dev, stream, ctypes.byref(L), *args, ws.data_ptr(), nb, err.data_ptr())
+    _tree_call("csa_attend_tree", dev, stream, layer._packed(), p_q, p_kv, p_sink, B, T, p_par, p_win, p_pool, cap,
+               p_rows, p_sc, p_n, p_pos, p_frq, p_out, p_sel, ws.data_ptr(), nb, err.data_ptr())
     return err
 
 
@@ -807,34 +849,33 @@ def commit_tree(layer: Layer, parent, leaf, pos, n_rows_a, kv, window, proj_a, f
     n_rows_i advance in place unless pos_out, n_rows_a_out, n_rows_i_out are given.  The index pool's arguments come
     together or not at all.  Returns the device error word tensor."""
     B, T, dev = _tree_dims("parent", parent, ())
-    dt, D, F = layer.dtype, layer.D, _frontier_len(layer)
-    i32, vec = torch.int32, (B,)
+    dt, i32, D, F, vec = layer.dtype, torch.int32, layer.D, _frontier_len(layer), (B,)
     wide = 2 * layer.lanes
 
-    def pool_args(nm, d, pj, fr, rw, pl, nr, nr_out, spec):
+    def pool_args(names, d, pj, fr, rw, pl, nr, nr_out, spec):
         if not isinstance(pl, torch.Tensor) or pl.dim() != 3:
-            raise ValueError(f"pool_{nm}: expected [{B}, cap, {spec[1]}]")
+            raise ValueError(f"{names[3]}: expected [{B}, cap, {spec[1]}]")
         cap = pl.shape[1]
-        return [_tree_ptr(f"proj_{nm}", pj, dt, (B, T, wide * d), dev),
-                _tree_ptr(f"frontier_{nm}", fr, dt, (B, F, wide * d), dev),
-                _tree_ptr(f"rows_{nm}", rw, spec[0], (B, T, spec[1]), dev),
-                _tree_ptr(f"pool_{nm}", pl, spec[0], (B, cap, spec[1]), dev), cap,
-                _tree_ptr(f"n_rows_{nm}", nr, i32, vec, dev),
-                _tree_ptr(f"n_rows_{nm}_out", nr if nr_out is None else nr_out, i32, vec, dev)]
+        p = _ptrs(dev, (names[0], pj, dt, (B, T, wide * d)), (names[1], fr, dt, (B, F, wide * d)),
+                  (names[2], rw, spec[0], (B, T, spec[1])), (names[3], pl, spec[0], (B, cap, spec[1])),
+                  (names[4], nr, i32, vec), (names[5], nr if nr_out is None else nr_out, i32, vec))
+        return (*p[:4], cap, *p[4:])
 
-    args = [B, T, _tree_ptr("parent", parent, i32, (B, T)), _tree_ptr("leaf", leaf, i32, vec, dev),
-            _tree_ptr("pos", pos, i32, vec, dev),
-            _tree_ptr("pos_out", pos if pos_out is None else pos_out, i32, vec, dev),
-            _tree_ptr("kv", kv, dt, (B, T, D), dev), _tree_ptr("window", window, dt, (B, layer.ring_slots, D), dev)]
-    args += pool_args("a", D, proj_a, frontier_a, rows_a, pool_a, n_rows_a, n_rows_a_out, (dt, D))
+    p = _ptrs(dev, ("parent", parent, i32, (B, T)), ("leaf", leaf, i32, vec), ("pos", pos, i32, vec),
+              ("pos_out", pos if pos_out is None else pos_out, i32, vec), ("kv", kv, dt, (B, T, D)),
+              ("window", window, dt, (B, layer.ring_slots, D)))
+    pa = pool_args(_COMMIT_A, D, proj_a, frontier_a, rows_a, pool_a, n_rows_a, n_rows_a_out, (dt, D))
     if pool_i is not None:
-        args += pool_args("i", layer.Di, proj_i, frontier_i, rows_i, pool_i, n_rows_i, n_rows_i_out,
-                          layer.pool_spec(layer.Di))
+        pi = pool_args(_COMMIT_I, layer.Di, proj_i, frontier_i, rows_i, pool_i, n_rows_i, n_rows_i_out,
+                       layer.pool_spec(layer.Di))
     elif any(t is not None for t in (n_rows_i, proj_i, frontier_i, rows_i, n_rows_i_out)):
         raise ValueError("n_rows_i, proj_i, frontier_i, rows_i, n_rows_i_out come with pool_i")
     else:
-        args += [None, None, None, None, 0, None, None]
+        pi = (None, None, None, None, 0, None, None)
     err = _tree_err(err, dev)
-    L = layer._c()
-    _tree_call("csa_commit_tree", dev, stream, ctypes.byref(L), *args, err.data_ptr())
+    _tree_call("csa_commit_tree", dev, stream, layer._packed(), B, T, *p, *pa, *pi, err.data_ptr())
     return err
+
+
+_COMMIT_A, _COMMIT_I = (tuple(f.format(k) for f in ("proj_{}", "frontier_{}", "rows_{}", "pool_{}", "n_rows_{}",
+                                                      "n_rows_{}_out")) for k in "ai")

@@ -15,6 +15,8 @@ Tolerances (u = 2^-24, h = half a step of the model dtype at the value: 2^-9 of 
               leaves room for logits up to 32.  fp32: 1e-5 of the row's largest element.
   selection   equal, for the scores that the call was given.
 """
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -217,7 +219,7 @@ def test_compress_tree_fp8_index_rows():
     fa, fi = rnd(cfg, (2, 8, 2048), 21), rnd(cfg, (2, 8, 512), 22)
     got = {}
     for fp8 in (False, True):
-        L = csa.Layer(**{**vars(G.lib_layer(cfg)), "index_fp8": fp8})
+        L = dataclasses.replace(G.lib_layer(cfg), index_fp8=fp8)
         rows_i = (torch.zeros(2, 12, csa.FP8_ROW_BYTES, dtype=torch.uint8, device="cuda") if fp8
                   else torch.zeros(2, 12, 128, dtype=torch.bfloat16, device="cuda"))
         z = lambda n: torch.zeros(2, 12, n, dtype=torch.bfloat16, device="cuda")  # noqa: E731
@@ -226,7 +228,7 @@ def test_compress_tree_fp8_index_rows():
         assert err.item() == 0
         got[fp8] = rows_i
     want = torch.zeros_like(got[True])
-    csa.index_rows_fp8(csa.Layer(**{**vars(G.lib_layer(cfg)), "index_fp8": True}), got[False], want)
+    csa.index_rows_fp8(dataclasses.replace(G.lib_layer(cfg), index_fp8=True), got[False], want)
     live = got[False].any(-1)
     assert live.any() and torch.equal(got[True][live], want[live]) and not got[True][~live].any()
 

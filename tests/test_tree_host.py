@@ -189,3 +189,18 @@ def test_tree_helpers():
     layer = type("L", (), dict(ratio=1, topk=3))
     assert TR.select(layer, s, [], 5, 0).tolist() == [1, 3, 4]
     assert TR.select(layer, np.array([0.0, -0.0, 0.0, -1.0]), [], 4, 0).tolist() == [0, 1, 2]
+
+
+def test_packed_structures_are_the_c_layouts(lib):
+    """The binding packs the C structures as bytes: sizes and fields are those of their ctypes declarations."""
+    import struct
+    assert struct.calcsize(B._COMP_FMT) == ctypes.sizeof(B._Comp)
+    assert struct.calcsize(B._ROWS_FMT) == ctypes.sizeof(B._Rows)
+    c = B._Comp.from_buffer_copy(struct.pack(B._COMP_FMT, 16, 32, 48, 64, 7))
+    assert (c.wkv, c.wgate, c.ape, c.norm_w, c.d) == (16, 32, 48, 64, 7)
+    r = B._Rows.from_buffer_copy(struct.pack(B._ROWS_FMT, 16, 32, 0, 5, 6, 1, 1 << 40))
+    assert (r.x, r.out, r.weight, r.heads, r.dim, r.norm, r.x_stride) == (16, 32, None, 5, 6, 1, 1 << 40)
+    assert LAYER._packed() == bytes(LAYER._c()) and LAYER._packed() is LAYER._packed()
+    import dataclasses
+    other = dataclasses.replace(LAYER, topk=7)
+    assert other._packed() == bytes(other._c()) != LAYER._packed() and other != LAYER
