@@ -732,6 +732,11 @@ static cudaError_t launch_topk(const Dims& L, const float* scores, int cap, cons
 cudaError_t launch_topk_tree(const Dims& L, const float* scores, int B, int T, const int32_t* parent, int cap,
                              const int32_t* n_rows, const int32_t* pos, int32_t* sel, TreeNode* nodes, int32_t* err,
                              cudaStream_t s) {
+  int sms = 0, dev = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (topk_tree_many_fits(B * T, cap, T, sms))
+    return launch_topk_tree_many(L, scores, B, T, parent, cap, n_rows, pos, sel, nodes, err, s);
   const TopkTree tr{parent, T, nodes, err};
   const int32_t* none = nullptr;
   int32_t* no_count = nullptr;

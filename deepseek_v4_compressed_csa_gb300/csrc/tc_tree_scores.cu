@@ -13,7 +13,10 @@
 // Work: the (sequence, group of 4 nodes, tile) triples that exist, in that order, cut into equal runs, one per CTA
 // (one CTA per SM).  Each CTA finds its run by a scan over the sequences' row counts, so ragged batches stay
 // balanced.  Ten warps: 0 TMA (a ring of three key tiles, two query blocks of 64 KB), 1 MMA (two accumulators of 256
-// columns), 2-9 epilogue: two warps per TMEM lane quarter, two nodes each.
+// columns), 2-9 epilogue: two warps per TMEM lane quarter, two nodes each.  Of shared memory's 128 bytes a clock the
+// products take 96 and the key tiles 32, so the epilogue stays away from it: a warp keeps its 128 head weights in
+// registers, two bf16 to each (read from shared memory for every tile they cost 256 of a tile's clocks, and 60 us
+// became what 512 nodes over 8.2K rows took).
 #include "kernels.h"
 #include "tc.cuh"
 #include "tree.cuh"
@@ -31,8 +34,7 @@ constexpr int kStages = 3, kQSlots = 2, kAcc = 2;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kOffK = kQSlots * kQBytes;
-constexpr int kOffW = kOffK + kStages * kTileBytes;  // [256] head weights of the group in the epilogue
-constexpr int kOffBars = kOffW + kN * 4;
+constexpr int kOffBars = kOffK + kStages * kTileBytes;
 constexpr int kNumBars = 2 * kStages + 2 * kQSlots + 2 * kAcc + 1;
 constexpr int kOffRun = kOffBars + kNumBars * 8;     // the CTA's run: b, group, tile, count; TMEM address
 constexpr int kSmem = kOffRun + 32 + 1024;
@@ -86,7 +88,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qbuf = smem;
   uint8_t* kbuf = smem + kOffK;
-  float* wbuf = reinterpret_cast<float*>(smem + kOffW);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBars);
   uint64_t* empty = full + kStages;
   uint64_t* q_full = empty + kStages;
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kAcc; ++s) {
       tc::mbar_init(&acc_full[s], 1);
-      tc::mbar_init(&acc_empty[s], 32 * kEpiWarps);
+      tc::mbar_init(&acc_empty[s], kEpiWarps);
     }
     tc::mbar_init(drain, 1);
     tc::fence_mbar_init();
@@ -242,73 +243,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int quarter = warp & 3, row = quarter * 32 + lane, e = threadIdx.x - 64;
+    const int quarter = warp & 3, row = quarter * 32 + lane;
     const int q0 = ((warp - 2) >> 2) * 2;  // this warp's two nodes of the group
     int acc = 0;
     uint32_t acc_ph = 0;
     bool fresh = true;
     uint64_t closers[2] = {0, 0};
     bool live[2] = {false, false};
+    uint32_t wt[2][32];  // head weights 2 i (low half) and 2 i + 1 as bf16
     int n = 0;
     for (; w.left > 0; w.next(a)) {
       if (fresh) {
-        const int i0 = w.g * kG, cnt = min(kG, a.T - i0);
-        const size_t qb = (size_t)w.b * a.T + i0;
-        const float wt = (e >> 6) < cnt ? __bfloat162float(a.iw[qb * 64 + e]) * a.wscale : 0.f;
         n = a.n_rows[w.b];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+          const int i = w.g * kG + q0 + u, node = min(i, a.T - 1);
+          const uint4* src = reinterpret_cast<const uint4*>(a.iw + ((size_t)w.b * a.T + node) * 64);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint4 r = __ldg(src + j);
+            wt[u][4 * j] = r.x;
+            wt[u][4 * j + 1] = r.y;
+            wt[u][4 * j + 2] = r.z;
+            wt[u][4 * j + 3] = r.w;
+          }
           bool bad = false;
-          const uint64_t m = tree_path_warp(a.parent + (size_t)w.b * a.T, a.T, min(i0 + q0 + u, a.T - 1), bad);
-          live[u] = q0 + u < cnt && m != 0;
+          const uint64_t m = tree_path_warp(a.parent + (size_t)w.b * a.T, a.T, node, bad);
+          live[u] = i < a.T && m != 0;
           closers[u] = tree_closers(m, a.pos[w.b], a.ratio);
           if (bad && lane == 0) atomicOr(a.err, CSA_DEV_STATE);
         }
-        tc::named_bar(1, 32 * kEpiWarps);  // the previous group's weights are no longer read
-        wbuf[e] = wt;
-        tc::named_bar(1, 32 * kEpiWarps);
       }
-      // (after a wait that ran out, the rest of the group is walked without waiting)
+      // (after a wait that ran out, the run is walked without waiting)
       if (!failed) failed = __any_sync(0xffffffffu, !tc::mbar_wait(&acc_full[acc], acc_ph));
       tc::fence_after_sync();
-      uint32_t v[2][64];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + acc * kN + (q0 + u) * 64;
-        tc::tmem_ld32(ta, v[u]);
-        tc::tmem_ld32(ta + 32, v[u] + 32);
-      }
-      tc::tmem_wait_ld();
-      tc::fence_before_sync();
-      tc::mbar_arrive(&acc_empty[acc]);
       const bool tree = w.t == w.tiles - 1;
       const int col = tree ? n + row : w.t * kRows + row;
       const bool in = tree ? row < a.T : col < n;
-      const float4* w4 = reinterpret_cast<const float4*>(wbuf);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
+        uint32_t v[64];
+        const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + acc * kN + (q0 + u) * 64;
+        tc::tmem_ld32(ta, v);
+        tc::tmem_ld32(ta + 32, v + 32);
+        tc::tmem_wait_ld();
+        if (u == 1) {  // the accumulator has been read
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&acc_empty[acc]);
+        }
         // four partial sums (heads 0, 1, 2, 3 mod 4), as two packed pairs
         float2 s01 = make_float2(0.f, 0.f), s23 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int h4 = 0; h4 < 16; ++h4) {
-          const float4 wt = w4[(q0 + u) * 16 + h4];
-          s01 = __ffma2_rn(make_float2(wt.x, wt.y), make_float2(fmaxf(__uint_as_float(v[u][4 * h4]), 0.f),
-                                                                fmaxf(__uint_as_float(v[u][4 * h4 + 1]), 0.f)), s01);
-          s23 = __ffma2_rn(make_float2(wt.z, wt.w), make_float2(fmaxf(__uint_as_float(v[u][4 * h4 + 2]), 0.f),
-                                                                fmaxf(__uint_as_float(v[u][4 * h4 + 3]), 0.f)), s23);
+        for (int h = 0; h < 32; h += 2) {
+          const uint32_t w0 = wt[u][h], w1 = wt[u][h + 1];
+          s01 = __ffma2_rn(make_float2(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u)),
+                           make_float2(fmaxf(__uint_as_float(v[2 * h]), 0.f), fmaxf(__uint_as_float(v[2 * h + 1]), 0.f)),
+                           s01);
+          s23 = __ffma2_rn(make_float2(__uint_as_float(w1 << 16), __uint_as_float(w1 & 0xffff0000u)),
+                           make_float2(fmaxf(__uint_as_float(v[2 * h + 2]), 0.f),
+                                       fmaxf(__uint_as_float(v[2 * h + 3]), 0.f)),
+                           s23);
         }
-        float s = (s01.x + s01.y) + (s23.x + s23.y);
+        float s = ((s01.x + s01.y) + (s23.x + s23.y)) * a.wscale;
         if (tree && !((closers[u] >> (row & 63)) & 1)) s = -INFINITY;
-        if (in && live[u])
-          a.scores[((size_t)w.b * a.T + w.g * kG + q0 + u) * (a.cap + a.T) + col] = s;
+        if (in && live[u]) a.scores[((size_t)w.b * a.T + w.g * kG + q0 + u) * (a.cap + a.T) + col] = s;
       }
       fresh = w.last_of_group();
       if (++acc == kAcc) { acc = 0; acc_ph ^= 1; }
-      // one answer for the warps that share the weights' barrier
-      if (fresh && tc::named_bar_any(2, 32 * kEpiWarps, failed)) {
-        failed = true;
-        break;
-      }
     }
   }
   if (failed) atomicOr(a.err, tc::kErrTimeout);

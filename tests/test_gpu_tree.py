@@ -291,6 +291,9 @@ AT_CASES = {
     "flash_extremes": ("flash", [TR.bushy(5), TR.chain(5)], [2803, 2900], "extremes"),
     "flash_all_rows": ("flash", [TR.bushy(4)], [1001], None),
     "flash_many": ("flash", [TR.bushy(16, s) for s in range(12)], [2100 + 37 * s for s in range(12)], "normal"),
+    # more nodes than SMs: the selection kernel of many nodes; the last ones see fewer rows than they may keep
+    "flash_many_ties": ("flash", [TR.bushy(16, s) for s in range(11)], [2100 + 53 * s for s in range(10)] + [900], "ties"),
+    "flash_many_extremes": ("flash", [TR.bushy(32, s) for s in range(6)], [2801, 2300, 2044, 2045, 3000, 7], "extremes"),
     "flash_t64": ("flash", [TR.chain(64), TR.bushy(64)], [2500, 90], "normal"),
     "flash_long": ("flash", [TR.bushy(3)], [70001], "normal"),
     "flash_r128": ("flash_r128", [TR.chain(40), TR.bushy(33)], [120, 30000], None),
