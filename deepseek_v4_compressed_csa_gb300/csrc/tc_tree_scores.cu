@@ -51,6 +51,12 @@ struct TsArgs {
   int32_t* err;
 };
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Tiles of a group of sequence b: its committed rows and one of the tree's rows; 0 when the state is inconsistent.
 __device__ __forceinline__ int seq_tiles(const TsArgs& a, int b) {
   const int p0 = __ldg(a.pos + b), n = __ldg(a.n_rows + b);
@@ -58,25 +64,27 @@ __device__ __forceinline__ int seq_tiles(const TsArgs& a, int b) {
   return (n + kRows - 1) / kRows + 1;
 }
 
-// Walks the CTA's run: (b, g, t) of its items in order.
+// Walks the CTA's run group by group: tiles t .. t + cnt - 1 of group g of sequence b, of `tiles` in all.
 struct Walk {
-  int b, g, t, tiles, left;
+  int b, g, t, tiles, left, cnt;
   __device__ __forceinline__ void start(const TsArgs& a, const int* run) {
     b = run[0];
     g = run[1];
     t = run[2];
     left = run[3];
     tiles = left > 0 ? seq_tiles(a, b) : 0;
+    cnt = min(left, tiles - t);
   }
-  __device__ __forceinline__ bool last_of_group() const { return t == tiles - 1 || left == 1; }
   __device__ __forceinline__ void next(const TsArgs& a) {
-    --left;
-    if (++t < tiles || left <= 0) return;
+    left -= cnt;
+    if (left <= 0) return;
     t = 0;
-    if (++g < a.groups) return;
-    g = 0;
-    do tiles = seq_tiles(a, ++b);
-    while (tiles == 0 && b < a.B - 1);
+    if (++g == a.groups) {
+      g = 0;
+      do tiles = seq_tiles(a, ++b);
+      while (tiles == 0 && b < a.B - 1);
+    }
+    cnt = min(left, tiles);
   }
 };
 
@@ -174,32 +182,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       int stage = 0, nq = 0;
       uint32_t phase = 0, used = 0, par = 0, q_used = 0, q_par = 0;
-      bool fresh = true;  // the next item starts a group
-      for (; w.left > 0; w.next(a)) {
-        if (fresh) {
-          const int slot = nq % kQSlots;
-          const uint32_t ph = (nq / kQSlots) & 1;
-          if (!tc::mbar_wait(&q_empty[slot], ph ^ 1)) { failed = true; break; }
-          const int row = (w.b * a.T + w.g * kG) * 64;
-          tc::mbar_arrive_expect_tx(&q_full[slot], kQBytes);
-          tc::tma_load_2d(qbuf + slot * kQBytes, &tm_q, &q_full[slot], 0, row);
-          tc::tma_load_2d(qbuf + slot * kQBytes + kQBytes / 2, &tm_q, &q_full[slot], 64, row);
-          q_used |= 1u << slot;
-          q_par = (q_par & ~(1u << slot)) | (ph << slot);
-          ++nq;
+      for (; w.left > 0 && !failed; w.next(a), ++nq) {
+        const int slot = nq % kQSlots;
+        const uint32_t ph = (nq / kQSlots) & 1;
+        if (!tc::mbar_wait(&q_empty[slot], ph ^ 1)) { failed = true; break; }
+        const int qrow = (w.b * a.T + w.g * kG) * 64;
+        tc::mbar_arrive_expect_tx(&q_full[slot], kQBytes);
+        tc::tma_load_2d(qbuf + slot * kQBytes, &tm_q, &q_full[slot], 0, qrow);
+        tc::tma_load_2d(qbuf + slot * kQBytes + kQBytes / 2, &tm_q, &q_full[slot], 64, qrow);
+        q_used |= 1u << slot;
+        q_par = (q_par & ~(1u << slot)) | (ph << slot);
+        for (int t = w.t; t < w.t + w.cnt; ++t) {
+          if (!tc::mbar_wait(&empty[stage], phase ^ 1)) { failed = true; break; }
+          const bool tree = t == w.tiles - 1;
+          const CUtensorMap* tm = tree ? &tm_rows : &tm_keys;
+          const int row = tree ? w.b * a.T : w.b * a.cap + t * kRows;
+          uint8_t* dst = kbuf + stage * kTileBytes;
+          tc::mbar_arrive_expect_tx(&full[stage], kTileBytes);
+          tc::tma_load_2d(dst, tm, &full[stage], 0, row);
+          tc::tma_load_2d(dst + kTileBytes / 2, tm, &full[stage], 64, row);
+          used |= 1u << stage;
+          par = (par & ~(1u << stage)) | (phase << stage);
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
-        if (!tc::mbar_wait(&empty[stage], phase ^ 1)) { failed = true; break; }
-        const bool tree = w.t == w.tiles - 1;
-        const CUtensorMap* tm = tree ? &tm_rows : &tm_keys;
-        const int row = tree ? w.b * a.T : w.b * a.cap + w.t * kRows;
-        uint8_t* dst = kbuf + stage * kTileBytes;
-        tc::mbar_arrive_expect_tx(&full[stage], kTileBytes);
-        tc::tma_load_2d(dst, tm, &full[stage], 0, row);
-        tc::tma_load_2d(dst + kTileBytes / 2, tm, &full[stage], 64, row);
-        used |= 1u << stage;
-        par = (par & ~(1u << stage)) | (phase << stage);
-        if (++stage == kStages) { stage = 0; phase ^= 1; }
-        fresh = w.last_of_group();
       }
       // every load issued must land before the CTA may exit
       for (int s = 0; s < kStages; ++s)
@@ -209,34 +214,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
-    if (lane == 0) {
+    // (one elected thread; descriptors as a base plus constants: what this thread does between two tiles' products is
+    // time that the tensor pipe may stand still)
+    if (elect_one()) {
       constexpr uint32_t idesc = tc::idesc_bf16(kRows, kN);
+      const uint64_t kd = tc::sdesc_kmajor_sw128(tc::smem_u32(kbuf)), qd = tc::sdesc_kmajor_sw128(tc::smem_u32(qbuf));
       int stage = 0, acc = 0, nq = 0;
       uint32_t phase = 0, acc_ph = 0;
-      bool fresh = true;
-      for (; w.left > 0; w.next(a)) {
-        if (fresh) {
-          if (!tc::mbar_wait(&q_full[nq % kQSlots], (nq / kQSlots) & 1)) { failed = true; break; }
-          ++nq;
-        }
-        const int slot = (nq - 1) % kQSlots;
-        if (!tc::mbar_wait(&full[stage], phase)) { failed = true; break; }
-        if (!tc::mbar_wait(&acc_empty[acc], acc_ph ^ 1)) { failed = true; break; }
-        tc::fence_after_sync();
-        const uint32_t a_base = tc::smem_u32(kbuf + stage * kTileBytes);
-        const uint32_t b_base = tc::smem_u32(qbuf + slot * kQBytes);
+      for (; w.left > 0 && !failed; w.next(a), ++nq) {
+        const int slot = nq % kQSlots;
+        if (!tc::mbar_wait(&q_full[slot], (nq / kQSlots) & 1)) { failed = true; break; }
+        const uint64_t bd = qd + slot * (kQBytes >> 4);
+#pragma unroll 1
+        for (int j = 0; j < w.cnt; ++j) {
+          if (!tc::mbar_wait(&full[stage], phase) || !tc::mbar_wait(&acc_empty[acc], acc_ph ^ 1)) {
+            failed = true;
+            break;
+          }
+          tc::fence_after_sync();
+          const uint64_t ad = kd + stage * (kTileBytes >> 4);
+          const uint32_t d = tmem + acc * kN;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint64_t ad = tc::sdesc_kmajor_sw128(a_base + (kk >> 2) * (kTileBytes / 2) + (kk & 3) * 32);
-          const uint64_t bd = tc::sdesc_kmajor_sw128(b_base + (kk >> 2) * (kQBytes / 2) + (kk & 3) * 32);
-          tc::mma_bf16(tmem + acc * kN, ad, bd, idesc, kk > 0);
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma_bf16(d, ad + (((kk >> 2) * (kTileBytes / 2) + (kk & 3) * 32) >> 4),
+                         bd + (((kk >> 2) * (kQBytes / 2) + (kk & 3) * 32) >> 4), idesc, kk > 0);
+          tc::mma_commit(&empty[stage]);
+          tc::mma_commit(&acc_full[acc]);
+          if (++acc == kAcc) { acc = 0; acc_ph ^= 1; }
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
-        tc::mma_commit(&empty[stage]);
-        tc::mma_commit(&acc_full[acc]);
-        fresh = w.last_of_group();
-        if (fresh) tc::mma_commit(&q_empty[slot]);
-        if (++acc == kAcc) { acc = 0; acc_ph ^= 1; }
-        if (++stage == kStages) { stage = 0; phase ^= 1; }
+        tc::mma_commit(&q_empty[slot]);
       }
       tc::mma_commit(drain);  // every MMA retires before tensor memory is released
       if (!tc::mbar_wait(drain, 0)) failed = true;
@@ -247,70 +254,73 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q0 = ((warp - 2) >> 2) * 2;  // this warp's two nodes of the group
     int acc = 0;
     uint32_t acc_ph = 0;
-    bool fresh = true;
     uint64_t closers[2] = {0, 0};
     bool live[2] = {false, false};
     uint32_t wt[2][32];  // head weights 2 i (low half) and 2 i + 1 as bf16
-    int n = 0;
+    const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + q0 * 64;
     for (; w.left > 0; w.next(a)) {
-      if (fresh) {
-        n = a.n_rows[w.b];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int i = w.g * kG + q0 + u, node = min(i, a.T - 1);
-          const uint4* src = reinterpret_cast<const uint4*>(a.iw + ((size_t)w.b * a.T + node) * 64);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint4 r = __ldg(src + j);
-            wt[u][4 * j] = r.x;
-            wt[u][4 * j + 1] = r.y;
-            wt[u][4 * j + 2] = r.z;
-            wt[u][4 * j + 3] = r.w;
-          }
-          bool bad = false;
-          const uint64_t m = tree_path_warp(a.parent + (size_t)w.b * a.T, a.T, node, bad);
-          live[u] = i < a.T && m != 0;
-          closers[u] = tree_closers(m, a.pos[w.b], a.ratio);
-          if (bad && lane == 0) atomicOr(a.err, CSA_DEV_STATE);
-        }
-      }
-      // (after a wait that ran out, the run is walked without waiting)
-      if (!failed) failed = __any_sync(0xffffffffu, !tc::mbar_wait(&acc_full[acc], acc_ph));
-      tc::fence_after_sync();
-      const bool tree = w.t == w.tiles - 1;
-      const int col = tree ? n + row : w.t * kRows + row;
-      const bool in = tree ? row < a.T : col < n;
+      const int n = a.n_rows[w.b], stride = a.cap + a.T;
+      float* out = a.scores + ((size_t)w.b * a.T + w.g * kG + q0) * stride;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        uint32_t v[64];
-        const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + acc * kN + (q0 + u) * 64;
-        tc::tmem_ld32(ta, v);
-        tc::tmem_ld32(ta + 32, v + 32);
-        tc::tmem_wait_ld();
-        if (u == 1) {  // the accumulator has been read
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&acc_empty[acc]);
-        }
-        // four partial sums (heads 0, 1, 2, 3 mod 4), as two packed pairs
-        float2 s01 = make_float2(0.f, 0.f), s23 = make_float2(0.f, 0.f);
+        const int i = w.g * kG + q0 + u, node = min(i, a.T - 1);
+        const uint4* src = reinterpret_cast<const uint4*>(a.iw + ((size_t)w.b * a.T + node) * 64);
 #pragma unroll
-        for (int h = 0; h < 32; h += 2) {
-          const uint32_t w0 = wt[u][h], w1 = wt[u][h + 1];
-          s01 = __ffma2_rn(make_float2(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u)),
-                           make_float2(fmaxf(__uint_as_float(v[2 * h]), 0.f), fmaxf(__uint_as_float(v[2 * h + 1]), 0.f)),
-                           s01);
-          s23 = __ffma2_rn(make_float2(__uint_as_float(w1 << 16), __uint_as_float(w1 & 0xffff0000u)),
-                           make_float2(fmaxf(__uint_as_float(v[2 * h + 2]), 0.f),
-                                       fmaxf(__uint_as_float(v[2 * h + 3]), 0.f)),
-                           s23);
+        for (int j = 0; j < 8; ++j) {
+          const uint4 r = __ldg(src + j);
+          wt[u][4 * j] = r.x;
+          wt[u][4 * j + 1] = r.y;
+          wt[u][4 * j + 2] = r.z;
+          wt[u][4 * j + 3] = r.w;
         }
-        float s = ((s01.x + s01.y) + (s23.x + s23.y)) * a.wscale;
-        if (tree && !((closers[u] >> (row & 63)) & 1)) s = -INFINITY;
-        if (in && live[u]) a.scores[((size_t)w.b * a.T + w.g * kG + q0 + u) * (a.cap + a.T) + col] = s;
+        bool bad = false;
+        const uint64_t m = tree_path_warp(a.parent + (size_t)w.b * a.T, a.T, node, bad);
+        live[u] = i < a.T && m != 0;
+        closers[u] = tree_closers(m, a.pos[w.b], a.ratio);
+        if (bad && lane == 0) atomicOr(a.err, CSA_DEV_STATE);
       }
-      fresh = w.last_of_group();
-      if (++acc == kAcc) { acc = 0; acc_ph ^= 1; }
+#pragma unroll 1
+      for (int t = w.t; t < w.t + w.cnt; ++t) {
+        // (after a wait that ran out, the run is walked without waiting)
+        if (!failed) failed = __any_sync(0xffffffffu, !tc::mbar_wait(&acc_full[acc], acc_ph));
+        tc::fence_after_sync();
+        const bool tree = t == w.tiles - 1;
+        const int col = tree ? n + row : t * kRows + row;
+        const bool in = tree ? row < a.T : col < n;
+        uint32_t ta = t0 + acc * kN;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t v[64];
+          tc::tmem_ld32(ta, v);
+          tc::tmem_ld32(ta + 32, v + 32);
+          tc::tmem_wait_ld();
+          if (u == 1) {  // the accumulator has been read
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&acc_empty[acc]);
+          }
+          // (the packed weights change as far as the compiler knows: unpacked ahead of the loop they would not fit)
+#pragma unroll
+          for (int h = 0; h < 32; ++h) asm volatile("" : "+r"(wt[u][h]));
+          // four partial sums (heads 0, 1, 2, 3 mod 4), as two packed pairs
+          float2 s01 = make_float2(0.f, 0.f), s23 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int h = 0; h < 32; h += 2) {
+            const uint32_t w0 = wt[u][h], w1 = wt[u][h + 1];
+            s01 = __ffma2_rn(
+                make_float2(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u)),
+                make_float2(fmaxf(__uint_as_float(v[2 * h]), 0.f), fmaxf(__uint_as_float(v[2 * h + 1]), 0.f)), s01);
+            s23 = __ffma2_rn(
+                make_float2(__uint_as_float(w1 << 16), __uint_as_float(w1 & 0xffff0000u)),
+                make_float2(fmaxf(__uint_as_float(v[2 * h + 2]), 0.f), fmaxf(__uint_as_float(v[2 * h + 3]), 0.f)), s23);
+          }
+          float s = ((s01.x + s01.y) + (s23.x + s23.y)) * a.wscale;
+          if (tree && !((closers[u] >> (row & 63)) & 1)) s = -INFINITY;
+          if (in && live[u]) out[u * stride + col] = s;
+          ta += 64;
+        }
+        if (++acc == kAcc) { acc = 0; acc_ph ^= 1; }
+      }
     }
   }
   if (failed) atomicOr(a.err, tc::kErrTimeout);
