@@ -11,10 +11,12 @@
 // a product takes 48 and 64 clocks (it waits for shared memory below N = 128): 1536 + 2304 clocks a tile.  Shared memory
 // holds one tile (128 KB), the query block (64 KB) and P (32 KB), tensor memory the two halves of O^T and S^T, so S^T
 // of the next tile cannot be formed while a tile's softmax runs; the design keeps that gap and everything else short:
-//   loaders (warps 9-11)  copy rows by address with 16-byte cp.async, two rows' 256 bytes an instruction, in four pairs of 64-dim boxes: a pair of
-//     the next tile is refilled as soon as the PV products of the current tile have read it.  (As tile::gather4
-//     requests, 256 a tile, the same rows took 11.7 us a tile at ~7 B a clock per SM.)  A tile of consecutive committed
-//     rows (no selection) is eight TMA boxes.
+//   loaders (warps 9-15)  fill a tile in four pairs of 64-dim boxes: a pair of the next tile is refilled as soon as the
+//     PV products of the current tile have read it.  Consecutive committed rows (no selection) are TMA boxes; 128
+//     selected committed rows are 256 tile::gather4 requests, ten threads of each warp issuing (a warp issues one every
+//     ~75 clocks whatever its threads do: two warps took 11.7 us a tile, seven are near the copy engine's own rate);
+//     tiles of mixed sources (window, path, the selection's end) are 16-byte cp.async by address, which the products'
+//     own use of shared memory slows to ~28 B a clock where the copy engine keeps its pace.
 //   MMA (warp 8)  one thread; descriptors are a base plus a constant: built from addresses every time they cost it
 //     ~90 clocks a product, twice what the tensor pipe takes.
 //   softmax (warps 0-7)  thread = (key row, 32 heads).  The reference that exponents are taken against is the head's
@@ -40,7 +42,7 @@ constexpr int kPPart = kPR * 128;        // P^T part: 128 keys x 64 heads, MN-ma
 constexpr int kSoft = 256;               // warps 0-7
 constexpr int kHalf = kSoft / 2;         // threads of one head half
 constexpr int kMmaWarp = 8;
-constexpr int kLoadWarp0 = 9, kLoadWarps = 3;  // twelve warps in all: three per SM quarter, 168 registers a thread
+constexpr int kLoadWarp0 = 9, kLoadWarps = 7;  // sixteen warps in all, 128 registers a thread
 constexpr int kThreads = 32 * (kLoadWarp0 + kLoadWarps);
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColO3 = 384;         // O^T tile 3 (hi + lo in one accumulator); tiles 0-2: 128 m, hi | lo
@@ -141,7 +143,8 @@ __device__ __forceinline__ float reduce_scatter32(float (&v)[32]) {
 
 __global__ void __launch_bounds__(kThreads, 1)
     k_tc_tree_attend(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_out,
-                     const __grid_constant__ CUtensorMap tm_pool, const __grid_constant__ TaArgs a) {
+                     const __grid_constant__ CUtensorMap tm_pool, const __grid_constant__ CUtensorMap tm_row,
+                     const __grid_constant__ TaArgs a) {
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -180,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tma_prefetch(&tm_q);
     tc::tma_prefetch(&tm_out);
     tc::tma_prefetch(&tm_pool);
+    tc::tma_prefetch(&tm_row);
   }
   pdl_wait();
   if (warp == kMmaWarp) {
@@ -270,27 +274,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kLoadWarp0) {
     // ------------------------------------------------------------ loaders
-    // Warp w's instruction k of a pair copies 256 bytes of rows 2 i and 2 i + 1, i = w + 3 k (k < 22, i < 64), a half
-    // warp each.  Lane l holds the address of row 2 i + l / 16 of the instructions k = l % 16 and 16 + l % 16, so that one
-    // shuffle hands a half its row; the shuffles of eleven instructions go before their copies, which lets them overlap
-    // (one after another an instruction took ~95 clocks).
+    // By address: warp w's instruction k of a pair copies 256 bytes of rows 2 i and 2 i + 1, i = w + 7 k (i < 64), a
+    // half warp each; lane l holds the address of row 2 (w + 7 (l % 16)) + l / 16, so that one shuffle hands a half its
+    // row.  By gather: lane l of warp w requests box j % 2 of a pair and the four rows 4 (j / 2) .. of it, j = w + 7 l.
     // Nothing that takes long stands between a tile's copies: while tile i is copied, the columns of tile i + 2 are
     // being read, the rows of tile i + 1 are on their way into L2 (its columns have arrived), and the next node's
     // record is in registers.
+    constexpr int kInstr = (64 + kLoadWarps - 1) / kLoadWarps;  // 10
     const int w = warp - kLoadWarp0;
     const uint32_t r_base = tc::smem_u32(rows) + ((lane >> 3) & 1) * kBox;
     const int c = lane & 15;
-    const int r0 = 2 * (w + 3 * c) + (lane >> 4), r1 = c < 6 ? r0 + 2 * 3 * 16 : kPR;  // this lane's rows of a tile
+    const int my_row = c < kInstr && w + kLoadWarps * c < 64 ? 2 * (w + kLoadWarps * c) + (lane >> 4) : kPR;
+    const int j = w + kLoadWarps * lane;  // this lane's gather of a pair (none: j >= 64)
+    const int n_gather = (64 - w + kLoadWarps - 1) / kLoadWarps;
     struct Tile {  // a tile of the walk: query, first key, the query's keys and record
       int qi, k0, keys;
       TreeNode rec;
     };
-    auto load_node = [&](int qi) { return a.nodes[min(qi, a.Q - 1)]; };
     TreeNode ahead;  // the record of the query after the walk's
     auto start_query = [&](Tile& t, int qi) {  // the first query from qi on that has keys; `ahead` is qi's record
       for (; qi < a.Q; qi += gridDim.x) {
         t.rec = ahead;
-        ahead = load_node(qi + gridDim.x);
+        ahead = a.nodes[min(qi + (int)gridDim.x, a.Q - 1)];
         t.keys = node_keys(a, t.rec);
         if (t.keys > 0) break;
       }
@@ -302,24 +307,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       t.k0 += kPR;
       if (t.k0 >= t.keys) start_query(t, t.qi + gridDim.x);
     };
-    auto boxes = [&](const Tile& t) { return !a.sel && t.k0 + kPR <= t.rec.n; };  // 128 consecutive committed rows
-    auto column = [&](const Tile& t, int r) {  // of the tile's row r, where a selection has to be read for it
-      return t.qi < a.Q && a.sel && t.k0 + r < t.rec.nsel ? __ldg(a.sel + (size_t)t.qi * a.topk + t.k0 + r) : 0;
+    struct Columns {  // of this lane's row, of its gather's rows, of the tile's last row
+      int own, g[4], last;
     };
-    auto address = [&](const Tile& t, int r, int col) -> const __nv_bfloat16* {
-      if (t.qi >= a.Q || r >= kPR || t.k0 + r >= t.keys || boxes(t)) return nullptr;
-      const __nv_bfloat16* p = key_row(a, t.rec, t.qi, t.k0 + r, col);
+    auto columns = [&](const Tile& t, Columns& x) {
+      if (t.qi >= a.Q || !a.sel) return;
+      const int32_t* p = a.sel + (size_t)t.qi * a.topk + t.k0;
+      const int n = t.rec.nsel - t.k0;
+      if (my_row < min(n, kPR)) x.own = __ldg(p + my_row);
+      if (n >= kPR) {
+        x.last = __ldg(p + kPR - 1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j < 64) x.g[e] = __ldg(p + 4 * (j >> 1) + e);
+      }
+    };
+    enum { kByAddress, kByBox, kByGather };
+    auto tile_mode = [&](const Tile& t, const Columns& x) {
+      if (!a.sel) return t.k0 + kPR <= t.rec.n ? kByBox : kByAddress;
+      return t.k0 + kPR <= t.rec.nsel && x.last < t.rec.n ? kByGather : kByAddress;  // (columns ascend)
+    };
+    auto address = [&](const Tile& t, int mode, int col) -> const __nv_bfloat16* {
+      if (t.qi >= a.Q || my_row >= kPR || t.k0 + my_row >= t.keys || mode == kByBox) return nullptr;
+      const __nv_bfloat16* p = key_row(a, t.rec, t.qi, t.k0 + my_row, col);
 #pragma unroll
       for (int e = 0; e < 8; ++e) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 64 * e));
       return p;
     };
-    ahead = load_node(blockIdx.x);
+    ahead = a.nodes[min((int)blockIdx.x, a.Q - 1)];
     Tile cur, nxt;
+    Columns col{};
     start_query(cur, blockIdx.x);
+    columns(cur, col);
+    int mode = cur.qi < a.Q ? tile_mode(cur, col) : kByAddress;
+    const __nv_bfloat16* ptr = address(cur, mode, col.own);
+    int g0 = col.g[0], g1 = col.g[1], g2 = col.g[2], g3 = col.g[3];
     nxt = cur;
-    const __nv_bfloat16 *p0 = address(cur, r0, column(cur, r0)), *p1 = address(cur, r1, r1 < kPR ? column(cur, r1) : 0);
     advance(nxt);
-    int c0 = column(nxt, r0), c1 = r1 < kPR ? column(nxt, r1) : 0;
+    columns(nxt, col);
     uint32_t nq = 0, nt = 0;
     for (; cur.qi < a.Q && !failed; ++nt) {
       if (cur.k0 == 0) {
@@ -335,21 +360,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t par = (nt - 1) & 1;  // phase of the previous tile's releases
       const int pairs = (min(kPR, (cur.keys - cur.k0 + 15) & ~15)) >> 1;  // row pairs that the products read
-      const long long v0 = reinterpret_cast<long long>(p0), v1 = reinterpret_cast<long long>(p1);
-      const bool by_box = boxes(cur);
-      const int box_row = by_box ? (cur.qi / a.T) * a.cap + cur.k0 : 0;
+      const long long mine = reinterpret_cast<long long>(ptr);
+      const int how = mode, row0 = (cur.qi / a.T) * a.cap;
+      const int box_row = row0 + cur.k0, a0 = row0 + g0, a1 = row0 + g1, a2 = row0 + g2, a3 = row0 + g3;
       // the next tile's rows into L2, the columns of the one after it
       cur = nxt;
-      p0 = address(cur, r0, c0);
-      p1 = address(cur, r1, c1);
+      if (cur.qi < a.Q) mode = tile_mode(cur, col);
+      ptr = address(cur, mode, col.own);
+      g0 = col.g[0]; g1 = col.g[1]; g2 = col.g[2]; g3 = col.g[3];
       advance(nxt);
-      c0 = column(nxt, r0);
-      c1 = r1 < kPR ? column(nxt, r1) : 0;
+      columns(nxt, col);
 #pragma unroll 1
       for (int m = 0; m < 4; ++m) {
         if (nt > 0 && !failed && !tc::mbar_wait(box_free + m, par)) failed = true;
         if (__any_sync(0xffffffffu, failed)) { failed = true; break; }
-        if (by_box) {
+        if (how == kByBox) {
           if (lane == 0 && w == 0) {
             tc::mbar_arrive_expect_tx(rows_full + m, 2 * kBox);
             tc::tma_load_2d(rows + 2 * m * kBox, &tm_pool, rows_full + m, 128 * m, box_row);
@@ -359,19 +384,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           continue;
         }
+        if (how == kByGather) {
+          if (lane == 0) tc::mbar_arrive_expect_tx(rows_full + m, n_gather * 512);
+          __syncwarp();
+          if (j < 64)
+            tc::tma_gather4(rows + (2 * m + (j & 1)) * kBox + (j >> 1) * 512, &tm_row, rows_full + m,
+                            64 * (2 * m + (j & 1)), a0, a1, a2, a3);
+          continue;
+        }
+        const __nv_bfloat16* src[kInstr];
 #pragma unroll
-        for (int g = 0; g < 22; g += 11) {
-          const __nv_bfloat16* src[11];
+        for (int k = 0; k < kInstr; ++k)
+          src[k] = reinterpret_cast<const __nv_bfloat16*>(__shfl_sync(0xffffffffu, mine, k + (lane & 16)));
 #pragma unroll
-          for (int k = g; k < g + 11; ++k)
-            src[k - g] = reinterpret_cast<const __nv_bfloat16*>(
-                __shfl_sync(0xffffffffu, k < 16 ? v0 : v1, (k & 15) + (lane & 16)));
-#pragma unroll
-          for (int k = g; k < g + 11; ++k) {
-            const int i = w + 3 * k, r = 2 * i + (lane >> 4);
-            cp_async16_if(i < pairs, r_base + 2 * m * kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                          src[k - g] ? src[k - g] + 128 * m + 8 * c : a.pool, src[k - g] ? 16u : 0u);
-          }
+        for (int k = 0; k < kInstr; ++k) {
+          const int i = w + kLoadWarps * k, r = 2 * i + (lane >> 4);
+          cp_async16_if(i < pairs, r_base + 2 * m * kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                        src[k] ? src[k] + 128 * m + 8 * c : a.pool, src[k] ? 16u : 0u);
         }
         tc::cp_async_commit();
         if (m >= 1) {
@@ -382,15 +411,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (failed) break;
-      if (by_box) continue;
+      if (how != kByAddress) continue;
       tc::cp_async_wait_group<0>();
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(rows_full + 3);
     }
     tc::cp_async_wait_all();
-    // after a failed wait the query block in flight is given its time (its products wait for it otherwise)
-    if (failed && nq > 0 && w == 0 && lane == 0) tc::mbar_wait(q_full, (nq - 1) & 1);
+    // after a failed wait the bulk copies in flight are given their time (the products wait for them otherwise)
+    if (failed && lane == 0) {
+      if (nq > 0 && w == 0) tc::mbar_wait(q_full, (nq - 1) & 1);
+      for (int m = 0; m < 4; ++m) tc::mbar_wait(rows_full + m, nt & 1);
+    }
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------------------ softmax and epilogue
     const int quad = warp & 3, half = warp >> 2, hb = 32 * half, row = 32 * quad + lane;
@@ -625,13 +657,14 @@ cudaError_t launch_tc_attend_tree(const Dims& L, const TreeAttend& t, const int3
   a.Q = t.B * t.T; a.T = t.T; a.cap = t.cap; a.topk = L.topk; a.W = L.W; a.Wr = L.Wr;
   a.scale2 = L.scale * 1.4426950408889634f;
   a.err = err;
-  CUtensorMap tq, to, tp;
+  CUtensorMap tq, to, tp, tr;
   if (!make_tmap_2d_bf16(&tq, t.q, (uint64_t)a.Q * kAH, kAD, kAD * 2, 64) ||
       !make_tmap_2d_bf16(&to, t.out, (uint64_t)a.Q * kAH, kAD, kAD * 2, 32) ||
-      !make_tmap_2d_bf16(&tp, t.pool, (uint64_t)t.B * t.cap, kAD, kAD * 2, kPR))
+      !make_tmap_2d_bf16(&tp, t.pool, (uint64_t)t.B * t.cap, kAD, kAD * 2, kPR) ||
+      !make_tmap_2d_bf16(&tr, t.pool, (uint64_t)t.B * t.cap, kAD, kAD * 2, 1))
     return cudaErrorInvalidValue;
   cudaFuncSetAttribute(k_tc_tree_attend, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  CSA_LAUNCH(k_tc_tree_attend, dim3(min(a.Q, sms)), dim3(kThreads), kSmem, s, tq, to, tp, a);
+  CSA_LAUNCH(k_tc_tree_attend, dim3(min(a.Q, sms)), dim3(kThreads), kSmem, s, tq, to, tp, tr, a);
   return cudaGetLastError();
 }
 
