@@ -436,9 +436,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* stage = pbuf + half * kPPart;  // the epilogue's: two buffers of 32 heads x 128 dims
     uint8_t* pdst = pbuf + (row >> 3) * 1024 + (row & 7) * 128;
     uint32_t nq = 0, nt = 0;
+    int p_next = a.nodes[blockIdx.x].p, nsel_next = a.nodes[blockIdx.x].nsel;  // (the grid has at most Q blocks)
     for (int qi = blockIdx.x; qi < a.Q && !failed; qi += gridDim.x) {
-      const TreeNode rec = a.nodes[qi];
-      const int keys = node_keys(a, rec);
+      const int p = p_next, keys = nsel_next < 0 ? 0 : nsel_next + min(a.W, p + 1);
+      // the next record is on its way while this node is worked on
+      const TreeNode* next = a.nodes + min(qi + (int)gridDim.x, a.Q - 1);
+      p_next = next->p;
+      nsel_next = next->nsel;
       if (keys == 0) continue;
       // the previous query's stores have read the P buffer, its 1 / Z has been used
       if (quad == 0 && lane == 0) bulk_wait_read<0>();
@@ -477,12 +481,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float2 p = make_float2(ex2(x[4 * j + k].x), ex2(x[4 * j + k].y));
-              x[4 * j + k] = p;
-              const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
+              const float2 e = make_float2(ex2(x[4 * j + k].x), ex2(x[4 * j + k].y));
+              x[4 * j + k] = e;
+              const __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
               hi[k] = *reinterpret_cast<const uint32_t*>(&h);
-              const __nv_bfloat162 d = __floats2bfloat162_rn(p.x - __uint_as_float(hi[k] << 16),
-                                                             p.y - __uint_as_float(hi[k] & 0xffff0000u));
+              const __nv_bfloat162 d = __floats2bfloat162_rn(e.x - __uint_as_float(hi[k] << 16),
+                                                             e.y - __uint_as_float(hi[k] & 0xffff0000u));
               lo[k] = *reinterpret_cast<const uint32_t*>(&d);
             }
             const int off = ((4 * half + j) ^ (row & 7)) << 4;
@@ -569,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // inverse RoPE of this thread's dim of tile 3 (dims 448-511 are lane quarters 2 and 3)
       float rc = 1.f, rs = 0.f;
-      if (quad >= 2) rope_cs(rec.p, a.inv_freq, (32 * quad + lane - 64) >> 1, &rc, &rs);
+      if (quad >= 2) rope_cs(p, a.inv_freq, (32 * quad + lane - 64) >> 1, &rc, &rs);
       if (!failed && !tc::mbar_wait(pv_done, (nt - 1) & 1)) failed = true;
       // both halves: P is no longer read, the buffers may take outputs
       if (tc::named_bar_any(kBarAll, kSoft, failed)) {
