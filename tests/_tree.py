@@ -78,11 +78,17 @@ def select(layer, scores, path, p0, T):
     return cols[sorted(order[:layer.topk])]
 
 
-def output(layer, q, kv, sink, window, pool, rows_a, cols, path, p0, inv_freq):
-    """A node's attention output in float64 (rotated q)."""
+def keys(layer, q, kv, sink, window, pool, rows_a, cols, path, p0, inv_freq):
+    """The rows that a node attends to, in float64 [keys, D] (arguments as output's)."""
     n = p0 // layer.ratio
     p = p0 + len(path) - 1
     Wr = window.shape[0]
-    keys = [f64(pool[c]) if c < n else f64(rows_a[c - n]) for c in cols]
-    keys += [f64(window[t % Wr]) if t < p0 else f64(kv[path[t - p0]]) for t in O.window_tokens(layer, p)]
-    return O.rope(O.attend(layer, f64(q), np.stack(keys), sink), p, inv_freq, inverse=True)
+    rows = [f64(pool[c]) if c < n else f64(rows_a[c - n]) for c in cols]
+    rows += [f64(window[t % Wr]) if t < p0 else f64(kv[path[t - p0]]) for t in O.window_tokens(layer, p)]
+    return np.stack(rows)
+
+
+def output(layer, q, kv, sink, window, pool, rows_a, cols, path, p0, inv_freq):
+    """A node's attention output in float64 (rotated q)."""
+    k = keys(layer, q, kv, sink, window, pool, rows_a, cols, path, p0, inv_freq)
+    return O.rope(O.attend(layer, f64(q), k, sink), p0 + len(path) - 1, inv_freq, inverse=True)

@@ -373,6 +373,98 @@ def check_tree_outputs(cfg, layer, trees, pos, q, kv, sink, window, pool, rows, 
         assert not bad.any(), (b, i, np.argwhere(bad)[:3], np.abs(g - ref).max())
 
 
+EDGE_CASES = {
+    # layer, trees, positions, selection: split kernel (few nodes), many nodes, portable kernel
+    "flash_few": ("flash", [TR.bushy(5), TR.chain(7)], [4097, 2301], True),
+    "flash_many": ("flash", [TR.bushy(16, s) for s in range(11)], [2100 + 91 * s for s in range(11)], True),
+    "flash_many_rows": ("flash_r128", [TR.bushy(16, s) for s in range(11)], [9000 + 1291 * s for s in range(11)], False),
+    "flash_topk_odd": ("flash_topk", [TR.bushy(15, s) for s in range(12)], [900 + 77 * s for s in range(12)], True),
+    "flash_topk_odd_few": ("flash_topk", [TR.bushy(6)], [1403], True),
+    "flash_topk_1": ("flash_topk1", [TR.bushy(15, s) for s in range(12)], [77 * s for s in range(12)], True),
+    "flash_window": ("flash_window", [TR.bushy(9, s) for s in range(18)], [801 + 13 * s for s in range(18)], True),
+    "tiny_f32": ("tiny_f32", [TR.bushy(9), TR.chain(9)], [150, 70], True),
+}
+EDGE_LAYERS = {**LAYERS, "flash_topk": FLASH.replace(cid=65, topk=203), "flash_topk1": FLASH.replace(cid=66, topk=1),
+               "flash_window": FLASH.replace(cid=67, W=77, topk=131, rollback=19)}
+
+
+@pytest.mark.parametrize("case", list(EDGE_CASES))
+@pytest.mark.parametrize("loud", [1.0, 24.0])
+def test_attend_tree_sinks_and_large_logits(case, loud):
+    """Sinks from -infinity to far above every logit, and logits that grow along the keys, so that a head's largest one
+    is found late and far above both the sink and everything before it.
+
+    A logit is 512 products summed in fp32, by a pipe that may truncate: 32 steps of 16 products, each off by up to
+    2^-23 of the sum of absolute products A; the scale and the reference that is taken from it round three times more,
+    2^-22 of |logit| and of the reference.  With e the largest such error over a node's keys (in natural units), the
+    probabilities err by 2 e + 2^-14 relative (2^-16 for two bf16 parts, the exponential and the sums), the average by
+    that times the largest |key value|."""
+    name, trees, pos, select = EDGE_CASES[case]
+    cfg = EDGE_LAYERS[name]
+    B, T, cap = len(trees), max(len(t) for t in trees), max(pos) // cfg.ratio + 2
+    layer, invf = oracle_layer(cfg), f64(csa_synth.inv_freq(cfg)).astype(np.float32)
+    sink = rnd(cfg, (cfg.H,), 141, dtype=torch.float32)
+    for h, v in enumerate((float("-inf"), -3e38, -1e4, -200.0, 0.0, 150.0, 1e4)):
+        sink[h % cfg.H::cfg.H // 4] = v
+    q, kv = rnd(cfg, (B, T, cfg.H, cfg.D), 142, scale=loud), rnd(cfg, (B, T, cfg.D), 143)
+    ramp = torch.linspace(0.05, 2.0, cap, device="cuda")[None, :, None]
+    window = rnd(cfg, (B, cfg.ring_slots, cfg.D), 144)
+    pool = (rnd(cfg, (B, cap, cfg.D), 145).float() * ramp).to(cfg.storage)
+    rows = rnd(cfg, (B, T, cfg.D), 146)
+    scores = make_scores(cfg, B, T, cap, "normal" if select else None)
+    p = torch.tensor(pos, dtype=torch.int32, device="cuda")
+    out = torch.full((B, T, cfg.H, cfg.D), SENTINEL, dtype=cfg.storage, device="cuda")
+    again = out.clone()
+    for o in (out, again):
+        err = csa.attend_tree(G.lib_layer(cfg), q, kv, sink, window, pool, rows, scores, parents(trees, T),
+                              p // cfg.ratio, p, freqs(cfg), o)
+        assert err.item() == 0
+    assert torch.equal(out, again)
+    scale = cfg.D ** -0.5
+    for b in range(0, B, max(1, B // 4)):
+        for i in (0, T // 2, T - 1):
+            path = TR.paths(TR.padded(trees[b], T))[i]
+            if path is None:
+                continue
+            cols = TR.select(layer, None if scores is None else f64(scores[b, i]), path, pos[b], T)
+            args = (layer, q[b, i], kv[b], f64(sink), window[b], pool[b], rows[b], cols, path, pos[b], invf)
+            ref, keys = TR.output(*args), TR.keys(*args)
+            dot, absdot = f64(q[b, i]) @ keys.T * scale, np.abs(f64(q[b, i])) @ np.abs(keys).T * scale
+            e = 32 * 2.0 ** -23 * absdot.max(-1) + 2.0 ** -22 * (np.abs(dot).max(-1) + 100)
+            tol = ((2 * e + 2.0 ** -14) * 2 * np.abs(keys).max())[:, None]
+            g = f64(out[b, i])
+            bad = np.abs(g - ref) > half_step(np.abs(ref) + tol, cfg.dtype) + tol
+            assert np.isfinite(g).all() and not bad.any(), (b, i, np.argwhere(bad)[:3], np.abs(g - ref).max())
+
+
+def test_attend_tree_with_unused_sequences_and_long_pools():
+    """A batch whose sequences are all padding but two, one of which sees far more rows than a block's shared memory
+    holds scores for; the padding's outputs stay as they were."""
+    cfg = FLASH
+    for B, T, long in ((3, 4, 60000), (12, 14, 20000)):
+        trees = [[TR.NONE] * T for _ in range(B)]
+        trees[0], trees[B - 1] = TR.bushy(T), TR.chain(T)
+        pos = [0] * B
+        pos[0], pos[B - 1] = 4 * long + 2, 30
+        cap = long + 1
+        layer, invf = oracle_layer(cfg), f64(csa_synth.inv_freq(cfg)).astype(np.float32)
+        g = torch.Generator(device="cuda").manual_seed(5)
+        q = torch.randn(B, T, 64, 512, device="cuda", generator=g).bfloat16()
+        kv = torch.randn(B, T, 512, device="cuda", generator=g).bfloat16()
+        window = torch.randn(B, 128, 512, device="cuda", generator=g).bfloat16()
+        pool = torch.randn(1, cap, 512, device="cuda", generator=g).bfloat16().expand(B, cap, 512).contiguous()
+        rows = torch.randn(B, T, 512, device="cuda", generator=g).bfloat16()
+        scores = torch.randn(B, T, cap + T, device="cuda", generator=g)
+        sink = rnd(cfg, (64,), 150, dtype=torch.float32)
+        p = torch.tensor(pos, dtype=torch.int32, device="cuda")
+        out = torch.full((B, T, 64, 512), SENTINEL, dtype=torch.bfloat16, device="cuda")
+        sel = torch.full((B, T, 512), -9, dtype=torch.int32, device="cuda")
+        err = csa.attend_tree(G.lib_layer(cfg), q, kv, sink, window, pool, rows, scores, parents(trees, T), p // 4, p,
+                              freqs(cfg), out, sel_out=sel)
+        assert err.item() == 0
+        check_tree_outputs(cfg, layer, trees, pos, q, kv, sink, window, pool, rows, scores, out, sel, invf)
+
+
 def test_attend_tree_of_a_chain_is_a_verify_block():
     """A tree without branches against csa_attend_verify on the same tokens and selections."""
     B, T = 3, 4
