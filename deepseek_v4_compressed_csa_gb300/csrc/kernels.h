@@ -80,6 +80,29 @@ inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// Clusters of S blocks that the current device runs at once.  A cluster stays within one GPC, so that is less than
+// SMs / S blocks (of one block an SM, 23 clusters of 6 and 15 of 7 on 152 SMs): a grid of more has a second wave.
+template <typename... KArgs>
+inline int max_clusters(void (*kernel)(KArgs...), int threads, size_t smem, int S) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(S);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();  // leave no sticky error behind
+    return 0;
+  }
+  return n;
+}
+
 #define CSA_LAUNCH(...)                           \
   do {                                            \
     cudaError_t csa_e_ = launch_pdl(__VA_ARGS__); \
@@ -323,6 +346,8 @@ cudaError_t launch_attend_tree(const Dims& L, const TreeAttend& t, int32_t* err,
 // streaming its tiles (tc_tree_attend.cu), or S <= 4 splits per query merged in a cluster (tc_attend_decode.cu).
 cudaError_t launch_tc_attend_tree(const Dims& L, const TreeAttend& t, const int32_t* sel, int32_t* err,
                                   cudaStream_t s);
+// queries that launch_tc_attend_tree_split works on at once with S splits each
+int tc_attend_tree_split_max(int S);
 cudaError_t launch_tc_attend_tree_split(const Dims& L, const TreeAttend& t, const int32_t* sel, int S, int32_t* err,
                                         cudaStream_t s);
 // Pool 0: the attention pool; pool 1 (npool == 2): the index pool.

@@ -31,6 +31,8 @@
 // With one split the epilogue finalises the output (sink, normalisation, bf16,
 // inverse RoPE, bf16); with several it writes (m, l, acc) partials for the merge
 // kernel.  Splits are never longer than 160 rows (the caller picks enough).
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
@@ -177,8 +179,8 @@ __device__ __forceinline__ bool item_selection(const DecArgs& a, Item& it) {
     it.nsel = r.nsel;
     it.closers = r.closers;
   } else {
-  it.nrows = min(a.n_rows[it.b], a.cap);
-  it.nsel = a.sel ? min(max(a.n_sel[it.q], 0), a.topk) : max(0, min(it.nrows, (it.p + 1) / a.ratio));
+    it.nrows = min(a.n_rows[it.b], a.cap);
+    it.nsel = a.sel ? min(max(a.n_sel[it.q], 0), a.topk) : max(0, min(it.nrows, (it.p + 1) / a.ratio));
   }
   const int sper = (it.nsel + a.S - 1) / a.S;
   it.s_begin = min(it.nsel, it.s * sper);
@@ -768,6 +770,20 @@ cudaError_t launch_tc_attend_decode(const Dims& L, const void* q, const void* po
 }
 
 // A tree's nodes (csa_attend_tree): B * T queries of S splits each (S 1, or 2 or 4 as a cluster).
+int tc_attend_tree_split_max(int S) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][5];  // 0: not asked yet (a property of the device: asked once), else 1 + n
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
+  int n = known[dev][S].load(std::memory_order_relaxed) - 1;
+  if (n < 0) {
+    cudaFuncSetAttribute(k_tc_attend_decode<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    n = max_clusters(k_tc_attend_decode<true>, kThreads, kSmem, S);
+    known[dev][S].store(n + 1, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 cudaError_t launch_tc_attend_tree_split(const Dims& L, const TreeAttend& t, const int32_t* sel, int S, int32_t* err,
                                         cudaStream_t s) {
   const int Q = t.B * t.T;

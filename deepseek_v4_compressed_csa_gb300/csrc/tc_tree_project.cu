@@ -7,8 +7,12 @@
 // Flash pools), so the hidden axis is split over the S CTAs of a cluster.  They add their parts through distributed
 // shared memory: each CTA leaves its fp32 part in its own shared memory (the stage buffers, free by then), and CTA r
 // sums the S parts, in split order, of N / S tokens and writes them.  No partial sum goes to memory and no second
-// pass reads one.  Both pools are one grid.  Bound by the weights' stream (21 MB for both Flash pools) up to about a
-// hundred tokens, by the tensor pipe beyond.
+// pass reads one.  Both pools are one grid.  Bound by the weights' stream (21 MB for both Flash pools) for few tokens
+// (8 tokens: 11.8 us with the pooling after it, six splits; 13.4 with four, 18.3 with seven, whose clusters do not all
+// run at once), by the tiles' way into shared memory for many (512 tokens: 27 us with it; 48 KB of weights and tokens
+// for every 512 clocks of products).
+#include <atomic>
+
 #include "kernels.h"
 #include "tc.cuh"
 #include "tree.cuh"
@@ -20,6 +24,7 @@ namespace {
 constexpr int kThreads = 192;       // warp 0 TMA, warp 1 MMA and TMEM, warps 2-5 accumulators out; all add
 constexpr int kABytes = 128 * 128;  // 128 features x 64 values
 constexpr int kMaxStages = 8, kMaxSplit = 8;
+constexpr int kMaxSmem = 1024 + 200 * 1024;
 
 struct TpArgs {
   __nv_bfloat16* proj[2];
@@ -177,8 +182,23 @@ struct Plan {
   int N, n_tiles, S, stages, smem;
 };
 
+// Clusters of S CTAs, one CTA an SM, that run at once (a property of the device: asked once for each).
+int clusters(int S) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][kMaxSplit + 1];  // 0: not asked yet, else 1 + n
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
+  int n = known[dev][S].load(std::memory_order_relaxed) - 1;
+  if (n < 0) {
+    cudaFuncSetAttribute(k_tc_tree_project, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    n = max_clusters(k_tc_tree_project, kThreads, kMaxSmem, S);
+    known[dev][S].store(n + 1, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 // Tokens per tile and splits: the pair whose slowest CTA needs the fewest tensor clocks (an MMA of 128 x N x 16 takes
-// max(32 + N / 4, N / 2) of them: up to N = 128 it waits for shared memory), with every CTA on an SM of its own; a
+// max(32 + N / 4, N / 2) of them: up to N = 128 it waits for shared memory), with all clusters running at once; a
 // tile costs about 6000 clocks beside its products (launch, first fill, the parts' exchange).
 Plan plan(int m_tiles, int ntok, int kblk, int sms) {
   Plan best{};
@@ -186,9 +206,9 @@ Plan plan(int m_tiles, int ntok, int kblk, int sms) {
   for (int N = 32; N <= 256; N += 32) {
     const int n_tiles = (ntok + N - 1) / N;
     for (int S = 1; S <= kMaxSplit && S <= kblk; ++S) {
-      const long ctas = (long)m_tiles * n_tiles * S;
-      const long waves = (ctas + sms - 1) / sms;
-      if (S > 1 && waves > 1) continue;
+      const long tiles = (long)m_tiles * n_tiles;
+      if (S > 1 && tiles > clusters(S)) continue;
+      const long waves = S > 1 ? 1 : (tiles + sms - 1) / sms;
       const long mma = max(32 + N / 4, N / 2);
       const long cost = waves * (6000 + (long)((kblk + S - 1) / S) * 4 * mma);
       if (best_cost < 0 || cost < best_cost || (cost == best_cost && S < best.S)) {

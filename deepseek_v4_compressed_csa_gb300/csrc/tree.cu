@@ -726,12 +726,9 @@ static cudaError_t attend_tree_t(const Dims& L, const TreeAttend& t, int32_t* er
   // SM.  More: a CTA per query streaming its tiles.
   const bool codes_fit = (long long)t.B * t.cap < INT32_MAX && (long long)t.B * L.Wr < (1 << 28);
   if (tc_attend_supported(L) && codes_fit) {
-    int sms = 0, dev = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int n_max = t.scores ? L.topk : t.cap + t.T;
     for (int S = 1; S <= 4; S *= 2)
-      if ((L.W + S - 1) / S + (n_max + S - 1) / S <= 160 && (long)Q * S <= sms && (S == 1 || tc_attend_decode_cluster(S)))
+      if ((L.W + S - 1) / S + (n_max + S - 1) / S <= 160 && Q <= tc_attend_tree_split_max(S))
         return launch_tc_attend_tree_split(L, t, a.sel, S, err, s);
     return launch_tc_attend_tree(L, t, a.sel, err, s);
   }
