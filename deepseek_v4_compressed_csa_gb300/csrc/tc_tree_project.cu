@@ -8,9 +8,8 @@
 // shared memory: each CTA leaves its fp32 part in its own shared memory (the stage buffers, free by then), and CTA r
 // sums the S parts, in split order, of N / S tokens and writes them.  No partial sum goes to memory and no second
 // pass reads one.  Both pools are one grid.  Bound by the weights' stream (21 MB for both Flash pools) for few tokens
-// (8 tokens: 11.8 us with the pooling after it, six splits; 13.4 with four, 18.3 with seven, whose clusters do not all
-// run at once), by the tiles' way into shared memory for many (512 tokens: 27 us with it; 48 KB of weights and tokens
-// for every 512 clocks of products).
+// (8 tokens: 8.0 us, six splits; four take 1.6 us longer, seven 6.5, since their clusters do not all run at once), by the
+// tiles' way into shared memory for many (512 tokens: 17 us; 48 KB of weights and tokens for 512 clocks of products).
 #include <atomic>
 
 #include "kernels.h"
@@ -21,7 +20,7 @@ namespace csa {
 
 namespace {
 
-constexpr int kThreads = 192;       // warp 0 TMA, warp 1 MMA and TMEM, warps 2-5 accumulators out; all add
+constexpr int kThreads = 320;       // warp 0 TMA, warp 1 MMA and TMEM, warps 2-9 accumulators out; all add
 constexpr int kABytes = 128 * 128;  // 128 features x 64 values
 constexpr int kMaxStages = 8, kMaxSplit = 8;
 constexpr int kMaxSmem = 1024 + 200 * 1024;
@@ -34,6 +33,44 @@ struct TpArgs {
   const int32_t* pos;
   int32_t* err;
 };
+
+// Tokens [c0, c1) of the tile: S parts added in split order, one warp per token, four features a lane.  Twelve to
+// sixteen remote loads in flight a lane: one token at a time costs the latency of its parts each time (5 us for 512
+// tokens).
+template <int S>
+__device__ __forceinline__ void add_parts(const float* part, int c0, int c1, const uint8_t* live, __nv_bfloat16* out,
+                                          int stride) {
+  constexpr int kWarps = kThreads / 32, U = S > 4 ? 2 : 12 / S;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int c = c0 + warp; c < c1; c += U * kWarps) {
+    float4 v[U][S];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const float* at = part + min(c + k * kWarps, c1 - 1) * 128 + 4 * lane;
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        v[k][s] = S > 1 ? tc::ld_cluster_f4(tc::cluster_map(at, s)) : *reinterpret_cast<const float4*>(at);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      float4 t = v[k][0];
+#pragma unroll
+      for (int s = 1; s < S; ++s) {
+        t.x += v[k][s].x;
+        t.y += v[k][s].y;
+        t.z += v[k][s].z;
+        t.w += v[k][s].w;
+      }
+      const int at = c + k * kWarps;
+      if (at >= c1 || !live[at]) continue;
+      uint2 pk;
+      __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&pk);
+      h[0] = __floats2bfloat162_rn(t.x, t.y);
+      h[1] = __floats2bfloat162_rn(t.z, t.w);
+      *reinterpret_cast<uint2*>(out + (size_t)at * stride) = pk;
+    }
+  }
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
     k_tc_tree_project(const __grid_constant__ CUtensorMap tm_wkv0, const __grid_constant__ CUtensorMap tm_wg0,
@@ -134,9 +171,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!tc::mbar_wait(&acc_full, 0)) failed = true;
   tc::fence_after_sync();
   float* part = reinterpret_cast<float*>(smem);  // [N][128]
+  const int nt = min(N, a.ntok - n * N);         // the tile's tokens
   if (warp >= 2) {
     const int quarter = warp & 3;
-    for (int c0 = 0; c0 < N; c0 += 32) {
+    for (int c0 = warp < 6 ? 0 : 32; c0 < nt; c0 += 64) {
       uint32_t u[32];
       tc::tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + c0, u);
       tc::tmem_wait_ld();
@@ -147,30 +185,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before_sync();
   if (a.S > 1) tc::cluster_sync();
   else __syncthreads();
-  // this CTA's tokens of the tile: S parts added in split order, one warp per token, four features a lane
-  const int c1 = N * (split + 1) / a.S;
-  for (int c = N * split / a.S + warp; c < c1; c += kThreads / 32) {
-    float4 v[kMaxSplit];
-#pragma unroll
-    for (int s = 0; s < kMaxSplit; ++s)
-      if (s < a.S)
-        v[s] = a.S > 1 ? tc::ld_cluster_f4(tc::cluster_map(part + c * 128 + 4 * lane, s))
-                       : *reinterpret_cast<const float4*>(part + c * 128 + 4 * lane);
-    float4 t = v[0];
-#pragma unroll
-    for (int s = 1; s < kMaxSplit; ++s)
-      if (s < a.S) {
-        t.x += v[s].x;
-        t.y += v[s].y;
-        t.z += v[s].z;
-        t.w += v[s].w;
-      }
-    if (!live[c]) continue;
-    uint2 pk;
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&pk);
-    h[0] = __floats2bfloat162_rn(t.x, t.y);
-    h[1] = __floats2bfloat162_rn(t.z, t.w);
-    *reinterpret_cast<uint2*>(a.proj[pool] + (size_t)(n * N + c) * 2 * Ld + m * 128 + 4 * lane) = pk;
+  // this CTA's tokens of the tile
+  const int c0 = nt * split / a.S, c1 = nt * (split + 1) / a.S;
+  __nv_bfloat16* out = a.proj[pool] + (size_t)n * N * 2 * Ld + m * 128 + 4 * lane;
+  switch (a.S) {
+    case 1: add_parts<1>(part, c0, c1, live, out, 2 * Ld); break;
+    case 2: add_parts<2>(part, c0, c1, live, out, 2 * Ld); break;
+    case 3: add_parts<3>(part, c0, c1, live, out, 2 * Ld); break;
+    case 4: add_parts<4>(part, c0, c1, live, out, 2 * Ld); break;
+    case 5: add_parts<5>(part, c0, c1, live, out, 2 * Ld); break;
+    case 6: add_parts<6>(part, c0, c1, live, out, 2 * Ld); break;
+    case 7: add_parts<7>(part, c0, c1, live, out, 2 * Ld); break;
+    default: add_parts<8>(part, c0, c1, live, out, 2 * Ld); break;
   }
   if (failed) atomicOr(a.err, tc::kErrTimeout);
   if (a.S > 1) tc::cluster_sync();  // the parts stay in place until the others have read them

@@ -239,11 +239,13 @@ __device__ __forceinline__ void store2(__nv_bfloat16* p, float x, float y) {
 }
 __device__ __forceinline__ void store2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
 
-// Block (i, b, pool): node i of sequence b.  If its token completes window j along its path, the row that the
-// compressor would emit: entries before pos from the frontier ring, from pos on the path's nodes.  Arithmetic and
-// roundings are those of the committed rows (compress.cu: the pooled value, its norm and its rotation each in the
-// model dtype), so that an accepted row is the row decoding would have written.  A thread takes two neighbouring
-// channels, and eight entries' loads are in flight together.  Latency-bound: three of four nodes complete nothing.
+// Block (g, b, pool): the g-th node of sequence b that completes a window along its path: the row that the compressor
+// would emit, entries before pos from the frontier ring, from pos on the path's nodes.  Arithmetic and roundings are
+// those of the committed rows (compress.cu: the pooled value, its norm and its rotation each in the model dtype), so
+// that an accepted row is the row decoding would have written.  A thread takes two neighbouring channels, and eight
+// entries' loads are in flight together.  Latency-bound: what depends on the tree alone (the path, the rows' addresses,
+// weights, angles) stands before the programmatic wait, behind the projections; what is left adds 3 us to 8 nodes'
+// projections, 7 us to those of 512.
 template <typename T>
 __global__ void __launch_bounds__(256) k_tree_pool(const __grid_constant__ TreePool<T> pa,
                                                    const __grid_constant__ TreePool<T> pi, int T_, int ratio, int lanes,
@@ -252,41 +254,71 @@ __global__ void __launch_bounds__(256) k_tree_pool(const __grid_constant__ TreeP
                                                    const float* __restrict__ inv_freq, int32_t* err) {
   pdl_trigger();
   extern __shared__ __align__(16) float sm_tp[];  // [d] pooled, then normed; 32 reduction slots
-  __shared__ uint64_t s_mask;
-  __shared__ int s_path[kTreeMax];
+  __shared__ uint64_t s_masks[kTreeMax];
+  __shared__ int s_par[kTreeMax], s_path[kTreeMax], s_list[kTreeMax], s_count[2];
   const TreePool<T>& tp = blockIdx.z ? pi : pa;
   const int d = tp.d, Ld = lanes * d, rowlen = 2 * Ld;
   float* u = sm_tp;
   float* red = u + d;
-  const int i = blockIdx.x, b = blockIdx.y, p0 = pos[b];
-  if (threadIdx.x < 32) {
-    bool bad = false;
-    const uint64_t m = tree_path_warp(parent + (size_t)b * T_, T_, i, bad);
-    if (threadIdx.x == 0) {
-      s_mask = p0 < 0 ? 0 : m;
-      if (bad || (p0 < 0 && m)) atomicOr(err, CSA_DEV_STATE);
-      int k = 0;
-      for (uint64_t r = m; r; r &= r - 1) s_path[k++] = __ffsll((long long)r) - 1;
-    }
+  const int b = blockIdx.y, p0 = pos[b], tid = threadIdx.x;
+  const bool consistent = tree_masks_block(parent + (size_t)b * T_, T_, s_masks, s_par);
+  if (tid < kTreeMax) {  // the completing nodes in order (two warps)
+    const uint64_t m = s_masks[tid];
+    const bool closes = p0 >= 0 && m != 0 && (p0 + __popcll(m)) % ratio == 0;
+    const unsigned mine = __ballot_sync(0xffffffffu, closes);
+    if ((tid & 31) == 0) s_count[tid >> 5] = __popc(mine);
+    if (blockIdx.x == 0 && ((tid == 0 && !consistent) || (p0 < 0 && m != 0))) atomicOr(err, CSA_DEV_STATE);
+    s_par[tid] = closes ? __popc(mine & ((1u << (tid & 31)) - 1u)) : -1;
   }
   __syncthreads();
-  if (s_mask == 0) return;
-  const int p = p0 + __popcll(s_mask) - 1;
-  const bool closes = (p + 1) % ratio == 0;
+  if (tid < kTreeMax && s_par[tid] >= 0) s_list[s_par[tid] + (tid < 32 ? 0 : s_count[0])] = tid;
+  const bool works = p0 >= 0 && (int)blockIdx.x < s_count[0] + s_count[1], copies = p0 >= 0 && tp.src != tp.proj;
+  // One block waits in any case: a grid that ended before the projections would let the next call's wait pass early.
+  if (!works && !copies && blockIdx.x + blockIdx.y + blockIdx.z > 0) return;
   const T* src = tp.src + (size_t)b * T_ * rowlen;
-  if (!closes && tp.src == tp.proj) return;
-  pdl_wait();
-  if (tp.src != tp.proj)
-    for (int e = threadIdx.x * 8; e < rowlen; e += blockDim.x * 8)
-      copy8<T>(tp.proj + ((size_t)b * T_ + i) * rowlen + e, src + (size_t)i * rowlen + e);
-  if (!closes) return;
-  const int j = (p + 1) / ratio - 1;
   const T* fr = tp.frontier + (size_t)b * F * rowlen;
+  if (copies) {
+    pdl_wait();  // (the projections of every slot lie in the workspace)
+    if (s_masks[blockIdx.x] != 0)
+      for (int e = tid * 8; e < rowlen; e += blockDim.x * 8)
+        copy8<T>(tp.proj + ((size_t)b * T_ + blockIdx.x) * rowlen + e, src + (size_t)blockIdx.x * rowlen + e);
+  }
+  if (!works) {
+    pdl_wait();
+    return;
+  }
+  __syncthreads();
+  const int i = s_list[blockIdx.x];
+  const uint64_t mask = s_masks[i];
+  if (tid < kTreeMax && ((mask >> tid) & 1)) s_path[__popcll(mask & ((1ull << tid) - 1))] = tid;
+  __syncthreads();
+  const int p = p0 + __popcll(mask) - 1;
+  const int j = (p + 1) / ratio - 1;
   const int t_lo = lanes == 2 ? max(0, (j - 1) * ratio) : j * ratio;
   const int t_hi = (j + 1) * ratio;
+  const int c0 = 2 * tid;
+  float2 w0 = make_float2(0.f, 0.f);
+  float cs0 = 1.f, sn0 = 0.f;
+  if (c0 < d) {
+    w0 = load2(tp.norm_w + c0);
+    if (c0 >= d - R) rope_cs(j * ratio, inv_freq, (c0 - (d - R)) >> 1, &cs0, &sn0);
+  }
+  // committed entries and the position table on their way into L2 (a line a request)
+  for (int e = tid; e < (t_hi - t_lo) * 2; e += blockDim.x) {
+    const int t = t_lo + (e >> 1), at = ((lanes == 2 && t >= j * ratio) ? d : 0) + (e & 1) * Ld;
+    if (t < p0)
+      for (int k = 0; k < d; k += 128 / (int)sizeof(T))
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(fr + (size_t)(t % F) * rowlen + at + k));
+    if ((e & 1) == 0)
+      for (int k = 0; k < d; k += 32)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(tp.ape + (size_t)(t % ratio) * Ld + at + k));
+  }
+  pdl_wait();
   float ss = 0.f;
   for (int c = 2 * threadIdx.x; c < d; c += 2 * blockDim.x) {
     float2 m = make_float2(-INFINITY, -INFINITY), num = make_float2(0.f, 0.f), den = make_float2(0.f, 0.f);
+    // (a remainder per entry would be most of the loop's instructions: the ring slot and the phase run along)
+    int slot = t_lo % F, phase = 0, at = (lanes == 2 && t_lo >= j * ratio ? d : 0) + c;
     for (int t0 = t_lo; t0 < t_hi; t0 += 8) {
       float2 sv[8], kv[8];
 #pragma unroll
@@ -295,11 +327,15 @@ __global__ void __launch_bounds__(256) k_tree_pool(const __grid_constant__ TreeP
         sv[k] = make_float2(-INFINITY, -INFINITY);
         kv[k] = make_float2(0.f, 0.f);
         if (t < t_hi) {
-          const int at = ((lanes == 2 && t >= j * ratio) ? d : 0) + c;
-          const T* row = t < p0 ? fr + (size_t)(t % F) * rowlen : src + (size_t)s_path[t - p0] * rowlen;
-          kv[k] = load2(row + at);
-          const float2 g = load2(row + Ld + at), w = load2(tp.ape + (size_t)(t % ratio) * Ld + at);
+          const T* row = (t < p0 ? fr + (size_t)slot * rowlen : src + (size_t)s_path[t - p0] * rowlen) + at;
+          kv[k] = load2(row);
+          const float2 g = load2(row + Ld), w = load2(tp.ape + phase * Ld + at);
           sv[k] = make_float2(g.x + w.x, g.y + w.y);
+          if (++slot == F) slot = 0;
+          if (++phase == ratio) {
+            phase = 0;
+            if (lanes == 2) at += d;
+          }
         }
       }
       float2 cm = m;
@@ -326,11 +362,11 @@ __global__ void __launch_bounds__(256) k_tree_pool(const __grid_constant__ TreeP
   const float inv = 1.0f / sqrtf(ss / (float)d + eps);
   T* dst = tp.rows + ((size_t)b * T_ + i) * d;
   for (int c = 2 * threadIdx.x; c < d; c += 2 * blockDim.x) {  // (the thread's own channels, a rotated pair whole)
-    const float2 w = load2(tp.norm_w + c);
+    const float2 w = c == c0 ? w0 : load2(tp.norm_w + c);
     float x = rnd<T>(u[c] * inv * w.x), y = rnd<T>(u[c + 1] * inv * w.y);
     if (c >= d - R) {
-      float cs, sn;
-      rope_cs(j * ratio, inv_freq, (c - (d - R)) >> 1, &cs, &sn);
+      float cs = cs0, sn = sn0;
+      if (c != c0) rope_cs(j * ratio, inv_freq, (c - (d - R)) >> 1, &cs, &sn);
       const float x0 = x, y0 = y;
       x = fmaf(x0, cs, -y0 * sn);
       y = fmaf(x0, sn, y0 * cs);

@@ -793,6 +793,33 @@ def test_graph_replay_other_stream_and_two_graphs():
     assert torch.equal(ds[0]["out"], got) and errs[0].item() == 0 and errs[1].item() == 0
 
 
+def test_commit_right_after_projections_that_complete_nothing():
+    """No node completes a window, so that only the projections take long: a commit enqueued right behind them takes
+    what they wrote."""
+    cfg = FLASH
+    B, T = 32, 16
+    d = _step(cfg, [TR.star(T)] * B, [4 * b + 4 for b in range(B)], 40)
+    leaf = torch.tensor([b % T for b in range(B)], dtype=torch.int32, device="cuda")
+    st = d["st"]
+    pos0, na, ni = st.pos.clone(), d["n_a"].clone(), d["n_i"].clone()
+    for _ in range(20):
+        for t in (d["proj_a"], d["proj_i"]):
+            t.fill_(SENTINEL)
+        for t, v in ((st.pos, pos0), (d["n_a"], na), (d["n_i"], ni)):
+            t.copy_(v)
+        err = err_word()
+        torch.cuda.synchronize()
+        csa.compress_tree(d["L"], d["ca"], d["x"], d["par"], st.pos, st.front_attn, d["proj_a"], d["rows_a"], d["invf"],
+                          comp_i=d["ci"], frontier_i=st.front_index, proj_i=d["proj_i"], rows_i=d["rows_i"], err=err)
+        run_commit(cfg, d, leaf, err)
+        assert err.item() == 0
+        for b in range(0, B, 5):
+            at = int(pos0[b]) % cfg.frontier_slots
+            assert torch.equal(st.front_attn[b, at], d["proj_a"][b, b % T])
+            assert torch.equal(st.front_index[b, at], d["proj_i"][b, b % T])
+            assert not (st.front_attn[b, at] == SENTINEL).all()
+
+
 def test_step_after_commit_in_one_stream():
     """Commit and the next step's calls enqueued without waiting: the step sees the committed state."""
     cfg = FLASH
