@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libcsa.so")
 CSA_F32, CSA_BF16 = 0, 1
 OP_COMPRESS, OP_INDEX_TOPK, OP_ATTEND_DECODE, OP_ATTEND_PREFILL, OP_COMPRESS_PAIR = 0, 1, 2, 3, 4
 OP_COMPRESS_VARLEN, OP_ATTEND_PREFILL_VARLEN = 5, 6
-OP_COMPRESS_TREE, OP_ATTEND_TREE = 7, 8
+OP_COMPRESS_TREE, OP_ATTEND_TREE, OP_INDEX_SCORES_TREE = 7, 8, 9
 FP8_ROW_BYTES = 144  # CSA_FP8_ROW_BYTES: 128 E4M3 codes, the fp32 scale, 12 zero bytes
 DEV_CAPACITY, DEV_STATE, DEV_RANGE, DEV_ROLLBACK = 1, 2, 4, 8
 CSA_OK, CSA_ERR_ARG, CSA_ERR_UNSUPPORTED, CSA_ERR_CUDA, CSA_ERR_WORKSPACE = 0, 1, 2, 3, 4
@@ -122,7 +122,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.csa_norm_rope.restype = i32
     lib.csa_compress_tree.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
     lib.csa_compress_tree.restype = i32
-    lib.csa_index_scores_tree.argtypes = [vp, vp, vp, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp]
+    lib.csa_index_scores_tree.argtypes = [vp, vp, vp, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp, vp]
     lib.csa_index_scores_tree.restype = i32
     lib.csa_attend_tree.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp,
                                     vp]
@@ -657,9 +657,17 @@ def _ptrs(dev: int, *specs) -> list:
     return out
 
 
-def _tree_err(err, dev):
+def _tree_new(device, stream, new, *size, dtype):
+    """A tensor of the call's own: allocated, and zeroed where it is, on the stream that will use it."""
+    if stream is None:
+        return new(*size, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return new(*size, dtype=dtype, device=device)
+
+
+def _tree_err(err, dev, stream):
     if err is None:
-        return torch.zeros(1, dtype=torch.int32, device=f"cuda:{dev}")
+        return _tree_new(f"cuda:{dev}", stream, torch.zeros, 1, dtype=torch.int32)
     if not (isinstance(err, torch.Tensor) and err.dtype is torch.int32 and err.numel() >= 1):
         _expect_err(err)
     if err.get_device() != dev:
@@ -667,10 +675,10 @@ def _tree_err(err, dev):
     return err
 
 
-def _tree_ws(layer, op, B, T, cap, ws, dev):
+def _tree_ws(layer, op, B, T, cap, ws, dev, stream):
     """The caller's workspace (the library checks its size), or a new one."""
     if ws is None:
-        ws = torch.empty(max(workspace_size(layer, op, B, T, cap), 256), dtype=torch.uint8, device=f"cuda:{dev}")
+        ws = _tree_new(f"cuda:{dev}", stream, torch.empty, max(workspace_size(layer, op, B, T, cap), 256), dtype=torch.uint8)
     elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"ws: expected a contiguous tensor on device {dev}")
     return ws, ws.numel() * ws.element_size()
@@ -731,7 +739,7 @@ def norm_rope(layer: Layer, xs, pos=None, inv_freq=None, parent=None, weights=No
     dev = x.get_device()
     if outs is None:
         new = torch.empty if parent is None else torch.zeros
-        outs = [new(x.shape, dtype=x.dtype, device=x.device) for x in xs]
+        outs = [_tree_new(x.device, stream, new, x.shape, dtype=x.dtype) for x in xs]
     rows = b""
     dtype = layer.dtype
     for k in range(n):
@@ -765,7 +773,7 @@ def norm_rope(layer: Layer, xs, pos=None, inv_freq=None, parent=None, weights=No
         p_pos, p_frq = _ptrs(dev, ("pos", pos, torch.int32, (B,)),
                              ("inv_freq", inv_freq, torch.float32, (layer.R // 2,)))
     _tree_call("csa_norm_rope", dev, stream, layer._packed(), rows, n, B, T, p_par, p_pos, p_frq,
-               _tree_err(err, dev).data_ptr())
+               _tree_err(err, dev, stream).data_ptr())
     return list(outs)
 
 
@@ -789,16 +797,18 @@ def compress_tree(layer: Layer, comp_a: Compressor, x, parent, pos, frontier_a, 
                                  ("proj_i", proj_i, dt, (B, T, wide * comp_i.d)), ("rows_i", rows_i, row_dt, (B, T, row)))
     elif not (frontier_i is None and proj_i is None and rows_i is None):
         raise ValueError("frontier_i, proj_i, rows_i come with comp_i")
-    ws, nb = _tree_ws(layer, OP_COMPRESS_TREE, B, T, 1, ws, dev)
-    err = _tree_err(err, dev)
+    ws, nb = _tree_ws(layer, OP_COMPRESS_TREE, B, T, 1, ws, dev, stream)
+    err = _tree_err(err, dev, stream)
     _tree_call("csa_compress_tree", dev, stream, layer._packed(), Ca, Ci, p_x, B, T, p_par, p_pos, p_fa, p_pa, p_ra,
                p_fi, p_pi, p_ri, p_frq, ws.data_ptr(), nb, err.data_ptr())
     return err
 
 
-def index_scores_tree(layer: Layer, iq, iw, ikeys, rows_i, parent, n_rows, pos, scores, err=None, stream=None):
-    """csa_index_scores_tree: rotated iq [B, T, Hi, Di], iw [B, T, Hi], ikeys [B, cap, Di], rows_i [B, T, Di];
-    writes scores [B, T, cap + T] (fp32).  Returns the device error word tensor."""
+def index_scores_tree(layer: Layer, iq, iw, ikeys, rows_i, parent, n_rows, pos, scores, ws=None, err=None,
+                      stream=None):
+    """csa_index_scores_tree: rotated iq [B, T, Hi, Di], iw [B, T, Hi], ikeys [B, cap, Di], rows_i [B, T, Di] (both
+    uint8 [..., FP8_ROW_BYTES] with index_fp8, which alone needs ws); writes scores [B, T, cap + T] (fp32).  Returns
+    the device error word tensor."""
     dt, i32, Hi, Di = layer.dtype, torch.int32, layer.Hi, layer.Di
     B, T, dev = _tree_dims("iq", iq, (Hi, Di))
     if not isinstance(ikeys, torch.Tensor) or ikeys.dim() != 3:
@@ -809,9 +819,13 @@ def index_scores_tree(layer: Layer, iq, iw, ikeys, rows_i, parent, n_rows, pos, 
               ("ikeys", ikeys, key_dt, (B, cap, row)), ("rows_i", rows_i, key_dt, (B, T, row)),
               ("n_rows", n_rows, i32, (B,)), ("pos", pos, i32, (B,)),
               ("scores", scores, torch.float32, (B, T, cap + T)))
-    err = _tree_err(err, dev)
+    p_ws, nb = None, 0
+    if layer.index_fp8:
+        ws, nb = _tree_ws(layer, OP_INDEX_SCORES_TREE, B, T, cap, ws, dev, stream)
+        p_ws = ws.data_ptr()
+    err = _tree_err(err, dev, stream)
     _tree_call("csa_index_scores_tree", dev, stream, layer._packed(), p[0], p[1], B, T, p[2], p[3], cap, p[4], p[5],
-               p[6], p[7], err.data_ptr())
+               p[6], p[7], p_ws, nb, err.data_ptr())
     return err
 
 
@@ -835,8 +849,8 @@ def attend_tree(layer: Layer, q, kv, sink, window, pool, rows_a, scores, parent,
         p_sc, = _ptrs(dev, ("scores", scores, f32, (B, T, cap + T)))
     if sel_out is not None:
         p_sel, = _ptrs(dev, ("sel_out", sel_out, i32, (B, T, layer.topk)))
-    ws, nb = _tree_ws(layer, OP_ATTEND_TREE, B, T, cap, ws, dev)
-    err = _tree_err(err, dev)
+    ws, nb = _tree_ws(layer, OP_ATTEND_TREE, B, T, cap, ws, dev, stream)
+    err = _tree_err(err, dev, stream)
     _tree_call("csa_attend_tree", dev, stream, layer._packed(), p_q, p_kv, p_sink, B, T, p_par, p_win, p_pool, cap,
                p_rows, p_sc, p_n, p_pos, p_frq, p_out, p_sel, ws.data_ptr(), nb, err.data_ptr())
     return err
@@ -872,7 +886,7 @@ def commit_tree(layer: Layer, parent, leaf, pos, n_rows_a, kv, window, proj_a, f
         raise ValueError("n_rows_i, proj_i, frontier_i, rows_i, n_rows_i_out come with pool_i")
     else:
         pi = (None, None, None, None, 0, None, None)
-    err = _tree_err(err, dev)
+    err = _tree_err(err, dev, stream)
     _tree_call("csa_commit_tree", dev, stream, layer._packed(), B, T, *p, *pa, *pi, err.data_ptr())
     return err
 

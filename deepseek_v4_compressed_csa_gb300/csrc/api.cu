@@ -178,6 +178,10 @@ csa_status csa_workspace_size(const csa_layer* layer, int op, int B, int T, int 
       if (!tree_sizes_ok(B, T)) return CSA_ERR_ARG;
       *bytes = ws_attend_tree(L, B, T, cap);
       return CSA_OK;
+    case CSA_OP_INDEX_SCORES_TREE:
+      if (!tree_sizes_ok(B, T)) return CSA_ERR_ARG;
+      *bytes = tree_scores_ws(L, B, T);
+      return CSA_OK;
   }
   return CSA_ERR_ARG;
 }
@@ -513,17 +517,19 @@ csa_status csa_compress_tree(const csa_layer* layer, const csa_compressor* comp_
 
 csa_status csa_index_scores_tree(const csa_layer* layer, const void* iq, const void* iw, int B, int T,
                                  const int32_t* parent, const void* ikeys, int cap, const void* rows_i,
-                                 const int32_t* n_rows, const int32_t* pos, float* scores, int32_t* err,
-                                 void* stream) {
+                                 const int32_t* n_rows, const int32_t* pos, float* scores, void* ws, size_t ws_bytes,
+                                 int32_t* err, void* stream) {
   Dims L;
   csa_status st = make_dims(layer, &L);
   if (st != CSA_OK) return st;
-  if (!L.has_indexer() || L.ikey_fp8) return CSA_ERR_UNSUPPORTED;
+  if (!L.has_indexer()) return CSA_ERR_UNSUPPORTED;
   if (!tree_sizes_ok(B, T) || cap < 1) return CSA_ERR_ARG;
   if (!dev_tensor(iq) || !dev_i32(iw) || !dev_tensor(ikeys) || !dev_tensor(rows_i) || !dev_i32(scores))
     return CSA_ERR_ARG;
   if (!dev_i32(parent) || !dev_i32(n_rows) || !dev_i32(pos) || !dev_i32(err)) return CSA_ERR_ARG;
-  return cuda_status(launch_index_scores_tree(L, iq, iw, B, T, parent, ikeys, cap, rows_i, n_rows, pos, scores, err,
+  const size_t need = tree_scores_ws(L, B, T);
+  if (ws_bytes < need || (need && !dev_tensor(ws))) return CSA_ERR_WORKSPACE;
+  return cuda_status(launch_index_scores_tree(L, iq, iw, B, T, parent, ikeys, cap, rows_i, n_rows, pos, scores, ws, err,
                                               static_cast<cudaStream_t>(stream)));
 }
 

@@ -304,13 +304,14 @@ cudaError_t launch_compress_tree(const Dims& L, const TreeCompress* pools, int n
                                  cudaStream_t s);
 cudaError_t launch_index_scores_tree(const Dims& L, const void* iq, const void* iw, int B, int T,
                                      const int32_t* parent, const void* ikeys, int cap, const void* rows,
-                                     const int32_t* n_rows, const int32_t* pos, float* scores, int32_t* err,
+                                     const int32_t* n_rows, const int32_t* pos, float* scores, void* ws, int32_t* err,
                                      cudaStream_t s);
-// ---- tc_tree_scores.cu (the same on the tensor cores; bf16, Hi = 64, Di = 128)
+// ---- tc_tree_scores.cu (the same on the tensor cores; bf16, Hi = 64, Di = 128, keys in bf16 or fp8 rows)
 bool tc_tree_scores_supported(const Dims& L, int B, int cap);
+size_t tree_scores_ws(const Dims& L, int B, int T);
 cudaError_t launch_tc_tree_scores(const Dims& L, const void* iq, const void* iw, int B, int T, const int32_t* parent,
                                   const void* ikeys, int cap, const void* rows, const int32_t* n_rows,
-                                  const int32_t* pos, float* scores, int32_t* err, cudaStream_t s);
+                                  const int32_t* pos, float* scores, void* ws, int32_t* err, cudaStream_t s);
 // What the attention kernels read of a node: its path and the path's completing nodes as masks, its position, the
 // committed length and rows of its sequence, and its keys' count from the pool and the draft rows (nsel < 0: an
 // unused slot, or a node that an error skips).

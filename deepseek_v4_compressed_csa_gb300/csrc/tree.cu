@@ -728,10 +728,11 @@ static cudaError_t index_scores_tree_t(const Dims& L, const void* iq, const void
 
 cudaError_t launch_index_scores_tree(const Dims& L, const void* iq, const void* iw, int B, int T,
                                      const int32_t* parent, const void* ikeys, int cap, const void* rows,
-                                     const int32_t* n_rows, const int32_t* pos, float* scores, int32_t* err,
+                                     const int32_t* n_rows, const int32_t* pos, float* scores, void* ws, int32_t* err,
                                      cudaStream_t s) {
   if (tc_tree_scores_supported(L, B, cap))
-    return launch_tc_tree_scores(L, iq, iw, B, T, parent, ikeys, cap, rows, n_rows, pos, scores, err, s);
+    return launch_tc_tree_scores(L, iq, iw, B, T, parent, ikeys, cap, rows, n_rows, pos, scores, ws, err, s);
+  if (L.ikey_fp8) return cudaErrorNotSupported;  // (a pool of 2^31 rows)
   if (L.dtype == CSA_BF16)
     return index_scores_tree_t<__nv_bfloat16>(L, iq, iw, B, T, parent, ikeys, cap, rows, n_rows, pos, scores, err, s);
   return index_scores_tree_t<float>(L, iq, iw, B, T, parent, ikeys, cap, rows, n_rows, pos, scores, err, s);

@@ -92,7 +92,8 @@ enum {
   CSA_OP_COMPRESS_VARLEN = 5,       /* csa_compress_append_varlen: B sequences, T = N packed tokens */
   CSA_OP_ATTEND_PREFILL_VARLEN = 6, /* csa_attend_prefill_varlen: B sequences, T = N packed tokens */
   CSA_OP_COMPRESS_TREE = 7,         /* csa_compress_tree: B trees of T nodes */
-  CSA_OP_ATTEND_TREE = 8            /* csa_attend_tree: B trees of T nodes */
+  CSA_OP_ATTEND_TREE = 8,           /* csa_attend_tree: B trees of T nodes */
+  CSA_OP_INDEX_SCORES_TREE = 9      /* csa_index_scores_tree: B trees of T nodes */
 };
 
 /* One CSA layer.
@@ -500,12 +501,15 @@ csa_status csa_compress_tree(const csa_layer* layer, const csa_compressor* comp_
  *   scores [B, T, cap + T] fp32; columns c < n_rows[b]: committed row c;
  *   columns n_rows[b] + a, a < T: the row of node a for the nodes a of i's path
  *   that complete one, -infinity for the others; later columns are not touched.
- * ikeys [B, cap, Di], rows_i [B, T, Di].  Requires ratio == 4; index_fp8 is not
- * supported (CSA_ERR_UNSUPPORTED). */
+ * ikeys [B, cap, Di], rows_i [B, T, Di]; with index_fp8 both are fp8 rows, and the
+ * queries are brought into the same form (rotation, scale, codes) as in
+ * csa_index_topk.  Requires ratio == 4.
+ * Workspace: CSA_OP_INDEX_SCORES_TREE (cap ignored; 0 bytes, and ws may be NULL,
+ * without index_fp8). */
 csa_status csa_index_scores_tree(const csa_layer* layer, const void* iq, const void* iw, int B, int T,
                                  const int32_t* parent, const void* ikeys, int cap, const void* rows_i,
-                                 const int32_t* n_rows, const int32_t* pos, float* scores, int32_t* err,
-                                 void* stream);
+                                 const int32_t* n_rows, const int32_t* pos, float* scores, void* ws, size_t ws_bytes,
+                                 int32_t* err, void* stream);
 
 /* csa_attend_tree: selection and attention of every node.
  *   visible columns: c < n_rows[b], and n_rows[b] + a for the completing nodes a

@@ -13,6 +13,8 @@ Tolerances (u = 2^-24, h = half a step of the model dtype at the value: 2^-9 of 
   attention   h, plus 2^-11 of the row's largest element: logits err by under 2^-16 (512 products of bf16 values in
               fp32), probabilities by 2^-16 (two bf16 parts), and the average over keys cannot exceed twice that; 2^-11
               leaves room for logits up to 32.  fp32: 1e-5 of the row's largest element.
+  fp8 scores  as the scores, on the codes of keys and queries (products of two codes are exact in fp32); the folded
+              weight is rounded twice more, 2 u relative to every head's term.
   selection   equal, for the scores that the call was given.
 """
 import dataclasses
@@ -278,6 +280,117 @@ def test_index_scores_tree_against_float64(case):
             diff = g[fin] - ref[fin]
             assert (np.abs(diff) <= 2 * (cfg.Di + cfg.Hi + 8) * 2.0 ** -24 * bound[fin]).all()
             assert np.linalg.norm(diff) <= 2.0 ** -18 * max(np.linalg.norm(ref[fin]), 1e-30)
+
+
+@pytest.mark.parametrize("case", ["flash", "flash_t1", "flash_t64", "flash_t13"])
+def test_index_scores_tree_fp8_against_float64(case):
+    """Keys as fp8 rows: the codes of the queries are exact (the rotated heads are bf16, as the oracle takes them)."""
+    _, trees, pos = SC_CASES[case]
+    cfg = FLASH
+    B, T, cap = len(trees), max(len(t) for t in trees), max(pos) // 4 + 3
+    layer, L = oracle_layer(cfg), dataclasses.replace(G.lib_layer(cfg), index_fp8=True)
+    iq, iw = rnd(cfg, (B, T, 64, 128), 230), rnd(cfg, (B, T, 64), 231)
+    iq[0, 0, 5] = 0  # a head of zeros: scale 0, zero codes
+    src = [rnd(cfg, (B, cap, 128), 232), rnd(cfg, (B, T, 128), 233)]
+    src[0][0, 0] = 0
+    src[0][0, 1] *= 2.0 ** 40
+    ikeys, rows = (torch.zeros(*t.shape[:2], csa.FP8_ROW_BYTES, dtype=torch.uint8, device="cuda") for t in src)
+    for t, o in zip(src, (ikeys, rows)):
+        csa.index_rows_fp8(L, t, o)
+    keys8 = [(o[..., :128].cpu().numpy().astype(np.int64),
+              np.ascontiguousarray(o[..., 128:132].cpu().numpy()).view(np.float32)[..., 0]) for o in (ikeys, rows)]
+    for b in range(B):  # what no node may read: codes and scales that are NaN
+        ikeys[b, pos[b] // 4:] = 0xFF
+        for i, path in enumerate(TR.paths(TR.padded(trees[b], T))):
+            if path is None or (pos[b] + len(path)) % 4:
+                rows[b, i] = 0xFF
+    scores = torch.full((B, T, cap + T), SENTINEL, device="cuda")
+    p = torch.tensor(pos, dtype=torch.int32, device="cuda")
+    err = csa.index_scores_tree(L, iq, iw, ikeys, rows, parents(trees, T), p // 4, p, scores)
+    assert err.item() == 0
+    got = f64(scores)
+    for b in range(B):
+        n = pos[b] // 4
+        assert (got[b, :, n + T:] == SENTINEL).all()
+        codes = np.concatenate([keys8[0][0][b, :n], keys8[1][0][b]])
+        scale = np.concatenate([keys8[0][1][b, :n], keys8[1][1][b]]).astype(np.float64)
+        kv = O.e4m3_decode(codes)
+        for i, path in enumerate(TR.paths(TR.padded(trees[b], T))):
+            if path is None:
+                assert (got[b, i] == SENTINEL).all()
+                continue
+            q = [O.quantize_fp8_row(f64(iq[b, i, h])) for h in range(64)]
+            qc, qs = np.stack([c for c, _ in q]), np.array([x for _, x in q], dtype=np.float64)
+            ref = O.index_scores_fp8(layer, qc, qs, f64(iw[b, i]), codes, scale)
+            w = np.abs(f64(iw[b, i])) * (128 ** -0.5) * (64 ** -0.5) * qs / 128
+            bound = (w[:, None] * (np.abs(O.e4m3_decode(qc)) @ np.abs(kv).T)).sum(0) * scale
+            seen = np.zeros(n + T, dtype=bool)
+            seen[TR.columns(layer, path, pos[b], T)] = True
+            g = got[b, i, :n + T]
+            assert (g[~seen] == -np.inf).all()
+            assert (np.abs(g - ref)[seen] <= 2 * (cfg.Di + cfg.Hi + 8) * 2.0 ** -24 * bound[seen]).all()
+
+
+def test_tree_step_with_fp8_index_rows():
+    """The step and the commit of a layer whose index pool holds fp8 rows: scores on the rows that compress_tree wrote,
+    a selection that is theirs, and the accepted rows moved byte for byte."""
+    cfg, trees, pos = FLASH, [TR.bushy(9), TR.chain(7)], [2051, 4002]
+    d = _step(cfg, trees, pos, 1100, seed=300)
+    L = d["L"] = dataclasses.replace(d["L"], index_fp8=True)
+    st, T = d["st"], 9
+    keys16 = st.ikeys
+    st.ikeys = torch.zeros(2, 1100, csa.FP8_ROW_BYTES, dtype=torch.uint8, device="cuda")
+    csa.index_rows_fp8(L, keys16, st.ikeys)
+    d["rows_i"] = torch.zeros(2, T, csa.FP8_ROW_BYTES, dtype=torch.uint8, device="cuda")
+    err = err_word()
+    run_step(cfg, d, err)
+    assert err.item() == 0
+    layer, invf = oracle_layer(cfg), f64(csa_synth.inv_freq(cfg)).astype(np.float32)
+    keep = st.ikeys.clone()
+    for b in range(2):
+        for i, path in enumerate(TR.paths(TR.padded(trees[b], T))):
+            if path is not None:
+                cols = TR.select(layer, f64(d["scores"][b, i]), path, pos[b], T)
+                assert d["sel"][b, i, :len(cols)].tolist() == cols.tolist()
+    leaf = [8, 6]
+    run_commit(cfg, d, torch.tensor(leaf, dtype=torch.int32, device="cuda"), err)
+    assert err.item() == 0
+    for b in range(2):
+        for k, node in enumerate(TR.paths(trees[b])[leaf[b]]):
+            if (pos[b] + k + 1) % 4 == 0:
+                keep[b, (pos[b] + k + 1) // 4 - 1] = d["rows_i"][b, node]
+                assert d["rows_i"][b, node].any()
+    assert torch.equal(st.ikeys, keep)
+
+
+def test_calls_on_a_given_stream_own_what_they_allocate():
+    """stream=: outputs, workspaces and the error word of the call's own are allocated and zeroed on that stream."""
+    cfg = FLASH
+    d = _step(cfg, [TR.bushy(8)] * 3, [3001, 3200, 57], 900, seed=400)
+    st, L = d["st"], d["L"]
+    want, side = None, torch.cuda.Stream()
+    for stream in (None, side, side):
+        side.wait_stream(torch.cuda.current_stream())
+        big = torch.randn(4096, 4096, device="cuda")  # work on the current stream that the side stream does not await
+        for _ in range(4):
+            big = big @ big * 1e-3
+        q, kv, iq = csa.norm_rope(L, [d["q"], d["kv"], d["iq"]], st.pos, d["invf"], parent=d["par"],
+                                  norm=[True, True, False], stream=stream)
+        errs = [csa.compress_tree(L, d["ca"], d["x"], d["par"], st.pos, st.front_attn, d["proj_a"], d["rows_a"],
+                                  d["invf"], comp_i=d["ci"], frontier_i=st.front_index, proj_i=d["proj_i"],
+                                  rows_i=d["rows_i"], stream=stream),
+                csa.index_scores_tree(L, iq, d["iw"], st.ikeys, d["rows_i"], d["par"], d["n_a"], st.pos, d["scores"],
+                                      stream=stream),
+                csa.attend_tree(L, q, kv, d["sink"], st.window, st.pool, d["rows_a"], d["scores"], d["par"], d["n_a"],
+                                st.pos, d["invf"], d["out"], sel_out=d["sel"], stream=stream)]
+        torch.cuda.synchronize()
+        assert all(e.item() == 0 for e in errs)
+        got = [t.clone() for t in (q, kv, iq, d["scores"], d["out"], d["sel"])]
+        if want is None:
+            want = got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        for k in ("scores", "out", "sel"):
+            d[k].zero_()
 
 
 # ------------------------------------------------------------------------------------------------ attend_tree

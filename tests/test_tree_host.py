@@ -71,17 +71,26 @@ def test_compress_tree_refusals(lib):
 
 
 def test_index_scores_tree_refusals(lib):
-    def call(layer=None, B_=2, T=8, cap=100, **over):
+    def call(layer=None, B_=2, T=8, cap=100, ws=None, ws_bytes=0, **over):
         a = dict(iq=FAKE, iw=FAKE, parent=FAKE, ikeys=FAKE, rows=FAKE, n_rows=FAKE, pos=FAKE, scores=FAKE, err=FAKE)
         a.update(over)
         return lib.csa_index_scores_tree(ctypes.byref(layer or _layer()), a["iq"], a["iw"], B_, T, a["parent"],
-                                         a["ikeys"], cap, a["rows"], a["n_rows"], a["pos"], a["scores"], a["err"], None)
+                                         a["ikeys"], cap, a["rows"], a["n_rows"], a["pos"], a["scores"], ws, ws_bytes,
+                                         a["err"], None)
     for k in ("iq", "iw", "parent", "ikeys", "rows", "n_rows", "pos", "scores", "err"):
         assert call(**{k: None}) == B.CSA_ERR_ARG, k
         assert call(**{k: FAKE + 1}) == B.CSA_ERR_ARG, k
     assert call(T=65) == B.CSA_ERR_ARG and call(cap=0) == B.CSA_ERR_ARG and call(B_=0) == B.CSA_ERR_ARG
     assert call(layer=_layer(ratio=128)) == B.CSA_ERR_UNSUPPORTED
-    assert call(layer=_layer(index_fp8=1)) == B.CSA_ERR_UNSUPPORTED
+    # fp8 rows: the queries' codes and weights go into the workspace
+    fp8, need = _layer(index_fp8=1), 2 * 8 * 64 * 132
+    for kw in (dict(), dict(ws=FAKE, ws_bytes=need - 1), dict(ws_bytes=need), dict(ws=FAKE + 8, ws_bytes=need)):
+        assert call(layer=fp8, **kw) == B.CSA_ERR_WORKSPACE, kw
+    n = ctypes.c_size_t()
+    assert lib.csa_workspace_size(ctypes.byref(fp8), B.OP_INDEX_SCORES_TREE, 2, 8, 1, ctypes.byref(n)) == 0
+    assert n.value == need
+    assert lib.csa_workspace_size(ctypes.byref(_layer()), B.OP_INDEX_SCORES_TREE, 2, 8, 1, ctypes.byref(n)) == 0
+    assert n.value == 0
 
 
 def test_attend_tree_refusals(lib):
