@@ -25,6 +25,16 @@
 //     sums); a logit far below the sink gives zero, as it should.  Sums stay per thread until the node's last tile.
 //   epilogue (warps 0-7)  O^T / Z, rotated back, rounded once, through the P buffer (free then) to TMA stores: a thread
 //     holds one dim of 32 heads, and its 2-byte stores straight to memory cost 7 us a node.
+// 512 nodes of 640 keys, 512 of them selected: 100 us beside 22 for the selection; 128 nodes of 1.9K consecutive keys
+// each: 64 us, 5.7K clocks a tile of the 3.8K that its products take.
+//
+// Few nodes with long lists (kSplit): a cluster of S CTAs per node, each its run of the tiles, the parts of O^T joined
+// through distributed shared memory.  S is the largest of 8, 4, 2 whose clusters all run at once and that leaves two
+// tiles to each CTA (one tile each gains nothing over the join): 8 nodes over 8.2K rows take 48 us instead of 196, 64
+// over 2K 44 instead of 59.  The same for the nodes left over after whole rounds of the SMs saves 2 us of 122 at 512
+// nodes, which its bookkeeping costs again: those stay a CTA each.
+#include <atomic>
+
 #include "kernels.h"
 #include "tc.cuh"
 #include "tree.cuh"
@@ -48,6 +58,7 @@ constexpr int kTmemCols = 512;
 constexpr uint32_t kColO3 = 384;         // O^T tile 3 (hi + lo in one accumulator); tiles 0-2: 128 m, hi | lo
 constexpr uint32_t kColS = 448;          // S^T
 constexpr float kRaiseAt = 64.f;         // log2 headroom over the reference
+constexpr int kMaxSplit = 8;
 constexpr int kBarAll = 3;               // named barriers: 1, 2 the halves, 3 all softmax warps
 
 constexpr int kOffQ = 8 * kBox;
@@ -70,7 +81,9 @@ struct TaArgs {
   const TreeNode* nodes;       // [Q]
   const float* sink;
   const float* inv_freq;
+  __nv_bfloat16* out;          // [Q, 64, 512]
   int Q, T, cap, topk, W, Wr;
+  int S;                       // kSplit: CTAs of the cluster that shares a query
   float scale2;                // softmax scale * log2(e)
   int32_t* err;
 };
@@ -88,6 +101,18 @@ __device__ __forceinline__ const __nv_bfloat16* key_row(const TaArgs& a, const T
   }
   const int t = r.p - min(a.W, r.p + 1) + 1 + (k - r.nsel);
   return t < r.p0 ? a.ring + (b * a.Wr + t % a.Wr) * kAD : a.kv + (b * a.T + tree_node_at(r.mask, t - r.p0)) * kAD;
+}
+
+// The keys [k0, k1) among a query's that this CTA takes: all, or (kSplit) its run of the tiles.
+template <bool kSplit>
+__device__ __forceinline__ void key_range(const TaArgs& a, int keys, int& k0, int& k1) {
+  k0 = 0;
+  k1 = keys;
+  if constexpr (kSplit) {
+    const int tiles = (keys + kPR - 1) / kPR, rank = blockIdx.x % a.S;
+    k0 = min(keys, (int)((long long)tiles * rank / a.S) * kPR);
+    k1 = min(keys, (int)((long long)tiles * (rank + 1) / a.S) * kPR);
+  }
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -141,6 +166,82 @@ __device__ __forceinline__ float reduce_scatter32(float (&v)[32]) {
   return v[0];
 }
 
+// The softmax warps: the joined output of query qi.  CTA r of the cluster takes dims [512 r / S, 512 (r + 1) / S) of
+// every head, four a thread, from the S parts in rank order.  Parts are relative to references of their own: the largest
+// one is the common one.  (A part without keys has a sum of zero and no O^T.)  table: S x 64 floats.
+__device__ __forceinline__ void join_parts(const TaArgs& a, const uint8_t* rows, const float* nref, const float* sums,
+                                           float* table, int qi) {
+  const int tid = threadIdx.x, per = kAD / a.S / 4, d = kAD / a.S * (blockIdx.x % a.S) + 4 * (tid % per);
+  if (tid < kAH) {  // each part's factor of head tid
+    float ref[kMaxSplit], sum[kMaxSplit], top = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < kMaxSplit; ++s) {
+      if (s >= a.S) break;
+      ref[s] = -tc::ld_cluster_f32(tc::cluster_map(nref + tid, s));
+      sum[s] = tc::ld_cluster_f32(tc::cluster_map(sums + tid, s));
+      top = fmaxf(top, ref[s]);
+    }
+    float Z = exp2f(__ldg(a.sink + tid) * 1.4426950408889634f - top);
+#pragma unroll
+    for (int s = 0; s < kMaxSplit; ++s) {
+      if (s >= a.S) break;
+      ref[s] = sum[s] == 0.f ? 0.f : exp2f(ref[s] - top);
+      Z = fmaf(ref[s], sum[s], Z);
+    }
+#pragma unroll
+    for (int s = 0; s < kMaxSplit; ++s) {
+      if (s >= a.S) break;
+      table[s * kAH + tid] = ref[s] / Z;
+    }
+  }
+  float c0 = 1.f, s0 = 0.f, c1 = 1.f, s1 = 0.f;
+  const bool turned = d >= kAD - 64;
+  if (turned) {
+    const int p = a.nodes[qi].p, i = (d - (kAD - 64)) >> 1;
+    rope_cs(p, a.inv_freq, i, &c0, &s0);
+    rope_cs(p, a.inv_freq, i + 1, &c1, &s1);
+  }
+  tc::named_bar(kBarAll, kSoft);
+  const float* part = reinterpret_cast<const float*>(rows) + d;
+  constexpr int kU = 8;  // heads in flight a thread
+  const int step = kSoft / per;
+  for (int h0 = tid / per; h0 < kAH; h0 += kU * step) {
+    float4 o[kU];
+#pragma unroll
+    for (int k = 0; k < kU; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < a.S; ++s) {
+      float4 v[kU];
+      float f[kU];
+#pragma unroll
+      for (int k = 0; k < kU; ++k) {
+        const int h = h0 + k * step;
+        f[k] = h < kAH ? table[s * kAH + h] : 0.f;
+        if (f[k] != 0.f) v[k] = tc::ld_cluster_f4(tc::cluster_map(part + h * kAD, s));
+      }
+#pragma unroll
+      for (int k = 0; k < kU; ++k)
+        if (f[k] != 0.f)
+          o[k] = make_float4(fmaf(f[k], v[k].x, o[k].x), fmaf(f[k], v[k].y, o[k].y), fmaf(f[k], v[k].z, o[k].z),
+                             fmaf(f[k], v[k].w, o[k].w));
+    }
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      const int h = h0 + k * step;
+      if (h >= kAH) break;
+      float4 y = o[k];
+      if (turned)
+        y = make_float4(fmaf(y.x, c0, y.y * s0), fmaf(-y.x, s0, y.y * c0), fmaf(y.z, c1, y.w * s1),
+                        fmaf(-y.z, s1, y.w * c1));
+      uint2 pk;
+      __nv_bfloat162* b = reinterpret_cast<__nv_bfloat162*>(&pk);
+      b[0] = __floats2bfloat162_rn(y.x, y.y);
+      b[1] = __floats2bfloat162_rn(y.z, y.w);
+      *reinterpret_cast<uint2*>(a.out + ((size_t)qi * kAH + h) * kAD + d) = pk;
+    }
+  }
+}
+
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     k_tc_tree_attend(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_out,
                      const __grid_constant__ CUtensorMap tm_pool, const __grid_constant__ CUtensorMap tm_row,
@@ -195,6 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   bool failed = false;
+  int joins = -1;  // kSplit, softmax warps: the query whose parts the cluster joins
+  const int q_first = kSplit ? blockIdx.x / a.S : blockIdx.x, q_step = kSplit ? gridDim.x / a.S : gridDim.x;
 
   if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
@@ -206,11 +309,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t vd = tc::sdesc_mnmajor_sw128(tc::smem_u32(rows), kBox, 1024);
       const uint64_t pd = tc::sdesc_mnmajor_sw128(tc::smem_u32(pbuf), kPPart, 1024);
       uint32_t nq = 0, nt = 0;
-      for (int qi = blockIdx.x; qi < a.Q && !failed; qi += gridDim.x) {
-        const int keys = node_keys(a, a.nodes[qi]);
-        if (keys == 0) continue;
+      for (int qi = q_first; qi < a.Q && !failed; qi += q_step) {
+        int first, keys;
+        key_range<kSplit>(a, node_keys(a, a.nodes[qi]), first, keys);
+        if (first == keys) continue;
         if (!tc::mbar_wait(q_full, nq & 1)) { failed = true; break; }
-        for (int k0 = 0; k0 < keys; k0 += kPR, ++nt) {
+        for (int k0 = first; k0 < keys; k0 += kPR, ++nt) {
           const uint32_t par = nt & 1;
           // S^T = K Q^T, pair by pair as the rows land
 #pragma unroll
@@ -227,11 +331,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool last = k0 + kPR >= keys;
           if (last) tc::mma_commit(q_empty);
           if (!tc::mbar_wait(p_full, par)) { failed = true; break; }
-          if (k0 == 0 && nq > 0 && !tc::mbar_wait(o_free, (nq - 1) & 1)) { failed = true; break; }
+          if (k0 == first && nq > 0 && !tc::mbar_wait(o_free, (nq - 1) & 1)) { failed = true; break; }
           tc::fence_after_sync();
           // O^T += V^T P^T: dims 128 m .., tiles 0-2 with both parts side by side, tile 3 with the parts in turn.  The
           // last tile's products stop at its last 16 keys.
-          const uint32_t acc = k0 > 0;
+          const uint32_t acc = k0 > first;
           if (!last || keys - k0 > kPR - 16) {
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
@@ -287,25 +391,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int my_row = c < kInstr && w + kLoadWarps * c < 64 ? 2 * (w + kLoadWarps * c) + (lane >> 4) : kPR;
     const int j = w + kLoadWarps * lane;  // this lane's gather of a pair (none: j >= 64)
     const int n_gather = (64 - w + kLoadWarps - 1) / kLoadWarps;
-    struct Tile {  // a tile of the walk: query, first key, the query's keys and record
+    struct Tile {  // a tile of the walk: query, first key, the end of the CTA's keys of the query, its record
       int qi, k0, keys;
+      bool first;  // kSplit: of the query's tiles here
       TreeNode rec;
     };
     TreeNode ahead;  // the record of the query after the walk's
-    auto start_query = [&](Tile& t, int qi) {  // the first query from qi on that has keys; `ahead` is qi's record
-      for (; qi < a.Q; qi += gridDim.x) {
+    auto start_query = [&](Tile& t, int qi) {  // the first query from qi on that has keys here; `ahead` is qi's record
+      for (; qi < a.Q; qi += q_step) {
         t.rec = ahead;
-        ahead = a.nodes[min(qi + (int)gridDim.x, a.Q - 1)];
-        t.keys = node_keys(a, t.rec);
-        if (t.keys > 0) break;
+        ahead = a.nodes[min(qi + q_step, a.Q - 1)];
+        key_range<kSplit>(a, node_keys(a, t.rec), t.k0, t.keys);
+        if (t.keys > t.k0) break;
       }
       t.qi = qi;
-      t.k0 = 0;
+      if constexpr (kSplit) t.first = true;
     };
     auto advance = [&](Tile& t) {
       if (t.qi >= a.Q) return;
       t.k0 += kPR;
-      if (t.k0 >= t.keys) start_query(t, t.qi + gridDim.x);
+      if constexpr (kSplit) t.first = false;
+      if (t.k0 >= t.keys) start_query(t, t.qi + q_step);
     };
     struct Columns {  // of this lane's row, of its gather's rows, of the tile's last row
       int own, g[4], last;
@@ -334,10 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int e = 0; e < 8; ++e) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 64 * e));
       return p;
     };
-    ahead = a.nodes[min((int)blockIdx.x, a.Q - 1)];
+    ahead = a.nodes[q_first];  // (the grid has at most Q clusters)
     Tile cur, nxt;
     Columns col{};
-    start_query(cur, blockIdx.x);
+    start_query(cur, q_first);
     columns(cur, col);
     int mode = cur.qi < a.Q ? tile_mode(cur, col) : kByAddress;
     const __nv_bfloat16* ptr = address(cur, mode, col.own);
@@ -347,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     columns(nxt, col);
     uint32_t nq = 0, nt = 0;
     for (; cur.qi < a.Q && !failed; ++nt) {
-      if (cur.k0 == 0) {
+      if (kSplit ? cur.first : cur.k0 == 0) {
         if (w == 0 && lane == 0) {
           // the query block, once the previous query's last score product has retired
           if (nq > 0 && !tc::mbar_wait(q_empty, (nq - 1) & 1)) failed = true;
@@ -436,14 +542,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* stage = pbuf + half * kPPart;  // the epilogue's: two buffers of 32 heads x 128 dims
     uint8_t* pdst = pbuf + (row >> 3) * 1024 + (row & 7) * 128;
     uint32_t nq = 0, nt = 0;
-    int p_next = a.nodes[blockIdx.x].p, nsel_next = a.nodes[blockIdx.x].nsel;  // (the grid has at most Q blocks)
-    for (int qi = blockIdx.x; qi < a.Q && !failed; qi += gridDim.x) {
-      const int p = p_next, keys = nsel_next < 0 ? 0 : nsel_next + min(a.W, p + 1);
+    int p_next = a.nodes[q_first].p, nsel_next = a.nodes[q_first].nsel;
+    for (int qi = q_first; qi < a.Q && !failed; qi += q_step) {
+      const int p = p_next, all_keys = nsel_next < 0 ? 0 : nsel_next + min(a.W, p + 1);
       // the next record is on its way while this node is worked on
-      const TreeNode* next = a.nodes + min(qi + (int)gridDim.x, a.Q - 1);
+      const TreeNode* next = a.nodes + min(qi + q_step, a.Q - 1);
       p_next = next->p;
       nsel_next = next->nsel;
-      if (keys == 0) continue;
+      if (all_keys == 0) continue;
+      int first, keys;
+      key_range<kSplit>(a, all_keys, first, keys);
       // the previous query's stores have read the P buffer, its 1 / Z has been used
       if (quad == 0 && lane == 0) bulk_wait_read<0>();
       if (quad == 0) nref[hb + lane] = -ref0;
@@ -451,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2 l[16];
 #pragma unroll
       for (int h = 0; h < 16; ++h) l[h] = make_float2(0.f, 0.f);
-      for (int k0 = 0; k0 < keys; k0 += kPR, ++nt) {
+      for (int k0 = first; k0 < keys; k0 += kPR, ++nt) {
         if (!tc::mbar_wait(s_full, nt & 1)) failed = true;
         tc::fence_after_sync();
         const bool live = k0 + row < keys;
@@ -532,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::named_bar(bar, kHalf);
 #pragma unroll
           for (int h = 0; h < 16; ++h) l[h] = __fmul2_rn(l[h], make_float2(v[2 * h], v[2 * h + 1]));
-          if (k0 > 0) {  // every earlier PV product has retired (S^T was issued after it)
+          if (k0 > first) {  // every earlier PV product has retired (S^T was issued after it)
 #pragma unroll 1
             for (int g = 0; g < 7; ++g) {
               const uint32_t ta = ts + (g < 6 ? 64 * g : kColO3);
@@ -568,19 +676,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::named_bar(bar, kHalf);
       if (quad == 0 && !failed) {
         const int h = hb + lane;
-        const float Z = exp2f(z2 + nref[h]) + ((red[h] + red[64 + h]) + (red[128 + h] + red[192 + h]));
-        invz[h] = 1.0f / Z;
+        const float sum = (red[h] + red[64 + h]) + (red[128 + h] + red[192 + h]);
+        invz[h] = kSplit ? sum : 1.0f / (exp2f(z2 + nref[h]) + sum);
       }
       // inverse RoPE of this thread's dim of tile 3 (dims 448-511 are lane quarters 2 and 3)
       float rc = 1.f, rs = 0.f;
       if (quad >= 2) rope_cs(p, a.inv_freq, (32 * quad + lane - 64) >> 1, &rc, &rs);
-      if (!failed && !tc::mbar_wait(pv_done, (nt - 1) & 1)) failed = true;
+      if (!failed && (!kSplit || first < keys) && !tc::mbar_wait(pv_done, (nt - 1) & 1)) failed = true;
       // both halves: P is no longer read, the buffers may take outputs
       if (tc::named_bar_any(kBarAll, kSoft, failed)) {
         failed = true;
         break;
       }
       tc::fence_after_sync();
+      if constexpr (kSplit) {
+        // The CTA's part of O^T into its own shared memory, [64 heads][512 dims] over the key rows (the last products
+        // have retired), its sums and references beside it.
+        float* part = reinterpret_cast<float*>(rows) + hb * kAD + row;
+#pragma unroll 1
+        for (int m = 0; m < 4 && first < keys; ++m) {
+          uint32_t u[32];
+          tc::tmem_ld32(ts + (m < 3 ? 128 * m : kColO3), u);
+          tc::tmem_wait_ld();
+          if (m < 3) {
+            uint32_t u2[32];
+            tc::tmem_ld32(ts + 128 * m + 64, u2);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int h = 0; h < 32; ++h) u[h] = __float_as_uint(__uint_as_float(u[h]) + __uint_as_float(u2[h]));
+          }
+#pragma unroll
+          for (int h = 0; h < 32; ++h) part[h * kAD + 128 * m] = __uint_as_float(u[h]);
+        }
+        joins = qi;
+        break;  // (a cluster has one query)
+      }
       const float4* iz4 = reinterpret_cast<const float4*>(invz + hb);
 #pragma unroll 1
       for (int m = 0; m < 4; ++m) {
@@ -639,10 +769,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (quad == 0 && lane == 0) bulk_wait_all();  // shared memory is read, the output written
   }
+  if constexpr (kSplit) {
+    __syncwarp();
+    tc::cluster_sync();  // the parts are written
+    if (joins >= 0) join_parts(a, rows, nref, invz, reinterpret_cast<float*>(pbuf), joins);
+    __syncwarp();
+    tc::cluster_sync();  // ... and read
+  }
   if (failed) atomicOr(a.err, tc::kErrTimeout);
   tc::fence_before_sync();
   __syncthreads();
   if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+// Clusters of S CTAs, one CTA an SM, that run at once (a property of the device: asked once for each).
+int clusters(int S) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][kMaxSplit + 1];  // 0: not asked yet, else 1 + n
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
+  int n = known[dev][S].load(std::memory_order_relaxed) - 1;
+  if (n < 0) {
+    cudaFuncSetAttribute(k_tc_tree_attend<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    n = max_clusters(k_tc_tree_attend<true>, kThreads, kSmem, S);
+    known[dev][S].store(n + 1, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 }  // namespace
@@ -667,8 +819,17 @@ cudaError_t launch_tc_attend_tree(const Dims& L, const TreeAttend& t, const int3
       !make_tmap_2d_bf16(&tp, t.pool, (uint64_t)t.B * t.cap, kAD, kAD * 2, kPR) ||
       !make_tmap_2d_bf16(&tr, t.pool, (uint64_t)t.B * t.cap, kAD, kAD * 2, 1))
     return cudaErrorInvalidValue;
-  cudaFuncSetAttribute(k_tc_tree_attend, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  CSA_LAUNCH(k_tc_tree_attend, dim3(min(a.Q, sms)), dim3(kThreads), kSmem, s, tq, to, tp, tr, a);
+  a.out = static_cast<__nv_bfloat16*>(t.out);
+  const long long tiles = ((t.scores ? L.topk : (long long)t.cap + t.T) + L.W + kPR - 1) / kPR;
+  for (a.S = kMaxSplit; a.S > 1; a.S /= 2)
+    if (tiles >= 2 * a.S && a.Q <= clusters(a.S)) {
+      cudaFuncSetAttribute(k_tc_tree_attend<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      const cudaError_t e = launch_pdl_cluster(k_tc_tree_attend<true>, dim3(a.Q * a.S), dim3(kThreads), kSmem, s, a.S, tq,
+                                               to, tp, tr, a);
+      return e != cudaSuccess ? e : cudaGetLastError();
+    }
+  cudaFuncSetAttribute(k_tc_tree_attend<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  CSA_LAUNCH(k_tc_tree_attend<false>, dim3(min(a.Q, sms)), dim3(kThreads), kSmem, s, tq, to, tp, tr, a);
   return cudaGetLastError();
 }
 

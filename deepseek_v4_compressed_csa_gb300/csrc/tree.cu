@@ -760,7 +760,7 @@ static cudaError_t attend_tree_t(const Dims& L, const TreeAttend& t, int32_t* er
                t.ws.nodes, err);
   }
   // Tensor-core shapes.  Few nodes: S splits of one 160-row tile each, a cluster per query, while every split has an
-  // SM.  More: a CTA per query streaming its tiles.
+  // SM.  More nodes or keys: tc_tree_attend.cu.
   const bool codes_fit = (long long)t.B * t.cap < INT32_MAX && (long long)t.B * L.Wr < (1 << 28);
   if (tc_attend_supported(L) && codes_fit) {
     const int n_max = t.scores ? L.topk : t.cap + t.T;

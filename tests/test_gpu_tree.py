@@ -487,7 +487,14 @@ def check_tree_outputs(cfg, layer, trees, pos, q, kv, sink, window, pool, rows, 
 
 
 EDGE_CASES = {
-    # layer, trees, positions, selection: split kernel (few nodes), many nodes, portable kernel
+    # layer, trees, positions, selection: split kernel (few nodes), many nodes, portable kernel; nodes whose keys a
+    # cluster of CTAs shares: few nodes with all rows wanted, some of
+    # them with fewer tiles than CTAs; more nodes than SMs
+    "flash_rows_8_ways": ("flash", [TR.bushy(3), TR.star(4)], [9001, 5], False),
+    "flash_rows_4_ways": ("flash", [TR.bushy(10), TR.chain(14)], [3300, 40], False),
+    "flash_rows_2_ways": ("flash", [TR.bushy(20, s) for s in range(3)], [2004, 700, 1], False),
+    "flash_left_over": ("flash", [TR.bushy(16, s) for s in range(10)], [2100 + 91 * s for s in range(9)] + [3], True),
+    "flash_r128_left_over": ("flash_r128", [TR.bushy(19, s) for s in range(9)], [60000 + 9091 * s for s in range(8)] + [99], False),
     "flash_few": ("flash", [TR.bushy(5), TR.chain(7)], [4097, 2301], True),
     "flash_many": ("flash", [TR.bushy(16, s) for s in range(11)], [2100 + 91 * s for s in range(11)], True),
     "flash_many_rows": ("flash_r128", [TR.bushy(16, s) for s in range(11)], [9000 + 1291 * s for s in range(11)], False),
