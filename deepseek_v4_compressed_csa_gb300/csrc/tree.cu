@@ -18,10 +18,12 @@ namespace {
 // once.  Bound by memory (2 x the tensors' bytes) only while a row costs few instructions: a row of up to 256 values
 // sits in 2^k lanes (several rows a warp), a longer one in a warp, 8 values a lane and chunk, sums and products run as
 // packed pairs, and a block takes a whole token, so that its angles (sines of up to 10^5 rad, some hundred instructions
-// each) are found once; with few tokens a token's rows are split over blocks.  4096 tokens of 64 x 512, 512 and 64 x 128
-// values: 130 us, 5.2 TB/s (two or four tokens a block 134 and 153 us; four rows in flight a warp in place of two 131 us).
+// each) are found once, its rows requested into L2 meanwhile; with few tokens a token's rows are split over blocks.  4096
+// tokens of 64 x 512, 512 and 64 x 128 values: 112 us, 6.1 TB/s (without the requests 128 us; two row groups in flight a
+// warp in place of one 118 us, the next one's loads before a group's arithmetic 120 us; two tokens a block 4% more).
 constexpr int kNrParts = 4;
 constexpr int kNrWarps = 8;
+constexpr int kNrAhead = 128 * 1024;  // bytes of a token's tensor that are prefetched
 
 template <typename T>
 struct NrPart {
@@ -69,7 +71,6 @@ __device__ __forceinline__ void raw_get(const Raw8<float>& r, float2 (&o)[4]) {
 template <typename T, int kChunks>
 __device__ __forceinline__ void norm_rope_part(const NrPart<T>& pt, int tok, int first, int step, int R, float eps,
                                                bool rotate, const float2* cs) {
-  constexpr int kB = sizeof(T) == 2 && kChunks < 4 ? 2 : 1;  // row groups in flight
   const int lane = threadIdx.x & 31, lg = kChunks > 1 ? 5 : pt.lpr_log2, sub = lane & ((1 << lg) - 1);
   const int rpw = 32 >> lg, n8 = pt.dim >> 3, r0 = pt.dim - R, heads = pt.heads, dim = pt.dim, norm = pt.norm;
   const float* w = pt.w;
@@ -77,67 +78,59 @@ __device__ __forceinline__ void norm_rope_part(const NrPart<T>& pt, int tok, int
   const T* x = pt.x + (size_t)tok * pt.x_stride + sub * 8;
   T* out = pt.out + (size_t)tok * heads * dim + sub * 8;
   const int h0 = lane >> lg;
-  for (int g0 = first; g0 * rpw < heads; g0 += kB * step) {
-    Raw8<T> raw[kB][kChunks];
+  for (int g = first; g * rpw < heads; g += step) {
+    const int h = g * rpw + h0;
+    Raw8<T> raw[kChunks];
 #pragma unroll
-    for (int u = 0; u < kB; ++u) {
-      const int h = (g0 + u * step) * rpw + h0;
+    for (int i = 0; i < kChunks; ++i)
+      if (h < heads && sub + 32 * i < n8) raw_load(raw[i], x + (size_t)h * dim + 256 * i);
+    float2 v[kChunks][4];
+    float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      if (h < heads && sub + 32 * i < n8) {
+        raw_get(raw[i], v[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s2 = __ffma2_rn(v[i][e], v[i][e], s2);
+      }
+    }
+    if (norm) {
+      float ss = s2.x + s2.y;
+      if (kChunks > 1) {
+        ss = warp_sum(ss);
+      } else {
+        for (int o = 1 << lg >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      }
+      const float inv = rsqrtf(fmaf(ss, inv_dim, eps));
+      const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
       for (int i = 0; i < kChunks; ++i)
-        if (h < heads && sub + 32 * i < n8) raw_load(raw[u][i], x + (size_t)h * dim + 256 * i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][e] = __fmul2_rn(v[i][e], inv2);
     }
 #pragma unroll
-    for (int u = 0; u < kB; ++u) {
-      if ((g0 + u * step) * rpw >= heads) break;  // the whole warp
-      const int h = (g0 + u * step) * rpw + h0;
-      float2 v[kChunks][4];
-      float2 s2 = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        if (h < heads && sub + 32 * i < n8) {
-          raw_get(raw[u][i], v[i]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s2 = __ffma2_rn(v[i][e], v[i][e], s2);
-        }
+    for (int i = 0; i < kChunks; ++i) {
+      const int c = sub + 32 * i;
+      if (h >= heads || c >= n8) continue;
+      if (norm && w) {
+        const float4 wa = __ldg(reinterpret_cast<const float4*>(w + 8 * c));
+        const float4 wb = __ldg(reinterpret_cast<const float4*>(w + 8 * c) + 1);
+        v[i][0] = __fmul2_rn(v[i][0], make_float2(wa.x, wa.y));
+        v[i][1] = __fmul2_rn(v[i][1], make_float2(wa.z, wa.w));
+        v[i][2] = __fmul2_rn(v[i][2], make_float2(wb.x, wb.y));
+        v[i][3] = __fmul2_rn(v[i][3], make_float2(wb.z, wb.w));
       }
-      if (norm) {
-        float ss = s2.x + s2.y;
-        if (kChunks > 1) {
-          ss = warp_sum(ss);
-        } else {
-          for (int o = 1 << lg >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        }
-        const float inv = rsqrtf(fmaf(ss, inv_dim, eps));
-        const float2 inv2 = make_float2(inv, inv);
+      if (rotate && 8 * c >= r0) {
+        const float4* t = reinterpret_cast<const float4*>(cs + ((8 * c - r0) >> 1));
+        const float4 t0 = t[0], t1 = t[1];
+        const float2 a[4] = {make_float2(t0.x, t0.y), make_float2(t0.z, t0.w), make_float2(t1.x, t1.y),
+                             make_float2(t1.z, t1.w)};
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[i][e] = __fmul2_rn(v[i][e], inv2);
+        for (int e = 0; e < 4; ++e)
+          v[i][e] = make_float2(fmaf(v[i][e].x, a[e].x, -v[i][e].y * a[e].y),
+                                fmaf(v[i][e].x, a[e].y, v[i][e].y * a[e].x));
       }
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const int c = sub + 32 * i;
-        if (h >= heads || c >= n8) continue;
-        if (norm && w) {
-          const float4 wa = __ldg(reinterpret_cast<const float4*>(w + 8 * c));
-          const float4 wb = __ldg(reinterpret_cast<const float4*>(w + 8 * c) + 1);
-          v[i][0] = __fmul2_rn(v[i][0], make_float2(wa.x, wa.y));
-          v[i][1] = __fmul2_rn(v[i][1], make_float2(wa.z, wa.w));
-          v[i][2] = __fmul2_rn(v[i][2], make_float2(wb.x, wb.y));
-          v[i][3] = __fmul2_rn(v[i][3], make_float2(wb.z, wb.w));
-        }
-        if (rotate && 8 * c >= r0) {
-          const float4* t = reinterpret_cast<const float4*>(cs + ((8 * c - r0) >> 1));
-          const float4 t0 = t[0], t1 = t[1];
-          const float2 a[4] = {make_float2(t0.x, t0.y), make_float2(t0.z, t0.w), make_float2(t1.x, t1.y),
-                               make_float2(t1.z, t1.w)};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[i][e] = make_float2(fmaf(v[i][e].x, a[e].x, -v[i][e].y * a[e].y),
-                                  fmaf(v[i][e].x, a[e].y, v[i][e].y * a[e].x));
-        }
-        store8(out + (size_t)h * dim + 256 * i, reinterpret_cast<const float*>(v[i]));
-      }
+      store8(out + (size_t)h * dim + 256 * i, reinterpret_cast<const float*>(v[i]));
     }
   }
 }
@@ -150,9 +143,17 @@ __global__ void __launch_bounds__(32 * kNrWarps, kLong ? 2 : 3) k_norm_rope(cons
   extern __shared__ __align__(16) float2 cs[];  // [R / 2] cos, sin
   __shared__ int s_depth;
   pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tok = blockIdx.x, b = tok / a.T_, i = tok - b * a.T_;
   const bool rotate = a.inv_freq != nullptr;
+  // a block with the whole token: its rows are on their way into L2 while the angles are found
+  if (gridDim.y == 1)
+    for (int k = 0; k < a.n_parts; ++k) {
+      const NrPart<T>& pt = a.part[k];
+      const char* x = reinterpret_cast<const char*>(pt.x + (size_t)tok * pt.x_stride);
+      for (int o = tid * 128; o < min(pt.heads * pt.dim * (int)sizeof(T), kNrAhead); o += 32 * kNrWarps * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(x + o));
+    }
   if (warp == 0) {
     int depth = i;
     if (a.parent) {
