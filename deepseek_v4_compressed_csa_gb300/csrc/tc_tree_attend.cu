@@ -27,13 +27,13 @@
 //     holds one dim of 32 heads, and its 2-byte stores straight to memory cost 7 us a node.  Transposing by stmatrix or by
 //     shuffles instead changes nothing (within 1 us for the 512 nodes below), plain 16-byte stores out of the buffer cost
 //     3 us: the next node's first tile, whose rows take 3.5K clocks to land, hides all but 2.4K of its 7.5K clocks.
-// 512 nodes of 640 keys, 512 of them selected: 100 us beside 22 for the selection; 128 nodes of 1.9K consecutive keys
+// 512 nodes of 640 keys, 512 of them selected: 100 us beside 17 for the selection; 128 nodes of 1.9K consecutive keys
 // each: 64 us, 5.7K clocks a tile of the 3.8K that its products take.
 //
 // Few nodes with long lists (kSplit): a cluster of S CTAs per node, each its run of the tiles, the parts of O^T joined
 // through distributed shared memory.  S is the largest of 8, 4, 2 whose clusters all run at once and that leaves two
 // tiles to each CTA (one tile each gains nothing over the join): 8 nodes over 8.2K rows take 48 us instead of 196, 64
-// over 2K 44 instead of 59.  The same for the nodes left over after whole rounds of the SMs saves 2 us of 122 at 512
+// over 2K 44 instead of 59.  The same for the nodes left over after whole rounds of the SMs saves 2 us of 117 at 512
 // nodes, which its bookkeeping costs again: those stay a CTA each.
 #include <atomic>
 
