@@ -524,7 +524,7 @@ csa_status csa_index_scores_tree(const csa_layer* layer, const void* iq, const v
   if (st != CSA_OK) return st;
   if (!L.has_indexer()) return CSA_ERR_UNSUPPORTED;
   if (!tree_sizes_ok(B, T) || cap < 1) return CSA_ERR_ARG;
-  if (!dev_tensor(iq) || !dev_i32(iw) || !dev_tensor(ikeys) || !dev_tensor(rows_i) || !dev_i32(scores))
+  if (!dev_tensor(iq) || !dev_tensor(iw) || !dev_tensor(ikeys) || !dev_tensor(rows_i) || !dev_i32(scores))
     return CSA_ERR_ARG;
   if (!dev_i32(parent) || !dev_i32(n_rows) || !dev_i32(pos) || !dev_i32(err)) return CSA_ERR_ARG;
   const size_t need = tree_scores_ws(L, B, T);

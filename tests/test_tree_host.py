@@ -80,6 +80,8 @@ def test_index_scores_tree_refusals(lib):
     for k in ("iq", "iw", "parent", "ikeys", "rows", "n_rows", "pos", "scores", "err"):
         assert call(**{k: None}) == B.CSA_ERR_ARG, k
         assert call(**{k: FAKE + 1}) == B.CSA_ERR_ARG, k
+    for k in ("iq", "iw", "ikeys", "rows"):  # rows that are read 16 bytes at a time
+        assert call(**{k: FAKE + 8}) == B.CSA_ERR_ARG, k
     assert call(T=65) == B.CSA_ERR_ARG and call(cap=0) == B.CSA_ERR_ARG and call(B_=0) == B.CSA_ERR_ARG
     assert call(layer=_layer(ratio=128)) == B.CSA_ERR_UNSUPPORTED
     # fp8 rows: the queries' codes and weights go into the workspace
