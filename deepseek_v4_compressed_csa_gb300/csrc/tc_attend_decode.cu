@@ -109,6 +109,12 @@ struct DecArgs {
   int32_t* err;
 };
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Reduce 64 columns over the 32 lanes of a warp; lane L returns columns 2L, 2L+1.
 template <bool kMax>
 __device__ __forceinline__ float2 reduce_scatter64(float (&v)[64]) {
@@ -393,42 +399,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
 
   if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && nr > 0) {
+    // (an elected thread, descriptors as a base plus constants: built from addresses for every product they cost ~90
+    // clocks, where the tensor pipe takes 48 and 64)
+    if (nr > 0 && elect_one()) {
       constexpr uint32_t id_qk = tc::idesc_bf16(128, 64);
       constexpr uint32_t id_pv = tc::idesc_bf16(128, 128, true, true);
-      const uint32_t p_base = tc::smem_u32(pbuf);
+      const uint64_t kd = tc::sdesc_kmajor_sw128(r_base), qd = tc::sdesc_kmajor_sw128(q_base);
+      const uint64_t vd = tc::sdesc_mnmajor_sw128(r_base, kBox, 1024);
+      const uint64_t pd = tc::sdesc_mnmajor_sw128(tc::smem_u32(pbuf), kPPart, 1024);
       do {
         if (!tc::mbar_wait(rows_full, 0)) { failed = true; break; }
         tc::fence_after_sync();
 #pragma unroll 1
         for (int half = 0; half < (nr > 128 ? 2 : 1); ++half) {
-          const uint32_t a_off = half ? 128 * 128 : 0;  // rows 128-255: sixteen 8-row atoms further
-#pragma unroll 8
-          for (int k = 0; k < 32; ++k) {
-            const uint64_t ad = tc::sdesc_kmajor_sw128(r_base + (k >> 2) * kBox + a_off + (k & 3) * 32);
-            const uint64_t bd = tc::sdesc_kmajor_sw128(q_base + (k >> 2) * kQBox + (k & 3) * 32);
-            tc::mma_bf16(tm_s + 64 * half, ad, bd, id_qk, k > 0);
-          }
+          const uint64_t hd = kd + half * (128 * 128 >> 4);  // rows 128-255: sixteen 8-row atoms further
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            tc::mma_bf16(tm_s + 64 * half, hd + (((k >> 2) * kBox + (k & 3) * 32) >> 4),
+                         qd + (((k >> 2) * kQBox + (k & 3) * 32) >> 4), id_qk, k > 0);
         }
         tc::mma_commit(s_full);
         if (!tc::mbar_wait(p_full, 0)) { failed = true; break; }
         tc::fence_after_sync();
         // O^T tile m += V^T [P_hi | P_lo]^T: one read of V serves both parts (N = 2 x 64)
         const int ksteps = (nr + 15) >> 4;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
 #pragma unroll 1
-          for (int kk = 0; kk < ksteps; ++kk) {
-            const uint64_t ad = tc::sdesc_mnmajor_sw128(r_base + 2 * m * kBox + kk * 2048, kBox, 1024);
-            const uint64_t bd = tc::sdesc_mnmajor_sw128(p_base + kk * 2048, kPPart, 1024);
-            tc::mma_bf16(tm_o + 128 * m, ad, bd, id_pv, kk > 0);
-          }
+        for (int kk = 0; kk < ksteps; ++kk) {
+          const uint64_t va = vd + kk * (2048 >> 4), pa = pd + kk * (2048 >> 4);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) tc::mma_bf16(tm_o + 128 * m, va + (2 * m * kBox >> 4), pa, id_pv, kk > 0);
         }
         tc::mma_commit(pv_done);
       } while (false);
     }
     __syncwarp();
-    failed = __shfl_sync(0xffffffffu, (int)failed, 0) != 0;
+    failed = __any_sync(0xffffffffu, failed);
   } else if (warp < kMainWarps) {
     // ------------------------------------------------------------ main warps (160 threads, one per row)
     const int row = tid;
