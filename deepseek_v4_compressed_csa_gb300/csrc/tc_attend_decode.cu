@@ -55,6 +55,7 @@ constexpr int kMain = 32 * kMainWarps;
 constexpr int kMmaWarp = kMainWarps;     // TMEM owner and MMA issuer
 constexpr int kEpiWarps = 8;             // epilogue: every warp, two per TMEM lane quarter (warps 6-7 join there)
 constexpr int kThreads = 32 * kEpiWarps;
+constexpr int kGather = kThreads - 32;   // the selected rows are copied by every warp but the issuer's
 constexpr int kTmemCols = 512;           // S^T (cols 0-127), then O^T over all 512 (hi | lo per 128-dim tile)
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -109,6 +110,15 @@ struct DecArgs {
   int32_t* err;
 };
 
+// 16-byte global -> shared copy of the lanes with `on`; src_bytes = 0 writes zeros
+__device__ __forceinline__ void cp_async16_if(bool on, uint32_t dst_smem, const void* src, uint32_t src_bytes) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "@p cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst_smem),
+      "l"(src), "r"(src_bytes), "r"((uint32_t)on)
+      : "memory");
+}
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
@@ -219,16 +229,17 @@ __device__ __forceinline__ int selected_code(const DecArgs& a, const Item& it, i
   return kRowNone;
 }
 
+// (selects, no branches: four rows' addresses are found side by side)
 template <bool kTree>
 __device__ __forceinline__ const __nv_bfloat16* code_ptr(const DecArgs& a, int code) {
-  if (code >= 0) return a.pool + (size_t)code * kAD;
+  const int x = kRowRing0 - code;
+  const __nv_bfloat16* base = code >= 0 ? a.pool : a.ring;
+  int row = code >= 0 ? code : x;
   if constexpr (kTree) {
-    const int x = kRowRing0 - code;
-    if (x >= kTreeRow) return a.trows + (size_t)(x - kTreeRow) * kAD;
-    if (x >= kTreeKv) return a.tkv + (size_t)(x - kTreeKv) * kAD;
+    base = code < 0 && x >= kTreeKv ? (x >= kTreeRow ? a.trows : a.tkv) : base;
+    row -= code < 0 && x >= kTreeKv ? (x >= kTreeRow ? kTreeRow : kTreeKv) : 0;
   }
-  if (code <= kRowRing0) return a.ring + (size_t)(kRowRing0 - code) * kAD;
-  return nullptr;
+  return code >= 0 || code <= kRowRing0 ? base + (size_t)row * kAD : nullptr;
 }
 
 __device__ __forceinline__ void rope8(uint4& raw, int c, const float* rcos, const float* rsin) {
@@ -281,21 +292,30 @@ __device__ __forceinline__ void write_p(uint8_t* pbuf, int row, const float (&sv
 }
 
 // Copy tile rows [r0, r1) from their codes (cp.async, 2 x 512 contiguous bytes per warp instruction; rows spread
-// over the main warps); an empty row is zero-filled and the new token is skipped (roped separately).
+// over `warps` warps); an empty row is zero-filled and the new token is skipped (roped separately).
 template <bool kTree>
-__device__ __forceinline__ void gather_rows(const DecArgs& a, const int* rowc, uint32_t r_base, int r0, int r1) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll 4
-  for (int r = r0 + warp; r < r1; r += kMainWarps) {
-    const int code = rowc[r];
-    if (code == kRowNew) continue;
-    const __nv_bfloat16* src = code_ptr<kTree>(a, code);
+__device__ __forceinline__ void gather_rows(const DecArgs& a, const int* rowc, uint32_t r_base, int r0, int r1,
+                                            int warp, int warps) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kU = 4;  // rows whose addresses are found together
+  for (int r = r0 + warp; r < r1; r += kU * warps) {
+    const __nv_bfloat16* src[kU];
+    bool on[kU];
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const int ch = lane + 32 * hh;
-      const uint32_t dst = r_base + (ch >> 3) * kBox + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-      tc::cp_async16(dst, src ? static_cast<const void*>(src + ch * 8) : static_cast<const void*>(a.pool),
-                     src ? 16u : 0u);
+    for (int u = 0; u < kU; ++u) {
+      const int ru = r + u * warps, code = ru < r1 ? rowc[ru] : kRowNew;
+      on[u] = code != kRowNew;
+      src[u] = code_ptr<kTree>(a, code);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int ru = r + u * warps;
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int ch = lane + 32 * hh;
+        cp_async16_if(on[u], r_base + (ch >> 3) * kBox + ru * 128 + (((ch & 7) ^ (ru & 7)) << 4),
+                      src[u] ? src[u] + ch * 8 : a.pool, src[u] ? 16u : 0u);
+      }
     }
   }
 }
@@ -326,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    tc::mbar_init(rows_full, kMain);
+    tc::mbar_init(rows_full, kGather);
     tc::mbar_init(s_full, 1);
     tc::mbar_init(p_full, kMain);
     tc::mbar_init(pv_done, 1);
@@ -356,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
       rsin[tid] = sn;
     }
     tc::named_bar(1, kMain);
-    gather_rows<kTree>(a, rowc, r_base, 0, it.nw);
+    gather_rows<kTree>(a, rowc, r_base, 0, it.nw, warp, kMainWarps);
     // the new token (the window's last): RoPE at p, into the tile and into its ring slot (the slot belongs to the
     // token leaving the window, which no CTA reads)
     const int cur_row = (!kTree && !a.kv_in_ring && it.nw > 0 && it.w_begin + it.nw == it.nwin) ? it.nw - 1 : -1;
@@ -434,7 +454,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
     }
     __syncwarp();
     failed = __any_sync(0xffffffffu, failed);
-  } else if (warp < kMainWarps) {
+  } else if (warp > kMmaWarp) {
+    // ------------------------------------------------------------ the last warps share the selected rows' copies
+    tc::named_bar(3, kGather);
+    gather_rows<kTree>(a, rowc, r_base, it.nw, kCR, warp - 1, kGather / 32);
+    tc::cp_async_wait_all();
+    tc::fence_proxy_async_smem();
+    tc::mbar_arrive(rows_full);
+  } else {
     // ------------------------------------------------------------ main warps (160 threads, one per row)
     const int row = tid;
     // ---- the selection share: codes of rows nw .. 159 (empty past nr), then their copies
@@ -443,8 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
       const int j = (a.sel && row < nr) ? a.sel[(size_t)it.q * a.topk + k] : 0;
       rowc[row] = row < nr ? selected_code<kTree>(a, it, k, j) : kRowNone;
     }
-    tc::named_bar(1, kMain);
-    gather_rows<kTree>(a, rowc, r_base, it.nw, kCR);
+    tc::named_bar(3, kGather);
+    gather_rows<kTree>(a, rowc, r_base, it.nw, kCR, warp, kGather / 32);
     tc::cp_async_wait_all();
     tc::fence_proxy_async_smem();
     tc::fence_before_sync();
