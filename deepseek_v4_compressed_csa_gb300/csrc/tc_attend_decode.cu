@@ -19,7 +19,8 @@
 // memory once.
 //   QK       S^T = K Q^T twice, M = 128 (TMEM lanes), N = 64 heads, K = 512:
 //            rows 0-127, and rows 128-255 of which lanes 0-31 (rows 128-159) are
-//            used (the rest read neighbouring, initialised shared memory);
+//            used (the rest, and rows past the chunk's end, give scores that no one
+//            reads);
 //   softmax  five warps, thread = row (warp 4 reads lanes 0-31 of the second
 //            product); per-head column max and sum by a warp reduce-scatter and a
 //            5-warp combine;
@@ -321,8 +322,9 @@ __device__ __forceinline__ void gather_rows(const DecArgs& a, const int* rowc, u
 }
 
 // S > 1 writes (m, l, acc) partials for the merge kernel; S == 1 finalises directly.  kTree: the nodes of trees
-// (csa_attend_tree); S is 1 or a cluster, and the output is rounded once, after its rotation.
-template <bool kTree>
+// (csa_attend_tree); S is 1 or a cluster, and the output is rounded once, after its rotation.  kSp: the most splits of a
+// cluster, 4 or 8.
+template <bool kTree, int kSp>
 __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
   const uint32_t tm_s = tmem;  // S^T: rows 0-127 in cols 0-63, rows 128-255 in cols 64-127
   const uint32_t tm_o = tmem;  // O^T tile m: cols 128m + (0-63: P_hi part, 64-127: P_lo part); overwrites S^T
   const bool live = item_selection<kTree>(a, it);
-  const int nr = it.nw + it.ns;
+  const int nr = it.nw + it.ns, nz = (nr + 15) & ~15;  // rows, and those that the PV product reads (the last ones zero)
   bool failed = false;
 
   if (warp == kMmaWarp) {
@@ -457,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
   } else if (warp > kMmaWarp) {
     // ------------------------------------------------------------ the last warps share the selected rows' copies
     tc::named_bar(3, kGather);
-    gather_rows<kTree>(a, rowc, r_base, it.nw, kCR, warp - 1, kGather / 32);
+    gather_rows<kTree>(a, rowc, r_base, it.nw, nz, warp - 1, kGather / 32);
     tc::cp_async_wait_all();
     tc::fence_proxy_async_smem();
     tc::mbar_arrive(rows_full);
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
       rowc[row] = row < nr ? selected_code<kTree>(a, it, k, j) : kRowNone;
     }
     tc::named_bar(3, kGather);
-    gather_rows<kTree>(a, rowc, r_base, it.nw, kCR, warp, kGather / 32);
+    gather_rows<kTree>(a, rowc, r_base, it.nw, nz, warp, kGather / 32);
     tc::cp_async_wait_all();
     tc::fence_proxy_async_smem();
     tc::fence_before_sync();
@@ -593,10 +595,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
     if (tid < 64) {
       // M = max(z, m_s); f_s = e^{m_s - M} (0 for a split without rows); Z = e^{z - M} + sum_s l_s f_s
       const float z = a.sink[tid];
-      float ms[4], ls[4];
+      float ms[kSp], ls[kSp];
       float M = z;
 #pragma unroll
-      for (int sp = 0; sp < 4; ++sp) {
+      for (int sp = 0; sp < kSp; ++sp) {
         if (sp < S) {
           const float2 v = tc::ld_cluster_f2(tc::cluster_map(mls + 2 * tid, sp));
           ms[sp] = v.x;
@@ -606,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
       }
       float zs = 0.f;
 #pragma unroll
-      for (int sp = 0; sp < 4; ++sp) {
+      for (int sp = 0; sp < kSp; ++sp) {
         if (sp < S) {
           const float f = ms[sp] == -INFINITY ? 0.f : expf(ms[sp] - M);
           tab[tid * (S + 1) + sp] = f;
@@ -617,26 +619,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
     }
     __syncthreads();
     // warp w: heads 8w .. 8w + 7, four at a time with every split's values requested together (one remote round
-    // trip per four heads; one per head measured slower, and so did a remote store of every value, and fetching
+    // trip per four heads; one per head measured slower, and so did a remote store of every value, a bulk copy of every
+    // rank's slice (9.1K clocks for the 96 KB of four splits instead of 8.2K), and fetching
     // the splits' statistics in the same round); lane: 4-dim columns of this rank's slice.  A split's values are
     // read whatever its weight (a split without rows left zeros) and added only when the weight is not zero.
-    const int r = it.s, ncol = kAD / 4 / S;
-    for (int c = lane; c < ncol; c += 32) {
+    // (eight splits: a slice is half a warp wide, each half takes two of the four heads)
+    constexpr int kHeads = 16 / kSp;  // of the four, a lane's
+    const int r = it.s, ncol = kAD / 4 / S, group = kSp == 8 ? lane >> 4 : 0;
+    for (int c = kSp == 8 ? lane & 15 : lane; c < ncol; c += 32) {
       const int d = r * (kAD / S) + 4 * c;
 #pragma unroll 1
-      for (int h0 = warp * 8; h0 < warp * 8 + 8; h0 += 4) {
-        float4 x[4][4];
+      for (int h0 = warp * 8 + group * kHeads; h0 < warp * 8 + 8; h0 += 4) {
+        float4 x[kHeads][kSp];
 #pragma unroll
-        for (int hh = 0; hh < 4; ++hh)
+        for (int hh = 0; hh < kHeads; ++hh)
 #pragma unroll
-          for (int sp = 0; sp < 4; ++sp)
+          for (int sp = 0; sp < kSp; ++sp)
             if (sp < S) x[hh][sp] = tc::ld_cluster_f4(tc::cluster_map(accs + (h0 + hh) * kAD + d, sp));
 #pragma unroll
-        for (int hh = 0; hh < 4; ++hh) {
+        for (int hh = 0; hh < kHeads; ++hh) {
         const int h = h0 + hh;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int sp = 0; sp < 4; ++sp) {
+        for (int sp = 0; sp < kSp; ++sp) {
           const float f = sp < S ? tab[h * (S + 1) + sp] : 0.f;
           if (f != 0.f) {
             v[0] = fmaf(x[hh][sp].x, f, v[0]);
@@ -751,7 +756,7 @@ bool tc_attend_decode_cluster(int S) {
   static int known[5] = {-1, -1, -1, -1, -1};
   if (S != 2 && S != 4) return false;
   if (known[S] < 0) {
-    cudaFuncSetAttribute(k_tc_attend_decode<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cudaFuncSetAttribute(k_tc_attend_decode<false, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(S);
     cfg.blockDim = dim3(kThreads);
@@ -764,7 +769,7 @@ bool tc_attend_decode_cluster(int S) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, k_tc_attend_decode<false>, &cfg);
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, k_tc_attend_decode<false, 4>, &cfg);
     if (e != cudaSuccess) cudaGetLastError();  // leave no sticky error behind
     known[S] = (e == cudaSuccess && n > 0) ? 1 : 0;
   }
@@ -790,27 +795,28 @@ cudaError_t launch_tc_attend_decode(const Dims& L, const void* q, const void* po
   a.part_ml = part_ml; a.part_acc = part_acc;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.err = err;
-  cudaFuncSetAttribute(k_tc_attend_decode<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaFuncSetAttribute(k_tc_attend_decode<false, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (cluster) {
     if (S != 2 && S != 4) return cudaErrorInvalidValue;
-    const cudaError_t e = launch_pdl_cluster(k_tc_attend_decode<false>, dim3(Q * S), dim3(kThreads), kSmem, s, S, a);
+    const cudaError_t e = launch_pdl_cluster(k_tc_attend_decode<false, 4>, dim3(Q * S), dim3(kThreads), kSmem, s, S, a);
     if (e != cudaSuccess) return e;
   } else {
-    CSA_LAUNCH(k_tc_attend_decode<false>, dim3(Q * S), dim3(kThreads), kSmem, s, a);
+    CSA_LAUNCH(k_tc_attend_decode<false, 4>, dim3(Q * S), dim3(kThreads), kSmem, s, a);
   }
   return cudaGetLastError();
 }
 
-// A tree's nodes (csa_attend_tree): B * T queries of S splits each (S 1, or 2 or 4 as a cluster).
+// A tree's nodes (csa_attend_tree): B * T queries of S splits each (S 1, or 2, 4 or 8 as a cluster).
 int tc_attend_tree_split_max(int S) {
   constexpr int kDevices = 64;
-  static std::atomic<int> known[kDevices][5];  // 0: not asked yet (a property of the device: asked once), else 1 + n
+  static std::atomic<int> known[kDevices][9];  // 0: not asked yet (a property of the device: asked once), else 1 + n
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
   int n = known[dev][S].load(std::memory_order_relaxed) - 1;
   if (n < 0) {
-    cudaFuncSetAttribute(k_tc_attend_decode<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    n = max_clusters(k_tc_attend_decode<true>, kThreads, kSmem, S);
+    const auto kernel = S > 4 ? k_tc_attend_decode<true, 8> : k_tc_attend_decode<true, 4>;
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    n = max_clusters(kernel, kThreads, kSmem, S);
     known[dev][S].store(n + 1, std::memory_order_relaxed);
   }
   return n;
@@ -833,12 +839,13 @@ cudaError_t launch_tc_attend_tree_split(const Dims& L, const TreeAttend& t, cons
   a.scale2 = L.scale * 1.4426950408889634f;
   a.out = static_cast<__nv_bfloat16*>(t.out);
   a.err = err;
-  cudaFuncSetAttribute(k_tc_attend_decode<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const auto kernel = S > 4 ? k_tc_attend_decode<true, 8> : k_tc_attend_decode<true, 4>;
+  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (S > 1) {
-    const cudaError_t e = launch_pdl_cluster(k_tc_attend_decode<true>, dim3(Q * S), dim3(kThreads), kSmem, s, S, a);
+    const cudaError_t e = launch_pdl_cluster(kernel, dim3(Q * S), dim3(kThreads), kSmem, s, S, a);
     if (e != cudaSuccess) return e;
   } else {
-    CSA_LAUNCH(k_tc_attend_decode<true>, dim3(Q), dim3(kThreads), kSmem, s, a);
+    CSA_LAUNCH(kernel, dim3(Q), dim3(kThreads), kSmem, s, a);
   }
   return cudaGetLastError();
 }

@@ -496,6 +496,8 @@ EDGE_CASES = {
     "flash_left_over": ("flash", [TR.bushy(16, s) for s in range(10)], [2100 + 91 * s for s in range(9)] + [3], True),
     "flash_r128_left_over": ("flash_r128", [TR.bushy(19, s) for s in range(9)], [60000 + 9091 * s for s in range(8)] + [99], False),
     "flash_few": ("flash", [TR.bushy(5), TR.chain(7)], [4097, 2301], True),
+    "flash_few_4_splits": ("flash", [TR.bushy(9), TR.chain(8)], [3001, 2051], True),
+    "flash_few_short": ("flash", [TR.bushy(7), TR.star(8)], [600, 3], True),
     "flash_many": ("flash", [TR.bushy(16, s) for s in range(11)], [2100 + 91 * s for s in range(11)], True),
     "flash_many_rows": ("flash_r128", [TR.bushy(16, s) for s in range(11)], [9000 + 1291 * s for s in range(11)], False),
     "flash_topk_odd": ("flash_topk", [TR.bushy(15, s) for s in range(12)], [900 + 77 * s for s in range(12)], True),
