@@ -71,6 +71,7 @@ NR_CASES = {
     "flash_one_token": ("flash", 1, 1, None, 32767),
     "flash_batch_tree": ("flash", 3, 16, "bushy", 100001),
     "flash_chunk": ("flash", 1, 300, None, 5),
+    "flash_long_chunk": ("flash", 1, 1400, None, 5),  # a block per token
     "tiny_f32_tree": ("tiny_f32", 4, 7, "bushy", 999),
     "odd_dims_tree": ("odd_bf16", 2, 64, "bushy", 0),
     "odd_dims_chain64": ("odd_bf16", 1, 64, "chain", 262143),
@@ -110,6 +111,29 @@ def test_norm_rope_against_float64(case, rotate):
                 ref = TR.norm_rope(x[b, i], wt, norm, cfg.rms_eps, int(pos[b]) + len(paths[i]) - 1, f if rotate else None)
                 pair = np.repeat(np.hypot(ref[..., ::2], ref[..., 1::2]), 2, axis=-1)
                 assert (np.abs(g - ref) <= half_step(np.abs(ref) + 2.0 ** -18 * pair, cfg.dtype) + 2.0 ** -18 * pair).all()
+
+
+@pytest.mark.parametrize("name", ["flash", "tiny_f32"])
+@pytest.mark.parametrize("T", [3, 1300])
+def test_norm_rope_long_and_short_rows(name, T):
+    """Rows of up to 1024 values (four chunks a lane) next to short ones, in one call."""
+    cfg = LAYERS[name]
+    f = f64(csa_synth.inv_freq(cfg)).astype(np.float32)
+    short = cfg.R + 8
+    xs = [rnd(cfg, (2, T, 3, 1024), 7, scale=3.0), rnd(cfg, (2, T, 520), 8), rnd(cfg, (2, T, 5, short), 9)]
+    ws = [None, rnd(cfg, (520,), 10, dtype=torch.float32), rnd(cfg, (short,), 11, dtype=torch.float32)]
+    pos = torch.tensor([70000, 0], dtype=torch.int32, device="cuda")
+    err = err_word()
+    got = csa.norm_rope(G.lib_layer(cfg), xs, pos, freqs(cfg), weights=ws, err=err)
+    assert err.item() == 0
+    for x, w, o in zip(xs, ws, got):
+        x4, o4 = (x, o) if x.dim() == 4 else (x[:, :, None], o[:, :, None])
+        for b in range(2):
+            for i in (0, 1, T - 1):
+                ref = TR.norm_rope(x4[b, i], w, True, cfg.rms_eps, int(pos[b]) + i, f)
+                pair = np.repeat(np.hypot(ref[..., ::2], ref[..., 1::2]), 2, axis=-1)
+                tol = 2.0 ** -18 * pair
+                assert (np.abs(f64(o4[b, i]) - ref) <= half_step(np.abs(ref) + tol, cfg.dtype) + tol).all()
 
 
 def test_norm_rope_in_place_and_zero_rows():
@@ -487,14 +511,14 @@ def check_tree_outputs(cfg, layer, trees, pos, q, kv, sink, window, pool, rows, 
 
 
 EDGE_CASES = {
-    # layer, trees, positions, selection: split kernel (few nodes), many nodes, portable kernel; nodes whose keys a
-    # cluster of CTAs shares: few nodes with all rows wanted, some of
-    # them with fewer tiles than CTAs; more nodes than SMs
+    # layer, trees, positions, selection: nodes whose keys a cluster of CTAs shares (all rows wanted; some nodes with
+    # fewer tiles than CTAs), more nodes than SMs, splits of a tile (few nodes), odd sizes, the portable kernel
     "flash_rows_8_ways": ("flash", [TR.bushy(3), TR.star(4)], [9001, 5], False),
     "flash_rows_4_ways": ("flash", [TR.bushy(10), TR.chain(14)], [3300, 40], False),
     "flash_rows_2_ways": ("flash", [TR.bushy(20, s) for s in range(3)], [2004, 700, 1], False),
     "flash_left_over": ("flash", [TR.bushy(16, s) for s in range(10)], [2100 + 91 * s for s in range(9)] + [3], True),
-    "flash_r128_left_over": ("flash_r128", [TR.bushy(19, s) for s in range(9)], [60000 + 9091 * s for s in range(8)] + [99], False),
+    "flash_r128_left_over": ("flash_r128", [TR.bushy(19, s) for s in range(9)],
+                             [60000 + 9091 * s for s in range(8)] + [99], False),
     "flash_few": ("flash", [TR.bushy(5), TR.chain(7)], [4097, 2301], True),
     "flash_few_4_splits": ("flash", [TR.bushy(9), TR.chain(8)], [3001, 2051], True),
     "flash_few_short": ("flash", [TR.bushy(7), TR.star(8)], [600, 3], True),
@@ -503,11 +527,18 @@ EDGE_CASES = {
     "flash_topk_odd": ("flash_topk", [TR.bushy(15, s) for s in range(12)], [900 + 77 * s for s in range(12)], True),
     "flash_topk_odd_few": ("flash_topk", [TR.bushy(6)], [1403], True),
     "flash_topk_1": ("flash_topk1", [TR.bushy(15, s) for s in range(12)], [77 * s for s in range(12)], True),
+    "flash_topk_2048_few": ("flash_topk2048", [TR.bushy(6), TR.chain(5)], [12001, 8100], True),
+    "flash_topk_2048_many": ("flash_topk2048", [TR.bushy(16, s) for s in range(10)],
+                             [7000 + 997 * s for s in range(10)], True),
+    "flash_wide_window_few": ("flash_wide", [TR.bushy(6), TR.chain(8)], [3001, 650], True),
+    "flash_wide_window_many": ("flash_wide", [TR.bushy(16, s) for s in range(10)],
+                               [300 + 397 * s for s in range(10)], True),
     "flash_window": ("flash_window", [TR.bushy(9, s) for s in range(18)], [801 + 13 * s for s in range(18)], True),
     "tiny_f32": ("tiny_f32", [TR.bushy(9), TR.chain(9)], [150, 70], True),
 }
 EDGE_LAYERS = {**LAYERS, "flash_topk": FLASH.replace(cid=65, topk=203), "flash_topk1": FLASH.replace(cid=66, topk=1),
-               "flash_window": FLASH.replace(cid=67, W=77, topk=131, rollback=19)}
+               "flash_window": FLASH.replace(cid=67, W=77, topk=131, rollback=19),
+               "flash_topk2048": FLASH.replace(cid=68, topk=2048), "flash_wide": FLASH.replace(cid=69, W=700, topk=300)}
 
 
 @pytest.mark.parametrize("case", list(EDGE_CASES))
@@ -585,6 +616,38 @@ def test_attend_tree_with_unused_sequences_and_long_pools():
                               freqs(cfg), out, sel_out=sel)
         assert err.item() == 0
         check_tree_outputs(cfg, layer, trees, pos, q, kv, sink, window, pool, rows, scores, out, sel, invf)
+
+
+@pytest.mark.parametrize("T", [2, 40])
+def test_attend_tree_rows_past_32_bit_offsets(T):
+    """Two pools of 2.2 million rows (2.25e9 values): a few nodes (split kernel) and many (a CTA each)."""
+    cfg, B, cap = FLASH, 2, 2200000
+    layer, invf = oracle_layer(cfg), f64(csa_synth.inv_freq(cfg)).astype(np.float32)
+    trees, pos = [TR.chain(T), TR.bushy(T)], [4 * cap - 4 * T - 3, 4 * cap - 4 * T - 2]
+    g = torch.Generator(device="cuda").manual_seed(9)
+    n = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda").normal_(generator=g)  # noqa: E731
+    pool, q, kv, window, rows = n(B, cap, 512), n(B, T, 64, 512), n(B, T, 512), n(B, 128, 512), n(B, T, 512)
+    scores = torch.empty(B, T, cap + T, device="cuda").normal_(generator=g)
+    sink = rnd(cfg, (64,), 160, dtype=torch.float32)
+    p = torch.tensor(pos, dtype=torch.int32, device="cuda")
+    out, sel = torch.empty_like(q), torch.empty(B, T, 512, dtype=torch.int32, device="cuda")
+    err = csa.attend_tree(G.lib_layer(cfg), q, kv, sink, window, pool, rows, scores, parents(trees, T), p // 4, p,
+                          freqs(cfg), out, sel_out=sel)
+    assert err.item() == 0
+    for b in range(B):
+        for i in (0, T - 1):
+            path = TR.paths(trees[b])[i]
+            seen = torch.full((cap + T,), float("-inf"), device="cuda")
+            cols = TR.columns(layer, path, pos[b], T)
+            cols = torch.tensor(cols[pos[b] // 4:], device="cuda", dtype=torch.long)  # the path's rows
+            seen[:pos[b] // 4] = scores[b, i, :pos[b] // 4]
+            seen[cols] = scores[b, i, cols]
+            top = seen.topk(cfg.topk).indices.sort().values
+            assert torch.equal(sel[b, i].long(), top) and top.max() > cap // 2
+            ref = TR.output(layer, q[b, i], kv[b], f64(sink), window[b], pool[b], rows[b], top.tolist(), path, pos[b],
+                            invf)
+            tol = 2.0 ** -11 * np.abs(ref).max(-1, keepdims=True)
+            assert (np.abs(f64(out[b, i]) - ref) <= half_step(np.abs(ref) + tol, cfg.dtype) + tol).all(), (b, i)
 
 
 def test_attend_tree_of_a_chain_is_a_verify_block():
