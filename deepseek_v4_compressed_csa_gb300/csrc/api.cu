@@ -100,6 +100,7 @@ size_t ws_prefill(const Dims& L, int T, int cap) {
 }
 
 // A batch of trees: at most 64 nodes each (a path is a 64-bit mask), and grids of B x T queries.
+constexpr int kTreeCapMax = INT32_MAX - 256;  // columns, cap + T of them, are ints
 bool tree_sizes_ok(int B, int T) {
   return B >= 1 && B <= 65535 && T >= 1 && T <= 64 && (long long)B * T <= (1 << 18);
 }
@@ -523,7 +524,7 @@ csa_status csa_index_scores_tree(const csa_layer* layer, const void* iq, const v
   csa_status st = make_dims(layer, &L);
   if (st != CSA_OK) return st;
   if (!L.has_indexer()) return CSA_ERR_UNSUPPORTED;
-  if (!tree_sizes_ok(B, T) || cap < 1) return CSA_ERR_ARG;
+  if (!tree_sizes_ok(B, T) || cap < 1 || cap > kTreeCapMax) return CSA_ERR_ARG;
   if (!dev_tensor(iq) || !dev_tensor(iw) || !dev_tensor(ikeys) || !dev_tensor(rows_i) || !dev_i32(scores))
     return CSA_ERR_ARG;
   if (!dev_i32(parent) || !dev_i32(n_rows) || !dev_i32(pos) || !dev_i32(err)) return CSA_ERR_ARG;
@@ -540,7 +541,7 @@ csa_status csa_attend_tree(const csa_layer* layer, const void* q, const void* kv
   Dims L;
   csa_status st = make_dims(layer, &L);
   if (st != CSA_OK) return st;
-  if (!tree_sizes_ok(B, T) || cap < 1) return CSA_ERR_ARG;
+  if (!tree_sizes_ok(B, T) || cap < 1 || cap > kTreeCapMax) return CSA_ERR_ARG;
   if (!dev_tensor(q) || !dev_tensor(kv) || !dev_i32(sink) || !dev_tensor(window) || !dev_tensor(pool) ||
       !dev_tensor(rows_a) || !dev_tensor(inv_freq) || !dev_tensor(out))
     return CSA_ERR_ARG;

@@ -826,8 +826,8 @@ cudaError_t launch_tc_attend_tree(const Dims& L, const TreeAttend& t, const int3
   for (a.S = kMaxSplit; a.S > 1; a.S /= 2)
     if (tiles >= 2 * a.S && a.Q <= clusters(a.S)) {
       cudaFuncSetAttribute(k_tc_tree_attend<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-      const cudaError_t e = launch_pdl_cluster(k_tc_tree_attend<true>, dim3(a.Q * a.S), dim3(kThreads), kSmem, s, a.S, tq,
-                                               to, tp, tr, a);
+      const cudaError_t e = launch_pdl_cluster(k_tc_tree_attend<true>, dim3(a.Q * a.S), dim3(kThreads), kSmem, s, a.S,
+                                               tq, to, tp, tr, a);
       return e != cudaSuccess ? e : cudaGetLastError();
     }
   cudaFuncSetAttribute(k_tc_tree_attend<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);

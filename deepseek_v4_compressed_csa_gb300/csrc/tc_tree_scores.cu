@@ -334,7 +334,8 @@ __global__ void __launch_bounds__(TsCfg<kFp8>::kThreads, 1)
         const int col = tree ? n + row : t * kRows + row;
         const bool in = tree ? row < a.T : col < n;
         float scale = a.wscale;
-        if constexpr (kFp8) {  // (the tile has landed: its products have retired; this wait makes its bytes visible here)
+        // (the tile has landed: its products have retired; this wait makes its bytes visible here)
+        if constexpr (kFp8) {
           if (!failed) failed = __any_sync(0xffffffffu, !tc::mbar_wait(&full[stage], phase));
           scale *= *reinterpret_cast<const float*>(smem + C::kOffScale + (stage * kRows + row) * 16);
           __syncwarp();
@@ -365,7 +366,8 @@ __global__ void __launch_bounds__(TsCfg<kFp8>::kThreads, 1)
                 w01 = make_float2(ww.x, ww.y);
                 w23 = make_float2(ww.z, ww.w);
               } else {
-                // (the packed weights change as far as the compiler knows: unpacked ahead of the loop they would not fit)
+                // (the packed weights change as far as the compiler knows: unpacked ahead of the loop they would not
+                // fit)
                 uint32_t &w0 = wt[u][(h0 + k) / 2], &w1 = wt[u][(h0 + k) / 2 + 1];
                 asm volatile("" : "+r"(w0), "+r"(w1));
                 w01 = make_float2(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u));
@@ -451,7 +453,8 @@ cudaError_t launch_tc_tree_scores(const Dims& L, const void* iq, const void* iw,
     CSA_LAUNCH(k_tree_quant_iq, dim3((unsigned)((heads + 7) / 8)), dim3(256), 0, s,
                static_cast<const __nv_bfloat16*>(iq), a.iw, (int)heads, q8, w8);
     cudaFuncSetAttribute(k_tc_tree_scores<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, TsCfg<true>::kSmem);
-    CSA_LAUNCH(k_tc_tree_scores<true>, grid, dim3(TsCfg<true>::kThreads), TsCfg<true>::kSmem, s, tk, tr, tq, tks, trs, a);
+    CSA_LAUNCH(k_tc_tree_scores<true>, grid, dim3(TsCfg<true>::kThreads), TsCfg<true>::kSmem, s, tk, tr, tq, tks, trs,
+               a);
     return cudaGetLastError();
   }
   if (!make_tmap_2d_bf16(&tk, ikeys, (uint64_t)B * cap, 128, 256, kRows) ||
@@ -459,7 +462,8 @@ cudaError_t launch_tc_tree_scores(const Dims& L, const void* iq, const void* iw,
       !make_tmap_2d_bf16(&tq, iq, heads, 128, 256, kN))
     return cudaErrorInvalidValue;
   cudaFuncSetAttribute(k_tc_tree_scores<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, TsCfg<false>::kSmem);
-  CSA_LAUNCH(k_tc_tree_scores<false>, grid, dim3(TsCfg<false>::kThreads), TsCfg<false>::kSmem, s, tk, tr, tq, tk, tr, a);
+  CSA_LAUNCH(k_tc_tree_scores<false>, grid, dim3(TsCfg<false>::kThreads), TsCfg<false>::kSmem, s, tk, tr, tq, tk, tr,
+             a);
   return cudaGetLastError();
 }
 

@@ -498,7 +498,8 @@ csa_status csa_compress_tree(const csa_layer* layer, const csa_compressor* comp_
 
 /* csa_index_scores_tree: the nodes' index scores, csa_index_topk's formula on
  * rotated queries iq [B, T, Hi, Di] (csa_norm_rope without a norm), iw [B, T, Hi]:
- *   scores [B, T, cap + T] fp32; columns c < n_rows[b]: committed row c;
+ *   scores [B, T, cap + T] fp32 (cap <= 2^31 - 257, here and in csa_attend_tree);
+ *   columns c < n_rows[b]: committed row c;
  *   columns n_rows[b] + a, a < T: the row of node a for the nodes a of i's path
  *   that complete one, -infinity for the others; later columns are not touched.
  * ikeys [B, cap, Di], rows_i [B, T, Di]; with index_fp8 both are fp8 rows, and the

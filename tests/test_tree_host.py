@@ -83,6 +83,7 @@ def test_index_scores_tree_refusals(lib):
     for k in ("iq", "iw", "ikeys", "rows"):  # rows that are read 16 bytes at a time
         assert call(**{k: FAKE + 8}) == B.CSA_ERR_ARG, k
     assert call(T=65) == B.CSA_ERR_ARG and call(cap=0) == B.CSA_ERR_ARG and call(B_=0) == B.CSA_ERR_ARG
+    assert call(cap=2 ** 31 - 256) == B.CSA_ERR_ARG
     assert call(layer=_layer(ratio=128)) == B.CSA_ERR_UNSUPPORTED
     # fp8 rows: the queries' codes and weights go into the workspace
     fp8, need = _layer(index_fp8=1), 2 * 8 * 64 * 132
@@ -107,6 +108,7 @@ def test_attend_tree_refusals(lib):
         assert call(**{k: None}) == B.CSA_ERR_ARG, k
         assert call(**{k: FAKE + 2}) == B.CSA_ERR_ARG, k
     assert call(T=65) == B.CSA_ERR_ARG and call(cap=0) == B.CSA_ERR_ARG
+    assert call(cap=2 ** 31 - 256) == B.CSA_ERR_ARG
     assert call(layer=_layer(ratio=128)) == B.CSA_ERR_ARG          # scores on a layer without an indexer
     assert call(scores=None, sel=FAKE) == B.CSA_ERR_ARG            # a selection without scores
     assert call(sel=FAKE + 2) == B.CSA_ERR_ARG
