@@ -722,8 +722,8 @@ static cudaError_t index_scores_tree_t(const Dims& L, const void* iq, const void
                                        cudaStream_t s) {
   const float wscale = (float)(1.0 / sqrt((double)L.Di * (double)L.Hi));
   CSA_LAUNCH(k_tree_scores<T>, dim3(B * T_, min(1024, (cap + T_ + 63) / 64)), dim3(256),
-             8 * (size_t)L.Di * sizeof(float), s, static_cast<const T*>(iq), static_cast<const T*>(iw), L.Hi, L.Di, static_cast<const T*>(ikeys), cap,
-             static_cast<const T*>(rows), parent, T_, n_rows, pos, L.ratio, wscale, scores, err);
+             8 * (size_t)L.Di * sizeof(float), s, static_cast<const T*>(iq), static_cast<const T*>(iw), L.Hi, L.Di,
+             static_cast<const T*>(ikeys), cap, static_cast<const T*>(rows), parent, T_, n_rows, pos, L.ratio, wscale, scores, err);
   return cudaGetLastError();
 }
 
