@@ -111,21 +111,6 @@ struct DecArgs {
   int32_t* err;
 };
 
-// 16-byte global -> shared copy of the lanes with `on`; src_bytes = 0 writes zeros
-__device__ __forceinline__ void cp_async16_if(bool on, uint32_t dst_smem, const void* src, uint32_t src_bytes) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %3, 0;\n\t"
-      "@p cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst_smem),
-      "l"(src), "r"(src_bytes), "r"((uint32_t)on)
-      : "memory");
-}
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
-
 // Reduce 64 columns over the 32 lanes of a warp; lane L returns columns 2L, 2L+1.
 template <bool kMax>
 __device__ __forceinline__ float2 reduce_scatter64(float (&v)[64]) {
@@ -314,7 +299,7 @@ __device__ __forceinline__ void gather_rows(const DecArgs& a, const int* rowc, u
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const int ch = lane + 32 * hh;
-        cp_async16_if(on[u], r_base + (ch >> 3) * kBox + ru * 128 + (((ch & 7) ^ (ru & 7)) << 4),
+        tc::cp_async16_if(on[u], r_base + (ch >> 3) * kBox + ru * 128 + (((ch & 7) ^ (ru & 7)) << 4),
                       src[u] ? src[u] + ch * 8 : a.pool, src[u] ? 16u : 0u);
       }
     }
@@ -423,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tc_attend_decode(DecArgs a) {
     // ------------------------------------------------------------ MMA issuer
     // (an elected thread, descriptors as a base plus constants: built from addresses for every product they cost ~90
     // clocks, where the tensor pipe takes 48 and 64)
-    if (nr > 0 && elect_one()) {
+    if (nr > 0 && tc::elect_one()) {
       constexpr uint32_t id_qk = tc::idesc_bf16(128, 64);
       constexpr uint32_t id_pv = tc::idesc_bf16(128, 128, true, true);
       const uint64_t kd = tc::sdesc_kmajor_sw128(r_base), qd = tc::sdesc_kmajor_sw128(q_base);

@@ -117,25 +117,11 @@ __device__ __forceinline__ void key_range(const TaArgs& a, int keys, int& k0, in
   }
 }
 
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
 // 2^x by the hardware approximation (relative error ~2^-22; results below 2^-126 flush to zero)
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-// 16-byte global -> shared copy of the lanes with `on`; src_bytes = 0 writes zeros
-__device__ __forceinline__ void cp_async16_if(bool on, uint32_t dst_smem, const void* src, uint32_t src_bytes) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %3, 0;\n\t"
-      "@p cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst_smem),
-      "l"(src), "r"(src_bytes), "r"((uint32_t)on)
-      : "memory");
 }
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
@@ -303,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    if (elect_one()) {
+    if (tc::elect_one()) {
       constexpr uint32_t id_qk = tc::idesc_bf16(128, 64);
       constexpr uint32_t id_pv2 = tc::idesc_bf16(128, 128, true, true);
       constexpr uint32_t id_pv1 = tc::idesc_bf16(128, 64, true, true);
@@ -507,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < kInstr; ++k) {
           const int i = w + kLoadWarps * k, r = 2 * i + (lane >> 4);
-          cp_async16_if(i < pairs, r_base + 2 * m * kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+          tc::cp_async16_if(i < pairs, r_base + 2 * m * kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4),
                         src[k] ? src[k] + 128 * m + 8 * c : a.pool, src[k] ? 16u : 0u);
         }
         tc::cp_async_commit();

@@ -8,8 +8,10 @@
 // shared memory: each CTA leaves its fp32 part in its own shared memory (the stage buffers, free by then), and CTA r
 // sums the S parts, in split order, of N / S tokens and writes them.  No partial sum goes to memory and no second
 // pass reads one.  Both pools are one grid.  Bound by the weights' stream (21 MB for both Flash pools) for few tokens
-// (8 tokens: 8.0 us, six splits; four take 1.6 us longer, seven 6.5, since their clusters do not all run at once), by the
-// tiles' way into shared memory for many (512 tokens: 17 us; 48 KB of weights and tokens for 512 clocks of products).
+// (8 tokens: 8.6 us with the pooling behind it, six splits; four took 1.6 us longer, seven 6.5, since their clusters do
+// not all run at once, and products issued by a thread that a lane number chose, not elect.sync, 2.1), by the tiles' way
+// into shared memory for many (512 tokens: 23.5 us with the pooling; 48 KB of weights and tokens for 512 clocks of
+// products).
 #include <atomic>
 
 #include "kernels.h"
@@ -136,18 +138,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (tc::elect_one()) {
       const uint32_t idesc = tc::idesc_bf16(128, N);
+      const uint64_t base = tc::sdesc_kmajor_sw128(tc::smem_u32(smem));
+      int s = 0;
+      uint32_t phase = 0;
+#pragma unroll 1
       for (int kb = 0; kb < nk; ++kb) {
-        const int s = kb % a.stages;
-        if (!tc::mbar_wait(&full[s], (kb / a.stages) & 1)) { failed = true; break; }
+        if (!tc::mbar_wait(&full[s], phase)) { failed = true; break; }
         tc::fence_after_sync();
-        const uint32_t ab = tc::smem_u32(smem + s * stage_bytes);
-        const uint64_t ad = tc::sdesc_kmajor_sw128(ab), bd = tc::sdesc_kmajor_sw128(ab + kABytes);
+        const uint64_t ad = base + ((uint32_t)(s * stage_bytes) >> 4), bd = ad + (kABytes >> 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // (32 bytes further: two descriptor address units)
           tc::mma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc, (kb > 0 || k > 0) ? 1u : 0u);
         tc::mma_commit(&empty[s]);
+        if (++s == a.stages) { s = 0; phase ^= 1; }
       }
       tc::mma_commit(&acc_full);  // every MMA, and so every load, has retired when this completes
     }

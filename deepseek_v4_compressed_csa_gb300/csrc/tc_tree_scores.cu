@@ -71,12 +71,6 @@ struct TsArgs {
   int32_t* err;
 };
 
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
-
 // Tiles of a group of sequence b: its committed rows and one of the tree's rows; 0 when the state is inconsistent.
 __device__ __forceinline__ int seq_tiles(const TsArgs& a, int b) {
   const int p0 = __ldg(a.pos + b), n = __ldg(a.n_rows + b);
@@ -249,7 +243,7 @@ __global__ void __launch_bounds__(TsCfg<kFp8>::kThreads, 1)
     // ------------------------------------------------------------ MMA
     // (one elected thread; descriptors as a base plus constants: what this thread does between two tiles' products is
     // time that the tensor pipe may stand still)
-    if (elect_one()) {
+    if (tc::elect_one()) {
       constexpr uint32_t idesc = kFp8 ? tc::idesc_e4m3(kRows, kN) : tc::idesc_bf16(kRows, kN);
       const uint64_t kd = tc::sdesc_kmajor_sw128(tc::smem_u32(kbuf)), qd = tc::sdesc_kmajor_sw128(tc::smem_u32(qbuf));
       int stage = 0, acc = 0, nq = 0;
