@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int k0 = a.kblk * split / a.S, nk = a.kblk * (split + 1) / a.S - k0;
   const uint32_t tcols = N <= 32 ? 32 : (N <= 64 ? 64 : (N <= 128 ? 128 : 256));
   const int first = min(a.stages, nk);
-  if (threadIdx.x == 0) {
+  if (warp == 0 && tc::elect_one()) {
     for (int s = 0; s < a.stages; ++s) {
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool failed = false;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (tc::elect_one()) {
       for (int kb = first; kb < nk; ++kb) {
         const int s = kb % a.stages;
         if (!tc::mbar_wait(&empty[s], ((kb / a.stages) & 1) ^ 1)) { failed = true; break; }

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(TsCfg<kFp8>::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA
-    if (lane == 0) {
+    if (tc::elect_one()) {
       int stage = 0, nq = 0;
       uint32_t phase = 0, used = 0, par = 0, q_used = 0, q_par = 0;
       for (; w.left > 0 && !failed; w.next(a), ++nq) {
