@@ -11,14 +11,17 @@ library's CUDA kernels; there is no CPU path.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import struct
+import sysconfig
 from dataclasses import dataclass
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libcsa.so")
+_CHECKS_PATH = os.path.join(_HERE, "_lib", "csa_checks" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 CSA_F32, CSA_BF16 = 0, 1
 OP_COMPRESS, OP_INDEX_TOPK, OP_ATTEND_DECODE, OP_ATTEND_PREFILL, OP_COMPRESS_PAIR = 0, 1, 2, 3, 4
@@ -65,11 +68,12 @@ _COMP_FMT, _ROWS_FMT = "@4Pi0P", "@3P3iq"
 
 
 _lib = None
+_addresses = None  # csrc/checks.c: what _ptrs does, in C
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libcsa.so (built by build.py); raises if it is missing."""
-    global _lib
+    global _lib, _addresses
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -130,6 +134,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.csa_commit_tree.argtypes = [vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp,
                                     i32, vp, vp, vp, vp]
     lib.csa_commit_tree.restype = i32
+    if os.path.exists(_CHECKS_PATH):  # (not built where Python's headers are missing)
+        spec = importlib.util.spec_from_file_location("csa_checks", _CHECKS_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _addresses = module.addresses
     _lib = lib
     return lib
 
@@ -645,6 +654,11 @@ def _refuse(name: str, t, dtype, shape, dev):
 def _ptrs(dev: int, *specs) -> list:
     """Addresses of a tree call's tensors, each spec (name, tensor, dtype, shape), after checks of type, shape, device
     and contiguity."""
+    if _addresses is not None:
+        out = _addresses(dev, *specs)
+        if type(out) is list:
+            return out
+        _refuse(*out, dev)
     out = []
     for name, t, dtype, shape in specs:
         try:
@@ -866,30 +880,29 @@ def commit_tree(layer: Layer, parent, leaf, pos, n_rows_a, kv, window, proj_a, f
     dt, i32, D, F, vec = layer.dtype, torch.int32, layer.D, _frontier_len(layer), (B,)
     wide = 2 * layer.lanes
 
-    def pool_args(names, d, pj, fr, rw, pl, nr, nr_out, spec):
-        if not isinstance(pl, torch.Tensor) or pl.dim() != 3:
-            raise ValueError(f"{names[3]}: expected [{B}, cap, {spec[1]}]")
-        cap = pl.shape[1]
-        p = _ptrs(dev, (names[0], pj, dt, (B, T, wide * d)), (names[1], fr, dt, (B, F, wide * d)),
-                  (names[2], rw, spec[0], (B, T, spec[1])), (names[3], pl, spec[0], (B, cap, spec[1])),
-                  (names[4], nr, i32, vec), (names[5], nr if nr_out is None else nr_out, i32, vec))
-        return (*p[:4], cap, *p[4:])
-
-    p = _ptrs(dev, ("parent", parent, i32, (B, T)), ("leaf", leaf, i32, vec), ("pos", pos, i32, vec),
-              ("pos_out", pos if pos_out is None else pos_out, i32, vec), ("kv", kv, dt, (B, T, D)),
-              ("window", window, dt, (B, layer.ring_slots, D)))
-    pa = pool_args(_COMMIT_A, D, proj_a, frontier_a, rows_a, pool_a, n_rows_a, n_rows_a_out, (dt, D))
+    if not isinstance(pool_a, torch.Tensor) or pool_a.dim() != 3:
+        raise ValueError(f"pool_a: expected [{B}, cap, {D}]")
+    cap_a, wide_a = pool_a.shape[1], wide * D
+    specs = [("parent", parent, i32, (B, T)), ("leaf", leaf, i32, vec), ("pos", pos, i32, vec),
+             ("pos_out", pos if pos_out is None else pos_out, i32, vec), ("kv", kv, dt, (B, T, D)),
+             ("window", window, dt, (B, layer.ring_slots, D)), ("proj_a", proj_a, dt, (B, T, wide_a)),
+             ("frontier_a", frontier_a, dt, (B, F, wide_a)), ("rows_a", rows_a, dt, (B, T, D)),
+             ("pool_a", pool_a, dt, (B, cap_a, D)), ("n_rows_a", n_rows_a, i32, vec),
+             ("n_rows_a_out", n_rows_a if n_rows_a_out is None else n_rows_a_out, i32, vec)]
     if pool_i is not None:
-        pi = pool_args(_COMMIT_I, layer.Di, proj_i, frontier_i, rows_i, pool_i, n_rows_i, n_rows_i_out,
-                       layer.pool_spec(layer.Di))
+        row_dt, row = layer.pool_spec(layer.Di)
+        if not isinstance(pool_i, torch.Tensor) or pool_i.dim() != 3:
+            raise ValueError(f"pool_i: expected [{B}, cap, {row}]")
+        cap_i, wide_i = pool_i.shape[1], wide * layer.Di
+        specs += (("proj_i", proj_i, dt, (B, T, wide_i)), ("frontier_i", frontier_i, dt, (B, F, wide_i)),
+                  ("rows_i", rows_i, row_dt, (B, T, row)), ("pool_i", pool_i, row_dt, (B, cap_i, row)),
+                  ("n_rows_i", n_rows_i, i32, vec),
+                  ("n_rows_i_out", n_rows_i if n_rows_i_out is None else n_rows_i_out, i32, vec))
     elif any(t is not None for t in (n_rows_i, proj_i, frontier_i, rows_i, n_rows_i_out)):
         raise ValueError("n_rows_i, proj_i, frontier_i, rows_i, n_rows_i_out come with pool_i")
-    else:
-        pi = (None, None, None, None, 0, None, None)
+    p = _ptrs(dev, *specs)
+    pi = (None, None, None, None, 0, None, None) if pool_i is None else (*p[12:16], cap_i, *p[16:])
     err = _tree_err(err, dev, stream)
-    _tree_call("csa_commit_tree", dev, stream, layer._packed(), B, T, *p, *pa, *pi, err.data_ptr())
+    _tree_call("csa_commit_tree", dev, stream, layer._packed(), B, T, *p[:10], cap_a, *p[10:12], *pi, err.data_ptr())
     return err
 
-
-_COMMIT_A, _COMMIT_I = (tuple(f.format(k) for f in ("proj_{}", "frontier_{}", "rows_{}", "pool_{}", "n_rows_{}",
-                                                      "n_rows_{}_out")) for k in "ai")

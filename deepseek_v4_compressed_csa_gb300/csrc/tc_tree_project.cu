@@ -234,11 +234,13 @@ int clusters(int S) {
 Plan plan(int m_tiles, int ntok, int kblk, int sms) {
   Plan best{};
   long best_cost = -1;
+  int most[kMaxSplit + 1];  // clusters of S at once
+  for (int S = 2; S <= kMaxSplit; ++S) most[S] = clusters(S);
   for (int N = 32; N <= 256; N += 32) {
     const int n_tiles = (ntok + N - 1) / N;
     for (int S = 1; S <= kMaxSplit && S <= kblk; ++S) {
       const long tiles = (long)m_tiles * n_tiles;
-      if (S > 1 && tiles > clusters(S)) continue;
+      if (S > 1 && tiles > most[S]) break;  // (fewer still of a larger cluster)
       const long waves = S > 1 ? 1 : (tiles + sms - 1) / sms;
       const long mma = max(32 + N / 4, N / 2);
       const long cost = waves * (6000 + (long)((kblk + S - 1) / S) * 4 * mma);

@@ -217,3 +217,43 @@ def test_packed_structures_are_the_c_layouts(lib):
     import dataclasses
     other = dataclasses.replace(LAYER, topk=7)
     assert other._packed() == bytes(other._c()) != LAYER._packed() and other != LAYER
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_checks_of_tensors(lib, native, monkeypatch):
+    """The checks in C and those in Python: the same addresses, the same refusals (device -1: CPU tensors)."""
+    if native and B._addresses is None:
+        pytest.skip("the checks in C are not built here (no Python headers)")
+    if not native:
+        monkeypatch.setattr(B, "_addresses", None)
+    t, v = z(2, 3, 4), z(5, dt=torch.int32)
+    good = [("t", t, torch.bfloat16, (2, 3, 4)), ("v", v, torch.int32, (5,)), ("s", z(0, 7), torch.bfloat16, (0, 7))]
+    assert B._ptrs(-1, *good)[:2] == [t.data_ptr(), v.data_ptr()] and B._ptrs(-1) == []
+    for bad, error in ((("t", t, torch.float16, (2, 3, 4)), TypeError), (("t", None, torch.bfloat16, (2,)), ValueError),
+                       (("t", t, torch.bfloat16, (2, 3, 5)), ValueError), (("t", t, torch.bfloat16, (2, 12)), ValueError),
+                       (("t", t[:, :2], torch.bfloat16, (2, 2, 4)), ValueError), (("t", 5, torch.int32, ()), TypeError),
+                       (("t", t.transpose(0, 1), torch.bfloat16, (3, 2, 4)), ValueError)):
+        with pytest.raises(error, match="t"):
+            B._ptrs(-1, good[1], bad)
+    with pytest.raises(ValueError, match="t"):
+        B._ptrs(0, good[0])
+
+
+def test_checks_hold_no_references(lib):
+    import sys
+    if B._addresses is None:
+        pytest.skip("the checks in C are not built here (no Python headers)")
+    t = z(2, 3)
+    spec, wrong = ("t", t, torch.bfloat16, (2, 3)), ("t", t, torch.bfloat16, (3, 2))
+    before = [sys.getrefcount(x) for x in (t, spec, wrong, spec[3], torch.bfloat16)]
+    for _ in range(1000):
+        assert B._addresses(-1, spec, spec) == [t.data_ptr()] * 2
+        assert B._addresses(-1, spec, wrong) is wrong
+    after = [sys.getrefcount(x) for x in (t, spec, wrong, spec[3], torch.bfloat16)]
+    assert after == before
+    with pytest.raises(TypeError):
+        B._addresses()
+    with pytest.raises(TypeError):
+        B._addresses(-1, ("t", t))
+    with pytest.raises(TypeError):
+        B._addresses("x", spec)
