@@ -735,8 +735,8 @@ cudaError_t launch_topk_tree(const Dims& L, const float* scores, int B, int T, c
   int sms = 0, dev = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (topk_tree_many_fits(B * T, cap, T, sms))
-    return launch_topk_tree_many(L, scores, B, T, parent, cap, n_rows, pos, sel, nodes, err, s);
+  if (topk_tree_small_blocks(B * T, cap, T, sms))
+    return launch_topk_tree_small(L, scores, B, T, parent, cap, n_rows, pos, sel, nodes, err, s);
   const TopkTree tr{parent, T, nodes, err};
   const int32_t* none = nullptr;
   int32_t* no_count = nullptr;

@@ -324,8 +324,8 @@ cudaError_t launch_topk_tree(const Dims& L, const float* scores, int B, int T, c
                              const int32_t* n_rows, const int32_t* pos, int32_t* sel, TreeNode* nodes, int32_t* err,
                              cudaStream_t s);
 // ---- tree_topk.cu: the same for more nodes than SMs (a block of 256 threads per node, its keys in shared memory)
-bool topk_tree_many_fits(int Q, int cap, int T, int sms);
-cudaError_t launch_topk_tree_many(const Dims& L, const float* scores, int B, int T, const int32_t* parent, int cap,
+bool topk_tree_small_blocks(int Q, int cap, int T, int sms);
+cudaError_t launch_topk_tree_small(const Dims& L, const float* scores, int B, int T, const int32_t* parent, int cap,
                                   const int32_t* n_rows, const int32_t* pos, int32_t* sel, TreeNode* nodes,
                                   int32_t* err, cudaStream_t s);
 struct TreeAttendWs {

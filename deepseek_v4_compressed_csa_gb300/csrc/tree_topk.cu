@@ -1,4 +1,4 @@
-// Selections of many nodes at once (csa_attend_tree): the topk largest scores of every node's visible columns, ties to
+// Selections by blocks of 256 threads (csa_attend_tree): the topk largest scores of every node's visible columns, ties to
 // the lower column, in ascending order.
 //
 // The register kernel of indexer.cu gives a query 1024 threads: the lowest latency for a few queries, but one block
@@ -26,7 +26,7 @@ __device__ __forceinline__ int warp_incl(int v) {
   return v;
 }
 
-__global__ void __launch_bounds__(kThreads) k_tree_topk_many(const float* __restrict__ scores, int cap, int T,
+__global__ void __launch_bounds__(kThreads) k_tree_topk(const float* __restrict__ scores, int cap, int T,
                                                              const int32_t* __restrict__ parent,
                                                              const int32_t* __restrict__ pos,
                                                              const int32_t* __restrict__ n_rows, int ratio, int topk,
@@ -187,16 +187,22 @@ __global__ void __launch_bounds__(kThreads) k_tree_topk_many(const float* __rest
 
 }  // namespace
 
-bool topk_tree_many_fits(int Q, int cap, int T, int sms) {
-  return Q > sms && (size_t)(cap + T) * sizeof(uint32_t) <= 64 * 1024;  // at least three blocks an SM
+// More nodes than SMs: up to 64 KB of keys, at least three blocks an SM.  Few nodes, whose attention takes several CTAs
+// each: up to 33 KB, since a block of 1024 threads fills its SM's registers and keeps the attention's CTA, which fetches
+// queries and window rows ahead, away from it (8 nodes of 2K columns: selection and attention 20.8 us, with the register
+// kernel 23.8; of 8K 23.5 and 24.4; of 15K 26.8 and 26.2).  In between the register kernel (64 nodes of 8K columns: 35
+// us, here 41).
+bool topk_tree_small_blocks(int Q, int cap, int T, int sms) {
+  const size_t bytes = (size_t)(cap + T) * sizeof(uint32_t);
+  return (Q > sms && bytes <= 64 * 1024) || (4 * Q <= sms && bytes <= 33 * 1024);
 }
 
-cudaError_t launch_topk_tree_many(const Dims& L, const float* scores, int B, int T, const int32_t* parent, int cap,
+cudaError_t launch_topk_tree_small(const Dims& L, const float* scores, int B, int T, const int32_t* parent, int cap,
                                   const int32_t* n_rows, const int32_t* pos, int32_t* sel, TreeNode* nodes,
                                   int32_t* err, cudaStream_t s) {
   const size_t smem = (size_t)(cap + T) * sizeof(uint32_t);
-  cudaFuncSetAttribute(k_tree_topk_many, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
-  CSA_LAUNCH(k_tree_topk_many, dim3(B * T), dim3(kThreads), smem, s, scores, cap, T, parent, pos, n_rows, L.ratio,
+  cudaFuncSetAttribute(k_tree_topk, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+  CSA_LAUNCH(k_tree_topk, dim3(B * T), dim3(kThreads), smem, s, scores, cap, T, parent, pos, n_rows, L.ratio,
              L.topk, sel, nodes, err);
   return cudaGetLastError();
 }
