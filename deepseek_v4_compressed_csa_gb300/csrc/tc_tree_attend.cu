@@ -12,11 +12,12 @@
 // holds one tile (128 KB), the query block (64 KB) and P (32 KB), tensor memory the two halves of O^T and S^T, so S^T
 // of the next tile cannot be formed while a tile's softmax runs; the design keeps that gap and everything else short:
 //   loaders (warps 9-15)  fill a tile in four pairs of 64-dim boxes: a pair of the next tile is refilled as soon as the
-//     PV products of the current tile have read it.  Consecutive committed rows (no selection) are TMA boxes; 128
-//     selected committed rows are 256 tile::gather4 requests, ten threads of each warp issuing (a warp issues one every
-//     ~75 clocks whatever its threads do: two warps took 11.7 us a tile, seven are near the copy engine's own rate);
-//     tiles of mixed sources (window, path, the selection's end) are 16-byte cp.async by address, which the products'
-//     own use of shared memory slows to ~28 B a clock where the copy engine keeps its pace.
+//     PV products of the current tile have read it.  Consecutive committed rows (no selection) are TMA boxes; of 128
+//     selected committed rows four warps fetch 56 by tile::gather4, 28 requests each (a warp issues one every ~75 clocks
+//     whatever its threads do, and the copy engine takes ~14 clocks for one), three warps the others by cp.async, which
+//     the products' own use of shared memory slows to ~28 B a clock: all rows by seven gathering warps take 117.5 us
+//     where this takes 115.3, 56 to 96 gathered rows much the same;
+//     tiles of mixed sources (window, path, the selection's end) are cp.async by address.
 //   MMA (warp 8)  one thread; descriptors are a base plus a constant: built from addresses every time they cost it
 //     ~90 clocks a product, twice what the tensor pipe takes.
 //   softmax (warps 0-7)  thread = (key row, 32 heads).  The reference that exponents are taken against is the head's
@@ -27,13 +28,13 @@
 //     holds one dim of 32 heads, and its 2-byte stores straight to memory cost 7 us a node.  Transposing by stmatrix or by
 //     shuffles instead changes nothing (within 1 us for the 512 nodes below), plain 16-byte stores out of the buffer cost
 //     3 us: the next node's first tile, whose rows take 3.5K clocks to land, hides all but 2.4K of its 7.5K clocks.
-// 512 nodes of 640 keys, 512 of them selected: 100 us beside 17 for the selection; 128 nodes of 1.9K consecutive keys
+// 512 nodes of 640 keys, 512 of them selected: 98 us beside 17 for the selection; 128 nodes of 1.9K consecutive keys
 // each: 64 us, 5.7K clocks a tile of the 3.8K that its products take.
 //
 // Few nodes with long lists (kSplit): a cluster of S CTAs per node, each its run of the tiles, the parts of O^T joined
 // through distributed shared memory.  S is the largest of 8, 4, 2 whose clusters all run at once and that leaves two
 // tiles to each CTA (one tile each gains nothing over the join): 8 nodes over 8.2K rows take 48 us instead of 196, 64
-// over 2K 44 instead of 59.  The same for the nodes left over after whole rounds of the SMs saves 2 us of 117 at 512
+// over 2K 44 instead of 59.  The same for the nodes left over after whole rounds of the SMs saves 2 us at 512
 // nodes, which its bookkeeping costs again: those stay a CTA each.
 #include <atomic>
 
@@ -56,6 +57,10 @@ constexpr int kHalf = kSoft / 2;         // threads of one head half
 constexpr int kMmaWarp = 8;
 constexpr int kLoadWarp0 = 9, kLoadWarps = 7;  // sixteen warps in all, 128 registers a thread
 constexpr int kThreads = 32 * (kLoadWarp0 + kLoadWarps);
+constexpr int kGatherWarps = 4, kGatherRows = 56;  // of a selected tile: the copy engine's share, the others by cp.async
+constexpr int kGatherLanes = kGatherRows / 2 / kGatherWarps;                          // requests of a warp for a pair
+constexpr int kCopyInstr = (kPR - kGatherRows) / 2 / (kLoadWarps - kGatherWarps);     // row pairs of a copying warp
+static_assert(kGatherLanes * kGatherWarps * 2 == kGatherRows && kCopyInstr <= 16, "whole shares");
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColO3 = 384;         // O^T tile 3 (hi + lo in one accumulator); tiles 0-2: 128 m, hi | lo
 constexpr uint32_t kColS = 448;          // S^T
@@ -368,7 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ loaders
     // By address: warp w's instruction k of a pair copies 256 bytes of rows 2 i and 2 i + 1, i = w + 7 k (i < 64), a
     // half warp each; lane l holds the address of row 2 (w + 7 (l % 16)) + l / 16, so that one shuffle hands a half its
-    // row.  By gather: lane l of warp w requests box j % 2 of a pair and the four rows 4 (j / 2) .. of it, j = w + 7 l.
+    // row.  By gather: lane l of warp w < kGatherWarps requests box j % 2 of a pair and the four rows 4 (j / 2) .. of it,
+    // j = w + kGatherWarps l; the other warps copy the rows behind those, as by address (lane l holds the pool row).
     // Nothing that takes long stands between a tile's copies: while tile i is copied, the columns of tile i + 2 are
     // being read, the rows of tile i + 1 are on their way into L2 (its columns have arrived), and the next node's
     // record is in registers.
@@ -377,8 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t r_base = tc::smem_u32(rows) + ((lane >> 3) & 1) * kBox;
     const int c = lane & 15;
     const int my_row = c < kInstr && w + kLoadWarps * c < 64 ? 2 * (w + kLoadWarps * c) + (lane >> 4) : kPR;
-    const int j = w + kLoadWarps * lane;  // this lane's gather of a pair (none: j >= 64)
-    const int n_gather = (64 - w + kLoadWarps - 1) / kLoadWarps;
+    const bool gathers = w < kGatherWarps;
+    const int j = w + kGatherWarps * lane;  // this lane's gather of a pair (lane < kGatherLanes)
+    const int copy0 = kGatherRows / 2 + w - kGatherWarps;  // a copying warp's row pairs: copy0 + 2 k ..
+    const int copy_row = 2 * (copy0 + (kLoadWarps - kGatherWarps) * c) + (lane >> 4);  // (c < kCopyInstr) this lane's
     struct Tile {  // a tile of the walk: query, first key, the end of the CTA's keys of the query, its record
       int qi, k0, keys;
       bool first;  // kSplit: of the query's tiles here
@@ -401,8 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (kSplit) t.first = false;
       if (t.k0 >= t.keys) start_query(t, t.qi + q_step);
     };
-    struct Columns {  // of this lane's row, of its gather's rows, of the tile's last row
-      int own, g[4], last;
+    struct Columns {  // of this lane's row, of its gather's rows (a copying warp: g[0], of the row it copies), of the
+      int own, g[4], last;  // tile's last row
     };
     auto columns = [&](const Tile& t, Columns& x) {
       if (t.qi >= a.Q || !a.sel) return;
@@ -411,9 +419,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (my_row < min(n, kPR)) x.own = __ldg(p + my_row);
       if (n >= kPR) {
         x.last = __ldg(p + kPR - 1);
+        if (!gathers) {
+          if (c < kCopyInstr) x.g[0] = __ldg(p + copy_row);
+        } else if (lane < kGatherLanes) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (j < 64) x.g[e] = __ldg(p + 4 * (j >> 1) + e);
+          for (int e = 0; e < 4; ++e) x.g[e] = __ldg(p + 4 * (j >> 1) + e);
+        }
       }
     };
     enum { kByAddress, kByBox, kByGather };
@@ -439,6 +450,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     nxt = cur;
     advance(nxt);
     columns(nxt, col);
+    // the warp's cp.async copies of pair m have been issued: those of the pair before are waited for and reported
+    auto copied = [&](int m) {
+      tc::cp_async_commit();
+      if (m >= 1) {
+        tc::cp_async_wait_group<1>();
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(rows_full + m - 1);
+      }
+    };
     uint32_t nq = 0, nt = 0;
     for (; cur.qi < a.Q && !failed; ++nt) {
       if (kSplit ? cur.first : cur.k0 == 0) {
@@ -479,11 +500,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         if (how == kByGather) {
-          if (lane == 0) tc::mbar_arrive_expect_tx(rows_full + m, n_gather * 512);
-          __syncwarp();
-          if (j < 64)
-            tc::tma_gather4(rows + (2 * m + (j & 1)) * kBox + (j >> 1) * 512, &tm_row, rows_full + m,
-                            64 * (2 * m + (j & 1)), a0, a1, a2, a3);
+          if (gathers) {
+            if (lane == 0) tc::mbar_arrive_expect_tx(rows_full + m, kGatherLanes * 512);
+            __syncwarp();
+            if (lane < kGatherLanes)
+              tc::tma_gather4(rows + (2 * m + (j & 1)) * kBox + (j >> 1) * 512, &tm_row, rows_full + m,
+                              64 * (2 * m + (j & 1)), a0, a1, a2, a3);
+            continue;
+          }
+#pragma unroll
+          for (int k = 0; k < kCopyInstr; ++k) {
+            const int pool_row = __shfl_sync(0xffffffffu, a0, k + (lane & 16));
+            const int r = 2 * (copy0 + (kLoadWarps - kGatherWarps) * k) + (lane >> 4);
+            tc::cp_async16(r_base + 2 * m * kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                           a.pool + (size_t)pool_row * kAD + 128 * m + 8 * c, 16u);
+          }
+          copied(m);
           continue;
         }
         const __nv_bfloat16* src[kInstr];
@@ -496,16 +528,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::cp_async16_if(i < pairs, r_base + 2 * m * kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4),
                         src[k] ? src[k] + 128 * m + 8 * c : a.pool, src[k] ? 16u : 0u);
         }
-        tc::cp_async_commit();
-        if (m >= 1) {
-          tc::cp_async_wait_group<1>();
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(rows_full + m - 1);
-        }
+        copied(m);
       }
       if (failed) break;
-      if (how != kByAddress) continue;
+      if (how == kByBox || (how == kByGather && gathers)) continue;
       tc::cp_async_wait_group<0>();
       tc::fence_proxy_async_smem();
       __syncwarp();
