@@ -738,7 +738,8 @@ def norm_rope(layer: Layer, xs, pos=None, inv_freq=None, parent=None, weights=No
     """csa_norm_rope: every head row of the tensors xs (up to four, each [B, T, heads, dim] or [B, T, dim]) RMS-normed
     (norm[k], default True; weights[k] fp32 [dim] or None) and rotated to its token's position: pos[b] + depth in the
     tree `parent` [B, T], or pos[b] + i without one.  inv_freq None: no rotation (for the calls that rotate by
-    themselves).  An x may be a slice of a wider tensor: its heads contiguous, one stride from token to token.
+    themselves).  An x may be a slice of a wider tensor: its heads contiguous, one stride from token to token, at least
+    a token's size (an expanded tensor is refused).
     Returns the outputs (`outs`, or new tensors; a new tensor's rows of unused tree slots are zeros)."""
     n = len(xs)
     if not 1 <= n <= 4:
@@ -770,9 +771,11 @@ def norm_rope(layer: Layer, xs, pos=None, inv_freq=None, parent=None, weights=No
         if not x.is_contiguous():
             st = x.stride()
             stride = st[1] if T > 1 else (st[0] if B > 1 else 0)
+            # (a stride below a token's size: a broadcast tensor, or tokens over one another; 0 is 'dense' to the library)
             if st[-1] != 1 or (len(shape) == 4 and heads > 1 and st[2] != dim) or (
-                    T > 1 and B > 1 and st[0] != T * st[1]):
-                raise ValueError(f"xs[{k}]: strides {st}; heads must be contiguous, tokens one stride apart")
+                    T > 1 and B > 1 and st[0] != T * st[1]) or (B * T > 1 and stride < heads * dim):
+                raise ValueError(f"xs[{k}]: strides {st}; heads must be contiguous, tokens one stride of at least a "
+                                 "token apart")
         if not (isinstance(out, torch.Tensor) and out.dtype is dtype and out.shape == shape
                 and out.get_device() == dev and out.is_contiguous()):
             _refuse(f"outs[{k}]", out, dtype, shape, dev)

@@ -257,3 +257,55 @@ def test_checks_hold_no_references(lib):
         B._addresses(-1, ("t", t))
     with pytest.raises(TypeError):
         B._addresses("x", spec)
+
+
+# ------------------------------------------------------------------------------------------------ tokens of norm_rope
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """What the binding would hand to the library; nothing is launched."""
+    got = []
+    monkeypatch.setattr(B, "_tree_call", lambda fn, dev, stream, *args: got.append((fn, args)))
+    return got
+
+
+def _rows_of(args):
+    return B._Rows.from_buffer_copy(args[1])
+
+
+def _norm_rope(x):
+    return csa.norm_rope(LAYER, [_cuda_like(x)], outs=[_cuda_like(z(*x.shape))], err=_cuda_like(z(1, dt=torch.int32)))
+
+
+@pytest.mark.parametrize("shape, src", [
+    ((2, 3, 8, 128), (1, 1, 8, 128)), ((1, 3, 8, 128), (1, 1, 8, 128)), ((4, 1, 8, 128), (1, 1, 8, 128)),
+    ((4, 1, 128), (1, 1, 128)), ((1, 5, 128), (1, 1, 128)), ((2, 3, 128), (1, 1, 128)), ((2, 3, 8, 128), (2, 1, 8, 128)),
+    ((2, 3, 8, 128), (1, 3, 8, 128))])
+def test_norm_rope_refuses_broadcast_tokens(lib, calls, shape, src):
+    """An expanded tensor holds fewer tokens than its shape says: a token stride of 0 must not be taken for 'dense'."""
+    with pytest.raises(ValueError, match=r"xs\[0\]: strides"):
+        _norm_rope(z(*src).expand(*shape))
+    assert not calls
+
+
+def test_norm_rope_refuses_overlapping_tokens(lib, calls):
+    """Tokens one value or one head apart lie over one another."""
+    buf = z(4096)
+    for shape, strides in (((1, 3, 8, 128), (0, 128, 128, 1)), ((3, 1, 8, 128), (512, 512, 128, 1)),
+                           ((1, 4, 128), (0, 8, 1)), ((2, 2, 8, 128), (1024, 512, 128, 1))):
+        with pytest.raises(ValueError, match=r"xs\[0\]: strides"):
+            _norm_rope(buf.as_strided(shape, strides))
+    assert not calls
+
+
+def test_norm_rope_takes_slices_of_wider_tensors(lib, calls):
+    """What the call documents: heads contiguous, one real stride from token to token; a single token has none."""
+    wide = z(2, 3, 1160)
+    for x, stride in ((wide[..., :1024].unflatten(-1, (8, 128)), 1160), (wide[..., 1024:1152], 1160),
+                      (wide[:1, :, :128], 1160), (wide[:, :1, :128], 3 * 1160), (wide[:1, :1, :128], 0),
+                      (z(2, 3, 8, 128), 0)):
+        _norm_rope(x)
+        fn, args = calls.pop()
+        row = _rows_of(args)
+        assert fn == "csa_norm_rope" and row.x_stride == stride and row.x == x.data_ptr(), (x.shape, x.stride())
