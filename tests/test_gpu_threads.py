@@ -1,0 +1,128 @@
+"""Calls from several host threads, each on a stream of its own with buffers of its own: every call succeeds and gives
+what it gives alone, whatever the other threads call and whatever the thread did before."""
+import dataclasses
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import csa_synth
+from tests import _tree as TR
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import deepseek_v4_compressed_csa_gb300 as csa
+    from deepseek_v4_compressed_csa_gb300 import _binding as B
+    from tests import _gpu as G
+
+FLASH = csa_synth.CONFIGS[3].replace(X=512)
+TINY = csa_synth.CONFIGS[1]
+CALLS = 6000
+
+
+def rnd(cfg, shape, tag, dtype=None):
+    a = np.random.default_rng([6, cfg.cid, tag]).standard_normal(shape, dtype=np.float32)
+    return torch.from_numpy(a).to(dtype or cfg.storage).cuda()
+
+
+def z(*shape, dt=torch.bfloat16):
+    return torch.zeros(*shape, dtype=dt, device="cuda")
+
+
+def i32(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------------------------------------ a thread's first call
+
+
+def fresh_thread_jobs():
+    """Every kind of call that describes tensors to the copy engine, its buffers and stream ready: name, call, all
+    that it writes."""
+    cfg, nb, T, cap, many = FLASH.replace(rollback=4), 2, 4, 600, 40
+    L, invf, err, stream = G.lib_layer(cfg), csa_synth.inv_freq(cfg).cuda(), i32(0), torch.cuda.Stream()
+    fp8 = dataclasses.replace(L, index_fp8=True)
+    ca, ci = (G.lib_comp(csa_synth.compressor(cfg, w)) for w in ("attn", "index"))
+    ws = {op: z(csa.workspace_size(layer, op, b, t, cap) + 256, dt=torch.uint8) for op, layer, b, t in (
+        (csa.OP_COMPRESS, L, nb, T), (csa.OP_COMPRESS_PAIR, L, nb, 1), (csa.OP_INDEX_TOPK, L, nb, 1),
+        (csa.OP_ATTEND_DECODE, L, nb, 1), (csa.OP_ATTEND_PREFILL, L, 1, 40), (csa.OP_ATTEND_TREE, L, many, T),
+        (csa.OP_INDEX_SCORES_TREE, fp8, nb, T), (csa.OP_COMPRESS_TREE, L, nb, T))}
+    pos, n = i32(2051, 1205), i32(512, 301)
+    par = torch.tensor([TR.bushy(T)] * nb, dtype=torch.int32, device="cuda")
+    x, iq, iw = rnd(cfg, (nb, T, cfg.X), 40), rnd(cfg, (nb, T, 64, 128), 41), rnd(cfg, (nb, T, 64), 42)
+    keys, pool, window = rnd(cfg, (nb, cap, 128), 43), rnd(cfg, (nb, cap, 512), 44), rnd(cfg, (nb, cfg.ring_slots, 512), 45)
+    fa, fi = rnd(cfg, (nb, cfg.frontier_slots, 2048), 46), rnd(cfg, (nb, cfg.frontier_slots, 512), 47)
+    q, kv, sink = rnd(cfg, (nb, T, 64, 512), 48), rnd(cfg, (nb, T, 512), 49), z(64, dt=torch.float32)
+    rows, rows_i, scores = rnd(cfg, (nb, T, 512), 50), rnd(cfg, (nb, T, 128), 51), rnd(cfg, (nb, T, cap + T), 52, torch.float32)
+    keys8, rows8 = z(nb, cap, csa.FP8_ROW_BYTES, dt=torch.uint8), z(nb, T, csa.FP8_ROW_BYTES, dt=torch.uint8)
+    csa.index_rows_fp8(fp8, keys, keys8)
+    csa.index_rows_fp8(fp8, rows_i, rows8)
+    iq1, iw1, q1, kv1, x1 = (t[:, :1].contiguous() for t in (iq, iw, q, kv, x))
+    iq1, iw1, q1, kv1 = (t[:, 0] for t in (iq1, iw1, q1, kv1))
+    chunk = [rnd(cfg, s, 60 + k) for k, s in enumerate(((40, 64, 512), (40, 512), (40, 64, 128), (40, 64)))]
+    wide = [t[:1].expand(many, *t.shape[1:]).contiguous() for t in (q, kv, window, pool, rows, scores, par, n, pos)]
+    out, out1, outm, outc = z(*q.shape), z(*q1.shape), z(*wide[0].shape), z(*chunk[0].shape)
+    sel, n_sel = z(nb, cfg.topk, dt=torch.int32), z(nb, dt=torch.int32)
+    proj, prow, iproj, irow = z(nb, T, 2048), z(nb, T, 512), z(nb, T, 512), z(nb, T, 128)
+    got, got8 = z(nb, T, cap + T, dt=torch.float32), z(nb, T, cap + T, dt=torch.float32)
+    p2, i2, f2, g2, na, ni = z(nb, cap, 512), z(nb, cap, 128), fa.clone(), fi.clone(), n.clone(), n.clone()
+    win2, win1, n522 = window.clone(), window[0].clone(), i32(522)  # (the rows after the chunk)
+    k = dict(err=err, stream=stream)
+    return err, [
+        ("compress_tree", lambda: csa.compress_tree(
+            L, ca, x, par, pos, fa, proj, prow, invf, comp_i=ci, frontier_i=fi, proj_i=iproj, rows_i=irow,
+            ws=ws[csa.OP_COMPRESS_TREE], **k), (proj, prow, iproj, irow)),
+        ("index_scores_tree", lambda: csa.index_scores_tree(L, iq, iw, keys, rows_i, par, n, pos, got, **k), (got,)),
+        ("index_scores_tree, fp8 rows", lambda: csa.index_scores_tree(
+            fp8, iq, iw, keys8, rows8, par, n, pos, got8, ws=ws[csa.OP_INDEX_SCORES_TREE], **k), (got8,)),
+        ("attend_tree", lambda: csa.attend_tree(
+            L, q, kv, sink, window, pool, rows, scores, par, n, pos, invf, out, ws=ws[csa.OP_ATTEND_TREE], **k), (out,)),
+        ("attend_tree, many nodes", lambda: csa.attend_tree(
+            L, *wide[:2], sink, *wide[2:], invf, outm, ws=ws[csa.OP_ATTEND_TREE], **k), (outm,)),
+        ("compress_append", lambda: csa.compress_append(L, ca, x, pos, f2, p2, na, invf, ws=ws[csa.OP_COMPRESS], **k),
+         (p2, f2, na)),
+        ("compress_append_pair", lambda: csa.compress_append_pair(
+            L, ca, ci, x1, pos, f2, p2, na, g2, i2, ni, invf, ws=ws[csa.OP_COMPRESS_PAIR], **k),
+         (p2, i2, f2, g2, na, ni)),
+        ("index_topk", lambda: csa.index_topk(L, iq1, iw1, keys, n, pos, invf, sel, n_sel, ws=ws[csa.OP_INDEX_TOPK], **k),
+         (sel, n_sel)),
+        ("attend_decode", lambda: csa.attend_decode(
+            L, q1, kv1, sink, win2, pool, n, None, None, pos, invf, out1, ws=ws[csa.OP_ATTEND_DECODE], **k),
+         (out1, win2)),
+        ("attend_prefill_chunk", lambda: csa.attend_prefill_chunk(
+            L, *chunk, sink, 2051, win1, pool[0], keys[0], n522, invf, outc, ws=ws[csa.OP_ATTEND_PREFILL], **k),
+         (outc, win1)),
+    ]
+
+
+def test_first_cuda_call_of_a_thread():
+    """Each call as the first thing that a host thread does with CUDA: it has no current context before it."""
+    err, jobs = fresh_thread_jobs()
+    failures = []
+    for name, call, written in jobs:
+        before = [t.clone() for t in written]
+        torch.cuda.synchronize()
+        call()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in written]
+        assert not all(torch.equal(w, b) for w, b in zip(want, before)), name
+        for t, b in zip(written, before):
+            t.copy_(b)
+        torch.cuda.synchronize()
+
+        def work(call=call, name=name):
+            try:
+                call()
+            except Exception as e:  # noqa: BLE001 (whatever it is, the test names it)
+                failures.append((name, repr(e)))
+        thread = threading.Thread(target=work)
+        thread.start()
+        thread.join()
+        torch.cuda.synchronize()
+        if not any(f[0] == name for f in failures):
+            assert all(torch.equal(t, w) for t, w in zip(written, want)), name
+        for t, b in zip(written, before):
+            t.copy_(b)
+    assert not failures and err.item() == 0, failures
