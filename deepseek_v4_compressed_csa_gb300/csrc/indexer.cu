@@ -710,6 +710,7 @@ __global__ void __launch_bounds__(1024) k_topk_reg(const float* __restrict__ sco
 }
 
 constexpr int kTopkSmemMaxCap = 52 * 1024;
+constexpr int kTopkSmemMax = (kTopkSmemMaxCap + 2048) * 4;  // keys and histogram
 
 static cudaError_t launch_topk(const Dims& L, const float* scores, int cap, const int32_t* n_rows, const int32_t* pos,
                         int pos0, const int32_t* cu, int Q, int32_t* sel, int32_t* n_sel, cudaStream_t s) {
@@ -746,7 +747,7 @@ cudaError_t launch_topk_tree(const Dims& L, const float* scores, int B, int T, c
                static_cast<const __nv_bfloat16*>(nullptr), tr);
   } else if (cap + T <= kTopkSmemMaxCap) {
     const size_t smem = (size_t)(cap + T) * 4 + 2048 * 4;
-    cudaFuncSetAttribute(k_topk_smem<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    allow_smem<kTopkSmemMax>(k_topk_smem<true>);
     CSA_LAUNCH(k_topk_smem<true>, dim3(B * T), dim3(1024), smem, s, scores, cap, n_rows, pos, 0, none, L.ratio, L.topk,
                sel, no_count, tr);
   } else {

@@ -80,6 +80,15 @@ inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// Lets `kernel` be launched with up to kBytes of dynamic shared memory.  The limit belongs to the function on the device,
+// not to a launch: set to one call's need, it would fall under a larger call's that another host thread is about to
+// launch.  So it is a constant, the most that any call takes.
+template <int kBytes, typename... KArgs>
+inline void allow_smem(void (*kernel)(KArgs...)) {
+  static_assert(kBytes <= 232448, "shared memory per block");
+  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+}
+
 // Clusters of S blocks that the current device runs at once.  A cluster stays within one GPC, so that is less than
 // SMs / S blocks (of one block an SM, 23 clusters of 6 and 15 of 7 on 152 SMs): a grid of more has a second wave.
 template <typename... KArgs>

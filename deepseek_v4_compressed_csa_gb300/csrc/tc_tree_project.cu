@@ -221,7 +221,7 @@ int clusters(int S) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
   int n = known[dev][S].load(std::memory_order_relaxed) - 1;
   if (n < 0) {
-    cudaFuncSetAttribute(k_tc_tree_project, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    allow_smem<kMaxSmem>(k_tc_tree_project);
     n = max_clusters(k_tc_tree_project, kThreads, kMaxSmem, S);
     known[dev][S].store(n + 1, std::memory_order_relaxed);
   }
@@ -290,7 +290,7 @@ cudaError_t launch_tc_tree_project(const Dims& L, const TreeCompress* pools, int
   if (!make_tmap_2d_bf16(&tx, x, (uint64_t)B * T, L.X, (uint64_t)L.X * 2, p.N)) return cudaErrorInvalidValue;
   a.ntok = B * T; a.T = T; a.N = p.N; a.n_tiles = p.n_tiles; a.S = p.S; a.kblk = L.X / 64; a.stages = p.stages;
   a.parent = parent; a.pos = pos; a.err = err;
-  cudaFuncSetAttribute(k_tc_tree_project, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
+  allow_smem<kMaxSmem>(k_tc_tree_project);
   const dim3 grid(m_tiles * p.n_tiles * p.S);
   const cudaError_t e =
       p.S > 1 ? launch_pdl_cluster(k_tc_tree_project, grid, dim3(kThreads), p.smem, s, p.S, tw[0], tg[0], tw[1], tg[1],

@@ -126,3 +126,89 @@ def test_first_cuda_call_of_a_thread():
         for t, b in zip(written, before):
             t.copy_(b)
     assert not failures and err.item() == 0, failures
+
+
+# ------------------------------------------------------------------------------------------------ calls of different sizes
+
+
+def recorded(call):
+    """The library function that `call` uses and the arguments that it hands over, but for the stream (the last one)."""
+    got = []
+
+    class Recorder:
+        def __getattr__(self, name):
+            return lambda *args: got.append((name, args)) or 0
+    keep = B.load_library, B._lib
+    B.load_library, B._lib = (lambda: keep[1]), Recorder()
+    try:
+        call()
+    finally:
+        B.load_library, B._lib = keep
+    (name, args), = got
+    return getattr(csa.load_library(), name), args[:-1]
+
+
+def side_by_side(jobs):
+    """jobs: (call, outputs).  Each call by itself, then all of them CALLS times from a thread each, the C calls one
+    behind the other (Python lets the other threads run while one is in them)."""
+    alone, raw = [], []
+    for call, outs in jobs:
+        call()
+        torch.cuda.synchronize()
+        alone.append([o.clone() for o in outs])
+        raw.append(recorded(call))
+    torch.cuda.synchronize()
+    failures, gate = [], threading.Barrier(len(jobs))
+
+    def work(k):
+        stream = torch.cuda.Stream()
+        f, args = raw[k]
+        gate.wait()
+        for n in range(CALLS):
+            code = f(*args, stream.cuda_stream)
+            if code:
+                failures.append((k, n, code))
+                return
+            if n % 100 == 99:
+                stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failures, failures
+    for (_, outs), want in zip(jobs, alone):
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+
+
+def test_compress_tree_of_different_sizes():
+    """Token tiles and split counts, and with them the shared memory of the projections, go by the number of nodes."""
+    cfg, jobs = FLASH, []
+    comp, invf, L = G.lib_comp(csa_synth.compressor(cfg, "attn")), csa_synth.inv_freq(cfg).cuda(), G.lib_layer(cfg)
+    for nb, T in ((1, 3), (8, 16), (32, 16)):
+        x, frontier = rnd(cfg, (nb, T, cfg.X), 1 + nb), rnd(cfg, (nb, cfg.frontier_slots, 2048), 2 + nb)
+        par = torch.tensor([TR.bushy(T, b) for b in range(nb)], dtype=torch.int32, device="cuda")
+        pos, err, ws = torch.arange(nb, dtype=torch.int32, device="cuda") * 5, i32(0), z(256, dt=torch.uint8)
+        proj, rows = z(nb, T, 2048), z(nb, T, 512)
+        jobs.append((lambda a=(L, comp, x, par, pos, frontier, proj, rows, invf), ws=ws, err=err: csa.compress_tree(
+            *a, ws=ws, err=err), (proj, rows, err)))
+    side_by_side(jobs)
+
+
+def test_attend_tree_selecting_from_different_capacities():
+    """Selections whose keys fill different amounts of shared memory (pools of 17 to 50 thousand rows)."""
+    cfg, jobs, T, n = TINY, [], 3, 1000
+    L, invf = G.lib_layer(cfg), csa_synth.inv_freq(cfg).cuda()
+    for cap in (17000, 30000, 50000):
+        q, kv, sink = rnd(cfg, (1, T, cfg.H, cfg.D), 10), rnd(cfg, (1, T, cfg.D), 11), rnd(cfg, (cfg.H,), 12)
+        window, pool, rows = rnd(cfg, (1, cfg.W, cfg.D), 13), rnd(cfg, (1, cap, cfg.D), 14), rnd(cfg, (1, T, cfg.D), 15)
+        out, sel, err = torch.zeros_like(q), z(1, T, cfg.topk, dt=torch.int32), i32(0)
+        ws = z(csa.workspace_size(L, csa.OP_ATTEND_TREE, 1, T, cap), dt=torch.uint8)
+        a = (L, q, kv, sink, window, pool, rows, rnd(cfg, (1, T, cap + T), 16), i32(*TR.chain(T))[None], i32(n),
+             i32(n * cfg.ratio), invf, out)
+        jobs.append((lambda a=a, sel=sel, ws=ws, err=err: csa.attend_tree(*a, sel_out=sel, ws=ws, err=err),
+                     (out, sel, err)))
+    side_by_side(jobs)
