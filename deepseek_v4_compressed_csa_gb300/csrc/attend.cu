@@ -401,6 +401,7 @@ __global__ void k_attend_merge(const float* __restrict__ part_ml, const float* _
   }
 }
 
+constexpr int kAttendSmemMax = 232448;  // what a block can have (fp32 rows of more than 784 dims need more)
 template <typename T>
 static size_t attend_smem(int D) {
   return (size_t)kHG * D * sizeof(T) + (size_t)kCH * (D + 8) * sizeof(T) + (size_t)kHG * kCH * sizeof(float) +
@@ -410,7 +411,7 @@ static size_t attend_smem(int D) {
 template <typename T>
 static cudaError_t run_attend(AttnArgs& a, int Q, cudaStream_t s) {
   const size_t smem = attend_smem<T>(a.D);
-  cudaFuncSetAttribute(k_attend_simt<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  allow_smem<kAttendSmemMax>(k_attend_simt<T>);
   dim3 g((a.H + kHG - 1) / kHG, a.S, Q);
   CSA_LAUNCH(k_attend_simt<T>, dim3(g), dim3(256), smem, s, a);
   if (a.S > 1) {

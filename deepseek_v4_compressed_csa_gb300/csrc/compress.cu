@@ -812,7 +812,8 @@ static cudaError_t compress_pair_block(const Dims& L, const csa_compressor& ca, 
                       cap_i, si, tc_project_cols(L, ci.d, ntok), 0};
   const int dm = max(ca.d, ci.d), stride = 2 * L.lanes * dm;
   const size_t smem = (size_t)(kBlockOld + T_) * stride * sizeof(T) + (2 * (size_t)dm + 32) * sizeof(float);
-  cudaFuncSetAttribute(k_pool_block<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr int dm_max = 512;  // (and two lanes: launch_compress_pair)
+  allow_smem<(kBlockOld + kBlockMax) * 4 * dm_max * (int)sizeof(T) + (2 * dm_max + 32) * 4>(k_pool_block<T>);
   CSA_LAUNCH(k_pool_block<T>, dim3(2 * B), dim3(kBlockThreads), smem, s, ta, tb, B, T_, pos, err, L.R, L.F, L.eps,
              inv_freq, stride);
   return cudaGetLastError();

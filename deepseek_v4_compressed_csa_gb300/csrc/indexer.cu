@@ -720,7 +720,7 @@ static cudaError_t launch_topk(const Dims& L, const float* scores, int cap, cons
                static_cast<const __nv_bfloat16*>(nullptr), TopkTree{});
   } else if (cap <= kTopkSmemMaxCap) {
     const size_t smem = (size_t)cap * 4 + 2048 * 4;
-    cudaFuncSetAttribute(k_topk_smem<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    allow_smem<kTopkSmemMax>(k_topk_smem<false>);
     CSA_LAUNCH(k_topk_smem<false>, dim3(Q), dim3(1024), smem, s, scores, cap, n_rows, pos, pos0, cu, L.ratio, L.topk,
                sel, n_sel, TopkTree{});
   } else {
@@ -837,13 +837,13 @@ cudaError_t launch_index_topk(const Dims& L, const void* iq, const void* iw, int
                               const int32_t* n_rows, const int32_t* pos, int pos0, const float* inv_freq,
                               int32_t* sel, int32_t* n_sel, const IndexWs& ws, int32_t* err, cudaStream_t s,
                               const int32_t* cu) {
-  const int smax = 227 * 1024;
+  constexpr int smax = 227 * 1024;
   if (L.dtype == CSA_BF16) {
-    cudaFuncSetAttribute(k_index_scores<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smax);
+    allow_smem<smax>(k_index_scores<__nv_bfloat16>);
     return index_t<__nv_bfloat16>(L, iq, iw, Q, ikeys, cap, n_rows, pos, pos0, cu, inv_freq, sel, n_sel, ws, err,
                                   s);
   }
-  cudaFuncSetAttribute(k_index_scores<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, smax);
+  allow_smem<smax>(k_index_scores<float>);
   return index_t<float>(L, iq, iw, Q, ikeys, cap, n_rows, pos, pos0, cu, inv_freq, sel, n_sel, ws, err, s);
 }
 

@@ -629,7 +629,7 @@ cudaError_t launch_tc_attend(const Dims& L, const void* q, const void* pool, voi
   a.err = err;
   const int items = Q * S;
   const int grid = pos ? items : min(items, g_sms_at);
-  cudaFuncSetAttribute(k_tc_attend, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAt);
+  allow_smem<kSmemAt>(k_tc_attend);
   CSA_LAUNCH(k_tc_attend, dim3(grid), dim3(kThreadsAt), kSmemAt, s, a);
   return cudaGetLastError();
 }

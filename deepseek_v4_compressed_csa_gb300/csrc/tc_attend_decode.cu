@@ -741,7 +741,7 @@ bool tc_attend_decode_cluster(int S) {
   static int known[5] = {-1, -1, -1, -1, -1};
   if (S != 2 && S != 4) return false;
   if (known[S] < 0) {
-    cudaFuncSetAttribute(k_tc_attend_decode<false, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    allow_smem<kSmem>(k_tc_attend_decode<false, 4>);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(S);
     cfg.blockDim = dim3(kThreads);
@@ -780,7 +780,7 @@ cudaError_t launch_tc_attend_decode(const Dims& L, const void* q, const void* po
   a.part_ml = part_ml; a.part_acc = part_acc;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.err = err;
-  cudaFuncSetAttribute(k_tc_attend_decode<false, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  allow_smem<kSmem>(k_tc_attend_decode<false, 4>);
   if (cluster) {
     if (S != 2 && S != 4) return cudaErrorInvalidValue;
     const cudaError_t e = launch_pdl_cluster(k_tc_attend_decode<false, 4>, dim3(Q * S), dim3(kThreads), kSmem, s, S, a);
@@ -800,7 +800,7 @@ int tc_attend_tree_split_max(int S) {
   int n = known[dev][S].load(std::memory_order_relaxed) - 1;
   if (n < 0) {
     const auto kernel = S > 4 ? k_tc_attend_decode<true, 8> : k_tc_attend_decode<true, 4>;
-    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    allow_smem<kSmem>(kernel);
     n = max_clusters(kernel, kThreads, kSmem, S);
     known[dev][S].store(n + 1, std::memory_order_relaxed);
   }
@@ -825,7 +825,7 @@ cudaError_t launch_tc_attend_tree_split(const Dims& L, const TreeAttend& t, cons
   a.out = static_cast<__nv_bfloat16*>(t.out);
   a.err = err;
   const auto kernel = S > 4 ? k_tc_attend_decode<true, 8> : k_tc_attend_decode<true, 4>;
-  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  allow_smem<kSmem>(kernel);
   if (S > 1) {
     const cudaError_t e = launch_pdl_cluster(kernel, dim3(Q * S), dim3(kThreads), kSmem, s, S, a);
     if (e != cudaSuccess) return e;

@@ -667,7 +667,7 @@ cudaError_t launch_tc_attend_prefill(const Dims& L, const void* q, const void* p
       !make_tmap_2d_bf16(&tr, ring, (uint64_t)nseq * L.Wr, kAD, kAD * 2, 1) ||
       !make_tmap_2d_bf16(&tkt, kvr, (uint64_t)T, kAD, kAD * 2, a.chunk_tiles ? kPR : 1))
     return cudaErrorInvalidValue;
-  cudaFuncSetAttribute(k_tc_attend_prefill, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  allow_smem<kSmem>(k_tc_attend_prefill);
   CSA_LAUNCH(k_tc_attend_prefill, dim3(min(T, g_sms_pf)), dim3(kThreads), kSmem, s, tq, tp, tk, tr, tkt, a);
   return cudaGetLastError();
 }

@@ -960,12 +960,12 @@ cudaError_t launch_tc_index_scores(const Dims& L, const void* iq, const void* iw
     a.w8 = w8;
     if (G == 1) {
       constexpr int smem = IdxCfg<1, true>::kSmem;
-      cudaFuncSetAttribute(k_tc_index_scores<1, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      allow_smem<smem>(k_tc_index_scores<1, false, true>);
       CSA_LAUNCH(k_tc_index_scores<1, false, true>, dim3(grid), dim3(IdxCfg<1, true>::kThreads), smem, s, tk8, tq8,
                  tks, a);
     } else {
       constexpr int smem = IdxCfg<4, true>::kSmem;
-      cudaFuncSetAttribute(k_tc_index_scores<4, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      allow_smem<smem>(k_tc_index_scores<4, false, true>);
       CSA_LAUNCH(k_tc_index_scores<4, false, true>, dim3(grid), dim3(IdxCfg<4, true>::kThreads), smem, s, tk8, tq8,
                  tks, a);
     }
@@ -980,21 +980,21 @@ cudaError_t launch_tc_index_scores(const Dims& L, const void* iq, const void* iw
     CUtensorMap tqr;
     if (!make_tmap_2d_bf16(&tqr, qr16, (uint64_t)Q * 64, 128, 256, 64)) return cudaErrorInvalidValue;
     constexpr int smem = IdxCfg<1>::kSmem;
-    cudaFuncSetAttribute(k_tc_index_scores<1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    allow_smem<smem>(k_tc_index_scores<1, false>);
     CSA_LAUNCH(k_tc_index_scores<1, false>, dim3(grid), dim3(IdxCfg<1>::kThreads), smem, s, tk, tqr, tk, a);
     return cudaGetLastError();
   }
   if (G == 1 && overlap) {
     constexpr int smem = IdxCfg<1>::kSmem;
-    cudaFuncSetAttribute(k_tc_index_scores<1, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    allow_smem<smem>(k_tc_index_scores<1, true>);
     CSA_LAUNCH(k_tc_index_scores<1, true>, dim3(grid), dim3(IdxCfg<1>::kThreads), smem, s, tk, tq, tk, a);
   } else if (G == 1) {
     constexpr int smem = IdxCfg<1>::kSmem;
-    cudaFuncSetAttribute(k_tc_index_scores<1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    allow_smem<smem>(k_tc_index_scores<1, false>);
     CSA_LAUNCH(k_tc_index_scores<1, false>, dim3(grid), dim3(IdxCfg<1>::kThreads), smem, s, tk, tq, tk, a);
   } else {
     constexpr int smem = IdxCfg<4>::kSmem;
-    cudaFuncSetAttribute(k_tc_index_scores<4, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    allow_smem<smem>(k_tc_index_scores<4, false>);
     CSA_LAUNCH(k_tc_index_scores<4, false>, dim3(grid), dim3(IdxCfg<4>::kThreads), smem, s, tk, tq, tk, a);
   }
   return cudaGetLastError();

@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kPThreads = 192;  // warp 0 TMA, warp 1 MMA + TMEM, warps 2-5 epilogue
 constexpr int kABytes = 128 * 128;  // 128 rows x 64 bf16
+constexpr int kRingBytes = 200 * 1024;  // of one CTA an SM
 constexpr int kMaxSplits = 16;
 
 struct PjArgs {
@@ -261,10 +262,11 @@ int tc_project_cols(const Dims& L, int d, int ntok) {
 // step from 12.6k to 12.8k layer-steps/s against one CTA per SM with 8 stages.
 constexpr int kPairCtasPerSm = 2;
 
+constexpr int kPairBudget = 233472 / kPairCtasPerSm - 1024 - 1024 - 256;  // per-SM shared memory, reserve, slack
+static_assert(kPairBudget >= kABytes + 256 * 128, "a stage of the widest token tile");
 int pair_stages(int N, int n_kblk_min) {
   const int stage_bytes = kABytes + N * 128;
-  const int budget = 233472 / kPairCtasPerSm - 1024 - 1024 - 256;  // per-SM shared memory, reserve, slack
-  return max(1, min(8, min(n_kblk_min, budget / stage_bytes)));
+  return max(1, min(8, min(n_kblk_min, kPairBudget / stage_bytes)));
 }
 
 // Split counts for the two single-token projections run as one grid: powers of two no larger than each one's own
@@ -311,7 +313,7 @@ cudaError_t launch_tc_project_pair(const Dims& L, int d0, const void* wkv0, cons
   const int stage_bytes = kABytes + p0.N * 128;
   const int stages = pair_stages(p0.N, min(a0.n_kblk, a1.n_kblk));
   const size_t smem = 1024 + (size_t)stages * stage_bytes + 256;
-  cudaFuncSetAttribute(k_tc_project_pair, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  allow_smem<1024 + kPairBudget + 256>(k_tc_project_pair);
   CSA_LAUNCH(k_tc_project_pair, dim3(p0.m_tiles * s0 + p1.m_tiles * s1), dim3(kPThreads), smem, s, tw0, tg0, tw1,
              tg1, tx, a0, a1, p0.m_tiles, p1.m_tiles, stages);
   return cudaGetLastError();
@@ -333,9 +335,9 @@ cudaError_t launch_tc_project(const Dims& L, int d, const void* x, int ntok, con
     cudaMemsetAsync(tickets, 0, (size_t)p.m_tiles * p.n_tiles * sizeof(int), s);
   }
   const int stage_bytes = kABytes + p.N * 128;
-  const int stages = min(8, min(a.n_kblk, (200 * 1024) / stage_bytes));
+  const int stages = min(8, min(a.n_kblk, kRingBytes / stage_bytes));
   const size_t smem = 1024 + (size_t)stages * stage_bytes + 256;
-  cudaFuncSetAttribute(k_tc_project, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  allow_smem<1024 + kRingBytes + 256>(k_tc_project);
   dim3 grid(p.m_tiles, p.n_tiles, p.splits);
   CSA_LAUNCH(k_tc_project, dim3(grid), dim3(kPThreads), smem, s, tw, tg, tx, a, stages);
   return cudaGetLastError();

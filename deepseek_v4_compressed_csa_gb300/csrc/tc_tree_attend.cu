@@ -804,7 +804,7 @@ int clusters(int S) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
   int n = known[dev][S].load(std::memory_order_relaxed) - 1;
   if (n < 0) {
-    cudaFuncSetAttribute(k_tc_tree_attend<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    allow_smem<kSmem>(k_tc_tree_attend<true>);
     n = max_clusters(k_tc_tree_attend<true>, kThreads, kSmem, S);
     known[dev][S].store(n + 1, std::memory_order_relaxed);
   }
@@ -837,12 +837,12 @@ cudaError_t launch_tc_attend_tree(const Dims& L, const TreeAttend& t, const int3
   const long long tiles = ((t.scores ? L.topk : (long long)t.cap + t.T) + L.W + kPR - 1) / kPR;
   for (a.S = kMaxSplit; a.S > 1; a.S /= 2)
     if (tiles >= 2 * a.S && a.Q <= clusters(a.S)) {
-      cudaFuncSetAttribute(k_tc_tree_attend<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      allow_smem<kSmem>(k_tc_tree_attend<true>);
       const cudaError_t e = launch_pdl_cluster(k_tc_tree_attend<true>, dim3(a.Q * a.S), dim3(kThreads), kSmem, s, a.S,
                                                tq, to, tp, tr, a);
       return e != cudaSuccess ? e : cudaGetLastError();
     }
-  cudaFuncSetAttribute(k_tc_tree_attend<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  allow_smem<kSmem>(k_tc_tree_attend<false>);
   CSA_LAUNCH(k_tc_tree_attend<false>, dim3(min(a.Q, sms)), dim3(kThreads), kSmem, s, tq, to, tp, tr, a);
   return cudaGetLastError();
 }

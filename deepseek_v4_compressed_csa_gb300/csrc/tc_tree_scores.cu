@@ -446,7 +446,7 @@ cudaError_t launch_tc_tree_scores(const Dims& L, const void* iq, const void* iw,
       return cudaErrorInvalidValue;
     CSA_LAUNCH(k_tree_quant_iq, dim3((unsigned)((heads + 7) / 8)), dim3(256), 0, s,
                static_cast<const __nv_bfloat16*>(iq), a.iw, (int)heads, q8, w8);
-    cudaFuncSetAttribute(k_tc_tree_scores<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, TsCfg<true>::kSmem);
+    allow_smem<TsCfg<true>::kSmem>(k_tc_tree_scores<true>);
     CSA_LAUNCH(k_tc_tree_scores<true>, grid, dim3(TsCfg<true>::kThreads), TsCfg<true>::kSmem, s, tk, tr, tq, tks, trs,
                a);
     return cudaGetLastError();
@@ -455,7 +455,7 @@ cudaError_t launch_tc_tree_scores(const Dims& L, const void* iq, const void* iw,
       !make_tmap_2d_bf16(&tr, rows, (uint64_t)B * T, 128, 256, kRows) ||
       !make_tmap_2d_bf16(&tq, iq, heads, 128, 256, kN))
     return cudaErrorInvalidValue;
-  cudaFuncSetAttribute(k_tc_tree_scores<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, TsCfg<false>::kSmem);
+  allow_smem<TsCfg<false>::kSmem>(k_tc_tree_scores<false>);
   CSA_LAUNCH(k_tc_tree_scores<false>, grid, dim3(TsCfg<false>::kThreads), TsCfg<false>::kSmem, s, tk, tr, tq, tk, tr,
              a);
   return cudaGetLastError();

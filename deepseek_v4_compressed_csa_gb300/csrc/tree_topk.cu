@@ -201,7 +201,7 @@ cudaError_t launch_topk_tree_small(const Dims& L, const float* scores, int B, in
                                   const int32_t* n_rows, const int32_t* pos, int32_t* sel, TreeNode* nodes,
                                   int32_t* err, cudaStream_t s) {
   const size_t smem = (size_t)(cap + T) * sizeof(uint32_t);
-  cudaFuncSetAttribute(k_tree_topk, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+  allow_smem<64 * 1024>(k_tree_topk);
   CSA_LAUNCH(k_tree_topk, dim3(B * T), dim3(kThreads), smem, s, scores, cap, T, parent, pos, n_rows, L.ratio,
              L.topk, sel, nodes, err);
   return cudaGetLastError();

@@ -191,3 +191,12 @@ def test_index_rows_fp8_host_checks(lib):
     assert lib.csa_index_rows_fp8(ctypes.byref(L8), FAKE + 8, 4, FAKE, None) == B.CSA_ERR_ARG
     assert lib.csa_index_rows_fp8(ctypes.byref(L8), FAKE, 4, None, None) == B.CSA_ERR_ARG
     assert lib.csa_index_rows_fp8(ctypes.byref(L8), None, 0, None, None) == B.CSA_OK  # nothing to do
+
+
+def test_shared_memory_limits_are_constants():
+    """The limit of a kernel's dynamic shared memory is the function's, seen by every host thread: it is set in one
+    place, as a template argument, and so never to one call's own size."""
+    csrc = os.path.join(os.path.dirname(B.LIB_PATH), "..", "csrc")
+    uses = [(f, line.strip()) for f in sorted(os.listdir(csrc)) for line in open(os.path.join(csrc, f))
+            if "cudaFuncSetAttribute" in line]
+    assert [f for f, _ in uses] == ["kernels.h"] and "kBytes" in uses[0][1], uses

@@ -139,12 +139,12 @@ def recorded(call):
         def __getattr__(self, name):
             return lambda *args: got.append((name, args)) or 0
     keep = B.load_library, B._lib
-    B.load_library, B._lib = (lambda: keep[1]), Recorder()
+    B.load_library, B._lib = (lambda: Recorder()), Recorder()
     try:
         call()
     finally:
         B.load_library, B._lib = keep
-    (name, args), = got
+    (name, args), = [g for g in got if g[0] != "csa_workspace_size"]
     return getattr(csa.load_library(), name), args[:-1]
 
 
@@ -211,4 +211,51 @@ def test_attend_tree_selecting_from_different_capacities():
              i32(n * cfg.ratio), invf, out)
         jobs.append((lambda a=a, sel=sel, ws=ws, err=err: csa.attend_tree(*a, sel_out=sel, ws=ws, err=err),
                      (out, sel, err)))
+    side_by_side(jobs)
+
+
+def test_index_topk_of_different_capacities():
+    cfg, jobs = TINY, []
+    L, invf = G.lib_layer(cfg), csa_synth.inv_freq(cfg).cuda()
+    for cap in (17000, 30000, 50000):
+        iq, iw, keys = rnd(cfg, (1, cfg.Hi, cfg.Di), 20), rnd(cfg, (1, cfg.Hi), 21), rnd(cfg, (1, cap, cfg.Di), 22)
+        sel, n_sel, err = z(1, cfg.topk, dt=torch.int32), i32(0), i32(0)
+        ws = z(csa.workspace_size(L, csa.OP_INDEX_TOPK, 1, 1, cap), dt=torch.uint8)
+        a = (L, iq, iw, keys, i32(1000), i32(1000 * cfg.ratio - 1), invf, sel, n_sel)
+        jobs.append((lambda a=a, ws=ws, err=err: csa.index_topk(*a, ws=ws, err=err), (sel, n_sel, err)))
+    side_by_side(jobs)
+
+
+@pytest.mark.parametrize("pair", [False, True])
+def test_compress_append_of_different_sizes(pair):
+    """Three tokens a sequence from position 0: no window completes, so that a call can be made again and again."""
+    cfg, jobs = FLASH, []
+    comps = [G.lib_comp(csa_synth.compressor(cfg, w)) for w in ("attn", "index")]
+    L, invf = G.lib_layer(cfg), csa_synth.inv_freq(cfg).cuda()
+    for nb, T in ((2, 3), (16, 3), (40, 2)) if pair else ((1, 3), (16, 3), (100, 3)):
+        x, pos, err = rnd(cfg, (nb, T, cfg.X), 30 + nb), z(nb, dt=torch.int32), i32(0)
+        front = [z(nb, cfg.frontier_slots, 4 * d) for d in (512, 128)]
+        pools, n = [z(nb, 8, d) for d in (512, 128)], [z(nb, dt=torch.int32) for _ in range(2)]
+        ws = z(csa.workspace_size(L, csa.OP_COMPRESS_PAIR if pair else csa.OP_COMPRESS, nb, T, 8), dt=torch.uint8)
+
+        def call(x=x, pos=pos, err=err, front=front, pools=pools, n=n, ws=ws):
+            if pair:
+                csa.compress_append_pair(L, *comps, x, pos, front[0], pools[0], n[0], front[1], pools[1], n[1], invf,
+                                         ws=ws, err=err)
+            else:
+                csa.compress_append(L, comps[0], x, pos, front[0], pools[0], n[0], invf, ws=ws, err=err)
+        jobs.append((call, (*pools, *front, *n, err)))
+    side_by_side(jobs)
+
+
+def test_attend_decode_of_layers_of_different_widths():
+    jobs = []
+    for D in (64, 256, 512):
+        cfg = TINY.replace(D=D)
+        q, kv, sink = rnd(cfg, (2, cfg.H, D), 70), rnd(cfg, (2, D), 71), rnd(cfg, (cfg.H,), 72)
+        window, pool, out, err = rnd(cfg, (2, cfg.W, D), 73), rnd(cfg, (2, 40, D), 74), z(2, cfg.H, D, dt=cfg.storage), i32(0)
+        L = G.lib_layer(cfg)
+        ws = z(csa.workspace_size(L, csa.OP_ATTEND_DECODE, 2, 1, 40), dt=torch.uint8)
+        a = (L, q, kv, sink, window, pool, i32(30, 17), None, None, i32(121, 70), csa_synth.inv_freq(cfg).cuda(), out)
+        jobs.append((lambda a=a, ws=ws, err=err: csa.attend_decode(*a, ws=ws, err=err), (out, window, err)))
     side_by_side(jobs)
