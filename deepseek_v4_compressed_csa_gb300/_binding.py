@@ -733,6 +733,14 @@ def _tree_comp(layer: Layer, comp: Compressor, which: str, dev: int) -> bytes:
         (f"{which}.norm_w", comp.norm_w, torch.float32, (d,))), d)
 
 
+class RowOutputs(list):
+    """norm_rope's outputs, a list of tensors; `err` is the call's device error word tensor."""
+
+    def __init__(self, outs, err):
+        super().__init__(outs)
+        self.err = err
+
+
 def norm_rope(layer: Layer, xs, pos=None, inv_freq=None, parent=None, weights=None, norm=None, outs=None, err=None,
               stream=None):
     """csa_norm_rope: every head row of the tensors xs (up to four, each [B, T, heads, dim] or [B, T, dim]) RMS-normed
@@ -740,7 +748,9 @@ def norm_rope(layer: Layer, xs, pos=None, inv_freq=None, parent=None, weights=No
     tree `parent` [B, T], or pos[b] + i without one.  inv_freq None: no rotation (for the calls that rotate by
     themselves).  An x may be a slice of a wider tensor: its heads contiguous, one stride from token to token, at least
     a token's size (an expanded tensor is refused).
-    Returns the outputs (`outs`, or new tensors; a new tensor's rows of unused tree slots are zeros)."""
+    Returns the outputs (`outs`, or new tensors; a new tensor's rows of unused tree slots are zeros) as a list whose `err`
+    is the device error word tensor; rows of tokens that it reports (pos[b] < 0, an inconsistent tree) are not written, and
+    in a new tensor hold nothing defined unless it has tree slots."""
     n = len(xs)
     if not 1 <= n <= 4:
         raise ValueError(f"norm_rope takes 1 to 4 tensors, got {n}")
@@ -789,9 +799,9 @@ def norm_rope(layer: Layer, xs, pos=None, inv_freq=None, parent=None, weights=No
     if inv_freq is not None:
         p_pos, p_frq = _ptrs(dev, ("pos", pos, torch.int32, (B,)),
                              ("inv_freq", inv_freq, torch.float32, (layer.R // 2,)))
-    _tree_call("csa_norm_rope", dev, stream, layer._packed(), rows, n, B, T, p_par, p_pos, p_frq,
-               _tree_err(err, dev, stream).data_ptr())
-    return list(outs)
+    err = _tree_err(err, dev, stream)
+    _tree_call("csa_norm_rope", dev, stream, layer._packed(), rows, n, B, T, p_par, p_pos, p_frq, err.data_ptr())
+    return RowOutputs(outs, err)
 
 
 def compress_tree(layer: Layer, comp_a: Compressor, x, parent, pos, frontier_a, proj_a, rows_a, inv_freq, comp_i=None,

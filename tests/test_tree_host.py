@@ -309,3 +309,14 @@ def test_norm_rope_takes_slices_of_wider_tensors(lib, calls):
         fn, args = calls.pop()
         row = _rows_of(args)
         assert fn == "csa_norm_rope" and row.x_stride == stride and row.x == x.data_ptr(), (x.shape, x.stride())
+
+
+def test_norm_rope_returns_its_error_word(lib, calls, monkeypatch):
+    """Without err= the call makes the word: it lives with the outputs, where the caller can read it."""
+    monkeypatch.setattr(B, "_tree_new", lambda device, stream, new, *size, dtype: _cuda_like(new(*size, dtype=dtype)))
+    x = _cuda_like(z(2, 3, 8, 128))
+    got = csa.norm_rope(LAYER, [x], outs=[_cuda_like(z(2, 3, 8, 128))])
+    assert isinstance(got, list) and len(got) == 1
+    assert got.err.dtype == torch.int32 and got.err.tolist() == [0] and calls[0][1][-1] == got.err.data_ptr()
+    own = _cuda_like(z(1, dt=torch.int32))
+    assert csa.norm_rope(LAYER, [x], outs=[x], err=own).err is own and calls[1][1][-1] == own.data_ptr()
