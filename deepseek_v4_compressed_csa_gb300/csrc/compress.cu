@@ -48,8 +48,8 @@ template <typename T, int NTOK>
 __global__ void __launch_bounds__(256) k_project_simt(const T* __restrict__ x, const T* __restrict__ wkv,
                                                       const T* __restrict__ wg, int ntok, int X, int Ld,
                                                       T* __restrict__ out) {
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();  // (k_tree_pool reads the tree and the positions ahead of its own wait)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int o = blockIdx.x * 8 + warp;
   if (o >= 2 * Ld) return;

@@ -168,7 +168,9 @@ __device__ __forceinline__ int block_excl_count(int flag, int* warp_tot, int* to
 
 // Selections of a tree's nodes (kTree instances of the top-k kernels): query q is node q % T of sequence q / T, its
 // columns are the n committed rows and the T rows of the tree (the last ones visible by the path alone), its row of
-// scores is cap + T long, and what the attention reads of the node is written to nodes[q].
+// scores is cap + T long, and what the attention reads of the node is written to nodes[q].  These kernels let the
+// attention start only once all work before them is complete: it reads queries, parents, latent rows and the window ring
+// ahead of its own wait, and a kernel that writes one of them may have let its successors start early.
 struct TopkTree {
   const int32_t* parent;
   int T;
@@ -220,8 +222,9 @@ __global__ void __launch_bounds__(1024) k_topk(const float* __restrict__ scores,
                                                const int32_t* __restrict__ n_rows, const int32_t* __restrict__ pos,
                                                int pos0, const int32_t* __restrict__ cu, int ratio, int topk,
                                                int32_t* __restrict__ sel, int32_t* __restrict__ n_sel, TopkTree tr) {
-  pdl_trigger();
+  if (!kTree) pdl_trigger();
   pdl_wait();
+  if (kTree) pdl_trigger();
   __shared__ int hist[256];
   __shared__ int warp_tot[32];
   __shared__ int s_total;
@@ -409,8 +412,9 @@ __global__ void __launch_bounds__(1024) k_topk_smem(const float* __restrict__ sc
                                                     const int32_t* __restrict__ pos, int pos0,
                                                     const int32_t* __restrict__ cu, int ratio, int topk,
                                                     int32_t* __restrict__ sel, int32_t* __restrict__ n_sel, TopkTree tr) {
-  pdl_trigger();
+  if (!kTree) pdl_trigger();
   pdl_wait();
+  if (kTree) pdl_trigger();
   extern __shared__ uint32_t sm_keys[];  // [cap (+ T)] keys, then hist[2048]
   const int stride = kTree ? cap + tr.T : cap;
   int* hist = reinterpret_cast<int*>(sm_keys + stride);
@@ -584,7 +588,7 @@ __global__ void __launch_bounds__(1024) k_topk_reg(const float* __restrict__ sco
                                                    int32_t* __restrict__ n_sel, const __nv_bfloat16* __restrict__ qr,
                                                    const float* __restrict__ w, const __nv_bfloat16* __restrict__ keys,
                                                    TopkTree tr) {
-  pdl_trigger();
+  if (!kTree) pdl_trigger();
   __shared__ int hist[3][2048];  // pass n counts into hist[n] and clears the next pass's bins
   __shared__ int warp_tot[32], warp_tot2[32];
   __shared__ float part[2][64];
@@ -600,6 +604,7 @@ __global__ void __launch_bounds__(1024) k_topk_reg(const float* __restrict__ sco
   const int r0 = threadIdx.x * K;
   const float* sc = scores + (size_t)q * (kTree ? cap + tr.T : cap) + r0;
   pdl_wait();
+  if (kTree) pdl_trigger();
   float fk[kTopkRegKeys];
 #pragma unroll
   for (int i = 0; i < kTopkRegKeys; ++i) fk[i] = (i < K && r0 + i < nv_max) ? __ldg(sc + i) : 0.f;

@@ -78,7 +78,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_tc_tree_project(const __grid_constant__ CUtensorMap tm_wkv0, const __grid_constant__ CUtensorMap tm_wg0,
                       const __grid_constant__ CUtensorMap tm_wkv1, const __grid_constant__ CUtensorMap tm_wg1,
                       const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ TpArgs a) {
-  pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full;
@@ -116,6 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   pdl_wait();
+  pdl_trigger();  // (not before: the pooling reads the tree and the positions ahead of its own wait)
   if (warp == 1) {
     tc::tmem_alloc(&tmem_slot, tcols);
     tc::tmem_relinquish();

@@ -461,13 +461,16 @@ struct TreeAttnArgs {
   T* out;
 };
 
-// One warp per node: the records of a call without a selection.
+// One warp per node: the records of a call without a selection.  early: the attention behind it reads nothing ahead of its
+// own wait (the persistent kernel; 0.6 us of 64 for 128 nodes); otherwise it starts only once all work before this kernel
+// is complete, as behind a selection (indexer.cu, TopkTree).
 __global__ void __launch_bounds__(256) k_tree_nodes(const int32_t* __restrict__ parent, int T_, int Q,
                                                     const int32_t* __restrict__ pos,
                                                     const int32_t* __restrict__ n_rows, int cap, int ratio,
-                                                    TreeNode* __restrict__ nodes, int32_t* err) {
-  pdl_trigger();
+                                                    TreeNode* __restrict__ nodes, int early, int32_t* err) {
+  if (early) pdl_trigger();
   pdl_wait();
+  if (!early) pdl_trigger();
   const int q = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (q >= Q) return;
   NodeView v;
@@ -751,6 +754,19 @@ template <typename T>
 static cudaError_t attend_tree_t(const Dims& L, const TreeAttend& t, int32_t* err, cudaStream_t s) {
   const int Q = t.B * t.T;
   TreeAttnArgs<T> a{};
+  // Tensor-core shapes.  Few nodes: S splits of one 160-row tile each, a cluster per query, while all clusters run at
+  // once; eight of half a tile where four would do (8 nodes of 640 keys: 22.5 us instead of 23.4).  More nodes or keys
+  // (S = 0): tc_tree_attend.cu.
+  const bool codes_fit = (long long)t.B * t.cap < INT32_MAX && (long long)t.B * L.Wr < (1 << 28);
+  const bool on_tc = tc_attend_supported(L) && codes_fit;
+  int S = 0;
+  if (on_tc) {
+    const long long n_max = t.scores ? L.topk : (long long)t.cap + t.T;
+    S = 1;
+    while (S <= 4 && ((L.W + S - 1) / S + (n_max + S - 1) / S > 160 || Q > tc_attend_tree_split_max(S))) S *= 2;
+    if (S > 4) S = 0;
+    if (S == 4 && L.W + n_max >= 8 * 80 && Q <= tc_attend_tree_split_max(8)) S = 8;
+  }
   if (t.scores) {
     int32_t* sel = t.sel_out ? t.sel_out : t.ws.sel;
     cudaError_t e = launch_topk_tree(L, t.scores, t.B, t.T, t.parent, t.cap, t.n_rows, t.pos, sel, t.ws.nodes, err, s);
@@ -758,22 +774,10 @@ static cudaError_t attend_tree_t(const Dims& L, const TreeAttend& t, int32_t* er
     a.sel = sel;
   } else {
     CSA_LAUNCH(k_tree_nodes, dim3((Q + 7) / 8), dim3(256), 0, s, t.parent, t.T, Q, t.pos, t.n_rows, t.cap, L.ratio,
-               t.ws.nodes, err);
+               t.ws.nodes, on_tc && S == 0, err);
   }
-  // Tensor-core shapes.  Few nodes: S splits of one 160-row tile each, a cluster per query, while all clusters run at
-  // once; eight of half a tile where four would do (8 nodes of 640 keys: 22.5 us instead of 23.4).  More nodes or keys:
-  // tc_tree_attend.cu.
-  const bool codes_fit = (long long)t.B * t.cap < INT32_MAX && (long long)t.B * L.Wr < (1 << 28);
-  if (tc_attend_supported(L) && codes_fit) {
-    const long long n_max = t.scores ? L.topk : (long long)t.cap + t.T;
-    int S = 1;
-    while (S <= 4 && ((L.W + S - 1) / S + (n_max + S - 1) / S > 160 || Q > tc_attend_tree_split_max(S))) S *= 2;
-    if (S <= 4) {
-      if (S == 4 && L.W + n_max >= 8 * 80 && Q <= tc_attend_tree_split_max(8)) S = 8;
-      return launch_tc_attend_tree_split(L, t, a.sel, S, err, s);
-    }
-    return launch_tc_attend_tree(L, t, a.sel, err, s);
-  }
+  if (S > 0) return launch_tc_attend_tree_split(L, t, a.sel, S, err, s);
+  if (on_tc) return launch_tc_attend_tree(L, t, a.sel, err, s);
   a.q = static_cast<const T*>(t.q); a.kv = static_cast<const T*>(t.kv); a.window = static_cast<const T*>(t.window);
   a.pool = static_cast<const T*>(t.pool); a.rows = static_cast<const T*>(t.rows);
   a.nodes = t.ws.nodes; a.sink = t.sink; a.inv_freq = t.inv_freq;

@@ -32,7 +32,6 @@ __global__ void __launch_bounds__(kThreads) k_tree_topk(const float* __restrict_
                                                              const int32_t* __restrict__ n_rows, int ratio, int topk,
                                                              int32_t* __restrict__ sel, TreeNode* __restrict__ nodes,
                                                              int32_t* err) {
-  pdl_trigger();
   extern __shared__ uint32_t keys[];  // [cap + T]
   __shared__ int hist[kBins];
   __shared__ int wtot[kWarps], w_gt[kWarps], w_eq[kWarps];
@@ -43,6 +42,7 @@ __global__ void __launch_bounds__(kThreads) k_tree_topk(const float* __restrict_
   const int n = max(0, min(cap, pos[q / T] / ratio));
   for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
   pdl_wait();
+  pdl_trigger();  // (indexer.cu, TopkTree)
   const float* sc = scores + (size_t)q * (cap + T);
   constexpr int kU = 8;
   float f[kU];

@@ -42,6 +42,9 @@
  *     positions) and the window ring, so these must be complete when the call
  *     is enqueued behind work that does not trigger early (any ordinary kernel
  *     or copy; csa_advance_positions for pos).
+ *     Of the *_tree calls' inputs these are x, the weights and pos; whatever else
+ *     they read (parent, kv, rings, pools, draft buffers) may come from any call
+ *     before them.
  *   - Errors found on the host are returned synchronously, before anything is
  *     enqueued (fail closed: nothing is modified).  Errors that depend on
  *     device-resident values (positions, row counts, indices) are OR-ed into

@@ -50,3 +50,39 @@ def test_norm_rope_reports_skipped_tokens(own):
     got = csa.norm_rope(L, [x], i32(5, 6, 7), invf, parent=par)
     assert got.err.item() == csa.DEV_STATE
     assert not got[0][:, 2].any() and torch.equal(got[0][:, :2], good[0][:, :2])
+
+
+# ------------------------------------------------------------------------------------------------ order of calls
+
+
+@pytest.mark.parametrize("select", [True, False])
+def test_tree_calls_right_behind_a_decode_step(select):
+    """attend_decode puts its token into the window ring and lets its successor start before it has; attend_tree behind
+    it (its own positions in hand, nothing in between) sees that token all the same."""
+    cfg = FLASH
+    nb, T, cap = 2, 4, 700
+    L, invf, sink = G.lib_layer(cfg), csa_synth.inv_freq(cfg).cuda(), csa_synth.sinks(cfg).cuda()
+    pos, n = i32(2049, 1201), i32(512, 300)
+    nxt = pos + 1
+    pool, ring = T0.rnd(cfg, (nb, cap, 512), 910), T0.rnd(cfg, (nb, cfg.W, 512), 911)
+    q, rows, par = T0.rnd(cfg, (nb, T, 64, 512), 912), T0.rnd(cfg, (nb, T, 512), 913), i32(*[-1, 0, 0, -1] * nb).view(nb, T)
+    kv, q1 = T0.rnd(cfg, (nb, T, 512), 914), T0.rnd(cfg, (nb, 64, 512), 915)
+    scores = T0.rnd(cfg, (nb, T, cap + T), 916, dtype=torch.float32) if select else None
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = [torch.empty(csa.workspace_size(L, op, nb, t, cap) + 256, dtype=torch.uint8, device="cuda")
+          for op, t in ((csa.OP_ATTEND_DECODE, 1), (csa.OP_ATTEND_TREE, T))]
+    outs, before = [], None
+    for k in range(30):
+        new = T0.rnd(cfg, (nb, 512), 920 + k, scale=8.0)
+        for wait in (True, False):
+            window, out, out1 = ring.clone(), torch.zeros_like(q), torch.zeros_like(q1)
+            torch.cuda.synchronize()
+            csa.attend_decode(L, q1, new, sink, window, pool, n, None, None, pos, invf, out1, ws=ws[0], err=err)
+            if wait:
+                torch.cuda.synchronize()
+            csa.attend_tree(L, q, kv, sink, window, pool, rows, scores, par, n, nxt, invf, out, ws=ws[1], err=err)
+            torch.cuda.synchronize()
+            outs.append(out)
+        assert torch.equal(outs[-1], outs[-2]) and err.item() == 0
+        assert before is None or not torch.equal(outs[-1], before)
+        before = outs[-1]
