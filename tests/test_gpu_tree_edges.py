@@ -9,7 +9,6 @@ import pytest
 import torch
 
 import csa_synth
-from oracle import csa_oracle as O
 from tests import _tree as TR
 from tests._common import f64, oracle_layer
 
@@ -86,3 +85,269 @@ def test_tree_calls_right_behind_a_decode_step(select):
         assert torch.equal(outs[-1], outs[-2]) and err.item() == 0
         assert before is None or not torch.equal(outs[-1], before)
         before = outs[-1]
+
+
+# ------------------------------------------------------------------------------------------------ selections
+
+
+SELECTIONS = {
+    # columns a node, trees: which kernel selects (few nodes: 256 threads up to 33 KB of keys, then keys in registers, in
+    # shared memory, in global memory; more nodes than SMs: 256 threads)
+    "small_blocks": (1000, [TR.chain(3)]),
+    "registers": (12000, [TR.chain(3)]),
+    "registers_64_nodes": (5000, [TR.bushy(64)]),
+    "shared": (20000, [TR.chain(3), TR.star(2)]),
+    "global": (60000, [TR.chain(3)]),
+    "many_nodes": (1100, [TR.chain(64), TR.bushy(64), TR.bushy(64, 1)]),
+    "many_nodes_15K": (15000, [TR.chain(64), TR.bushy(64), TR.bushy(25, 1)]),
+}
+
+
+def edge_scores(kind, shape, seed):
+    r = np.random.default_rng([13, seed])
+    lowest, inf = np.finfo(np.float32).min, np.float32(np.inf)
+    s = r.standard_normal(shape, dtype=np.float32)
+    if kind == "ties":
+        s = r.integers(0, 4, shape).astype(np.float32)
+    elif kind == "zeros":  # both zeros: one value
+        s = np.where(r.random(shape) < 0.5, np.float32(0.0), np.float32(-0.0))
+    elif kind == "minus_inf":  # nearly all of them: the selection has to take some
+        s = np.where(r.random(shape) < 0.002, s, -inf)
+    elif kind == "lowest":
+        s = np.where(r.random(shape) < 0.002, s, np.where(r.random(shape) < 0.3, -inf, lowest))
+    elif kind == "plus_inf":
+        s = np.where(r.random(shape) < 0.9, inf, s)
+    elif kind == "denormals":
+        s = (r.integers(-5, 6, shape) * np.float32(1e-45)).astype(np.float32)
+    elif kind == "ascending":
+        s = np.broadcast_to(np.arange(shape[-1], dtype=np.float32) - 1e4, shape).copy()
+    elif kind == "descending":
+        s = np.broadcast_to(-np.arange(shape[-1], dtype=np.float32), shape).copy()
+    return torch.from_numpy(s.astype(np.float32)).cuda()
+
+
+@pytest.mark.parametrize("topk", [16, 700])
+@pytest.mark.parametrize("where", list(SELECTIONS))
+def test_selection_at_the_borders_of_the_order(where, topk):
+    """Ties, both zeros, infinities, the lowest float and denormals, with the threshold among them, in every selection
+    kernel; what a node does not see is NaN."""
+    cap, trees = SELECTIONS[where]
+    cfg = TINY.replace(topk=topk)
+    nb, T = len(trees), max(len(t) for t in trees)
+    pos = [4 * (cap - 20 - 7 * b) + 2 for b in range(nb)]
+    p = i32(*pos)
+    layer, invf = oracle_layer(cfg), f64(csa_synth.inv_freq(cfg)).astype(np.float32)
+    q, kv, sink = T0.rnd(cfg, (nb, T, cfg.H, cfg.D), 940), T0.rnd(cfg, (nb, T, cfg.D), 941), T0.rnd(cfg, (cfg.H,), 942)
+    window, pool = T0.rnd(cfg, (nb, cfg.W, cfg.D), 943), T0.rnd(cfg, (1, cap, cfg.D), 944).expand(nb, -1, -1).contiguous()
+    rows = T0.rnd(cfg, (nb, T, cfg.D), 945)
+    for n, kind in enumerate(("ties", "zeros", "minus_inf", "lowest", "plus_inf", "denormals", "ascending", "descending")):
+        scores = edge_scores(kind, (nb, T, cap + T), n)
+        for b in range(nb):
+            scores[b, :, pos[b] // 4 + T:] = float("nan")
+            for i, path in enumerate(TR.paths(TR.padded(trees[b], T))):
+                if path is None or (pos[b] + len(path)) % 4:
+                    scores[b, :, pos[b] // 4 + i] = float("nan")
+        out = torch.full((nb, T, cfg.H, cfg.D), SENTINEL, device="cuda")
+        sel = torch.full((nb, T, topk), -9, dtype=torch.int32, device="cuda")
+        err = csa.attend_tree(G.lib_layer(cfg), q, kv, sink, window, pool, rows, scores, T0.parents(trees, T), p // 4, p,
+                              csa_synth.inv_freq(cfg).cuda(), out, sel_out=sel)
+        assert err.item() == 0
+        T0.check_tree_outputs(cfg, layer, trees, pos, q, kv, sink, window, pool, rows, scores, out, sel, invf, sampled=2)
+
+
+# ------------------------------------------------------------------------------------------------ splits of a node's keys
+
+
+SPLIT_LAYERS = {"topk16": FLASH.replace(cid=71, topk=16), "topk32": FLASH.replace(cid=72, topk=32),
+                "topk150": FLASH.replace(cid=73, topk=150), "topk151_w99": FLASH.replace(cid=74, topk=151, W=99),
+                "r128": FLASH.replace(cid=75, ratio=128)}
+SPLIT_CASES = {
+    # one split (window and selection in one tile of 160 rows), its last row used, two splits, no selection
+    "one_split": ("topk16", [TR.bushy(9), TR.chain(7), TR.star(3)], [803, 41, 0], True),
+    "one_split_full": ("topk32", [TR.bushy(16, s) for s in range(9)], [900 + 61 * s for s in range(9)], True),
+    "one_split_short": ("topk32", [TR.bushy(5), [-1]], [70, 2], True),
+    "two_splits": ("topk150", [TR.bushy(7), TR.chain(9)], [1201, 603], True),
+    "two_splits_odd": ("topk151_w99", [TR.bushy(7), TR.chain(9)], [1201, 80], True),
+    "one_split_rows": ("r128", [TR.bushy(7), TR.chain(8)], [900, 127], False),
+}
+
+
+@pytest.mark.parametrize("case", list(SPLIT_CASES))
+@pytest.mark.parametrize("loud", [1.0, 24.0])
+def test_attend_tree_in_few_splits(case, loud, monkeypatch):
+    name, trees, pos, select = SPLIT_CASES[case]
+    monkeypatch.setitem(T0.LAYERS, name, SPLIT_LAYERS[name])
+    monkeypatch.setitem(T0.AT_CASES, case, (name, trees, pos, "normal" if select else None))
+    monkeypatch.setitem(T0.EDGE_LAYERS, name, SPLIT_LAYERS[name])
+    monkeypatch.setitem(T0.EDGE_CASES, case, (name, trees, pos, select))
+    if loud == 1.0:
+        T0.test_attend_tree_against_float64(case)
+    T0.test_attend_tree_sinks_and_large_logits(case, loud)
+
+
+# ------------------------------------------------------------------------------------------------ errors
+
+
+ERROR_CASES = {
+    # layer, nodes a sequence, sequences, first position, selection: the few nodes' kernel with eight, four and one
+    # splits, a cluster of CTAs over a long list, a CTA per SM, fp8 index rows
+    "few": ("flash", 3, 6, 2500, True),
+    "few_4_splits": ("flash", 6, 6, 2500, True),
+    "few_rows": ("flash", 3, 6, 9001, False),
+    "many": ("flash", 16, 12, 2500, True),
+    "many_rows": ("r128", 24, 8, 30000, False),
+    "one_split": ("topk16", 4, 6, 900, True),
+    "fp8": ("fp8", 7, 6, 2500, True),
+}
+
+
+@pytest.mark.parametrize("case", list(ERROR_CASES))
+def test_errors_on_the_tensor_core_paths(case):
+    """Sequence 0: parents at or above their node.  1: a node under an unused slot.  2: one row too many.  3: a negative
+    position.  4: more rows than the pool has.  The call reports them, leaves those nodes' entries as they were and gives
+    every other node what it gives without them."""
+    name, T, nb, p0, select = ERROR_CASES[case]
+    cfg = {"flash": FLASH, "fp8": FLASH, **SPLIT_LAYERS}[name]
+    trees = [TR.bushy(T, s) for s in range(nb)]
+    trees[0], trees[1] = TR.chain(T), TR.chain(T)
+    pos = [p0 + 37 * b for b in range(nb)]
+    cap = max(pos) // cfg.ratio + 20
+
+    def state():
+        d = T0._step(cfg, trees, pos, cap, seed=500)
+        if name == "fp8":
+            d["L"] = dataclasses.replace(d["L"], index_fp8=True)
+            keys = torch.zeros(nb, cap, csa.FP8_ROW_BYTES, dtype=torch.uint8, device="cuda")
+            csa.index_rows_fp8(d["L"], d["st"].ikeys, keys)
+            d["st"].ikeys, d["rows_i"] = keys, torch.zeros(nb, T, csa.FP8_ROW_BYTES, dtype=torch.uint8, device="cuda")
+        if not select:
+            d.pop("scores", None)
+            d.pop("sel", None)
+        return d
+
+    def run(d, err):
+        if select or not cfg.has_indexer:
+            return T0.run_step(cfg, d, err)
+        T0.run_step(cfg, dict(d, scores=torch.zeros(nb, T, cap + T, device="cuda"), sel=None), err)
+        csa.attend_tree(d["L"], d["q2"], d["kv2"], d["sink"], d["st"].window, d["st"].pool, d["rows_a"], None, d["par"],
+                        d["n_a"], d["st"].pos, d["invf"], d["out"], err=err)
+
+    good, bad = state(), state()
+    err = T0.err_word()
+    names = [k for k in ("q2", "kv2", "proj_a", "rows_a", "proj_i", "rows_i", "scores", "sel", "out") if k in good]
+    for d in (good, bad):
+        for k in names:
+            d[k].fill_(7)
+    run(good, err)
+    assert err.item() == 0
+    dead = torch.zeros(nb, T, dtype=torch.bool, device="cuda")  # by their tree or position: no call touches them
+    bad["par"][0, T - 1] = T - 1
+    bad["par"][0, 1] = 1000
+    dead[0, 1:] = True  # (a chain: everything behind node 1)
+    bad["par"][1, 0] = -9
+    dead[1] = True
+    bad["st"].pos[3] = -5
+    dead[3] = True
+    bad["n_a"][2] += 1
+    bad["n_a"][4] = 1 << 30
+    counted = dead.clone()  # and by their row count: the calls that take one
+    counted[2] = counted[4] = True
+    run(bad, err)
+    assert err.item() == csa.DEV_STATE
+    for k in names:
+        gone = counted if k in ("scores", "sel", "out") else dead
+        assert (bad[k][gone] == 7).all(), k
+        assert torch.equal(bad[k][~gone], good[k][~gone]), k
+    # each call by itself reports what it is given
+    for k in range(2 if not cfg.has_indexer else 3):
+        e = T0.err_word()
+        d = bad
+        if k == 0:
+            csa.attend_tree(d["L"], d["q2"], d["kv2"], d["sink"], d["st"].window, d["st"].pool, d["rows_a"],
+                            d.get("scores"), d["par"], d["n_a"], d["st"].pos, d["invf"], d["out"], err=e)
+        elif k == 1:
+            csa.compress_tree(d["L"], d["ca"], d["x"], d["par"], d["st"].pos, d["st"].front_attn, d["proj_a"],
+                              d["rows_a"], d["invf"], err=e)
+        else:
+            csa.index_scores_tree(d["L"], d["iq2"], d["iw"], d["st"].ikeys, d["rows_i"], d["par"], d["n_a"], d["st"].pos,
+                                  torch.zeros(nb, T, cap + T, device="cuda"), err=e)
+        assert e.item() == csa.DEV_STATE, k
+
+
+# ------------------------------------------------------------------------------------------------ after a commit
+
+
+AFTER_CASES = {
+    "flash": (FLASH, [TR.chain(8), TR.bushy(8)], [2045, 4098]),
+    "flash_r128": (FLASH.replace(cid=76, ratio=128), [TR.chain(8), TR.bushy(8)], [1148, 380]),
+    "tiny_f32": (TINY, [TR.chain(12), TR.bushy(12)], [61, 130]),
+}
+
+
+@pytest.mark.parametrize("case", list(AFTER_CASES))
+def test_a_committed_cache_decodes_on(case):
+    """A tree step and its commit, then decoding: projections, selections and outputs against the oracle, which starts
+    from the committed cache."""
+    from tests.test_gpu_parity import _oracle_decode_check, _seq_projs, _step_rows
+    from tests._common import oracle_comp
+    cfg, trees, pos = AFTER_CASES[case]
+    d, err = T0._step(cfg, trees, pos, max(pos) // cfg.ratio + 40, seed=600), T0.err_word()
+    st = d["st"]
+    T0.run_step(cfg, d, err)
+    T0.run_commit(cfg, d, i32(*[len(t) - 1 for t in trees]), err)
+    assert err.item() == 0 and st.pos.tolist() == [p + len(TR.paths(t)[-1]) for p, t in zip(pos, trees)]
+    st.n_rows = d["n_a"]
+    run = G.Runner(cfg)
+    layer, sink, invf = oracle_layer(cfg), f64(csa_synth.sinks(cfg)), f64(csa_synth.inv_freq(cfg)).astype(np.float32)
+    comps = [None if c is None else oracle_comp(c) for c in (run.ca_host, run.ci_host)]
+    cut = lambda t, b: None if t is None else f64(t[b:b + 1])  # noqa: E731
+    # (rows past the committed ones are not zero in this cache and never read)
+    state = [dict(pool=cut(st.pool, b), ikeys=cut(st.ikeys, b), window=cut(st.window, b), front_a=cut(st.front_attn, b),
+                  front_i=cut(st.front_index, b), n_rows=st.n_rows[b:b + 1].cpu().numpy().astype(np.int64),
+                  pos=st.pos[b:b + 1].cpu().numpy().astype(np.int64)) for b in range(2)]
+    for k in range(6):
+        si = csa_synth.step_inputs(cfg.replace(cid=cfg.cid + 700), k, B=2)
+        out, sel, n_sel = run.decode_step(st, si)
+        torch.cuda.synchronize()
+        assert run.err.item() == 0
+        for b in range(2):
+            _oracle_decode_check(layer, *comps, state[b], _step_rows(si, b), sink, invf, out[b].cpu(),
+                                 None if sel is None else sel[b].cpu().numpy(),
+                                 None if n_sel is None else int(n_sel[b]), f"step {k} seq {b}", _seq_projs(run, b))
+
+
+@pytest.mark.parametrize("case", list(AFTER_CASES))
+def test_trim_behind_a_commit_is_a_shorter_commit(case):
+    """An accepted path rewound by csa_trim against the commit of its first nodes alone: the same state, and the same bits
+    in every decode step after it."""
+    cfg, trees, pos = AFTER_CASES[case]
+    cfg = cfg.replace(cid=cfg.cid + 20, rollback=16)
+    cap = max(pos) // cfg.ratio + 40
+    a, b = (T0._step(cfg, trees, pos, cap, seed=700) for _ in range(2))
+    paths = [TR.paths(t)[-1] for t in trees]
+    back = [len(paths[0]) - 1, len(paths[1]) - 2]
+    err = T0.err_word()
+    for d in (a, b):
+        T0.run_step(cfg, d, err)
+    hw = a["st"].pos.clone()
+    T0.run_commit(cfg, a, i32(*[p[-1] for p in paths]), err)
+    T0.run_commit(cfg, b, i32(*[p[-1 - n] for p, n in zip(paths, back)]), err)
+    csa.trim(a["L"], i32(*back), a["st"].pos, a["n_a"], a["n_i"] if cfg.has_indexer else None, hw, err=err)
+    assert err.item() == 0
+    assert torch.equal(a["st"].pos, b["st"].pos) and torch.equal(a["n_a"], b["n_a"])
+    runs = [G.Runner(cfg) for _ in range(2)]
+    for d in (a, b):
+        d["st"].n_rows = d["n_a"]
+    for k in range(10):
+        si = csa_synth.step_inputs(cfg.replace(cid=cfg.cid + 700), k, B=2)
+        got = [r.decode_step(d["st"], si) for r, d in zip(runs, (a, b))]
+        for x, y in zip(*got):
+            assert x is None or torch.equal(x, y), k
+    assert all(r.err.item() == 0 for r in runs) and torch.equal(a["n_a"], b["n_a"])
+    for s in range(2):
+        n = int(a["n_a"][s])
+        assert torch.equal(a["st"].pool[s, :n], b["st"].pool[s, :n])
+    # beyond the margin: refused, nothing changed
+    keep, refused = a["st"].pos.clone(), T0.err_word()
+    csa.trim(a["L"], i32(17, 17), a["st"].pos, a["n_a"], a["n_a"].clone() if cfg.has_indexer else None, hw, err=refused)
+    assert refused.item() == csa.DEV_ROLLBACK and torch.equal(a["st"].pos, keep)
