@@ -155,7 +155,7 @@ __device__ __forceinline__ Item make_item(const DecArgs& a) {
     it.p0 = a.pos[it.b];
     bool bad = false;
     it.mask = tree_path_warp(a.parent + (size_t)it.b * a.T_, a.T_, it.q % a.T_, bad);
-    it.p = it.mask && it.p0 >= 0 ? it.p0 + __popcll(it.mask) - 1 : -1;
+    it.p = it.mask && tree_pos_ok(it.p0) ? it.p0 + __popcll(it.mask) - 1 : -1;
   } else {
     it.b = it.q / a.qps;
     it.p = a.pos[it.b] + it.q % a.qps;

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // which of the tile's tokens are nodes (the walk stands behind the products)
     for (int c = threadIdx.x - 64; c < N; c += kThreads - 64) {
       const int tok = n * N + c, b = tok / a.T;
-      bool ok = tok < a.ntok && a.pos[min(b, (a.ntok - 1) / a.T)] >= 0;
+      bool ok = tok < a.ntok && tree_pos_ok(a.pos[min(b, (a.ntok - 1) / a.T)]);
       if (ok) {
         const int32_t* row = a.parent + (size_t)b * a.T;
         for (int i = tok - b * a.T; i >= 0;) {

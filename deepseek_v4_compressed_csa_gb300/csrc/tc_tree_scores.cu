@@ -74,7 +74,7 @@ struct TsArgs {
 // Tiles of a group of sequence b: its committed rows and one of the tree's rows; 0 when the state is inconsistent.
 __device__ __forceinline__ int seq_tiles(const TsArgs& a, int b) {
   const int p0 = __ldg(a.pos + b), n = __ldg(a.n_rows + b);
-  if (p0 < 0 || n != p0 / a.ratio || n > a.cap) return 0;
+  if (!tree_pos_ok(p0) || n != p0 / a.ratio || n > a.cap) return 0;
   return (n + kRows - 1) / kRows + 1;
 }
 

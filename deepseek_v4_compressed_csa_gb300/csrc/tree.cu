@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(32 * kNrWarps, kLong ? 2 : 3) k_norm_rope(cons
     }
     if (depth >= 0 && rotate) {
       const int p0 = a.pos[b];
-      if (p0 < 0) {
+      if (p0 < 0 || p0 > INT32_MAX - depth) {
         if (lane == 0) atomicOr(a.err, CSA_DEV_STATE);
         depth = -1;
       } else {
@@ -262,18 +262,19 @@ __global__ void __launch_bounds__(256) k_tree_pool(const __grid_constant__ TreeP
   float* u = sm_tp;
   float* red = u + d;
   const int b = blockIdx.y, p0 = pos[b], tid = threadIdx.x;
+  const bool pos_ok = tree_pos_ok(p0);
   const bool consistent = tree_masks_block(parent + (size_t)b * T_, T_, s_masks, s_par);
   if (tid < kTreeMax) {  // the completing nodes in order (two warps)
     const uint64_t m = s_masks[tid];
-    const bool closes = p0 >= 0 && m != 0 && (p0 + __popcll(m)) % ratio == 0;
+    const bool closes = pos_ok && m != 0 && (p0 + __popcll(m)) % ratio == 0;
     const unsigned mine = __ballot_sync(0xffffffffu, closes);
     if ((tid & 31) == 0) s_count[tid >> 5] = __popc(mine);
-    if (blockIdx.x == 0 && ((tid == 0 && !consistent) || (p0 < 0 && m != 0))) atomicOr(err, CSA_DEV_STATE);
+    if (blockIdx.x == 0 && ((tid == 0 && !consistent) || (!pos_ok && m != 0))) atomicOr(err, CSA_DEV_STATE);
     s_par[tid] = closes ? __popc(mine & ((1u << (tid & 31)) - 1u)) : -1;
   }
   __syncthreads();
   if (tid < kTreeMax && s_par[tid] >= 0) s_list[s_par[tid] + (tid < 32 ? 0 : s_count[0])] = tid;
-  const bool works = p0 >= 0 && (int)blockIdx.x < s_count[0] + s_count[1], copies = p0 >= 0 && tp.src != tp.proj;
+  const bool works = pos_ok && (int)blockIdx.x < s_count[0] + s_count[1], copies = pos_ok && tp.src != tp.proj;
   // One block waits in any case: a grid that ended before the projections would let the next call's wait pass early.
   if (!works && !copies && blockIdx.x + blockIdx.y + blockIdx.z > 0) return;
   const T* src = tp.src + (size_t)b * T_ * rowlen;
@@ -611,7 +612,7 @@ __global__ void __launch_bounds__(32 * kCommitWarps) k_tree_commit(const __grid_
   for (int k = 0; k < a.npool; ++k) rows[k] = a.pool[k].n_rows[b];
   const bool tree_ok = tree_masks_block(a.parent + (size_t)b * a.T_, a.T_, masks, par);
   int bad = 0;
-  if (p0 < 0 || !tree_ok || leaf < -1 || leaf >= a.T_ || (leaf >= 0 && masks[leaf] == 0)) bad = CSA_DEV_STATE;
+  if (!tree_pos_ok(p0) || !tree_ok || leaf < -1 || leaf >= a.T_ || (leaf >= 0 && masks[leaf] == 0)) bad = CSA_DEV_STATE;
   const uint64_t m = bad || leaf < 0 ? 0 : masks[leaf];
   const int n = __popcll(m), end = p0 + n;
   for (int k = 0; k < a.npool; ++k) {

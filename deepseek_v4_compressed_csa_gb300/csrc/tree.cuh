@@ -14,6 +14,9 @@ namespace csa {
 constexpr int kTreeMax = 64;
 constexpr int kTreeNone = -2;
 
+// A committed length that every node's position, and the one behind it, fit on in 32 bits.
+__device__ __forceinline__ bool tree_pos_ok(int p0) { return p0 >= 0 && p0 <= INT32_MAX - kTreeMax; }
+
 // Parent of node i as the walks use it: kTreeNone for an unused slot or (bad set) a parent that is not below i.
 __device__ __forceinline__ int tree_parent(const int32_t* __restrict__ parent, int T, int i, bool& bad) {
   if (i >= T) return kTreeNone;
@@ -110,7 +113,7 @@ __device__ __forceinline__ bool node_view(NodeView& v, const int32_t* parent, in
   v.n = n_rows[v.b];
   bool bad = false;
   v.mask = tree_path_warp(parent + (size_t)v.b * T_, T_, v.i, bad);
-  const bool state = v.p0 < 0 || v.n != v.p0 / ratio || v.n > cap;
+  const bool state = !tree_pos_ok(v.p0) || v.n != v.p0 / ratio || v.n > cap;
   if ((bad || (state && v.mask)) && (threadIdx.x & 31) == 0) atomicOr(err, CSA_DEV_STATE);
   if (state || v.mask == 0) return false;
   v.p = v.p0 + __popcll(v.mask) - 1;

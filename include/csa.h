@@ -450,8 +450,8 @@ csa_status csa_trim(const csa_layer* layer, int B, const int32_t* n_back, int32_
  *   parent    [B, T] int32 or NULL; an unused slot's rows are left as they were
  *   pos [B]   (may be NULL without a rotation), inv_freq [R/2] fp32
  * Errors: CSA_ERR_ARG for sizes out of range (B, T, B*T <= 2^24, heads <= 4096,
- * T <= 64 with a parent array); CSA_DEV_STATE for pos[b] < 0 or an inconsistent
- * parent array (those tokens are skipped). */
+ * T <= 64 with a parent array); CSA_DEV_STATE for pos[b] < 0, a position past
+ * 2^31 - 1 or an inconsistent parent array (those tokens are skipped). */
 typedef struct {
   const void* x;
   void* out;
@@ -485,7 +485,7 @@ csa_status csa_norm_rope(const csa_layer* layer, const csa_rows* rows, int n, in
  * An unused slot's entries and outputs are left as they were.  A parent that is
  * not below its node, or a used node under an unused one, raises CSA_DEV_STATE
  * and the nodes it concerns are skipped; so does a sequence with pos[b] < 0 or
- * n_rows[b] != floor(pos[b] / ratio).  With two calls in flight on different
+ * above 2^31 - 65, or n_rows[b] != floor(pos[b] / ratio).  With two calls in flight on different
  * streams, workspaces and draft buffers must differ.
  *
  * csa_compress_tree: x [B, T, X] model dtype; the entries of a window before

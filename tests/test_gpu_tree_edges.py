@@ -351,3 +351,43 @@ def test_trim_behind_a_commit_is_a_shorter_commit(case):
     keep, refused = a["st"].pos.clone(), T0.err_word()
     csa.trim(a["L"], i32(17, 17), a["st"].pos, a["n_a"], a["n_a"].clone() if cfg.has_indexer else None, hw, err=refused)
     assert refused.item() == csa.DEV_ROLLBACK and torch.equal(a["st"].pos, keep)
+
+
+# ------------------------------------------------------------------------------------------------ positions
+
+
+@pytest.mark.parametrize("name", ["flash", "tiny_f32"])
+def test_positions_near_the_end_of_32_bits(name):
+    """A sequence whose nodes' positions would not fit (its row count agrees with it): reported and left alone by every
+    call; the sequence next to it is served."""
+    cfg = {"flash": FLASH, "tiny_f32": TINY}[name]
+    trees, pos = [TR.chain(8), TR.bushy(8)], [2045, 1203]
+    good, bad = (T0._step(cfg, trees, pos, 600, seed=800) for _ in range(2))
+    names = ["q2", "kv2", "proj_a", "rows_a", "proj_i", "rows_i", "scores", "sel", "out"]
+    for d in (good, bad):
+        for k in names:
+            d[k].fill_(7)
+    end = 2 ** 31 - 3
+    bad["st"].pos[1], bad["n_a"][1], bad["n_i"][1] = end, end // cfg.ratio, end // cfg.ratio
+    errs = [T0.err_word() for _ in range(2)]
+    for d, e in zip((good, bad), errs):
+        T0.run_step(cfg, d, e)
+    assert errs[0].item() == 0 and errs[1].item() == csa.DEV_STATE
+    last = [i for i, p in enumerate(TR.paths(trees[1])) if end + len(p) - 1 > 2 ** 31 - 1]
+    assert last
+    for k in names:
+        assert torch.equal(bad[k][0], good[k][0]), k
+        gone = bad[k][1][last] if k in ("q2", "kv2") else bad[k][1]  # (norm_rope goes by the token)
+        assert (gone == 7).all(), k
+    st = bad["st"]
+    keep = [t[1].clone() for t in (st.window, st.pool, st.ikeys, st.front_attn, st.front_index)]
+    e = T0.err_word()
+    T0.run_commit(cfg, bad, i32(7, 7), e)
+    assert e.item() == csa.DEV_STATE and st.pos.tolist() == [2053, end]
+    assert bad["n_a"].tolist() == [2053 // cfg.ratio, end // cfg.ratio]
+    for a, b in zip(keep, (st.window, st.pool, st.ikeys, st.front_attn, st.front_index)):
+        assert torch.equal(a, b[1])
+    # a chunk without a tree: the tokens that fit are served
+    x = T0.rnd(cfg, (1, 6, cfg.H, cfg.D), 990)
+    got = csa.norm_rope(G.lib_layer(cfg), [x], i32(end), csa_synth.inv_freq(cfg).cuda(), outs=[torch.full_like(x, 7)])
+    assert got.err.item() == csa.DEV_STATE and (got[0][0, 3:] == 7).all() and not (got[0][0, :3] == 7).all()
