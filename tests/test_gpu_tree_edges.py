@@ -391,3 +391,75 @@ def test_positions_near_the_end_of_32_bits(name):
     x = T0.rnd(cfg, (1, 6, cfg.H, cfg.D), 990)
     got = csa.norm_rope(G.lib_layer(cfg), [x], i32(end), csa_synth.inv_freq(cfg).cuda(), outs=[torch.full_like(x, 7)])
     assert got.err.item() == csa.DEV_STATE and (got[0][0, 3:] == 7).all() and not (got[0][0, :3] == 7).all()
+
+
+# ------------------------------------------------------------------------------------------------ the largest batches
+
+
+@pytest.mark.parametrize("nb, T", [(65535, 1), (4096, 64)])
+def test_largest_batches(nb, T):
+    """As many sequences, and as many nodes, as the calls take: sequences from all over the batch against the same ones
+    by themselves (the attention in float64: few and many nodes run different kernels)."""
+    cfg = FLASH.replace(X=64)
+    cap, ratio = 6, 4
+    g = torch.Generator(device="cuda").manual_seed(17)
+    n = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda").normal_(generator=g)  # noqa: E731
+    one = TR.bushy(T)
+    pos = torch.arange(nb, dtype=torch.int32, device="cuda") % (4 * cap - 3 if T == 1 else 3)
+    par = torch.tensor(one, dtype=torch.int32, device="cuda").expand(nb, T).contiguous()
+    L, invf, sink = G.lib_layer(cfg), csa_synth.inv_freq(cfg).cuda(), csa_synth.sinks(cfg).cuda()
+    ca, ci = (G.lib_comp(csa_synth.compressor(cfg, w)) for w in ("attn", "index"))
+    pick = [0, 1, nb // 2, nb - 2, nb - 1]
+
+    def step(d, pos, par, err):
+        b = par.shape[0]
+        z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+        o = dict(proj_a=z(b, T, 2048), rows_a=z(b, T, 512), proj_i=z(b, T, 512), rows_i=z(b, T, 128),
+                 scores=z(b, T, cap + T, dt=torch.float32), out=torch.full((b, T, 64, 512), SENTINEL,
+                                                                           dtype=torch.bfloat16, device="cuda"))
+        o["q"], o["kv"], o["iq"] = csa.norm_rope(L, [d["q"], d["kv"], d["iq"]], pos, invf, parent=par, err=err)
+        csa.compress_tree(L, ca, d["x"], par, pos, d["fa"], o["proj_a"], o["rows_a"], invf, comp_i=ci, frontier_i=d["fi"],
+                          proj_i=o["proj_i"], rows_i=o["rows_i"], err=err)
+        csa.index_scores_tree(L, o["iq"], d["iw"], d["keys"], o["rows_i"], par, pos // ratio, pos, o["scores"], err=err)
+        csa.attend_tree(L, o["q"], o["kv"], sink, d["window"], d["pool"], o["rows_a"], o["scores"], par, pos // ratio,
+                        pos, invf, o["out"], err=err)
+        return o
+
+    d = dict(q=n(nb, T, 64, 512), kv=n(nb, T, 512), iq=n(nb, T, 64, 128), iw=n(nb, T, 64), x=n(nb, T, 64),
+             fa=n(nb, 8, 2048), fi=n(nb, 8, 512), keys=n(nb, cap, 128), pool=n(nb, cap, 512), window=n(nb, cfg.W, 512))
+    err = T0.err_word()
+    big = step(d, pos, par, err)
+    small = step({k: v[pick].contiguous() for k, v in d.items()}, pos[pick].contiguous(), par[pick].contiguous(), err)
+    assert err.item() == 0
+    for k in ("q", "kv", "iq"):
+        assert torch.equal(big[k][pick], small[k]), k
+    layer, f = oracle_layer(cfg), f64(csa_synth.inv_freq(cfg)).astype(np.float32)
+    for k in ("proj_a", "proj_i"):  # fp32 sums of 64 products in another order: the neighbouring value at most
+        a, b = f64(big[k][pick]), f64(small[k])
+        assert (np.abs(a - b) <= G.ulp(np.abs(b), "bf16") + 2.0 ** -12 * np.abs(b).max()).all(), k
+    at = [int(p) for p in pos[pick]]
+    for j, b in enumerate(pick):
+        for i, path in enumerate(TR.paths(one)):
+            ref, bound = TR.scores_row(layer, big["iq"][b, i], d["iw"][b, i], d["keys"][b], big["rows_i"][b], path, at[j])
+            got = f64(big["scores"][b, i, :at[j] // ratio + T])
+            assert np.array_equal(np.isfinite(got), np.isfinite(ref))
+            fin = np.isfinite(ref)
+            assert (np.abs(got[fin] - ref[fin]) <= 2 * (128 + 64 + 8) * 2.0 ** -24 * bound[fin]).all()
+    T0.check_tree_outputs(cfg, layer, [one] * len(pick), at, big["q"][pick], big["kv"][pick], f64(sink),
+                          d["window"][pick], d["pool"][pick], big["rows_a"][pick], big["scores"][pick],
+                          big["out"][pick], None, f)
+    st = {k: d[k].clone() for k in ("window", "pool", "keys", "fa", "fi")}
+    p2, na, ni = pos.clone(), pos // ratio, pos // ratio
+    leaf = torch.full((nb,), T - 1, dtype=torch.int32, device="cuda")
+    csa.commit_tree(L, par, leaf, p2, na, big["kv"], st["window"], big["proj_a"], st["fa"], big["rows_a"], st["pool"],
+                    n_rows_i=ni, proj_i=big["proj_i"], frontier_i=st["fi"], rows_i=big["rows_i"], pool_i=st["keys"],
+                    err=err)
+    path = TR.paths(one)[-1]
+    assert err.item() == 0 and torch.equal(p2, pos + len(path)) and torch.equal(na, p2 // ratio)
+    for b, p in zip(pick, at):
+        for k, node in enumerate(path):
+            assert torch.equal(st["window"][b, (p + k) % cfg.W], big["kv"][b, node])
+            if k >= len(path) - 8:
+                assert torch.equal(st["fa"][b, (p + k) % 8], big["proj_a"][b, node])
+            if (p + k + 1) % ratio == 0:
+                assert torch.equal(st["pool"][b, (p + k + 1) // ratio - 1], big["rows_a"][b, node])
