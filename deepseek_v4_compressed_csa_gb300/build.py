@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import shlex
 import shutil
 import subprocess
 import sys
@@ -57,18 +58,31 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    # the binding's argument checks as a CPython extension (without Python's headers the binding checks in Python)
-    include = sysconfig.get_paths()["include"]
-    if not os.path.exists(os.path.join(include, "Python.h")):
-        return LIB
-    tmp = CHECKS + ".tmp"
-    cmd = [os.environ.get("CC") or "gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", include,
-           os.path.join(CSRC, "checks.c"), "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"gcc failed on checks.c:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CHECKS)
+    build_checks()
     return LIB
+
+
+def build_checks() -> str | None:
+    """The binding's argument checks as a CPython extension; None where Python's headers or a C compiler that works are
+    missing (the binding then checks in Python, a few microseconds a call slower)."""
+    if os.path.exists(CHECKS):
+        os.remove(CHECKS)
+    include = sysconfig.get_paths()["include"]
+    why = "no Python.h"
+    if os.path.exists(os.path.join(include, "Python.h")):
+        tmp = CHECKS + ".tmp"
+        try:
+            cmd = [*(shlex.split(os.environ.get("CC") or "") or ["gcc"]), "-O2", "-Wall", "-shared", "-fPIC", "-I",
+                   include, os.path.join(CSRC, "checks.c"), "-o", tmp]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode == 0 and os.path.exists(tmp):
+                os.replace(tmp, CHECKS)
+                return CHECKS
+            why = f"{' '.join(cmd)} failed\n{r.stdout}{r.stderr}"
+        except (OSError, ValueError) as e:  # no such compiler; a CC that does not parse
+            why = str(e)
+    print(f"the checks in C are left out: {why}", file=sys.stderr)
+    return None
 
 
 if __name__ == "__main__":
