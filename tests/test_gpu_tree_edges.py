@@ -463,3 +463,78 @@ def test_largest_batches(nb, T):
                 assert torch.equal(st["fa"][b, (p + k) % 8], big["proj_a"][b, node])
             if (p + k + 1) % ratio == 0:
                 assert torch.equal(st["pool"][b, (p + k + 1) // ratio - 1], big["rows_a"][b, node])
+
+
+# ------------------------------------------------------------------------------------------------ other layers
+
+
+MIXED = T0.ODD.replace(cid=80, D=64) if torch.cuda.is_available() else None  # one pool on the tensor cores, one not
+MORE_LAYERS = {} if MIXED is None else {
+    "attn_on_tc": MIXED,
+    "index_on_tc": T0.ODD.replace(cid=81, Di=64),
+    "flash_rollback": FLASH.replace(cid=82, rollback=37),
+    "flash_r128_rollback": FLASH.replace(cid=83, ratio=128, rollback=5),
+    "tiny_r1": TINY.replace(cid=84, ratio=1),
+    "tiny_r3": TINY.replace(cid=85, ratio=3),
+    "tiny_rollback": TINY.replace(cid=86, rollback=9),
+    "flash_w1": FLASH.replace(cid=87, W=1, topk=64),
+    "tiny_w1": TINY.replace(cid=88, W=1),
+    "one_head": T0.ODD.replace(cid=89, H=1, Hi=1, D=24, R=8, Di=8),
+    "wide_rows": TINY.replace(cid=90, D=1024, H=2),
+}
+
+
+@pytest.mark.parametrize("name", ["attn_on_tc", "index_on_tc", "flash_rollback", "flash_r128_rollback", "tiny_r1",
+                                  "tiny_r3", "tiny_rollback", "one_head", "wide_rows"])
+def test_compress_tree_of_other_layers(name, monkeypatch):
+    """Pools that are projected on different units, rings with a rollback margin, ratios down to 1."""
+    monkeypatch.setitem(T0.LAYERS, name, MORE_LAYERS[name])
+    for k, (trees, pos) in enumerate((([TR.chain(20), TR.bushy(17)], [61, 0]), ([TR.bushy(64)], [259]),
+                                      ([[-1], [-1], [-1]], [3, 127, 4]))):
+        case = f"{name}_{k}"
+        monkeypatch.setitem(T0.CT_CASES, case, (name, trees, pos))
+        T0.test_compress_tree_against_paths(case)
+
+
+@pytest.mark.parametrize("name", ["flash_w1", "tiny_w1", "one_head", "wide_rows", "tiny_r1", "tiny_r3", "flash_rollback"])
+def test_attend_tree_of_other_layers(name, monkeypatch):
+    """Windows of one token, one head, the widest rows, ratios down to 1."""
+    cfg = MORE_LAYERS[name]
+    monkeypatch.setitem(T0.LAYERS, name, cfg)
+    monkeypatch.setitem(T0.EDGE_LAYERS, name, cfg)
+    select = cfg.has_indexer
+    for k, (trees, pos) in enumerate((([TR.chain(9), TR.bushy(7)], [400, 0]), ([TR.bushy(16, s) for s in range(11)],
+                                                                               [300 + 7 * s for s in range(11)]))):
+        case = f"{name}_{k}"
+        monkeypatch.setitem(T0.EDGE_CASES, case, (name, trees, pos, select))
+        if cfg.H >= 4:  # (that test gives every fourth head its sink)
+            T0.test_attend_tree_sinks_and_large_logits(case, 1.0)
+        if cfg.rollback == 0:
+            monkeypatch.setitem(T0.AT_CASES, case, (name, trees, pos, "ties" if select else None))
+            T0.test_attend_tree_against_float64(case)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R", [8, 24, 64])
+def test_norm_rope_of_every_width(dtype, R):
+    """Rows of every width from the rotated dims to 1024 values, odd head counts, strided and dense."""
+    cfg = TINY.replace(cid=91, dtype=dtype, D=64, Di=64, R=R)
+    f = f64(csa_synth.inv_freq(cfg)).astype(np.float32)
+    L, invf, pos = G.lib_layer(cfg), csa_synth.inv_freq(cfg).cuda(), i32(777, 0)
+    widths = sorted(set(range(R, 1025, 8)))
+    for k in range(0, len(widths), 4):
+        xs, ws, ref = [], [], []
+        for j, dim in enumerate(widths[k:k + 4]):
+            heads = (1, 3, 33, 2)[(k + j) % 4]
+            wide = T0.rnd(cfg, (2, 3, heads * dim + 8 * (j % 2)), 1000 + dim, scale=2.0)
+            xs.append(wide[..., :heads * dim].unflatten(-1, (heads, dim)))
+            ws.append(T0.rnd(cfg, (dim,), 2000 + dim, dtype=torch.float32) if j != 1 else None)
+        got = csa.norm_rope(L, xs, pos, invf, weights=ws)
+        assert got.err.item() == 0
+        for x, w, o in zip(xs, ws, got):
+            for b in range(2):
+                for i in range(3):
+                    want = TR.norm_rope(x[b, i], w, True, cfg.rms_eps, int(pos[b]) + i, f)
+                    pair = np.repeat(np.hypot(want[..., ::2], want[..., 1::2]), 2, axis=-1)
+                    tol = 2.0 ** -18 * pair
+                    assert (np.abs(f64(o[b, i]) - want) <= T0.half_step(np.abs(want) + tol, dtype) + tol).all(), x.shape
