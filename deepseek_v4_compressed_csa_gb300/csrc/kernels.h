@@ -332,7 +332,8 @@ struct TreeNode {
 cudaError_t launch_topk_tree(const Dims& L, const float* scores, int B, int T, const int32_t* parent, int cap,
                              const int32_t* n_rows, const int32_t* pos, int32_t* sel, TreeNode* nodes, int32_t* err,
                              cudaStream_t s);
-// ---- tree_topk.cu: the same for more nodes than SMs (a block of 256 threads per node, its keys in shared memory)
+// ---- tree_topk.cu: the same by a block of 256 threads per node with its keys in shared memory, where
+// topk_tree_small_blocks says so (more nodes than SMs and up to 64 KB of keys, or few nodes and up to 33 KB)
 bool topk_tree_small_blocks(int Q, int cap, int T, int sms);
 cudaError_t launch_topk_tree_small(const Dims& L, const float* scores, int B, int T, const int32_t* parent, int cap,
                                   const int32_t* n_rows, const int32_t* pos, int32_t* sel, TreeNode* nodes,
@@ -353,7 +354,7 @@ struct TreeAttend {
 };
 cudaError_t launch_attend_tree(const Dims& L, const TreeAttend& t, int32_t* err, cudaStream_t s);
 // The same on the tensor cores (tc_attend_supported shapes), the node records already in t.ws: a CTA per query
-// streaming its tiles (tc_tree_attend.cu), or S <= 4 splits per query merged in a cluster (tc_attend_decode.cu).
+// streaming its tiles (tc_tree_attend.cu), or S = 1, 2, 4 or 8 splits per query merged in a cluster (tc_attend_decode.cu).
 cudaError_t launch_tc_attend_tree(const Dims& L, const TreeAttend& t, const int32_t* sel, int32_t* err,
                                   cudaStream_t s);
 // queries that launch_tc_attend_tree_split works on at once with S splits each

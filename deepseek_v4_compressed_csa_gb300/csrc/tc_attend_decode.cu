@@ -97,7 +97,8 @@ struct DecArgs {
   int Wr;                       // ring slots (W + rollback); the query attends its last W tokens
   int qps;                      // consecutive queries per sequence (a verify block; 1 for decode)
   int kv_in_ring;               // the new tokens are already in the ring (verify): none is roped here
-  int cluster;                  // S in {2, 4}: the S splits of a query are one cluster and merge through DSMEM
+  int cluster;                  // the S splits of a query (2 or 4; 8 in the kSp = 8 instance) are one cluster and merge
+                                // through DSMEM
   // a tree's nodes (kTree; q already rotated): query q is node q % T of sequence q / T
   const int32_t* parent;        // [B, T]
   const TreeNode* nodes;        // [B * T], written by the kernel before

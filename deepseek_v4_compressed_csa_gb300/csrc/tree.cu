@@ -243,7 +243,8 @@ __device__ __forceinline__ void store2(float* p, float x, float y) { *reinterpre
 // Block (g, b, pool): the g-th node of sequence b that completes a window along its path: the row that the compressor
 // would emit, entries before pos from the frontier ring, from pos on the path's nodes.  Arithmetic and roundings are
 // those of the committed rows (compress.cu: the pooled value, its norm and its rotation each in the model dtype), so
-// that an accepted row is the row decoding would have written.  A thread takes two neighbouring channels, and eight
+// that from equal projections an accepted row is the row decoding would have written (the projections' sums are split
+// in another way than decoding's, tc_tree_project.cu, and may round to the neighbouring value).  A thread takes two neighbouring channels, and eight
 // entries' loads are in flight together.  Latency-bound: what depends on the tree alone (the path, the rows' addresses,
 // weights, angles) stands before the programmatic wait, behind the projections; what is left adds 3 us to 8 nodes'
 // projections, 7 us to those of 512.

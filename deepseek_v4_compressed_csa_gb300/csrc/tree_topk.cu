@@ -4,7 +4,7 @@
 // The register kernel of indexer.cu gives a query 1024 threads: the lowest latency for a few queries, but one block
 // per SM, its barriers and histogram rounds exposed.  With more nodes than SMs a block of 256 threads holding its keys
 // in shared memory lets four or five nodes share an SM and cover each other's waits: 512 nodes of 8.2K columns take
-// 17 us instead of 38.  Radix select over digits of 11, 11 and 10 bits, then one ascending pass.  Bound by its
+// 17 us instead of 38.  With few nodes it leaves room on its SM for the attention's CTA (topk_tree_small_blocks).  Radix select over digits of 11, 11 and 10 bits, then one ascending pass.  Bound by its
 // instructions, some seventy for every 32 columns (the ascending pass alone took 35 with a rank per column, and 22 us).
 #include "kernels.h"
 #include "tree.cuh"

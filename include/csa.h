@@ -489,9 +489,13 @@ csa_status csa_norm_rope(const csa_layer* layer, const csa_rows* rows, int n, in
  * streams, workspaces and draft buffers must differ.
  *
  * csa_compress_tree: x [B, T, X] model dtype; the entries of a window before
- * pos[b] come from the frontier rings, the others from the path's nodes; every
- * rounding is csa_compress_append's, so that a committed row is the row it would
- * have written.  comp_i and its buffers are NULL for the attention pool alone.
+ * pos[b] come from the frontier rings, the others from the path's nodes; the
+ * stages and their roundings are csa_compress_append's.  The projections' fp32
+ * sums may be split differently along the hidden axis there and here (and here by
+ * B*T and the device): a projection may round to the neighbouring value, and the
+ * row that it enters may differ by as much; otherwise a committed row is the row
+ * csa_compress_append would have written.  One call's results do not change from
+ * run to run.  comp_i and its buffers are NULL for the attention pool alone.
  * Workspace: CSA_OP_COMPRESS_TREE (cap ignored). */
 csa_status csa_compress_tree(const csa_layer* layer, const csa_compressor* comp_a, const csa_compressor* comp_i,
                              const void* x, int B, int T, const int32_t* parent, const int32_t* pos,
