@@ -541,7 +541,7 @@ csa_status csa_attend_tree(const csa_layer* layer, const void* q, const void* kv
   Dims L;
   csa_status st = make_dims(layer, &L);
   if (st != CSA_OK) return st;
-  if (!tree_sizes_ok(B, T) || cap < 1 || cap > kTreeCapMax) return CSA_ERR_ARG;
+  if (!tree_sizes_ok(B, T) || cap < 1 || (long long)cap + T + L.W > kTreeCapMax) return CSA_ERR_ARG;  // (a node's keys)
   if (!dev_tensor(q) || !dev_tensor(kv) || !dev_i32(sink) || !dev_tensor(window) || !dev_tensor(pool) ||
       !dev_tensor(rows_a) || !dev_tensor(inv_freq) || !dev_tensor(out))
     return CSA_ERR_ARG;

@@ -505,7 +505,7 @@ csa_status csa_compress_tree(const csa_layer* layer, const csa_compressor* comp_
 
 /* csa_index_scores_tree: the nodes' index scores, csa_index_topk's formula on
  * rotated queries iq [B, T, Hi, Di] (csa_norm_rope without a norm), iw [B, T, Hi]:
- *   scores [B, T, cap + T] fp32 (cap <= 2^31 - 257, here and in csa_attend_tree);
+ *   scores [B, T, cap + T] fp32 (cap <= 2^31 - 257);
  *   columns c < n_rows[b]: committed row c;
  *   columns n_rows[b] + a, a < T: the row of node a for the nodes a of i's path
  *   that complete one, -infinity for the others; later columns are not touched.
@@ -519,7 +519,7 @@ csa_status csa_index_scores_tree(const csa_layer* layer, const void* iq, const v
                                  const int32_t* n_rows, const int32_t* pos, float* scores, void* ws, size_t ws_bytes,
                                  int32_t* err, void* stream);
 
-/* csa_attend_tree: selection and attention of every node.
+/* csa_attend_tree: selection and attention of every node (cap + T + W <= 2^31 - 257).
  *   visible columns: c < n_rows[b], and n_rows[b] + a for the completing nodes a
  *   of the path; the topk largest scores among them (ties to the lower column),
  *   all of them when there are no more or when scores is NULL (layers without an

@@ -320,3 +320,12 @@ def test_norm_rope_returns_its_error_word(lib, calls, monkeypatch):
     assert got.err.dtype == torch.int32 and got.err.tolist() == [0] and calls[0][1][-1] == got.err.data_ptr()
     own = _cuda_like(z(1, dt=torch.int32))
     assert csa.norm_rope(LAYER, [x], outs=[x], err=own).err is own and calls[1][1][-1] == own.data_ptr()
+
+
+def test_attend_tree_key_counts_fit(lib):
+    """A node's keys are counted in 32 bits: capacity, nodes and window together are bounded."""
+    def call(W, cap):
+        return lib.csa_attend_tree(ctypes.byref(_layer(W=W)), FAKE, FAKE, FAKE, 2, 8, FAKE, FAKE, FAKE, cap, FAKE, FAKE, FAKE,
+                                   FAKE, FAKE, FAKE, None, None, 0, FAKE, None)
+    assert call(1 << 30, 1 << 30) == B.CSA_ERR_ARG and call(128, 2 ** 31 - 257 - 135) == B.CSA_ERR_ARG
+    assert call(128, 2 ** 31 - 257 - 136) == B.CSA_ERR_WORKSPACE  # (sizes accepted, no workspace given)
