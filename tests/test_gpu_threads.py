@@ -46,8 +46,8 @@ def fresh_thread_jobs():
     fp8 = dataclasses.replace(L, index_fp8=True)
     ca, ci = (G.lib_comp(csa_synth.compressor(cfg, w)) for w in ("attn", "index"))
     ws = {op: z(csa.workspace_size(layer, op, b, t, cap) + 256, dt=torch.uint8) for op, layer, b, t in (
-        (csa.OP_COMPRESS, L, nb, T), (csa.OP_COMPRESS_PAIR, L, nb, 1), (csa.OP_INDEX_TOPK, L, nb, 1),
-        (csa.OP_ATTEND_DECODE, L, nb, 1), (csa.OP_ATTEND_PREFILL, L, 1, 40), (csa.OP_ATTEND_TREE, L, many, T),
+        (csa.OP_COMPRESS, L, nb, T), (csa.OP_COMPRESS_PAIR, L, nb, 1), (csa.OP_INDEX_TOPK, L, nb * T, 1),
+        (csa.OP_ATTEND_DECODE, L, nb * T, 1), (csa.OP_ATTEND_PREFILL, L, 1, 40), (csa.OP_ATTEND_TREE, L, many, T),
         (csa.OP_INDEX_SCORES_TREE, fp8, nb, T), (csa.OP_COMPRESS_TREE, L, nb, T))}
     pos, n = i32(2051, 1205), i32(512, 301)
     par = torch.tensor([TR.bushy(T)] * nb, dtype=torch.int32, device="cuda")
@@ -69,6 +69,13 @@ def fresh_thread_jobs():
     got, got8 = z(nb, T, cap + T, dt=torch.float32), z(nb, T, cap + T, dt=torch.float32)
     p2, i2, f2, g2, na, ni = z(nb, cap, 512), z(nb, cap, 128), fa.clone(), fi.clone(), n.clone(), n.clone()
     win2, win1, n522 = window.clone(), window[0].clone(), i32(522)  # (the rows after the chunk)
+    nq, nkv, leaf, cpos, cn, win3, f3, p3 = z(*q.shape), z(*kv.shape), i32(T - 1, 0), pos.clone(), n.clone(), \
+        window.clone(), fa.clone(), pool.clone()
+    proj0 = rnd(cfg, (nb, T, 2048), 53)
+    ssel, sn_sel, vout, win4 = z(nb, cfg.topk, dt=torch.int32), z(nb, dt=torch.int32), z(*q.shape), window.clone()
+    vsel, vn_sel = z(nb, T, cfg.topk, dt=torch.int32), z(nb, T, dt=torch.int32)
+    vsel0 = torch.arange(cfg.topk, dtype=torch.int32, device="cuda").expand(nb, T, -1).contiguous()
+    vn_sel0 = n[:, None].expand(nb, T).contiguous().clamp(max=256)
     k = dict(err=err, stream=stream)
     return err, [
         ("compress_tree", lambda: csa.compress_tree(
@@ -91,6 +98,15 @@ def fresh_thread_jobs():
         ("attend_decode", lambda: csa.attend_decode(
             L, q1, kv1, sink, win2, pool, n, None, None, pos, invf, out1, ws=ws[csa.OP_ATTEND_DECODE], **k),
          (out1, win2)),
+        ("norm_rope", lambda: csa.norm_rope(L, [q, kv], pos, invf, parent=par, outs=[nq, nkv], **k), (nq, nkv)),
+        ("commit_tree", lambda: csa.commit_tree(L, par, leaf, cpos, cn, kv, win3, proj0, f3, rows, p3, **k),
+         (cpos, cn, win3, f3, p3)),
+        ("index_topk_static", lambda: csa.index_topk_static(L, iq1, iw1, keys, n, pos, invf, ssel, sn_sel, **k),
+         (ssel, sn_sel)),
+        ("index_topk_verify", lambda: csa.index_topk_verify(L, iq, iw, keys, n, pos, invf, vsel, vn_sel,
+                                                            ws=ws[csa.OP_INDEX_TOPK], **k), (vsel, vn_sel)),
+        ("attend_verify", lambda: csa.attend_verify(L, q, kv, sink, win4, pool, n, vsel0, vn_sel0, pos, invf, vout,
+                                                    ws=ws[csa.OP_ATTEND_DECODE], **k), (vout, win4)),
         ("attend_prefill_chunk", lambda: csa.attend_prefill_chunk(
             L, *chunk, sink, 2051, win1, pool[0], keys[0], n522, invf, outc, ws=ws[csa.OP_ATTEND_PREFILL], **k),
          (outc, win1)),
