@@ -310,7 +310,7 @@ def trim(layer: Layer, n_back, pos, n_rows_a, n_rows_i, hw, err=None, stream=Non
         _expect(name, t, torch.int32, (B,))
     _expect("n_rows_i", n_rows_i, torch.int32, (B,), optional=not layer.has_indexer)
     _expect_err(err)
-    err = _err(err, pos.device)
+    err = _err(err, pos.device, stream)
     L = layer._c()
     _check("csa_trim", load_library().csa_trim(ctypes.byref(L), B, _ptr(n_back), _ptr(pos), _ptr(n_rows_a),
                                                _ptr(n_rows_i), _ptr(hw), _ptr(err), _stream(stream)))
@@ -324,15 +324,23 @@ def workspace_size(layer: Layer, op: int, B: int, T: int, cap: int) -> int:
     return int(n.value)
 
 
-def _ws(layer, op, B, T, cap, ws, device):
+def _new(device, stream, new, *size, dtype):
+    """A tensor of the call's own: allocated, and zeroed where it is, on the stream that will use it."""
+    if stream is None:
+        return new(*size, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return new(*size, dtype=dtype, device=device)
+
+
+def _ws(layer, op, B, T, cap, ws, device, stream):
     need = workspace_size(layer, op, B, T, cap)
     if ws is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        ws = _new(device, stream, torch.empty, max(need, 256), dtype=torch.uint8)
     return ws, ws.numel() * ws.element_size()
 
 
-def _err(err, device):
-    return torch.zeros(1, dtype=torch.int32, device=device) if err is None else err
+def _err(err, device, stream):
+    return _new(device, stream, torch.zeros, 1, dtype=torch.int32) if err is None else err
 
 
 def compress_append(layer: Layer, comp: Compressor, x, pos, frontier, pool, n_rows, inv_freq, ws=None, err=None,
@@ -350,8 +358,8 @@ def compress_append(layer: Layer, comp: Compressor, x, pos, frontier, pool, n_ro
     _expect("n_rows", n_rows, torch.int32, (B,))
     _expect("inv_freq", inv_freq, torch.float32, (layer.R // 2,))
     _expect_err(err)
-    ws, nb = _ws(layer, OP_COMPRESS, B, T, cap, ws, x.device)
-    err = _err(err, x.device)
+    ws, nb = _ws(layer, OP_COMPRESS, B, T, cap, ws, x.device, stream)
+    err = _err(err, x.device, stream)
     L, C = layer._c(), comp._c()
     _check("csa_compress_append", load_library().csa_compress_append(
         ctypes.byref(L), ctypes.byref(C), _ptr(x), B, T, _ptr(pos), _ptr(frontier), _ptr(pool), cap, _ptr(n_rows),
@@ -378,8 +386,8 @@ def compress_append_pair(layer: Layer, comp_a: Compressor, comp_i: Compressor, x
     _expect("inv_freq", inv_freq, torch.float32, (layer.R // 2,))
     _expect_err(err)
     cap_a, cap_i = pool_a.shape[1], pool_i.shape[1]
-    ws, nb = _ws(layer, OP_COMPRESS_PAIR, B, T, max(cap_a, cap_i), ws, x.device)
-    err = _err(err, x.device)
+    ws, nb = _ws(layer, OP_COMPRESS_PAIR, B, T, max(cap_a, cap_i), ws, x.device, stream)
+    err = _err(err, x.device, stream)
     L, Ca, Ci = layer._c(), comp_a._c(), comp_i._c()
     _check("csa_compress_append_pair", load_library().csa_compress_append_pair(
         ctypes.byref(L), ctypes.byref(Ca), ctypes.byref(Ci), _ptr(x), B, T, _ptr(pos), _ptr(frontier_a),
@@ -406,8 +414,8 @@ def _expect_index(layer: Layer, iq, iw, ikeys, n_rows, pos, inv_freq, sel, n_sel
 def index_topk(layer: Layer, iq, iw, ikeys, n_rows, pos, inv_freq, sel, n_sel, ws=None, err=None, stream=None):
     _expect_index(layer, iq, iw, ikeys, n_rows, pos, inv_freq, sel, n_sel, err)
     B, cap = iq.shape[0], ikeys.shape[1]
-    ws, nb = _ws(layer, OP_INDEX_TOPK, B, 1, cap, ws, iq.device)
-    err = _err(err, iq.device)
+    ws, nb = _ws(layer, OP_INDEX_TOPK, B, 1, cap, ws, iq.device, stream)
+    err = _err(err, iq.device, stream)
     L = layer._c()
     _check("csa_index_topk", load_library().csa_index_topk(
         ctypes.byref(L), _ptr(iq), _ptr(iw), B, _ptr(ikeys), cap, _ptr(n_rows), _ptr(pos), _ptr(inv_freq),
@@ -421,8 +429,8 @@ def index_topk_overlapped(layer: Layer, iq, iw, ikeys, n_rows, pos, inv_freq, se
     rest waits for `pool_ready` (a torch.cuda.Event recorded after the index pool's compress call)."""
     _expect_index(layer, iq, iw, ikeys, n_rows, pos, inv_freq, sel, n_sel, err)
     B, cap = iq.shape[0], ikeys.shape[1]
-    ws, nb = _ws(layer, OP_INDEX_TOPK, B, 1, cap, ws, iq.device)
-    err = _err(err, iq.device)
+    ws, nb = _ws(layer, OP_INDEX_TOPK, B, 1, cap, ws, iq.device, stream)
+    err = _err(err, iq.device, stream)
     L = layer._c()
     ev = pool_ready.cuda_event if pool_ready is not None else None
     _check("csa_index_topk_overlapped", load_library().csa_index_topk_overlapped(
@@ -435,7 +443,7 @@ def index_topk_static(layer: Layer, iq, iw, ikeys, n_rows, pos, inv_freq, sel, n
     """csa_index_topk_static: the decode indexer with the library's own fixed scratch array (no workspace)."""
     _expect_index(layer, iq, iw, ikeys, n_rows, pos, inv_freq, sel, n_sel, err)
     B, cap = iq.shape[0], ikeys.shape[1]
-    err = _err(err, iq.device)
+    err = _err(err, iq.device, stream)
     L = layer._c()
     _check("csa_index_topk_static", load_library().csa_index_topk_static(
         ctypes.byref(L), _ptr(iq), _ptr(iw), B, _ptr(ikeys), cap, _ptr(n_rows), _ptr(pos), _ptr(inv_freq),
@@ -467,8 +475,8 @@ def attend_decode(layer: Layer, q, kv_new, sink, window, pool, n_rows, sel, n_se
     _expect("out", out, layer.dtype, (B, layer.H, layer.D))
     _expect_err(err)
     cap = pool.shape[1]
-    ws, nb = _ws(layer, OP_ATTEND_DECODE, B, 1, cap, ws, q.device)
-    err = _err(err, q.device)
+    ws, nb = _ws(layer, OP_ATTEND_DECODE, B, 1, cap, ws, q.device, stream)
+    err = _err(err, q.device, stream)
     L = layer._c()
     _check("csa_attend_decode", load_library().csa_attend_decode(
         ctypes.byref(L), _ptr(q), _ptr(kv_new), _ptr(sink), B, _ptr(window), _ptr(pool), cap, _ptr(n_rows),
@@ -498,8 +506,8 @@ def attend_prefill_chunk(layer: Layer, q, kv_new, iq, iw, sink, pos0: int, windo
     _expect("sel_out", sel_out, torch.int32, (T, layer.topk), optional=True)
     _expect_err(err)
     cap = pool.shape[-2]
-    ws, nb = _ws(layer, OP_ATTEND_PREFILL, 1, T, cap, ws, q.device)
-    err = _err(err, q.device)
+    ws, nb = _ws(layer, OP_ATTEND_PREFILL, 1, T, cap, ws, q.device, stream)
+    err = _err(err, q.device, stream)
     L = layer._c()
     _check("csa_attend_prefill_chunk", load_library().csa_attend_prefill_chunk(
         ctypes.byref(L), _ptr(q), _ptr(kv_new), _ptr(iq), _ptr(iw), _ptr(sink), T, int(pos0), _ptr(window),
@@ -531,8 +539,8 @@ def compress_append_varlen(layer: Layer, comp: Compressor, x, cu_seqlens, T_max:
     _expect("n_rows", n_rows, torch.int32, (B,))
     _expect("inv_freq", inv_freq, torch.float32, (layer.R // 2,))
     _expect_err(err)
-    ws, nb = _ws(layer, OP_COMPRESS_VARLEN, B, N, cap, ws, x.device)
-    err = _err(err, x.device)
+    ws, nb = _ws(layer, OP_COMPRESS_VARLEN, B, N, cap, ws, x.device, stream)
+    err = _err(err, x.device, stream)
     L, C = layer._c(), comp._c()
     _check("csa_compress_append_varlen", load_library().csa_compress_append_varlen(
         ctypes.byref(L), ctypes.byref(C), _ptr(x), B, _ptr(cu_seqlens), N, int(T_max), _ptr(pos), _ptr(frontier),
@@ -569,8 +577,8 @@ def attend_prefill_varlen(layer: Layer, q, kv_new, iq, iw, sink, cu_seqlens, T_m
     _expect("out", out, layer.dtype, (N, layer.H, layer.D))
     _expect("sel_out", sel_out, torch.int32, (N, layer.topk), optional=True)
     _expect_err(err)
-    ws, nb = _ws(layer, OP_ATTEND_PREFILL_VARLEN, B, N, cap, ws, q.device)
-    err = _err(err, q.device)
+    ws, nb = _ws(layer, OP_ATTEND_PREFILL_VARLEN, B, N, cap, ws, q.device, stream)
+    err = _err(err, q.device, stream)
     L = layer._c()
     _check("csa_attend_prefill_varlen", load_library().csa_attend_prefill_varlen(
         ctypes.byref(L), _ptr(q), _ptr(kv_new), _ptr(iq), _ptr(iw), _ptr(sink), B, _ptr(cu_seqlens), N, int(T_max),
@@ -596,8 +604,8 @@ def index_topk_verify(layer: Layer, iq, iw, ikeys, n_rows, pos, inv_freq, sel, n
     _expect("n_sel", n_sel, torch.int32, (B, T))
     _expect_err(err)
     cap = ikeys.shape[1]
-    ws, nb = _ws(layer, OP_INDEX_TOPK, B * T, 1, cap, ws, iq.device)
-    err = _err(err, iq.device)
+    ws, nb = _ws(layer, OP_INDEX_TOPK, B * T, 1, cap, ws, iq.device, stream)
+    err = _err(err, iq.device, stream)
     L = layer._c()
     _check("csa_index_topk_verify", load_library().csa_index_topk_verify(
         ctypes.byref(L), _ptr(iq), _ptr(iw), B, T, _ptr(ikeys), cap, _ptr(n_rows), _ptr(pos), _ptr(inv_freq),
@@ -627,8 +635,8 @@ def attend_verify(layer: Layer, q, kv_new, sink, window, pool, n_rows, sel, n_se
     _expect("out", out, layer.dtype, (B, T, layer.H, layer.D))
     _expect_err(err)
     cap = pool.shape[1]
-    ws, nb = _ws(layer, OP_ATTEND_DECODE, B * T, 1, cap, ws, q.device)
-    err = _err(err, q.device)
+    ws, nb = _ws(layer, OP_ATTEND_DECODE, B * T, 1, cap, ws, q.device, stream)
+    err = _err(err, q.device, stream)
     L = layer._c()
     _check("csa_attend_verify", load_library().csa_attend_verify(
         ctypes.byref(L), _ptr(q), _ptr(kv_new), _ptr(sink), B, T, _ptr(window), _ptr(pool), cap, _ptr(n_rows),
@@ -671,17 +679,9 @@ def _ptrs(dev: int, *specs) -> list:
     return out
 
 
-def _tree_new(device, stream, new, *size, dtype):
-    """A tensor of the call's own: allocated, and zeroed where it is, on the stream that will use it."""
-    if stream is None:
-        return new(*size, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return new(*size, dtype=dtype, device=device)
-
-
 def _tree_err(err, dev, stream):
     if err is None:
-        return _tree_new(f"cuda:{dev}", stream, torch.zeros, 1, dtype=torch.int32)
+        return _new(f"cuda:{dev}", stream, torch.zeros, 1, dtype=torch.int32)
     if not (isinstance(err, torch.Tensor) and err.dtype is torch.int32 and err.numel() >= 1):
         _expect_err(err)
     if err.get_device() != dev:
@@ -692,7 +692,7 @@ def _tree_err(err, dev, stream):
 def _tree_ws(layer, op, B, T, cap, ws, dev, stream):
     """The caller's workspace (the library checks its size), or a new one."""
     if ws is None:
-        ws = _tree_new(f"cuda:{dev}", stream, torch.empty, max(workspace_size(layer, op, B, T, cap), 256), dtype=torch.uint8)
+        ws = _new(f"cuda:{dev}", stream, torch.empty, max(workspace_size(layer, op, B, T, cap), 256), dtype=torch.uint8)
     elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"ws: expected a contiguous tensor on device {dev}")
     return ws, ws.numel() * ws.element_size()
@@ -764,7 +764,7 @@ def norm_rope(layer: Layer, xs, pos=None, inv_freq=None, parent=None, weights=No
     dev = x.get_device()
     if outs is None:
         new = torch.empty if parent is None else torch.zeros
-        outs = [_tree_new(x.device, stream, new, x.shape, dtype=x.dtype) for x in xs]
+        outs = [_new(x.device, stream, new, x.shape, dtype=x.dtype) for x in xs]
     rows = b""
     dtype = layer.dtype
     for k in range(n):

@@ -1,0 +1,90 @@
+"""stream=: what a call allocates by itself, its workspace and its error word, belongs to the stream that it runs on."""
+import numpy as np
+import pytest
+import torch
+
+import csa_synth
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import deepseek_v4_compressed_csa_gb300 as csa
+    from tests import _gpu as G
+
+FLASH = csa_synth.CONFIGS[3].replace(X=512)
+
+
+def rnd(shape, tag, dtype=torch.bfloat16):
+    a = np.random.default_rng([8, tag]).standard_normal(shape, dtype=np.float32)
+    return torch.from_numpy(a).to(dtype).cuda()
+
+
+def i32(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def keep_busy():
+    """Some milliseconds of work on the current stream."""
+    a = torch.randn(4096, 4096, device="cuda")
+    for _ in range(20):
+        a = a @ a * 1e-3
+    return a
+
+
+def jobs():
+    """name, call(stream), expected error word: calls that report something, their error words their own."""
+    cfg, nb = FLASH, 2
+    L, invf, z = G.lib_layer(cfg), csa_synth.inv_freq(cfg).cuda(), torch.zeros
+    comp = G.lib_comp(csa_synth.compressor(cfg, "attn"))
+    x, front, pool = rnd((nb, 4, cfg.X), 1), rnd((nb, 8, 2048), 2), rnd((nb, 700, 512), 3)
+    q, kv, window, sink = rnd((nb, 64, 512), 4), rnd((nb, 512), 5), rnd((nb, cfg.W, 512), 6), z(64, device="cuda")
+    out, far = torch.empty_like(q), torch.full((nb, cfg.topk), 699, dtype=torch.int32, device="cuda")
+    p0, p1, n0, n1, k, back, ten, ten2, hw = (i32(*v) for v in ((40, 41), (2000, 2001), (9, 11), (500, 500), (8, 8), (5, 5),
+                                                               (10, 10), (10, 10), (40, 40)))
+    p2 = hw.clone()
+    return [
+        ("compress_append", lambda s: csa.compress_append(L, comp, x, p0, front, pool, n0, invf, stream=s), csa.DEV_STATE),
+        ("attend_decode", lambda s: csa.attend_decode(L, q, kv, sink, window, pool, n1, far, k, p1, invf, out, stream=s),
+         csa.DEV_RANGE),
+        ("trim", lambda s: csa.trim(L, back, p2, ten, ten2, hw, stream=s), csa.DEV_ROLLBACK),
+    ]
+
+
+def test_error_words_are_zeroed_on_the_calls_stream():
+    """The current stream is busy, the call's is not: its report must not be wiped by a zeroing that comes later."""
+    side = torch.cuda.Stream()
+    for name, call, want in jobs():
+        for stream in (None, side, side):
+            torch.cuda.synchronize()
+            big = keep_busy() if stream is not None else None
+            err = call(stream)
+            torch.cuda.synchronize()
+            assert err.item() == want, (name, stream)
+            del big
+
+
+def test_workspaces_stay_with_the_calls_stream():
+    """The call's stream is busy when it is made, so that its kernels run later: memory that others allocate and write on
+    the current stream meanwhile is not its workspace."""
+    cfg, nb, cap = FLASH, 4, 9000
+    L, invf, side = G.lib_layer(cfg), csa_synth.inv_freq(cfg).cuda(), torch.cuda.Stream()
+    iq, iw, keys = rnd((nb, 64, 128), 10), rnd((nb, 64), 11), rnd((nb, cap, 128), 12)
+    n, pos = i32(8000, 7000, 8999, 3000), i32(32003, 28001, 35999, 12000)
+    sel, n_sel = torch.zeros(nb, cfg.topk, dtype=torch.int32, device="cuda"), torch.zeros(nb, dtype=torch.int32, device="cuda")
+    size = max(256, csa.workspace_size(L, csa.OP_INDEX_TOPK, nb, 1, cap))
+    assert csa.index_topk(L, iq, iw, keys, n, pos, invf, sel, n_sel).item() == 0
+    torch.cuda.synchronize()
+    want = sel.clone(), n_sel.clone()
+    for _ in range(5):
+        sel.zero_()
+        n_sel.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            keep_busy()
+        err = csa.index_topk(L, iq, iw, keys, n, pos, invf, sel, n_sel, stream=side)
+        others = [torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        for _ in range(200):
+            for t in others:
+                t.fill_(0xFF)
+        torch.cuda.synchronize()
+        assert err.item() == 0 and torch.equal(sel, want[0]) and torch.equal(n_sel, want[1])

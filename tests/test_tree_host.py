@@ -313,7 +313,7 @@ def test_norm_rope_takes_slices_of_wider_tensors(lib, calls):
 
 def test_norm_rope_returns_its_error_word(lib, calls, monkeypatch):
     """Without err= the call makes the word: it lives with the outputs, where the caller can read it."""
-    monkeypatch.setattr(B, "_tree_new", lambda device, stream, new, *size, dtype: _cuda_like(new(*size, dtype=dtype)))
+    monkeypatch.setattr(B, "_new", lambda device, stream, new, *size, dtype: _cuda_like(new(*size, dtype=dtype)))
     x = _cuda_like(z(2, 3, 8, 128))
     got = csa.norm_rope(LAYER, [x], outs=[_cuda_like(z(2, 3, 8, 128))])
     assert isinstance(got, list) and len(got) == 1
