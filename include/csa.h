@@ -32,6 +32,8 @@
  *   - Storage dtype (layer->dtype): CSA_BF16 or CSA_F32 for activations,
  *     weights, pools, windows and outputs ("model dtype").  APE, norm weights,
  *     sink logits and the RoPE table are always fp32.  Arithmetic is fp32.
+ *   - Any host thread may call, several at once; calls in flight together need
+ *     workspaces and outputs of their own (the static scratch: see that call).
  *   - All work is enqueued asynchronously on `stream` (a cudaStream_t; NULL is
  *     the legacy default stream).  No call synchronises or reads device memory
  *     on the host, so calls can be captured in a CUDA graph.
