@@ -88,3 +88,48 @@ def test_workspaces_stay_with_the_calls_stream():
                 t.fill_(0xFF)
         torch.cuda.synchronize()
         assert err.item() == 0 and torch.equal(sel, want[0]) and torch.equal(n_sel, want[1])
+
+
+@pytest.mark.parametrize("graphs", [False, True])
+def test_tree_steps_on_two_streams_at_once(graphs):
+    """Whole tree steps of two batches of different sizes, enqueued (or replayed) on two streams without waiting for one
+    another: each gives what it gives alone."""
+    from tests import _tree as TR
+    from tests import test_gpu_tree as T0
+    cfg = FLASH
+    shapes = (([TR.bushy(16, s) for s in range(12)], [2100 + 37 * s for s in range(12)]),
+              ([TR.bushy(5), TR.chain(8)], [3001, 700]))
+    names, T = ("out", "sel", "scores", "rows_a", "rows_i", "proj_a", "q2", "kv2"), [16, 8]
+    ds = [T0._step(cfg, trees, pos, 900, seed=1000 + k) for k, (trees, pos) in enumerate(shapes)]
+    errs, streams = [T0.err_word() for _ in ds], [torch.cuda.Stream() for _ in ds]
+    wss = [dict(c=torch.empty(256, dtype=torch.uint8, device="cuda"),
+                a=torch.empty(csa.workspace_size(d["L"], csa.OP_ATTEND_TREE, len(s[1]), t, 900), dtype=torch.uint8,
+                              device="cuda")) for d, s, t in zip(ds, shapes, T)]
+    want = []
+    for d, e, w in zip(ds, errs, wss):
+        T0.run_step(cfg, d, e, w)
+        torch.cuda.synchronize()
+        want.append([d[k].clone() for k in names])
+    runs = []
+    for d, e, w, s in zip(ds, errs, wss, streams):
+        if graphs:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                T0.run_step(cfg, d, e, w)
+            runs.append(g.replay)
+        else:
+            runs.append(lambda d=d, e=e, w=w: T0.run_step(cfg, d, e, w))
+    for _ in range(10):
+        for d in ds:
+            for k in names:
+                d[k].zero_()
+        torch.cuda.synchronize()
+        for _ in range(8):
+            for r, s in zip(runs, streams):
+                with torch.cuda.stream(s):
+                    r()
+        torch.cuda.synchronize()
+        for d, w in zip(ds, want):
+            for k, t in zip(names, w):
+                assert torch.equal(d[k], t), k
+    assert all(e.item() == 0 for e in errs)
