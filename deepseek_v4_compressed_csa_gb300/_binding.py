@@ -325,9 +325,12 @@ def workspace_size(layer: Layer, op: int, B: int, T: int, cap: int) -> int:
 
 
 def _new(device, stream, new, *size, dtype):
-    """A tensor of the call's own: allocated, and zeroed where it is, on the stream that will use it."""
+    """A tensor of the call's own: allocated, and zeroed where it is, on the stream that will use it (torch's, or any
+    object with its handle as cuda_stream)."""
     if stream is None:
         return new(*size, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
     with torch.cuda.stream(stream):
         return new(*size, dtype=dtype, device=device)
 

@@ -133,3 +133,26 @@ def test_tree_steps_on_two_streams_at_once(graphs):
             for k, t in zip(names, w):
                 assert torch.equal(d[k], t), k
     assert all(e.item() == 0 for e in errs)
+
+
+def test_streams_by_handle():
+    """stream= takes any object that has a handle, a side stream's or the default stream's, with and without buffers of
+    the caller's."""
+    class Handle:
+        def __init__(self, handle):
+            self.cuda_stream = handle
+    side = torch.cuda.Stream()
+    cfg = FLASH
+    x, L, invf = rnd((2, 3, 8, 128), 20), G.lib_layer(cfg), csa_synth.inv_freq(cfg).cuda()
+    want = csa.norm_rope(L, [x], i32(7, 9), invf)[0]
+    pos = i32(7, 9)
+    torch.cuda.synchronize()
+    for handle in (side.cuda_stream, torch.cuda.default_stream().cuda_stream):
+        for name, call, word in jobs():
+            torch.cuda.synchronize()
+            err = call(Handle(handle))
+            torch.cuda.synchronize()
+            assert err.item() == word, (name, handle)
+        got = csa.norm_rope(L, [x], pos, invf, stream=Handle(handle))
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want) and got.err.item() == 0
