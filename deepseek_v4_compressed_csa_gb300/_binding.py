@@ -27,6 +27,7 @@ CSA_F32, CSA_BF16 = 0, 1
 OP_COMPRESS, OP_INDEX_TOPK, OP_ATTEND_DECODE, OP_ATTEND_PREFILL, OP_COMPRESS_PAIR = 0, 1, 2, 3, 4
 OP_COMPRESS_VARLEN, OP_ATTEND_PREFILL_VARLEN = 5, 6
 OP_COMPRESS_TREE, OP_ATTEND_TREE, OP_INDEX_SCORES_TREE = 7, 8, 9
+OP_ATTEND_PAGES = 10
 FP8_ROW_BYTES = 144  # CSA_FP8_ROW_BYTES: 128 E4M3 codes, the fp32 scale, 12 zero bytes
 DEV_CAPACITY, DEV_STATE, DEV_RANGE, DEV_ROLLBACK = 1, 2, 4, 8
 CSA_OK, CSA_ERR_ARG, CSA_ERR_UNSUPPORTED, CSA_ERR_CUDA, CSA_ERR_WORKSPACE = 0, 1, 2, 3, 4
@@ -36,7 +37,7 @@ EXPORTS = ("csa_kernel_launches", "csa_frontier_slots", "csa_workspace_size", "c
            "csa_index_topk_static", "csa_index_topk_overlapped", "csa_advance_positions",
            "csa_compress_append_pair", "csa_trim", "csa_index_topk_verify", "csa_attend_verify",
            "csa_compress_append_varlen", "csa_attend_prefill_varlen", "csa_index_rows_fp8", "csa_norm_rope",
-           "csa_compress_tree", "csa_index_scores_tree", "csa_attend_tree", "csa_commit_tree")
+           "csa_compress_tree", "csa_index_scores_tree", "csa_attend_tree", "csa_commit_tree", "csa_add_norm", "csa_append_pages", "csa_attend_pages")
 
 
 class CSAError(RuntimeError):
@@ -64,7 +65,7 @@ class _Rows(ctypes.Structure):
 
 
 # the same layouts for struct.pack, a few microseconds a call cheaper than building ctypes structures
-_COMP_FMT, _ROWS_FMT = "@4Pi0P", "@3P3iq"
+_COMP_FMT, _ROWS_FMT, _PAGES_FMT = "@4Pi0P", "@3P3iq", "@2P2i"
 
 
 _lib = None
@@ -134,6 +135,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.csa_commit_tree.argtypes = [vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp,
                                     i32, vp, vp, vp, vp]
     lib.csa_commit_tree.restype = i32
+    i64 = ctypes.c_longlong
+    lib.csa_add_norm.argtypes = [vp, vp, i64, vp, i64, vp, i64, i32, vp, vp, vp, vp, i32, vp]
+    lib.csa_add_norm.restype = i32
+    lib.csa_append_pages.argtypes = [vp, vp, vp, i64, i64, i32, i32, vp, i32, vp, vp, vp, i32, vp, vp, vp]
+    lib.csa_append_pages.restype = i32
+    lib.csa_attend_pages.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, vp, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, sz,
+                                     vp, vp]
+    lib.csa_attend_pages.restype = i32
     if os.path.exists(_CHECKS_PATH):  # (not built where Python's headers are missing)
         spec = importlib.util.spec_from_file_location("csa_checks", _CHECKS_PATH)
         module = importlib.util.module_from_spec(spec)
@@ -922,3 +931,197 @@ def commit_tree(layer: Layer, parent, leaf, pos, n_rows_a, kv, window, proj_a, f
     _tree_call("csa_commit_tree", dev, stream, layer._packed(), B, T, *p[:10], cap_a, *p[10:12], *pi, err.data_ptr())
     return err
 
+
+def _row_stride(name: str, t, width: int) -> int:
+    """Elements between the rows of a tensor [.., width] whose rows are one stride apart and contiguous themselves (0:
+    dense)."""
+    if t.is_contiguous():
+        return 0
+    shape, st = t.shape, t.stride()
+    lead = [(n, k) for n, k in zip(shape[:-1], st[:-1]) if n != 1]
+    ok = st[-1] == 1 or width == 1
+    for (_, k), (n, inner) in zip(lead, lead[1:]):
+        ok = ok and k == n * inner
+    step = lead[-1][1] if lead else 0
+    if not ok or (lead and step < width):
+        raise ValueError(f"{name}: strides {st}; rows must be contiguous, one stride of at least a row apart")
+    return step
+
+
+class NormOutputs(tuple):
+    """add_norm's outputs (out, residual_out, codes, scales); None for what was not asked for."""
+
+    out = property(lambda self: self[0])
+    residual = property(lambda self: self[1])
+    codes = property(lambda self: self[2])
+    scales = property(lambda self: self[3])
+
+
+def add_norm(layer: Layer, x, residual=None, weight=None, group=None, out=None, residual_out=None, codes=None,
+             scales=None, stream=None):
+    """csa_add_norm: rows x [.., X] (+ residual [.., X]) RMS-normed (weight fp32 [X] or None); with `group` also in 8
+    bits: codes uint8 [.., X] (E4M3) and scales fp32 [.., X / group], of groups of 8 to 256 values (a power of two) or
+    whole rows (group = X).  Outputs are those given, or new tensors; out=False or residual_out=False leaves that one
+    out (the latter also where there is no residual).  residual_out may be x or residual itself, and so may out.  Rows of
+    x and residual may be a stride apart.  Returns (out, residual_out, codes, scales) as NormOutputs."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise TypeError("x: expected a tensor [.., X]")
+    dtype, shape = layer.dtype, x.shape
+    X = shape[-1]
+    if x.dtype is not dtype:
+        raise TypeError(f"x: dtype {x.dtype}, expected {dtype}")
+    if not x.is_cuda:
+        raise ValueError("x: CSA tensors must live on a CUDA device")
+    dev = x.get_device()
+    N = x.numel() // X if X else 0
+    x_stride = _row_stride("x", x, X)
+    if out is None:
+        out = _new(x.device, stream, torch.empty, shape, dtype=dtype)
+    if residual is None:
+        if residual_out is not None and residual_out is not False:
+            raise ValueError("residual_out comes with residual")
+    elif residual_out is None:
+        residual_out = _new(x.device, stream, torch.empty, shape, dtype=dtype)
+    specs, r_stride = [], 0
+    if residual is not None:
+        if not (isinstance(residual, torch.Tensor) and residual.dtype is dtype and residual.shape == shape
+                and residual.get_device() == dev):
+            _refuse("residual", residual, dtype, shape, dev)
+        r_stride = _row_stride("residual", residual, X)
+    if weight is not None:
+        specs.append(("weight", weight, torch.float32, (X,)))
+    has_out, has_res = out is not False, residual_out is not None and residual_out is not False
+    if has_out:
+        specs.append(("out", out, dtype, shape))
+    if has_res:
+        specs.append(("residual_out", residual_out, dtype, shape))
+    if group is not None:
+        if group < 1 or X % group:
+            raise ValueError(f"group = {group}: expected a divisor of {X}")
+        few = (*shape[:-1], X // group)
+        if codes is None:
+            codes = _new(x.device, stream, torch.empty, shape, dtype=torch.uint8)
+        if scales is None:
+            scales = _new(x.device, stream, torch.empty, few, dtype=torch.float32)
+        specs += (("codes", codes, torch.uint8, shape), ("scales", scales, torch.float32, few))
+    elif codes is not None or scales is not None:
+        raise ValueError("codes and scales come with group")
+    p = iter(_ptrs(dev, *specs))
+    p_w = next(p) if weight is not None else None
+    p_out = next(p) if has_out else None
+    p_res = next(p) if has_res else None
+    p_codes, p_scales = (next(p), next(p)) if group is not None else (None, None)
+    _tree_call("csa_add_norm", dev, stream, layer._packed(), x.data_ptr(), x_stride,
+               None if residual is None else residual.data_ptr(), r_stride, p_w, N, X, p_out, p_res, p_codes, p_scales,
+               group or 0)
+    return NormOutputs((out if has_out else None, residual_out if has_res else None, codes, scales))
+
+
+@dataclass(frozen=True)
+class Pages:
+    """A pool of cache pages in 8 bits (csa_pages): codes uint8 [n_pages, page_rows, D] (E4M3), scales fp32 [n_pages,
+    page_rows]; a row stands for scale * code."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    def _specs(self, layer: Layer) -> tuple:
+        """What _ptrs checks of the pool's two tensors."""
+        c = self.codes
+        if not isinstance(c, torch.Tensor) or c.dim() != 3 or c.shape[2] != layer.D:
+            raise ValueError(f"Pages.codes: expected a uint8 tensor [n_pages, page_rows, {layer.D}]")
+        shape = c.shape
+        return ("Pages.codes", c, torch.uint8, shape), ("Pages.scales", self.scales, torch.float32, shape[:2])
+
+    def _packed(self, p_codes: int, p_scales: int) -> bytes:
+        n, rows = self.scales.shape
+        return struct.pack(_PAGES_FMT, p_codes, p_scales, n, rows)
+
+
+def _table(name: str, t, B: int):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[0] != B:
+        raise ValueError(f"{name}: expected an int32 tensor [{B}, pages of a sequence]")
+    return (name, t, torch.int32, t.shape)
+
+
+def append_pages(layer: Layer, rows, pages: Pages, table, pos, n_new=None, weight=None, norm=False, inv_freq=None,
+                 err=None, stream=None):
+    """csa_append_pages: rows [B, T, D] become logical rows pos[b] .. pos[b] + n_new[b] - 1 (n_new None: T each) of the
+    sequences' tables [B, width]: RMS-normed (norm, with weight fp32 [D] or None), rotated to those positions (inv_freq;
+    None: not rotated) and put in 8 bits with a scale per row.  A token of rows is contiguous; tokens and sequences may be
+    strides apart.  Returns the device error word tensor."""
+    D, i32, f32 = layer.D, torch.int32, torch.float32
+    B, T, dev = _tree_dims("rows", rows, (D,))
+    if rows.dtype is not layer.dtype:
+        raise TypeError(f"rows: dtype {rows.dtype}, expected {layer.dtype}")
+    stride_b = stride_t = 0
+    if not rows.is_contiguous():
+        st = rows.stride()
+        if st[2] != 1 or (T > 1 and st[1] < D) or (B > 1 and st[0] < D):
+            raise ValueError(f"rows: strides {st}; a token must be contiguous, tokens and sequences at least one apart")
+        stride_t = st[1] if T > 1 else 0
+        stride_b = st[0] if B > 1 else 0
+    if weight is not None and not norm:
+        raise ValueError("weight comes with norm")
+    specs = [*pages._specs(layer), _table("table", table, B), ("pos", pos, i32, (B,))]
+    if n_new is not None:
+        specs.append(("n_new", n_new, i32, (B,)))
+    if weight is not None:
+        specs.append(("weight", weight, f32, (D,)))
+    if inv_freq is not None:
+        specs.append(("inv_freq", inv_freq, f32, (layer.R // 2,)))
+    p = iter(_ptrs(dev, *specs))
+    handle = pages._packed(next(p), next(p))
+    p_table, p_pos = next(p), next(p)
+    p_new = next(p) if n_new is not None else None
+    p_w = next(p) if weight is not None else None
+    p_frq = next(p) if inv_freq is not None else None
+    err = _tree_err(err, dev, stream)
+    _tree_call("csa_append_pages", dev, stream, layer._packed(), handle, rows.data_ptr(), stride_b, stride_t, B, T,
+               p_table, table.shape[1], p_pos, p_new, p_w, 1 if norm else 0, p_frq, err.data_ptr())
+    return err
+
+
+def attend_pages(layer: Layer, q, pages: Pages, sink, pos, out, token_table=None, first=0, row_table=None, n_rows=None,
+                 sel=None, n_sel=None, n_new=None, inv_freq=None, ws=None, err=None, stream=None):
+    """csa_attend_pages: rotated q [B, T, H, D], query i of sequence b at pos[b] + i, over the rows of a paged cache: the
+    last W tokens and the first `first` ones of token_table [B, width] (None: no tokens), and of row_table [B, width]
+    (None: no compressed rows) the rows sel [B, T, topk] with counts n_sel [B, T], or without sel every visible row below
+    n_rows [B].  sink fp32 [H] or None; n_new int32 [B]: the queries of each sequence (None: T); inv_freq: out
+    [B, T, H, D] is rotated back (None: not).  Returns the device error word tensor."""
+    dt, i32, f32, H, D = layer.dtype, torch.int32, torch.float32, layer.H, layer.D
+    B, T, dev = _tree_dims("q", q, (H, D))
+    if token_table is None and row_table is None:
+        raise ValueError("attend_pages needs token_table, row_table, or both")
+    if row_table is None and not (n_rows is None and sel is None and n_sel is None):
+        raise ValueError("n_rows, sel, n_sel come with row_table")
+    if (sel is None) != (n_sel is None):
+        raise ValueError("sel and n_sel come together")
+    specs = [*pages._specs(layer), ("q", q, dt, (B, T, H, D)), ("pos", pos, i32, (B,)), ("out", out, dt, (B, T, H, D))]
+    if sink is not None:
+        specs.append(("sink", sink, f32, (H,)))
+    if token_table is not None:
+        specs.append(_table("token_table", token_table, B))
+    if row_table is not None:
+        specs += (_table("row_table", row_table, B), ("n_rows", n_rows, i32, (B,)))
+    if sel is not None:
+        specs += (("sel", sel, i32, (B, T, layer.topk)), ("n_sel", n_sel, i32, (B, T)))
+    if n_new is not None:
+        specs.append(("n_new", n_new, i32, (B,)))
+    if inv_freq is not None:
+        specs.append(("inv_freq", inv_freq, f32, (layer.R // 2,)))
+    p = iter(_ptrs(dev, *specs))
+    handle = pages._packed(next(p), next(p))
+    p_q, p_pos, p_out = next(p), next(p), next(p)
+    p_sink = next(p) if sink is not None else None
+    p_tok = next(p) if token_table is not None else None
+    p_row, p_n = (next(p), next(p)) if row_table is not None else (None, None)
+    p_sel, p_ns = (next(p), next(p)) if sel is not None else (None, None)
+    p_new = next(p) if n_new is not None else None
+    p_frq = next(p) if inv_freq is not None else None
+    ws, nb = _tree_ws(layer, OP_ATTEND_PAGES, B, T, 1, ws, dev, stream)
+    err = _tree_err(err, dev, stream)
+    _tree_call("csa_attend_pages", dev, stream, layer._packed(), handle, p_q, B, T, p_sink, p_pos, p_new, p_tok,
+               0 if p_tok is None else token_table.shape[1], first, p_row, 0 if p_row is None else row_table.shape[1],
+               p_n, p_sel, p_ns, p_frq, p_out, ws.data_ptr(), nb, err.data_ptr())
+    return err

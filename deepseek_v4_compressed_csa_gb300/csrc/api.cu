@@ -5,6 +5,7 @@
 #include "kernels.h"
 
 #include <atomic>
+#include <initializer_list>
 
 using namespace csa;
 
@@ -116,6 +117,31 @@ size_t ws_attend_tree(const Dims& L, int B, int T, int cap) {
   return c.off;
 }
 
+size_t ws_attend_pages(const Dims& L, int Q) {
+  Carver c(nullptr);
+  PagedArgs a{};
+  carve_paged(c, L, Q, &a);
+  return c.off;
+}
+// B x T queries or new tokens around a cache in pages
+constexpr int kPagedQueries = 1 << 16;
+constexpr long long kPagedRows = INT32_MAX - 256;  // rows of the pool (their numbers are ints)
+constexpr long long kPagedTable = 1 << 30;         // rows that a sequence's table has room for
+bool pages_ok(const csa_pages* p) {
+  return p && dev_tensor(p->codes) && dev_i32(p->scales) && p->n_pages >= 1 && p->page_rows >= 1 &&
+         (long long)p->n_pages * p->page_rows <= kPagedRows;
+}
+bool table_ok(const csa_pages* p, const int32_t* table, int pages) {
+  return dev_i32(table) && pages >= 1 && (long long)pages * p->page_rows <= kPagedTable;
+}
+// [lo, hi) of a tensor of n rows of `row` bytes, `stride` bytes apart
+struct Span {
+  uintptr_t lo, hi;
+  Span(const void* p, long long n, long long row, long long stride)
+      : lo(reinterpret_cast<uintptr_t>(p)), hi(lo + (uintptr_t)((n - 1) * stride + row)) {}
+  bool meets(const Span& o) const { return lo < o.hi && o.lo < hi; }
+};
+
 }  // namespace
 
 extern "C" {
@@ -182,6 +208,10 @@ csa_status csa_workspace_size(const csa_layer* layer, int op, int B, int T, int 
     case CSA_OP_INDEX_SCORES_TREE:
       if (!tree_sizes_ok(B, T)) return CSA_ERR_ARG;
       *bytes = tree_scores_ws(L, B, T);
+      return CSA_OK;
+    case CSA_OP_ATTEND_PAGES:
+      if (T < 1 || (long long)B * T > kPagedQueries) return CSA_ERR_ARG;
+      *bytes = ws_attend_pages(L, B * T);
       return CSA_OK;
   }
   return CSA_ERR_ARG;
@@ -584,6 +614,100 @@ csa_status csa_commit_tree(const csa_layer* layer, int B, int T, const int32_t* 
   t.n_rows[1] = n_rows_i; t.n_rows_out[1] = n_rows_i_out; t.cap[1] = cap_i;
   t.npool = pool_i ? 2 : 1; t.B = B; t.T = T;
   return cuda_status(launch_commit_tree(L, t, err, static_cast<cudaStream_t>(stream)));
+}
+
+csa_status csa_add_norm(const csa_layer* layer, const void* x, long long x_stride, const void* residual,
+                        long long residual_stride, const float* weight, long long N, int X, void* out,
+                        void* residual_out, void* codes, float* scales, int group, void* stream) {
+  Dims L;
+  csa_status st = make_dims(layer, &L);
+  if (st != CSA_OK) return st;
+  if (N < 0 || N > INT32_MAX || X < 8 || X % 8 || X > 16384) return CSA_ERR_ARG;
+  if (N == 0) return CSA_OK;  // (its tensors may have no address)
+  if ((codes == nullptr) != (scales == nullptr) || (!out && !residual_out && !codes)) return CSA_ERR_ARG;
+  if (codes && group != X && (group < 8 || group > 256 || (group & (group - 1)) || X % group)) return CSA_ERR_ARG;
+  if (!dev_tensor(x) || (residual && !dev_tensor(residual)) || (weight && !dev_tensor(weight))) return CSA_ERR_ARG;
+  if ((out && !dev_tensor(out)) || (residual_out && !dev_tensor(residual_out)) || (codes && !dev_tensor(codes)) ||
+      (scales && !dev_i32(scales)))
+    return CSA_ERR_ARG;
+  for (long long stride : {x_stride, residual_stride})
+    if (stride != 0 && (stride < X || stride % 8 || stride > (1LL << 31))) return CSA_ERR_ARG;
+  AddNorm t{x, residual, weight, out, residual_out, static_cast<uint8_t*>(codes), scales, N,
+            x_stride ? x_stride : X, residual_stride ? residual_stride : X, X, codes ? group : X};
+  // a thread writes what it has read itself: an output may be a dense input, and nothing else that is read or written
+  const long long es = (long long)esize(L.dtype), row = X * es, n = N;
+  const Span in[2] = {Span(x, n, row, t.x_stride * es), Span(residual ? residual : x, n, row, (residual ? t.r_stride : t.x_stride) * es)};
+  const long long in_stride[2] = {t.x_stride, residual ? t.r_stride : t.x_stride};
+  const void* outs[4] = {out, residual_out, codes, scales};
+  const long long bytes[4] = {row, row, X, (long long)(X / t.group) * 4};
+  for (int i = 0; i < 4; ++i) {
+    if (!outs[i]) continue;
+    const Span o(outs[i], n, bytes[i], bytes[i]);
+    for (int k = 0; k < 2; ++k)
+      if (o.meets(in[k]) && !(i < 2 && o.lo == in[k].lo && in_stride[k] == X)) return CSA_ERR_ARG;
+    if (weight && o.meets(Span(weight, 1, X * 4LL, 0))) return CSA_ERR_ARG;
+    for (int k = 0; k < i; ++k)
+      if (outs[k] && o.meets(Span(outs[k], n, bytes[k], bytes[k]))) return CSA_ERR_ARG;
+  }
+  return cuda_status(launch_add_norm(L, t, static_cast<cudaStream_t>(stream)));
+}
+
+csa_status csa_append_pages(const csa_layer* layer, const csa_pages* pages, const void* rows, long long stride_b,
+                            long long stride_t, int B, int T, const int32_t* table, int width, const int32_t* pos,
+                            const int32_t* n_new, const float* weight, int norm, const float* inv_freq, int32_t* err,
+                            void* stream) {
+  Dims L;
+  csa_status st = make_dims(layer, &L);
+  if (st != CSA_OK) return st;
+  if (B < 1 || T < 1 || (long long)B * T > (1 << 24) || (norm != 0 && norm != 1)) return CSA_ERR_ARG;
+  if (!pages_ok(pages) || !table_ok(pages, table, width) || !dev_tensor(rows) || !dev_i32(pos) || !dev_i32(err))
+    return CSA_ERR_ARG;
+  if ((n_new && !dev_i32(n_new)) || (weight && !dev_tensor(weight)) || (inv_freq && !dev_tensor(inv_freq)))
+    return CSA_ERR_ARG;
+  if (stride_t != 0 && (stride_t < L.D || stride_t % 8 || stride_t > (1LL << 31))) return CSA_ERR_ARG;
+  const long long st_t = stride_t ? stride_t : L.D, st_b = stride_b ? stride_b : T * st_t;
+  if (st_b % 8 || st_b < 0 || st_b > (1LL << 40)) return CSA_ERR_ARG;
+  PagedAppend t{rows, st_b, st_t, static_cast<uint8_t*>(pages->codes), pages->scales, table, pos, n_new, weight,
+                inv_freq, err, L.eps, pages->n_pages, pages->page_rows, width, B, T, L.D, L.R, norm};
+  return cuda_status(launch_append_pages(L, t, static_cast<cudaStream_t>(stream)));
+}
+
+csa_status csa_attend_pages(const csa_layer* layer, const csa_pages* pages, const void* q, int B, int T,
+                            const float* sink, const int32_t* pos, const int32_t* n_new, const int32_t* token_table,
+                            int token_width, int first, const int32_t* row_table, int row_width, const int32_t* n_rows,
+                            const int32_t* sel, const int32_t* n_sel, const float* inv_freq, void* out, void* ws,
+                            size_t ws_bytes, int32_t* err, void* stream) {
+  Dims L;
+  csa_status st = make_dims(layer, &L);
+  if (st != CSA_OK) return st;
+  if (B < 1 || T < 1 || (long long)B * T > kPagedQueries || first < 0) return CSA_ERR_ARG;
+  if (!pages_ok(pages) || !dev_tensor(q) || !dev_tensor(out) || !dev_i32(pos) || !dev_i32(err)) return CSA_ERR_ARG;
+  if (!token_table && !row_table) return CSA_ERR_ARG;
+  if (token_table && !table_ok(pages, token_table, token_width)) return CSA_ERR_ARG;
+  if (row_table && (!table_ok(pages, row_table, row_width) || !dev_i32(n_rows))) return CSA_ERR_ARG;
+  if (sel && (!row_table || !L.has_indexer() || !dev_i32(sel) || !dev_i32(n_sel))) return CSA_ERR_ARG;
+  if ((sink && !dev_i32(sink)) || (n_new && !dev_i32(n_new)) || (inv_freq && !dev_tensor(inv_freq)))
+    return CSA_ERR_ARG;
+  const long long n = (long long)B * T, row = (long long)L.H * L.D * esize(L.dtype);
+  if (Span(q, n, row, row).meets(Span(out, n, row, row))) return CSA_ERR_ARG;
+  // the tiles of a call are counted in ints; the smallest hold 32 keys, and each of a query's three sections ends one
+  const long long P = pages->page_rows;
+  const long long most = (row_table ? (sel ? (long long)L.topk : row_width * P) : 0) + (token_table ? token_width * P : 0);
+  if (n * (most / 32 + 4) > INT32_MAX) return CSA_ERR_ARG;
+  if (ws_bytes < ws_attend_pages(L, (int)n) || !dev_tensor(ws)) return CSA_ERR_WORKSPACE;
+  PagedArgs a{};
+  Carver c(ws);
+  carve_paged(c, L, (int)n, &a);
+  a.codes = static_cast<const uint8_t*>(pages->codes);
+  a.scales = pages->scales;
+  a.q = q; a.out = out; a.sink = sink; a.inv_freq = inv_freq;
+  a.pos = pos; a.n_new = n_new; a.token_table = token_table; a.row_table = row_table; a.n_rows = n_rows;
+  a.sel = sel; a.n_sel = n_sel;
+  a.n_pages = pages->n_pages; a.P = pages->page_rows; a.token_pages = token_width; a.row_pages = row_width;
+  a.B = B; a.T = T; a.H = L.H; a.D = L.D; a.R = L.R; a.W = L.W; a.first = first; a.ratio = L.ratio; a.topk = L.topk;
+  a.scale2 = L.scale * 1.4426950408889634f;
+  a.err = err;
+  return cuda_status(launch_attend_pages(L, a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -375,4 +375,56 @@ struct TreeCommit {
 };
 cudaError_t launch_commit_tree(const Dims& L, const TreeCommit& c, int32_t* err, cudaStream_t s);
 
+// ---- add_norm.cu: h = x + residual, its RMS norm, and the norm in 8 bits
+struct AddNorm {
+  const void *x, *residual;   // [N, X], rows x_stride, r_stride elements apart; residual may be null
+  const float* weight;        // [X] or null
+  void *out, *residual_out;   // [N, X] or null
+  uint8_t* codes;             // [N, X] or null
+  float* scales;              // [N, X / group]
+  long long N, x_stride, r_stride;
+  int X, group;
+};
+cudaError_t launch_add_norm(const Dims& L, const AddNorm& t, cudaStream_t s);
+
+// ---- a cache in pages and 8 bits
+struct PagedAppend {
+  const void* rows;            // [B, T, D], strides in elements
+  long long stride_b, stride_t;
+  uint8_t* codes;              // [n_pages, P, D]
+  float* scales;               // [n_pages, P]
+  const int32_t *table, *pos, *n_new;
+  const float *weight, *inv_freq;
+  int32_t* err;
+  float eps;
+  int n_pages, P, pages, B, T, D, R, norm;
+};
+// ---- paged_append.cu
+cudaError_t launch_append_pages(const Dims& L, const PagedAppend& t, cudaStream_t s);
+
+struct PagedArgs {
+  const uint8_t* codes;        // [n_pages, P, D]
+  const float* scales;         // [n_pages, P]
+  const void* q;               // [B, T, H, D], rotated
+  void* out;                   // [B, T, H, D]
+  const float *sink, *inv_freq;  // either may be null
+  const int32_t *pos, *n_new, *token_table, *row_table, *n_rows, *sel, *n_sel;
+  int n_pages, P, token_pages, row_pages;  // the pool's pages, rows a page, and the tables' widths
+  int B, T, H, D, R, W, first, ratio, topk;
+  int min_tiles;               // the shortest run of tiles of a block
+  float scale2;                // softmax scale * log2(e)
+  float* part;                 // [2 blocks, H, D] parts of split queries, relative to their maximum
+  float2* ml;                  // [2 blocks, H] their maxima (in powers of two) and sums
+  int2* parts;                 // [B T] block of a query's first part, and their count
+  int32_t* err;
+};
+// Blocks (one an SM) that a call is spread over at most.
+constexpr int kPagedBlocks = 152;
+void carve_paged(Carver& c, const Dims& L, int Q, PagedArgs* a);
+// ---- paged_attend.cu: the portable kernel, and the merge of split queries
+cudaError_t launch_attend_pages(const Dims& L, PagedArgs a, cudaStream_t s);
+// ---- tc_paged_attend.cu (tensor cores; bf16, H = 64, D = 512, R = 64, pages of whole 8-row groups)
+bool tc_paged_supported(const Dims& L, int n_pages, int P);
+cudaError_t launch_tc_paged(const Dims& L, const PagedArgs& a, int blocks, cudaStream_t s);
+
 }  // namespace csa

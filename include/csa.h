@@ -17,7 +17,8 @@
  *   (*_varlen: a packed batch of chunks of different lengths; *_verify: verify
  *   blocks of T tokens per sequence; csa_trim: rewind for speculative decoding;
  *   csa_norm_rope: per-head norm and rotation of what they take; *_tree: a tree
- *   of drafted tokens per sequence.)
+ *   of drafted tokens per sequence; csa_add_norm: the hidden states' norm, in
+ *   the model dtype and 8 bits; *_pages: a cache in pages and 8 bits.)
  *
  * Definitions follow the pages the method is described on:
  *   [MTPLX#216]  "DeepSeek-V4-Flash: native deepseek_v4 AR backend"
@@ -98,7 +99,8 @@ enum {
   CSA_OP_ATTEND_PREFILL_VARLEN = 6, /* csa_attend_prefill_varlen: B sequences, T = N packed tokens */
   CSA_OP_COMPRESS_TREE = 7,         /* csa_compress_tree: B trees of T nodes */
   CSA_OP_ATTEND_TREE = 8,           /* csa_attend_tree: B trees of T nodes */
-  CSA_OP_INDEX_SCORES_TREE = 9      /* csa_index_scores_tree: B trees of T nodes */
+  CSA_OP_INDEX_SCORES_TREE = 9,     /* csa_index_scores_tree: B trees of T nodes */
+  CSA_OP_ATTEND_PAGES = 10          /* csa_attend_pages: B sequences of T queries (cap ignored) */
 };
 
 /* One CSA layer.
@@ -554,6 +556,100 @@ csa_status csa_commit_tree(const csa_layer* layer, int B, int T, const int32_t* 
                            int32_t* n_rows_a_out, const void* proj_i, void* frontier_i, const void* rows_i,
                            void* pool_i, int cap_i, const int32_t* n_rows_i, int32_t* n_rows_i_out, int32_t* err,
                            void* stream);
+
+/* csa_add_norm — the hidden states that a layer takes: the residual's addition,
+ * the RMS norm, and the norm once more in 8 bits, in one pass.
+ *
+ * Definition (per row of X values, in fp32):
+ *   h = x + residual                                  (residual NULL: h = x)
+ *   y = h * (mean(h^2) + rms_eps)^-1/2 * weight       (weight NULL: ones)
+ *   residual_out = h, out = y, each rounded to the model dtype once;
+ *   per group of `group` values of y: scale = max |y| / 448,
+ *   codes = E4M3(y / scale) (nearest even, saturating), zeros where the scale is 0.
+ * The norm is that of the fp32 sum, not of the rounded one.  A NaN makes its
+ * group's scale NaN; codes and scales stand for code * scale.
+ * Arguments
+ *   x, residual     N rows of X model-dtype values, x_stride / residual_stride
+ *                   elements apart (0: dense; else a multiple of 8, at least X)
+ *   weight [X] fp32 or NULL
+ *   out, residual_out [N, X] model dtype, dense; either may be NULL
+ *   codes [N, X] bytes and scales [N, X / group] fp32, both or neither (group is
+ *                   then ignored)
+ *   group           8, 16, 32, 64, 128 or 256, dividing X; or X
+ * An output may be x or residual itself where that is dense; apart from that no
+ * output may overlap an input or another output (CSA_ERR_ARG, as are no output
+ * at all, X not a multiple of 8 or above 16384, N < 0 or above 2^31 - 1).  N == 0
+ * enqueues nothing.  One kernel on `stream`; it reads nothing before its
+ * predecessors in the stream have completed, and the next kernel starts once it
+ * has written, so its outputs may be any call's inputs. */
+csa_status csa_add_norm(const csa_layer* layer, const void* x, long long x_stride, const void* residual,
+                        long long residual_stride, const float* weight, long long N, int X, void* out,
+                        void* residual_out, void* codes, float* scales, int group, void* stream);
+
+/* csa_append_pages, csa_attend_pages — a layer's cache in pages and 8 bits.
+ *
+ * The pool of pages (csa_pages, caller-owned device memory) holds rows of D
+ * values: codes [n_pages, page_rows, D] E4M3 and scales [n_pages, page_rows]
+ * fp32, a row standing for scale * code.  table [B, width] int32 names, for
+ * sequence b, the page of its logical rows [k page_rows, (k + 1) page_rows) in
+ * table[b][k].  Pages of one pool may belong to tables of different kinds: a
+ * token table (logical row t is token t's latent row) and a table of compressed
+ * rows.  A page that nothing reads or writes any more (tokens behind the window)
+ * may be handed out again, its entry be anything.
+ * pos [B] int32: the position of each sequence's first query or new row of the
+ * call; n_new [B] int32 or NULL (T each): how many of its T are there, 0 .. T.
+ * What lies behind them is neither read for a result nor written.
+ * At most 2^31 - 257 rows in a pool, 2^30 in a table; a table's entry outside
+ * [0, n_pages) that a call meets raises CSA_DEV_RANGE, a row behind the table's
+ * width CSA_DEV_CAPACITY, and the row is left out; pos[b] < 0 or above
+ * 2^31 - 1 - T or n_new[b] outside [0, T] raises CSA_DEV_STATE and skips the sequence.
+ * Both calls read nothing before their predecessors in the stream have completed,
+ * and the next kernel starts once they have written.
+ *
+ * csa_append_pages: rows [B, T, D] model dtype become the logical rows
+ * pos[b] + i, i < n_new[b], of table's sequences.  Per row, in fp32:
+ *   y = x * (mean(x^2) + rms_eps)^-1/2 * weight   (norm != 0; weight NULL: ones)
+ *   y = RoPE(y, pos[b] + i)                       (inv_freq NULL: no rotation)
+ *   scale = max |y| / 448, codes = E4M3(y / scale) (nearest even, saturating;
+ *   zeros where the scale is 0, a NaN scale for a row with a NaN)
+ * stride_b, stride_t: elements between sequences and tokens (0: dense; else
+ * multiples of 8, tokens at least D apart).  B * T <= 2^24.  Two rows of one call
+ * in one place (tables that share a page being written) leave either of them. */
+typedef struct {
+  void* codes;
+  float* scales;
+  int n_pages, page_rows;
+} csa_pages;
+csa_status csa_append_pages(const csa_layer* layer, const csa_pages* pages, const void* rows, long long stride_b,
+                            long long stride_t, int B, int T, const int32_t* table, int width, const int32_t* pos,
+                            const int32_t* n_new, const float* weight, int norm, const float* inv_freq, int32_t* err,
+                            void* stream);
+
+/* csa_attend_pages: query i < n_new[b] of sequence b, at p = pos[b] + i, attends
+ *   compressed rows: row_table's rows sel[b][i][0 .. n_sel[b][i]) (each index as
+ *     often as it is listed; one outside [0, n_rows[b]) raises CSA_DEV_RANGE and
+ *     is left out), or without sel all rows j < n_rows[b] with
+ *     (j + 1) * ratio <= p + 1; none with row_table NULL;
+ *   tokens: token_table's rows t in [p - W + 1, p] (layer->W) and t in
+ *     [0, first), t >= 0, each once; none with token_table NULL;
+ *   l_hk = scale * q[b][i][h] . key_k,  o_h = sum_k e^{l_hk} key_k / (e^{sink_h} + sum_k e^{l_hk})
+ *   out[b][i][h] = RoPE^-1(o_h, p) in fp32, rounded to the model dtype once.
+ * The cache holds the queries' own rows already (csa_append_pages).  q is rotated
+ * (csa_norm_rope).  A query without any key gives zeros.
+ *   q, out [B, T, H, D] model dtype, apart from one another; sink [H] fp32 or NULL (no sink);
+ *   sel [B, T, topk], n_sel [B, T] int32 (ratio 4, with row_table); inv_freq NULL:
+ *   no rotation of the output.
+ * On the tensor cores (bf16, H = 64, D = 512, R = 64, page_rows a multiple of 8)
+ * queries and probabilities enter the products as two E4M3 parts each, about 8
+ * bits (what bf16 operands would keep), sums in fp32; the portable kernel takes any other layer, all in fp32.  A
+ * call's result depends on how its keys are cut into tiles, not on the run.
+ * B * T <= 2^16, and CSA_ERR_ARG where the tables' widths times B * T could hold 2^36 keys.
+ * Workspace: CSA_OP_ATTEND_PAGES. */
+csa_status csa_attend_pages(const csa_layer* layer, const csa_pages* pages, const void* q, int B, int T,
+                            const float* sink, const int32_t* pos, const int32_t* n_new, const int32_t* token_table,
+                            int token_width, int first, const int32_t* row_table, int row_width, const int32_t* n_rows,
+                            const int32_t* sel, const int32_t* n_sel, const float* inv_freq, void* out, void* ws,
+                            size_t ws_bytes, int32_t* err, void* stream);
 
 /* csa_index_topk_static — csa_index_topk without a caller-supplied workspace.
  *
