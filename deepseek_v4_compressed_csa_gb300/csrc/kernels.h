@@ -402,6 +402,8 @@ struct PagedAppend {
 // ---- paged_append.cu
 cudaError_t launch_append_pages(const Dims& L, const PagedAppend& t, cudaStream_t s);
 
+struct PagedQuery;
+struct PagedRun;
 struct PagedArgs {
   const uint8_t* codes;        // [n_pages, P, D]
   const float* scales;         // [n_pages, P]
@@ -411,20 +413,26 @@ struct PagedArgs {
   const int32_t *pos, *n_new, *token_table, *row_table, *n_rows, *sel, *n_sel;
   int n_pages, P, token_pages, row_pages;  // the pool's pages, rows a page, and the tables' widths
   int B, T, H, D, R, W, first, ratio, topk;
-  int min_tiles;               // the shortest run of tiles of a block
   float scale2;                // softmax scale * log2(e)
-  float* part;                 // [2 blocks, H, D] parts of split queries, relative to their maximum
-  float2* ml;                  // [2 blocks, H] their maxima (in powers of two) and sums
+  // workspace
+  PagedRun* runs;              // [kPagedBlocks] what each block works on
+  PagedQuery* queries;         // [B T]
   int2* parts;                 // [B T] block of a query's first part, and their count
+  float* part;                 // [2 blocks][D / cols][H][cols] parts of split queries, relative to their maximum
+  float2* ml;                  // [2 blocks][H] their maxima (in powers of two) and sums
+  uint8_t* q8;                 // tensor cores: [B T][32][128 rows][16] the queries' E4M3 parts
+  float* q8_scale;             // [B T][H]
+  int cols;                    // dims that a part holds side by side
+  int tile, shift, min_tiles;  // keys a tile; log2 of the rows that lie in one page; the shortest run of tiles
   int32_t* err;
 };
 // Blocks (one an SM) that a call is spread over at most.
 constexpr int kPagedBlocks = 152;
+// ---- paged_attend.cu: the plan, the portable kernel, and the merge of split queries
 void carve_paged(Carver& c, const Dims& L, int Q, PagedArgs* a);
-// ---- paged_attend.cu: the portable kernel, and the merge of split queries
 cudaError_t launch_attend_pages(const Dims& L, PagedArgs a, cudaStream_t s);
 // ---- tc_paged_attend.cu (tensor cores; bf16, H = 64, D = 512, R = 64, pages of whole 8-row groups)
-bool tc_paged_supported(const Dims& L, int n_pages, int P);
-cudaError_t launch_tc_paged(const Dims& L, const PagedArgs& a, int blocks, cudaStream_t s);
+bool tc_paged_supported(const Dims& L, int P);
+cudaError_t launch_tc_paged(const PagedArgs& a, cudaStream_t s);
 
 }  // namespace csa

@@ -123,12 +123,13 @@ def attend_ref(L, q, codes, s, sink, tensor_cores):
     n = lg.shape[1]
     err = A * (2 * d_lg + (n + 32) * U32)
     if tensor_cores:
-        # the queries' parts: 2^-14 of E4M3's smallest normal number below the largest value, 2^-23 of it; the
-        # probabilities' two parts: 2^-8 of each, or 2^-16 of the largest of p_k s_k (half of E4M3's smallest step, 2^-10,
-        # where the largest is at least 2^6); exp2 and its argument's fp32 rounding
-        err = err + A * (2.0 ** -8 + 2 * scale * q.abs().amax(1, keepdim=True) * 2.0 ** -23 * keys.abs().sum(1).max() + 2.0 ** -20)
+        # The queries' two E4M3 parts, the second 16 times finer: off by half of its smallest step, 2^-14 of the scale at
+        # which the head's largest value is at least 2^7 (so 2^-21 of it); exp2 and its argument's fp32 rounding.
+        err = err + A * (2 * scale * q.abs().amax(1, keepdim=True) * 2.0 ** -21 * keys.abs().sum(1).max() + 2.0 ** -20)
+        # The probabilities' parts of w = p s, E5M2 (at most 2^-3 off) and what that leaves in E4M3 (2^-4 of it, or half of
+        # its smallest step, 2^-10 where the largest w is at least 2^7).
         w = p * s
-        err = err + w.amax(1, keepdim=True) * 2.0 ** -16 * codes.abs().sum(0)[None]
+        err = err + (2.0 ** -7 * w + torch.minimum(2.0 ** -3 * w, w.amax(1, keepdim=True) * 2.0 ** -17)) @ codes.abs()
     return p @ keys, err
 
 
