@@ -402,8 +402,17 @@ struct PagedAppend {
 // ---- paged_append.cu
 cudaError_t launch_append_pages(const Dims& L, const PagedAppend& t, cudaStream_t s);
 
-struct PagedQuery;
-struct PagedRun;
+// n / d for 0 <= n < 2^31 by a multiplication: with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1,
+// n / d = (floor(m n / 2^32) + n) / 2^l (T. Granlund and P. L. Montgomery, Division by Invariant Integers).
+struct FastDiv {
+  uint32_t m;
+  int l;
+};
+inline FastDiv fast_div(uint32_t d) {
+  int l = 0;
+  while ((1ull << l) < d) ++l;
+  return FastDiv{(uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1), l};
+}
 struct PagedArgs {
   const uint8_t* codes;        // [n_pages, P, D]
   const float* scales;         // [n_pages, P]
@@ -411,24 +420,21 @@ struct PagedArgs {
   void* out;                   // [B, T, H, D]
   const float *sink, *inv_freq;  // either may be null
   const int32_t *pos, *n_new, *token_table, *row_table, *n_rows, *sel, *n_sel;
+  FastDiv by_page;             // division by P
   int n_pages, P, token_pages, row_pages;  // the pool's pages, rows a page, and the tables' widths
   int B, T, H, D, R, W, first, ratio, topk;
   float scale2;                // softmax scale * log2(e)
   // workspace
-  PagedRun* runs;              // [kPagedBlocks] what each block works on
-  PagedQuery* queries;         // [B T]
   int2* parts;                 // [B T] block of a query's first part, and their count
   float* part;                 // [2 blocks][D / cols][H][cols] parts of split queries, relative to their maximum
   float2* ml;                  // [2 blocks][H] their maxima (in powers of two) and sums
-  uint8_t* q8;                 // tensor cores: [B T][32][128 rows][16] the queries' E4M3 parts
-  float* q8_scale;             // [B T][H]
   int cols;                    // dims that a part holds side by side
   int tile, shift, min_tiles;  // keys a tile; log2 of the rows that lie in one page; the shortest run of tiles
   int32_t* err;
 };
 // Blocks (one an SM) that a call is spread over at most.
 constexpr int kPagedBlocks = 152;
-// ---- paged_attend.cu: the plan, the portable kernel, and the merge of split queries
+// ---- paged_attend.cu: the portable kernel, and the merge of split queries
 void carve_paged(Carver& c, const Dims& L, int Q, PagedArgs* a);
 cudaError_t launch_attend_pages(const Dims& L, PagedArgs a, cudaStream_t s);
 // ---- tc_paged_attend.cu (tensor cores; bf16, H = 64, D = 512, R = 64, pages of whole 8-row groups)

@@ -1,5 +1,5 @@
-// Attention over a cache in pages and 8 bits: the plan of a call, the portable kernel (any head layout and size, bf16 and
-// fp32), and the merge of queries that several blocks worked on.
+// Attention over a cache in pages and 8 bits: the portable kernel (any head layout and size, bf16 and fp32), and the merge
+// of queries that several blocks worked on.
 //
 //   l_k = scale q_h . key_k;  o_h = sum_k e^{l_k} key_k / (e^{sink_h} + sum_k e^{l_k});  out_h = RoPE^-1(o_h, p)
 //
@@ -11,158 +11,6 @@
 namespace csa {
 
 namespace {
-
-// ---------------------------------------------------------------- the plan
-// The last block: every query's keys and tiles, their sum, each block's run.  The others (tensor cores): the queries as
-// two E4M3 parts each, q = 2^e (hi + lo / 16), a warp a row, in the order in which the attention kernel's lanes take them.
-constexpr int kPlanThreads = 256;
-
-// Query q's keys; what is wrong with them raises error bits.
-__device__ __forceinline__ PagedQuery find_query(const PagedArgs& a, int q) {
-  PagedQuery k;
-  const int b = q / a.T, i = q - b * a.T, p0 = a.pos[b], n = a.n_new ? a.n_new[b] : a.T;
-  const bool ok = p0 >= 0 && p0 <= INT32_MAX - a.T && n >= 0 && n <= a.T;
-  int bits = ok ? 0 : CSA_DEV_STATE;
-  k.q = q;
-  k.p = p0 + i;
-  k.n0 = k.f = k.w0 = k.nw = k.n_rows = k.tiles = 0;
-  if (ok && i < n) {
-    if (a.row_table) {
-      k.n_rows = a.n_rows[b];
-      if (k.n_rows < 0) {
-        bits |= CSA_DEV_STATE;
-        k.n_rows = 0;
-      }
-      const int held = a.row_pages * a.P;  // rows that the table has room for (at most 2^30)
-      if (a.sel) {
-        k.n0 = a.n_sel[q];
-        if (k.n0 < 0 || k.n0 > a.topk) bits |= CSA_DEV_RANGE;
-        k.n0 = min(max(k.n0, 0), a.topk);
-        k.n_rows = min(k.n_rows, held);  // (a selected row behind the table's end is out of range)
-      } else {
-        k.n0 = min(k.n_rows, (int)(((unsigned)k.p + 1u) / (unsigned)a.ratio));
-        if (k.n0 > held) {
-          bits |= CSA_DEV_CAPACITY;
-          k.n0 = held;
-        }
-      }
-    }
-    if (a.token_table) {
-      int last = k.p;
-      const int held = a.token_pages * a.P;
-      if (last >= held) {
-        bits |= CSA_DEV_CAPACITY;
-        last = held - 1;
-      }
-      k.w0 = k.p >= a.W ? k.p - a.W + 1 : 0;
-      k.nw = max(0, last - k.w0 + 1);
-      k.f = min(min(a.first, k.w0), last + 1);
-    }
-    int tiles;
-    if (a.shift == 0) {
-      tiles = (int)(((long long)k.n0 + k.f + k.nw + a.tile - 1) / a.tile);
-    } else {
-      const TileCut c = cut_tiles(a.sel != nullptr, k, a.tile, a.shift);
-      const int per = a.tile >> a.shift;
-      tiles = c.sel_tiles + (int)(((long long)c.runs0 + c.runs1 + c.runs2 + per - 1) / per);
-    }
-    k.tiles = max(1, tiles);
-  }
-  if (bits) atomicOr(a.err, bits);
-  return k;
-}
-
-__device__ __forceinline__ void store_query(PagedQuery* r, const PagedQuery& k) {
-  reinterpret_cast<int4*>(r)[0] = make_int4(k.p, k.n0, k.f, k.w0);
-  reinterpret_cast<int4*>(r)[1] = make_int4(k.nw, k.n_rows, k.tiles, k.q);
-}
-
-__device__ __forceinline__ void make_plan(const PagedArgs& a, int* sm) {
-  const int Q = a.B * a.T, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int each = (Q + kPlanThreads - 1) / kPlanThreads, q0 = min(Q, tid * each), q1 = min(Q, q0 + each);
-  int mine = 0;
-  PagedQuery k;
-  for (int q = q0; q < q1; ++q) {
-    k = find_query(a, q);
-    store_query(a.queries + q, k);
-    mine += k.tiles;
-  }
-  int inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
-  }
-  if (lane == 31) sm[warp] = inc;
-  __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    before += w < warp ? sm[w] : 0;
-    total += sm[w];
-  }
-  const int per = max(a.min_tiles, (total + kPagedBlocks - 1) / kPagedBlocks);
-  int pre = before + inc - mine;
-  for (int q = q0; q < q1; ++q) {
-    if (each > 1) k = a.queries[q];
-    if (k.tiles > 0) {
-      const int c0 = pre / per, c1 = (pre + k.tiles - 1) / per;
-      a.parts[q] = make_int2(c0, c1 - c0 + 1);
-      for (int c = (pre + per - 1) / per; c <= c1; ++c) {  // the runs that begin in this query
-        reinterpret_cast<int4*>(a.runs + c)[0] = make_int4(c * per, min(total, c * per + per), pre, 0);
-        store_query(&a.runs[c].k, k);
-      }
-    } else {
-      a.parts[q] = make_int2(0, 0);
-    }
-    pre += k.tiles;
-  }
-  for (int c = (total + per - 1) / per + tid; c < kPagedBlocks; c += kPlanThreads)
-    reinterpret_cast<int4*>(a.runs + c)[0] = make_int4(0, 0, 0, 0);
-}
-
-// Row of the split queries' tile: a 32-row quarter holds 16 heads' hi parts, then their lo parts.
-__device__ __forceinline__ void split_query_row(const PagedArgs& a, int row) {
-  const int lane = threadIdx.x & 31, q = row >> 6, h = row & 63;
-  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (size_t)row * 512) + 2 * lane;
-  const uint4 v[2] = {src[0], src[1]};
-  const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-  // the largest magnitude by its bits: bf16 pairs compared as unsigned halves
-  uint32_t mx = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) mx = __vmaxu2(mx, w[e] & 0x7fff7fffu);
-  mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
-  // 2^-e with e = exponent - 7: values below 2^8, exact products; a row of denormals, or zeros, stays small; a row that
-  // holds an infinity or a NaN becomes NaN by its product with 0
-  const int be = max((int)(mx >> 7), 8);
-  const float inv = be == 255 ? 0.f : __uint_as_float((uint32_t)(261 - be) << 23);
-  uint32_t hi[4], lo[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float x0 = __uint_as_float(w[2 * e] << 16) * inv, x1 = __uint_as_float(w[2 * e] & 0xffff0000u) * inv;
-    const float x2 = __uint_as_float(w[2 * e + 1] << 16) * inv, x3 = __uint_as_float(w[2 * e + 1] & 0xffff0000u) * inv;
-    hi[e] = e4m3x4(x0, x1, x2, x3);
-    const float2 b0 = e4m3x2_f(hi[e]), b1 = e4m3x2_f(hi[e] >> 16);
-    lo[e] = e4m3x4((x0 - b0.x) * 16.f, (x1 - b0.y) * 16.f, (x2 - b1.x) * 16.f, (x3 - b1.y) * 16.f);
-  }
-  uint4* dst = reinterpret_cast<uint4*>(a.q8) + ((size_t)q * 32 + lane) * 128 + 32 * (h >> 4) + (h & 15);
-  dst[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-  dst[16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-  // what a product of the parts stands for: 2^e, and the softmax scale with it
-  if (lane == 0) a.q8_scale[row] = be == 255 ? NAN : __uint_as_float((uint32_t)(be - 7) << 23) * a.scale2;
-}
-
-__global__ void __launch_bounds__(kPlanThreads) k_plan_pages(const __grid_constant__ PagedArgs a) {
-  pdl_trigger();  // (the attention kernel alone follows, and waits)
-  __shared__ int sm[kPlanThreads / 32];
-  pdl_wait();
-  if (blockIdx.x == gridDim.x - 1) {
-    make_plan(a, sm);
-    return;
-  }
-  const int row = blockIdx.x * (kPlanThreads / 32) + (threadIdx.x >> 5);
-  if (row < a.B * a.T * 64) split_query_row(a, row);
-}
 
 // ---------------------------------------------------------------- the portable kernel
 constexpr int kSimtTile = 32;   // keys a tile: a lane each
@@ -177,21 +25,21 @@ template <typename T>
 __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __grid_constant__ PagedArgs a) {
   pdl_trigger();  // (the merge alone follows, and waits)
   extern __shared__ __align__(16) float sm_pa[];
-  __shared__ int s_row[kSimtTile];
+  __shared__ int s_row[kSimtTile], s_sums[kSimtWarps];
+  __shared__ PagedRun s_run;
   const int D = a.D, KS = D + kSimtPad, n8 = D >> 3;
   float* ks = sm_pa;                    // [kSimtTile][KS] keys
   float* qs = sm_pa + kSimtTile * KS;   // [kSimtWarps][D] queries of this group of heads
   pdl_wait();
-  const PagedRun* run = a.runs + blockIdx.x;
-  const int4 r4 = *reinterpret_cast<const int4*>(run);
-  const int t0 = r4.x, t1 = r4.y;
-  int pre = r4.z;
+  paged_plan(a, &s_run, s_sums);
+  const int t0 = s_run.t0, t1 = s_run.t1;
   if (t0 >= t1) return;
-  PagedQuery k = load_query(&run->k);
+  int pre = s_run.pre;
+  PagedQuery k = s_run.k;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 #pragma unroll 1
   while (true) {
-    const int q = k.q, b = q / a.T;
+    const int q = k.q, b = k.b;
     const int begin = max(t0 - pre, 0), end = min(t1 - pre, k.tiles), nkeys = k.n0 + k.f + k.nw;
     const bool whole = begin == 0 && end == k.tiles;
     const int slot = 2 * blockIdx.x + (begin == 0 ? 1 : 0);
@@ -220,10 +68,10 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
           int r = -1;
           if (x < k.n0) {
             const int j = a.sel ? __ldg(a.sel + (size_t)q * a.topk + x) : x;
-            if (!a.sel || (j >= 0 && j < k.n_rows)) r = paged_row(a.row_table, a.row_pages, b, j, a.P, a.n_pages);
+            if (!a.sel || (j >= 0 && j < k.n_rows)) r = paged_row(a, a.row_table + (size_t)b * a.row_pages, j);
           } else if (x < nkeys) {
             const int y = x - k.n0;
-            r = paged_row(a.token_table, a.token_pages, b, y < k.f ? y : k.w0 + (y - k.f), a.P, a.n_pages);
+            r = paged_row(a, a.token_table + (size_t)b * a.token_pages, y < k.f ? y : k.w0 + (y - k.f));
           }
           if (r < 0 && x < nkeys) atomicOr(a.err, CSA_DEV_RANGE);
           s_row[tid] = r;
@@ -313,47 +161,62 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
     }
     pre += k.tiles;
     if (pre >= t1) return;
-    k = load_query(a.queries + q + 1);
+    k = next_query(a, q);
   }
 }
 
 // ---------------------------------------------------------------- merge of split queries
 // With (m_s, l_s, acc_s) of the parts: M = max(z, m_s), Z = 2^{z - M} + sum_s l_s 2^{m_s - M},
-// o = sum_s acc_s 2^{m_s - M} / Z (z the sink in powers of two).  A block of eight warps takes one head of a query (few
+// o = sum_s acc_s 2^{m_s - M} / Z (z the sink in powers of two).  A block of eight warps takes one head of a query (up to 8
 // queries: each has many parts) or eight; a head's warps take its parts in turn.  The weights are found first, from all
-// parts' statistics at once, so that the sum over the accumulators is loads and products only, eight in flight.
-constexpr int kMergeC = 8;       // 4-value columns a lane holds, 128 values apart: D <= 1024
+// parts' statistics at once, so that the sum over the accumulators is loads and products only, several parts in flight;
+// the angles of the rotation are found meanwhile, once a block.
 constexpr int kMergeWarps = 8;
 
-template <typename T, int kC>
-__global__ void __launch_bounds__(32 * kMergeWarps) k_merge_pages(const __grid_constant__ PagedArgs a, int heads) {
+// kC: 4-value columns a lane holds, 128 values apart; kAhead: parts in flight
+template <typename T, int kC, int kAhead, bool kOneHead>
+__global__ void __launch_bounds__(32 * kMergeWarps) k_merge_pages(const __grid_constant__ PagedArgs a) {
   // no early trigger: what follows finds the outputs written
-  extern __shared__ __align__(16) float sm_merge[];  // [kMergeWarps][kPagedBlocks] weights; heads == 1: [kMergeWarps][D] sums
+  extern __shared__ __align__(16) float sm_merge[];  // [kMergeWarps][kPagedBlocks] weights; [R / 2] angles; sums
   pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n4 = a.D >> 2;
-  const int hh = heads == 1 ? 0 : warp, h = blockIdx.y * heads + hh;
-  const int first = heads == 1 ? warp : 0, step = heads == 1 ? kMergeWarps : 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n4 = a.D >> 2;
+  const int h = kOneHead ? blockIdx.y : blockIdx.y * kMergeWarps + warp;
+  const int first = kOneHead ? warp : 0, step = kOneHead ? kMergeWarps : 1;
   float* wt = sm_merge + warp * kPagedBlocks;  // (a query has at most a part in every block)
-  float4* sums = reinterpret_cast<float4*>(sm_merge + kMergeWarps * kPagedBlocks);
+  float2* cs = reinterpret_cast<float2*>(sm_merge + kMergeWarps * kPagedBlocks);
+  float4* sums = reinterpret_cast<float4*>(sm_merge + kMergeWarps * kPagedBlocks + a.R);  // kOneHead: [kMergeWarps][D]
+  const bool on = h < a.H;
 #pragma unroll 1
   for (int q = blockIdx.x; q < a.B * a.T; q += gridDim.x) {
     const int2 at = a.parts[q];
     if (at.y <= 1) continue;
-    const bool on = h < a.H;
+    __syncthreads();  // (the query before has been read)
+    if (a.inv_freq) {
+      const int p = a.pos[q / a.T] + q % a.T;
+      for (int i = tid; i < a.R / 2; i += 32 * kMergeWarps) rope_cs(p, a.inv_freq, i, &cs[i].x, &cs[i].y);
+    }
+    auto slot = [&](int s) { return (size_t)(2 * (at.x + s) + (s == 0)); };
     float inv = 0.f;
-    if (heads == 1) __syncthreads();  // (the query before has been read)
     if (on) {
-      // every warp of a head finds all weights
       const float z2 = a.sink ? a.sink[h] * 1.4426950408889634f : -INFINITY;
+      constexpr int kL = (kPagedBlocks + 31) / 32;
+      float2 ml[kL];
       float M = z2;
-      for (int s = lane; s < at.y; s += 32) M = fmaxf(M, a.ml[(size_t)(2 * (at.x + s) + (s == 0)) * a.H + h].x);
+#pragma unroll
+      for (int i = 0; i < kL; ++i) {
+        const int s = lane + 32 * i;
+        ml[i] = s < at.y ? a.ml[slot(s) * a.H + h] : make_float2(-INFINITY, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < kL; ++i) M = fmaxf(M, ml[i].x);
       M = warp_max(M);
       float Z = 0.f;
-      for (int s = lane; s < at.y; s += 32) {
-        const float2 ml = a.ml[(size_t)(2 * (at.x + s) + (s == 0)) * a.H + h];
-        const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);  // (a part without keys)
-        wt[s] = f;
-        Z = fmaf(ml.y, f, Z);
+#pragma unroll
+      for (int i = 0; i < kL; ++i) {
+        const int s = lane + 32 * i;
+        const float f = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - M);  // (a part without keys)
+        if (s < at.y) wt[s] = f;
+        Z = fmaf(ml[i].y, f, Z);
       }
       Z = warp_sum(Z) + (z2 == -INFINITY ? 0.f : exp2f(z2 - M));
       inv = Z == 0.f ? 0.f : 1.f / Z;
@@ -363,7 +226,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) k_merge_pages(const __grid_c
 #pragma unroll
     for (int c = 0; c < kC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (on) {
-      constexpr int kAhead = kC <= 4 ? 4 : 2;
+#pragma unroll 1
       for (int s0 = first; s0 < at.y; s0 += kAhead * step) {
         float4 x[kAhead][kC];
         float f[kAhead];
@@ -371,12 +234,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) k_merge_pages(const __grid_c
         for (int g = 0; g < kAhead; ++g) {
           const int s = min(s0 + g * step, at.y - 1);
           f[g] = s0 + g * step < at.y ? wt[s] : 0.f;
-          const float* src = a.part + (size_t)(2 * (at.x + s) + (s == 0)) * a.H * a.D;
+          const float* src = a.part + slot(s) * a.H * a.D;
 #pragma unroll
           for (int c = 0; c < kC; ++c) {
-            const int d = 4 * (lane + 32 * c), blk = a.cols == 128 ? c : 0;
+            const int d = 4 * (lane + 32 * c), blk = a.cols == a.D ? 0 : d >> 5;  // (blocks of 32 dims, or all)
             if (lane + 32 * c < n4)
-              x[g][c] = __ldcg(reinterpret_cast<const float4*>(src + ((size_t)blk * a.H + h) * a.cols + (d - blk * 128)));
+              x[g][c] = __ldcg(reinterpret_cast<const float4*>(src + ((size_t)blk * a.H + h) * a.cols + (d - blk * 32)));
           }
         }
 #pragma unroll
@@ -393,83 +256,86 @@ __global__ void __launch_bounds__(32 * kMergeWarps) k_merge_pages(const __grid_c
           }
         }
       }
-    }
-    if (heads == 1) {
+      if (kOneHead) {
 #pragma unroll
-      for (int c = 0; c < kC; ++c)
-        if (lane + 32 * c < n4) sums[warp * n4 + lane + 32 * c] = acc[c];
-      __syncthreads();
-    }
-    if (!on) continue;
-    const int p = a.pos[q / a.T] + q % a.T;
-    // a head's columns: by its warp from registers, or over the block's warps from their sums
-    for (int c = 0; c < kC; ++c) {
-      const int col = heads == 1 ? (int)threadIdx.x + 256 * c : lane + 32 * c;
-      if (col >= n4) break;
-      float4 v4;
-      if (heads == 1) {
-        v4 = sums[col];
-        for (int w = 1; w < kMergeWarps; ++w) {
-          const float4 x = sums[w * n4 + col];
-          v4.x += x.x; v4.y += x.y; v4.z += x.z; v4.w += x.w;
-        }
-      } else {
-        v4 = acc[0];
-#pragma unroll
-        for (int e = 1; e < kC; ++e)
-          if (e == c) v4 = acc[e];
+        for (int c = 0; c < kC; ++c)
+          if (lane + 32 * c < n4) sums[warp * n4 + lane + 32 * c] = acc[c];
       }
+    }
+    __syncthreads();  // (the sums, the angles)
+    if (!on) continue;
+    auto write = [&](int col, float4 v4) {
       const int d = 4 * col;
       float v[4] = {v4.x * inv, v4.y * inv, v4.z * inv, v4.w * inv};
       if (a.inv_freq && d >= a.D - a.R) {
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
-          float cs, sn;
-          rope_cs(p, a.inv_freq, (d + e - (a.D - a.R)) >> 1, &cs, &sn);
+          const float2 t = cs[(d + e - (a.D - a.R)) >> 1];
           const float x0 = v[e], x1 = v[e + 1];
-          v[e] = fmaf(x0, cs, x1 * sn);
-          v[e + 1] = fmaf(-x0, sn, x1 * cs);
+          v[e] = fmaf(x0, t.x, x1 * t.y);
+          v[e + 1] = fmaf(-x0, t.y, x1 * t.x);
         }
       }
       T* o = static_cast<T*>(a.out) + ((size_t)q * a.H + h) * a.D + d;
+      if constexpr (sizeof(T) == 2) {
+        uint2 u;
+        reinterpret_cast<__nv_bfloat162*>(&u)[0] = __floats2bfloat162_rn(v[0], v[1]);
+        reinterpret_cast<__nv_bfloat162*>(&u)[1] = __floats2bfloat162_rn(v[2], v[3]);
+        *reinterpret_cast<uint2*>(o) = u;
+      } else {
+        *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+      }
+    };
+    if (kOneHead) {  // the head's columns over all threads
+      for (int col = tid; col < n4; col += 32 * kMergeWarps) {
+        float4 v4 = sums[col];
+        for (int w = 1; w < kMergeWarps; ++w) {
+          const float4 x = sums[w * n4 + col];
+          v4.x += x.x; v4.y += x.y; v4.z += x.z; v4.w += x.w;
+        }
+        write(col, v4);
+      }
+    } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = from_f<T>(v[e]);
+      for (int c = 0; c < kC; ++c)
+        if (lane + 32 * c < n4) write(lane + 32 * c, acc[c]);
     }
   }
 }
 
 template <typename T, int kC>
 cudaError_t merge_c(const PagedArgs& a, cudaStream_t s) {
-  const int Q = a.B * a.T;
-  const int heads = Q <= 8 ? 1 : kMergeWarps;
-  const int smem = (kMergeWarps * kPagedBlocks + (heads == 1 ? kMergeWarps * a.D : 0)) * 4;
-  CSA_LAUNCH((k_merge_pages<T, kC>), dim3(min(Q, 4 * kPagedBlocks), (a.H + heads - 1) / heads), dim3(32 * kMergeWarps),
-             smem, s, a, heads);
+  const int Q = a.B * a.T, smem = (kMergeWarps * kPagedBlocks + a.R) * 4;
+  if (Q <= 8) {
+    constexpr int kSmem = (kMergeWarps * kPagedBlocks + 1024 + kMergeWarps * 1024) * 4;
+    static_assert(kSmem <= 48 * 1024, "the sums fit what every kernel may take");
+    CSA_LAUNCH((k_merge_pages<T, kC, kC <= 4 ? 4 : 2, true>), dim3(Q, a.H), dim3(32 * kMergeWarps),
+               smem + kMergeWarps * a.D * 4, s, a);
+  } else {
+    CSA_LAUNCH((k_merge_pages<T, kC, 2, false>), dim3(min(Q, 4 * kPagedBlocks), (a.H + kMergeWarps - 1) / kMergeWarps),
+               dim3(32 * kMergeWarps), smem, s, a);
+  }
   return cudaGetLastError();
 }
 template <typename T>
 cudaError_t launch_merge(const PagedArgs& a, cudaStream_t s) {
-  return a.D <= 128 ? merge_c<T, 1>(a, s) : a.D <= 512 ? merge_c<T, 4>(a, s) : merge_c<T, kMergeC>(a, s);
+  return a.D <= 128 ? merge_c<T, 1>(a, s) : a.D <= 512 ? merge_c<T, 4>(a, s) : merge_c<T, 8>(a, s);
 }
 
 template <typename T>
 cudaError_t attend_t(const Dims& L, PagedArgs a, cudaStream_t s) {
-  const int Q = a.B * a.T;
+  a.min_tiles = 2;
   if (tc_paged_supported(L, a.P)) {
     a.tile = 64;
     a.shift = 3;  // the largest power of two that divides a page, at most a tile
     while (a.shift < 6 && a.P % (2 << a.shift) == 0) ++a.shift;
-    a.min_tiles = 2;
-    a.cols = 128;
-    CSA_LAUNCH(k_plan_pages, dim3(Q * 64 / (kPlanThreads / 32) + 1), dim3(kPlanThreads), 0, s, a);
+    a.cols = 32;
     const cudaError_t e = launch_tc_paged(a, s);
     if (e != cudaSuccess) return e;
   } else {
     a.tile = kSimtTile;
     a.shift = 0;
-    a.min_tiles = 2;
     a.cols = a.D;
-    CSA_LAUNCH(k_plan_pages, dim3(1), dim3(kPlanThreads), 0, s, a);
     allow_smem<kSimtSmemMax>(k_attend_pages_simt<T>);
     CSA_LAUNCH(k_attend_pages_simt<T>, dim3(kPagedBlocks), dim3(32 * kSimtWarps), simt_smem(a.D), s, a);
   }
@@ -479,15 +345,9 @@ cudaError_t attend_t(const Dims& L, PagedArgs a, cudaStream_t s) {
 }  // namespace
 
 void carve_paged(Carver& c, const Dims& L, int Q, PagedArgs* a) {
-  a->runs = c.take<PagedRun>(kPagedBlocks);
-  a->queries = c.take<PagedQuery>(Q);
   a->parts = c.take<int2>(Q);
   a->ml = c.take<float2>((size_t)2 * kPagedBlocks * L.H);
   a->part = c.take<float>((size_t)2 * kPagedBlocks * L.H * L.D);
-  if (tc_paged_supported(L, 8)) {
-    a->q8 = c.take<uint8_t>((size_t)Q * 64 * 1024);
-    a->q8_scale = c.take<float>((size_t)Q * 64);
-  }
 }
 
 cudaError_t launch_attend_pages(const Dims& L, PagedArgs a, cudaStream_t s) {

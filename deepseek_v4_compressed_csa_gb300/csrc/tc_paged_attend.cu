@@ -9,7 +9,7 @@
 // 8-bit parts:
 //   q = 2^e (hi + lo / 16), E4M3 both: the 8 bits of a bf16 value, exact but for values 2^-14 below the head's largest.
 //     The parts are two rows of one operand, M = 128 = 64 heads x 2, kept in tensor memory (its 128 columns are an A
-//     operand that no product reads from shared memory); k_plan_pages splits them;
+//     operand that no product reads from shared memory);
 //   P = hi + lo, E5M2 and E4M3, both added to the same accumulator: 7 bits (at most 2^-7 of a probability, about 2^-9.5 on
 //     average, signs mixed), 3 bits down to 2^-21 of the largest and something down to 2^-24.  (Two E4M3 parts keep 8 bits
 //     but drop everything below 2^-16 of the largest: beside one dominant key, what 64 thousand others add up to.)
@@ -55,11 +55,13 @@ constexpr int kOffFac = kOffMask + kStages * 8 + 16;      // [2][64] factors of 
 constexpr int kOffRef = kOffFac + 2 * kH * 4;             // [64] R
 constexpr int kOffStat = kOffRef + kH * 4;                // [2][64] float2 (m, l) of the groups
 constexpr int kOffOut = kOffStat + 2 * kH * 8;            // [64] factors of the output
-constexpr int kOffRope = kOffOut + kH * 4;                // cos[32], sin[32]
+constexpr int kOffMax = kOffOut + kH * 4;                 // [2][64] largest magnitudes of the query rows' halves
+constexpr int kOffRope = kOffMax + 2 * kH * 4;            // cos[32], sin[32]
 constexpr int kOffBars = kOffRope + 64 * 4;
 constexpr int kOffTmem = kOffBars + 32 * 8;
-constexpr int kSmem = kOffTmem + 32 + 1024;
-static_assert(kOffBars % 8 == 0 && kOffFac % 16 == 0 && kOffOut % 16 == 0 && kSmem <= 232448, "shared memory");
+constexpr int kOffPlan = kOffTmem + 32;                   // PagedRun, [warps] sums
+constexpr int kSmem = kOffPlan + (int)sizeof(PagedRun) + 4 * kThreads / 32 + 1024;
+static_assert(kOffBars % 8 == 0 && kOffFac % 16 == 0 && kOffOut % 16 == 0 && kOffPlan % 8 == 0 && kSmem <= 232448, "shared memory");
 
 // 2^x by the hardware approximation (relative error ~2^-22; results below 2^-126 flush to zero)
 __device__ __forceinline__ float ex2(float x) {
@@ -107,7 +109,7 @@ __device__ __forceinline__ Run run_of(const PagedQuery& k, const TileCut& c, int
 
 struct Smem {
   uint8_t* base;
-  uint64_t *full, *empty, *s_full, *p_full, *pv_done, *decided, *q_ready, *drain;
+  uint64_t *full, *empty, *s_full, *s_free, *p_full, *pv_done, *decided, *q_ready, *drain;
   volatile int* dead;
 };
 
@@ -125,8 +127,7 @@ __device__ __forceinline__ bool warp_wait(const Smem& sm, uint64_t* bar, uint32_
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    k_tc_attend_pages(const __grid_constant__ CUtensorMap tm_runs, const __grid_constant__ CUtensorMap tm_rows,
-                      const __grid_constant__ PagedArgs a) {
+    k_tc_attend_pages(const __grid_constant__ CUtensorMap tm_runs, const __grid_constant__ PagedArgs a) {
   pdl_trigger();  // (the merge alone follows, and waits)
   extern __shared__ uint8_t smem_raw[];
   Smem sm;
@@ -135,27 +136,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   sm.full = bars;
   sm.empty = bars + kStages;
   sm.s_full = bars + 2 * kStages;
-  sm.p_full = sm.s_full + 2;
+  sm.s_free = sm.s_full + 2;
+  sm.p_full = sm.s_free + 2;
   sm.pv_done = sm.p_full + 2;
   sm.decided = sm.pv_done + 2;
   sm.q_ready = sm.decided + 2;
   sm.drain = sm.q_ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm.base + kOffTmem);
   sm.dead = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* issued = sm.dead + 1;  // tiles whose copies loader 0 has issued
+  volatile int* issued = sm.dead + 1;  // a loader's last tile whose copies it has issued, + 1
   float* scales = reinterpret_cast<float*>(sm.base + kOffScale);
   volatile uint64_t* masks = reinterpret_cast<volatile uint64_t*>(sm.base + kOffMask);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     tc::tma_prefetch(&tm_runs);
-    tc::tma_prefetch(&tm_rows);
     for (int i = 0; i < kStages; ++i) {
-      tc::mbar_init(sm.full + i, kLoaders + 32);  // every loader's copy, and loader 0's lanes for the scales
+      tc::mbar_init(sm.full + i, 1 + 32);  // the copies, and the loader's lanes for the scales (or all they copy)
       tc::mbar_init(sm.empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(sm.s_full + i, 1);
+      tc::mbar_init(sm.s_free + i, kGroup);
       tc::mbar_init(sm.p_full + i, kGroup);
       tc::mbar_init(sm.pv_done + i, 1);
       tc::mbar_init(sm.decided + i, kGroup);
@@ -163,15 +165,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(sm.q_ready, kSoft);
     tc::mbar_init(sm.drain, 1);
     *sm.dead = 0;
-    *issued = 0;
+    for (int i = 0; i < kLoaders; ++i) issued[i] = 0;
     tc::fence_mbar_init();
   }
   pdl_wait();  // predecessors complete: what they wrote is visible and their tensor memory is free
-  const PagedRun* run = a.runs + blockIdx.x;
-  const int4 r4 = __ldg(reinterpret_cast<const int4*>(run));
-  const int t0 = r4.x, t1 = r4.y, pre0 = r4.z;
+  PagedRun* plan = reinterpret_cast<PagedRun*>(sm.base + kOffPlan);
+  paged_plan(a, plan, reinterpret_cast<int*>(plan + 1));
+  const int t0 = plan->t0, t1 = plan->t1;
   if (t0 >= t1) return;  // (all of the block)
-  const PagedQuery k0 = load_query(&run->k);
+  const int pre0 = plan->pre;
+  const PagedQuery k0 = plan->k;
   if (warp == kMmaWarp) {
     tc::tmem_alloc(tmem_slot, kCols);
     tc::tmem_relinquish();
@@ -182,127 +185,129 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp < kLoaders) {
-    // ------------------------------------------------------------ loaders: a tile's copies, 128 dims of some rows each,
-    // are dealt out to their lanes
-    int pre = pre0, j = 0;  // j: tiles of this block so far
-    const int shift = a.shift, per = kTile >> shift;
+    // ------------------------------------------------------------ loaders: warp w takes the tiles j with j % 3 == w
+    // Dense runs come by one copy each 128 dims; selected rows by a warp's 512-byte cp.async each (tile::gather4 takes a
+    // warp some 75 clocks per 512 bytes: 4.8K a tile, against 1K), which are waited for before the warp's next tile.
+    int pre = pre0, j = 0;  // j: tiles of this block before the query
+    const int shift = a.shift, per = kTile >> shift, copies = 4 * per;
     PagedQuery k = k0;
     bool ok = true;
+    int pending = -1;  // stage of selected rows on their way
+    auto landed = [&] {
+      if (pending < 0) return;
+      tc::cp_async_wait_all();
+      tc::fence_proxy_async_smem();
+      tc::mbar_arrive(sm.full + pending);
+      if (lane == 0) tc::mbar_arrive(sm.full + pending);  // (in place of the copies' own arrival)
+      pending = -1;
+    };
 #pragma unroll 1
     while (true) {
       const TileCut cut = cut_tiles(a.sel != nullptr, k, kTile, shift);
-      const int begin = max(t0 - pre, 0), end = min(t1 - pre, k.tiles), b = k.q / a.T;
+      const int begin = max(t0 - pre, 0), end = min(t1 - pre, k.tiles);
       const int32_t* sel = a.sel + (size_t)k.q * a.topk;
-      const int32_t* rows_b = a.row_table + (size_t)b * a.row_pages;
-      const int32_t* tokens_b = a.token_table + (size_t)b * a.token_pages;
-      // The lookups run ahead: a tile's selected rows two tiles before its copies are issued, its pages one before.
-      // keys lane and lane + 32 of tile t: their selected rows (-1 behind the last; -2 out of range)
-      auto selected = [&](int t, int e) -> int {
+      const int32_t* rows_b = a.row_table + (size_t)k.b * a.row_pages;
+      const int32_t* tokens_b = a.token_table + (size_t)k.b * a.token_pages;
+      // The lookups run ahead: a tile's selected rows two of the warp's tiles before its copies are issued, its pages one
+      // before.  Each is loaded into the registers of the tile's before, dead by then: a move would wait for the load.
+      auto selected = [&](int t, int e) -> int {  // key lane + 32 e of tile t: its row, -1 behind the last
         const int x = t * kTile + lane + 32 * e;
-        if (t >= end || x >= k.n0) return -1;
-        const int row = (int)tc::ld_nc_u32_now(sel + x);
-        return row;
+        return t < end && t < cut.sel_tiles && x < k.n0 ? (int)tc::ld_nc_u32_now(sel + x) : -1;
       };
       // a tile's pages as the table has them: selected, of both keys; dense, of the lane's run
       auto pages_of = [&](int t, int j0, int j1, int& p0, int& p1) {
         p0 = p1 = -1;
         if (t >= end) return;
         if (t < cut.sel_tiles) {
-          if (j0 >= 0 && j0 < k.n_rows) p0 = (int)tc::ld_nc_u32_now(rows_b + j0 / a.P);
-          if (j1 >= 0 && j1 < k.n_rows) p1 = (int)tc::ld_nc_u32_now(rows_b + j1 / a.P);
+          if ((unsigned)j0 < (unsigned)k.n_rows) p0 = (int)tc::ld_nc_u32_now(rows_b + page_of(a, j0));
+          if ((unsigned)j1 < (unsigned)k.n_rows) p1 = (int)tc::ld_nc_u32_now(rows_b + page_of(a, j1));
         } else if (lane < per) {
           const Run r = run_of(k, cut, (t - cut.sel_tiles) * per + lane, shift);
-          if (r.hi > r.lo) p0 = (int)tc::ld_nc_u32_now((r.rows ? rows_b : tokens_b) + r.start / a.P);
+          if (r.hi > r.lo) p0 = (int)tc::ld_nc_u32_now((r.rows ? rows_b : tokens_b) + page_of(a, r.start));
         }
       };
-      int j0 = -1, j1 = -1, n0 = -1, n1 = -1, p0, p1;
-      if (begin < cut.sel_tiles) {
-        j0 = selected(begin, 0);
-        j1 = selected(begin, 1);
-        if (begin + 1 < cut.sel_tiles) {
-          n0 = selected(begin + 1, 0);
-          n1 = selected(begin + 1, 1);
-        }
-      }
-      pages_of(begin, j0, j1, p0, p1);
+      int t = begin + (warp + kLoaders - j % kLoaders) % kLoaders;
+      int j0 = selected(t, 0), j1 = selected(t, 1), n0 = selected(t + kLoaders, 0), n1 = selected(t + kLoaders, 1), p0, p1;
+      pages_of(t, j0, j1, p0, p1);
 #pragma unroll 1
-      for (int t = begin; t < end; ++t, ++j) {
-        const int st = j % kStages;
-        int q0, q1, f0 = -1, f1 = -1;
-        if (t + 2 < cut.sel_tiles) {
-          f0 = selected(t + 2, 0);
-          f1 = selected(t + 2, 1);
-        }
-        pages_of(t + 1, n0, n1, q0, q1);
+      for (; t < end; t += kLoaders) {
+        const int jt = j + t - begin, st = jt % kStages;
+        const bool is_sel = t < cut.sel_tiles;
         int r0, r1;        // physical rows of keys lane and lane + 32, -1 for none
         int run_row = -1;  // dense: the first physical row of the lane's run, -1 for none
-        const bool is_sel = t < cut.sel_tiles;
         if (is_sel) {
           const int x = t * kTile + lane;
-          r0 = (unsigned)p0 < (unsigned)a.n_pages ? p0 * a.P + j0 % a.P : -1;
-          r1 = (unsigned)p1 < (unsigned)a.n_pages ? p1 * a.P + j1 % a.P : -1;
+          r0 = (unsigned)p0 < (unsigned)a.n_pages ? p0 * a.P + (j0 - page_of(a, j0) * a.P) : -1;
+          r1 = (unsigned)p1 < (unsigned)a.n_pages ? p1 * a.P + (j1 - page_of(a, j1) * a.P) : -1;
           if ((x < k.n0 && r0 < 0) || (x + 32 < k.n0 && r1 < 0)) atomicOr(a.err, CSA_DEV_RANGE);
         } else {
-          Run r{};
-          if (lane < per) r = run_of(k, cut, (t - cut.sel_tiles) * per + lane, shift);
-          if (r.hi > r.lo) {
-            if ((unsigned)p0 < (unsigned)a.n_pages) run_row = p0 * a.P + r.start % a.P;
-            else atomicOr(a.err, CSA_DEV_RANGE);
+          int span = 0;  // the run's rows [lo, hi) that count, 8 bits each
+          if (lane < per) {
+            const Run r = run_of(k, cut, (t - cut.sel_tiles) * per + lane, shift);
+            if (r.hi > r.lo) {
+              if ((unsigned)p0 < (unsigned)a.n_pages) {
+                run_row = p0 * a.P + (r.start - page_of(a, r.start) * a.P);
+                span = max(r.lo - r.start, 0) | min(r.hi - r.start, kTile) << 8;
+              } else {
+                atomicOr(a.err, CSA_DEV_RANGE);
+              }
+            }
           }
           int rr[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int key = lane + 32 * e, from = key >> shift, off = key & ((1 << shift) - 1);
-            const int row = __shfl_sync(0xffffffffu, run_row, from), start = __shfl_sync(0xffffffffu, r.start, from);
-            const int lo = __shfl_sync(0xffffffffu, r.lo, from), hi = __shfl_sync(0xffffffffu, r.hi, from);
-            rr[e] = row >= 0 && start + off >= lo && start + off < hi ? row + off : -1;
+            const int row = __shfl_sync(0xffffffffu, run_row, from), sp = __shfl_sync(0xffffffffu, span, from);
+            rr[e] = off >= (sp & 255) && off < sp >> 8 ? row + off : -1;
           }
           r0 = rr[0];
           r1 = rr[1];
         }
-        ok = warp_wait(sm, sm.empty + st, ((j / kStages) & 1) ^ 1);
+        j0 = n0;
+        j1 = n1;
+        pages_of(t + kLoaders, j0, j1, p0, p1);
+        n0 = selected(t + 2 * kLoaders, 0);
+        n1 = selected(t + 2 * kLoaders, 1);
+        landed();
+        ok = warp_wait(sm, sm.empty + st, ((jt / kStages) & 1) ^ 1);
         if (!ok) break;
-        if (warp == 0) {
-          const uint32_t on0 = __ballot_sync(0xffffffffu, r0 >= 0), on1 = __ballot_sync(0xffffffffu, r1 >= 0);
-          const uint32_t dst = tc::smem_u32(scales + st * kTile + lane);
-          tc::cp_async4(dst, a.scales + max(r0, 0), r0 >= 0 ? 4u : 0u);
-          tc::cp_async4(dst + 128, a.scales + max(r1, 0), r1 >= 0 ? 4u : 0u);
-          if (lane == 0) {
-            masks[st] = (uint64_t)on1 << 32 | on0;
-            *issued = j + 1;
-          }
-          __syncwarp();
-          tc::cp_async_arrive(sm.full + st);
+        const uint32_t on0 = __ballot_sync(0xffffffffu, r0 >= 0), on1 = __ballot_sync(0xffffffffu, r1 >= 0);
+        const uint32_t sdst = tc::smem_u32(scales + st * kTile + lane);
+        if (lane == 0) {
+          masks[st] = (uint64_t)on1 << 32 | on0;
+          issued[warp] = jt + 1;
         }
-        // copy x: rows 4 (x / 4) .. + 3 (gathered) or run x / 4, dims 128 (x % 4) ..; loader w has x = w, w + 3, ..
-        const int copies = is_sel ? 64 : 4 * per, mine = (copies - warp + kLoaders - 1) / kLoaders;
-        if (lane == 0) tc::mbar_arrive_expect_tx(sm.full + st, mine * (kStage / copies));
         __syncwarp();
-        const int x = kLoaders * lane + warp, part = min(x >> 2, 15), c = x & 3;
-        uint8_t* dst = sm.base + st * kStage + c * kBox;
-        if (is_sel) {
-          // (an empty row is row 0 of the pool, cleared before the product that its values would enter)
-          int g[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = 4 * part + e;
-            const int x0 = __shfl_sync(0xffffffffu, r0, key & 31), x1 = __shfl_sync(0xffffffffu, r1, key & 31);
-            g[e] = max(key < 32 ? x0 : x1, 0);
-          }
-          if (x < copies) tc::tma_gather4(dst + part * 512, &tm_rows, sm.full + st, c * 128, g[0], g[1], g[2], g[3]);
-        } else {
-          const int row = __shfl_sync(0xffffffffu, run_row, part & 31);
-          // (a run in no page: rows behind the pool's end, which the copy fills with zeros)
-          if (x < copies)
-            tc::tma_load_2d(dst + (part << shift) * 128, &tm_runs, sm.full + st, c * 128, row >= 0 ? row : a.n_pages * a.P);
+        if (!is_sel) {
+          // copy x: run x / 4, dims 128 (x % 4) ..; a run in no page: rows behind the pool's end, which come as zeros
+          if (lane == 0) tc::mbar_arrive_expect_tx(sm.full + st, kStage);
+          __syncwarp();
+          const int part = min(lane >> 2, per - 1), row = __shfl_sync(0xffffffffu, run_row, part);
+          if (lane < copies)
+            tc::tma_load_2d(sm.base + st * kStage + (lane & 3) * kBox + (part << shift) * 128, &tm_runs, sm.full + st,
+                            (lane & 3) * 128, row >= 0 ? row : a.n_pages * a.P);
         }
-        j0 = n0; j1 = n1; n0 = f0; n1 = f1; p0 = q0; p1 = q1;
+        tc::cp_async4(sdst, a.scales + max(r0, 0), r0 >= 0 ? 4u : 0u);
+        tc::cp_async4(sdst + 128, a.scales + max(r1, 0), r1 >= 0 ? 4u : 0u);
+        if (!is_sel) {
+          tc::cp_async_arrive(sm.full + st);
+        } else {
+          const uint32_t dst = tc::smem_u32(sm.base + st * kStage) + (lane >> 3) * kBox;
+          const uint8_t* src = a.codes + lane * 16;
+#pragma unroll 8
+          for (int r = 0; r < kTile; ++r) {
+            const int row = __shfl_sync(0xffffffffu, r < 32 ? r0 : r1, r & 31);
+            tc::cp_async16(dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4), src + (size_t)max(row, 0) * kD, row >= 0 ? 16u : 0u);
+          }
+          pending = st;
+        }
       }
+      j += end - begin;
       pre += k.tiles;
       if (!ok || pre >= t1) break;
-      do k = load_query(a.queries + k.q + 1);
-      while (k.tiles == 0);
+      k = next_query(a, k.q);
     }
+    landed();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
     constexpr uint32_t id_qk = tc::idesc_e4m3(128, kTile);
@@ -330,34 +335,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       return true;
     };
+    // S of tile jt, whose buffer's last scores the softmax warps have read
+    auto qk = [&](int jt) {
+      if (!warp_wait(sm, sm.full + jt % kStages, (jt / kStages) & 1)) return false;
+      if (jt >= 2 && !warp_wait(sm, sm.s_free + (jt & 1), ((jt >> 1) & 1) ^ 1)) return false;
+      tc::fence_after_sync();
+      if (tc::elect_one()) {
+        const uint64_t kb = kd + (uint64_t)((jt % kStages) * kStage >> 4);
+#pragma unroll
+        for (int s = 0; s < 16; ++s)
+          tc::mma_f8_ta(tmem + kColS + 64 * (jt & 1), tmem + kColQ + 8 * s, kb + (((s >> 2) * kBox + (s & 3) * 32) >> 4),
+                        id_qk, s > 0);
+        tc::mma_commit(sm.s_full + (jt & 1));
+      }
+      __syncwarp();
+      return true;
+    };
     bool ok = true;
 #pragma unroll 1
     while (true) {
-      const int begin = max(t0 - pre, 0), end = min(t1 - pre, k.tiles);
+      const int begin = max(t0 - pre, 0), end = min(t1 - pre, k.tiles), n = end - begin;
       ok = warp_wait(sm, sm.q_ready, seg & 1);
       ++seg;
-      tc::fence_after_sync();
+      // scores two tiles ahead of the outputs: they wait for keys and for a buffer that is free once its scores have been
+      // read, so the softmax groups always find the next ones
+      ok = ok && qk(j) && (n < 2 || qk(j + 1));
 #pragma unroll 1
-      for (int t = begin; ok && t < end; ++t, ++j) {
-        ok = warp_wait(sm, sm.full + j % kStages, (j / kStages) & 1);
-        if (!ok) break;
-        tc::fence_after_sync();
-        if (tc::elect_one()) {
-          const uint64_t kb = kd + (uint64_t)((j % kStages) * kStage >> 4);
-#pragma unroll
-          for (int s = 0; s < 16; ++s)
-            tc::mma_f8_ta(tmem + kColS + 64 * (j & 1), tmem + kColQ + 8 * s, kb + (((s >> 2) * kBox + (s & 3) * 32) >> 4),
-                          id_qk, s > 0);
-          tc::mma_commit(sm.s_full + (j & 1));
-        }
-        __syncwarp();
-        if (t > begin) ok = pv(j - 1, t - 1 == begin);
+      for (int i = 0; ok && i < n; ++i) {
+        // (keys that are late do not hold back the output, which frees a stage)
+        const bool ahead = i + 2 < n;
+        const bool there = ahead && __all_sync(0xffffffffu, tc::mbar_try_wait(sm.full + (j + i + 2) % kStages, ((j + i + 2) / kStages) & 1));
+        if (there) ok = qk(j + i + 2);
+        ok = ok && pv(j + i, i == 0);
+        if (ahead && !there) ok = ok && qk(j + i + 2);
       }
-      if (ok) ok = pv(j - 1, end - 1 == begin);
+      j += n;
       pre += k.tiles;
       if (!ok || pre >= t1) break;
-      do k = load_query(a.queries + k.q + 1);
-      while (k.tiles == 0);
+      k = next_query(a, k.q);
     }
   } else {
     // ------------------------------------------------------------ softmax: group g takes the tiles j with j % 2 == g
@@ -377,20 +392,56 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     while (true) {
       const int begin = max(t0 - pre, 0), end = min(t1 - pre, k.tiles), n = end - begin;
-      // ---- the query's parts into tensor memory, half of the columns each group (every product that read the last
-      // query's has retired)
+      // ---- the query as two parts of 2^-e q into tensor memory, a group half of the dims: a thread has, of rows lane / 4
+      // and lane / 4 + 8 of its quarter's 16 heads, every fourth four values (every product that read the last query's
+      // parts has retired)
       {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q8) + ((size_t)k.q * 32 + 16 * g) * 128 + 32 * quad + lane;
-        uint32_t w[64];
+        const int r = lane >> 2;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)k.q * kH + 16 * quad + r) * kD + 256 * g + 4 * (lane & 3);
+        uint2 v[2][16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) *reinterpret_cast<uint4*>(w + 4 * e) = tc::ld_nc_v4_now(src + e * 128);
-        const float c = __ldg(a.q8_scale + (size_t)k.q * kH + h);
-        tc::tmem_st32(tmem + kColQ + 64 * g + lanes, w);
-        tc::tmem_st32(tmem + kColQ + 64 * g + 32 + lanes, w + 32);
+        for (int e = 0; e < 16; ++e) {
+          v[0][e] = tc::ld_nc_v2_now(src + 16 * e);
+          v[1][e] = tc::ld_nc_v2_now(src + 8 * kD + 16 * e);
+        }
+        uint32_t* amax = reinterpret_cast<uint32_t*>(sm.base + kOffMax);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          // the largest magnitude by its bits: bf16 pairs compared as unsigned halves
+          uint32_t mx = 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) mx = __vmaxu2(mx, __vmaxu2(v[x][e].x & 0x7fff7fffu, v[x][e].y & 0x7fff7fffu));
+          mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          if ((lane & 3) == 0) amax[g * kH + 16 * quad + r + 8 * x] = max(mx & 0xffffu, mx >> 16);
+        }
+        if (g == 0 && gt < 32 && a.inv_freq) rope_cs(k.p, a.inv_freq, gt, rcos + gt, rsin + gt);
+        tc::named_bar(4, kSoft);
+        // 2^-e with e = exponent - 7: values below 2^8, exact products; a row of denormals, or zeros, stays small; a row that
+        // holds an infinity or a NaN becomes NaN (by its product with 0, and its scores by their factor)
+        auto expo = [&](int hh) { return max((int)(max(amax[hh], amax[kH + hh]) >> 7), 8); };
+        uint32_t hi[32], lo[32];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int be = expo(16 * quad + r + 8 * x);
+          const float inv = be == 255 ? 0.f : __uint_as_float((uint32_t)(261 - be) << 23);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float x0 = __uint_as_float(v[x][e].x << 16) * inv, x1 = __uint_as_float(v[x][e].x & 0xffff0000u) * inv;
+            const float x2 = __uint_as_float(v[x][e].y << 16) * inv, x3 = __uint_as_float(v[x][e].y & 0xffff0000u) * inv;
+            hi[2 * e + x] = e4m3x4(x0, x1, x2, x3);
+            const float2 b0 = e4m3x2_f(hi[2 * e + x]), b1 = e4m3x2_f(hi[2 * e + x] >> 16);
+            lo[2 * e + x] = e4m3x4((x0 - b0.x) * 16.f, (x1 - b0.y) * 16.f, (x2 - b1.x) * 16.f, (x3 - b1.y) * 16.f);
+          }
+        }
+        tc::tmem_st_16x64(tmem + kColQ + 64 * g + lanes, hi);
+        tc::tmem_st_16x64(tmem + kColQ + 64 * g + lanes + (16u << 16), lo);
         tc::tmem_wait_st();
         tc::fence_before_sync();
         tc::mbar_arrive(sm.q_ready);
-        if (g == 0 && gt < 32 && a.inv_freq) rope_cs(k.p, a.inv_freq, gt, rcos + gt, rsin + gt);
+        // what a product of the parts stands for: 2^e, and the softmax scale with it
+        const int be_h = expo(h);
+        const float c = be_h == 255 ? NAN : __uint_as_float((uint32_t)(be_h - 7) << 23) * a.scale2;
         const float c_own = plane ? c * 0.0625f : c, c_other = plane ? c : c * 0.0625f;
         float m = -INFINITY, l = 0.f;
         const int first = (j & 1) == g ? 0 : 1;  // this group's first tile of the query
@@ -406,6 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::tmem_ld32(t_s, x);
             tc::tmem_ld32(t_s + 32, x + 32);
             tc::tmem_wait_ld();
+            tc::fence_before_sync();
+            tc::mbar_arrive(sm.s_free + g);
             // hi part lanes keep keys 0-31 and send 32-63, lo part lanes the other way round
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
@@ -515,8 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (plane == 0) stat[g * kH + h] = make_float2(m, l);
       }
       j += n;
-      // ---- the run's part of this query, or its output: both groups, 16 steps of 8 KB through their buffers
-      const bool whole = begin == 0 && end == k.tiles;
+      // ---- the run's part of this query, or its output, through shared memory: the probabilities' buffers, or, behind the
+      // block's last tile, the stages, which hold all of it at once
+      const bool whole = begin == 0 && end == k.tiles, last = pre + k.tiles >= t1;
       const size_t slot = 2 * blockIdx.x + (begin == 0 ? 1 : 0);
       tc::named_bar(4, kSoft);  // (both groups' statistics, the last R, the angles)
       if (g == 0 && plane == 0) {
@@ -545,12 +599,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = g; c < 8; c += 2) {
           const int blk = c >> 1, h0 = 32 * (c & 1), ri = (128 * blk + dp - (kD - kR)) >> 1;
+          // a head's 128 values: 256 bytes apart, or, in the stages, where they are in the output
+          uint8_t* buf = last ? sm.base + h0 * (2 * kD) + 256 * blk : pbuf;
+          const int pitch = last ? 2 * kD : 256;
           uint32_t x[32];
           tc::tmem_ld32(tmem + kColO + 64 * blk + h0 + lanes, x);
           tc::tmem_wait_ld();
           const bool turn = ri >= 0 && a.inv_freq;
           const float cs = turn ? rcos[ri] : 1.f, sn = turn ? rsin[ri] : 0.f;
-          if (c != g) {
+          if (!last && c != g) {
             if (gt < 32) tc::bulk_wait_read();
             tc::named_bar(2 + g, kGroup);
           }
@@ -565,53 +622,61 @@ __global__ void __launch_bounds__(kThreads, 1)
               y0 = fmaf(z0, cs, y1 * sn);
               y1 = fmaf(-z0, sn, y1 * cs);
             }
-            *reinterpret_cast<__nv_bfloat162*>(pbuf + (e + odd) * 256 + dp * 2) = __floats2bfloat162_rn(y0, y1);
+            *reinterpret_cast<__nv_bfloat162*>(buf + (e + odd) * pitch + dp * 2) = __floats2bfloat162_rn(y0, y1);
           }
           tc::fence_proxy_async_smem();
+          if (last) continue;
           tc::named_bar(2 + g, kGroup);
           if (gt < 32) {
             tc::bulk_store(static_cast<__nv_bfloat16*>(a.out) + ((size_t)k.q * kH + h0 + gt) * kD + 128 * blk, pbuf + gt * 256, 256);
             tc::bulk_commit();
           }
         }
+        if (last) {
+          tc::named_bar(4, kSoft);
+          if (g == 0 && gt < 8) {
+            tc::bulk_store(static_cast<uint8_t*>(a.out) + (size_t)k.q * kH * kD * 2 + gt * 8192, sm.base + gt * 8192, 8192);
+            tc::bulk_commit();
+          }
+        }
       } else {
-        // 16 heads x 128 dims of fp32 a step, one copy
+        // a warp's 32 dims of 64 heads, twice: 16 heads a step
 #pragma unroll 1
-        for (int c = g; c < 16; c += 2) {
-          const int blk = c >> 2, h0 = 16 * (c & 3);
+        for (int c = 0; c < 8; ++c) {
+          const int blk = 2 * g + (c >> 2), h0 = 16 * (c & 3);
+          uint8_t* buf = last ? sm.base + ((blk * 4 + quad) * 4 + (c & 3)) * 2048 : pbuf + quad * 2048;
           uint32_t x[16];
           tc::tmem_ld16(tmem + kColO + 64 * blk + h0 + lanes, x);
           tc::tmem_wait_ld();
-          if (c != g) {
-            if (gt == 0) tc::bulk_wait_read();
-            tc::named_bar(2 + g, kGroup);
+          if (!last && c > 0) {
+            if (lane == 0) tc::bulk_wait_read();
+            __syncwarp();
           }
-          float* dst = reinterpret_cast<float*>(pbuf) + 32 * quad + lane;
+          float* dst = reinterpret_cast<float*>(buf) + lane;
 #pragma unroll
           for (int e4 = 0; e4 < 4; ++e4) {
             const float4 f4 = *reinterpret_cast<const float4*>(fout + h0 + 4 * e4);
-            dst[128 * (4 * e4)] = __uint_as_float(x[4 * e4]) * f4.x;
-            dst[128 * (4 * e4 + 1)] = __uint_as_float(x[4 * e4 + 1]) * f4.y;
-            dst[128 * (4 * e4 + 2)] = __uint_as_float(x[4 * e4 + 2]) * f4.z;
-            dst[128 * (4 * e4 + 3)] = __uint_as_float(x[4 * e4 + 3]) * f4.w;
+            dst[32 * (4 * e4)] = __uint_as_float(x[4 * e4]) * f4.x;
+            dst[32 * (4 * e4 + 1)] = __uint_as_float(x[4 * e4 + 1]) * f4.y;
+            dst[32 * (4 * e4 + 2)] = __uint_as_float(x[4 * e4 + 2]) * f4.z;
+            dst[32 * (4 * e4 + 3)] = __uint_as_float(x[4 * e4 + 3]) * f4.w;
           }
           tc::fence_proxy_async_smem();
-          tc::named_bar(2 + g, kGroup);
-          if (gt == 0) {
-            tc::bulk_store(a.part + slot * kH * kD + (size_t)(blk * kH + h0) * 128, pbuf, kPBuf);
+          __syncwarp();
+          if (lane == 0) {
+            tc::bulk_store(a.part + slot * kH * kD + (size_t)((blk * 4 + quad) * kH + h0) * 32, buf, 2048);
             tc::bulk_commit();
           }
         }
       }
-      if (gt < 32) tc::bulk_wait_read();
+      tc::bulk_wait_read();
       tc::fence_before_sync();
       tc::named_bar(4, kSoft);  // (the buffers are free, O^T and the statistics have been read)
       pre += k.tiles;
       if (pre >= t1) break;
-      do k = load_query(a.queries + k.q + 1);
-      while (k.tiles == 0);
+      k = next_query(a, k.q);
     }
-    if (gt < 32) tc::bulk_wait();
+    tc::bulk_wait();
   }
   // ---- everything in flight has landed and retired before shared and tensor memory go
   tc::fence_before_sync();
@@ -619,8 +684,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (*sm.dead) {
     if (tid == 0) {
       atomicOr(a.err, tc::kErrTimeout);
-      const int upto = *issued;
-      for (int i = max(0, upto - kStages); i < upto; ++i) tc::mbar_wait(sm.full + i % kStages, (i / kStages) & 1);
+      for (int w = 0; w < kLoaders; ++w)
+        for (int i = issued[w] - 1; i >= 0 && i > issued[w] - 1 - kStages; i -= kLoaders)
+          tc::mbar_wait(sm.full + i % kStages, (i / kStages) & 1);
     }
   }
   if (warp == kMmaWarp) {
@@ -643,12 +709,10 @@ bool tc_paged_supported(const Dims& L, int P) {
 
 cudaError_t launch_tc_paged(const PagedArgs& a, cudaStream_t s) {
   const uint64_t rows = (uint64_t)a.n_pages * a.P;
-  CUtensorMap tm_runs, tm_rows;
-  if (!make_tmap_2d_u8(&tm_runs, a.codes, rows, kD, kD, 128, 1u << a.shift, true) ||
-      !make_tmap_2d_u8(&tm_rows, a.codes, rows, kD, kD, 128, 1, true))
-    return cudaErrorInvalidValue;
+  CUtensorMap tm_runs;
+  if (!make_tmap_2d_u8(&tm_runs, a.codes, rows, kD, kD, 128, 1u << a.shift, true)) return cudaErrorInvalidValue;
   allow_smem<kSmem>(k_tc_attend_pages);
-  CSA_LAUNCH(k_tc_attend_pages, dim3(kPagedBlocks), dim3(kThreads), kSmem, s, tm_runs, tm_rows, a);
+  CSA_LAUNCH(k_tc_attend_pages, dim3(kPagedBlocks), dim3(kThreads), kSmem, s, tm_runs, a);
   return cudaGetLastError();
 }
 
