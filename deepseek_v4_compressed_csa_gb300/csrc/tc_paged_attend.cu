@@ -11,7 +11,7 @@
 //     The parts are two rows of one operand, M = 128 = 64 heads x 2, kept in tensor memory (its 128 columns are an A
 //     operand that no product reads from shared memory);
 //   P = hi + lo, E5M2 and E4M3, both added to the same accumulator: 7 bits (at most 2^-7 of a probability, about 2^-9.5 on
-//     average, signs mixed), 3 bits down to 2^-21 of the largest and something down to 2^-24.  (Two E4M3 parts keep 8 bits
+//     average, signs mixed), 3 bits down to 2^-19 of the largest and something down to 2^-22.  (Two E4M3 parts keep 8 bits
 //     but drop everything below 2^-16 of the largest: beside one dominant key, what 64 thousand others add up to.)
 // A tile is 64 keys, one 32 KB stage of six, read once from memory, used K-major for S and MN-major (as V^T) for O:
 //   S [128 x 64] = [Q_hi | Q_lo] K^T, 16 products of K = 32 (two buffers);
@@ -22,8 +22,8 @@
 //
 // Softmax with the scales: t = scale2 S ks, m a running maximum, l = sum 2^{t - m}.  What enters the product is
 // 2^t ks 2^{7 - R}, R a reference that follows the maximum of log2(2^t ks) in steps: at most 2^11, where lo, up to 1/8 of
-// hi, still fits E4M3.  O^T is rescaled only when some head's maximum has passed its R by 4 (powers of two); every head's R
-// then follows.  A tile takes its four warps some 2500 clocks, most of them latency, and the products' pipe 1300: two groups
+// hi, still fits E4M3.  It starts 4 times above the first tile's maximum, and O^T is rescaled only when some head's maximum has
+// passed its R by 4 (powers of two); every head's R then follows.  A tile takes its four warps some 2500 clocks, most of them latency, and the products' pipe 1300: two groups
 // of four take tiles in turn, each with an m and l of its own; R is one, so each tile's decision about it waits for the
 // tile's before.
 #include "paged.cuh"
@@ -47,6 +47,7 @@ constexpr int kThreads = 32 * (kLoaders + 1) + kSoft;
 constexpr int kColO = 0, kColS = 256, kColQ = 384, kCols = 512;
 constexpr float kGain = 7.f;                  // R stands for 2^7 in the product
 constexpr float kStep = 4.f;                  // how far a maximum may pass R
+constexpr float kHead = 2.f;                  // how far R is set above the first tile's maximum: most grow a little
 
 constexpr int kOffP = kStages * kStage;
 constexpr int kOffScale = kOffP + 2 * kPBuf;              // [kStages][64]
@@ -310,70 +311,72 @@ __global__ void __launch_bounds__(kThreads, 1)
     landed();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
-    constexpr uint32_t id_qk = tc::idesc_e4m3(128, kTile);
-    constexpr uint32_t id_hi = tc::idesc_e4m3(128, kH, true, true), id_lo = tc::idesc_e4m3(128, kH, true);
-    const uint64_t kd = tc::sdesc_kmajor_sw128(tc::smem_u32(sm.base));
-    const uint64_t vd = tc::sdesc_mnmajor_sw128(tc::smem_u32(sm.base), kBox, 1024);
-    const uint64_t pd = tc::sdesc_kmajor_sw128(tc::smem_u32(sm.base + kOffP));
-    int pre = pre0, j = 0, seg = 0;
-    PagedQuery k = k0;
-    // the product O^T of tile jp, whose probabilities the softmax warps have written
-    auto pv = [&](int jp, bool first) {
-      if (!warp_wait(sm, sm.p_full + (jp & 1), (jp >> 1) & 1)) return false;
-      tc::fence_after_sync();
-      if (tc::elect_one()) {
-        const uint64_t va = vd + (uint64_t)((jp % kStages) * kStage >> 4), pa = pd + (uint64_t)((jp & 1) * kPBuf >> 4);
+    // (one elected thread for all of it, stages and phases counted up, descriptors a base plus constants: what this thread
+    // does between two products is time that the tensor pipe may stand still; issued by elections product by product, with
+    // descriptors from the tile's number, they cost 70 clocks each, where the pipe takes 32 and 48)
+    if (tc::elect_one()) {
+      constexpr uint32_t id_qk = tc::idesc_e4m3(128, kTile);
+      constexpr uint32_t id_hi = tc::idesc_e4m3(128, kH, true, true), id_lo = tc::idesc_e4m3(128, kH, true);
+      const uint64_t kd = tc::sdesc_kmajor_sw128(tc::smem_u32(sm.base));
+      const uint64_t vd = tc::sdesc_mnmajor_sw128(tc::smem_u32(sm.base), kBox, 1024);
+      const uint64_t pd = tc::sdesc_kmajor_sw128(tc::smem_u32(sm.base + kOffP));
+      int sq = 0, sp = 0, bq = 0, bp = 0;       // stages and buffers of the next scores and the next output
+      uint32_t fq = 0, hq = 1, hp = 0, seg = 0; // phases: of full[sq], of s_free[bq], of p_full[bp]; of q_ready
+      // S of the next tile, whose buffer's last scores the softmax warps have read
+      auto qk = [&] {
+        if (!wait(sm, sm.full + sq, fq) || !wait(sm, sm.s_free + bq, hq)) return false;
+        tc::fence_after_sync();
+        const uint64_t kb = kd + sq * (kStage >> 4);
+        const uint32_t d = tmem + kColS + 64 * bq;
+#pragma unroll
+        for (int s = 0; s < 16; ++s)
+          tc::mma_f8_ta(d, tmem + kColQ + 8 * s, kb + (((s >> 2) * kBox + (s & 3) * 32) >> 4), id_qk, s > 0);
+        tc::mma_commit(sm.s_full + bq);
+        if (++sq == kStages) { sq = 0; fq ^= 1; }
+        if ((bq ^= 1) == 0) hq ^= 1;
+        return true;
+      };
+      // O^T += of the next tile, whose probabilities they have written
+      auto pv = [&](uint32_t add) {
+        if (!wait(sm, sm.p_full + bp, hp)) return false;
+        tc::fence_after_sync();
+        const uint64_t va = vd + sp * (kStage >> 4), pa = pd + bp * (kPBuf >> 4);
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
           for (int s = 0; s < 4; ++s)  // hi keys 0-31, 32-63, lo keys 0-31, 32-63
             tc::mma_f8(tmem + kColO + 64 * m, va + ((m * kBox + (s & 1) * 4096) >> 4), pa + (s * 32 >> 4),
-                       s < 2 ? id_hi : id_lo, !first || s > 0);
-        tc::mma_commit(sm.empty + jp % kStages);
-        tc::mma_commit(sm.pv_done + (jp & 1));
-      }
-      __syncwarp();
-      return true;
-    };
-    // S of tile jt, whose buffer's last scores the softmax warps have read
-    auto qk = [&](int jt) {
-      if (!warp_wait(sm, sm.full + jt % kStages, (jt / kStages) & 1)) return false;
-      if (jt >= 2 && !warp_wait(sm, sm.s_free + (jt & 1), ((jt >> 1) & 1) ^ 1)) return false;
-      tc::fence_after_sync();
-      if (tc::elect_one()) {
-        const uint64_t kb = kd + (uint64_t)((jt % kStages) * kStage >> 4);
-#pragma unroll
-        for (int s = 0; s < 16; ++s)
-          tc::mma_f8_ta(tmem + kColS + 64 * (jt & 1), tmem + kColQ + 8 * s, kb + (((s >> 2) * kBox + (s & 3) * 32) >> 4),
-                        id_qk, s > 0);
-        tc::mma_commit(sm.s_full + (jt & 1));
-      }
-      __syncwarp();
-      return true;
-    };
-    bool ok = true;
+                       s < 2 ? id_hi : id_lo, s > 0 ? 1u : add);
+        tc::mma_commit(sm.empty + sp);
+        tc::mma_commit(sm.pv_done + bp);
+        if (++sp == kStages) sp = 0;
+        if ((bp ^= 1) == 0) hp ^= 1;
+        return true;
+      };
+      int pre = pre0;
+      PagedQuery k = k0;
+      bool ok = true;
 #pragma unroll 1
-    while (true) {
-      const int begin = max(t0 - pre, 0), end = min(t1 - pre, k.tiles), n = end - begin;
-      ok = warp_wait(sm, sm.q_ready, seg & 1);
-      ++seg;
-      // scores two tiles ahead of the outputs: they wait for keys and for a buffer that is free once its scores have been
-      // read, so the softmax groups always find the next ones
-      ok = ok && qk(j) && (n < 2 || qk(j + 1));
+      while (true) {
+        const int n = min(t1 - pre, k.tiles) - max(t0 - pre, 0);
+        ok = wait(sm, sm.q_ready, seg & 1);
+        ++seg;
+        // scores two tiles ahead of the outputs: they wait for keys and for a buffer that is free once its scores have been
+        // read, so the softmax groups always find the next ones
+        ok = ok && qk() && (n < 2 || qk());
 #pragma unroll 1
-      for (int i = 0; ok && i < n; ++i) {
-        // (keys that are late do not hold back the output, which frees a stage)
-        const bool ahead = i + 2 < n;
-        const bool there = ahead && __all_sync(0xffffffffu, tc::mbar_try_wait(sm.full + (j + i + 2) % kStages, ((j + i + 2) / kStages) & 1));
-        if (there) ok = qk(j + i + 2);
-        ok = ok && pv(j + i, i == 0);
-        if (ahead && !there) ok = ok && qk(j + i + 2);
+        for (int i = 0; ok && i < n; ++i) {
+          if (i + 2 < n) ok = qk();
+          ok = ok && pv(i > 0);
+        }
+        pre += k.tiles;
+        if (!ok || pre >= t1) break;
+        k = next_query(a, k.q);
       }
-      j += n;
-      pre += k.tiles;
-      if (!ok || pre >= t1) break;
-      k = next_query(a, k.q);
+      tc::mma_commit(sm.drain);  // every product retires before tensor memory is released
+      if (!tc::mbar_wait(sm.drain, 0)) *sm.dead = 1;
     }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax: group g takes the tiles j with j % 2 == g
     const int quad = warp & 3, plane = lane >> 4, h = 16 * quad + (lane & 15);
@@ -511,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // ---- the reference follows log2 of the largest 2^t ks: after the tile before has decided
           const float lv = vt > 0.f ? mr + lg2(vt) : -INFINITY;
           if (jt > 0) wait(sm, sm.decided + (g ^ 1), ((jt - 1) >> 1) & 1);
-          float ref = i == 0 ? lv : refs[h];
+          float ref = i == 0 ? lv + kHead : refs[h];
           if (i == 0) {
             if (plane == 0) refs[h] = ref;
           } else if (tc::named_bar_any(2 + g, kGroup, lv > ref + kStep)) {
@@ -640,32 +643,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        // a warp's 32 dims of 64 heads, twice: 16 heads a step
+        // a warp's 32 dims of 64 heads, twice: 8 KB at once in the stages, or 16 heads a step
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          const int blk = 2 * g + (c >> 2), h0 = 16 * (c & 3);
-          uint8_t* buf = last ? sm.base + ((blk * 4 + quad) * 4 + (c & 3)) * 2048 : pbuf + quad * 2048;
-          uint32_t x[16];
-          tc::tmem_ld16(tmem + kColO + 64 * blk + h0 + lanes, x);
+        for (int c = 0; c < 4; ++c) {
+          const int blk = 2 * g + (c >> 1), h0 = 32 * (c & 1);
+          float* part = a.part + slot * kH * kD + (size_t)((blk * 4 + quad) * kH + h0) * 32;
+          uint32_t x[32];
+          tc::tmem_ld32(tmem + kColO + 64 * blk + h0 + lanes, x);
           tc::tmem_wait_ld();
-          if (!last && c > 0) {
-            if (lane == 0) tc::bulk_wait_read();
-            __syncwarp();
-          }
-          float* dst = reinterpret_cast<float*>(buf) + lane;
+          uint8_t* buf = last ? sm.base + ((blk * 4 + quad) * kH + h0) * 128 : pbuf + quad * 2048;
 #pragma unroll
-          for (int e4 = 0; e4 < 4; ++e4) {
-            const float4 f4 = *reinterpret_cast<const float4*>(fout + h0 + 4 * e4);
-            dst[32 * (4 * e4)] = __uint_as_float(x[4 * e4]) * f4.x;
-            dst[32 * (4 * e4 + 1)] = __uint_as_float(x[4 * e4 + 1]) * f4.y;
-            dst[32 * (4 * e4 + 2)] = __uint_as_float(x[4 * e4 + 2]) * f4.z;
-            dst[32 * (4 * e4 + 3)] = __uint_as_float(x[4 * e4 + 3]) * f4.w;
-          }
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tc::bulk_store(a.part + slot * kH * kD + (size_t)((blk * 4 + quad) * kH + h0) * 32, buf, 2048);
-            tc::bulk_commit();
+          for (int half = 0; half < 2; ++half) {
+            if (!last && c + half > 0) {
+              if (lane == 0) tc::bulk_wait_read();
+              __syncwarp();
+            }
+            float* dst = reinterpret_cast<float*>(buf) + (last ? 512 * half : 0) + lane;
+#pragma unroll
+            for (int e4 = 0; e4 < 4; ++e4) {
+              const float4 f4 = *reinterpret_cast<const float4*>(fout + h0 + 16 * half + 4 * e4);
+              const uint32_t* y = x + 16 * half + 4 * e4;
+              dst[32 * (4 * e4)] = __uint_as_float(y[0]) * f4.x;
+              dst[32 * (4 * e4 + 1)] = __uint_as_float(y[1]) * f4.y;
+              dst[32 * (4 * e4 + 2)] = __uint_as_float(y[2]) * f4.z;
+              dst[32 * (4 * e4 + 3)] = __uint_as_float(y[3]) * f4.w;
+            }
+            if (!last || (half && (c & 1))) {
+              tc::fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (last) tc::bulk_store(part - 1024, buf - 4096, 8192);
+                else tc::bulk_store(part + 512 * half, buf, 2048);
+                tc::bulk_commit();
+              }
+            }
           }
         }
       }
@@ -688,13 +699,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = issued[w] - 1; i >= 0 && i > issued[w] - 1 - kStages; i -= kLoaders)
           tc::mbar_wait(sm.full + i % kStages, (i / kStages) & 1);
     }
-  }
-  if (warp == kMmaWarp) {
-    if (tc::elect_one()) {
-      tc::mma_commit(sm.drain);
-      if (!tc::mbar_wait(sm.drain, 0)) atomicOr(a.err, tc::kErrTimeout);
-    }
-    __syncwarp();
   }
   tc::fence_before_sync();
   __syncthreads();
