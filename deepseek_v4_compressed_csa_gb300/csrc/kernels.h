@@ -428,6 +428,7 @@ struct PagedArgs {
   int2* parts;                 // [B T] block of a query's first part, and their count
   float* part;                 // [2 blocks][D / cols][H][cols] parts of split queries, relative to their maximum
   float2* ml;                  // [2 blocks][H] their maxima (in powers of two) and sums
+  float2* turns;               // [blocks][R / 2] cos, sin of the output's rotation, by the block of the first part
   int cols;                    // dims that a part holds side by side
   int tile, shift, min_tiles;  // keys a tile; log2 of the rows that lie in one page; the shortest run of tiles
   int32_t* err;

@@ -134,56 +134,170 @@ __device__ __forceinline__ PagedQuery next_query(const PagedArgs& a, int q) {
 }
 
 // ---------------------------------------------------------------- work over the blocks
-// The tiles of all queries, one after another, are cut into equal runs, one a block: block c has tiles [c per, (c + 1) per).
-// However ragged the batch, blocks end together, and one query of a long cache is spread over the device.  A run that
-// covers a query whole writes its output; otherwise it leaves its part: slot 2 c + 1 if the query begins in the run, 2 c if
-// it began before.  parts[q] says where a query's parts are.  Every block finds the plan itself (a few loads a query, spread
-// over its threads): a kernel before it would cost more than that for the batches that count in microseconds.
+// Each query is cut into equal pieces of at most L tiles, and a block takes one piece, or neighbouring ones: its run
+// [t0, t1) of all queries' tiles, one after another.  A run that covers a query whole writes its output; otherwise it leaves
+// its part: slot 2 c + 1 if the query begins in the run of block c, 2 c if it began before.  parts[q] says where a query's
+// parts are.  A part costs its block some 2 us and the merge as much, so queries are not cut for the last bit of balance:
+//   fewer queries than blocks: every piece has a block of its own.  Of two lengths at which there are enough, the shorter:
+//     the longest query over blocks / queries pieces, and total / (blocks - queries), since ceil(n / L) <= n / L + 1 (128
+//     queries of 11 tiles on 152 blocks stay whole: 29 us; in even runs of 10 tiles 55);
+//   more: L = total / blocks, so only longer queries than that are cut, and block c takes the pieces that begin in
+//     [c, c + 1) total / blocks.  No piece is longer than that, so every block up to the last piece's has one.
+// Every block finds the plan itself (a few loads a query, spread over its threads): a kernel before it would cost more than
+// that for the batches that count in microseconds.
 struct PagedRun {
   int t0, t1;      // the run's tiles
   int pre;         // tiles before its first query
   PagedQuery k;    // that query
 };
+constexpr int kPlanInts = 96;  // scratch of paged_plan
 
-// Whole block (at most 1024 threads); `sm` in shared memory is the result.
-__device__ __forceinline__ void paged_plan(const PagedArgs& a, PagedRun* sm, int* sums) {
-  const int Q = a.B * a.T, nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+__device__ __forceinline__ unsigned div_up(unsigned n, unsigned d) { return (n + d - 1) / d; }
+
+// Sums over the block's threads of v: before this one, and of all.  scratch: 32 ints, 16-byte aligned; the block's barrier
+// stands between the sums' writes and their reads.
+__device__ __forceinline__ int warp_scan(int v, int* scratch) {
+  const int lane = threadIdx.x & 31;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) scratch[threadIdx.x >> 5] = inc;
+  return inc - v;
+}
+template <int nw>
+__device__ __forceinline__ int2 scan_warps(const int* scratch) {
+  const int warp = threadIdx.x >> 5;
+  int before = 0, total = 0;
+#pragma unroll
+  for (int w4 = 0; w4 < nw; w4 += 4) {
+    const int4 v = *reinterpret_cast<const int4*>(scratch + w4);
+    before += (w4 < warp ? v.x : 0) + (w4 + 1 < warp ? v.y : 0) + (w4 + 2 < warp ? v.z : 0) + (w4 + 3 < warp ? v.w : 0);
+    total += v.x + v.y + v.z + v.w;
+  }
+  return make_int2(before, total);
+}
+
+// Equal pieces of n tiles: the first n % m of them are a tile longer
+struct Pieces {
+  int m, base, rem;
+  __device__ __forceinline__ Pieces(int n, int count) : m(count), base(n / max(count, 1)), rem(n - base * count) {}
+  __device__ __forceinline__ int start(int i) const { return i * base + min(i, rem); }
+  // the first piece that starts at or behind tile x (m if none)
+  __device__ __forceinline__ int from(int x) const {
+    if (x <= 0) return 0;
+    const int longer = rem * (base + 1);
+    const unsigned i = x <= longer ? div_up(x, base + 1) : rem + div_up(x - longer, max(base, 1));
+    return (int)min(i, (unsigned)m);
+  }
+};
+
+// Whole block of 32 nw threads (nw a multiple of 4); `sm` in shared memory is the result.
+template <int nw>
+__device__ __forceinline__ void paged_plan(const PagedArgs& a, PagedRun* sm, int* scratch) {
+  constexpr int nt = 32 * nw;
+  const int Q = a.B * a.T, tid = threadIdx.x, G = gridDim.x, c = blockIdx.x;
   const int each = (Q + nt - 1) / nt, q0 = min(Q, tid * each), q1 = min(Q, q0 + each);
-  const bool lead = blockIdx.x == 0;
-  int mine = 0;
+  const bool lead = c == 0;
+  int mine = 0, live = 0, longest = 0;
   PagedQuery k;
   for (int q = q0; q < q1; ++q) {
     k = find_query(a, q, lead);
     mine += k.tiles;
+    live += k.tiles > 0;
+    longest = max(longest, k.tiles);
   }
-  int inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
+  int pre = warp_scan(mine, scratch);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  live = __reduce_add_sync(0xffffffffu, live);
+  if ((tid & 31) == 0) {
+    scratch[32 + (tid >> 5)] = longest;
+    scratch[48 + (tid >> 5)] = live;
   }
-  if (lane == 31) sums[warp] = inc;
   __syncthreads();
-  int pre = inc - mine, total = 0;
-  for (int w = 0; w < nw; ++w) {
-    pre += w < warp ? sums[w] : 0;
-    total += sums[w];
-  }
   // (a call has fewer than 2^31 tiles: the host refuses tables and batches that could hold more)
-  const int per = max(a.min_tiles, (int)(((long long)total + gridDim.x - 1) / gridDim.x));
-  const int t0 = (int)min((long long)total, (long long)blockIdx.x * per), t1 = (int)min((long long)total, (long long)t0 + per);
+  const int2 warps = scan_warps<nw>(scratch);
+  const int total = warps.y, queries = scan_warps<nw>(scratch + 48).y;
+  pre += warps.x;
+#pragma unroll
+  for (int w = 0; w < nw; ++w) longest = max(longest, scratch[32 + w]);
+  int t0 = total, t1 = total;  // (a block behind the last piece has nothing)
+  if (queries < G) {
+    const int L = max(max(a.min_tiles, (int)div_up(total, G)),
+                      min((int)div_up(longest, queries > 0 ? G / queries : 1), (int)div_up(total, G - queries)));
+    // (each is 1 but for batches of some hundred slots of which few are in use)
+    int count = 0;
+    for (int q = q0; q < q1; ++q) {
+      if (each > 1) k = find_query(a, q, false);
+      count += (int)div_up(k.tiles, L);
+    }
+    int first = warp_scan(tid < Q ? count : 0, scratch + 64);
+    __syncthreads();
+    first += scan_warps<nw>(scratch + 64).x;
+    for (int q = q0; q < q1; ++q) {
+      if (each > 1) k = find_query(a, q, false);
+      const Pieces p(k.tiles, (int)div_up(k.tiles, L));
+      const int i = c - first;
+      if (i >= 0 && i < p.m) {
+        sm->t0 = pre + p.start(i);
+        sm->t1 = pre + p.start(i + 1);
+        sm->pre = pre;
+        sm->k = k;
+      }
+      if (lead) a.parts[q] = make_int2(first, p.m);
+      first += p.m;
+      pre += k.tiles;
+    }
+    if (tid == 0) scratch[80] = scan_warps<nw>(scratch + 64).y;
+    __syncthreads();
+    if (c >= scratch[80]) {  // a block without a piece
+      if (tid == 0) sm->t0 = sm->t1 = 0;
+      __syncthreads();
+    }
+    return;
+  }
+  const int base = total / G, rem = total - base * G, L = max(1, base);
+  auto begin = [&](int b) { return b * base + (b * rem + G - 1) / G; };  // ceil(b total / G)
+  const int lo = begin(c), hi = begin(c + 1);
+  int* run = scratch + 80;
+  if (tid == 0) run[0] = run[1] = total;
+  __syncthreads();
+  int at = pre;
+  for (int q = q0; q < q1; ++q) {
+    if (each > 1) k = find_query(a, q, false);
+    const Pieces p(k.tiles, (int)div_up(k.tiles, L));
+    const int i0 = p.from(lo - at), i1 = p.from(hi - at);
+    if (i0 < p.m) atomicMin(run, at + p.start(i0));
+    if (i1 < p.m) atomicMin(run + 1, at + p.start(i1));
+    if (lead) {
+      auto block_of = [&](int x) {  // the block in whose share tile x lies
+        int b = min(G - 1, (int)((float)x * ((float)G / (float)total)));
+        while (b > 0 && begin(b) > x) --b;
+        while (b < G - 1 && begin(b + 1) <= x) ++b;
+        return b;
+      };
+      const int b0 = p.m > 0 ? block_of(at) : 0;
+      a.parts[q] = make_int2(b0, p.m > 0 ? block_of(at + p.start(p.m - 1)) - b0 + 1 : 0);
+    }
+    at += k.tiles;
+  }
+  __syncthreads();
+  t0 = run[0];
+  t1 = run[1];
+  at = pre;
+  for (int q = q0; q < q1 && t0 < t1; ++q) {
+    if (each > 1) k = find_query(a, q, false);
+    if (k.tiles > 0 && at <= t0 && t0 < at + k.tiles) {
+      sm->pre = at;
+      sm->k = k;
+    }
+    at += k.tiles;
+  }
   if (tid == 0) {
     sm->t0 = t0;
     sm->t1 = t1;
-  }
-  for (int q = q0; q < q1; ++q) {
-    if (each > 1) k = find_query(a, q, false);
-    if (k.tiles > 0 && pre <= t0 && t0 < pre + k.tiles) {
-      sm->pre = pre;
-      sm->k = k;
-    }
-    if (lead) a.parts[q] = make_int2(pre / per, k.tiles > 0 ? (pre + k.tiles - 1) / per - pre / per + 1 : 0);
-    pre += k.tiles;
   }
   __syncthreads();
 }

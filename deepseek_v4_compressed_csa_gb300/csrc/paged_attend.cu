@@ -25,13 +25,14 @@ template <typename T>
 __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __grid_constant__ PagedArgs a) {
   pdl_trigger();  // (the merge alone follows, and waits)
   extern __shared__ __align__(16) float sm_pa[];
-  __shared__ int s_row[kSimtTile], s_sums[kSimtWarps];
+  __shared__ int s_row[kSimtTile];
+  __shared__ __align__(16) int s_plan[kPlanInts];
   __shared__ PagedRun s_run;
   const int D = a.D, KS = D + kSimtPad, n8 = D >> 3;
   float* ks = sm_pa;                    // [kSimtTile][KS] keys
   float* qs = sm_pa + kSimtTile * KS;   // [kSimtWarps][D] queries of this group of heads
   pdl_wait();
-  paged_plan(a, &s_run, s_sums);
+  paged_plan<kSimtWarps>(a, &s_run, s_plan);
   const int t0 = s_run.t0, t1 = s_run.t1;
   if (t0 >= t1) return;
   int pre = s_run.pre;
@@ -43,6 +44,12 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
     const int begin = max(t0 - pre, 0), end = min(t1 - pre, k.tiles), nkeys = k.n0 + k.f + k.nw;
     const bool whole = begin == 0 && end == k.tiles;
     const int slot = 2 * blockIdx.x + (begin == 0 ? 1 : 0);
+    if (begin == 0 && !whole && a.inv_freq)  // (for the merge: an angle costs a lane some hundred instructions)
+      for (int i = tid; i < a.R / 2; i += blockDim.x) {
+        float2 t;
+        rope_cs(k.p, a.inv_freq, i, &t.x, &t.y);
+        a.turns[(size_t)blockIdx.x * (a.R / 2) + i] = t;
+      }
 #pragma unroll 1
     for (int h0 = 0; h0 < a.H && begin < end; h0 += kSimtWarps) {
       const int h = h0 + warp;
@@ -167,116 +174,136 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
 
 // ---------------------------------------------------------------- merge of split queries
 // With (m_s, l_s, acc_s) of the parts: M = max(z, m_s), Z = 2^{z - M} + sum_s l_s 2^{m_s - M},
-// o = sum_s acc_s 2^{m_s - M} / Z (z the sink in powers of two).  A block of eight warps takes one head of a query (up to 8
-// queries: each has many parts) or eight; a head's warps take its parts in turn.  The weights are found first, from all
-// parts' statistics at once, so that the sum over the accumulators is loads and products only, several parts in flight;
-// the angles of the rotation are found meanwhile, once a block.
+// o = sum_s acc_s 2^{m_s - M} / Z (z the sink in powers of two).  An item is 512 values of a head of a split query, 16 a lane;
+// `share` warps take its parts in turn.  What the kernel waits for is memory, two round trips (where the parts are; their
+// statistics and the first accumulators together), if it has few enough instructions beside its loads (128 values an item
+// cost 1500 a warp, 8.7 us for 8 queries of 18 parts) and blocks: one started a head of every query cost 8 us on 128 queries
+// of which none was split.  So a block finds the split queries itself and walks their items.
 constexpr int kMergeWarps = 8;
+constexpr int kMergeAhead = 4;  // parts in flight a warp
 
-// kC: 4-value columns a lane holds, 128 values apart; kAhead: parts in flight
-template <typename T, int kC, int kAhead, bool kOneHead>
-__global__ void __launch_bounds__(32 * kMergeWarps) k_merge_pages(const __grid_constant__ PagedArgs a) {
+template <typename T>
+__global__ void __launch_bounds__(32 * kMergeWarps, 2) k_merge_pages(const __grid_constant__ PagedArgs a, int share) {
   // no early trigger: what follows finds the outputs written
-  extern __shared__ __align__(16) float sm_merge[];  // [kMergeWarps][kPagedBlocks] weights; [R / 2] angles; sums
+  __shared__ int4 s_list[kPagedBlocks];  // split queries: q, block of the first part, parts (at least two of the blocks each)
+  __shared__ int s_count[kMergeWarps];
+  __shared__ float4 s_acc[kMergeWarps][128];
+  __shared__ float s_wt[kMergeWarps][kPagedBlocks];  // weights of a warp's item's parts
   pdl_wait();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n4 = a.D >> 2;
-  const int h = kOneHead ? blockIdx.y : blockIdx.y * kMergeWarps + warp;
-  const int first = kOneHead ? warp : 0, step = kOneHead ? kMergeWarps : 1;
-  float* wt = sm_merge + warp * kPagedBlocks;  // (a query has at most a part in every block)
-  float2* cs = reinterpret_cast<float2*>(sm_merge + kMergeWarps * kPagedBlocks);
-  float4* sums = reinterpret_cast<float4*>(sm_merge + kMergeWarps * kPagedBlocks + a.R);  // kOneHead: [kMergeWarps][D]
-  const bool on = h < a.H;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, Q = a.B * a.T;
+  int n_split = 0;
+  for (int q0 = 0; q0 < Q; q0 += 32 * kMergeWarps) {
+    const int2 at = q0 + tid < Q ? a.parts[q0 + tid] : make_int2(0, 0);
+    const uint32_t on = __ballot_sync(0xffffffffu, at.y > 1);
+    if (lane == 0) s_count[warp] = __popc(on);
+    __syncthreads();
+    int before = n_split;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+      before += w < warp ? s_count[w] : 0;
+      n_split += s_count[w];
+    }
+    if (at.y > 1) s_list[before + __popc(on & ((1u << lane) - 1))] = make_int4(q0 + tid, at.x, at.y, 0);
+    __syncthreads();
+  }
+  const int chunks = (a.D + 511) / 512, items = n_split * a.H * chunks, per = kMergeWarps / share;
+  const int first = warp % share;
 #pragma unroll 1
-  for (int q = blockIdx.x; q < a.B * a.T; q += gridDim.x) {
-    const int2 at = a.parts[q];
-    if (at.y <= 1) continue;
-    __syncthreads();  // (the query before has been read)
-    if (a.inv_freq) {
-      const int p = a.pos[q / a.T] + q % a.T;
-      for (int i = tid; i < a.R / 2; i += 32 * kMergeWarps) rope_cs(p, a.inv_freq, i, &cs[i].x, &cs[i].y);
+  for (int i0 = blockIdx.x * per; i0 < items; i0 += gridDim.x * per) {
+    const int item = min(i0 + warp / share, items - 1);  // (a warp behind the last repeats it)
+    const int hq = item / chunks, lq = hq / a.H, h = hq - lq * a.H, d0 = 512 * (item - hq * chunks) + 4 * lane;
+    const int4 at = s_list[lq];
+    // part s of the query: slot 2 (block + s), the first one the slot behind; a lane's columns: 4 values, 128 apart
+    const size_t one = (size_t)a.H * a.D, step = 2 * one * share;
+    const float* src = a.part + 2 * one * (at.y + first) + (first == 0 ? one : 0);
+    size_t off[4];
+    bool on[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int d = d0 + 128 * c, blk = a.cols == a.D ? 0 : d >> 5;  // (blocks of 32 dims, or all)
+      on[c] = d < a.D;
+      off[c] = ((size_t)blk * a.H + h) * a.cols + (d - blk * 32);
     }
-    auto slot = [&](int s) { return (size_t)(2 * (at.x + s) + (s == 0)); };
-    float inv = 0.f;
-    if (on) {
-      const float z2 = a.sink ? a.sink[h] * 1.4426950408889634f : -INFINITY;
-      constexpr int kL = (kPagedBlocks + 31) / 32;
-      float2 ml[kL];
-      float M = z2;
+    float4 x[kMergeAhead][4];
+    auto fetch = [&](int s0, const float* p) {
 #pragma unroll
-      for (int i = 0; i < kL; ++i) {
-        const int s = lane + 32 * i;
-        ml[i] = s < at.y ? a.ml[slot(s) * a.H + h] : make_float2(-INFINITY, 0.f);
+      for (int g = 0; g < kMergeAhead; ++g) {
+        if (s0 + g * share < at.z) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (on[c]) x[g][c] = __ldcg(reinterpret_cast<const float4*>(p + off[c]));
+        }
+        p += s0 + g * share == 0 ? step - one : step;
       }
-#pragma unroll
-      for (int i = 0; i < kL; ++i) M = fmaxf(M, ml[i].x);
-      M = warp_max(M);
-      float Z = 0.f;
-#pragma unroll
-      for (int i = 0; i < kL; ++i) {
-        const int s = lane + 32 * i;
-        const float f = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - M);  // (a part without keys)
-        if (s < at.y) wt[s] = f;
-        Z = fmaf(ml[i].y, f, Z);
-      }
-      Z = warp_sum(Z) + (z2 == -INFINITY ? 0.f : exp2f(z2 - M));
-      inv = Z == 0.f ? 0.f : 1.f / Z;
+      return p;
+    };
+    src = fetch(first, src);
+    // the weights (every warp of an item finds them)
+    const float z2 = a.sink ? a.sink[h] * 1.4426950408889634f : -INFINITY;
+    const float2* stat = a.ml + (size_t)2 * at.y * a.H + h;
+    float M = z2, Z = 0.f;
+    const float2 ml0 = lane < at.z ? __ldcg(stat + 2 * lane * a.H + (lane == 0 ? a.H : 0)) : make_float2(-INFINITY, 0.f);
+    M = fmaxf(M, ml0.x);
+    for (int s = lane + 32; s < at.z; s += 32) M = fmaxf(M, __ldcg(stat + 2 * s * a.H).x);
+    M = warp_max(M);
+    float* wt = s_wt[warp];
+    __syncwarp();  // (the weights of the item before have been read)
+    for (int s = lane; s < at.z; s += 32) {
+      const float2 ml = s < 32 ? ml0 : __ldcg(stat + 2 * s * a.H);
+      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);  // (a part without keys)
+      wt[s] = f;
+      Z = fmaf(ml.y, f, Z);
     }
+    Z = warp_sum(Z) + (z2 == -INFINITY ? 0.f : exp2f(z2 - M));
     __syncwarp();
-    float4 acc[kC];
+    float4 acc[4];
 #pragma unroll
-    for (int c = 0; c < kC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (on) {
+    for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-      for (int s0 = first; s0 < at.y; s0 += kAhead * step) {
-        float4 x[kAhead][kC];
-        float f[kAhead];
+    for (int s0 = first; s0 < at.z; s0 += kMergeAhead * share) {
+      if (s0 > first) src = fetch(s0, src);
 #pragma unroll
-        for (int g = 0; g < kAhead; ++g) {
-          const int s = min(s0 + g * step, at.y - 1);
-          f[g] = s0 + g * step < at.y ? wt[s] : 0.f;
-          const float* src = a.part + slot(s) * a.H * a.D;
+      for (int g = 0; g < kMergeAhead; ++g) {
+        const int s = s0 + g * share;
+        const float f = s < at.z ? wt[s] : 0.f;
+        if (f == 0.f) continue;  // (what a part without keys holds counts for nothing)
 #pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            const int d = 4 * (lane + 32 * c), blk = a.cols == a.D ? 0 : d >> 5;  // (blocks of 32 dims, or all)
-            if (lane + 32 * c < n4)
-              x[g][c] = __ldcg(reinterpret_cast<const float4*>(src + ((size_t)blk * a.H + h) * a.cols + (d - blk * 32)));
-          }
+        for (int c = 0; c < 4; ++c) {
+          acc[c].x = fmaf(x[g][c].x, f, acc[c].x);
+          acc[c].y = fmaf(x[g][c].y, f, acc[c].y);
+          acc[c].z = fmaf(x[g][c].z, f, acc[c].z);
+          acc[c].w = fmaf(x[g][c].w, f, acc[c].w);
         }
-#pragma unroll
-        for (int g = 0; g < kAhead; ++g) {
-          if (f[g] == 0.f) continue;  // (what a part without keys holds counts for nothing)
-#pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            if (lane + 32 * c < n4) {
-              acc[c].x = fmaf(x[g][c].x, f[g], acc[c].x);
-              acc[c].y = fmaf(x[g][c].y, f[g], acc[c].y);
-              acc[c].z = fmaf(x[g][c].z, f[g], acc[c].z);
-              acc[c].w = fmaf(x[g][c].w, f[g], acc[c].w);
-            }
-          }
-        }
-      }
-      if (kOneHead) {
-#pragma unroll
-        for (int c = 0; c < kC; ++c)
-          if (lane + 32 * c < n4) sums[warp * n4 + lane + 32 * c] = acc[c];
       }
     }
-    __syncthreads();  // (the sums, the angles)
-    if (!on) continue;
-    auto write = [&](int col, float4 v4) {
-      const int d = 4 * col;
-      float v[4] = {v4.x * inv, v4.y * inv, v4.z * inv, v4.w * inv};
-      if (a.inv_freq && d >= a.D - a.R) {
+    if (share > 1) {
+      __syncthreads();  // (the items before have been read)
 #pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const float2 t = cs[(d + e - (a.D - a.R)) >> 1];
-          const float x0 = v[e], x1 = v[e + 1];
-          v[e] = fmaf(x0, t.x, x1 * t.y);
-          v[e + 1] = fmaf(-x0, t.y, x1 * t.x);
+      for (int c = 0; c < 4; ++c) s_acc[warp][lane + 32 * c] = acc[c];
+      __syncthreads();
+      if (first != 0) continue;
+      for (int g = 1; g < share; ++g)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float4 v = s_acc[warp + g][lane + 32 * c];
+          acc[c].x += v.x; acc[c].y += v.y; acc[c].z += v.z; acc[c].w += v.w;
         }
+    }
+    const float inv = Z == 0.f ? 0.f : 1.f / Z;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (!on[c]) continue;
+      const int d = d0 + 128 * c;
+      float v[4] = {acc[c].x * inv, acc[c].y * inv, acc[c].z * inv, acc[c].w * inv};
+      if (a.inv_freq && d >= a.D - a.R) {
+        const float4 t = __ldcg(reinterpret_cast<const float4*>(a.turns + (size_t)at.y * (a.R / 2) + ((d - (a.D - a.R)) >> 1)));
+        const float x0 = v[0], x2 = v[2];
+        v[0] = fmaf(x0, t.x, v[1] * t.y);
+        v[1] = fmaf(-x0, t.y, v[1] * t.x);
+        v[2] = fmaf(x2, t.z, v[3] * t.w);
+        v[3] = fmaf(-x2, t.w, v[3] * t.z);
       }
-      T* o = static_cast<T*>(a.out) + ((size_t)q * a.H + h) * a.D + d;
+      T* o = static_cast<T*>(a.out) + ((size_t)at.x * a.H + h) * a.D + d;
       if constexpr (sizeof(T) == 2) {
         uint2 u;
         reinterpret_cast<__nv_bfloat162*>(&u)[0] = __floats2bfloat162_rn(v[0], v[1]);
@@ -285,47 +312,26 @@ __global__ void __launch_bounds__(32 * kMergeWarps) k_merge_pages(const __grid_c
       } else {
         *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
       }
-    };
-    if (kOneHead) {  // the head's columns over all threads
-      for (int col = tid; col < n4; col += 32 * kMergeWarps) {
-        float4 v4 = sums[col];
-        for (int w = 1; w < kMergeWarps; ++w) {
-          const float4 x = sums[w * n4 + col];
-          v4.x += x.x; v4.y += x.y; v4.z += x.z; v4.w += x.w;
-        }
-        write(col, v4);
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < kC; ++c)
-        if (lane + 32 * c < n4) write(lane + 32 * c, acc[c]);
     }
   }
 }
 
-template <typename T, int kC>
-cudaError_t merge_c(const PagedArgs& a, cudaStream_t s) {
-  const int Q = a.B * a.T, smem = (kMergeWarps * kPagedBlocks + a.R) * 4;
-  if (Q <= 8) {
-    constexpr int kSmem = (kMergeWarps * kPagedBlocks + 1024 + kMergeWarps * 1024) * 4;
-    static_assert(kSmem <= 48 * 1024, "the sums fit what every kernel may take");
-    CSA_LAUNCH((k_merge_pages<T, kC, kC <= 4 ? 4 : 2, true>), dim3(Q, a.H), dim3(32 * kMergeWarps),
-               smem + kMergeWarps * a.D * 4, s, a);
-  } else {
-    CSA_LAUNCH((k_merge_pages<T, kC, 2, false>), dim3(min(Q, 4 * kPagedBlocks), (a.H + kMergeWarps - 1) / kMergeWarps),
-               dim3(32 * kMergeWarps), smem, s, a);
-  }
-  return cudaGetLastError();
-}
 template <typename T>
 cudaError_t launch_merge(const PagedArgs& a, cudaStream_t s) {
-  return a.D <= 128 ? merge_c<T, 1>(a, s) : a.D <= 512 ? merge_c<T, 4>(a, s) : merge_c<T, 8>(a, s);
+  // few queries have many parts each (about blocks / queries): a warp takes four at a time, more of them share an item
+  const int Q = a.B * a.T;
+  int share = 1;
+  while (share < kMergeWarps && share * kMergeAhead * Q < kPagedBlocks) share *= 2;
+  const long long items = (long long)min(Q, kPagedBlocks) * a.H * ((a.D + 511) / 512), per = kMergeWarps / share;
+  CSA_LAUNCH(k_merge_pages<T>, dim3((unsigned)min((items + per - 1) / per, 2LL * kPagedBlocks)), dim3(32 * kMergeWarps), 0,
+             s, a, share);
+  return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t attend_t(const Dims& L, PagedArgs a, cudaStream_t s) {
-  a.min_tiles = 2;
   if (tc_paged_supported(L, a.P)) {
+    a.min_tiles = 2;
     a.tile = 64;
     a.shift = 3;  // the largest power of two that divides a page, at most a tile
     while (a.shift < 6 && a.P % (2 << a.shift) == 0) ++a.shift;
@@ -333,6 +339,7 @@ cudaError_t attend_t(const Dims& L, PagedArgs a, cudaStream_t s) {
     const cudaError_t e = launch_tc_paged(a, s);
     if (e != cudaSuccess) return e;
   } else {
+    a.min_tiles = 1;
     a.tile = kSimtTile;
     a.shift = 0;
     a.cols = a.D;
@@ -347,6 +354,7 @@ cudaError_t attend_t(const Dims& L, PagedArgs a, cudaStream_t s) {
 void carve_paged(Carver& c, const Dims& L, int Q, PagedArgs* a) {
   a->parts = c.take<int2>(Q);
   a->ml = c.take<float2>((size_t)2 * kPagedBlocks * L.H);
+  a->turns = c.take<float2>((size_t)kPagedBlocks * (L.R / 2));
   a->part = c.take<float>((size_t)2 * kPagedBlocks * L.H * L.D);
 }
 

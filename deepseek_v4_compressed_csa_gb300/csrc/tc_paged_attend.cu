@@ -55,14 +55,15 @@ constexpr int kOffMask = kOffScale + kStages * kTile * 4; // [kStages] u64
 constexpr int kOffFac = kOffMask + kStages * 8 + 16;      // [2][64] factors of a group's rescale
 constexpr int kOffRef = kOffFac + 2 * kH * 4;             // [64] R
 constexpr int kOffStat = kOffRef + kH * 4;                // [2][64] float2 (m, l) of the groups
-constexpr int kOffOut = kOffStat + 2 * kH * 8;            // [64] factors of the output
+constexpr int kOffTop = kOffStat + 2 * kH * 8;            // [2][64] the first two tiles' maxima
+constexpr int kOffOut = kOffTop + 2 * kH * 4;             // [64] factors of the output
 constexpr int kOffMax = kOffOut + kH * 4;                 // [2][64] largest magnitudes of the query rows' halves
 constexpr int kOffRope = kOffMax + 2 * kH * 4;            // cos[32], sin[32]
 constexpr int kOffBars = kOffRope + 64 * 4;
 constexpr int kOffTmem = kOffBars + 32 * 8;
-constexpr int kOffPlan = kOffTmem + 32;                   // PagedRun, [warps] sums
-constexpr int kSmem = kOffPlan + (int)sizeof(PagedRun) + 4 * kThreads / 32 + 1024;
-static_assert(kOffBars % 8 == 0 && kOffFac % 16 == 0 && kOffOut % 16 == 0 && kOffPlan % 8 == 0 && kSmem <= 232448, "shared memory");
+constexpr int kOffPlan = kOffTmem + 32;                   // PagedRun, scratch of the plan
+constexpr int kSmem = kOffPlan + (int)sizeof(PagedRun) + 4 * kPlanInts + 1024;
+static_assert(kOffBars % 8 == 0 && kOffFac % 16 == 0 && kOffOut % 16 == 0 && kOffPlan % 16 == 0 && sizeof(PagedRun) % 16 == 0 && kSmem <= 232448, "shared memory");
 
 // 2^x by the hardware approximation (relative error ~2^-22; results below 2^-126 flush to zero)
 __device__ __forceinline__ float ex2(float x) {
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();  // predecessors complete: what they wrote is visible and their tensor memory is free
   PagedRun* plan = reinterpret_cast<PagedRun*>(sm.base + kOffPlan);
-  paged_plan(a, plan, reinterpret_cast<int*>(plan + 1));
+  paged_plan<kThreads / 32>(a, plan, reinterpret_cast<int*>(plan + 1));
   const int t0 = plan->t0, t1 = plan->t1;
   if (t0 >= t1) return;  // (all of the block)
   const int pre0 = plan->pre;
@@ -385,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* fac = reinterpret_cast<float*>(sm.base + kOffFac) + g * kH;
     float* refs = reinterpret_cast<float*>(sm.base + kOffRef);
     float2* stat = reinterpret_cast<float2*>(sm.base + kOffStat);
+    float* top = reinterpret_cast<float*>(sm.base + kOffTop);
     float* fout = reinterpret_cast<float*>(sm.base + kOffOut);
     float* rcos = reinterpret_cast<float*>(sm.base + kOffRope);
     float* rsin = rcos + 32;
@@ -410,13 +412,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t* amax = reinterpret_cast<uint32_t*>(sm.base + kOffMax);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          // the largest magnitude by its bits: bf16 pairs compared as unsigned halves
-          uint32_t mx = 0;
+          __nv_bfloat162 m4[4];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) mx = __vmaxu2(mx, __vmaxu2(v[x][e].x & 0x7fff7fffu, v[x][e].y & 0x7fff7fffu));
-          mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          if ((lane & 3) == 0) amax[g * kH + 16 * quad + r + 8 * x] = max(mx & 0xffffu, mx >> 16);
+          for (int e = 0; e < 16; ++e) {
+            const __nv_bfloat162 u = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[x][e].x)),
+                                                 __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[x][e].y)));
+            m4[e & 3] = e < 4 ? u : __hmax2_nan(m4[e & 3], u);
+          }
+          const __nv_bfloat162 m2 = __hmax2_nan(__hmax2_nan(m4[0], m4[1]), __hmax2_nan(m4[2], m4[3]));
+          uint32_t mx = *reinterpret_cast<const uint32_t*>(&m2) & 0x7fff7fffu;
+          mx = max(mx & 0xffffu, mx >> 16);  // (the bits of magnitudes are ordered as they are, a NaN's above all)
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          if ((lane & 3) == 0) amax[g * kH + 16 * quad + r + 8 * x] = mx;
         }
         if (g == 0 && gt < 32 && a.inv_freq) rope_cs(k.p, a.inv_freq, gt, rcos + gt, rsin + gt);
         tc::named_bar(4, kSoft);
@@ -511,12 +519,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           l += l2;
           vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, 16));
-          // ---- the reference follows log2 of the largest 2^t ks: after the tile before has decided
+          // ---- the reference follows log2 of the largest 2^t ks: the first two tiles find it together, later ones after
+          // the tile before has decided
           const float lv = vt > 0.f ? mr + lg2(vt) : -INFINITY;
-          if (jt > 0) wait(sm, sm.decided + (g ^ 1), ((jt - 1) >> 1) & 1);
-          float ref = i == 0 ? lv + kHead : refs[h];
-          if (i == 0) {
-            if (plane == 0) refs[h] = ref;
+          float ref;
+          if (i < 2 && n > 1) {
+            if (plane == 0) top[i * kH + h] = lv;
+            tc::named_bar(4, kSoft);
+            ref = fmaxf(top[h], top[kH + h]) + kHead;
+          } else if (i == 0) {
+            ref = lv + kHead;
+          } else {
+            wait(sm, sm.decided + (g ^ 1), ((jt - 1) >> 1) & 1);
+            ref = refs[h];
+          }
+          if (i < 2) {
+            if (i == 0 && plane == 0) refs[h] = ref;
           } else if (tc::named_bar_any(2 + g, kGroup, lv > ref + kStep)) {
             const float up = fmaxf(ref, lv);
             // (a head of which nothing but zeros has entered the product needs no factor)
@@ -576,6 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = begin == 0 && end == k.tiles, last = pre + k.tiles >= t1;
       const size_t slot = 2 * blockIdx.x + (begin == 0 ? 1 : 0);
       tc::named_bar(4, kSoft);  // (both groups' statistics, the last R, the angles)
+      if (begin == 0 && !whole && g == 1 && gt < kR / 2 && a.inv_freq)
+        a.turns[blockIdx.x * (kR / 2) + gt] = make_float2(rcos[gt], rsin[gt]);
       if (g == 0 && plane == 0) {
         const float2 s0 = stat[h], s1 = stat[kH + h];
         const float m = fmaxf(s0.x, s1.x), mr = m == -INFINITY ? 0.f : m, ref = refs[h];
