@@ -70,11 +70,13 @@ _COMP_FMT, _ROWS_FMT, _PAGES_FMT = "@4Pi0P", "@3P3iq", "@2P2i"
 
 _lib = None
 _addresses = None  # csrc/checks.c: what _ptrs does, in C
+_plain = None  # csrc/checks.c: whole calls on plain tensors; with the addresses of the library's functions
+_at = {}
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libcsa.so (built by build.py); raises if it is missing."""
-    global _lib, _addresses
+    global _lib, _addresses, _plain
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -148,6 +150,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         _addresses = module.addresses
+        module.setup(torch.float32, torch.uint8, torch.int32, torch._C._cuda_getCurrentRawStream,
+                     torch._C._cuda_getDevice)
+        for name in ("add_norm", "append_pages", "attend_pages"):
+            _at[name] = ctypes.cast(getattr(lib, "csa_" + name), ctypes.c_void_p).value
+        _plain = module
     _lib = lib
     return lib
 
@@ -964,6 +971,14 @@ def add_norm(layer: Layer, x, residual=None, weight=None, group=None, out=None, 
     whole rows (group = X).  Outputs are those given, or new tensors; out=False or residual_out=False leaves that one
     out (the latter also where there is no residual).  residual_out may be x or residual itself, and so may out.  Rows of
     x and residual may be a stride apart.  Returns (out, residual_out, codes, scales) as NormOutputs."""
+    if _plain is not None:
+        code = _plain.add_norm(_at["add_norm"], layer._packed(), layer.dtype, x, residual, weight, group, out,
+                               residual_out, codes, scales, stream)
+        if code is not None:
+            if code:
+                raise CSAError("csa_add_norm", code)
+            return NormOutputs((None if out is False else out, None if residual_out is False else residual_out, codes,
+                                scales))
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise TypeError("x: expected a tensor [.., X]")
     dtype, shape = layer.dtype, x.shape
@@ -1050,6 +1065,13 @@ def append_pages(layer: Layer, rows, pages: Pages, table, pos, n_new=None, weigh
     sequences' tables [B, width]: RMS-normed (norm, with weight fp32 [D] or None), rotated to those positions (inv_freq;
     None: not rotated) and put in 8 bits with a scale per row.  A token of rows is contiguous; tokens and sequences may be
     strides apart.  Returns the device error word tensor."""
+    if _plain is not None:
+        code = _plain.append_pages(_at["append_pages"], layer._packed(), layer.dtype, layer.D, layer.R // 2, rows,
+                                   pages.codes, pages.scales, table, pos, n_new, weight, norm, inv_freq, err, stream)
+        if code is not None:
+            if code:
+                raise CSAError("csa_append_pages", code)
+            return err
     D, i32, f32 = layer.D, torch.int32, torch.float32
     B, T, dev = _tree_dims("rows", rows, (D,))
     if rows.dtype is not layer.dtype:
@@ -1089,6 +1111,14 @@ def attend_pages(layer: Layer, q, pages: Pages, sink, pos, out, token_table=None
     (None: no compressed rows) the rows sel [B, T, topk] with counts n_sel [B, T], or without sel every visible row below
     n_rows [B].  sink fp32 [H] or None; n_new int32 [B]: the queries of each sequence (None: T); inv_freq: out
     [B, T, H, D] is rotated back (None: not).  Returns the device error word tensor."""
+    if _plain is not None:
+        code = _plain.attend_pages(_at["attend_pages"], layer._packed(), layer.dtype, layer.H, layer.D, layer.R // 2,
+                                   layer.topk, q, pages.codes, pages.scales, sink, pos, out, token_table, first,
+                                   row_table, n_rows, sel, n_sel, n_new, inv_freq, ws, err, stream)
+        if code is not None:
+            if code:
+                raise CSAError("csa_attend_pages", code)
+            return err
     dt, i32, f32, H, D = layer.dtype, torch.int32, torch.float32, layer.H, layer.D
     B, T, dev = _tree_dims("q", q, (H, D))
     if token_table is None and row_table is None:

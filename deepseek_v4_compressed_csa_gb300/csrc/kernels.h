@@ -430,7 +430,8 @@ struct PagedArgs {
   float2* ml;                  // [2 blocks][H] their maxima (in powers of two) and sums
   float2* turns;               // [blocks][R / 2] cos, sin of the output's rotation, by the block of the first part
   int cols;                    // dims that a part holds side by side
-  int tile, shift, min_tiles;  // keys a tile; log2 of the rows that lie in one page; the shortest run of tiles
+  int tile, shift, min_tiles;  // keys a tile; log2 of the rows that lie in one page; the shortest piece of a query, in tiles
+  int merge;                   // whether a merge follows (0: min_tiles is so large that no query is split)
   int32_t* err;
 };
 // Blocks (one an SM) that a call is spread over at most.

@@ -142,7 +142,7 @@ __device__ __forceinline__ PagedQuery next_query(const PagedArgs& a, int q) {
 //     the longest query over blocks / queries pieces, and total / (blocks - queries), since ceil(n / L) <= n / L + 1 (128
 //     queries of 11 tiles on 152 blocks stay whole: 29 us; in even runs of 10 tiles 55);
 //   more: L = total / blocks, so only longer queries than that are cut, and block c takes the pieces that begin in
-//     [c, c + 1) total / blocks.  No piece is longer than that, so every block up to the last piece's has one.
+//     [c, c + 1) total / blocks.  No piece of a cut query is longer than that, so all its blocks have one.
 // Every block finds the plan itself (a few loads a query, spread over its threads): a kernel before it would cost more than
 // that for the batches that count in microseconds.
 struct PagedRun {
@@ -258,7 +258,7 @@ __device__ __forceinline__ void paged_plan(const PagedArgs& a, PagedRun* sm, int
     }
     return;
   }
-  const int base = total / G, rem = total - base * G, L = max(1, base);
+  const int base = total / G, rem = total - base * G, L = a.merge ? max(1, base) : max(a.min_tiles, base);
   auto begin = [&](int b) { return b * base + (b * rem + G - 1) / G; };  // ceil(b total / G)
   const int lo = begin(c), hi = begin(c + 1);
   int* run = scratch + 80;

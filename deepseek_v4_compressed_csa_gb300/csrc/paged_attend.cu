@@ -23,7 +23,7 @@ __host__ __device__ constexpr int simt_smem(int D) { return (kSimtTile * (D + kS
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __grid_constant__ PagedArgs a) {
-  pdl_trigger();  // (the merge alone follows, and waits)
+  if (a.merge) pdl_trigger();  // (what follows otherwise finds the outputs written)
   extern __shared__ __align__(16) float sm_pa[];
   __shared__ int s_row[kSimtTile];
   __shared__ __align__(16) int s_plan[kPlanInts];
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
 
 // ---------------------------------------------------------------- merge of split queries
 // With (m_s, l_s, acc_s) of the parts: M = max(z, m_s), Z = 2^{z - M} + sum_s l_s 2^{m_s - M},
-// o = sum_s acc_s 2^{m_s - M} / Z (z the sink in powers of two).  An item is 512 values of a head of a split query, 16 a lane;
+// o = sum_s acc_s 2^{m_s - M} / Z (z the sink in powers of two).  An item is 128 kC values of a head of a split query, 4 kC a lane;
 // `share` warps take its parts in turn.  What the kernel waits for is memory, two round trips (where the parts are; their
 // statistics and the first accumulators together), if it has few enough instructions beside its loads (128 values an item
 // cost 1500 a warp, 8.7 us for 8 queries of 18 parts) and blocks: one started a head of every query cost 8 us on 128 queries
@@ -182,12 +182,12 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
 constexpr int kMergeWarps = 8;
 constexpr int kMergeAhead = 4;  // parts in flight a warp
 
-template <typename T>
+template <typename T, int kC>
 __global__ void __launch_bounds__(32 * kMergeWarps, 2) k_merge_pages(const __grid_constant__ PagedArgs a, int share) {
   // no early trigger: what follows finds the outputs written
   __shared__ int4 s_list[kPagedBlocks];  // split queries: q, block of the first part, parts (at least two of the blocks each)
   __shared__ int s_count[kMergeWarps];
-  __shared__ float4 s_acc[kMergeWarps][128];
+  __shared__ float4 s_acc[kMergeWarps][32 * kC];
   __shared__ float s_wt[kMergeWarps][kPagedBlocks];  // weights of a warp's item's parts
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, Q = a.B * a.T;
@@ -206,31 +206,31 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 2) k_merge_pages(const __gri
     if (at.y > 1) s_list[before + __popc(on & ((1u << lane) - 1))] = make_int4(q0 + tid, at.x, at.y, 0);
     __syncthreads();
   }
-  const int chunks = (a.D + 511) / 512, items = n_split * a.H * chunks, per = kMergeWarps / share;
+  const int chunks = (a.D + 128 * kC - 1) / (128 * kC), items = n_split * a.H * chunks, per = kMergeWarps / share;
   const int first = warp % share;
 #pragma unroll 1
   for (int i0 = blockIdx.x * per; i0 < items; i0 += gridDim.x * per) {
     const int item = min(i0 + warp / share, items - 1);  // (a warp behind the last repeats it)
-    const int hq = item / chunks, lq = hq / a.H, h = hq - lq * a.H, d0 = 512 * (item - hq * chunks) + 4 * lane;
+    const int hq = item / chunks, lq = hq / a.H, h = hq - lq * a.H, d0 = 128 * kC * (item - hq * chunks) + 4 * lane;
     const int4 at = s_list[lq];
     // part s of the query: slot 2 (block + s), the first one the slot behind; a lane's columns: 4 values, 128 apart
     const size_t one = (size_t)a.H * a.D, step = 2 * one * share;
     const float* src = a.part + 2 * one * (at.y + first) + (first == 0 ? one : 0);
-    size_t off[4];
-    bool on[4];
+    size_t off[kC];
+    bool on[kC];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < kC; ++c) {
       const int d = d0 + 128 * c, blk = a.cols == a.D ? 0 : d >> 5;  // (blocks of 32 dims, or all)
       on[c] = d < a.D;
       off[c] = ((size_t)blk * a.H + h) * a.cols + (d - blk * 32);
     }
-    float4 x[kMergeAhead][4];
+    float4 x[kMergeAhead][kC];
     auto fetch = [&](int s0, const float* p) {
 #pragma unroll
       for (int g = 0; g < kMergeAhead; ++g) {
         if (s0 + g * share < at.z) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < kC; ++c)
             if (on[c]) x[g][c] = __ldcg(reinterpret_cast<const float4*>(p + off[c]));
         }
         p += s0 + g * share == 0 ? step - one : step;
@@ -256,9 +256,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 2) k_merge_pages(const __gri
     }
     Z = warp_sum(Z) + (z2 == -INFINITY ? 0.f : exp2f(z2 - M));
     __syncwarp();
-    float4 acc[4];
+    float4 acc[kC];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < kC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (int s0 = first; s0 < at.z; s0 += kMergeAhead * share) {
       if (s0 > first) src = fetch(s0, src);
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 2) k_merge_pages(const __gri
         const float f = s < at.z ? wt[s] : 0.f;
         if (f == 0.f) continue;  // (what a part without keys holds counts for nothing)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kC; ++c) {
           acc[c].x = fmaf(x[g][c].x, f, acc[c].x);
           acc[c].y = fmaf(x[g][c].y, f, acc[c].y);
           acc[c].z = fmaf(x[g][c].z, f, acc[c].z);
@@ -279,19 +279,19 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 2) k_merge_pages(const __gri
     if (share > 1) {
       __syncthreads();  // (the items before have been read)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s_acc[warp][lane + 32 * c] = acc[c];
+      for (int c = 0; c < kC; ++c) s_acc[warp][lane + 32 * c] = acc[c];
       __syncthreads();
       if (first != 0) continue;
       for (int g = 1; g < share; ++g)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kC; ++c) {
           const float4 v = s_acc[warp + g][lane + 32 * c];
           acc[c].x += v.x; acc[c].y += v.y; acc[c].z += v.z; acc[c].w += v.w;
         }
     }
     const float inv = Z == 0.f ? 0.f : 1.f / Z;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < kC; ++c) {
       if (!on[c]) continue;
       const int d = d0 + 128 * c;
       float v[4] = {acc[c].x * inv, acc[c].y * inv, acc[c].z * inv, acc[c].w * inv};
@@ -316,16 +316,37 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 2) k_merge_pages(const __gri
   }
 }
 
-template <typename T>
-cudaError_t launch_merge(const PagedArgs& a, cudaStream_t s) {
-  // few queries have many parts each (about blocks / queries): a warp takes four at a time, more of them share an item
+template <typename T, int kC>
+cudaError_t merge_c(const PagedArgs& a, cudaStream_t s) {
   const int Q = a.B * a.T;
+  // few queries have many parts each (about blocks / queries): a warp takes four at a time, more of them share an item
   int share = 1;
   while (share < kMergeWarps && share * kMergeAhead * Q < kPagedBlocks) share *= 2;
-  const long long items = (long long)min(Q, kPagedBlocks) * a.H * ((a.D + 511) / 512), per = kMergeWarps / share;
-  CSA_LAUNCH(k_merge_pages<T>, dim3((unsigned)min((items + per - 1) / per, 2LL * kPagedBlocks)), dim3(32 * kMergeWarps), 0,
-             s, a, share);
+  const long long items = (long long)min(Q, kPagedBlocks) * a.H * ((a.D + 128 * kC - 1) / (128 * kC)), per = kMergeWarps / share;
+  CSA_LAUNCH((k_merge_pages<T, kC>), dim3((unsigned)min((items + per - 1) / per, 2LL * kPagedBlocks)), dim3(32 * kMergeWarps),
+             0, s, a, share);
   return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_merge(const PagedArgs& a, cudaStream_t s) {
+  // items enough for every SM: a quarter of the Flash row's values for up to four queries
+  return a.D <= 128 || a.B * a.T <= 4 ? merge_c<T, 1>(a, s) : merge_c<T, 4>(a, s);
+}
+
+// Whether queries are short enough to stay whole, by what the call's sizes say: then no merge follows.  Splitting them pays
+// while there are blocks to spare and more tiles to share out than the merge costs (some 5 us, six tiles' time): one query
+// of 11 tiles 17.4 us split and 20 whole, one of 3 tiles 17 and 14.
+bool stay_whole(PagedArgs* a) {
+  const int Q = a->B * a->T, u = 1 << a->shift;
+  if (a->row_table && !a->sel) return false;
+  long long most = a->sel ? (a->topk + a->tile - 1) / a->tile : 0;
+  if (a->token_table) {
+    const long long room = (long long)a->token_pages * a->P, f = a->first < room ? a->first : room, w = a->W < room ? a->W : room;
+    most += ((f + u - 1) / u + (w + u - 1) / u + 1 + (a->tile >> a->shift) - 1) / (a->tile >> a->shift);
+  }
+  if (most > (2 * Q < kPagedBlocks ? 4 : 16)) return false;
+  a->min_tiles = (int)most;
+  return true;
 }
 
 template <typename T>
@@ -336,6 +357,7 @@ cudaError_t attend_t(const Dims& L, PagedArgs a, cudaStream_t s) {
     a.shift = 3;  // the largest power of two that divides a page, at most a tile
     while (a.shift < 6 && a.P % (2 << a.shift) == 0) ++a.shift;
     a.cols = 32;
+    a.merge = !stay_whole(&a);
     const cudaError_t e = launch_tc_paged(a, s);
     if (e != cudaSuccess) return e;
   } else {
@@ -343,10 +365,11 @@ cudaError_t attend_t(const Dims& L, PagedArgs a, cudaStream_t s) {
     a.tile = kSimtTile;
     a.shift = 0;
     a.cols = a.D;
+    a.merge = !stay_whole(&a);
     allow_smem<kSimtSmemMax>(k_attend_pages_simt<T>);
     CSA_LAUNCH(k_attend_pages_simt<T>, dim3(kPagedBlocks), dim3(32 * kSimtWarps), simt_smem(a.D), s, a);
   }
-  return launch_merge<T>(a, s);
+  return a.merge ? launch_merge<T>(a, s) : cudaSuccess;
 }
 
 }  // namespace

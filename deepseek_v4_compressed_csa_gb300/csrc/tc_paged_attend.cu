@@ -130,7 +130,7 @@ __device__ __forceinline__ bool warp_wait(const Smem& sm, uint64_t* bar, uint32_
 
 __global__ void __launch_bounds__(kThreads, 1)
     k_tc_attend_pages(const __grid_constant__ CUtensorMap tm_runs, const __grid_constant__ PagedArgs a) {
-  pdl_trigger();  // (the merge alone follows, and waits)
+  if (a.merge) pdl_trigger();  // (what follows otherwise finds the outputs written)
   extern __shared__ uint8_t smem_raw[];
   Smem sm;
   sm.base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
