@@ -704,6 +704,8 @@ csa_status csa_attend_pages(const csa_layer* layer, const csa_pages* pages, cons
   a.pos = pos; a.n_new = n_new; a.token_table = token_table; a.row_table = row_table; a.n_rows = n_rows;
   a.sel = sel; a.n_sel = n_sel;
   a.by_page = fast_div((uint32_t)pages->page_rows);
+  a.by_T = fast_div((uint32_t)T);
+  a.by_ratio = fast_div((uint32_t)L.ratio);
   a.n_pages = pages->n_pages; a.P = pages->page_rows; a.token_pages = token_width; a.row_pages = row_width;
   a.B = B; a.T = T; a.H = L.H; a.D = L.D; a.R = L.R; a.W = L.W; a.first = first; a.ratio = L.ratio; a.topk = L.topk;
   a.scale2 = L.scale * 1.4426950408889634f;

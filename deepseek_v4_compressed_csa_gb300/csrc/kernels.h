@@ -420,7 +420,7 @@ struct PagedArgs {
   void* out;                   // [B, T, H, D]
   const float *sink, *inv_freq;  // either may be null
   const int32_t *pos, *n_new, *token_table, *row_table, *n_rows, *sel, *n_sel;
-  FastDiv by_page;             // division by P
+  FastDiv by_page, by_T, by_ratio;  // division by P, T, ratio
   int n_pages, P, token_pages, row_pages;  // the pool's pages, rows a page, and the tables' widths
   int B, T, H, D, R, W, first, ratio, topk;
   float scale2;                // softmax scale * log2(e)

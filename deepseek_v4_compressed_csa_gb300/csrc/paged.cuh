@@ -37,14 +37,31 @@ __device__ __forceinline__ float inv_rms(float inv_n, float eps, Sum sum) {
   constexpr float f = 5.42101086242752217e-20f;  // 2^-64
   return rsqrtf(fmaf(sum(f), inv_n, eps * f * f)) * f;
 }
+// cos and sin of theta = (float)p * inv_freq[i] (one fp32 product, as in rope_cs).  Far positions: by theta's remainder to
+// the nearest multiple of pi / 2, in fp64 with pi / 2 as the sum of two doubles (right to fp32): sincosf's own reduction of
+// angles above 10^5 cost a warp of the attention 5K clocks.
+__device__ __forceinline__ void turn_cs(int p, const float* inv_freq, int i, float* c, float* s) {
+  const float th = __fmul_rn((float)p, __ldg(inv_freq + i));
+  const bool far = fabsf(th) > 1e5f && fabsf(th) < 536870912.f;
+  float r = th, sr, cr;
+  int n = 0;
+  if (far) {
+    const double k = rint((double)th * 0.63661977236758134308);
+    r = (float)fma(-k, 6.123233995736766036e-17, fma(-k, 1.5707963267948966192, (double)th));
+    n = (int)k & 3;
+  }
+  sincosf(r, &sr, &cr);
+  const float x = n & 1 ? sr : cr, y = n & 1 ? cr : sr;
+  *c = n == 1 || n == 2 ? -x : x;
+  *s = n & 2 ? -y : y;
+}
 // v / s rounded once, 0 where the scale is 0 (a row of zeros, or so small that amax / 448 is)
 __device__ __forceinline__ float over_scale(float v, float s) { return s == 0.f ? 0.f : __fdiv_rn(v, s); }
 
 // ---------------------------------------------------------------- the queries of a call and their keys
+__device__ __forceinline__ int divided(const FastDiv& d, int n) { return (int)((__umulhi(d.m, (uint32_t)n) + (uint32_t)n) >> d.l); }
 // The page of a table that logical row j lies in
-__device__ __forceinline__ int page_of(const PagedArgs& a, int j) {
-  return (int)((__umulhi(a.by_page.m, (uint32_t)j) + (uint32_t)j) >> a.by_page.l);
-}
+__device__ __forceinline__ int page_of(const PagedArgs& a, int j) { return divided(a.by_page, j); }
 // Physical row of logical row j of a sequence's table, -1 where the table names no page of the pool.
 __device__ __forceinline__ int paged_row(const PagedArgs& a, const int32_t* __restrict__ table, int j) {
   const int k = page_of(a, j), page = __ldg(table + k);
@@ -81,7 +98,7 @@ __device__ __forceinline__ TileCut cut_tiles(bool selected, const PagedQuery& k,
 // report: raise the error bits of what is wrong with query q
 __device__ __forceinline__ PagedQuery find_query(const PagedArgs& a, int q, bool report) {
   PagedQuery k;
-  const int b = q / a.T, i = q - b * a.T;
+  const int b = divided(a.by_T, q), i = q - b * a.T;
   // (all at once: one round trip)
   const int p0 = a.pos[b], n = a.n_new ? a.n_new[b] : a.T, rows = a.row_table ? a.n_rows[b] : 0, ns = a.sel ? a.n_sel[q] : 0;
   const bool ok = p0 >= 0 && p0 <= INT32_MAX - a.T && n >= 0 && n <= a.T;
@@ -100,7 +117,7 @@ __device__ __forceinline__ PagedQuery find_query(const PagedArgs& a, int q, bool
         k.n0 = min(max(ns, 0), a.topk);
         k.n_rows = min(k.n_rows, held);  // (a selected row behind the table's end is out of range)
       } else {
-        k.n0 = min(k.n_rows, (int)(((unsigned)k.p + 1u) / (unsigned)a.ratio));
+        k.n0 = min(k.n_rows, divided(a.by_ratio, k.p + 1));
         if (k.n0 > held) {
           bits |= CSA_DEV_CAPACITY;
           k.n0 = held;
@@ -194,11 +211,53 @@ struct Pieces {
   }
 };
 
+// The length of pieces where every piece gets a block of its own (queries < kPagedBlocks)
+__device__ __forceinline__ int piece_length(const PagedArgs& a, int total, int queries, int longest) {
+  const int each = (int)((float)kPagedBlocks / (float)max(queries, 1));  // (rounded right: whole quotients are exact)
+  return max(max(a.min_tiles, (int)div_up(total, kPagedBlocks)),
+             min((int)div_up(longest, each), (int)div_up(total, kPagedBlocks - queries)));
+}
+
+// Up to 32 queries, by one warp (the others wait at the barrier at its end): a third of the instructions of the plan below,
+// which a launch has to fetch before it runs them.
+__device__ __forceinline__ void paged_plan_warp(const PagedArgs& a, PagedRun* sm) {
+  const int Q = a.B * a.T, lane = threadIdx.x, c = blockIdx.x;
+  if (threadIdx.x < 32) {
+    PagedQuery k;
+    k.tiles = 0;
+    if (lane < Q) k = find_query(a, lane, c == 0);
+    const int n = k.tiles;
+    const int total = __reduce_add_sync(0xffffffffu, n), queries = __popc(__ballot_sync(0xffffffffu, n > 0));
+    const int L = piece_length(a, total, queries, __reduce_max_sync(0xffffffffu, n));
+    const Pieces p(n, (int)div_up(n, L));
+    int first = p.m, pre = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, first, o), v = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) {
+        first += u;
+        pre += v;
+      }
+    }
+    const int pieces = __shfl_sync(0xffffffffu, first, 31), i = c - (first - p.m);
+    pre -= n;
+    if (i >= 0 && i < p.m) {
+      sm->t0 = pre + p.start(i);
+      sm->t1 = pre + p.start(i + 1);
+      sm->pre = pre;
+      sm->k = k;
+    }
+    if (c >= pieces && lane == 0) sm->t0 = sm->t1 = 0;
+    if (c == 0 && lane < Q) a.parts[lane] = make_int2(first - p.m, p.m);
+  }
+  __syncthreads();
+}
+
 // Whole block of 32 nw threads (nw a multiple of 4); `sm` in shared memory is the result.
 template <int nw>
-__device__ __forceinline__ void paged_plan(const PagedArgs& a, PagedRun* sm, int* scratch) {
+__device__ __noinline__ void paged_plan_block(const PagedArgs& a, PagedRun* sm, int* scratch) {
   constexpr int nt = 32 * nw;
-  const int Q = a.B * a.T, tid = threadIdx.x, G = gridDim.x, c = blockIdx.x;
+  const int Q = a.B * a.T, tid = threadIdx.x, G = kPagedBlocks, c = blockIdx.x;
   const int each = (Q + nt - 1) / nt, q0 = min(Q, tid * each), q1 = min(Q, q0 + each);
   const bool lead = c == 0;
   int mine = 0, live = 0, longest = 0;
@@ -225,8 +284,7 @@ __device__ __forceinline__ void paged_plan(const PagedArgs& a, PagedRun* sm, int
   for (int w = 0; w < nw; ++w) longest = max(longest, scratch[32 + w]);
   int t0 = total, t1 = total;  // (a block behind the last piece has nothing)
   if (queries < G) {
-    const int L = max(max(a.min_tiles, (int)div_up(total, G)),
-                      min((int)div_up(longest, queries > 0 ? G / queries : 1), (int)div_up(total, G - queries)));
+    const int L = piece_length(a, total, queries, longest);
     // (each is 1 but for batches of some hundred slots of which few are in use)
     int count = 0;
     for (int q = q0; q < q1; ++q) {
@@ -300,6 +358,12 @@ __device__ __forceinline__ void paged_plan(const PagedArgs& a, PagedRun* sm, int
     sm->t1 = t1;
   }
   __syncthreads();
+}
+
+template <int nw>
+__device__ __forceinline__ void paged_plan(const PagedArgs& a, PagedRun* sm, int* scratch) {
+  if (a.B * a.T <= 32) paged_plan_warp(a, sm);
+  else paged_plan_block<nw>(a, sm, scratch);
 }
 
 }  // namespace csa

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
     if (begin == 0 && !whole && a.inv_freq)  // (for the merge: an angle costs a lane some hundred instructions)
       for (int i = tid; i < a.R / 2; i += blockDim.x) {
         float2 t;
-        rope_cs(k.p, a.inv_freq, i, &t.x, &t.y);
+        turn_cs(k.p, a.inv_freq, i, &t.x, &t.y);
         a.turns[(size_t)blockIdx.x * (a.R / 2) + i] = t;
       }
 #pragma unroll 1
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
             float cs, sn;
-            rope_cs(k.p, a.inv_freq, (d + e - (D - a.R)) >> 1, &cs, &sn);
+            turn_cs(k.p, a.inv_freq, (d + e - (D - a.R)) >> 1, &cs, &sn);
             const float x0 = v[e], x1 = v[e + 1];
             v[e] = fmaf(x0, cs, x1 * sn);
             v[e + 1] = fmaf(-x0, sn, x1 * cs);

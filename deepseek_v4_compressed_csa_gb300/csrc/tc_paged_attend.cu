@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (a.merge) pdl_trigger();  // (what follows otherwise finds the outputs written)
   extern __shared__ uint8_t smem_raw[];
   Smem sm;
-  sm.base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  sm.base = smem_raw + (-tc::smem_u32(smem_raw) & 1023u);  // (by an offset: the accesses stay shared-memory ones)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm.base + kOffBars);
   sm.full = bars;
   sm.empty = bars + kStages;
@@ -426,27 +426,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           if ((lane & 3) == 0) amax[g * kH + 16 * quad + r + 8 * x] = mx;
         }
-        if (g == 0 && gt < 32 && a.inv_freq) rope_cs(k.p, a.inv_freq, gt, rcos + gt, rsin + gt);
+        if (g == 0 && gt < 32 && a.inv_freq) turn_cs(k.p, a.inv_freq, gt, rcos + gt, rsin + gt);
         tc::named_bar(4, kSoft);
         // 2^-e with e = exponent - 7: values below 2^8, exact products; a row of denormals, or zeros, stays small; a row that
         // holds an infinity or a NaN becomes NaN (by its product with 0, and its scores by their factor)
         auto expo = [&](int hh) { return max((int)(max(amax[hh], amax[kH + hh]) >> 7), 8); };
-        uint32_t hi[32], lo[32];
+        float inv[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int be = expo(16 * quad + r + 8 * x);
-          const float inv = be == 255 ? 0.f : __uint_as_float((uint32_t)(261 - be) << 23);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float x0 = __uint_as_float(v[x][e].x << 16) * inv, x1 = __uint_as_float(v[x][e].x & 0xffff0000u) * inv;
-            const float x2 = __uint_as_float(v[x][e].y << 16) * inv, x3 = __uint_as_float(v[x][e].y & 0xffff0000u) * inv;
-            hi[2 * e + x] = e4m3x4(x0, x1, x2, x3);
-            const float2 b0 = e4m3x2_f(hi[2 * e + x]), b1 = e4m3x2_f(hi[2 * e + x] >> 16);
-            lo[2 * e + x] = e4m3x4((x0 - b0.x) * 16.f, (x1 - b0.y) * 16.f, (x2 - b1.x) * 16.f, (x3 - b1.y) * 16.f);
-          }
+          inv[x] = be == 255 ? 0.f : __uint_as_float((uint32_t)(261 - be) << 23);
         }
-        tc::tmem_st_16x64(tmem + kColQ + 64 * g + lanes, hi);
-        tc::tmem_st_16x64(tmem + kColQ + 64 * g + lanes + (16u << 16), lo);
+        // (four rounds of the same code, the values moved up in between: unrolled, its 15 KB of instructions arrive behind
+        // the keys that every SM is fetching: 9.5K clocks in the largest batch, 3K by itself)
+#pragma unroll 1
+        for (int round = 0; round < 4; ++round) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x0 = __uint_as_float(v[x][e].x << 16) * inv[x], x1 = __uint_as_float(v[x][e].x & 0xffff0000u) * inv[x];
+              const float x2 = __uint_as_float(v[x][e].y << 16) * inv[x], x3 = __uint_as_float(v[x][e].y & 0xffff0000u) * inv[x];
+              hi[2 * e + x] = e4m3x4(x0, x1, x2, x3);
+              const float2 b0 = e4m3x2_f(hi[2 * e + x]), b1 = e4m3x2_f(hi[2 * e + x] >> 16);
+              lo[2 * e + x] = e4m3x4((x0 - b0.x) * 16.f, (x1 - b0.y) * 16.f, (x2 - b1.x) * 16.f, (x3 - b1.y) * 16.f);
+            }
+#pragma unroll
+            for (int e = 0; e < 12; ++e) v[x][e] = v[x][e + 4];
+          }
+          const uint32_t col = tmem + kColQ + 64 * g + 16 * round + lanes;
+          tc::tmem_st_16x16(col, hi);
+          tc::tmem_st_16x16(col + (16u << 16), lo);
+        }
         tc::tmem_wait_st();
         tc::fence_before_sync();
         tc::mbar_arrive(sm.q_ready);
