@@ -50,7 +50,9 @@ constexpr float kStep = 4.f;                  // how far a maximum may pass R
 constexpr float kHead = 2.f;                  // how far R is set above the first tile's maximum: most grow a little
 
 constexpr int kOffP = kStages * kStage;
-constexpr int kOffScale = kOffP + 2 * kPBuf;              // [kStages][64]
+constexpr int kTurn = 16 * (256 + 16);                    // a group's buffer for outputs: 16 heads x 128 dims
+constexpr int kOffTurn = kOffP + 2 * kPBuf;
+constexpr int kOffScale = kOffTurn + 2 * kTurn;           // [kStages][64]
 constexpr int kOffMask = kOffScale + kStages * kTile * 4; // [kStages] u64
 constexpr int kOffFac = kOffMask + kStages * 8 + 16;      // [2][64] factors of a group's rescale
 constexpr int kOffRef = kOffFac + 2 * kH * 4;             // [64] R
@@ -504,12 +506,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 32; ++e)
               if (!(on >> e & 1u)) s[e] = -INFINITY;
             // rows that are no keys hold whatever their page does: zeros, before the product would meet a NaN among them
-            for (int e = gt; e < kTile * 32; e += kGroup) {
-              const int r = e >> 5;
-              if (!(mask64 >> r & 1ull))
-                *reinterpret_cast<uint4*>(sm.base + st * kStage + ((e & 31) >> 3) * kBox + r * 128 + (e & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            }
+            uint8_t* z = sm.base + st * kStage + ((gt & 31) >> 3) * kBox + (gt & 7) * 16;  // a warp a row
+#pragma unroll 4
+            for (int r = gt >> 5; r < kTile; r += 4)
+              if (!((uint32_t)(mask64 >> (r & 32)) >> (r & 31) & 1u)) *reinterpret_cast<uint4*>(z + r * 128) = make_uint4(0u, 0u, 0u, 0u);
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) mt = fmaxf(mt, s[e]);
@@ -601,8 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (plane == 0) stat[g * kH + h] = make_float2(m, l);
       }
       j += n;
-      // ---- the run's part of this query, or its output, through shared memory: the probabilities' buffers, or, behind the
-      // block's last tile, the stages, which hold all of it at once
+      // ---- the run's part of this query, or its output, through shared memory: small buffers, or, behind the block's last
+      // tile, the stages, which hold all of it at once
       const bool whole = begin == 0 && end == k.tiles, last = pre + k.tiles >= t1;
       const size_t slot = 2 * blockIdx.x + (begin == 0 ? 1 : 0);
       tc::named_bar(4, kSoft);  // (both groups' statistics, the last R, the angles)
@@ -628,49 +628,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_after_sync();
       tc::named_bar(4, kSoft);
       if (whole) {
-        // 32 heads x 128 dims of bf16 a step; dims in lanes: two heads at a time, even lanes hold head e's pair of dims, odd
-        // lanes head e + 1's
-        const int odd = lane & 1, dp = 32 * quad + lane - odd;
+        // 16 heads x 128 dims of bf16 a step: accumulators as 8 x 8 tiles (dims x heads), which stmatrix turns.  A head's row
+        // is 16 bytes longer than its values, so that a tile's eight rows lie in different banks.
+        const int r = lane >> 2, c2 = 2 * (lane & 3), pitch = last ? 2 * kD + 16 : 256 + 16;
 #pragma unroll 1
-        for (int c = g; c < 8; c += 2) {
-          const int blk = c >> 1, h0 = 32 * (c & 1), ri = (128 * blk + dp - (kD - kR)) >> 1;
-          // a head's 128 values: 256 bytes apart, or, in the stages, where they are in the output
-          uint8_t* buf = last ? sm.base + h0 * (2 * kD) + 256 * blk : pbuf;
-          const int pitch = last ? 2 * kD : 256;
-          uint32_t x[32];
-          tc::tmem_ld32(tmem + kColO + 64 * blk + h0 + lanes, x);
+        for (int u = 0; u < 8; ++u) {
+          const int blk = 2 * g + (u >> 2), h0 = 16 * (u & 3);
+          uint32_t x[2][8];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) tc::tmem_ld_16x16(tmem + kColO + 64 * blk + h0 + lanes + ((uint32_t)(16 * hf) << 16), x[hf]);
           tc::tmem_wait_ld();
-          const bool turn = ri >= 0 && a.inv_freq;
-          const float cs = turn ? rcos[ri] : 1.f, sn = turn ? rsin[ri] : 0.f;
-          if (!last && c != g) {
-            if (gt < 32) tc::bulk_wait_read();
+          if (!last && u > 0) {
+            if (gt < 16) tc::bulk_wait_read();
             tc::named_bar(2 + g, kGroup);
           }
+          uint8_t* buf = last ? sm.base + h0 * pitch + 256 * blk : sm.base + kOffTurn + g * kTurn;
+          const uint32_t dst = tc::smem_u32(buf) + (lane & 7) * pitch + 64 * quad + 16 * (lane >> 3);
+          const bool turn = blk == 3 && quad >= 2 && a.inv_freq;
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 f2 = *reinterpret_cast<const float2*>(fout + h0 + e);
-            const float v0 = __uint_as_float(x[e]) * f2.x, v1 = __uint_as_float(x[e + 1]) * f2.y;
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-            float y0 = odd ? got : v0, y1 = odd ? v1 : got;
-            if (turn) {
-              const float z0 = y0;
-              y0 = fmaf(z0, cs, y1 * sn);
-              y1 = fmaf(-z0, sn, y1 * cs);
+          for (int n8 = 0; n8 < 2; ++n8) {
+            const float2 f2 = *reinterpret_cast<const float2*>(fout + h0 + 8 * n8 + c2);
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // dims 8 i .. of the warp's 32
+              float v0 = __uint_as_float(x[i >> 1][4 * n8 + 2 * (i & 1)]) * f2.x;
+              float v1 = __uint_as_float(x[i >> 1][4 * n8 + 2 * (i & 1) + 1]) * f2.y;
+              if (turn) {  // the pair's other dim is four lanes on
+                const int ri = (32 * (quad - 2) + 8 * i + r) >> 1;
+                const float cs = rcos[ri], sn = r & 1 ? -rsin[ri] : rsin[ri];
+                const float o0 = __shfl_xor_sync(0xffffffffu, v0, 4), o1 = __shfl_xor_sync(0xffffffffu, v1, 4);
+                v0 = fmaf(v0, cs, o0 * sn);
+                v1 = fmaf(v1, cs, o1 * sn);
+              }
+              const __nv_bfloat162 w = __floats2bfloat162_rn(v0, v1);
+              y[i] = *reinterpret_cast<const uint32_t*>(&w);
             }
-            *reinterpret_cast<__nv_bfloat162*>(buf + (e + odd) * pitch + dp * 2) = __floats2bfloat162_rn(y0, y1);
+            tc::stmatrix_x4_trans(dst + 8 * n8 * pitch, y);
           }
-          tc::fence_proxy_async_smem();
           if (last) continue;
+          tc::fence_proxy_async_smem();
           tc::named_bar(2 + g, kGroup);
-          if (gt < 32) {
-            tc::bulk_store(static_cast<__nv_bfloat16*>(a.out) + ((size_t)k.q * kH + h0 + gt) * kD + 128 * blk, pbuf + gt * 256, 256);
+          if (gt < 16) {
+            tc::bulk_store(static_cast<__nv_bfloat16*>(a.out) + ((size_t)k.q * kH + h0 + gt) * kD + 128 * blk, buf + gt * pitch, 256);
             tc::bulk_commit();
           }
         }
         if (last) {
+          tc::fence_proxy_async_smem();
           tc::named_bar(4, kSoft);
-          if (g == 0 && gt < 8) {
-            tc::bulk_store(static_cast<uint8_t*>(a.out) + (size_t)k.q * kH * kD * 2 + gt * 8192, sm.base + gt * 8192, 8192);
+          if (gt < 32) {
+            const int row = 32 * g + gt;
+            tc::bulk_store(static_cast<__nv_bfloat16*>(a.out) + ((size_t)k.q * kH + row) * kD, sm.base + row * pitch, 2 * kD);
             tc::bulk_commit();
           }
         }
