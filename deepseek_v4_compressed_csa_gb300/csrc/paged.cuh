@@ -37,18 +37,25 @@ __device__ __forceinline__ float inv_rms(float inv_n, float eps, Sum sum) {
   constexpr float f = 5.42101086242752217e-20f;  // 2^-64
   return rsqrtf(fmaf(sum(f), inv_n, eps * f * f)) * f;
 }
-// cos and sin of theta = (float)p * inv_freq[i] (one fp32 product, as in rope_cs).  Far positions: by theta's remainder to
-// the nearest multiple of pi / 2, in fp64 with pi / 2 as the sum of two doubles (right to fp32): sincosf's own reduction of
-// angles above 10^5 cost a warp of the attention 5K clocks.
+// cos and sin of theta = (float)p * inv_freq[i] (one fp32 product, as in rope_cs).  Far positions: theta = m 2^e as a fraction
+// of a turn, m 2^e / 2 pi modulo 1, in 64-bit fixed point (M. H. Payne and R. N. Hanek, Radian Reduction for Trigonometric
+// Functions; one word of 1 / 2 pi is enough up to theta = 2^29, off by less than 2^-35 turns), and from it the remainder to
+// the nearest quarter turn: sincosf's own reduction of angles above 10^5 cost a warp of the attention 5K clocks, one in fp64
+// nearly as much.
 __device__ __forceinline__ void turn_cs(int p, const float* inv_freq, int i, float* c, float* s) {
-  const float th = __fmul_rn((float)p, __ldg(inv_freq + i));
-  const bool far = fabsf(th) > 1e5f && fabsf(th) < 536870912.f;
+  const float th = __fmul_rn((float)p, __ldg(inv_freq + i)), mag = fabsf(th);
   float r = th, sr, cr;
   int n = 0;
-  if (far) {
-    const double k = rint((double)th * 0.63661977236758134308);
-    r = (float)fma(-k, 6.123233995736766036e-17, fma(-k, 1.5707963267948966192, (double)th));
-    n = (int)k & 3;
+  if (mag > 1e5f && mag < 536870912.f) {
+    const uint32_t bits = __float_as_uint(mag);
+    const int e = (int)(bits >> 23) - 150;  // -7 .. 5
+    const uint64_t m = (bits & 0x7fffffu) | 0x800000u, f = 0x28be60db9391054aull;  // f: 2^64 / 2 pi
+    const uint64_t lo = m * f, hi = __umul64hi(m, f);
+    uint64_t u = e >= 0 ? lo << e : (lo >> -e) | (hi << (64 + e));
+    if (th < 0.f) u = 0 - u;
+    const uint64_t quarter = (u + (1ull << 61)) >> 62;
+    n = (int)quarter & 3;
+    r = (float)(int64_t)(u - (quarter << 62)) * 3.4061215800304e-19f;  // 2 pi / 2^64
   }
   sincosf(r, &sr, &cr);
   const float x = n & 1 ? sr : cr, y = n & 1 ? cr : sr;

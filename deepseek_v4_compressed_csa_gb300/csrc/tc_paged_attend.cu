@@ -50,7 +50,7 @@ constexpr float kStep = 4.f;                  // how far a maximum may pass R
 constexpr float kHead = 2.f;                  // how far R is set above the first tile's maximum: most grow a little
 
 constexpr int kOffP = kStages * kStage;
-constexpr int kTurn = 16 * (256 + 16);                    // a group's buffer for outputs: 16 heads x 128 dims
+constexpr int kTurn = 16 * 256;                           // a group's buffer for outputs: 16 heads x 128 dims
 constexpr int kOffTurn = kOffP + 2 * kPBuf;
 constexpr int kOffScale = kOffTurn + 2 * kTurn;           // [kStages][64]
 constexpr int kOffMask = kOffScale + kStages * kTile * 4; // [kStages] u64
@@ -65,7 +65,7 @@ constexpr int kOffBars = kOffRope + 64 * 4;
 constexpr int kOffTmem = kOffBars + 32 * 8;
 constexpr int kOffPlan = kOffTmem + 32;                   // PagedRun, scratch of the plan
 constexpr int kSmem = kOffPlan + (int)sizeof(PagedRun) + 4 * kPlanInts + 1024;
-static_assert(kOffBars % 8 == 0 && kOffFac % 16 == 0 && kOffOut % 16 == 0 && kOffPlan % 16 == 0 && sizeof(PagedRun) % 16 == 0 && kSmem <= 232448, "shared memory");
+static_assert(kOffBars % 8 == 0 && kOffTurn % 1024 == 0 && kOffFac % 16 == 0 && kOffOut % 16 == 0 && kOffPlan % 16 == 0 && sizeof(PagedRun) % 16 == 0 && kSmem <= 232448, "shared memory");
 
 // 2^x by the hardware approximation (relative error ~2^-22; results below 2^-126 flush to zero)
 __device__ __forceinline__ float ex2(float x) {
@@ -131,7 +131,8 @@ __device__ __forceinline__ bool warp_wait(const Smem& sm, uint64_t* bar, uint32_
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    k_tc_attend_pages(const __grid_constant__ CUtensorMap tm_runs, const __grid_constant__ PagedArgs a) {
+    k_tc_attend_pages(const __grid_constant__ CUtensorMap tm_runs, const __grid_constant__ CUtensorMap tm_out16,
+                      const __grid_constant__ CUtensorMap tm_out64, const __grid_constant__ PagedArgs a) {
   if (a.merge) pdl_trigger();  // (what follows otherwise finds the outputs written)
   extern __shared__ uint8_t smem_raw[];
   Smem sm;
@@ -155,6 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     tc::tma_prefetch(&tm_runs);
+    tc::tma_prefetch(&tm_out64);
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(sm.full + i, 1 + 32);  // the copies, and the loader's lanes for the scales (or all they copy)
       tc::mbar_init(sm.empty + i, 1);
@@ -628,9 +630,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_after_sync();
       tc::named_bar(4, kSoft);
       if (whole) {
-        // 16 heads x 128 dims of bf16 a step: accumulators as 8 x 8 tiles (dims x heads), which stmatrix turns.  A head's row
-        // is 16 bytes longer than its values, so that a tile's eight rows lie in different banks.
-        const int r = lane >> 2, c2 = 2 * (lane & 3), pitch = last ? 2 * kD + 16 : 256 + 16;
+        // 16 heads x 128 dims of bf16 a step: accumulators as 8 x 8 tiles (dims x heads), which stmatrix turns, into boxes of
+        // 64 dims in the 128-byte swizzle (a head's row 128 bytes) that go out by one copy each: of 64 heads at the end, of
+        // 16 on the way.  (A copy a head, 1 KB each, cost 4K clocks: a lane's copies are issued one after another.)
+        const int r = lane >> 2, c2 = 2 * (lane & 3), chunk = 4 * (quad & 1) + (lane >> 3), h8 = lane & 7;
 #pragma unroll 1
         for (int u = 0; u < 8; ++u) {
           const int blk = 2 * g + (u >> 2), h0 = 16 * (u & 3);
@@ -639,11 +642,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int hf = 0; hf < 2; ++hf) tc::tmem_ld_16x16(tmem + kColO + 64 * blk + h0 + lanes + ((uint32_t)(16 * hf) << 16), x[hf]);
           tc::tmem_wait_ld();
           if (!last && u > 0) {
-            if (gt < 16) tc::bulk_wait_read();
+            if (gt < 2) tc::bulk_wait_read();
             tc::named_bar(2 + g, kGroup);
           }
-          uint8_t* buf = last ? sm.base + h0 * pitch + 256 * blk : sm.base + kOffTurn + g * kTurn;
-          const uint32_t dst = tc::smem_u32(buf) + (lane & 7) * pitch + 64 * quad + 16 * (lane >> 3);
+          uint8_t* turned = sm.base + kOffTurn + g * kTurn;
+          uint8_t* box = last ? sm.base + (2 * blk + (quad >> 1)) * (kH * 128) + h0 * 128 : turned + (quad >> 1) * (16 * 128);
+          const uint32_t dst = tc::smem_u32(box) + h8 * 128 + ((chunk ^ h8) << 4);
           const bool turn = blk == 3 && quad >= 2 && a.inv_freq;
 #pragma unroll
           for (int n8 = 0; n8 < 2; ++n8) {
@@ -663,22 +667,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               const __nv_bfloat162 w = __floats2bfloat162_rn(v0, v1);
               y[i] = *reinterpret_cast<const uint32_t*>(&w);
             }
-            tc::stmatrix_x4_trans(dst + 8 * n8 * pitch, y);
+            tc::stmatrix_x4_trans(dst + 8 * n8 * 128, y);
           }
           if (last) continue;
           tc::fence_proxy_async_smem();
           tc::named_bar(2 + g, kGroup);
-          if (gt < 16) {
-            tc::bulk_store(static_cast<__nv_bfloat16*>(a.out) + ((size_t)k.q * kH + h0 + gt) * kD + 128 * blk, buf + gt * pitch, 256);
+          if (gt < 2) {
+            tc::tma_store_2d(&tm_out16, turned + gt * (16 * 128), 128 * blk + 64 * gt, k.q * kH + h0);
             tc::bulk_commit();
           }
         }
         if (last) {
           tc::fence_proxy_async_smem();
-          tc::named_bar(4, kSoft);
-          if (gt < 32) {
-            const int row = 32 * g + gt;
-            tc::bulk_store(static_cast<__nv_bfloat16*>(a.out) + ((size_t)k.q * kH + row) * kD, sm.base + row * pitch, 2 * kD);
+          tc::named_bar(2 + g, kGroup);
+          if (lane == 0) {
+            const int bx = 4 * g + quad;
+            tc::tma_store_2d(&tm_out64, sm.base + bx * (kH * 128), 64 * bx, k.q * kH);
             tc::bulk_commit();
           }
         }
@@ -753,10 +757,13 @@ bool tc_paged_supported(const Dims& L, int P) {
 
 cudaError_t launch_tc_paged(const PagedArgs& a, cudaStream_t s) {
   const uint64_t rows = (uint64_t)a.n_pages * a.P;
-  CUtensorMap tm_runs;
-  if (!make_tmap_2d_u8(&tm_runs, a.codes, rows, kD, kD, 128, 1u << a.shift, true)) return cudaErrorInvalidValue;
+  const uint64_t heads = (uint64_t)a.B * a.T * kH;
+  CUtensorMap tm_runs, tm_out16, tm_out64;
+  if (!make_tmap_2d_u8(&tm_runs, a.codes, rows, kD, kD, 128, 1u << a.shift, true) ||
+      !make_tmap_2d_bf16(&tm_out16, a.out, heads, kD, 2 * kD, 16) || !make_tmap_2d_bf16(&tm_out64, a.out, heads, kD, 2 * kD, kH))
+    return cudaErrorInvalidValue;
   allow_smem<kSmem>(k_tc_attend_pages);
-  CSA_LAUNCH(k_tc_attend_pages, dim3(kPagedBlocks), dim3(kThreads), kSmem, s, tm_runs, a);
+  CSA_LAUNCH(k_tc_attend_pages, dim3(kPagedBlocks), dim3(kThreads), kSmem, s, tm_runs, tm_out16, tm_out64, a);
   return cudaGetLastError();
 }
 
