@@ -37,13 +37,13 @@ __device__ __forceinline__ float inv_rms(float inv_n, float eps, Sum sum) {
   constexpr float f = 5.42101086242752217e-20f;  // 2^-64
   return rsqrtf(fmaf(sum(f), inv_n, eps * f * f)) * f;
 }
-// cos and sin of theta = (float)p * inv_freq[i] (one fp32 product, as in rope_cs).  Far positions: theta = m 2^e as a fraction
+// cos and sin of theta = (float)p * freq (one fp32 product, as in rope_cs).  Far positions: theta = m 2^e as a fraction
 // of a turn, m 2^e / 2 pi modulo 1, in 64-bit fixed point (M. H. Payne and R. N. Hanek, Radian Reduction for Trigonometric
 // Functions; one word of 1 / 2 pi is enough up to theta = 2^29, off by less than 2^-35 turns), and from it the remainder to
 // the nearest quarter turn: sincosf's own reduction of angles above 10^5 cost a warp of the attention 5K clocks, one in fp64
 // nearly as much.
-__device__ __forceinline__ void turn_cs(int p, const float* inv_freq, int i, float* c, float* s) {
-  const float th = __fmul_rn((float)p, __ldg(inv_freq + i)), mag = fabsf(th);
+__device__ __forceinline__ void turn_cs(int p, float freq, float* c, float* s) {
+  const float th = __fmul_rn((float)p, freq), mag = fabsf(th);
   float r = th, sr, cr;
   int n = 0;
   if (mag > 1e5f && mag < 536870912.f) {

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(32 * kApWarps) k_append_pages(const __grid_con
   }
   if (a.inv_freq) {
     float2* cs = cs_all + warp * (a.R / 2);
-    for (int f = lane; f < a.R / 2; f += 32) turn_cs(p, a.inv_freq, f, &cs[f].x, &cs[f].y);
+    for (int f = lane; f < a.R / 2; f += 32) turn_cs(p, __ldg(a.inv_freq + f), &cs[f].x, &cs[f].y);
     __syncwarp();
   }
   if (a.norm) {

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
     if (begin == 0 && !whole && a.inv_freq)  // (for the merge: an angle costs a lane some hundred instructions)
       for (int i = tid; i < a.R / 2; i += blockDim.x) {
         float2 t;
-        turn_cs(k.p, a.inv_freq, i, &t.x, &t.y);
+        turn_cs(k.p, __ldg(a.inv_freq + i), &t.x, &t.y);
         a.turns[(size_t)blockIdx.x * (a.R / 2) + i] = t;
       }
 #pragma unroll 1
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
             float cs, sn;
-            turn_cs(k.p, a.inv_freq, (d + e - (D - a.R)) >> 1, &cs, &sn);
+            turn_cs(k.p, __ldg(a.inv_freq + ((d + e - (D - a.R)) >> 1)), &cs, &sn);
             const float x0 = v[e], x1 = v[e + 1];
             v[e] = fmaf(x0, cs, x1 * sn);
             v[e + 1] = fmaf(-x0, sn, x1 * cs);
@@ -178,41 +178,53 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
 // `share` warps take its parts in turn.  What the kernel waits for is memory, two round trips (where the parts are; their
 // statistics and the first accumulators together), if it has few enough instructions beside its loads (128 values an item
 // cost 1500 a warp, 8.7 us for 8 queries of 18 parts) and blocks: one started a head of every query cost 8 us on 128 queries
-// of which none was split.  So a block finds the split queries itself and walks their items.
+// of which none was split.  So a block finds the split queries itself and walks their items, one in most calls: all
+// accumulators of 8 queries or of one long one fit the device's registers.
 constexpr int kMergeWarps = 8;
-constexpr int kMergeAhead = 4;  // parts in flight a warp
+__host__ __device__ constexpr int merge_ahead(int chunks) { return 16 / chunks; }  // parts in flight a warp: 64 registers
 
 template <typename T, int kC>
 __global__ void __launch_bounds__(32 * kMergeWarps, 2) k_merge_pages(const __grid_constant__ PagedArgs a, int share) {
   // no early trigger: what follows finds the outputs written
-  __shared__ int4 s_list[kPagedBlocks];  // split queries: q, block of the first part, parts (at least two of the blocks each)
+  // split queries: q, block of the first part, parts (at least two of the blocks each)
+  __shared__ int4 s_list[kMergeWarps][kPagedBlocks];
   __shared__ int s_count[kMergeWarps];
   __shared__ float4 s_acc[kMergeWarps][32 * kC];
   __shared__ float s_wt[kMergeWarps][kPagedBlocks];  // weights of a warp's item's parts
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, Q = a.B * a.T;
   int n_split = 0;
-  for (int q0 = 0; q0 < Q; q0 += 32 * kMergeWarps) {
-    const int2 at = q0 + tid < Q ? a.parts[q0 + tid] : make_int2(0, 0);
+  if (Q <= 32) {  // every warp writes the same list, its own for all it reads: no barrier
+    const int2 at = lane < Q ? __ldcg(a.parts + lane) : make_int2(0, 0);
     const uint32_t on = __ballot_sync(0xffffffffu, at.y > 1);
-    if (lane == 0) s_count[warp] = __popc(on);
-    __syncthreads();
-    int before = n_split;
+    n_split = __popc(on);
+    if (at.y > 1) s_list[warp][__popc(on & ((1u << lane) - 1))] = make_int4(lane, at.x, at.y, 0);
+    __syncwarp();
+  } else {
+    for (int q0 = 0; q0 < Q; q0 += 32 * kMergeWarps) {
+      const int2 at = q0 + tid < Q ? __ldcg(a.parts + q0 + tid) : make_int2(0, 0);
+      const uint32_t on = __ballot_sync(0xffffffffu, at.y > 1);
+      if (lane == 0) s_count[warp] = __popc(on);
+      __syncthreads();
+      int before = n_split;
 #pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) {
-      before += w < warp ? s_count[w] : 0;
-      n_split += s_count[w];
+      for (int w = 0; w < kMergeWarps; ++w) {
+        before += w < warp ? s_count[w] : 0;
+        n_split += s_count[w];
+      }
+      if (at.y > 1) s_list[0][before + __popc(on & ((1u << lane) - 1))] = make_int4(q0 + tid, at.x, at.y, 0);
+      __syncthreads();
     }
-    if (at.y > 1) s_list[before + __popc(on & ((1u << lane) - 1))] = make_int4(q0 + tid, at.x, at.y, 0);
-    __syncthreads();
   }
+  const int4* list = s_list[Q <= 32 ? warp : 0];
   const int chunks = (a.D + 128 * kC - 1) / (128 * kC), items = n_split * a.H * chunks, per = kMergeWarps / share;
+  constexpr int kAhead = merge_ahead(kC), kL = (kPagedBlocks + 31) / 32;
   const int first = warp % share;
 #pragma unroll 1
   for (int i0 = blockIdx.x * per; i0 < items; i0 += gridDim.x * per) {
     const int item = min(i0 + warp / share, items - 1);  // (a warp behind the last repeats it)
     const int hq = item / chunks, lq = hq / a.H, h = hq - lq * a.H, d0 = 128 * kC * (item - hq * chunks) + 4 * lane;
-    const int4 at = s_list[lq];
+    const int4 at = list[lq];
     // part s of the query: slot 2 (block + s), the first one the slot behind; a lane's columns: 4 values, 128 apart
     const size_t one = (size_t)a.H * a.D, step = 2 * one * share;
     const float* src = a.part + 2 * one * (at.y + first) + (first == 0 ? one : 0);
@@ -224,10 +236,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 2) k_merge_pages(const __gri
       on[c] = d < a.D;
       off[c] = ((size_t)blk * a.H + h) * a.cols + (d - blk * 32);
     }
-    float4 x[kMergeAhead][kC];
+    float4 x[kAhead][kC];
     auto fetch = [&](int s0, const float* p) {
 #pragma unroll
-      for (int g = 0; g < kMergeAhead; ++g) {
+      for (int g = 0; g < kAhead; ++g) {
         if (s0 + g * share < at.z) {
 #pragma unroll
           for (int c = 0; c < kC; ++c)
@@ -237,22 +249,28 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 2) k_merge_pages(const __gri
       }
       return p;
     };
+    const float2* stat = a.ml + (size_t)2 * at.y * a.H + h;
+    float2 ml[kL];  // (all at once)
+#pragma unroll
+    for (int i = 0; i < kL; ++i) {
+      const int s = lane + 32 * i;
+      ml[i] = s < at.z ? __ldcg(stat + (size_t)2 * s * a.H + (s == 0 ? a.H : 0)) : make_float2(-INFINITY, 0.f);
+    }
     src = fetch(first, src);
     // the weights (every warp of an item finds them)
     const float z2 = a.sink ? a.sink[h] * 1.4426950408889634f : -INFINITY;
-    const float2* stat = a.ml + (size_t)2 * at.y * a.H + h;
     float M = z2, Z = 0.f;
-    const float2 ml0 = lane < at.z ? __ldcg(stat + 2 * lane * a.H + (lane == 0 ? a.H : 0)) : make_float2(-INFINITY, 0.f);
-    M = fmaxf(M, ml0.x);
-    for (int s = lane + 32; s < at.z; s += 32) M = fmaxf(M, __ldcg(stat + 2 * s * a.H).x);
+#pragma unroll
+    for (int i = 0; i < kL; ++i) M = fmaxf(M, ml[i].x);
     M = warp_max(M);
     float* wt = s_wt[warp];
     __syncwarp();  // (the weights of the item before have been read)
-    for (int s = lane; s < at.z; s += 32) {
-      const float2 ml = s < 32 ? ml0 : __ldcg(stat + 2 * s * a.H);
-      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);  // (a part without keys)
-      wt[s] = f;
-      Z = fmaf(ml.y, f, Z);
+#pragma unroll
+    for (int i = 0; i < kL; ++i) {
+      if (32 * i >= at.z) break;
+      const float f = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - M);  // (a part without keys)
+      if (lane + 32 * i < at.z) wt[lane + 32 * i] = f;
+      Z = fmaf(ml[i].y, f, Z);
     }
     Z = warp_sum(Z) + (z2 == -INFINITY ? 0.f : exp2f(z2 - M));
     __syncwarp();
@@ -260,10 +278,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 2) k_merge_pages(const __gri
 #pragma unroll
     for (int c = 0; c < kC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int s0 = first; s0 < at.z; s0 += kMergeAhead * share) {
+    for (int s0 = first; s0 < at.z; s0 += kAhead * share) {
       if (s0 > first) src = fetch(s0, src);
 #pragma unroll
-      for (int g = 0; g < kMergeAhead; ++g) {
+      for (int g = 0; g < kAhead; ++g) {
         const int s = s0 + g * share;
         const float f = s < at.z ? wt[s] : 0.f;
         if (f == 0.f) continue;  // (what a part without keys holds counts for nothing)
@@ -319,11 +337,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 2) k_merge_pages(const __gri
 template <typename T, int kC>
 cudaError_t merge_c(const PagedArgs& a, cudaStream_t s) {
   const int Q = a.B * a.T;
-  // few queries have many parts each (about blocks / queries): a warp takes four at a time, more of them share an item
+  // few queries have many parts each (about blocks / queries): as many warps share an item as take them at once, while the
+  // items find room on the device at once (two blocks an SM)
+  const long long items = (long long)min(Q, kPagedBlocks) * a.H * ((a.D + 128 * kC - 1) / (128 * kC)), room = 2LL * kPagedBlocks;
   int share = 1;
-  while (share < kMergeWarps && share * kMergeAhead * Q < kPagedBlocks) share *= 2;
-  const long long items = (long long)min(Q, kPagedBlocks) * a.H * ((a.D + 128 * kC - 1) / (128 * kC)), per = kMergeWarps / share;
-  CSA_LAUNCH((k_merge_pages<T, kC>), dim3((unsigned)min((items + per - 1) / per, 2LL * kPagedBlocks)), dim3(32 * kMergeWarps),
+  while (share < kMergeWarps && share * merge_ahead(kC) * Q < kPagedBlocks && 2 * share * items <= room * kMergeWarps) share *= 2;
+  const long long per = kMergeWarps / share;
+  CSA_LAUNCH((k_merge_pages<T, kC>), dim3((unsigned)min((items + per - 1) / per, room)), dim3(32 * kMergeWarps),
              0, s, a, share);
   return cudaGetLastError();
 }

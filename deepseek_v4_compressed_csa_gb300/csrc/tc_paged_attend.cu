@@ -175,6 +175,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_mbar_init();
   }
   pdl_wait();  // predecessors complete: what they wrote is visible and their tensor memory is free
+  // (small inputs that the softmax warps need later, before the keys that every SM fetches stand in their way)
+  const bool soft = warp > kMmaWarp;
+  const float freq = soft && a.inv_freq ? __ldg(a.inv_freq + lane) : 0.f;
+  const float z2 = soft && a.sink ? __ldg(a.sink + 16 * (warp & 3) + (lane & 15)) * 1.4426950408889634f : -INFINITY;
   PagedRun* plan = reinterpret_cast<PagedRun*>(sm.base + kOffPlan);
   paged_plan<kThreads / 32>(a, plan, reinterpret_cast<int*>(plan + 1));
   const int t0 = plan->t0, t1 = plan->t1;
@@ -430,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           if ((lane & 3) == 0) amax[g * kH + 16 * quad + r + 8 * x] = mx;
         }
-        if (g == 0 && gt < 32 && a.inv_freq) turn_cs(k.p, a.inv_freq, gt, rcos + gt, rsin + gt);
+        if (g == 0 && gt < 32 && a.inv_freq) turn_cs(k.p, freq, rcos + gt, rsin + gt);
         tc::named_bar(4, kSoft);
         // 2^-e with e = exponent - 7: values below 2^8, exact products; a row of denormals, or zeros, stays small; a row that
         // holds an infinity or a NaN becomes NaN (by its product with 0, and its scores by their factor)
@@ -616,7 +620,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float l = fmaf(s0.y, ex2(s0.x - mr), s1.y * ex2(s1.x - mr));
         float f = ref == -INFINITY ? 0.f : ex2(ref - kGain - mr);  // O^T * f = sum 2^{t - m} key
         if (whole) {
-          const float z2 = a.sink ? a.sink[h] * 1.4426950408889634f : -INFINITY;
           const float M = fmaxf(m, z2), gm = m == -INFINITY ? 0.f : ex2(m - M);
           const float Z = l * gm + (z2 == -INFINITY ? 0.f : ex2(z2 - M));
           f = Z == 0.f ? 0.f : f * (gm / Z);
