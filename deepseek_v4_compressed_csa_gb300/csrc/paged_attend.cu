@@ -13,21 +13,25 @@ namespace csa {
 namespace {
 
 // ---------------------------------------------------------------- the portable kernel
+// A tile's keys wait in shared memory as fp32; the next tile's codes are on their way in registers meanwhile, and the rows
+// of the one after it are looked up.  A warp takes a head: a lane a key for the logits, then lanes share a key's dims (rows
+// of up to 128 dims: several keys at a time) for the sums.
 constexpr int kSimtTile = 32;   // keys a tile: a lane each
 constexpr int kSimtWarps = 8;   // heads at a time, a warp each
-constexpr int kSimtMaxC = 4;    // chunks of 8 dims a lane: D <= 1024
 constexpr int kSimtPad = 4;     // floats behind a key's row: lanes read their keys' chunks without bank conflicts
 constexpr int kSimtSmemMax = (kSimtTile * (1024 + kSimtPad) + kSimtWarps * 1024) * 4;
 
 __host__ __device__ constexpr int simt_smem(int D) { return (kSimtTile * (D + kSimtPad) + kSimtWarps * D) * 4; }
 
-template <typename T>
+// kC: chunks of 8 dims a lane holds (D <= 256 kC); a tile's codes are kTile / 8 kC chunks a thread
+template <typename T, int kC>
 __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __grid_constant__ PagedArgs a) {
   if (a.merge) pdl_trigger();  // (what follows otherwise finds the outputs written)
   extern __shared__ __align__(16) float sm_pa[];
-  __shared__ int s_row[kSimtTile];
+  __shared__ int s_row[2][kSimtTile];
   __shared__ __align__(16) int s_plan[kPlanInts];
   __shared__ PagedRun s_run;
+  constexpr int kU = kSimtTile * 32 * kC / (32 * kSimtWarps);  // chunks of a tile a thread copies
   const int D = a.D, KS = D + kSimtPad, n8 = D >> 3;
   float* ks = sm_pa;                    // [kSimtTile][KS] keys
   float* qs = sm_pa + kSimtTile * KS;   // [kSimtWarps][D] queries of this group of heads
@@ -38,6 +42,10 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
   int pre = s_run.pre;
   PagedQuery k = s_run.k;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // lanes that share a key's dims, and keys at a time
+  int share = 32;
+  while (share > 1 && share / 2 >= n8) share /= 2;
+  const int sub = lane & (share - 1), group = lane / share, groups = 32 / share;
 #pragma unroll 1
   while (true) {
     const int q = k.q, b = k.b;
@@ -50,8 +58,22 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
         turn_cs(k.p, __ldg(a.inv_freq + i), &t.x, &t.y);
         a.turns[(size_t)blockIdx.x * (a.R / 2) + i] = t;
       }
+    // key x of the query: its physical row, -1 for none (thread x - 32 t of a tile)
+    auto row_of = [&](int x) {
+      if (x >= nkeys) return -1;
+      int r = -1;
+      if (x < k.n0) {
+        const int j = a.sel ? __ldg(a.sel + (size_t)q * a.topk + x) : x;
+        if (!a.sel || (j >= 0 && j < k.n_rows)) r = paged_row(a, a.row_table + (size_t)b * a.row_pages, j);
+      } else {
+        const int y = x - k.n0;
+        r = paged_row(a, a.token_table + (size_t)b * a.token_pages, y < k.f ? y : k.w0 + (y - k.f));
+      }
+      if (r < 0) atomicOr(a.err, CSA_DEV_RANGE);
+      return r;
+    };
 #pragma unroll 1
-    for (int h0 = 0; h0 < a.H && begin < end; h0 += kSimtWarps) {
+    for (int h0 = 0; h0 < a.H; h0 += kSimtWarps) {
       const int h = h0 + warp;
       __syncthreads();
       for (int e = tid; e < kSimtWarps * n8; e += blockDim.x) {
@@ -60,86 +82,90 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
         if (h0 + hh < a.H) load8(static_cast<const T*>(a.q) + ((size_t)q * a.H + h0 + hh) * D + c, v);
         store8(qs + hh * D + c, v);
       }
-      float m = -INFINITY, l = 0.f;
-      float acc[kSimtMaxC][8];
+      if (tid < kSimtTile) s_row[begin & 1][tid] = row_of(begin * kSimtTile + tid);
+      __syncthreads();
+      uint2 code[kU];
+      float scale[kU];
+      auto fetch = [&](int t) {  // the codes of tile t, whose rows are there
 #pragma unroll
-      for (int c = 0; c < kSimtMaxC; ++c)
+        for (int i = 0; i < kU; ++i) {
+          const int e = tid + i * 32 * kSimtWarps, x = e / n8, c = (e - x * n8) * 8, r = x < kSimtTile ? s_row[t & 1][x] : -1;
+          code[i] = r >= 0 ? __ldg(reinterpret_cast<const uint2*>(a.codes + (size_t)r * D + c)) : make_uint2(0u, 0u);
+          scale[i] = r >= 0 ? __ldg(a.scales + r) : 0.f;
+        }
+      };
+      fetch(begin);
+      float m = -INFINITY, l = 0.f;
+      float acc[kC][8];
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[c][e] = 0.f;
 #pragma unroll 1
       for (int t = begin; t < end; ++t) {
-        const int k0 = t * kSimtTile, nk = min(kSimtTile, nkeys - k0);
-        __syncthreads();
-        if (tid < kSimtTile) {
-          const int x = k0 + tid;
-          int r = -1;
-          if (x < k.n0) {
-            const int j = a.sel ? __ldg(a.sel + (size_t)q * a.topk + x) : x;
-            if (!a.sel || (j >= 0 && j < k.n_rows)) r = paged_row(a, a.row_table + (size_t)b * a.row_pages, j);
-          } else if (x < nkeys) {
-            const int y = x - k.n0;
-            r = paged_row(a, a.token_table + (size_t)b * a.token_pages, y < k.f ? y : k.w0 + (y - k.f));
-          }
-          if (r < 0 && x < nkeys) atomicOr(a.err, CSA_DEV_RANGE);
-          s_row[tid] = r;
-        }
-        __syncthreads();
-        for (int e = tid; e < kSimtTile * n8; e += blockDim.x) {
-          const int x = e / n8, c = (e - x * n8) * 8, r = s_row[x];
-          float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          if (r >= 0) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2*>(a.codes + (size_t)r * D + c));
-            const float s = __ldg(a.scales + r);
-            const float2 f[4] = {e4m3x2_f(u.x), e4m3x2_f(u.x >> 16), e4m3x2_f(u.y), e4m3x2_f(u.y >> 16)};
+        if (tid < kSimtTile && t + 1 < end) s_row[(t + 1) & 1][tid] = row_of((t + 1) * kSimtTile + tid);
+        __syncthreads();  // (the tile before has been read; the next one's rows are there)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              v[2 * i] = f[i].x * s;
-              v[2 * i + 1] = f[i].y * s;
-            }
-          }
+        for (int i = 0; i < kU; ++i) {
+          const int e = tid + i * 32 * kSimtWarps, x = e / n8, c = (e - x * n8) * 8;
+          if (x >= kSimtTile) continue;
+          const float s = scale[i];
+          const float2 f[4] = {e4m3x2_f(code[i].x), e4m3x2_f(code[i].x >> 16), e4m3x2_f(code[i].y), e4m3x2_f(code[i].y >> 16)};
+          const float v[8] = {f[0].x * s, f[0].y * s, f[1].x * s, f[1].y * s, f[2].x * s, f[2].y * s, f[3].x * s, f[3].y * s};
           store8(ks + x * KS + c, v);
         }
+        const bool on = s_row[t & 1][lane] >= 0;
+        if (t + 1 < end) fetch(t + 1);
         __syncthreads();
-        float dot = 0.f;
-        const bool on = lane < nk && s_row[lane] >= 0;
-        if (on) {
+        float d4[4] = {0.f, 0.f, 0.f, 0.f};
+        {
           const float* kr = ks + lane * KS;
           const float* qh = qs + warp * D;
+#pragma unroll 4
           for (int c = 0; c < D; c += 4) {
             const float4 x = *reinterpret_cast<const float4*>(kr + c), y = *reinterpret_cast<const float4*>(qh + c);
-            dot = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, dot))));
+            d4[0] = fmaf(x.x, y.x, d4[0]);
+            d4[1] = fmaf(x.y, y.y, d4[1]);
+            d4[2] = fmaf(x.z, y.z, d4[2]);
+            d4[3] = fmaf(x.w, y.w, d4[3]);
           }
         }
-        const float lg = on ? dot * a.scale2 : -INFINITY;
+        const float lg = on ? ((d4[0] + d4[1]) + (d4[2] + d4[3])) * a.scale2 : -INFINITY;
         const float mn = fmaxf(m, warp_max(lg)), ref = mn == -INFINITY ? 0.f : mn;
         const float p = exp2f(lg - ref), f = exp2f(m - ref);
         l = fmaf(l, f, warp_sum(p));
         m = mn;
 #pragma unroll
-        for (int c = 0; c < kSimtMaxC; ++c)
+        for (int c = 0; c < kC; ++c)
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[c][e] *= f;
-        for (int x = 0; x < nk; ++x) {
+        const int nk = min(kSimtTile, nkeys - t * kSimtTile);  // (rows behind the last hold zeros, and p is 0)
+#pragma unroll 4
+        for (int x0 = 0; x0 < nk; x0 += groups) {
+          const int x = x0 + group;
           const float px = __shfl_sync(0xffffffffu, p, x);
           const float* kr = ks + x * KS;
 #pragma unroll
-          for (int c = 0; c < kSimtMaxC; ++c) {
-            if (lane + 32 * c < n8) {
+          for (int c = 0; c < kC; ++c) {
+            if (sub + 32 * c < n8) {
               float v[8];
-              load8(kr + 8 * (lane + 32 * c), v);
+              load8(kr + 8 * (sub + 32 * c), v);
 #pragma unroll
               for (int e = 0; e < 8; ++e) acc[c][e] = fmaf(px, v[e], acc[c][e]);
             }
           }
         }
       }
-      if (h >= a.H) continue;
+      for (int o = share; o < 32; o <<= 1)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[0][e] += __shfl_xor_sync(0xffffffffu, acc[0][e], o);
+      if (h >= a.H || group > 0) continue;
       if (!whole) {
         const size_t at = (size_t)slot * a.H + h;
-        if (lane == 0) a.ml[at] = make_float2(m, l);
+        if (lane == 0) a.ml[at] = make_float2(l == l ? m : l, l);  // (a NaN is one for the merge, too)
 #pragma unroll
-        for (int c = 0; c < kSimtMaxC; ++c)
-          if (lane + 32 * c < n8) store8(a.part + at * D + 8 * (lane + 32 * c), acc[c]);
+        for (int c = 0; c < kC; ++c)
+          if (sub + 32 * c < n8) store8(a.part + at * D + 8 * (sub + 32 * c), acc[c]);
         continue;
       }
       const float z2 = a.sink ? a.sink[h] * 1.4426950408889634f : -INFINITY;
@@ -147,20 +173,24 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
       const float Z = l * f + (z2 == -INFINITY ? 0.f : exp2f(z2 - M));
       const float w = Z == 0.f ? 0.f : f / Z;  // (no key and no sink: zeros)
 #pragma unroll
-      for (int c = 0; c < kSimtMaxC; ++c) {
-        const int d = 8 * (lane + 32 * c);
+      for (int c = 0; c < kC; ++c) {
+        const int d = 8 * (sub + 32 * c);
         if (d >= D) continue;
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = acc[c][e] * w;
         if (a.inv_freq && d >= D - a.R) {
-#pragma unroll
+#pragma unroll 1
           for (int e = 0; e < 8; e += 2) {
             float cs, sn;
             turn_cs(k.p, __ldg(a.inv_freq + ((d + e - (D - a.R)) >> 1)), &cs, &sn);
-            const float x0 = v[e], x1 = v[e + 1];
-            v[e] = fmaf(x0, cs, x1 * sn);
-            v[e + 1] = fmaf(-x0, sn, x1 * cs);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              if (i != e) continue;
+              const float x0 = v[i], x1 = v[i + 1];
+              v[i] = fmaf(x0, cs, x1 * sn);
+              v[i + 1] = fmaf(-x0, sn, x1 * cs);
+            }
           }
         }
         store8(static_cast<T*>(a.out) + ((size_t)q * a.H + h) * D + d, v);
@@ -170,6 +200,13 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
     if (pre >= t1) return;
     k = next_query(a, q);
   }
+}
+
+template <typename T, int kC>
+cudaError_t simt_c(const PagedArgs& a, cudaStream_t s) {
+  allow_smem<kSimtSmemMax>(k_attend_pages_simt<T, kC>);
+  CSA_LAUNCH((k_attend_pages_simt<T, kC>), dim3(kPagedBlocks), dim3(32 * kSimtWarps), simt_smem(a.D), s, a);
+  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------- merge of split queries
@@ -386,8 +423,8 @@ cudaError_t attend_t(const Dims& L, PagedArgs a, cudaStream_t s) {
     a.shift = 0;
     a.cols = a.D;
     a.merge = !stay_whole(&a);
-    allow_smem<kSimtSmemMax>(k_attend_pages_simt<T>);
-    CSA_LAUNCH(k_attend_pages_simt<T>, dim3(kPagedBlocks), dim3(32 * kSimtWarps), simt_smem(a.D), s, a);
+    const cudaError_t e = a.D <= 256 ? simt_c<T, 1>(a, s) : a.D <= 512 ? simt_c<T, 2>(a, s) : simt_c<T, 4>(a, s);
+    if (e != cudaSuccess) return e;
   }
   return a.merge ? launch_merge<T>(a, s) : cudaSuccess;
 }

@@ -21,11 +21,11 @@
 // head's parts meet by one shuffle; after it the lane pair shares the head's 64 keys, 32 each.
 //
 // Softmax with the scales: t = scale2 S ks, m a running maximum, l = sum 2^{t - m}.  What enters the product is
-// 2^t ks 2^{7 - R}, R a reference that follows the maximum of log2(2^t ks) in steps: at most 2^11, where lo, up to 1/8 of
-// hi, still fits E4M3.  It starts 4 times above the first tile's maximum, and O^T is rescaled only when some head's maximum has
-// passed its R by 4 (powers of two); every head's R then follows.  A tile takes its four warps some 2500 clocks, most of them latency, and the products' pipe 1300: two groups
-// of four take tiles in turn, each with an m and l of its own; R is one, so each tile's decision about it waits for the
-// tile's before.
+// 2^t ks 2^{7 - R}, R a reference that follows the maximum of log2(2^t |ks|) in steps: at most 2^11, where lo, up to 1/8 of
+// hi, still fits E4M3.  It starts 4 times above the first tile's maximum, and O^T is rescaled only when some head's maximum
+// has passed its R by 4 (powers of two); every head's R then follows.  A tile takes its four warps some 2500 clocks, most
+// of them latency, and the products' pipe 1300: two groups of four take tiles in turn, each with an m and l of its own; R
+// is one, so each tile's decision about it waits for the tile's before.
 #include "paged.cuh"
 #include "tc.cuh"
 
@@ -533,13 +533,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             l2 += p2 + p3;
             // (a key that does not count has scale 0)
             s[4 * e4] = p0 * k4.x; s[4 * e4 + 1] = p1 * k4.y; s[4 * e4 + 2] = p2 * k4.z; s[4 * e4 + 3] = p3 * k4.w;
-            vt = fmaxf(fmaxf(vt, fmaxf(s[4 * e4], s[4 * e4 + 1])), fmaxf(s[4 * e4 + 2], s[4 * e4 + 3]));
+            vt = fmaxf(fmaxf(vt, fmaxf(fabsf(s[4 * e4]), fabsf(s[4 * e4 + 1]))), fmaxf(fabsf(s[4 * e4 + 2]), fabsf(s[4 * e4 + 3])));
           }
           l += l2;
           vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, 16));
           // ---- the reference follows log2 of the largest 2^t ks: the first two tiles find it together, later ones after
           // the tile before has decided
-          const float lv = vt > 0.f ? mr + lg2(vt) : -INFINITY;
+          // (at least 2^-115 of the probabilities: the gain stays finite, and smaller scales lose digits)
+          const float lv = vt > 0.f ? mr + fmaxf(lg2(vt), -115.f) : -INFINITY;
           float ref;
           if (i < 2 && n > 1) {
             if (plane == 0) top[i * kH + h] = lv;
@@ -624,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float Z = l * gm + (z2 == -INFINITY ? 0.f : ex2(z2 - M));
           f = Z == 0.f ? 0.f : f * (gm / Z);
         } else {
-          a.ml[slot * kH + h] = make_float2(m, l);
+          a.ml[slot * kH + h] = make_float2(l == l ? m : l, l);  // (a NaN is one for the merge, too)
         }
         fout[h] = f;
       }
