@@ -37,7 +37,8 @@ EXPORTS = ("csa_kernel_launches", "csa_frontier_slots", "csa_workspace_size", "c
            "csa_index_topk_static", "csa_index_topk_overlapped", "csa_advance_positions",
            "csa_compress_append_pair", "csa_trim", "csa_index_topk_verify", "csa_attend_verify",
            "csa_compress_append_varlen", "csa_attend_prefill_varlen", "csa_index_rows_fp8", "csa_norm_rope",
-           "csa_compress_tree", "csa_index_scores_tree", "csa_attend_tree", "csa_commit_tree", "csa_add_norm", "csa_append_pages", "csa_attend_pages")
+           "csa_compress_tree", "csa_index_scores_tree", "csa_attend_tree", "csa_commit_tree", "csa_add_norm",
+           "csa_append_pages", "csa_attend_pages")
 
 
 class CSAError(RuntimeError):

@@ -28,7 +28,7 @@ struct AnArgs {
   uint8_t* codes;
   float* scales;
   long long N, x_stride, r_stride;
-  int X, group, lanes;  // lanes: threads that hold a group (a power of two up to 32), 0: the whole row
+  int X, lanes;         // lanes: threads that hold a group (a power of two up to 32), 0: the whole row
   int group_log2;
   float inv_x, eps;
 };
@@ -193,7 +193,7 @@ cudaError_t add_norm_t(const Dims& L, const AddNorm& t, cudaStream_t s) {
   a.residual_out = static_cast<T*>(t.residual_out);
   a.codes = t.codes; a.scales = t.scales;
   a.N = t.N; a.x_stride = t.x_stride; a.r_stride = t.r_stride;
-  a.X = t.X; a.group = t.group;
+  a.X = t.X;
   a.lanes = t.codes && t.group <= 256 && t.group != t.X ? t.group / 8 : 0;
   while ((1 << a.group_log2) < t.group) ++a.group_log2;
   a.inv_x = 1.0f / (float)t.X;

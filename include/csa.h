@@ -565,7 +565,8 @@ csa_status csa_commit_tree(const csa_layer* layer, int B, int T, const int32_t* 
  *   y = h * (mean(h^2) + rms_eps)^-1/2 * weight       (weight NULL: ones)
  *   residual_out = h, out = y, each rounded to the model dtype once;
  *   per group of `group` values of y: scale = max |y| / 448,
- *   codes = E4M3(y / scale) (nearest even, saturating), zeros where the scale is 0.
+ *   codes = E4M3(y / scale) (nearest even, saturating; the quotient is a product
+ *   with the scale's reciprocal, within two roundings), zeros where the scale is 0.
  * The norm is that of the fp32 sum, not of the rounded one.  A NaN makes its
  * group's scale NaN; codes and scales stand for code * scale.
  * Arguments
@@ -614,7 +615,7 @@ csa_status csa_add_norm(const csa_layer* layer, const void* x, long long x_strid
  *   zeros where the scale is 0, a NaN scale for a row with a NaN)
  * stride_b, stride_t: elements between sequences and tokens (0: dense; else
  * multiples of 8, tokens at least D apart).  B * T <= 2^24.  Two rows of one call
- * in one place (tables that share a page being written) leave either of them. */
+ * in one place (tables that share a page being written) leave a mixture of both. */
 typedef struct {
   void* codes;
   float* scales;
@@ -636,15 +637,18 @@ csa_status csa_append_pages(const csa_layer* layer, const csa_pages* pages, cons
  *   out[b][i][h] = RoPE^-1(o_h, p) in fp32, rounded to the model dtype once.
  * The cache holds the queries' own rows already (csa_append_pages).  q is rotated
  * (csa_norm_rope).  A query without any key gives zeros.
- *   q, out [B, T, H, D] model dtype, apart from one another; sink [H] fp32 or NULL (no sink);
+ *   q, out [B, T, H, D] model dtype, apart from one another (and out from all else); sink [H] fp32 or NULL (no sink);
  *   sel [B, T, topk], n_sel [B, T] int32 (ratio 4, with row_table); inv_freq NULL:
  *   no rotation of the output.
  * On the tensor cores (bf16, H = 64, D = 512, R = 64, page_rows a multiple of 8)
- * queries and probabilities enter the products as two E4M3 parts each, about 8
- * bits (what bf16 operands would keep), sums in fp32; the portable kernel takes any other layer, all in fp32.  A
- * call's result depends on how its keys are cut into tiles, not on the run.
+ * the queries enter the products as two E4M3 parts (the 8 bits of a bf16 value,
+ * those 2^-14 below the head's largest fewer), the probabilities times the keys'
+ * scales as an E5M2 and an E4M3 part (7 bits, down to 2^-22 of the largest), sums
+ * in fp32; the portable kernel takes any other layer, all in fp32.  A call's result
+ * depends on how its keys are cut into tiles (by B, T and all lengths), not on the
+ * run: the same call gives the same bits.
  * B * T <= 2^16, and CSA_ERR_ARG where the tables' widths times B * T could hold 2^36 keys.
- * Workspace: CSA_OP_ATTEND_PAGES. */
+ * Workspace: CSA_OP_ATTEND_PAGES, not shared by two calls in flight. */
 csa_status csa_attend_pages(const csa_layer* layer, const csa_pages* pages, const void* q, int B, int T,
                             const float* sink, const int32_t* pos, const int32_t* n_new, const int32_t* token_table,
                             int token_width, int first, const int32_t* row_table, int row_width, const int32_t* n_rows,

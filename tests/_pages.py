@@ -126,9 +126,12 @@ def attend_ref(L, q, codes, s, sink, tensor_cores):
         # The queries' two E4M3 parts, the second 16 times finer: off by half of its smallest step, 2^-14 of the scale at
         # which the head's largest value is at least 2^7 (so 2^-21 of it); exp2 and its argument's fp32 rounding.
         err = err + A * (2 * scale * q.abs().amax(1, keepdim=True) * 2.0 ** -21 * keys.abs().sum(1).max() + 2.0 ** -20)
+        # A weight below fp32's smallest normal number, 2^-126, counts as nothing (the hardware's exp2 flushes it): its
+        # key's values are off by less than 2^-126 of themselves; with the sink far above every key that is all there is.
+        err = err + 2.0 ** -126 * keys.abs().sum(0)
         # The probabilities' parts of w = p s, E5M2 (at most 2^-3 off) and what that leaves in E4M3 (2^-4 of it, or half of
         # its smallest step, 2^-10 where the largest w is at least 2^5); what E5M2's smallest step, 2^-16, leaves is within that.
-        w = p * s
+        w = p * s.abs()
         err = err + (2.0 ** -7 * w + torch.minimum(2.0 ** -3 * w + w.amax(1, keepdim=True) * 2.0 ** -22, w.amax(1, keepdim=True) * 2.0 ** -15)) @ codes.abs()
     return p @ keys, err
 
