@@ -375,8 +375,9 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
                : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// wait until the sources of this thread's bulk groups have been read, or the copies are complete
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// wait until the sources of this thread's bulk groups, but for the last kPending, have been read, or the copies are complete
+template <int kPending = 0>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // barrier among `nthreads` threads (whole warps) on hardware barrier `id` (1..15)
 __device__ __forceinline__ void named_bar(int id, int nthreads) {

@@ -7,7 +7,7 @@
 // whole bf16 rate of the tensor cores, and turning codes into bf16 on the way for more than the rest of the SM has.  So
 // the codes go to the tensor cores as they are (kind::f8f6f4, twice the bf16 rate), and what meets them is split in two
 // 8-bit parts:
-//   q = 2^e (hi + lo / 16), E4M3 both: the 8 bits of a bf16 value, exact but for values 2^-14 below the head's largest.
+//   q = 2^e (hi + lo / 16), E4M3 both: the 8 bits of a bf16 value, exact but for values 2^-13 below the head's largest.
 //     The parts are two rows of one operand, M = 128 = 64 heads x 2, kept in tensor memory (its 128 columns are an A
 //     operand that no product reads from shared memory);
 //   P = hi + lo, E5M2 and E4M3, both added to the same accumulator: 7 bits (at most 2^-7 of a probability, about 2^-9.5 on
@@ -434,17 +434,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           if ((lane & 3) == 0) amax[g * kH + 16 * quad + r + 8 * x] = mx;
         }
-        if (g == 0 && gt < 32 && a.inv_freq) turn_cs(k.p, freq, rcos + gt, rsin + gt);
         tc::named_bar(4, kSoft);
         // 2^-e with e = exponent - 7: values below 2^8, exact products; a row of denormals, or zeros, stays small; a row that
         // holds an infinity or a NaN becomes NaN (by its product with 0, and its scores by their factor)
-        auto expo = [&](int hh) { return max((int)(max(amax[hh], amax[kH + hh]) >> 7), 8); };
-        float inv[2];
+        auto expo = [&](int hh) { return max((int)(max(amax[hh], amax[kH + hh]) >> 7), 12); };
+        __nv_bfloat162 inv[2], inv16[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int be = expo(16 * quad + r + 8 * x);
-          inv[x] = be == 255 ? 0.f : __uint_as_float((uint32_t)(261 - be) << 23);
+          inv[x] = __float2bfloat162_rn(be == 255 ? 0.f : __uint_as_float((uint32_t)(261 - be) << 23));
+          inv16[x] = __float2bfloat162_rn(be == 255 ? 0.f : __uint_as_float((uint32_t)(265 - be) << 23));
         }
+        // hi: the value cut to the four digits that E4M3 has, lo: the four behind them, both exact, as are the products with
+        // powers of two, so bf16 pairs do.  (hi below E4M3's normal numbers, 2^-13 of the head's largest, is rounded, by at
+        // most 2^-17 of that.  With lo from what hi became, converted back, it would be 2^-21, and 3K clocks instead of 2K.)
+        auto parts = [&](int x, const uint2& u, uint32_t* hi, uint32_t* lo) {
+          float h[4], l[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w = i ? u.y : u.x, m = w & 0xfff0fff0u;
+            const __nv_bfloat162 wv = *reinterpret_cast<const __nv_bfloat162*>(&w), mv = *reinterpret_cast<const __nv_bfloat162*>(&m);
+            const __nv_bfloat162 a2 = __hmul2(mv, inv[x]), b2 = __hmul2(__hsub2(wv, mv), inv16[x]);
+            const uint32_t aw = *reinterpret_cast<const uint32_t*>(&a2), bw = *reinterpret_cast<const uint32_t*>(&b2);
+            h[2 * i] = __uint_as_float(aw << 16); h[2 * i + 1] = __uint_as_float(aw & 0xffff0000u);
+            l[2 * i] = __uint_as_float(bw << 16); l[2 * i + 1] = __uint_as_float(bw & 0xffff0000u);
+          }
+          *hi = e4m3x4(h[0], h[1], h[2], h[3]);
+          *lo = e4m3x4(l[0], l[1], l[2], l[3]);
+        };
         // (four rounds of the same code, the values moved up in between: unrolled, its 15 KB of instructions arrive behind
         // the keys that every SM is fetching: 9.5K clocks in the largest batch, 3K by itself)
 #pragma unroll 1
@@ -453,13 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x0 = __uint_as_float(v[x][e].x << 16) * inv[x], x1 = __uint_as_float(v[x][e].x & 0xffff0000u) * inv[x];
-              const float x2 = __uint_as_float(v[x][e].y << 16) * inv[x], x3 = __uint_as_float(v[x][e].y & 0xffff0000u) * inv[x];
-              hi[2 * e + x] = e4m3x4(x0, x1, x2, x3);
-              const float2 b0 = e4m3x2_f(hi[2 * e + x]), b1 = e4m3x2_f(hi[2 * e + x] >> 16);
-              lo[2 * e + x] = e4m3x4((x0 - b0.x) * 16.f, (x1 - b0.y) * 16.f, (x2 - b1.x) * 16.f, (x3 - b1.y) * 16.f);
-            }
+            for (int e = 0; e < 4; ++e) parts(x, v[x][e], hi + 2 * e + x, lo + 2 * e + x);
 #pragma unroll
             for (int e = 0; e < 12; ++e) v[x][e] = v[x][e + 4];
           }
@@ -608,6 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (plane == 0) stat[g * kH + h] = make_float2(m, l);
       }
       j += n;
+      // (the group that has not the last tile: it waits for the other one; earlier, its instructions arrive behind the keys)
+      if ((j & 1) == g && gt < 32 && a.inv_freq) turn_cs(k.p, freq, rcos + gt, rsin + gt);
       // ---- the run's part of this query, or its output, through shared memory: small buffers, or, behind the block's last
       // tile, the stages, which hold all of it at once
       const bool whole = begin == 0 && end == k.tiles, last = pre + k.tiles >= t1;
@@ -638,47 +651,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 64 dims in the 128-byte swizzle (a head's row 128 bytes) that go out by one copy each: of 64 heads at the end, of
         // 16 on the way.  (A copy a head, 1 KB each, cost 4K clocks: a lane's copies are issued one after another.)
         const int r = lane >> 2, c2 = 2 * (lane & 3), chunk = 4 * (quad & 1) + (lane >> 3), h8 = lane & 7;
+        float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};  // of the lane's dims of the last 64
+        const bool turns = g == 1 && quad >= 2 && a.inv_freq;
+        if (turns) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int ri = (32 * (quad - 2) + 8 * i + r) >> 1;
+            cs[i] = rcos[ri];
+            sn[i] = r & 1 ? -rsin[ri] : rsin[ri];
+          }
+        }
 #pragma unroll 1
-        for (int u = 0; u < 8; ++u) {
-          const int blk = 2 * g + (u >> 2), h0 = 16 * (u & 3);
-          uint32_t x[2][8];
+        for (int u2 = 0; u2 < 8; u2 += 2) {  // (two steps' accumulators at once)
+          const int blk = 2 * g + (u2 >> 2);
+          uint32_t x[2][2][8];
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) tc::tmem_ld_16x16(tmem + kColO + 64 * blk + h0 + lanes + ((uint32_t)(16 * hf) << 16), x[hf]);
+          for (int i = 0; i < 4; ++i)
+            tc::tmem_ld_16x16(tmem + kColO + 64 * blk + 16 * ((u2 & 3) + (i >> 1)) + lanes + ((uint32_t)(16 * (i & 1)) << 16), x[i >> 1][i & 1]);
           tc::tmem_wait_ld();
-          if (!last && u > 0) {
-            if (gt < 2) tc::bulk_wait_read();
-            tc::named_bar(2 + g, kGroup);
-          }
-          uint8_t* turned = sm.base + kOffTurn + g * kTurn;
-          uint8_t* box = last ? sm.base + (2 * blk + (quad >> 1)) * (kH * 128) + h0 * 128 : turned + (quad >> 1) * (16 * 128);
-          const uint32_t dst = tc::smem_u32(box) + h8 * 128 + ((chunk ^ h8) << 4);
-          const bool turn = blk == 3 && quad >= 2 && a.inv_freq;
 #pragma unroll
-          for (int n8 = 0; n8 < 2; ++n8) {
-            const float2 f2 = *reinterpret_cast<const float2*>(fout + h0 + 8 * n8 + c2);
-            uint32_t y[4];
+          for (int s = 0; s < 2; ++s) {
+            const int u = u2 + s, h0 = 16 * (u & 3);
+            float v[2][8];  // of heads h0 + 8 n8 + c2 and the next one, dims 8 i + r
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {  // dims 8 i .. of the warp's 32
-              float v0 = __uint_as_float(x[i >> 1][4 * n8 + 2 * (i & 1)]) * f2.x;
-              float v1 = __uint_as_float(x[i >> 1][4 * n8 + 2 * (i & 1) + 1]) * f2.y;
-              if (turn) {  // the pair's other dim is four lanes on
-                const int ri = (32 * (quad - 2) + 8 * i + r) >> 1;
-                const float cs = rcos[ri], sn = r & 1 ? -rsin[ri] : rsin[ri];
-                const float o0 = __shfl_xor_sync(0xffffffffu, v0, 4), o1 = __shfl_xor_sync(0xffffffffu, v1, 4);
-                v0 = fmaf(v0, cs, o0 * sn);
-                v1 = fmaf(v1, cs, o1 * sn);
+            for (int n8 = 0; n8 < 2; ++n8) {
+              const float2 f2 = *reinterpret_cast<const float2*>(fout + h0 + 8 * n8 + c2);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                v[n8][2 * i] = __uint_as_float(x[s][i >> 1][4 * n8 + 2 * (i & 1)]) * f2.x;
+                v[n8][2 * i + 1] = __uint_as_float(x[s][i >> 1][4 * n8 + 2 * (i & 1) + 1]) * f2.y;
               }
-              const __nv_bfloat162 w = __floats2bfloat162_rn(v0, v1);
-              y[i] = *reinterpret_cast<const uint32_t*>(&w);
             }
-            tc::stmatrix_x4_trans(dst + 8 * n8 * 128, y);
-          }
-          if (last) continue;
-          tc::fence_proxy_async_smem();
-          tc::named_bar(2 + g, kGroup);
-          if (gt < 2) {
-            tc::tma_store_2d(&tm_out16, turned + gt * (16 * 128), 128 * blk + 64 * gt, k.q * kH + h0);
-            tc::bulk_commit();
+            if (turns && u >= 4) {  // the pair's other dim is four lanes on
+              float o[2][8];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i >> 3][i & 7] = __shfl_xor_sync(0xffffffffu, v[i >> 3][i & 7], 4);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i >> 3][i & 7] = fmaf(v[i >> 3][i & 7], cs[(i & 7) >> 1], o[i >> 3][i & 7] * sn[(i & 7) >> 1]);
+            }
+            // (on the way three buffers take turns: the third one back has been read by its copies)
+            if (!last && u >= 3) {
+              if (gt < 2) tc::bulk_wait_read<2>();
+              tc::named_bar(2 + g, kGroup);
+            }
+            uint8_t* turned = u % 3 == 0 ? sm.base + kOffTurn + g * kTurn : pbuf + (u % 3 - 1) * kTurn;
+            uint8_t* box = last ? sm.base + (2 * blk + (quad >> 1)) * (kH * 128) + h0 * 128 : turned + (quad >> 1) * (16 * 128);
+            const uint32_t dst = tc::smem_u32(box) + h8 * 128 + ((chunk ^ h8) << 4);
+#pragma unroll
+            for (int n8 = 0; n8 < 2; ++n8) {
+              uint32_t y[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 w = __floats2bfloat162_rn(v[n8][2 * i], v[n8][2 * i + 1]);
+                y[i] = *reinterpret_cast<const uint32_t*>(&w);
+              }
+              tc::stmatrix_x4_trans(dst + 8 * n8 * 128, y);
+            }
+            if (last) continue;
+            tc::fence_proxy_async_smem();
+            tc::named_bar(2 + g, kGroup);
+            if (gt < 2) {
+              tc::tma_store_2d(&tm_out16, turned + gt * (16 * 128), 128 * blk + 64 * gt, k.q * kH + h0);
+              tc::bulk_commit();
+            }
           }
         }
         if (last) {
@@ -731,8 +766,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::bulk_wait_read();
       tc::fence_before_sync();
       tc::named_bar(4, kSoft);  // (the buffers are free, O^T and the statistics have been read)
+      if (last) break;
       pre += k.tiles;
-      if (pre >= t1) break;
       k = next_query(a, k.q);
     }
     tc::bulk_wait();

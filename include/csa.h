@@ -642,7 +642,7 @@ csa_status csa_append_pages(const csa_layer* layer, const csa_pages* pages, cons
  *   no rotation of the output.
  * On the tensor cores (bf16, H = 64, D = 512, R = 64, page_rows a multiple of 8)
  * the queries enter the products as two E4M3 parts (the 8 bits of a bf16 value,
- * those 2^-14 below the head's largest fewer), the probabilities times the keys'
+ * those 2^-13 below the head's largest fewer), the probabilities times the keys'
  * scales as an E5M2 and an E4M3 part (7 bits, down to 2^-22 of the largest), sums
  * in fp32; the portable kernel takes any other layer, all in fp32.  A call's result
  * depends on how its keys are cut into tiles (by B, T and all lengths), not on the

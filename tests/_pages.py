@@ -123,9 +123,13 @@ def attend_ref(L, q, codes, s, sink, tensor_cores):
     n = lg.shape[1]
     err = A * (2 * d_lg + (n + 32) * U32)
     if tensor_cores:
-        # The queries' two E4M3 parts, the second 16 times finer: off by half of its smallest step, 2^-14 of the scale at
-        # which the head's largest value is at least 2^7 (so 2^-21 of it); exp2 and its argument's fp32 rounding.
-        err = err + A * (2 * scale * q.abs().amax(1, keepdim=True) * 2.0 ** -21 * keys.abs().sum(1).max() + 2.0 ** -20)
+        # The queries' two E4M3 parts: scaled so that the head's largest value is at least 2^7, the first holds four digits,
+        # exactly down to 2^-6 and within half of its smallest step, 2^-10, below; the second, 16 times finer, the four digits
+        # behind.  So values up to 2^-13 of the largest are off by at most 2^-17 of it, the others exact; exp2 and its
+        # argument's fp32 rounding.
+        top = q.abs().amax(1, keepdim=True)
+        low = (q.abs() <= top * 2.0 ** -13).to(F64) @ keys.abs().T
+        err = err + A * (2 * scale * top * 2.0 ** -17 * low.amax(1, keepdim=True) + 2.0 ** -20)
         # A weight below fp32's smallest normal number, 2^-126, counts as nothing (the hardware's exp2 flushes it): its
         # key's values are off by less than 2^-126 of themselves; with the sink far above every key that is all there is.
         err = err + 2.0 ** -126 * keys.abs().sum(0)
