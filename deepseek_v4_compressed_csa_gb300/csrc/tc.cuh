@@ -284,20 +284,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 
-// 16 lanes x 16 columns: thread t holds, for n < 2, columns 8 n + 2 (t % 4), + 1 of rows t / 4 (r[4 n], r[4 n + 1]) and
-// t / 4 + 8 (r[4 n + 2], r[4 n + 3]).
-__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
-// Four 8 x 8 tiles of 16-bit values, transposed: thread t holds row t / 4, columns 2 (t % 4), + 1 of tile i in r[i]; column c
-// of tile i is written as the 16 bytes at the address that thread 8 i + c gives.
-__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t* r) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3])
-               : "memory");
-}
 // 32 consecutive columns per thread, store.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -318,9 +304,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// 16 lanes x 16 columns, store: thread t holds, for n < 4, column 4 n + t % 4 of rows t / 4 (r[2 n]) and t / 4 + 8 (r[2 n + 1]).
+// 16 lanes x 16 columns, store: thread t holds, for n < 2, columns 8 n + 2 (t % 4), + 1 of rows t / 4 (r[4 n], r[4 n + 1]) and
+// t / 4 + 8 (r[4 n + 2], r[4 n + 3]).
 __device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
@@ -363,22 +350,6 @@ __device__ __forceinline__ void cp_async_wait_group() {
 __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
-// `bytes` (a multiple of 16) of shared memory to global memory, both 16-byte aligned, as part of the thread's bulk group
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
-               : "memory");
-}
-// 2-D tiled store, as part of the thread's bulk group; c0 = innermost coordinate (elements), c1 = row.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
-               "r"(smem_u32(src)), "r"(c0), "r"(c1)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// wait until the sources of this thread's bulk groups, but for the last kPending, have been read, or the copies are complete
-template <int kPending = 0>
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory"); }
-__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // barrier among `nthreads` threads (whole warps) on hardware barrier `id` (1..15)
 __device__ __forceinline__ void named_bar(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");

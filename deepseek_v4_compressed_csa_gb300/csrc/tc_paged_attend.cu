@@ -50,9 +50,7 @@ constexpr float kStep = 4.f;                  // how far a maximum may pass R
 constexpr float kHead = 2.f;                  // how far R is set above the first tile's maximum: most grow a little
 
 constexpr int kOffP = kStages * kStage;
-constexpr int kTurn = 16 * 256;                           // a group's buffer for outputs: 16 heads x 128 dims
-constexpr int kOffTurn = kOffP + 2 * kPBuf;
-constexpr int kOffScale = kOffTurn + 2 * kTurn;           // [kStages][64]
+constexpr int kOffScale = kOffP + 2 * kPBuf;              // [kStages][64]
 constexpr int kOffMask = kOffScale + kStages * kTile * 4; // [kStages] u64
 constexpr int kOffFac = kOffMask + kStages * 8 + 16;      // [2][64] factors of a group's rescale
 constexpr int kOffRef = kOffFac + 2 * kH * 4;             // [64] R
@@ -65,7 +63,7 @@ constexpr int kOffBars = kOffRope + 64 * 4;
 constexpr int kOffTmem = kOffBars + 32 * 8;
 constexpr int kOffPlan = kOffTmem + 32;                   // PagedRun, scratch of the plan
 constexpr int kSmem = kOffPlan + (int)sizeof(PagedRun) + 4 * kPlanInts + 1024;
-static_assert(kOffBars % 8 == 0 && kOffTurn % 1024 == 0 && kOffFac % 16 == 0 && kOffOut % 16 == 0 && kOffPlan % 16 == 0 && sizeof(PagedRun) % 16 == 0 && kSmem <= 232448, "shared memory");
+static_assert(kOffBars % 8 == 0 && kOffFac % 16 == 0 && kOffOut % 16 == 0 && kOffPlan % 16 == 0 && sizeof(PagedRun) % 16 == 0 && kSmem <= 232448, "shared memory");
 
 // 2^x by the hardware approximation (relative error ~2^-22; results below 2^-126 flush to zero)
 __device__ __forceinline__ float ex2(float x) {
@@ -131,8 +129,7 @@ __device__ __forceinline__ bool warp_wait(const Smem& sm, uint64_t* bar, uint32_
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    k_tc_attend_pages(const __grid_constant__ CUtensorMap tm_runs, const __grid_constant__ CUtensorMap tm_out16,
-                      const __grid_constant__ CUtensorMap tm_out64, const __grid_constant__ PagedArgs a) {
+    k_tc_attend_pages(const __grid_constant__ CUtensorMap tm_runs, const __grid_constant__ PagedArgs a) {
   if (a.merge) pdl_trigger();  // (what follows otherwise finds the outputs written)
   extern __shared__ uint8_t smem_raw[];
   Smem sm;
@@ -156,7 +153,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     tc::tma_prefetch(&tm_runs);
-    tc::tma_prefetch(&tm_out64);
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(sm.full + i, 1 + 32);  // the copies, and the loader's lanes for the scales (or all they copy)
       tc::mbar_init(sm.empty + i, 1);
@@ -179,20 +175,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool soft = warp > kMmaWarp;
   const float freq = soft && a.inv_freq ? __ldg(a.inv_freq + lane) : 0.f;
   const float z2 = soft && a.sink ? __ldg(a.sink + 16 * (warp & 3) + (lane & 15)) * 1.4426950408889634f : -INFINITY;
-  PagedRun* plan = reinterpret_cast<PagedRun*>(sm.base + kOffPlan);
-  paged_plan<kThreads / 32>(a, plan, reinterpret_cast<int*>(plan + 1));
-  const int t0 = plan->t0, t1 = plan->t1;
-  if (t0 >= t1) return;  // (all of the block)
-  const int pre0 = plan->pre;
-  const PagedQuery k0 = plan->k;
-  if (warp == kMmaWarp) {
+  if (warp == kMmaWarp) {  // (while the plan is made, whose barrier stands behind this)
     tc::tmem_alloc(tmem_slot, kCols);
     tc::tmem_relinquish();
   }
+  PagedRun* plan = reinterpret_cast<PagedRun*>(sm.base + kOffPlan);
   tc::fence_before_sync();
-  __syncthreads();
+  paged_plan<kThreads / 32>(a, plan, reinterpret_cast<int*>(plan + 1));
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  const int t0 = plan->t0, t1 = plan->t1;
+  if (t0 >= t1) {  // (all of the block)
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kCols);
+    return;
+  }
+  const int pre0 = plan->pre;
+  const PagedQuery k0 = plan->k;
 
   if (warp < kLoaders) {
     // ------------------------------------------------------------ loaders: warp w takes the tiles j with j % 3 == w
@@ -406,26 +404,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (true) {
       const int begin = max(t0 - pre, 0), end = min(t1 - pre, k.tiles), n = end - begin;
       // ---- the query as two parts of 2^-e q into tensor memory, a group half of the dims: a thread has, of rows lane / 4
-      // and lane / 4 + 8 of its quarter's 16 heads, every fourth four values (every product that read the last query's
+      // and lane / 4 + 8 of its quarter's 16 heads, every fourth eight values (every product that read the last query's
       // parts has retired)
       {
         const int r = lane >> 2;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)k.q * kH + 16 * quad + r) * kD + 256 * g + 4 * (lane & 3);
-        uint2 v[2][16];
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)k.q * kH + 16 * quad + r) * kD + 256 * g + 8 * (lane & 3);
+        uint4 v[2][8];  // (a line of memory a row and load: what the loads take is counted in lines, a clock each)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          v[0][e] = tc::ld_nc_v2_now(src + 16 * e);
-          v[1][e] = tc::ld_nc_v2_now(src + 8 * kD + 16 * e);
+        for (int e = 0; e < 8; ++e) {
+          v[0][e] = tc::ld_nc_v4_now(src + 32 * e);
+          v[1][e] = tc::ld_nc_v4_now(src + 8 * kD + 32 * e);
         }
         uint32_t* amax = reinterpret_cast<uint32_t*>(sm.base + kOffMax);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           __nv_bfloat162 m4[4];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const __nv_bfloat162 u = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[x][e].x)),
-                                                 __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[x][e].y)));
-            m4[e & 3] = e < 4 ? u : __hmax2_nan(m4[e & 3], u);
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t w[4] = {v[x][e].x, v[x][e].y, v[x][e].z, v[x][e].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 u = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+              m4[i] = e == 0 ? u : __hmax2_nan(m4[i], u);
+            }
           }
           const __nv_bfloat162 m2 = __hmax2_nan(__hmax2_nan(m4[0], m4[1]), __hmax2_nan(m4[2], m4[3]));
           uint32_t mx = *reinterpret_cast<const uint32_t*>(&m2) & 0x7fff7fffu;
@@ -448,16 +449,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // hi: the value cut to the four digits that E4M3 has, lo: the four behind them, both exact, as are the products with
         // powers of two, so bf16 pairs do.  (hi below E4M3's normal numbers, 2^-13 of the head's largest, is rounded, by at
         // most 2^-17 of that.  With lo from what hi became, converted back, it would be 2^-21, and 3K clocks instead of 2K.)
-        auto parts = [&](int x, const uint2& u, uint32_t* hi, uint32_t* lo) {
+        auto parts = [&](int x, uint32_t u0, uint32_t u1, uint32_t* hi, uint32_t* lo) {
           float h[4], l[4];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t w = i ? u.y : u.x, m = w & 0xfff0fff0u;
+            const uint32_t w = i ? u1 : u0, m = w & 0xfff0fff0u;
             const __nv_bfloat162 wv = *reinterpret_cast<const __nv_bfloat162*>(&w), mv = *reinterpret_cast<const __nv_bfloat162*>(&m);
             const __nv_bfloat162 a2 = __hmul2(mv, inv[x]), b2 = __hmul2(__hsub2(wv, mv), inv16[x]);
             const uint32_t aw = *reinterpret_cast<const uint32_t*>(&a2), bw = *reinterpret_cast<const uint32_t*>(&b2);
             h[2 * i] = __uint_as_float(aw << 16); h[2 * i + 1] = __uint_as_float(aw & 0xffff0000u);
-            l[2 * i] = __uint_as_float(bw << 16); l[2 * i + 1] = __uint_as_float(bw & 0xffff0000u);
+            l[2 * i] = __uint_as_float(bw << 16); l[2 * i + 1] = __uint_as_float(bw);  // (what is behind its four digits rounds away)
           }
           *hi = e4m3x4(h[0], h[1], h[2], h[3]);
           *lo = e4m3x4(l[0], l[1], l[2], l[3]);
@@ -470,9 +471,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) parts(x, v[x][e], hi + 2 * e + x, lo + 2 * e + x);
+            for (int e = 0; e < 2; ++e) {
+              parts(x, v[x][e].x, v[x][e].y, hi + 4 * e + 2 * x, lo + 4 * e + 2 * x);
+              parts(x, v[x][e].z, v[x][e].w, hi + 4 * e + 2 * x + 1, lo + 4 * e + 2 * x + 1);
+            }
 #pragma unroll
-            for (int e = 0; e < 12; ++e) v[x][e] = v[x][e + 4];
+            for (int e = 0; e < 6; ++e) v[x][e] = v[x][e + 2];
           }
           const uint32_t col = tmem + kColQ + 64 * g + 16 * round + lanes;
           tc::tmem_st_16x16(col, hi);
@@ -621,9 +625,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       j += n;
       // (the group that has not the last tile: it waits for the other one; earlier, its instructions arrive behind the keys)
       if ((j & 1) == g && gt < 32 && a.inv_freq) turn_cs(k.p, freq, rcos + gt, rsin + gt);
-      // ---- the run's part of this query, or its output, through shared memory: small buffers, or, behind the block's last
-      // tile, the stages, which hold all of it at once
-      const bool whole = begin == 0 && end == k.tiles, last = pre + k.tiles >= t1;
+      // ---- the run's part of this query, or its output
+      const bool whole = begin == 0 && end == k.tiles;
       const size_t slot = 2 * blockIdx.x + (begin == 0 ? 1 : 0);
       tc::named_bar(4, kSoft);  // (both groups' statistics, the last R, the angles)
       if (begin == 0 && !whole && g == 1 && gt < kR / 2 && a.inv_freq)
@@ -646,131 +649,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (j >= 2) wait(sm, sm.pv_done + (j & 1), ((j - 2) >> 1) & 1);  // (the other buffer's, retired before)
       tc::fence_after_sync();
       tc::named_bar(4, kSoft);
-      if (whole) {
-        // 16 heads x 128 dims of bf16 a step: accumulators as 8 x 8 tiles (dims x heads), which stmatrix turns, into boxes of
-        // 64 dims in the 128-byte swizzle (a head's row 128 bytes) that go out by one copy each: of 64 heads at the end, of
-        // 16 on the way.  (A copy a head, 1 KB each, cost 4K clocks: a lane's copies are issued one after another.)
-        const int r = lane >> 2, c2 = 2 * (lane & 3), chunk = 4 * (quad & 1) + (lane >> 3), h8 = lane & 7;
-        float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};  // of the lane's dims of the last 64
-        const bool turns = g == 1 && quad >= 2 && a.inv_freq;
-        if (turns) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int ri = (32 * (quad - 2) + 8 * i + r) >> 1;
-            cs[i] = rcos[ri];
-            sn[i] = r & 1 ? -rsin[ri] : rsin[ri];
-          }
-        }
+      // 32 heads of the warp's 32 dims a step, a lane a dim, from tensor memory to where they go: a part's 128 bytes a head in
+      // one store, of an output's two heads 64 bytes each, their pairs of dims put together by one shuffle.  (Through shared
+      // memory, turned by stmatrix, and from there by copies of boxes, it took 5.4K clocks; so it takes 2K.)
+      const bool odd = lane & 1;
 #pragma unroll 1
-        for (int u2 = 0; u2 < 8; u2 += 2) {  // (two steps' accumulators at once)
-          const int blk = 2 * g + (u2 >> 2);
-          uint32_t x[2][2][8];
+      for (int c = 0; c < 4; ++c) {
+        const int blk = 2 * g + (c >> 1), h0 = 32 * (c & 1);
+        uint32_t x[32];
+        tc::tmem_ld32(tmem + kColO + 64 * blk + h0 + lanes, x);
+        tc::tmem_wait_ld();
+        float v[32];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            tc::tmem_ld_16x16(tmem + kColO + 64 * blk + 16 * ((u2 & 3) + (i >> 1)) + lanes + ((uint32_t)(16 * (i & 1)) << 16), x[i >> 1][i & 1]);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const int u = u2 + s, h0 = 16 * (u & 3);
-            float v[2][8];  // of heads h0 + 8 n8 + c2 and the next one, dims 8 i + r
-#pragma unroll
-            for (int n8 = 0; n8 < 2; ++n8) {
-              const float2 f2 = *reinterpret_cast<const float2*>(fout + h0 + 8 * n8 + c2);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                v[n8][2 * i] = __uint_as_float(x[s][i >> 1][4 * n8 + 2 * (i & 1)]) * f2.x;
-                v[n8][2 * i + 1] = __uint_as_float(x[s][i >> 1][4 * n8 + 2 * (i & 1) + 1]) * f2.y;
-              }
-            }
-            if (turns && u >= 4) {  // the pair's other dim is four lanes on
-              float o[2][8];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i >> 3][i & 7] = __shfl_xor_sync(0xffffffffu, v[i >> 3][i & 7], 4);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i >> 3][i & 7] = fmaf(v[i >> 3][i & 7], cs[(i & 7) >> 1], o[i >> 3][i & 7] * sn[(i & 7) >> 1]);
-            }
-            // (on the way three buffers take turns: the third one back has been read by its copies)
-            if (!last && u >= 3) {
-              if (gt < 2) tc::bulk_wait_read<2>();
-              tc::named_bar(2 + g, kGroup);
-            }
-            uint8_t* turned = u % 3 == 0 ? sm.base + kOffTurn + g * kTurn : pbuf + (u % 3 - 1) * kTurn;
-            uint8_t* box = last ? sm.base + (2 * blk + (quad >> 1)) * (kH * 128) + h0 * 128 : turned + (quad >> 1) * (16 * 128);
-            const uint32_t dst = tc::smem_u32(box) + h8 * 128 + ((chunk ^ h8) << 4);
-#pragma unroll
-            for (int n8 = 0; n8 < 2; ++n8) {
-              uint32_t y[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 w = __floats2bfloat162_rn(v[n8][2 * i], v[n8][2 * i + 1]);
-                y[i] = *reinterpret_cast<const uint32_t*>(&w);
-              }
-              tc::stmatrix_x4_trans(dst + 8 * n8 * 128, y);
-            }
-            if (last) continue;
-            tc::fence_proxy_async_smem();
-            tc::named_bar(2 + g, kGroup);
-            if (gt < 2) {
-              tc::tma_store_2d(&tm_out16, turned + gt * (16 * 128), 128 * blk + 64 * gt, k.q * kH + h0);
-              tc::bulk_commit();
-            }
-          }
+        for (int e4 = 0; e4 < 8; ++e4) {
+          const float4 f4 = *reinterpret_cast<const float4*>(fout + h0 + 4 * e4);
+          v[4 * e4] = __uint_as_float(x[4 * e4]) * f4.x;
+          v[4 * e4 + 1] = __uint_as_float(x[4 * e4 + 1]) * f4.y;
+          v[4 * e4 + 2] = __uint_as_float(x[4 * e4 + 2]) * f4.z;
+          v[4 * e4 + 3] = __uint_as_float(x[4 * e4 + 3]) * f4.w;
         }
-        if (last) {
-          tc::fence_proxy_async_smem();
-          tc::named_bar(2 + g, kGroup);
-          if (lane == 0) {
-            const int bx = 4 * g + quad;
-            tc::tma_store_2d(&tm_out64, sm.base + bx * (kH * 128), 64 * bx, k.q * kH);
-            tc::bulk_commit();
-          }
+        if (!whole) {
+          float* part = a.part + slot * kH * kD + (size_t)((blk * 4 + quad) * kH + h0) * 32 + lane;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) part[32 * e] = v[e];
+          continue;
         }
-      } else {
-        // a warp's 32 dims of 64 heads, twice: 8 KB at once in the stages, or 16 heads a step
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const int blk = 2 * g + (c >> 1), h0 = 32 * (c & 1);
-          float* part = a.part + slot * kH * kD + (size_t)((blk * 4 + quad) * kH + h0) * 32;
-          uint32_t x[32];
-          tc::tmem_ld32(tmem + kColO + 64 * blk + h0 + lanes, x);
-          tc::tmem_wait_ld();
-          uint8_t* buf = last ? sm.base + ((blk * 4 + quad) * kH + h0) * 128 : pbuf + quad * 2048;
+        if (blk == 3 && quad >= 2 && a.inv_freq) {  // the last 64 dims: the pair's other one is the next lane's
+          const int ri = (32 * (quad - 2) + lane) >> 1;
+          const float cs = rcos[ri], sn = odd ? -rsin[ri] : rsin[ri];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (!last && c + half > 0) {
-              if (lane == 0) tc::bulk_wait_read();
-              __syncwarp();
-            }
-            float* dst = reinterpret_cast<float*>(buf) + (last ? 512 * half : 0) + lane;
+          for (int e = 0; e < 32; ++e) v[e] = fmaf(v[e], cs, __shfl_xor_sync(0xffffffffu, v[e], 1) * sn);
+        }
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + ((size_t)k.q * kH + h0 + odd) * kD + 128 * blk + 32 * quad + (lane & ~1);
 #pragma unroll
-            for (int e4 = 0; e4 < 4; ++e4) {
-              const float4 f4 = *reinterpret_cast<const float4*>(fout + h0 + 16 * half + 4 * e4);
-              const uint32_t* y = x + 16 * half + 4 * e4;
-              dst[32 * (4 * e4)] = __uint_as_float(y[0]) * f4.x;
-              dst[32 * (4 * e4 + 1)] = __uint_as_float(y[1]) * f4.y;
-              dst[32 * (4 * e4 + 2)] = __uint_as_float(y[2]) * f4.z;
-              dst[32 * (4 * e4 + 3)] = __uint_as_float(y[3]) * f4.w;
-            }
-            if (!last || (half && (c & 1))) {
-              tc::fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                if (last) tc::bulk_store(part - 1024, buf - 4096, 8192);
-                else tc::bulk_store(part + 512 * half, buf, 2048);
-                tc::bulk_commit();
-              }
-            }
-          }
+        for (int e = 0; e < 32; e += 2) {  // even lanes take the first head of two, odd lanes the second
+          const float got = __shfl_xor_sync(0xffffffffu, odd ? v[e] : v[e + 1], 1), keep = odd ? v[e + 1] : v[e];
+          *reinterpret_cast<__nv_bfloat162*>(o + e * kD) = __floats2bfloat162_rn(odd ? got : keep, odd ? keep : got);
         }
       }
-      tc::bulk_wait_read();
       tc::fence_before_sync();
-      tc::named_bar(4, kSoft);  // (the buffers are free, O^T and the statistics have been read)
-      if (last) break;
+      tc::named_bar(4, kSoft);  // (O^T and the statistics have been read)
       pre += k.tiles;
+      if (pre >= t1) break;
       k = next_query(a, k.q);
     }
-    tc::bulk_wait();
   }
   // ---- everything in flight has landed and retired before shared and tensor memory go
   tc::fence_before_sync();
@@ -796,13 +718,10 @@ bool tc_paged_supported(const Dims& L, int P) {
 
 cudaError_t launch_tc_paged(const PagedArgs& a, cudaStream_t s) {
   const uint64_t rows = (uint64_t)a.n_pages * a.P;
-  const uint64_t heads = (uint64_t)a.B * a.T * kH;
-  CUtensorMap tm_runs, tm_out16, tm_out64;
-  if (!make_tmap_2d_u8(&tm_runs, a.codes, rows, kD, kD, 128, 1u << a.shift, true) ||
-      !make_tmap_2d_bf16(&tm_out16, a.out, heads, kD, 2 * kD, 16) || !make_tmap_2d_bf16(&tm_out64, a.out, heads, kD, 2 * kD, kH))
-    return cudaErrorInvalidValue;
+  CUtensorMap tm_runs;
+  if (!make_tmap_2d_u8(&tm_runs, a.codes, rows, kD, kD, 128, 1u << a.shift, true)) return cudaErrorInvalidValue;
   allow_smem<kSmem>(k_tc_attend_pages);
-  CSA_LAUNCH(k_tc_attend_pages, dim3(kPagedBlocks), dim3(kThreads), kSmem, s, tm_runs, tm_out16, tm_out64, a);
+  CSA_LAUNCH(k_tc_attend_pages, dim3(kPagedBlocks), dim3(kThreads), kSmem, s, tm_runs, a);
   return cudaGetLastError();
 }
 
