@@ -85,7 +85,7 @@ struct PagedQuery {
   int q, b, p, n0, f, w0, nw, n_rows, tiles;
 };
 
-// Tiles of a.tile keys.  shift == 0: the keys in a row.  Else (the tensor-core kernel) a selection's rows by themselves,
+// Tiles of a.tile keys, a power of two.  shift == 0: the keys in a row.  Else (the tensor-core kernel) a selection's rows by themselves,
 // then runs of 2^shift rows, which lie in one page each, some to a tile.
 struct TileCut {
   int sel_tiles, runs0, runs1, runs2;  // runs of rows, of first tokens, of window tokens
@@ -94,7 +94,7 @@ struct TileCut {
 __device__ __forceinline__ TileCut cut_tiles(bool selected, const PagedQuery& k, int tile, int shift) {
   TileCut c;  // (tables hold at most 2^30 rows: no sum overflows)
   const int u = 1 << shift;
-  c.sel_tiles = selected ? (k.n0 + tile - 1) / tile : 0;
+  c.sel_tiles = selected ? (k.n0 + tile - 1) >> (31 - __clz(tile)) : 0;
   c.runs0 = selected ? 0 : (k.n0 + u - 1) >> shift;
   c.runs1 = (k.f + u - 1) >> shift;
   c.w_run = k.w0 >> shift;
@@ -144,7 +144,8 @@ __device__ __forceinline__ PagedQuery find_query(const PagedArgs& a, int q, bool
     }
     const TileCut c = cut_tiles(a.sel != nullptr && a.shift > 0, k, a.tile, a.shift);
     const int per = a.tile >> a.shift;
-    k.tiles = max(1, c.sel_tiles + (int)(((long long)c.runs0 + c.runs1 + c.runs2 + per - 1) / per));
+    const unsigned runs = (unsigned)c.runs0 + c.runs1 + c.runs2;  // (at most 2^30 each)
+    k.tiles = max(1, c.sel_tiles + (int)((runs + per - 1) >> (31 - __clz(per))));
   }
   if (report && bits) atomicOr(a.err, bits);
   return k;
@@ -175,6 +176,7 @@ struct PagedRun {
   PagedQuery k;    // that query
 };
 constexpr int kPlanInts = 96;  // scratch of paged_plan
+constexpr int kPlanWarp = 32;  // queries whose plan one warp makes
 
 __device__ __forceinline__ unsigned div_up(unsigned n, unsigned d) { return (n + d - 1) / d; }
 
@@ -369,7 +371,7 @@ __device__ __noinline__ void paged_plan_block(const PagedArgs& a, PagedRun* sm, 
 
 template <int nw>
 __device__ __forceinline__ void paged_plan(const PagedArgs& a, PagedRun* sm, int* scratch) {
-  if (a.B * a.T <= 32) paged_plan_warp(a, sm);
+  if (a.B * a.T <= kPlanWarp) paged_plan_warp(a, sm);
   else paged_plan_block<nw>(a, sm, scratch);
 }
 

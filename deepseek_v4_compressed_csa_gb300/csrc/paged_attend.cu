@@ -218,7 +218,9 @@ cudaError_t simt_c(const PagedArgs& a, cudaStream_t s) {
 // of which none was split.  So a block finds the split queries itself and walks their items, one in most calls: all
 // accumulators of 8 queries or of one long one fit the device's registers.
 constexpr int kMergeWarps = 8;
-__host__ __device__ constexpr int merge_ahead(int chunks) { return 16 / chunks; }  // parts in flight a warp: 64 registers
+// Parts in flight a warp, 4 chunks registers each: all that a long query's warp has to take (the first of a second round
+// cost 2 us), or as many as fit the registers of two blocks an SM
+__host__ __device__ constexpr int merge_ahead(int chunks) { return chunks == 1 ? kPagedBlocks / kMergeWarps : 10; }
 
 template <typename T, int kC>
 __global__ void __launch_bounds__(32 * kMergeWarps, 2) k_merge_pages(const __grid_constant__ PagedArgs a, int share) {
@@ -386,8 +388,8 @@ cudaError_t merge_c(const PagedArgs& a, cudaStream_t s) {
 }
 template <typename T>
 cudaError_t launch_merge(const PagedArgs& a, cudaStream_t s) {
-  // items enough for every SM: a quarter of the Flash row's values for up to four queries
-  return a.D <= 128 || a.B * a.T <= 4 ? merge_c<T, 1>(a, s) : merge_c<T, 4>(a, s);
+  // items enough for every SM: a quarter of the Flash row's values for up to four queries, else half
+  return a.D <= 128 || a.B * a.T <= 4 ? merge_c<T, 1>(a, s) : merge_c<T, 2>(a, s);
 }
 
 // Whether queries are short enough to stay whole, by what the call's sizes say: then no merge follows.  Splitting them pays
