@@ -21,6 +21,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libcsa.so")
+_TENSORS_PATH = os.path.join(_HERE, "_lib", "libcsa_tensors.so")
 _CHECKS_PATH = os.path.join(_HERE, "_lib", "csa_checks" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 CSA_F32, CSA_BF16 = 0, 1
@@ -153,6 +154,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         _addresses = module.addresses
         module.setup(torch.float32, torch.uint8, torch.int32, torch._C._cuda_getCurrentRawStream,
                      torch._C._cuda_getDevice)
+        if os.path.exists(_TENSORS_PATH):
+            try:
+                tensors = ctypes.CDLL(_TENSORS_PATH)  # (stays loaded: nothing unloads it)
+                module.tensors(ctypes.cast(tensors.csa_tensor, ctypes.c_void_p).value)
+            except OSError:  # built for another torch: attributes will do
+                pass
         for name in ("add_norm", "append_pages", "attend_pages"):
             _at[name] = ctypes.cast(getattr(lib, "csa_" + name), ctypes.c_void_p).value
         _plain = module

@@ -159,8 +159,9 @@ def _run(which, tensors, rest, fake=True):
 
 @pytest.fixture
 def calls(monkeypatch):
-    """What the binding would hand to the library; nothing is launched."""
+    """What the binding would hand to the library; nothing is launched (nor by the calls made in C, where a GPU is)."""
     got = []
+    monkeypatch.setattr(B, "_plain", None)
     monkeypatch.setattr(B, "_tree_call", lambda fn, dev, stream, *args: got.append((fn, args)))
     return got
 
