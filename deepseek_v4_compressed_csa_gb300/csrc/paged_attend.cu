@@ -14,27 +14,35 @@ namespace {
 
 // ---------------------------------------------------------------- the portable kernel
 // A tile's keys wait in shared memory as fp32; the next tile's codes are on their way in registers meanwhile, and the rows
-// of the one after it are looked up.  A warp takes a head: a lane a key for the logits, then lanes share a key's dims (rows
-// of up to 128 dims: several keys at a time) for the sums.
-constexpr int kSimtTile = 32;   // keys a tile: a lane each
-constexpr int kSimtWarps = 8;   // heads at a time, a warp each
+// of the one after it are looked up.  A warp takes kN heads and 32 of the tile's 32 kN keys: a lane a key for the logits,
+// then lanes share a key's dims (rows of up to 128 dims: several keys at a time) for the sums; the warps of a head are put
+// together behind the last tile.  What bounds it is reading the keys from shared memory, twice a head: 60 queries of 1K keys
+// (8 heads of 64 dims) take 38 us with a warp a head, 28 with a warp two, 23.5 with four.  Where a block has up to three tiles,
+// most warps have no keys with four, and two are better (a window of 32: 6.5 us against 7.1).
+constexpr int kSimtWarps = 8;   // and heads at a time
 constexpr int kSimtPad = 4;     // floats behind a key's row: lanes read their keys' chunks without bank conflicts
-constexpr int kSimtSmemMax = (kSimtTile * (1024 + kSimtPad) + kSimtWarps * 1024) * 4;
+__host__ __device__ constexpr int simt_heads(int chunks) { return 4 / chunks; }  // the most heads a warp, and tiles at once
+__host__ __device__ constexpr int simt_chunks(int D) { return D <= 256 ? 1 : D <= 512 ? 2 : 4; }
+__host__ __device__ constexpr int simt_smem(int D) {
+  return (32 * simt_heads(simt_chunks(D)) * (D + kSimtPad) + kSimtWarps * D) * 4;
+}
+constexpr int kSimtSmemMax = simt_smem(1024);
+static_assert(simt_smem(256) <= kSimtSmemMax && simt_smem(512) <= kSimtSmemMax && kSimtSmemMax <= 232448, "shared memory");
 
-__host__ __device__ constexpr int simt_smem(int D) { return (kSimtTile * (D + kSimtPad) + kSimtWarps * D) * 4; }
-
-// kC: chunks of 8 dims a lane holds (D <= 256 kC); a tile's codes are kTile / 8 kC chunks a thread
-template <typename T, int kC>
-__global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __grid_constant__ PagedArgs a) {
+// kC: chunks of 8 dims a lane holds (D <= 256 kC)
+template <typename T, int kC, int kN>
+__global__ void __launch_bounds__(32 * kSimtWarps, 1) k_attend_pages_simt(const __grid_constant__ PagedArgs a) {
   if (a.merge) pdl_trigger();  // (what follows otherwise finds the outputs written)
   extern __shared__ __align__(16) float sm_pa[];
-  __shared__ int s_row[2][kSimtTile];
+  constexpr int kTile = 32 * kN;  // kN tiles of the plan at once
+  __shared__ int s_row[2][kTile];
+  __shared__ float2 s_ml[kN * kSimtWarps];
   __shared__ __align__(16) int s_plan[kPlanInts];
   __shared__ PagedRun s_run;
-  constexpr int kU = kSimtTile * 32 * kC / (32 * kSimtWarps);  // chunks of a tile a thread copies
+  constexpr int kPass = kTile / kSimtWarps;  // rows of a tile a thread copies (one of kC chunks of) at most
   const int D = a.D, KS = D + kSimtPad, n8 = D >> 3;
-  float* ks = sm_pa;                    // [kSimtTile][KS] keys
-  float* qs = sm_pa + kSimtTile * KS;   // [kSimtWarps][D] queries of this group of heads
+  float* ks = sm_pa;                    // [kTile][KS] keys
+  float* qs = sm_pa + kTile * KS;       // [kSimtWarps][D] queries of this group of heads
   pdl_wait();
   paged_plan<kSimtWarps>(a, &s_run, s_plan);
   const int t0 = s_run.t0, t1 = s_run.t1;
@@ -46,10 +54,12 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
   int share = 32;
   while (share > 1 && share / 2 >= n8) share /= 2;
   const int sub = lane & (share - 1), group = lane / share, groups = 32 / share;
+  const int head0 = warp % (kSimtWarps / kN) * kN, key0 = warp / (kSimtWarps / kN) * 32;  // the warp's heads and keys
+  const int row0 = warp * groups + group, rows = kSimtWarps * groups;  // rows that the block copies at once, and the lane's
 #pragma unroll 1
   while (true) {
     const int q = k.q, b = k.b;
-    const int begin = max(t0 - pre, 0), end = min(t1 - pre, k.tiles), nkeys = k.n0 + k.f + k.nw;
+    const int begin = max(t0 - pre, 0), end = min(t1 - pre, k.tiles), stop = min(k.n0 + k.f + k.nw, 32 * end);
     const bool whole = begin == 0 && end == k.tiles;
     const int slot = 2 * blockIdx.x + (begin == 0 ? 1 : 0);
     if (begin == 0 && !whole && a.inv_freq)  // (for the merge: an angle costs a lane some hundred instructions)
@@ -58,9 +68,9 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
         turn_cs(k.p, __ldg(a.inv_freq + i), &t.x, &t.y);
         a.turns[(size_t)blockIdx.x * (a.R / 2) + i] = t;
       }
-    // key x of the query: its physical row, -1 for none (thread x - 32 t of a tile)
+    // key x of the query: its physical row, -1 for none (a thread a key of a tile)
     auto row_of = [&](int x) {
-      if (x >= nkeys) return -1;
+      if (x >= stop) return -1;
       int r = -1;
       if (x < k.n0) {
         const int j = a.sel ? __ldg(a.sel + (size_t)q * a.topk + x) : x;
@@ -82,83 +92,152 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
         if (h0 + hh < a.H) load8(static_cast<const T*>(a.q) + ((size_t)q * a.H + h0 + hh) * D + c, v);
         store8(qs + hh * D + c, v);
       }
-      if (tid < kSimtTile) s_row[begin & 1][tid] = row_of(begin * kSimtTile + tid);
+      if (tid < kTile) s_row[0][tid] = row_of(begin * 32 + tid);
       __syncthreads();
-      uint2 code[kU];
-      float scale[kU];
-      auto fetch = [&](int t) {  // the codes of tile t, whose rows are there
+      uint2 code[kPass][kC];
+      float scale[kPass];
+      auto fetch = [&](int t, int buf) {  // the codes of the tiles from t on, whose rows are there
 #pragma unroll
-        for (int i = 0; i < kU; ++i) {
-          const int e = tid + i * 32 * kSimtWarps, x = e / n8, c = (e - x * n8) * 8, r = x < kSimtTile ? s_row[t & 1][x] : -1;
-          code[i] = r >= 0 ? __ldg(reinterpret_cast<const uint2*>(a.codes + (size_t)r * D + c)) : make_uint2(0u, 0u);
+        for (int i = 0; i < kPass; ++i) {
+          if (row0 + i * rows >= min(kTile, 32 * (end - t))) break;
+          const int r = s_row[buf][row0 + i * rows];
           scale[i] = r >= 0 ? __ldg(a.scales + r) : 0.f;
+#pragma unroll
+          for (int c = 0; c < kC; ++c)
+            code[i][c] = r >= 0 && sub + 32 * c < n8 ? __ldg(reinterpret_cast<const uint2*>(a.codes + (size_t)r * D + 8 * (sub + 32 * c)))
+                                                     : make_uint2(0u, 0u);
         }
       };
-      fetch(begin);
-      float m = -INFINITY, l = 0.f;
-      float acc[kC][8];
+      fetch(begin, 0);
+      float ms[kN], ls[kN], sums[kN][kC][8];
 #pragma unroll
-      for (int c = 0; c < kC; ++c)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[c][e] = 0.f;
-#pragma unroll 1
-      for (int t = begin; t < end; ++t) {
-        if (tid < kSimtTile && t + 1 < end) s_row[(t + 1) & 1][tid] = row_of((t + 1) * kSimtTile + tid);
-        __syncthreads();  // (the tile before has been read; the next one's rows are there)
-#pragma unroll
-        for (int i = 0; i < kU; ++i) {
-          const int e = tid + i * 32 * kSimtWarps, x = e / n8, c = (e - x * n8) * 8;
-          if (x >= kSimtTile) continue;
-          const float s = scale[i];
-          const float2 f[4] = {e4m3x2_f(code[i].x), e4m3x2_f(code[i].x >> 16), e4m3x2_f(code[i].y), e4m3x2_f(code[i].y >> 16)};
-          const float v[8] = {f[0].x * s, f[0].y * s, f[1].x * s, f[1].y * s, f[2].x * s, f[2].y * s, f[3].x * s, f[3].y * s};
-          store8(ks + x * KS + c, v);
-        }
-        const bool on = s_row[t & 1][lane] >= 0;
-        if (t + 1 < end) fetch(t + 1);
-        __syncthreads();
-        float d4[4] = {0.f, 0.f, 0.f, 0.f};
-        {
-          const float* kr = ks + lane * KS;
-          const float* qh = qs + warp * D;
-#pragma unroll 4
-          for (int c = 0; c < D; c += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(kr + c), y = *reinterpret_cast<const float4*>(qh + c);
-            d4[0] = fmaf(x.x, y.x, d4[0]);
-            d4[1] = fmaf(x.y, y.y, d4[1]);
-            d4[2] = fmaf(x.z, y.z, d4[2]);
-            d4[3] = fmaf(x.w, y.w, d4[3]);
-          }
-        }
-        const float lg = on ? ((d4[0] + d4[1]) + (d4[2] + d4[3])) * a.scale2 : -INFINITY;
-        const float mn = fmaxf(m, warp_max(lg)), ref = mn == -INFINITY ? 0.f : mn;
-        const float p = exp2f(lg - ref), f = exp2f(m - ref);
-        l = fmaf(l, f, warp_sum(p));
-        m = mn;
+      for (int n = 0; n < kN; ++n) {
+        ms[n] = -INFINITY;
+        ls[n] = 0.f;
 #pragma unroll
         for (int c = 0; c < kC; ++c)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[c][e] *= f;
-        const int nk = min(kSimtTile, nkeys - t * kSimtTile);  // (rows behind the last hold zeros, and p is 0)
+          for (int e = 0; e < 8; ++e) sums[n][c][e] = 0.f;
+      }
+#pragma unroll 1
+      for (int t = begin, buf = 0; t < end; t += kN, buf ^= 1) {
+        if (tid < kTile && t + kN < end) s_row[buf ^ 1][tid] = row_of((t + kN) * 32 + tid);
+        __syncthreads();  // (the tiles before have been read; the next ones' rows are there)
+#pragma unroll
+        for (int i = 0; i < kPass; ++i) {
+          if (row0 + i * rows >= min(kTile, 32 * (end - t))) break;
+          const float s = scale[i];
+#pragma unroll
+          for (int c = 0; c < kC; ++c) {
+            if (sub + 32 * c >= n8) continue;
+            const uint2 u = code[i][c];
+            const float2 f[4] = {e4m3x2_f(u.x), e4m3x2_f(u.x >> 16), e4m3x2_f(u.y), e4m3x2_f(u.y >> 16)};
+            const float v[8] = {f[0].x * s, f[0].y * s, f[1].x * s, f[1].y * s, f[2].x * s, f[2].y * s, f[3].x * s, f[3].y * s};
+            store8(ks + (row0 + i * rows) * KS + 8 * (sub + 32 * c), v);
+          }
+        }
+        const bool on = s_row[buf][key0 + lane] >= 0;
+        if (t + kN < end) fetch(t + kN, buf ^ 1);
+        __syncthreads();
+        const int nk = min(32, stop - t * 32 - key0);  // (rows behind the last hold zeros, and p is 0)
+        if (nk <= 0) continue;
+        float d2[kN][2];
+#pragma unroll
+        for (int n = 0; n < kN; ++n) d2[n][0] = d2[n][1] = 0.f;
+        {
+          const float* kr = ks + (key0 + lane) * KS;
+          const float* qh = qs + head0 * D;
 #pragma unroll 4
+          for (int c = 0; c < D; c += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(kr + c);
+#pragma unroll
+            for (int n = 0; n < kN; ++n) {
+              const float4 y = *reinterpret_cast<const float4*>(qh + n * D + c);
+              d2[n][0] = fmaf(x.x, y.x, d2[n][0]);
+              d2[n][1] = fmaf(x.y, y.y, d2[n][1]);
+              d2[n][0] = fmaf(x.z, y.z, d2[n][0]);
+              d2[n][1] = fmaf(x.w, y.w, d2[n][1]);
+            }
+          }
+        }
+        float p[kN];
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          p[n] = on ? (d2[n][0] + d2[n][1]) * a.scale2 : -INFINITY;
+          const float mn = fmaxf(ms[n], warp_max(p[n])), ref = mn == -INFINITY ? 0.f : mn, f = exp2f(ms[n] - ref);
+          p[n] = exp2f(p[n] - ref);
+          ls[n] = fmaf(ls[n], f, warp_sum(p[n]));
+          ms[n] = mn;
+#pragma unroll
+          for (int c = 0; c < kC; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sums[n][c][e] *= f;
+        }
+#pragma unroll 2
         for (int x0 = 0; x0 < nk; x0 += groups) {
-          const int x = x0 + group;
-          const float px = __shfl_sync(0xffffffffu, p, x);
-          const float* kr = ks + x * KS;
+          const float* kr = ks + (key0 + x0 + group) * KS;
+          float px[kN];
+#pragma unroll
+          for (int n = 0; n < kN; ++n) px[n] = __shfl_sync(0xffffffffu, p[n], x0 + group);
 #pragma unroll
           for (int c = 0; c < kC; ++c) {
             if (sub + 32 * c < n8) {
               float v[8];
               load8(kr + 8 * (sub + 32 * c), v);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) acc[c][e] = fmaf(px, v[e], acc[c][e]);
+              for (int n = 0; n < kN; ++n)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sums[n][c][e] = fmaf(px[n], v[e], sums[n][c][e]);
             }
           }
         }
       }
+      // ---- the parts of a head: of the lanes that took other keys, then of the warps, through the tile's memory
       for (int o = share; o < 32; o <<= 1)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[0][e] += __shfl_xor_sync(0xffffffffu, acc[0][e], o);
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sums[n][0][e] += __shfl_xor_sync(0xffffffffu, sums[n][0][e], o);
+      float m = ms[0], l = ls[0], acc[kC][8];
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[c][e] = sums[0][c][e];
+      if (kN > 1) {
+        __syncthreads();  // (the last tile has been read)
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          const int at = key0 / 32 * kSimtWarps + head0 + n;  // [kN][kSimtWarps] parts
+          if (lane == 0) s_ml[at] = make_float2(ms[n], ls[n]);
+#pragma unroll
+          for (int c = 0; c < kC; ++c)
+            if (group == 0 && sub + 32 * c < n8) store8(ks + at * D + 8 * (sub + 32 * c), sums[n][c]);
+        }
+        __syncthreads();
+        m = -INFINITY;
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) m = fmaxf(m, s_ml[i * kSimtWarps + warp].x);
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[c][e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const float2 part = s_ml[i * kSimtWarps + warp];
+          // (a part without keys has m = -inf and zeros, but for a NaN that it may hold)
+          const float f = part.x == -INFINITY ? 1.f : exp2f(part.x - m);
+          l = fmaf(part.y, f, l);
+#pragma unroll
+          for (int c = 0; c < kC; ++c)
+            if (sub + 32 * c < n8) {
+              float v[8];
+              load8(ks + (i * kSimtWarps + warp) * D + 8 * (sub + 32 * c), v);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) acc[c][e] = fmaf(v[e], f, acc[c][e]);
+            }
+        }
+      }
       if (h >= a.H || group > 0) continue;
       if (!whole) {
         const size_t at = (size_t)slot * a.H + h;
@@ -202,10 +281,10 @@ __global__ void __launch_bounds__(32 * kSimtWarps) k_attend_pages_simt(const __g
   }
 }
 
-template <typename T, int kC>
+template <typename T, int kC, int kN>
 cudaError_t simt_c(const PagedArgs& a, cudaStream_t s) {
-  allow_smem<kSimtSmemMax>(k_attend_pages_simt<T, kC>);
-  CSA_LAUNCH((k_attend_pages_simt<T, kC>), dim3(kPagedBlocks), dim3(32 * kSimtWarps), simt_smem(a.D), s, a);
+  allow_smem<kSimtSmemMax>(k_attend_pages_simt<T, kC, kN>);
+  CSA_LAUNCH((k_attend_pages_simt<T, kC, kN>), dim3(kPagedBlocks), dim3(32 * kSimtWarps), simt_smem(a.D), s, a);
   return cudaGetLastError();
 }
 
@@ -392,42 +471,46 @@ cudaError_t launch_merge(const PagedArgs& a, cudaStream_t s) {
   return a.D <= 128 || a.B * a.T <= 4 ? merge_c<T, 1>(a, s) : merge_c<T, 2>(a, s);
 }
 
-// Whether queries are short enough to stay whole, by what the call's sizes say: then no merge follows.  Splitting them pays
-// while there are blocks to spare and more tiles to share out than the merge costs (some 5 us, six tiles' time): one query
-// of 11 tiles 17.4 us split and 20 whole, one of 3 tiles 17 and 14.
-bool stay_whole(PagedArgs* a) {
-  const int Q = a->B * a->T, u = 1 << a->shift;
-  if (a->row_table && !a->sel) return false;
-  long long most = a->sel ? (a->topk + a->tile - 1) / a->tile : 0;
-  if (a->token_table) {
-    const long long room = (long long)a->token_pages * a->P, f = a->first < room ? a->first : room, w = a->W < room ? a->W : room;
-    most += ((f + u - 1) / u + (w + u - 1) / u + 1 + (a->tile >> a->shift) - 1) / (a->tile >> a->shift);
+// The most tiles that a query of the call may have, by what its sizes say
+long long most_tiles(const PagedArgs& a) {
+  const long long u = 1 << a.shift, per = a.tile >> a.shift;
+  long long n = 0, runs = 0;
+  if (a.sel) n += (a.topk + a.tile - 1) / a.tile;
+  else if (a.row_table) runs += ((long long)a.row_pages * a.P + u - 1) / u;
+  if (a.token_table) {
+    const long long room = (long long)a.token_pages * a.P, f = a.first < room ? a.first : room, w = a.W < room ? a.W : room;
+    runs += (f + u - 1) / u + (w + u - 1) / u + 1;
   }
-  if (most > (2 * Q < kPagedBlocks ? 4 : 16)) return false;
-  a->min_tiles = (int)most;
-  return true;
+  return n + (runs + per - 1) / per;
+}
+
+// Whether queries are short enough to stay whole: then no merge follows.  Splitting them pays while there are blocks to spare
+// and more tiles to share out than the merge costs (some 5 us, six tiles' time): one query of 11 tiles takes 14.9 us split
+// and 18.5 whole, one of 3 tiles 14.2 and 11.4, 128 of 11 tiles 25.7 and 24.0.
+bool stay_whole(const PagedArgs& a, long long most) {
+  return !(a.row_table && !a.sel) && most <= (2 * a.B * a.T < kPagedBlocks ? 4 : 16);
 }
 
 template <typename T>
 cudaError_t attend_t(const Dims& L, PagedArgs a, cudaStream_t s) {
-  if (tc_paged_supported(L, a.P)) {
-    a.min_tiles = 2;
-    a.tile = 64;
-    a.shift = 3;  // the largest power of two that divides a page, at most a tile
-    while (a.shift < 6 && a.P % (2 << a.shift) == 0) ++a.shift;
-    a.cols = 32;
-    a.merge = !stay_whole(&a);
-    const cudaError_t e = launch_tc_paged(a, s);
-    if (e != cudaSuccess) return e;
+  const bool tc = tc_paged_supported(L, a.P);
+  a.tile = tc ? 64 : 32;
+  a.shift = tc ? 3 : 0;  // of a run: the largest power of two that divides a page, at most a tile
+  while (tc && a.shift < 6 && a.P % (2 << a.shift) == 0) ++a.shift;
+  a.cols = tc ? 32 : a.D;
+  const long long most = most_tiles(a);
+  a.merge = !stay_whole(a, most);
+  a.min_tiles = a.merge ? tc ? 2 : 1 : (int)most;
+  cudaError_t e;
+  if (tc) {
+    e = launch_tc_paged(a, s);
+  } else if (simt_chunks(a.D) == 1) {
+    const bool few = (a.merge ? (most * a.B * a.T + kPagedBlocks - 1) / kPagedBlocks : most) <= 3;  // tiles a block
+    e = few ? simt_c<T, 1, 2>(a, s) : simt_c<T, 1, 4>(a, s);
   } else {
-    a.min_tiles = 1;
-    a.tile = kSimtTile;
-    a.shift = 0;
-    a.cols = a.D;
-    a.merge = !stay_whole(&a);
-    const cudaError_t e = a.D <= 256 ? simt_c<T, 1>(a, s) : a.D <= 512 ? simt_c<T, 2>(a, s) : simt_c<T, 4>(a, s);
-    if (e != cudaSuccess) return e;
+    e = simt_chunks(a.D) == 2 ? simt_c<T, 2, 2>(a, s) : simt_c<T, 4, 1>(a, s);
   }
+  if (e != cudaSuccess) return e;
   return a.merge ? launch_merge<T>(a, s) : cudaSuccess;
 }
 
