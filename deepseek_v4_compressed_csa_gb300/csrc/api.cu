@@ -690,10 +690,11 @@ csa_status csa_attend_pages(const csa_layer* layer, const csa_pages* pages, cons
     return CSA_ERR_ARG;
   const long long n = (long long)B * T, row = (long long)L.H * L.D * esize(L.dtype);
   if (Span(q, n, row, row).meets(Span(out, n, row, row))) return CSA_ERR_ARG;
-  // the tiles of a call are counted in ints; the smallest hold 32 keys, and each of a query's three sections ends one
+  // a query's keys and the tiles of a call are counted in ints; the smallest hold 32 keys, and each of a query's three
+  // sections ends one
   const long long P = pages->page_rows;
   const long long most = (row_table ? (sel ? (long long)L.topk : row_width * P) : 0) + (token_table ? token_width * P : 0);
-  if (n * (most / 32 + 4) > INT32_MAX) return CSA_ERR_ARG;
+  if (most > INT32_MAX - 256 || n * (most / 32 + 4) > INT32_MAX) return CSA_ERR_ARG;
   if (ws_bytes < ws_attend_pages(L, (int)n) || !dev_tensor(ws)) return CSA_ERR_WORKSPACE;
   PagedArgs a{};
   Carver c(ws);

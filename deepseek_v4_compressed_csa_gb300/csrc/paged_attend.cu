@@ -17,8 +17,9 @@ namespace {
 // of the one after it are looked up.  A warp takes kN heads and 32 of the tile's 32 kN keys: a lane a key for the logits,
 // then lanes share a key's dims (rows of up to 128 dims: several keys at a time) for the sums; the warps of a head are put
 // together behind the last tile.  What bounds it is reading the keys from shared memory, twice a head: 60 queries of 1K keys
-// (8 heads of 64 dims) take 38 us with a warp a head, 28 with a warp two, 23.5 with four.  Where a block has up to three tiles,
-// most warps have no keys with four, and two are better (a window of 32: 6.5 us against 7.1).
+// (8 heads of 64 dims) take 38 us with a warp a head, 28 with a warp two, 23.5 with four.  But where a block has few tiles,
+// most warps have no keys with four: one to three tiles (a window of 32) 6.4 us with two heads a warp, 7.0 with four, 6.8
+// with one; one tile (15 queries of 250 keys, cut) 8.7 with one, 9.0 with two, 9.7 with four.
 constexpr int kSimtWarps = 8;   // and heads at a time
 constexpr int kSimtPad = 4;     // floats behind a key's row: lanes read their keys' chunks without bank conflicts
 __host__ __device__ constexpr int simt_heads(int chunks) { return 4 / chunks; }  // the most heads a warp, and tiles at once
@@ -505,8 +506,8 @@ cudaError_t attend_t(const Dims& L, PagedArgs a, cudaStream_t s) {
   if (tc) {
     e = launch_tc_paged(a, s);
   } else if (simt_chunks(a.D) == 1) {
-    const bool few = (a.merge ? (most * a.B * a.T + kPagedBlocks - 1) / kPagedBlocks : most) <= 3;  // tiles a block
-    e = few ? simt_c<T, 1, 2>(a, s) : simt_c<T, 1, 4>(a, s);
+    const long long tiles = a.merge ? (most * a.B * a.T + kPagedBlocks - 1) / kPagedBlocks : most;  // a block's, at most
+    e = tiles <= 1 ? simt_c<T, 1, 1>(a, s) : tiles <= 3 ? simt_c<T, 1, 2>(a, s) : simt_c<T, 1, 4>(a, s);
   } else {
     e = simt_chunks(a.D) == 2 ? simt_c<T, 2, 2>(a, s) : simt_c<T, 4, 1>(a, s);
   }

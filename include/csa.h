@@ -647,7 +647,7 @@ csa_status csa_append_pages(const csa_layer* layer, const csa_pages* pages, cons
  * in fp32; the portable kernel takes any other layer, all in fp32.  A call's result
  * depends on how its keys are cut into tiles (by B, T and all lengths), not on the
  * run: the same call gives the same bits.
- * B * T <= 2^16, and CSA_ERR_ARG where the tables' widths times B * T could hold 2^36 keys.
+ * B * T <= 2^16, and CSA_ERR_ARG where a sequence's tables have room for 2^31 - 256 keys, or B * T such for 2^36.
  * Workspace: CSA_OP_ATTEND_PAGES, not shared by two calls in flight. */
 csa_status csa_attend_pages(const csa_layer* layer, const csa_pages* pages, const void* q, int B, int T,
                             const float* sink, const int32_t* pos, const int32_t* n_new, const int32_t* token_table,

@@ -197,6 +197,17 @@ def test_batches(kind, name):
 
 
 @pytest.mark.parametrize("kind", ["small", "flash"])
+def test_largest_batch(kind):
+    """2^16 queries, few of them there; ratio 1."""
+    small, page = KINDS[kind]
+    L = P.layer(small, ratio=1)
+    there = {0: 7, 100: 256, 255: 31}
+    args = build(L, 256, 256, [300 * (b in there) for b in range(256)], page, "all", 3, [there.get(b, 0) for b in range(256)], seed=5)
+    assert call(L, *args).item() == 0
+    verify(L, *args)
+
+
+@pytest.mark.parametrize("kind", ["small", "flash"])
 @pytest.mark.parametrize("nb,T,ctx", [(1, 1, 90000), (2, 3, 30000), (5, 1, 20011)])
 def test_long_queries(kind, nb, T, ctx):
     """Queries that every block has a part of, split unevenly among some: the merge."""

@@ -113,6 +113,8 @@ def test_attend_pages_refusals(lib):
     wide = dict(B_=1 << 7, T=1 << 7, rw=1 << 24, sel=None, n_sel=None)
     assert _attend(lib, **wide) == B.CSA_ERR_ARG
     assert _attend(lib, B_=1 << 7, T=1 << 7, tw=1 << 24) == B.CSA_ERR_ARG
+    # ... or one query more keys than an int counts
+    assert _attend(lib, B_=1, T=1, tw=1 << 24, rw=1 << 24, sel=None, n_sel=None) == B.CSA_ERR_ARG
     for ws in (dict(ws=None), dict(ws=FAKE + 8), dict(ws_bytes=0)):
         assert _attend(lib, **ws) == B.CSA_ERR_WORKSPACE, ws
 
