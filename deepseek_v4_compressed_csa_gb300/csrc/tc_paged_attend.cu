@@ -26,6 +26,10 @@
 // has passed its R by 4 (powers of two); every head's R then follows.  A tile takes its four warps some 2500 clocks, most
 // of them latency, and the products' pipe 1300: two groups of four take tiles in turn, each with an m and l of its own; R
 // is one, so each tile's decision about it waits for the tile's before.
+//
+// Measured: 8 queries of 65.7K rows (272 MB) 57 us before the merge, 4.8 TB/s, 1700 clocks a tile: shared memory's, which
+// moves 176 KB of it at 128 bytes a clock (the keys once in and three times out, P, the scores' scales).  Feeding the products
+// faster changes nothing.  Short calls are the chain plan - queries - tile - output: one window of three tiles 11.4 us.
 #include "paged.cuh"
 #include "tc.cuh"
 
