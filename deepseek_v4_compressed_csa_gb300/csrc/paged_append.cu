@@ -3,8 +3,8 @@
 //   y = x (mean(x^2) + eps)^-1/2 w, its last R values rotated;  codes = E4M3(y / s), s = max |y| / 448
 //
 // in fp32, rounded once, to the codes.  A warp a row, which stays in its registers; the page is looked up while the row
-// is on its way.  A row costs 3 bytes a value: some thousand rows take as long as the launch (32 rows of 512 values 3.1 us,
-// 4096 rows 4.4, 1.4 TB/s).
+// is on its way.  A row costs 3 bytes a value: some thousand rows take as long as the launch (32 rows of 512 values 2.7 us,
+// 4096 rows 4.3, 1.5 TB/s; with the weights read after the norm and the page before it 3.0 and 4.4, cold 4.5 against 3.7).
 #include "paged.cuh"
 
 namespace csa {
@@ -41,11 +41,13 @@ __global__ void __launch_bounds__(32 * kApWarps) k_append_pages(const __grid_con
     if (lane == 0) atomicOr(a.err, CSA_DEV_CAPACITY);
     return;
   }
+  // (what else is read is on its way while the row is worked on: the page is needed last)
   const int page = __ldg(a.table + (size_t)b * a.pages + k);
-  if ((unsigned)page >= (unsigned)a.n_pages) {
-    if (lane == 0) atomicOr(a.err, CSA_DEV_RANGE);
-    return;
-  }
+  float w[kChunks][8];
+  const bool weighted = a.norm && a.weight;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c)
+    if (weighted && lane + 32 * c < n8) load8_nc(a.weight + 8 * (lane + 32 * c), w[c]);
   if (a.inv_freq) {
     float2* cs = cs_all + warp * (a.R / 2);
     for (int f = lane; f < a.R / 2; f += 32) turn_cs(p, __ldg(a.inv_freq + f), &cs[f].x, &cs[f].y);
@@ -70,11 +72,9 @@ __global__ void __launch_bounds__(32 * kApWarps) k_append_pages(const __grid_con
   for (int c = 0; c < kChunks; ++c) {
     const int d = 8 * (lane + 32 * c);
     if (d >= a.D) continue;
-    if (a.norm && a.weight) {
-      float w[8];
-      load8_nc(a.weight + d, w);
+    if (weighted) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[c][e] *= w[e];
+      for (int e = 0; e < 8; ++e) v[c][e] *= w[c][e];
     }
     if (a.inv_freq && d >= a.D - a.R) {
       const float2* cs = cs_all + warp * (a.R / 2) + ((d - (a.D - a.R)) >> 1);
@@ -91,6 +91,10 @@ __global__ void __launch_bounds__(32 * kApWarps) k_append_pages(const __grid_con
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if ((unsigned)page >= (unsigned)a.n_pages) {
+    if (lane == 0) atomicOr(a.err, CSA_DEV_RANGE);
+    return;
+  }
   const float s = __fdiv_rn(amax, 448.f);
   const size_t row = (size_t)page * a.P + (p - k * a.P);
 #pragma unroll
