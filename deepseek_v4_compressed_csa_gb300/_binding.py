@@ -995,6 +995,8 @@ def add_norm(layer: Layer, x, residual=None, weight=None, group=None, out=None, 
         raise TypeError(f"x: dtype {x.dtype}, expected {dtype}")
     if not x.is_cuda:
         raise ValueError("x: CSA tensors must live on a CUDA device")
+    if X > 16384:
+        raise ValueError(f"x: rows of {X} values, at most 16384")
     dev = x.get_device()
     N = x.numel() // X if X else 0
     x_stride = _row_stride("x", x, X)
@@ -1064,6 +1066,8 @@ class Pages:
 def _table(name: str, t, B: int):
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[0] != B:
         raise ValueError(f"{name}: expected an int32 tensor [{B}, pages of a sequence]")
+    if t.shape[1] > 1 << 30:
+        raise ValueError(f"{name}: {t.shape[1]} pages, at most 2^30 rows")
     return (name, t, torch.int32, t.shape)
 
 
@@ -1084,6 +1088,8 @@ def append_pages(layer: Layer, rows, pages: Pages, table, pos, n_new=None, weigh
     B, T, dev = _tree_dims("rows", rows, (D,))
     if rows.dtype is not layer.dtype:
         raise TypeError(f"rows: dtype {rows.dtype}, expected {layer.dtype}")
+    if B * T > 1 << 24:
+        raise ValueError(f"rows: {B} x {T} tokens, at most 2^24 a call")
     stride_b = stride_t = 0
     if not rows.is_contiguous():
         st = rows.stride()
@@ -1129,6 +1135,10 @@ def attend_pages(layer: Layer, q, pages: Pages, sink, pos, out, token_table=None
             return err
     dt, i32, f32, H, D = layer.dtype, torch.int32, torch.float32, layer.H, layer.D
     B, T, dev = _tree_dims("q", q, (H, D))
+    if B * T > 1 << 16:
+        raise ValueError(f"q: {B} x {T} queries, at most 2^16 a call")
+    if not 0 <= first <= 0x7fffffff:
+        raise ValueError(f"first = {first}: expected a count of tokens")
     if token_table is None and row_table is None:
         raise ValueError("attend_pages needs token_table, row_table, or both")
     if row_table is None and not (n_rows is None and sel is None and n_sel is None):

@@ -208,7 +208,7 @@ static PyObject* add_norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   } else if (a[9] != Py_None || a[10] != Py_None) {
     return not_plain();
   }
-  if (X > 1 << 30 || !stream_of(a[11], dev, &raw)) return not_plain();
+  if (X > 16384 || !stream_of(a[11], dev, &raw)) return not_plain();
   int (*fn)(const void*, const void*, long long, const void*, long long, const void*, long long, int, void*, void*, void*,
             void*, int, void*) = (int (*)(const void*, const void*, long long, const void*, long long, const void*,
                                           long long, int, void*, void*, void*, void*, int, void*))address_arg(a[0]);
@@ -251,7 +251,9 @@ static PyObject* append_pages(PyObject* self, PyObject* const* a, Py_ssize_t n) 
   Pool pool;
   int width;
   void *rows, *table, *pos, *fresh = NULL, *w = NULL, *frq = NULL, *err, *raw;
-  if (!look(a[5], a[2], &s, &dev, &rows) || s.n != 3 || s.d[2] != D || s.d[0] > 1 << 30 || s.d[1] > 1 << 30) return not_plain();
+  if (!look(a[5], a[2], &s, &dev, &rows) || s.n != 3 || s.d[2] != D || s.d[0] > 1 << 24 || s.d[1] > 1 << 24 ||
+      s.d[0] * s.d[1] > 1 << 24)
+    return not_plain();
   const int norm = PyObject_IsTrue(a[12]);
   if (norm < 0 || !pool_of(a[6], a[7], dev, D, &pool) || !table_of(a[8], dev, s.d[0], &table, &width) ||
       !AS(a[9], t_i32, &pos, s.d[0]))
@@ -288,7 +290,7 @@ static PyObject* attend_pages(PyObject* self, PyObject* const* a, Py_ssize_t n) 
        *frq = NULL, *ws, *err, *raw;
   if (!look(a[7], a[2], &s, &dev, &q) || s.n != 4 || s.d[2] != H || s.d[3] != D) return not_plain();
   const long long B = s.d[0], T = s.d[1], first = PyLong_AsLongLong(a[14]);
-  if (PyErr_Occurred() || B > 1 << 30 || T > 1 << 30 || first < 0 || first > 0x7fffffff) return not_plain();
+  if (PyErr_Occurred() || B > 1 << 16 || T > 1 << 16 || B * T > 1 << 16 || first < 0 || first > 0x7fffffff) return not_plain();
   if (!pool_of(a[8], a[9], dev, D, &pool) || !AS(a[11], t_i32, &pos, B) || !AS(a[12], a[2], &out, B, T, H, D))
     return not_plain();
   if ((a[10] != Py_None && !AS(a[10], t_f32, &sink, H)) || (a[13] != Py_None && !table_of(a[13], dev, B, &tok, &tw)))

@@ -220,6 +220,25 @@ def test_binding_refuses_what_does_not_fit_together(lib, calls):
     assert not calls
 
 
+def test_binding_refuses_what_an_int_does_not_hold(lib, calls):
+    """Sizes and counts that the C ABI's ints would cut off (tensors that are one value, expanded)."""
+    tensors, rest = _good("add_norm")
+    with pytest.raises(ValueError, match="16384"):
+        _run("add_norm", dict(x=z(1, 1).expand(1, (1 << 32) + 8)), {})
+    tensors, rest = _good("append_pages")
+    with pytest.raises(ValueError, match="2.24"):
+        _run("append_pages", {**tensors, "rows": z(1, 512).expand(1 << 25, 1, 512)}, rest)
+    with pytest.raises(ValueError, match="table"):
+        _run("append_pages", {**tensors, "table": z(2, 1, dt=I32).expand(2, (1 << 32) + 4)}, rest)
+    tensors, rest = _good("attend_pages")
+    for first in (-1, 1 << 31, (1 << 32) + 4):
+        with pytest.raises(ValueError, match="first"):
+            _run("attend_pages", tensors, dict(first=first))
+    with pytest.raises(ValueError, match="2.16"):
+        _run("attend_pages", {**tensors, "q": z(64, 512).expand(1 << 17, 1, 64, 512)}, rest)
+    assert not calls
+
+
 def test_binding_passes_strides(lib, calls):
     tensors, rest = _good("add_norm")
     wide = z(6, 512 + 8)
