@@ -318,6 +318,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       pre += k.tiles;
       if (!ok || pre >= t1) break;
       k = next_query(a, k.q);
+      // (the softmax warps want its 64 KB when they are done with the query before: 512 windows 49.5 -> 45.6 us)
+      if (warp == 0 && lane == 0)
+        tc::prefetch_l2(static_cast<const __nv_bfloat16*>(a.q) + (size_t)k.q * kH * kD, kH * kD * 2);
     }
     landed();
   } else if (warp == kMmaWarp) {
