@@ -9,6 +9,7 @@ import deepseek_v4_compressed_csa_gb300 as csa
 F8 = torch.float8_e4m3fn
 F64 = torch.float64
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}  # the most that one rounding is off, relative
+LEAST = {torch.bfloat16: 2.0 ** -134, torch.float32: 2.0 ** -150}  # and half of the smallest step, below the normal numbers
 U32 = 2.0 ** -24
 EPS = 1e-6
 
@@ -122,6 +123,10 @@ def attend_ref(L, q, codes, s, sink, tensor_cores):
     A = p @ keys.abs()  # [H, D]
     n = lg.shape[1]
     err = A * (2 * d_lg + (n + 32) * U32)
+    # A weight below fp32's smallest normal number, 2^-126, is rounded to a multiple of 2^-149, or counts as nothing (the
+    # hardware's exp2 flushes it): its key's values are off by less than 2^-126 of themselves; with the sink far above every
+    # key that is all there is.
+    err = err + 2.0 ** -126 * keys.abs().sum(0)
     if tensor_cores:
         # The queries' two E4M3 parts: scaled so that the head's largest value is at least 2^7, the first holds four digits,
         # exactly down to 2^-6 and within half of its smallest step, 2^-10, below; the second, 16 times finer, the four digits
@@ -130,9 +135,6 @@ def attend_ref(L, q, codes, s, sink, tensor_cores):
         top = q.abs().amax(1, keepdim=True)
         low = (q.abs() <= top * 2.0 ** -13).to(F64) @ keys.abs().T
         err = err + A * (2 * scale * top * 2.0 ** -17 * low.amax(1, keepdim=True) + 2.0 ** -20)
-        # A weight below fp32's smallest normal number, 2^-126, counts as nothing (the hardware's exp2 flushes it): its
-        # key's values are off by less than 2^-126 of themselves; with the sink far above every key that is all there is.
-        err = err + 2.0 ** -126 * keys.abs().sum(0)
         # The probabilities' parts of w = p s, E5M2 (at most 2^-3 off) and what that leaves in E4M3 (2^-4 of it, or half of
         # its smallest step, 2^-10 where the largest w is at least 2^5); what E5M2's smallest step, 2^-16, leaves is within that.
         w = p * s.abs()
@@ -168,5 +170,5 @@ def attend_all(L, q, cache, pos, counts, out0, token_table=None, first=0, row_ta
                 e = pair_sum(e + 8 * U32 * o.abs(), L.R)
                 o = turn(o, at, freq, -1.0)
             want[b, i] = o
-            allow[b, i] = e + (o.abs() + e) * HALF[L.dtype]
+            allow[b, i] = e + (o.abs() + e) * HALF[L.dtype] + LEAST[L.dtype]
     return want, allow

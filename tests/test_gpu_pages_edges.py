@@ -1,6 +1,7 @@
 """append_pages and attend_pages where they can go wrong: what tables, counts and selections say wrongly, batches of every
 plan, queries split over many blocks, far positions, large pools, odd values, streams, graphs, guard bands."""
 import math
+import random
 import threading
 
 import pytest
@@ -40,7 +41,7 @@ def expect(L, q, cache, keys, pos, sink, freq, out0=7.0):
             if freq is not None:
                 e = P.pair_sum(e + 8 * P.U32 * o.abs(), L.R)
                 o = P.turn(o, torch.full((L.H,), pos[b] + i, device="cuda"), freq, -1.0)
-            want[b, i], allow[b, i] = o, e + (o.abs() + e) * P.HALF[L.dtype]
+            want[b, i], allow[b, i] = o, e + (o.abs() + e) * P.HALF[L.dtype] + P.LEAST[L.dtype]
     return want, allow
 
 
@@ -226,6 +227,28 @@ def test_layers(D, R, H, dtype):
     L = P.layer(True, D=D, R=R, H=H, dtype=dtype, Di=max(R, 8), Hi=2, W=20, topk=33)
     for keys, ctx in (("all", [3, 5000, 400]), ("select", [250, 90, 30]), ("window", [0, 19, 77])):
         args = build(L, 3, 2, ctx, 9, keys, 1, [2, 1, 2], seed=D + R)
+        assert call(L, *args).item() == 0
+        verify(L, *args)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_shapes_at_random(seed):
+    """Layers, batches, lengths, pages and counts drawn over their ranges, six calls a seed."""
+    r = random.Random(seed)
+    for n in range(6):
+        kw = dict(ratio=r.choice([1, 4, 4, 128]), W=r.choice([1, 7, 32, 128, 300]), topk=r.choice([5, 64, 100, 512]))
+        small, keys = r.random() < 0.4, r.choice(["window", "select", "all"])
+        if small:
+            kw |= dict(H=r.choice([1, 3, 8, 11]), D=r.choice([16, 64, 72, 264, 512, 640]), R=r.choice([8, 16]), Di=16,
+                       dtype=r.choice([torch.float32, torch.bfloat16]))
+        L = P.layer(small, **{**kw, "ratio": 4 if keys == "select" else kw["ratio"]})
+        nb, T = int(200 ** r.random()), r.choice([1, 1, 2, 3, 8, 40])
+        nb = min(nb, max(1, 300 // T))
+        most = 60000 // (nb * T) * L.ratio if keys == "all" else 4000
+        ctx = [r.randint(0, max(1, min(most, 20000))) for _ in range(nb)]
+        counts = [r.choice([T, T, r.randint(0, T)]) for _ in range(nb)]
+        args = build(L, nb, T, ctx, r.choice([8, 16, 24, 40, 64, 128, 13, 1, 7]), keys, r.choice([0, 1, 4, 70]), counts,
+                     seed=100 * seed + n, junk=r.choice([-1, 1 << 29]), spread=r.choice([0.3, 1.0, 2.0]), q_scale=r.choice([0.5, 2.0, 6.0]))
         assert call(L, *args).item() == 0
         verify(L, *args)
 
