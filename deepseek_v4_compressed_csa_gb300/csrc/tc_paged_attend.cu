@@ -604,7 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_before_sync();
           }
           tc::mbar_arrive(sm.decided + g);
-          const float gain = ref == -INFINITY ? 0.f : ex2(kGain + mr - ref);
+          // (nothing in this tile weighs anything: lv does not bound mr - ref then, and a gain out of range would make the
+          // zeros NaN; a NaN stays one beside a gain of 0)
+          const float gain = lv == -INFINITY ? 0.f : ex2(kGain + mr - ref);
           // ---- the probabilities' two parts, once the buffer's last product has retired
           if (jt >= 2) wait(sm, sm.pv_done + g, ((jt >> 1) & 1) ^ 1);
           uint8_t* row = pbuf + h * 128;

@@ -1,0 +1,126 @@
+"""attend_pages on values that its tensor-core kernel keeps in few bits, or far apart: tiles in which nothing counts beside keys
+far below the largest logit, and many small weights that are alike."""
+import math
+
+import pytest
+import torch
+
+import deepseek_v4_compressed_csa_gb300 as csa
+from tests import _pages as P
+from tests.test_gpu_pages import gen, i32, normal
+from tests.test_gpu_pages_edges import KINDS, expect, phys
+
+pytestmark = pytest.mark.gpu
+
+TILE = 64
+
+
+def far_rows(L, n, nats, seed):
+    """Rows [n, D] and a query [1, 1, H, D] whose logits are nats (fp32 [n]) and a little: the first value makes them, the
+    others are noise."""
+    x = normal(gen(seed), n, L.D)
+    q = torch.zeros(1, 1, L.H, L.D, device="cuda")
+    q[..., 0] = 64.0
+    x[:, 0] = nats / (64.0 * L.D ** -0.5)
+    return x, q.to(L.dtype)
+
+
+def attend(L, cache, q, row, n, sel=None, sink=None):
+    """One query over rows 0 .. n - 1 of a table, or a selection of them: (output, error word)."""
+    out = torch.full_like(q, 7.0)
+    more = {}
+    if sel is not None:
+        full = torch.full((1, 1, L.topk), 1 << 30, dtype=torch.int32)
+        full[0, 0, : len(sel)] = torch.tensor(sel, dtype=torch.int32)
+        more = dict(sel=full.cuda(), n_sel=i32([[len(sel)]]))
+    err = csa.attend_pages(L, q, cache.pages, sink, i32([4 * n]), out, row_table=row.cuda(), n_rows=i32([n]), **more)
+    return out, err.item()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("form", ["whole", "cut"])
+@pytest.mark.parametrize("tiles", [2, 3, 4, 9])
+@pytest.mark.parametrize("nats", [-60.0, -86.0, -90.0, -120.0])
+def test_a_row_of_zeros_above_far_logits(kind, form, tiles, nats):
+    """A row of scale 0 has the logit 0, far above every other's: it takes all of the weight and gives nothing."""
+    small, page = KINDS[kind]
+    L = P.layer(small, topk=TILE * 4)
+    if form == "whole" and tiles > 4:
+        pytest.skip("selections of up to four tiles stay whole")
+    n = TILE * tiles
+    x, q = far_rows(L, n, torch.full((n,), nats, device="cuda"), 3)
+    for at in (0, TILE + 3, n - 1):
+        cache = P.Cache(L, page, -(-n // page) + 3)
+        row = cache.table(1, -(-n // page))
+        x0 = x.clone()
+        x0[at] = 0
+        cache.put(row, 0, list(range(n)), x0)
+        out, err = attend(L, cache, q, row, n, list(range(n)) if form == "whole" else None)
+        assert err == 0
+        P.check(out, *expect(L, q, cache, [[phys(cache, row, 0, range(n))]], [4 * n], None, None), f"at {at}")
+
+
+@pytest.mark.parametrize("kind", ["small", "flash"])
+@pytest.mark.parametrize("tiles", [2, 3, 4, 7])
+@pytest.mark.parametrize("nats", [-70.0, -90.0, -140.0])
+@pytest.mark.parametrize("what", ["selection", "table"])
+def test_a_tile_without_keys_beside_far_logits(kind, tiles, nats, what):
+    """Rows that are out of range, a tile full of them, are left out also where every other logit is far below 0."""
+    small, page = KINDS[kind]  # (a tile is whole pages)
+    L = P.layer(small, topk=TILE * 7)
+    n = TILE * tiles
+    x, q = far_rows(L, n, torch.full((n,), nats, device="cuda"), 4)
+    for lost in range(min(tiles, 4)):
+        cache = P.Cache(L, page, -(-n // page) + 3)
+        row = cache.table(1, -(-n // page))
+        cache.put(row, 0, list(range(n)), x)
+        keys = [j for j in range(n) if j // TILE != lost]
+        at = phys(cache, row, 0, keys)
+        if what == "selection":
+            sel = [j if j // TILE != lost else (-1 - j, 10 ** 6 + j)[j % 2] for j in range(n)]
+            out, err = attend(L, cache, q, row, n, sel)
+        else:
+            row[0, lost * TILE // page : (lost + 1) * TILE // page] = -7
+            out, err = attend(L, cache, q, row, n)
+        assert err == csa.DEV_RANGE
+        P.check(out, *expect(L, q, cache, [[at]], [4 * n], None, None), f"without tile {lost}")
+
+
+@pytest.mark.parametrize("kind", ["small", "flash"])
+@pytest.mark.parametrize("form", ["whole", "cut"])
+@pytest.mark.parametrize("tiles", [3, 4])
+def test_a_tile_of_zeros_behind_far_logits(kind, form, tiles):
+    """A tile of rows of scale 0 as the last one: its logits are the largest, its rows nothing."""
+    small, page = KINDS[kind]
+    L = P.layer(small, topk=TILE * 4)
+    n = TILE * tiles
+    for nats in (-60.0, -90.0, -130.0):
+        x, q = far_rows(L, n, torch.full((n,), nats, device="cuda"), 5)
+        x[n - TILE:] = 0
+        cache = P.Cache(L, page, -(-n // page) + 3)
+        row = cache.table(1, -(-n // page))
+        cache.put(row, 0, list(range(n)), x)
+        out, err = attend(L, cache, q, row, n, list(range(n)) if form == "whole" else None)
+        assert err == 0
+        P.check(out, *expect(L, q, cache, [[phys(cache, row, 0, range(n))]], [4 * n], None, None), f"{nats}")
+
+
+@pytest.mark.parametrize("small", [False, True])
+@pytest.mark.parametrize("tiles", [2, 5])
+def test_a_nan_in_a_tile_that_counts_for_nothing(small, tiles):
+    """A row of a NaN scale among rows of scale 0 is NaN all the same."""
+    kind = "small" if small else "flash"
+    page = KINDS[kind][1]
+    L = P.layer(small, topk=TILE * 5)
+    n = TILE * tiles
+    x, q = far_rows(L, n, torch.full((n,), -90.0, device="cuda"), 6)
+    for lost in (0, 1):
+        x0 = x.clone()
+        x0[lost * TILE : (lost + 1) * TILE] = 0
+        cache = P.Cache(L, page, -(-n // page) + 3)
+        row = cache.table(1, -(-n // page))
+        cache.put(row, 0, list(range(n)), x0)
+        cache.scales.view(-1)[phys(cache, row, 0, [lost * TILE + 9])[0]] = math.nan
+        for sel in (None, list(range(n))):
+            out, err = attend(L, cache, q, row, n, sel)
+            assert err == 0 and torch.isnan(out.float()).all()
