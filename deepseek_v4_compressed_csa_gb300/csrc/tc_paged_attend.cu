@@ -644,7 +644,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 s0 = stat[h], s1 = stat[kH + h];
         const float m = fmaxf(s0.x, s1.x), mr = m == -INFINITY ? 0.f : m, ref = refs[h];
         const float l = fmaf(s0.y, ex2(s0.x - mr), s1.y * ex2(s1.x - mr));
-        float f = ref == -INFINITY ? 0.f : ex2(ref - kGain - mr);  // O^T * f = sum 2^{t - m} key
+        // O^T * f = sum 2^{t - m} key.  (f as a square: where the largest weight is below 2^-117 of 2^m, a row of scale 0, f is
+        // below the normal numbers, which ex2 flushes and a product does not.)
+        const float root = ref == -INFINITY ? 0.f : ex2(0.5f * (ref - kGain - mr));
+        float f = root * root;
         if (whole) {
           const float M = fmaxf(m, z2), gm = m == -INFINITY ? 0.f : ex2(m - M);
           const float Z = l * gm + (z2 == -INFINITY ? 0.f : ex2(z2 - M));

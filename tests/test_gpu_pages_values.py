@@ -124,3 +124,29 @@ def test_a_nan_in_a_tile_that_counts_for_nothing(small, tiles):
         for sel in (None, list(range(n))):
             out, err = attend(L, cache, q, row, n, sel)
             assert err == 0 and torch.isnan(out.float()).all()
+
+
+@pytest.mark.parametrize("kind", ["small", "flash"])
+@pytest.mark.parametrize("form", ["whole", "cut"])
+@pytest.mark.parametrize("power", [-100.0, -117.0, -119.0, -122.0, -125.0])
+def test_one_key_far_below_rows_of_zeros(kind, form, power):
+    """A weight of 2^power beside one row of scale 0 and logit 0 reaches the output (as long as fp32 holds it as a normal
+    number); the rows between them, further below, do not."""
+    small, page = KINDS[kind]
+    L = P.layer(small, topk=TILE * 4)
+    n = 2 * TILE if form == "whole" else 8 * TILE
+    for key in (TILE, 2 * TILE - 1):
+        nats = torch.full((n,), -200.0, device="cuda")
+        nats[0] = 0
+        nats[key] = power * math.log(2)
+        x, q = far_rows(L, n, nats, 7)
+        others = [j for j in range(n) if j != key]
+        x[others, 1:] = 0
+        cache = P.Cache(L, page, -(-n // page) + 3)
+        row = cache.table(1, -(-n // page))
+        cache.put(row, 0, list(range(n)), x)
+        out, err = attend(L, cache, q, row, n, list(range(n)) if form == "whole" else None)
+        assert err == 0
+        want, allow = expect(L, q, cache, [[phys(cache, row, 0, range(n))]], [4 * n], None, None)
+        P.check(out[..., 1:], want[..., 1:], allow[..., 1:], f"key {key}")
+        assert (want[..., 1:].abs() > allow[..., 1:]).any()
