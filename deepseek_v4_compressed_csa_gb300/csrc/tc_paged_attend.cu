@@ -10,9 +10,13 @@
 //   q = 2^e (hi + lo / 16), E4M3 both: the 8 bits of a bf16 value, exact but for values 2^-13 below the head's largest.
 //     The parts are two rows of one operand, M = 128 = 64 heads x 2, kept in tensor memory (its 128 columns are an A
 //     operand that no product reads from shared memory);
-//   P = hi + lo, E5M2 and E4M3, both added to the same accumulator: 7 bits (at most 2^-7 of a probability, about 2^-9.5 on
-//     average, signs mixed), 3 bits down to 2^-19 of the largest and something down to 2^-22.  (Two E4M3 parts keep 8 bits
-//     but drop everything below 2^-16 of the largest: beside one dominant key, what 64 thousand others add up to.)
+//   P = hi + lo, E5M2 and E4M3, both added to the same accumulator: a weight p ks is off by at most 2^-8 of itself, or where
+//     that is more by 2^-15 of the largest, up to 1/8 of itself (from 2^-13 of the largest on E5M2's 3 bits are all there are;
+//     below 2^-20 its smallest step).  (Two E4M3 parts keep 8 bits but drop everything below 2^-16 of the largest.)  Thousands
+//     of small weights that are alike (rows that repeat) would all be rounded to one side: 16K of 1.125 x 2^-14 of one dominant
+//     key's weight counted for 11 % more or less than they weigh.  So a thread keeps account of what its keys have lost or
+//     gained; where that passes 2^-9 of their weights and of the largest, it rounds by thresholds spread evenly over its 32
+//     keys instead of to the nearest: one weight may then be off by a quarter, alike ones together by 2^-8.
 // A tile is 64 keys, one 32 KB stage of six, read once from memory, used K-major for S and MN-major (as V^T) for O:
 //   S [128 x 64] = [Q_hi | Q_lo] K^T, 16 products of K = 32 (two buffers);
 //   O^T [128 dims x 64 heads] x 4 += V^T P^T, 16 products (2 parts x 2 steps x 4): O^T takes 256 columns where O, with its
@@ -21,8 +25,8 @@
 // head's parts meet by one shuffle; after it the lane pair shares the head's 64 keys, 32 each.
 //
 // Softmax with the scales: t = scale2 S ks, m a running maximum, l = sum 2^{t - m}.  What enters the product is
-// 2^t ks 2^{7 - R}, R a reference that follows the maximum of log2(2^t |ks|) in steps: at most 2^11, where lo, up to 1/8 of
-// hi, still fits E4M3.  It starts 4 times above the first tile's maximum, and O^T is rescaled only when some head's maximum
+// 2^t ks 2^{7.9 - R}, R a reference that follows the maximum of log2(2^t |ks|) in steps: below 2^12, where lo, up to 2^8,
+// still fits E4M3.  It starts 4 times above the first tile's maximum, and O^T is rescaled only when some head's maximum
 // has passed its R by 4 (powers of two); every head's R then follows.  A tile takes its four warps some 2500 clocks, most
 // of them latency, and the products' pipe 1300: two groups of four take tiles in turn, each with an m and l of its own; R
 // is one, so each tile's decision about it waits for the tile's before.
@@ -49,7 +53,9 @@ constexpr int kGroup = 128;                   // softmax threads of a tile (four
 constexpr int kSoft = 2 * kGroup;
 constexpr int kThreads = 32 * (kLoaders + 1) + kSoft;
 constexpr int kColO = 0, kColS = 256, kColQ = 384, kCols = 512;
-constexpr float kGain = 7.f;                  // R stands for 2^7 in the product
+constexpr float kGain = 7.9f;                 // R stands for 2^7.9 in the product
+constexpr float kLost = 1.f / 512;            // what the weights may lose to rounding
+constexpr float kTop = 14.f;                  // a fourth (two groups, two lanes a head) of the least that the largest one is, 2^5.9
 constexpr float kStep = 4.f;                  // how far a maximum may pass R
 constexpr float kHead = 2.f;                  // how far R is set above the first tile's maximum: most grow a little
 
@@ -81,16 +87,65 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
-// four values as E5M2 codes, the first in the low byte
-__device__ __forceinline__ uint32_t e5m2x4(float a, float b, float c, float d) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E5M2);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E5M2);
-  return lo | (hi << 16);
+// Key e of a softmax thread's 32 rounds up what is at least (4 + 8 i) / 256 of a step above a code, i = 0 .. 31 once each,
+// neighbours far apart (the bits of e reversed): what is added before the lower 8 bits go.
+__host__ __device__ constexpr int spread(int e) {
+  return 4 + 8 * ((e & 1) << 4 | (e & 2) << 2 | (e & 4) | (e & 8) >> 2 | (e & 16) >> 4);
 }
-// an E5M2 code is the upper byte of an fp16 value: codes 0, 1 (sel 0x1404) or 2, 3 (sel 0x3424) of w
-__device__ __forceinline__ float2 e5m2x2_f(uint32_t w, uint32_t sel) {
-  const uint32_t h = __byte_perm(w, 0u, sel);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+// The same as a shift of lo by (spread - 127.5) / 256 of its smallest step, 2^-9: (2 spread - 255) 2^-18, the bits of an fp16
+__host__ __device__ constexpr uint32_t spread_lo(int e) {
+  const int n = 64 * (2 * spread(e) - 255), mag = n < 0 ? -n : n;  // in 2^-24
+  int s = 0;
+  while (mag >> s >= 2048) ++s;
+  return (n < 0 ? 0x8000u : 0u) + (mag < 1024 ? (uint32_t)mag : (uint32_t)(((s + 1) << 10) + (mag >> s) - 1024));
+}
+__device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+__device__ __forceinline__ uint32_t bits_of(const __half2& h) { return *reinterpret_cast<const uint32_t*>(&h); }
+
+// Four weights, of keys e .. e + 3 of the thread, below 2^12, as E5M2 and E4M3 codes (the first key in the low byte).  In pairs
+// of fp16 (11 bits of a weight): hi is its upper byte, lo what the rest rounds to.  To the nearest, or (kSpread) by the spread
+// thresholds: lo takes them from 2^-7 on; smaller weights leave lo nothing, and hi takes them.  lost: what the codes are short
+// of; mass: the weights / 64 (a sum of 16 fits fp16).  (A NaN is no code of hi's any more, but stays one in lo.)
+template <bool kSpread>
+__device__ __forceinline__ void split_weights(float v0, float v1, float v2, float v3, int e, uint32_t* hi, uint32_t* lo,
+                                              __half2* lost, __half2* mass) {
+  uint32_t up[2], rest[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2 h = i ? __floats2half2_rn(v2, v3) : __floats2half2_rn(v0, v1);
+    uint32_t add = 0x00800080u, shift = 0u;
+    if (kSpread) {
+      const uint32_t small = __hlt2_mask(__habs2(h), as_half2(0x20002000u));  // 2^-7
+      add = (small & (uint32_t)(spread(e + 2 * i) | spread(e + 2 * i + 1) << 16)) | (~small & add);
+      shift = ~small & (spread_lo(e + 2 * i) | spread_lo(e + 2 * i + 1) << 16);
+    }
+    up[i] = bits_of(h) + add;
+    const __half2 rem = __hsub2(h, as_half2(up[i] & 0xff00ff00u));  // (exact)
+    rest[i] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(kSpread ? __hadd2(rem, as_half2(shift)) : rem), __NV_SATFINITE, __NV_E4M3);
+    const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)rest[i], __NV_E4M3);
+    *lost = __hadd2(*lost, __hsub2(rem, __half2(back)));
+    *mass = __hfma2(__habs2(h), as_half2(0x24002400u), *mass);  // 2^-6
+  }
+  *hi = __byte_perm(up[0], up[1], 0x7531);
+  *lo = rest[0] | rest[1] << 16;
+}
+// The 32 weights s * gain of a thread into its row of P: (lost, mass)
+template <bool kSpread>
+__device__ __forceinline__ float2 store_weights(const float* s, float gain, uint8_t* row, int plane, int h) {
+  __half2 lost = as_half2(0u), mass = as_half2(0u);
+#pragma unroll
+  for (int c2 = 0; c2 < 2; ++c2) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float* v = s + 16 * c2 + 4 * e;
+      split_weights<kSpread>(v[0] * gain, v[1] * gain, v[2] * gain, v[3] * gain, 16 * c2 + 4 * e, hi + e, lo + e, &lost, &mass);
+    }
+    *reinterpret_cast<uint4*>(row + (((2 * plane + c2) ^ (h & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(row + (((4 + 2 * plane + c2) ^ (h & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  const float2 a = __half22float2(lost), b = __half22float2(mass);
+  return make_float2(a.x + a.y, 64.f * (b.x + b.y));
 }
 
 // Run x of a query: its first logical row, the rows [lo, hi) of its section that count, and the table.
@@ -497,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float c = be_h == 255 ? NAN : __uint_as_float((uint32_t)(be_h - 7) << 23) * a.scale2;
         const float c_own = plane ? c * 0.0625f : c, c_other = plane ? c : c * 0.0625f;
         float m = -INFINITY, l = 0.f;
+        float lost = 0.f, mass = 0.f;  // what this thread's keys have lost to rounding, and their weights, relative to 2^m
         const int first = (j & 1) == g ? 0 : 1;  // this group's first tile of the query
 #pragma unroll 1
         for (int i = first; i < n; i += 2) {
@@ -543,7 +599,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; ++e) mt = fmaxf(mt, s[e]);
           mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
           const float mn = fmaxf(m, mt), mr = mn == -INFINITY ? 0.f : mn;
-          l *= ex2(m - mr);
+          const float keep = ex2(m - mr);
+          l *= keep;
+          lost *= keep;
+          mass *= keep;
           m = mn;
           float vt = 0.f, l2 = 0.f;
 #pragma unroll
@@ -610,20 +669,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           // ---- the probabilities' two parts, once the buffer's last product has retired
           if (jt >= 2) wait(sm, sm.pv_done + g, ((jt >> 1) & 1) ^ 1);
           uint8_t* row = pbuf + h * 128;
-#pragma unroll
-          for (int c2 = 0; c2 < 2; ++c2) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float v0 = s[16 * c2 + 4 * e] * gain, v1 = s[16 * c2 + 4 * e + 1] * gain;
-              const float v2 = s[16 * c2 + 4 * e + 2] * gain, v3 = s[16 * c2 + 4 * e + 3] * gain;
-              hi[e] = e5m2x4(v0, v1, v2, v3);
-              const float2 b0 = e5m2x2_f(hi[e], 0x1404), b1 = e5m2x2_f(hi[e], 0x3424);
-              lo[e] = e4m3x4(v0 - b0.x, v1 - b0.y, v2 - b1.x, v3 - b1.y);
-            }
-            *reinterpret_cast<uint4*>(row + (((2 * plane + c2) ^ (h & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(row + (((4 + 2 * plane + c2) ^ (h & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
+          const float unit = ex2(fminf(ref - kGain - mr, 120.f));  // 1 / gain
+          float2 w = store_weights<false>(s, gain, row, plane, h);
+          mass = fmaf(w.y, unit, mass);
+          if (fabsf(fmaf(w.x, unit, lost)) > fmaf(mass, kLost, kTop * kLost * unit)) w = store_weights<true>(s, gain, row, plane, h);
+          lost = fmaf(w.x, unit, lost);
           tc::fence_proxy_async_smem();
           tc::fence_before_sync();
           tc::mbar_arrive(sm.p_full + g);

@@ -643,8 +643,13 @@ csa_status csa_append_pages(const csa_layer* layer, const csa_pages* pages, cons
  * On the tensor cores (bf16, H = 64, D = 512, R = 64, page_rows a multiple of 8)
  * the queries enter the products as two E4M3 parts (the 8 bits of a bf16 value,
  * those 2^-13 below the head's largest fewer), the probabilities times the keys'
- * scales as an E5M2 and an E4M3 part (7 bits, down to 2^-22 of the largest), sums
- * in fp32; the portable kernel takes any other layer, all in fp32.  A call's result
+ * scales in fp16 and from that as an E5M2 and an E4M3 part, sums in fp32.  Such a
+ * weight is off by at most 2^-8 of itself (and fp16's 2^-11), where that is more by
+ * 2^-15 of the head's largest weight, at most 1/8 of itself; below 2^-20 of the
+ * largest by 2^-22 of that.  Where small weights that are alike would all be rounded
+ * to one side, and that comes to 2^-9 of the weights, they are rounded by turns: one
+ * may then be off by 1/4 (or 2^-14 of the largest), many together by 2^-8.
+ * The portable kernel takes any other layer, all in fp32.  A call's result
  * depends on how its keys are cut into tiles (by B, T and all lengths), not on the
  * run: the same call gives the same bits.
  * B * T <= 2^16, and CSA_ERR_ARG where a sequence's tables have room for 2^31 - 256 keys, or B * T such for 2^36.

@@ -150,3 +150,47 @@ def test_one_key_far_below_rows_of_zeros(kind, form, power):
         want, allow = expect(L, q, cache, [[phys(cache, row, 0, range(n))]], [4 * n], None, None)
         P.check(out[..., 1:], want[..., 1:], allow[..., 1:], f"key {key}")
         assert (want[..., 1:].abs() > allow[..., 1:]).any()
+
+
+@pytest.mark.parametrize("depth,n", [(8, 256), (9, 512), (10, 1024), (11, 2048), (12, 4096), (14, 16384), (17, 131072)])
+@pytest.mark.parametrize("ratio", [1.0, 1 / 16])
+def test_many_small_weights_that_are_alike(depth, n, ratio):
+    """n rows that are the same, each of x 2^-depth of one dominant row's weight and together about as much, in whole queries:
+    what they are rounded to is right on the whole."""
+    L = P.layer(ratio=1)
+    nb, page = 160, 64
+    codes = torch.zeros(-(-(n + 1) // page), page, L.D, dtype=torch.uint8, device="cuda")
+    rows = codes.view(-1, L.D)
+    rows[1:, 1:] = 0x38            # 1
+    rows[1:, 2::2] = 0xB8          # -1
+    rows[0, 0], rows[0, L.D // 2:] = 0x7E, 0x3C  # 448; 1.5
+    q = torch.zeros(nb, 1, L.H, L.D, device="cuda", dtype=L.dtype)
+    q[..., 0] = 8.0
+    values = codes.view(P.F8).view(-1, L.D).to(P.F64)
+    table = torch.arange(codes.shape[0], dtype=torch.int32, device="cuda").expand(nb, -1).contiguous()
+    c = L.D ** -0.5
+    for x in (1.0, 1.06, 1.124, 1.126, 1.2, 1.249, 1.251, 1.3, 1.374, 1.376, 1.45, 1.55, 1.624, 1.626, 1.7, 1.874, 1.876, 1.99):
+        # weights are e^logit scale: the dominant row's is 2^depth / x times the others'
+        s0 = math.log(2.0 ** depth / x * ratio) / (8.0 * 448 * c)
+        scales = torch.full(codes.shape[:2], s0 * ratio, device="cuda")
+        scales[0, 0] = s0
+        out = torch.full_like(q, 7.0)
+        err = csa.attend_pages(L, q, csa.Pages(codes, scales), None, i32([n] * nb), out, row_table=table, n_rows=i32([n + 1] * nb))
+        assert err.item() == 0 and torch.equal(out, out[:1, :, :1].expand_as(out))
+        s = scales.view(-1)[:2].to(P.F64)
+        top = 8.0 * 448 * c * s[0]
+        p = torch.stack((torch.ones_like(top), torch.exp(-top)))
+        keys = values[:2] * s[:, None]
+        Z = p[0] + n * p[1]
+        want = (p[0] * keys[0] + n * p[1] * keys[1]) / Z
+        A = (p[0] * keys[0].abs() + n * p[1] * keys[1].abs()) / Z
+        # logits: sums of D products, a rounding each; sums of n weights.  The weights: fp16 (2^-11), then two parts, the nearest
+        # (2^-8 of a large one).  Of small ones that are alike, while they are rounded to the nearest, what is lost stays below
+        # 2^-9 of all weights and of the largest; from there on 32 thresholds are centred in a step of hi (1/64 of at most 1/4 of
+        # the weight) or of lo (1/64 and 1/512 of 2^-9, of weights from 2^-7 on).  Where the dominant row breaks the row of 32,
+        # one weight's quarter.
+        allow = A * (2 * (L.D + 8) * P.U32 * top + (n + 33) * P.U32 + 2.0 ** -20 + 2.0 ** -11) + 2.0 ** -8 * p[0] / Z * keys[0].abs()
+        w0, w1 = p[0] * s[0], p[1] * s[1]
+        allow = allow + (2.0 ** -9 * (2 * w0 + n * w1) + 2.0 ** -8 * 1.125 * n * w1 + 0.25 * w1) / Z * values[1].abs()
+        allow = allow + (want.abs() + allow) * P.HALF[L.dtype]
+        P.check(out[0, 0, 0], want, allow, f"x {x}")
