@@ -139,8 +139,20 @@ struct Span {
   uintptr_t lo, hi;
   Span(const void* p, long long n, long long row, long long stride)
       : lo(reinterpret_cast<uintptr_t>(p)), hi(lo + (uintptr_t)((n - 1) * stride + row)) {}
-  bool meets(const Span& o) const { return lo < o.hi && o.lo < hi; }
+  Span(const void* p, long long bytes) : Span(p, 1, bytes, 0) {}
+  bool meets(const Span& o) const { return lo && o.lo && lo < o.hi && o.lo < hi; }  // (a tensor that is not there meets none)
 };
+// Whether what a call writes lies apart from all that it reads, and from what else it writes.
+template <int kOuts, int kIns>
+bool apart(const Span (&outs)[kOuts], const Span (&ins)[kIns]) {
+  for (int i = 0; i < kOuts; ++i) {
+    for (const Span& in : ins)
+      if (outs[i].meets(in)) return false;
+    for (int k = 0; k < i; ++k)
+      if (outs[i].meets(outs[k])) return false;
+  }
+  return true;
+}
 
 }  // namespace
 
@@ -667,6 +679,11 @@ csa_status csa_append_pages(const csa_layer* layer, const csa_pages* pages, cons
   if (stride_t != 0 && (stride_t < L.D || stride_t % 8 || stride_t > (1LL << 31))) return CSA_ERR_ARG;
   const long long st_t = stride_t ? stride_t : L.D, st_b = stride_b ? stride_b : T * st_t;
   if (st_b % 8 || st_b < 0 || st_b > (1LL << 40)) return CSA_ERR_ARG;
+  const long long es = (long long)esize(L.dtype), n_rows = (long long)pages->n_pages * pages->page_rows;
+  const Span outs[] = {Span(pages->codes, n_rows * L.D), Span(pages->scales, n_rows * 4), Span(err, 4)};
+  const Span ins[] = {Span(rows, ((B - 1) * st_b + (T - 1) * st_t + L.D) * es), Span(table, (long long)B * width * 4),
+                      Span(pos, B * 4LL), Span(n_new, B * 4LL), Span(weight, L.D * 4LL), Span(inv_freq, L.R * 2LL)};
+  if (!apart(outs, ins)) return CSA_ERR_ARG;
   PagedAppend t{rows, st_b, st_t, static_cast<uint8_t*>(pages->codes), pages->scales, table, pos, n_new, weight,
                 inv_freq, err, L.eps, pages->n_pages, pages->page_rows, width, B, T, L.D, L.R, norm};
   return cuda_status(launch_append_pages(L, t, static_cast<cudaStream_t>(stream)));
@@ -688,14 +705,21 @@ csa_status csa_attend_pages(const csa_layer* layer, const csa_pages* pages, cons
   if (sel && (!row_table || !L.has_indexer() || !dev_i32(sel) || !dev_i32(n_sel))) return CSA_ERR_ARG;
   if ((sink && !dev_i32(sink)) || (n_new && !dev_i32(n_new)) || (inv_freq && !dev_tensor(inv_freq)))
     return CSA_ERR_ARG;
-  const long long n = (long long)B * T, row = (long long)L.H * L.D * esize(L.dtype);
-  if (Span(q, n, row, row).meets(Span(out, n, row, row))) return CSA_ERR_ARG;
+  const long long n = (long long)B * T;
   // a query's keys and the tiles of a call are counted in ints; the smallest hold 32 keys, and each of a query's three
   // sections ends one
   const long long P = pages->page_rows;
   const long long most = (row_table ? (sel ? (long long)L.topk : row_width * P) : 0) + (token_table ? token_width * P : 0);
   if (most > INT32_MAX - 256 || n * (most / 32 + 4) > INT32_MAX) return CSA_ERR_ARG;
-  if (ws_bytes < ws_attend_pages(L, (int)n) || !dev_tensor(ws)) return CSA_ERR_WORKSPACE;
+  const size_t need = ws_attend_pages(L, (int)n);
+  if (ws_bytes < need || !dev_tensor(ws)) return CSA_ERR_WORKSPACE;
+  const long long q_bytes = n * L.H * L.D * (long long)esize(L.dtype), n_slots = pages->n_pages * P;
+  const Span outs[] = {Span(out, q_bytes), Span(ws, (long long)need), Span(err, 4)};
+  const Span ins[] = {Span(pages->codes, n_slots * L.D), Span(pages->scales, n_slots * 4), Span(q, q_bytes), Span(sink, L.H * 4LL),
+                      Span(pos, B * 4LL), Span(n_new, B * 4LL), Span(token_table, (long long)B * token_width * 4),
+                      Span(row_table, (long long)B * row_width * 4), Span(row_table ? n_rows : nullptr, B * 4LL),
+                      Span(sel, n * L.topk * 4), Span(sel ? n_sel : nullptr, n * 4), Span(inv_freq, L.R * 2LL)};
+  if (!apart(outs, ins)) return CSA_ERR_ARG;
   PagedArgs a{};
   Carver c(ws);
   carve_paged(c, L, (int)n, &a);

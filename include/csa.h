@@ -604,6 +604,9 @@ csa_status csa_add_norm(const csa_layer* layer, const void* x, long long x_strid
  * [0, n_pages) that a call meets raises CSA_DEV_RANGE, a row behind the table's
  * width CSA_DEV_CAPACITY, and the row is left out; pos[b] < 0 or above
  * 2^31 - 1 - T or n_new[b] outside [0, T] raises CSA_DEV_STATE and skips the sequence.
+ * What a call writes (the pool or the output, workspace, error word) may overlap
+ * neither what it reads nor what else it writes, pages of the pool that it does not
+ * meet included (CSA_ERR_ARG).
  * Both calls read nothing before their predecessors in the stream have completed,
  * and the next kernel starts once they have written.
  *
@@ -637,7 +640,7 @@ csa_status csa_append_pages(const csa_layer* layer, const csa_pages* pages, cons
  *   out[b][i][h] = RoPE^-1(o_h, p) in fp32, rounded to the model dtype once.
  * The cache holds the queries' own rows already (csa_append_pages).  q is rotated
  * (csa_norm_rope).  A query without any key gives zeros.
- *   q, out [B, T, H, D] model dtype, apart from one another (and out from all else); sink [H] fp32 or NULL (no sink);
+ *   q, out [B, T, H, D] model dtype, apart from one another; sink [H] fp32 or NULL (no sink);
  *   sel [B, T, topk], n_sel [B, T] int32 (ratio 4, with row_table); inv_freq NULL:
  *   no rotation of the output.
  * On the tensor cores (bf16, H = 64, D = 512, R = 64, page_rows a multiple of 8)
