@@ -76,6 +76,22 @@ _plain = None  # csrc/checks.c: whole calls on plain tensors; with the addresses
 _at = {}
 
 
+def _tensors(path: str = _TENSORS_PATH) -> int:
+    """Address of csa_tensor (csrc/tensors.cpp) where it was built for this very torch, whose layout of a tensor it has
+    compiled in; otherwise 0, and the checks ask tensors by their attributes."""
+    if not os.path.exists(path):
+        return 0
+    try:
+        lib = ctypes.CDLL(path)  # (stays loaded: nothing unloads it)
+        built_for = lib.csa_tensors_torch
+        built_for.argtypes, built_for.restype = [], ctypes.c_char_p
+        if built_for().decode() != f"{torch.__version__} {torch.version.git_version}":
+            return 0
+        return ctypes.cast(lib.csa_tensor, ctypes.c_void_p).value
+    except (OSError, AttributeError):  # it needs what this torch has not; an older build that does not say
+        return 0
+
+
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libcsa.so (built by build.py); raises if it is missing."""
     global _lib, _addresses, _plain
@@ -154,12 +170,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         _addresses = module.addresses
         module.setup(torch.float32, torch.uint8, torch.int32, torch._C._cuda_getCurrentRawStream,
                      torch._C._cuda_getDevice)
-        if os.path.exists(_TENSORS_PATH):
-            try:
-                tensors = ctypes.CDLL(_TENSORS_PATH)  # (stays loaded: nothing unloads it)
-                module.tensors(ctypes.cast(tensors.csa_tensor, ctypes.c_void_p).value)
-            except OSError:  # built for another torch: attributes will do
-                pass
+        module.tensors(_tensors())
         for name in ("add_norm", "append_pages", "attend_pages"):
             _at[name] = ctypes.cast(getattr(lib, "csa_" + name), ctypes.c_void_p).value
         _plain = module

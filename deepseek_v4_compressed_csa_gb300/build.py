@@ -76,7 +76,8 @@ def build_tensors() -> str | None:
         root = os.path.dirname(torch.__file__)
         inc = os.path.join(root, "include")
         cmd = [*(shlex.split(os.environ.get("CXX") or "") or ["g++"]), "-O2", "-std=c++17", "-shared", "-fPIC",
-               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", inc, "-isystem",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               f'-DCSA_TORCH="{torch.__version__} {torch.version.git_version}"', "-isystem", inc, "-isystem",
                os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
                os.path.join(CSRC, "tensors.cpp"), "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
                "-o", tmp]

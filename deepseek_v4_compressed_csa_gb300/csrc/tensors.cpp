@@ -1,8 +1,11 @@
 // What checks.c asks of a tensor (type, device, layout, shape, address), from the tensor itself: 0.02 us a tensor, where
 // asking by its Python attributes takes 0.3.  An own library, without which the checks ask by attributes: it needs torch's
-// headers.
+// headers, which lay a tensor's members out in it, so it is of use to the torch that it was built for alone.
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+// That torch: its version and commit (CSA_TORCH, from the build).
+extern "C" const char* csa_tensors_torch(void) { return CSA_TORCH; }
 
 // 1: a dense CUDA tensor of this dtype and at most max_dims dimensions, its shape in dims[0 .. n); 0: another tensor;
 // -1: no plain tensor (a subclass may answer for itself).
