@@ -41,21 +41,32 @@ FALLBACK_BF16_TFLOPS = 1900.0
 
 # DRAM traffic (ncu dram__bytes_read.sum + dram__bytes_write.sum, every kernel captured cold) of one decode
 # layer-step of the headline workload and of one prefill chunk, with the hash of the kernel sources the counters
-# were taken on (csrc_digest()); the bench reports them only while the sources still hash the same.
-TRAFFIC = {"csrc_sha256": "0ed9d38f02abe1c3", "decode_layer_step_bytes": 117_480_000,
+# were taken on (csrc_digest(): what those kernels are compiled from); the bench reports them only while the sources
+# still hash the same.  A new hash comes with new counters.
+TRAFFIC = {"csrc_sha256": "81610c69776c1493", "decode_layer_step_bytes": 117_480_000,
            "decode_fp8_layer_step_bytes": 87_534_000, "prefill_chunk_bytes": 1_233_400_000,
            "profile": "profiles/traffic_decode_b32_ctx32k_and_prefill_t4096.md"}
 
 
-def csrc_digest() -> str:
-    """sha256 (first 16 hex digits) of the library's kernel sources."""
+# The translation units of the kernels that TRAFFIC's steps run and of the host code that sizes their launches.
+TRAFFIC_UNITS = ("attend.cu", "compress.cu", "indexer.cu", "tc_attend.cu", "tc_attend_decode.cu", "tc_attend_prefill.cu",
+                 "tc_indexer.cu", "tc_project.cu", "tmap.cu")
+
+
+def csrc_digest(d: str = os.path.join(ROOT, "deepseek_v4_compressed_csa_gb300", "csrc")) -> str:
+    """sha256 (first 16 hex digits) of TRAFFIC_UNITS and of what they include from their folder, by name."""
     import hashlib
-    d = os.path.join(ROOT, "deepseek_v4_compressed_csa_gb300", "csrc")
+    import re
+    texts, todo = {}, list(TRAFFIC_UNITS)
+    while todo:
+        f = todo.pop()
+        if f not in texts:
+            texts[f] = open(os.path.join(d, f), "rb").read()
+            todo += re.findall(r'^\s*#\s*include\s*"([^"/]+)"', texts[f].decode(), re.M)
     h = hashlib.sha256()
-    for f in sorted(os.listdir(d)):
-        if f.endswith((".cu", ".cuh", ".h")):
-            h.update(f.encode())
-            h.update(open(os.path.join(d, f), "rb").read())
+    for f in sorted(texts):
+        h.update(f.encode())
+        h.update(texts[f])
     return h.hexdigest()[:16]
 
 
