@@ -1087,7 +1087,8 @@ def append_pages(layer: Layer, rows, pages: Pages, table, pos, n_new=None, weigh
     """csa_append_pages: rows [B, T, D] become logical rows pos[b] .. pos[b] + n_new[b] - 1 (n_new None: T each) of the
     sequences' tables [B, width]: RMS-normed (norm, with weight fp32 [D] or None), rotated to those positions (inv_freq;
     None: not rotated) and put in 8 bits with a scale per row.  A token of rows is contiguous; tokens and sequences may be
-    strides apart.  Returns the device error word tensor."""
+    strides apart.  Compressed rows that compress_append put into its pool come as pool.gather(1, ..) at n_rows as it was before,
+    ceil(T / ratio) of them, with n_new = n_rows - before: all on the device.  Returns the device error word tensor."""
     if _plain is not None:
         code = _plain.append_pages(_at["append_pages"], layer._packed(), layer.dtype, layer.D, layer.R // 2, rows,
                                    pages.codes, pages.scales, table, pos, n_new, weight, norm, inv_freq, err, stream)
