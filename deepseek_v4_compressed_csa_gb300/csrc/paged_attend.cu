@@ -5,6 +5,8 @@
 //
 // over the keys of PagedQuery, key_k = scale_k code_k.  A block walks its run of tiles (paged.cuh) with a running maximum
 // and sum per head; all arithmetic in fp32, the output rounded once.
+#include <algorithm>
+
 #include "paged.cuh"
 #include "tc.cuh"
 
@@ -486,11 +488,20 @@ long long most_tiles(const PagedArgs& a) {
   return n + (runs + per - 1) / per;
 }
 
-// Whether queries are short enough to stay whole: then no merge follows.  Splitting them pays while there are blocks to spare
-// and more tiles to share out than the merge costs (some 5 us, six tiles' time): one query of 11 tiles takes 14.9 us split
-// and 18.5 whole, one of 3 tiles 14.2 and 11.4, 128 of 11 tiles 25.7 and 24.0.
-bool stay_whole(const PagedArgs& a, long long most) {
-  return !(a.row_table && !a.sel) && most <= (2 * a.B * a.T < kPagedBlocks ? 4 : 16);
+// Whether queries stay whole: then no merge follows.  Cutting one saves it the tiles that other blocks take (a tile: 0.9 us on
+// the tensor cores, elsewhere 0.4 us and 1 more per 150 dims for every 8 heads) and costs the parts and their merge, more for
+// more queries.  Measured, us whole / cut, selections of so many tiles each:
+//   tensor cores, 1 query: 6 tiles 14.0 / 14.8, 7 15.5 / 15.0; 20: 8 16.9 / 17.8, 11 19.6 / 19.0; 40: 14 25.0 / 26.8,
+//     16 27.1 / 27.6, 20 31.7 / 29.9; 70: 8 20.4 / 28.9, 20 32.0 / 35.4, 24 36.2 / 37.1; 128: 11 25.3 / 26.7, 24 37.5 / 39.8;
+//   fp32, 8 heads of 64, 1 query: 4 tiles 8.2 / 8.7, 6 10.6 / 8.7; 40: 8 12.6 / 13.2, 11 15.7 / 13.6; 70: 8 12.7 / 12.8,
+//     16 19.2 / 16.1; bf16, 32 heads of 512, 1 query: 1 tile 42 / 43, 2 56 / 43; 70: 4 102 / 61; 110: 4 102 / 103.
+// Where lengths differ a long query holds its block up, by 15 us at most.
+bool stay_whole(const PagedArgs& a, bool tc, long long most) {
+  if (a.row_table && !a.sel) return false;  // (as long as the table at most, and mostly not)
+  const int Q = a.B * a.T, each = Q < kPagedBlocks ? kPagedBlocks / Q : 1;  // pieces a query
+  const double tile = tc ? 0.9 : (a.H + 7) / 8 * (0.4 + a.D / 150.0), merge = tc ? 4 + Q / 9.0 : 3 + Q / 40.0;
+  const long long piece = std::max((most + each - 1) / each, tc ? 2LL : 1LL);
+  return tile * (most - piece) <= merge && tile * most <= 15;
 }
 
 template <typename T>
@@ -501,7 +512,7 @@ cudaError_t attend_t(const Dims& L, PagedArgs a, cudaStream_t s) {
   while (tc && a.shift < 6 && a.P % (2 << a.shift) == 0) ++a.shift;
   a.cols = tc ? 32 : a.D;
   const long long most = most_tiles(a);
-  a.merge = !stay_whole(a, most);
+  a.merge = !stay_whole(a, tc, most);
   a.min_tiles = a.merge ? tc ? 2 : 1 : (int)most;
   cudaError_t e;
   if (tc) {
