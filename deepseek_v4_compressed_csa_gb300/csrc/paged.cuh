@@ -28,13 +28,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// (mean(x^2) + eps)^-1/2 of a row whose square sum may pass fp32's range (values from about 2^60 on): then anew from the
-// values times 2^-64, sum(f) being their square sum times f^2 (the same answer in every thread that shares the row).
+// (mean(x^2) + eps)^-1/2 of a row whose square sum may pass fp32's range (values from about 2^57 on): then anew from the
+// values times 2^-80, sum(f) being their square sum times f^2 (the same answer in every thread that shares the row): 2^14
+// squares of the largest values there are sum up to 2^110.
 template <typename Sum>
 __device__ __forceinline__ float inv_rms(float inv_n, float eps, Sum sum) {
   const float ss = sum(1.f);
   if (!isinf(ss)) return rsqrtf(fmaf(ss, inv_n, eps));
-  constexpr float f = 5.42101086242752217e-20f;  // 2^-64
+  constexpr float f = 8.27180612553027674871e-25f;  // 2^-80
   return rsqrtf(fmaf(sum(f), inv_n, eps * f * f)) * f;
 }
 // cos and sin of theta = (float)p * freq (one fp32 product, as in rope_cs).  Far positions: theta = m 2^e as a fraction

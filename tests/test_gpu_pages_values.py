@@ -194,3 +194,41 @@ def test_many_small_weights_that_are_alike(depth, n, ratio):
         allow = allow + (2.0 ** -9 * (2 * w0 + n * w1) + 2.0 ** -8 * 1.125 * n * w1 + 0.25 * w1) / Z * values[1].abs()
         allow = allow + (want.abs() + allow) * P.HALF[L.dtype]
         P.check(out[0, 0, 0], want, allow, f"x {x}")
+
+
+@pytest.mark.parametrize("small", [False, True])
+@pytest.mark.parametrize("X", [128, 4096, 16384])
+def test_rows_near_the_ends_of_the_type_are_normed(small, X):
+    """Rows whose square sum passes fp32's range, up to the largest values there are, all of a size or one among small ones."""
+    L = P.layer(small)
+    g = gen(X)
+    x = normal(g, 8, X).abs().clamp(0.5, 1.9) * torch.sign(normal(g, 8, X))
+    for r, power in enumerate((56, 63, 70, 100, 120, 122, 125, 127)):
+        x[r] *= 2.0 ** power
+    x[7, : X // 2] *= 2.0 ** -40
+    x = x.to(L.dtype)
+    assert torch.isfinite(x).all()
+    got = csa.add_norm(L, x, torch.zeros_like(x), group=64)
+    h = x.to(P.F64)
+    y = h / (h.pow(2).mean(-1, keepdim=True) + L.rms_eps).sqrt()
+    err = y.abs() * 64 * P.U32  # (as in the other tests of it)
+    P.check(got.out, y, err + y.abs() * P.HALF[L.dtype])
+    P.check(got.residual, h, h.abs() * P.HALF[L.dtype])
+    P.check_codes(got.codes.view(8, -1, 64), got.scales, y.view(8, -1, 64), err.view(8, -1, 64))
+
+
+@pytest.mark.parametrize("kw", [dict(small=False), dict(small=True), dict(small=True, D=1024, R=8)])
+def test_latent_rows_near_the_ends_of_the_type_are_normed(kw):
+    L = P.layer(**kw)
+    g = gen(L.D)
+    x = (normal(g, 1, 8, L.D).abs().clamp(0.5, 1.9) * torch.sign(normal(g, 1, 8, L.D)))
+    for r, power in enumerate((56, 63, 70, 100, 120, 122, 125, 127)):
+        x[0, r] *= 2.0 ** power
+    x = x.to(L.dtype)
+    cache = P.Cache(L, 8, 2)
+    table = cache.table(1, 1)
+    at = torch.tensor(cache.place(table, 0, range(8)), device="cuda")
+    assert csa.append_pages(L, x, cache.pages, table.cuda(), i32([0]), norm=True).item() == 0
+    y = x[0].to(P.F64)
+    y = y / (y.pow(2).mean(-1, keepdim=True) + L.rms_eps).sqrt()
+    P.check_codes(cache.codes.view(-1, L.D)[at], cache.scales.view(-1)[at], y, y.abs() * 64 * P.U32)
