@@ -27,13 +27,14 @@
 // Softmax with the scales: t = scale2 S ks, m a running maximum, l = sum 2^{t - m}.  What enters the product is
 // 2^t ks 2^{7.9 - R}, R a reference that follows the maximum of log2(2^t |ks|) in steps: below 2^12, where lo, up to 2^8,
 // still fits E4M3.  It starts 4 times above the first tile's maximum, and O^T is rescaled only when some head's maximum
-// has passed its R by 4 (powers of two); every head's R then follows.  A tile takes its four warps some 2500 clocks, most
+// has passed its R by 4 (powers of two); every head's R then follows.  A tile takes its four warps some 2600 clocks, most
 // of them latency, and the products' pipe 1300: two groups of four take tiles in turn, each with an m and l of its own; R
 // is one, so each tile's decision about it waits for the tile's before.
 //
-// Measured: 8 queries of 65.7K rows (272 MB) 57 us before the merge, 4.8 TB/s, 1700 clocks a tile: shared memory's, which
-// moves 176 KB of it at 128 bytes a clock (the keys once in and three times out, P, the scores' scales).  Feeding the products
-// faster changes nothing.  Short calls are the chain plan - queries - tile - output: one window of three tiles 11.4 us.
+// Measured: 8 queries of 65.7K rows (272 MB) 58 us before the merge, 4.7 TB/s, 1700 clocks a tile, where shared memory moves
+// 176 KB of it at 128 bytes a clock (the keys once in and three times out, P, the scores' scales).  Feeding the products
+// faster changes nothing.  Short calls are the chain plan - queries - tile - output: one window of three tiles 11.8 us.  The
+// account of what rounding loses costs 1 to 3 % of a call, a decision by the account of the tile before just as much.
 #include "paged.cuh"
 #include "tc.cuh"
 

@@ -652,11 +652,15 @@ csa_status csa_append_pages(const csa_layer* layer, const csa_pages* pages, cons
  * largest by 2^-22 of that.  Where small weights that are alike would all be rounded
  * to one side, and that comes to 2^-9 of the weights, they are rounded by turns: one
  * may then be off by 1/4 (or 2^-14 of the largest), many together by 2^-8.
- * The portable kernel takes any other layer, all in fp32.  A call's result
+ * The portable kernel takes any other layer, all in fp32, and is far slower: the
+ * Flash shapes in pages of 13 rows take 79 us a selection and 900 us 128 of them,
+ * in pages of 16 rows 15 and 25; 16 heads over the 512-dim latent take 92 us where
+ * 64 take 22 (one query of 32K rows).  A call's result
  * depends on how its keys are cut into tiles (by B, T and all lengths), not on the
  * run: the same call gives the same bits.
  * B * T <= 2^16, and CSA_ERR_ARG where a sequence's tables have room for 2^31 - 256 keys, or B * T such for 2^36.
- * Workspace: CSA_OP_ATTEND_PAGES, not shared by two calls in flight. */
+ * Workspace: CSA_OP_ATTEND_PAGES (parts of queries for 152 blocks: 40 MB for the
+ * Flash shapes, whatever B and T), not shared by two calls in flight. */
 csa_status csa_attend_pages(const csa_layer* layer, const csa_pages* pages, const void* q, int B, int T,
                             const float* sink, const int32_t* pos, const int32_t* n_new, const int32_t* token_table,
                             int token_width, int first, const int32_t* row_table, int row_width, const int32_t* n_rows,
