@@ -134,6 +134,7 @@ bool pages_ok(const csa_pages* p) {
 bool table_ok(const csa_pages* p, const int32_t* table, int pages) {
   return dev_i32(table) && pages >= 1 && (long long)pages * p->page_rows <= kPagedTable;
 }
+constexpr long long kSpan = 1LL << 56;  // values that rows a stride apart may span: no sum of theirs passes 64 bits
 // [lo, hi) of a tensor of n rows of `row` bytes, `stride` bytes apart
 struct Span {
   uintptr_t lo, hi;
@@ -643,7 +644,7 @@ csa_status csa_add_norm(const csa_layer* layer, const void* x, long long x_strid
       (scales && !dev_i32(scales)))
     return CSA_ERR_ARG;
   for (long long stride : {x_stride, residual_stride})
-    if (stride != 0 && (stride < X || stride % 8 || stride > (1LL << 31))) return CSA_ERR_ARG;
+    if (stride != 0 && (stride < X || stride % 8 || stride > (1LL << 31) || stride > kSpan / N)) return CSA_ERR_ARG;
   AddNorm t{x, residual, weight, out, residual_out, static_cast<uint8_t*>(codes), scales, N,
             x_stride ? x_stride : X, residual_stride ? residual_stride : X, X, codes ? group : X};
   // a thread writes what it has read itself: an output may be a dense input, and nothing else that is read or written
@@ -678,7 +679,7 @@ csa_status csa_append_pages(const csa_layer* layer, const csa_pages* pages, cons
     return CSA_ERR_ARG;
   if (stride_t != 0 && (stride_t < L.D || stride_t % 8 || stride_t > (1LL << 31))) return CSA_ERR_ARG;
   const long long st_t = stride_t ? stride_t : L.D, st_b = stride_b ? stride_b : T * st_t;
-  if (st_b % 8 || st_b < 0 || st_b > (1LL << 40)) return CSA_ERR_ARG;
+  if (st_b % 8 || st_b < 0 || st_b > (1LL << 40) || st_b > kSpan / B) return CSA_ERR_ARG;
   const long long es = (long long)esize(L.dtype), n_rows = (long long)pages->n_pages * pages->page_rows;
   const Span outs[] = {Span(pages->codes, n_rows * L.D), Span(pages->scales, n_rows * 4), Span(err, 4)};
   const Span ins[] = {Span(rows, ((B - 1) * st_b + (T - 1) * st_t + L.D) * es), Span(table, (long long)B * width * 4),

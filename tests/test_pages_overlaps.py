@@ -4,7 +4,7 @@ import torch
 
 import deepseek_v4_compressed_csa_gb300 as csa
 from deepseek_v4_compressed_csa_gb300 import _binding as B
-from tests.test_pages_host import FAKE, GAP, _append, _attend, _pages, lib  # noqa: F401 (lib: a fixture)
+from tests.test_pages_host import FAKE, GAP, _append, _attend, _norm, _pages, lib  # noqa: F401 (lib: a fixture)
 
 ROWS, D = 10 * 64, 512  # of the pool that _pages describes
 CODES, SCALES = FAKE + 8 * GAP, FAKE + 9 * GAP
@@ -47,6 +47,13 @@ def test_attend_pages(lib):  # noqa: F811
     for at in over(here["out"], out, ws):
         assert _attend(lib, ws=at) == B.CSA_ERR_ARG
     assert _attend(lib, err=here["out"] + out - 4) == B.CSA_ERR_ARG and _attend(lib, err=FAKE + 15 * GAP + ws - 4) == B.CSA_ERR_ARG
+
+
+def test_strides_past_the_address_space(lib):  # noqa: F811
+    """Rows whose strides span more than an address counts: refused, not compared by a span that wrapped."""
+    assert _append(lib, B_=1 << 24, T=1, sb=1 << 40) == B.CSA_ERR_ARG
+    assert _append(lib, B_=1 << 20, T=16, sb=(1 << 36) + 8) == B.CSA_ERR_ARG
+    assert _norm(lib, N=(1 << 31) - 1, xs=1 << 31) == B.CSA_ERR_ARG and _norm(lib, N=(1 << 31) - 1, rs=1 << 31) == B.CSA_ERR_ARG
 
 
 @pytest.mark.gpu
